@@ -26,9 +26,11 @@
  *     space is the caller's workspace `ws` (size from flint_moe_workspace_bytes,
  *     256-byte aligned, no initialisation needed).  Calls that share one
  *     workspace must be ordered on one stream.
- *   - Only the Flint shapes are supported: hidden 2048, 256 routed experts,
- *     1 shared expert, intermediate 512, top-6.  Anything else returns
- *     FLINT_MOE_ERR_UNSUPPORTED (there is no generic fallback path).
+ *   - The sublayer calls support only the Flint shapes: hidden 2048, 256
+ *     routed experts, 1 shared expert, intermediate 512, top-6.  Anything else
+ *     returns FLINT_MOE_ERR_UNSUPPORTED (there is no generic fallback path).
+ *     The parts of an FP8 expert layer (flint_moe_route and the calls after
+ *     it) take any shape within their limits.
  */
 #ifndef FLINT_MOE_H
 #define FLINT_MOE_H
@@ -262,6 +264,128 @@ int flint_moe_pack_dense(const uint8_t *codes, const uint8_t *scales, int N, int
                          size_t packed_bytes, flint_moe_stream_t stream);
 int flint_moe_dense_gemv(const void *packed, int N, int K, float tensor_scale, const void *x, int B,
                          void *y, flint_moe_stream_t stream);
+
+/*
+ * ---- FP8 expert layers of any shape ---------------------------------------
+ *
+ * The five calls below are the parts of a mixture-of-experts layer whose
+ * weights are 8-bit (E4M3) with one fp32 scale per block of 128 x 128, for any
+ * number of experts, choices and widths within the limits given.  Used
+ * together, for T tokens with k choices each (P = T * k pairs):
+ *   flint_moe_route           logits        -> ids, w      [T][k]
+ *   flint_moe_group_pairs     ids           -> offsets, order, pos
+ *   flint_moe_quantize_rows   x, pos        -> q [P][H], scales (expert order)
+ *   flint_moe_block_gemm      gate and up   -> [P][2I]
+ *   flint_moe_quantize_rows   silu(g) * u   -> q [P][I], scales
+ *   flint_moe_block_gemm      down          -> [P][H]
+ *   flint_moe_combine         pos, w        -> y [T][H]
+ * "Expert order" is the pairs sorted by expert, those of one expert in
+ * ascending order of t * k + j.  The conventions at the top of this file hold,
+ * except that buffers may be of any shape within the limits; no workspace is
+ * needed.  Every call is deterministic: the same inputs give the same bits.
+ * All of them may be captured into a CUDA graph (the first call of a process
+ * on a device sets up the library and must come before the capture).
+ */
+
+/* Element types of activations. */
+enum { FLINT_MOE_T_BF16 = 0, FLINT_MOE_T_F32 = 1 };
+/* Score of a logit: 1 / (1 + exp(-x)), or softmax over the row's experts. */
+enum { FLINT_MOE_SCORE_SIGMOID = 0, FLINT_MOE_SCORE_SOFTMAX = 1 };
+/* Score of a group of experts: its best key, or the sum of its two best. */
+enum { FLINT_MOE_GROUP_MAX = 0, FLINT_MOE_GROUP_TOP2 = 1 };
+
+typedef struct {
+    int n_experts;   /* E, 1..1024                                            */
+    int top_k;       /* 1..16, at most top_groups * E / n_groups              */
+    int score;       /* FLINT_MOE_SCORE_*                                     */
+    int n_groups;    /* 1..32, divides E: group g is experts g*E/n .. ; 1: none */
+    int top_groups;  /* groups a token may choose from, 1..n_groups           */
+    int group_score; /* FLINT_MOE_GROUP_*                                     */
+    int renormalise; /* non-zero: selected scores are divided by their sum    */
+    float scale;     /* factor of every weight (finite)                       */
+} flint_moe_routing;
+
+/*
+ * Routing of T tokens (1..2^20).
+ *   logits  [T][E] of logits_type, rows row_stride >= E elements apart
+ *   bias    fp32 [E] added to the scores for the choice only, or NULL
+ *   ids     int32 [T][top_k] in descending order of key, w fp32 [T][top_k]
+ * The key of an expert is its logit, or score + bias when a bias is given.  An
+ * expert whose logit is -inf or NaN (or whose key is) cannot be chosen and
+ * takes no part in the softmax; places that no expert is left for hold id -1
+ * and weight 0.  Groups are kept by their score (with GROUP_TOP2 and no bias:
+ * the sum of the two best scores; one candidate counts alone).  Keys and group
+ * scores are compared as the real numbers that they stand for, as far as fp64
+ * tells them apart; ties go to the lower index.  Weights come from the scores
+ * without the bias, in fp32; renormalised ones are formed relative to the
+ * row's largest, so that very low logits do not underflow together.
+ */
+int flint_moe_route(const flint_moe_routing *routing, const void *logits, int logits_type,
+                    long long row_stride, int T, const float *bias, int32_t *ids, float *w,
+                    flint_moe_stream_t stream);
+
+/*
+ * Groups n_pairs (1..2^24) pairs by expert.
+ *   ids      int32 [n_pairs]; a pair whose id is outside 0..n_experts-1 is dropped
+ *   offsets  int32 [n_experts + 1]: expert e owns places offsets[e] ..
+ *            offsets[e + 1] - 1; offsets[n_experts] pairs are left
+ *   order    int32 [n_pairs]: the pair at each place, -1 behind the last
+ *   pos      int32 [n_pairs]: the place of each pair, -1 where dropped
+ */
+int flint_moe_group_pairs(const int32_t *ids, int n_pairs, int n_experts, int32_t *offsets,
+                          int32_t *order, int32_t *pos, flint_moe_stream_t stream);
+
+/*
+ * Quantises rows to E4M3 in blocks of 128 elements (the last one shorter where
+ * 128 does not divide K).
+ *   x       [rows][K] of x_type (silu_mul != 0: [rows][2K], and the row
+ *           quantised is silu(first half) * second half, formed in fp32 and not
+ *           rounded before), rows row_stride elements apart
+ *   pos     int32 [rows][top_k]: the places that each row is written to
+ *           (places outside 0..places-1 are skipped; two rows must not share
+ *           one), or NULL: row i is written to place i, and places == rows
+ *   q       E4M3 [places][K]; scales fp32 [ceil(K / 128)][places]
+ * With a = max(largest magnitude of the block, 2^-96): scale = a / 448 and
+ * code = e4m3(x * (448 / a)), round to nearest even; a block that holds an
+ * infinity or NaN gets a scale that is not finite.  Places that no row names
+ * are left as they were.  K a multiple of 16, at most 2^17; row_stride a
+ * multiple of 16 bytes; at most 2^24 rows and places.
+ */
+int flint_moe_quantize_rows(const void *x, int x_type, long long row_stride, int rows, int K,
+                            int silu_mul, const int32_t *pos, int top_k, int places, void *q,
+                            float *scales, flint_moe_stream_t stream);
+
+/*
+ * Block-scaled FP8 matrix product, dense or grouped by expert:
+ *   y[m][n] = sum over K blocks kb of a_scales[kb][m] * b_scales[e][n / 128][kb]
+ *             * sum over k in kb of a[m][k] * b[e][n][k]
+ * with fp32 sums and one rounding to y's type.
+ *   a        E4M3 [M][K], a_scales fp32 [ceil(K / 128)][M]
+ *   b        E4M3 [n_experts][N][K] (row-major, as a checkpoint has it),
+ *            b_scales fp32 [n_experts][ceil(N / 128)][ceil(K / 128)]
+ *   offsets  int32 [n_experts + 1] on the device: rows offsets[e] ..
+ *            offsets[e + 1] - 1 of a belong to expert e.  They must start at 0,
+ *            not descend and not pass M; rows of y behind the last are left as
+ *            they were.  NULL: dense, n_experts == 1.
+ *   y        [M][N] of y_type
+ * M 1..2^24, N a multiple of 8, K a multiple of 16 (both at most 2^17), up to
+ * 1024 experts.
+ */
+int flint_moe_block_gemm(const void *a, const float *a_scales, int M, const void *b,
+                         const float *b_scales, int n_experts, const int32_t *offsets, int N,
+                         int K, void *y, int y_type, flint_moe_stream_t stream);
+
+/*
+ * y[t] = bf16( sum over j of w[t][j] * rows[pos[t][j]] + shared[t] ), summed in
+ * fp32 in the order written.
+ *   rows    [n_rows][N] of rows_type; pos int32 [T][top_k] (a place outside
+ *           0..n_rows-1 adds nothing), w fp32 [T][top_k]
+ *   shared  bf16 [T][N] or NULL; y bf16 [T][N]
+ * T 1..2^20, top_k 1..16, N a multiple of 8, at most 2^17.
+ */
+int flint_moe_combine(const void *rows, int rows_type, int n_rows, const int32_t *pos,
+                      const float *w, int T, int top_k, int N, const void *shared, void *y,
+                      flint_moe_stream_t stream);
 
 /* Frees cached CUDA graphs of every device the calling thread used.  Call
  * before freeing buffers whose addresses a cached stack graph holds. */

@@ -10,14 +10,19 @@ from .flint_moe import (  # noqa: F401
     FlintLayer,
     FlintMoeError,
     alloc_workspace,
+    block_gemm,
+    combine,
     decode_layer,
     decode_stack,
     device_error,
+    group_pairs,
     load_library,
     pack_layer,
     pack_weights,
     packed_bytes,
     prefill_layer,
+    quantize_rows,
     release,
+    route,
     workspace_bytes,
 )

@@ -93,6 +93,8 @@ int device_state(DeviceState** out) {
     if (dense_kernels_init() != cudaSuccess) return FLINT_MOE_ERR_CUDA;
     if (medium_kernels_init() != cudaSuccess) return FLINT_MOE_ERR_CUDA;
     if (prefill_kernels_init(dev) != cudaSuccess) return FLINT_MOE_ERR_CUDA;
+    if (route_kernels_init() != cudaSuccess) return FLINT_MOE_ERR_CUDA;
+    if (block_gemm_kernels_init() != cudaSuccess) return FLINT_MOE_ERR_CUDA;
     if (cudaStreamCreateWithFlags(&s.capture_stream, cudaStreamNonBlocking) != cudaSuccess)
       return FLINT_MOE_ERR_CUDA;
     s.ready = true;
@@ -521,6 +523,150 @@ int flint_moe_dense_gemv(const void* packed, int N, int K, float tensor_scale, c
   if (st != FLINT_MOE_OK) return st;
   return to_status(launch_dense_gemv(packed, N, K, tensor_scale, x, B, y, ds->sm_count, ds->err,
                                      reinterpret_cast<cudaStream_t>(stream)));
+}
+
+// Largest row counts of the FP8 expert operators: tokens, and rows in expert
+// order (tokens x choices).
+static constexpr int OPS_MAX_TOKENS = 1 << 20;
+static constexpr int OPS_MAX_ROWS = 1 << 24;
+// Largest widths (a multiple of 8 outputs, of 16 inputs).
+static constexpr int OPS_MAX_N = 1 << 17;
+static constexpr int OPS_MAX_K = 1 << 17;
+
+int flint_moe_route(const flint_moe_routing* r, const void* logits, int logits_type, long long row_stride, int T,
+                    const float* bias, int32_t* ids, float* w, flint_moe_stream_t stream) {
+  if (r == nullptr) return FLINT_MOE_ERR_INVALID_ARG;
+  if (logits_type != FLINT_MOE_T_BF16 && logits_type != FLINT_MOE_T_F32) return FLINT_MOE_ERR_UNSUPPORTED;
+  if (r->score != FLINT_MOE_SCORE_SIGMOID && r->score != FLINT_MOE_SCORE_SOFTMAX) return FLINT_MOE_ERR_UNSUPPORTED;
+  if (r->group_score != FLINT_MOE_GROUP_MAX && r->group_score != FLINT_MOE_GROUP_TOP2) return FLINT_MOE_ERR_UNSUPPORTED;
+  if (r->n_experts < 1 || r->top_k < 1 || r->n_groups < 1 || r->top_groups < 1 || T < 1)
+    return FLINT_MOE_ERR_INVALID_ARG;
+  if (r->n_experts > ROUTE_MAX_E || r->top_k > ROUTE_MAX_K || r->n_groups > ROUTE_MAX_GROUPS || T > OPS_MAX_TOKENS)
+    return FLINT_MOE_ERR_UNSUPPORTED;
+  if (r->n_experts % r->n_groups != 0 || r->top_groups > r->n_groups ||
+      r->top_k > r->top_groups * (r->n_experts / r->n_groups))
+    return FLINT_MOE_ERR_INVALID_ARG;
+  if (!std::isfinite(r->scale)) return FLINT_MOE_ERR_INVALID_ARG;
+  if (row_stride < r->n_experts || row_stride > (1LL << 31)) return FLINT_MOE_ERR_INVALID_ARG;
+  if (logits == nullptr || ids == nullptr || w == nullptr) return FLINT_MOE_ERR_INVALID_ARG;
+  if (!aligned(logits, 16) || !aligned(ids, 16) || !aligned(w, 16) || !opt_aligned(bias))
+    return FLINT_MOE_ERR_INVALID_ARG;
+  const bool bf16 = logits_type == FLINT_MOE_T_BF16;
+  const size_t sel = (size_t)T * r->top_k * 4;
+  const size_t in = ((size_t)(T - 1) * (size_t)row_stride + r->n_experts) * (bf16 ? 2 : 4);
+  if (outputs_overlap({{ids, sel}, {w, sel}}, {{logits, in}, {bias, (size_t)r->n_experts * 4}}))
+    return FLINT_MOE_ERR_INVALID_ARG;
+  RouteSpec s;
+  s.E = r->n_experts;
+  s.top_k = r->top_k;
+  s.n_groups = r->top_groups == r->n_groups ? 1 : r->n_groups;  // every group kept: no groups
+  s.top_groups = r->top_groups;
+  s.softmax = r->score == FLINT_MOE_SCORE_SOFTMAX;
+  s.top2 = r->group_score == FLINT_MOE_GROUP_TOP2;
+  s.renorm = r->renormalise != 0;
+  s.scale = r->scale;
+  std::lock_guard<std::mutex> lk(g_mu);
+  DeviceState* ds = nullptr;
+  int st = device_state(&ds);
+  if (st != FLINT_MOE_OK) return st;
+  return to_status(launch_route(s, logits, bf16, row_stride, T, bias, ids, w, reinterpret_cast<cudaStream_t>(stream)));
+}
+
+int flint_moe_group_pairs(const int32_t* ids, int n_pairs, int n_experts, int32_t* offsets, int32_t* order,
+                          int32_t* pos, flint_moe_stream_t stream) {
+  if (n_pairs < 1 || n_experts < 1) return FLINT_MOE_ERR_INVALID_ARG;
+  if (n_pairs > OPS_MAX_ROWS || n_experts > ROUTE_MAX_E) return FLINT_MOE_ERR_UNSUPPORTED;
+  if (ids == nullptr || offsets == nullptr || order == nullptr || pos == nullptr) return FLINT_MOE_ERR_INVALID_ARG;
+  if (!aligned(ids, 16) || !aligned(offsets, 16) || !aligned(order, 16) || !aligned(pos, 16))
+    return FLINT_MOE_ERR_INVALID_ARG;
+  const size_t n = (size_t)n_pairs * 4;
+  if (outputs_overlap({{offsets, (size_t)(n_experts + 1) * 4}, {order, n}, {pos, n}}, {{ids, n}}))
+    return FLINT_MOE_ERR_INVALID_ARG;
+  std::lock_guard<std::mutex> lk(g_mu);
+  DeviceState* ds = nullptr;
+  int st = device_state(&ds);
+  if (st != FLINT_MOE_OK) return st;
+  return to_status(
+      launch_group_pairs(ids, n_pairs, n_experts, offsets, order, pos, reinterpret_cast<cudaStream_t>(stream)));
+}
+
+int flint_moe_quantize_rows(const void* x, int x_type, long long row_stride, int rows, int K, int silu_mul,
+                            const int32_t* pos, int top_k, int places, void* q, float* scales,
+                            flint_moe_stream_t stream) {
+  if (x_type != FLINT_MOE_T_BF16 && x_type != FLINT_MOE_T_F32) return FLINT_MOE_ERR_UNSUPPORTED;
+  if (rows < 1 || K < 1 || places < 1 || (pos != nullptr && top_k < 1)) return FLINT_MOE_ERR_INVALID_ARG;
+  if (rows > OPS_MAX_ROWS || places > OPS_MAX_ROWS || K % 16 != 0 || K > OPS_MAX_K ||
+      (pos != nullptr && top_k > ROUTE_MAX_K))
+    return FLINT_MOE_ERR_UNSUPPORTED;
+  if (pos == nullptr && places != rows) return FLINT_MOE_ERR_INVALID_ARG;
+  const long long size = x_type == FLINT_MOE_T_BF16 ? 2 : 4, width = silu_mul ? 2LL * K : K;
+  if (row_stride < width || row_stride > (1LL << 31)) return FLINT_MOE_ERR_INVALID_ARG;
+  if (row_stride * size % 16 != 0) return FLINT_MOE_ERR_UNSUPPORTED;
+  if (x == nullptr || q == nullptr || scales == nullptr) return FLINT_MOE_ERR_INVALID_ARG;
+  if (!aligned(x, 16) || !aligned(q, 16) || !aligned(scales, 16) || !opt_aligned(pos)) return FLINT_MOE_ERR_INVALID_ARG;
+  const size_t in = (size_t)((rows - 1) * row_stride + width) * (size_t)size;
+  if (outputs_overlap({{q, (size_t)places * K}, {scales, (size_t)places * ((K + 127) / 128) * 4}},
+                      {{x, in}, {pos, (size_t)rows * (pos ? top_k : 0) * 4}}))
+    return FLINT_MOE_ERR_INVALID_ARG;
+  std::lock_guard<std::mutex> lk(g_mu);
+  DeviceState* ds = nullptr;
+  int st = device_state(&ds);
+  if (st != FLINT_MOE_OK) return st;
+  return to_status(launch_quantize_rows(x, x_type == FLINT_MOE_T_BF16, row_stride, rows, K, silu_mul != 0, pos, top_k,
+                                        places, q, scales, reinterpret_cast<cudaStream_t>(stream)));
+}
+
+int flint_moe_block_gemm(const void* a, const float* a_scales, int M, const void* b, const float* b_scales,
+                         int n_experts, const int32_t* offsets, int N, int K, void* y, int y_type,
+                         flint_moe_stream_t stream) {
+  if (y_type != FLINT_MOE_T_BF16 && y_type != FLINT_MOE_T_F32) return FLINT_MOE_ERR_UNSUPPORTED;
+  if (M < 1 || N < 1 || K < 1 || n_experts < 1) return FLINT_MOE_ERR_INVALID_ARG;
+  if (M > OPS_MAX_ROWS || n_experts > ROUTE_MAX_E || N % 8 != 0 || N > OPS_MAX_N || K % 16 != 0 || K > OPS_MAX_K)
+    return FLINT_MOE_ERR_UNSUPPORTED;
+  if (offsets == nullptr && n_experts != 1) return FLINT_MOE_ERR_INVALID_ARG;
+  if (a == nullptr || a_scales == nullptr || b == nullptr || b_scales == nullptr || y == nullptr)
+    return FLINT_MOE_ERR_INVALID_ARG;
+  if (!aligned(a, 16) || !aligned(a_scales, 16) || !aligned(b, 16) || !aligned(b_scales, 16) || !aligned(y, 16) ||
+      !opt_aligned(offsets))
+    return FLINT_MOE_ERR_INVALID_ARG;
+  const size_t kb = (size_t)(K + 127) / 128, nb = (size_t)(N + 127) / 128;
+  if (outputs_overlap({{y, (size_t)M * N * (y_type == FLINT_MOE_T_BF16 ? 2 : 4)}},
+                      {{a, (size_t)M * K},
+                       {a_scales, (size_t)M * kb * 4},
+                       {b, (size_t)n_experts * N * K},
+                       {b_scales, (size_t)n_experts * nb * kb * 4},
+                       {offsets, (size_t)(n_experts + 1) * 4}}))
+    return FLINT_MOE_ERR_INVALID_ARG;
+  std::lock_guard<std::mutex> lk(g_mu);
+  DeviceState* ds = nullptr;
+  int st = device_state(&ds);
+  if (st != FLINT_MOE_OK) return st;
+  return to_status(launch_block_gemm(a, a_scales, M, b, b_scales, n_experts, offsets, N, K, y,
+                                     y_type == FLINT_MOE_T_F32, ds->sm_count, ds->err,
+                                     reinterpret_cast<cudaStream_t>(stream)));
+}
+
+int flint_moe_combine(const void* rows, int rows_type, int n_rows, const int32_t* pos, const float* w, int T,
+                      int top_k, int N, const void* shared, void* y, flint_moe_stream_t stream) {
+  if (rows_type != FLINT_MOE_T_BF16 && rows_type != FLINT_MOE_T_F32) return FLINT_MOE_ERR_UNSUPPORTED;
+  if (n_rows < 1 || T < 1 || top_k < 1 || N < 1) return FLINT_MOE_ERR_INVALID_ARG;
+  if (n_rows > OPS_MAX_ROWS || T > OPS_MAX_TOKENS || top_k > ROUTE_MAX_K || N % 8 != 0 || N > OPS_MAX_N)
+    return FLINT_MOE_ERR_UNSUPPORTED;
+  if (rows == nullptr || pos == nullptr || w == nullptr || y == nullptr) return FLINT_MOE_ERR_INVALID_ARG;
+  if (!aligned(rows, 16) || !aligned(pos, 16) || !aligned(w, 16) || !aligned(y, 16) || !opt_aligned(shared))
+    return FLINT_MOE_ERR_INVALID_ARG;
+  const size_t act = (size_t)T * N * 2, sel = (size_t)T * top_k * 4;
+  if (outputs_overlap({{y, act}}, {{rows, (size_t)n_rows * N * (rows_type == FLINT_MOE_T_BF16 ? 2 : 4)},
+                                   {pos, sel},
+                                   {w, sel},
+                                   {shared, act}}))
+    return FLINT_MOE_ERR_INVALID_ARG;
+  std::lock_guard<std::mutex> lk(g_mu);
+  DeviceState* ds = nullptr;
+  int st = device_state(&ds);
+  if (st != FLINT_MOE_OK) return st;
+  return to_status(launch_combine(rows, rows_type == FLINT_MOE_T_BF16, n_rows, pos, w, T, top_k, N, shared, y,
+                                  reinterpret_cast<cudaStream_t>(stream)));
 }
 
 int flint_moe_release(void) {

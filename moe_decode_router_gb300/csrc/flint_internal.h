@@ -153,6 +153,33 @@ cudaError_t launch_pack_dense(const uint8_t* codes, const uint8_t* scales, int N
 cudaError_t launch_dense_gemv(const void* packed, int N, int K, float ts, const void* x, int B, void* y, int sm_count,
                               unsigned* err, cudaStream_t st);
 
+// Routing from given logits, and grouping of pairs by expert (route.cu).
+constexpr int ROUTE_MAX_E = 1024;
+constexpr int ROUTE_MAX_K = 16;
+constexpr int ROUTE_MAX_GROUPS = 32;
+struct RouteSpec {
+  int E, top_k, n_groups, top_groups, softmax, top2, renorm;
+  float scale;
+};
+cudaError_t route_kernels_init();
+cudaError_t launch_route(const RouteSpec& r, const void* logits, bool bf16, long long stride, int T, const float* bias,
+                         int32_t* ids, float* w, cudaStream_t st);
+cudaError_t launch_group_pairs(const int32_t* ids, int P, int E, int32_t* offsets, int32_t* order, int32_t* pos,
+                               cudaStream_t st);
+
+// Quantisation of rows in blocks of 128, and the weighted combine (rows.cu).
+cudaError_t launch_quantize_rows(const void* x, bool bf16, long long stride, int rows, int K, bool silu,
+                                 const int32_t* pos, int top_k, long long places, void* q, float* scales,
+                                 cudaStream_t st);
+cudaError_t launch_combine(const void* rows, bool bf16, long long n_rows, const int32_t* pos, const float* w, int T,
+                           int top_k, int N, const void* shared, void* y, cudaStream_t st);
+
+// Block-scaled FP8 matrix product, dense or grouped by expert (block_gemm.cu).
+cudaError_t block_gemm_kernels_init();
+cudaError_t launch_block_gemm(const void* a, const float* sa, int M, const void* b, const float* sb, int E,
+                              const int32_t* offsets, int N, int K, void* y, bool f32, int sm_count, unsigned* err,
+                              cudaStream_t st);
+
 cudaError_t launch_pack(int fmt, const void* gate_up, const uint8_t* gu_scales, const void* down,
                         const uint8_t* dn_scales, void* packed, cudaStream_t st);
 

@@ -1,0 +1,201 @@
+// Row-wise operators around the FP8 expert products: quantisation of rows in
+// blocks of 128 (with the gated activation in the same pass, and written to
+// every place that the routing gives a row), and the weighted combine.
+#include "flint_common.cuh"
+#include "flint_internal.h"
+
+namespace flint {
+
+namespace {
+
+__device__ __forceinline__ void bf16x8_to_f32(const uint4 r, float (&v)[8]) {
+  const uint32_t w[4] = {r.x, r.y, r.z, r.w};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    v[2 * i] = __uint_as_float(w[i] << 16);
+    v[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
+  }
+}
+template <bool BF16>
+__device__ __forceinline__ void load8(const void* base, size_t at, float (&v)[8]) {
+  if (BF16) {
+    bf16x8_to_f32(__ldg(reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(base) + at)), v);
+  } else {
+    const float4* s = reinterpret_cast<const float4*>(static_cast<const float*>(base) + at);
+    const float4 a = __ldg(s), b = __ldg(s + 1);
+    v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w;
+    v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
+  }
+}
+
+__device__ __forceinline__ uint32_t e4m3x2(float lo, float hi) {
+  uint16_t r;
+  asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(r) : "f"(hi), "f"(lo));
+  return r;
+}
+
+// Smallest block maximum that a scale is made for: 448 / 2^-96 stays finite.
+constexpr float Q_FLOOR = 1.262177448353618888658765704e-29f;  // 2^-96
+constexpr float E4M3_TOP = 448.f;
+
+struct QuantParams {
+  const void* x;
+  long long stride;
+  int rows, K, kb;  // kb: blocks of a row
+  const int32_t* pos;
+  int top_k;
+  long long places;  // rows of q and of a scale line
+  uint8_t* q;
+  float* scales;
+};
+
+// 16 lanes per block of 128, 8 values each.  The block's largest magnitude a
+// (NaN if the block holds one) gives scale = a / 448 and codes
+// e4m3(x * (448 / a)), one rounding to nearest even.
+template <bool BF16, bool SILU>
+__global__ void __launch_bounds__(256) quantize_kernel(const QuantParams p) {
+  pdl_wait();
+  pdl_trigger();
+  const int lane = threadIdx.x & 15;
+  const long long unit = (long long)blockIdx.x * 16 + (threadIdx.x >> 4);
+  const bool live = unit < (long long)p.rows * p.kb;
+  const int row = live ? (int)(unit / p.kb) : 0, b = live ? (int)(unit % p.kb) : 0;
+  const int k = b * 128 + lane * 8;
+  const bool in = live && k < p.K;  // K is a multiple of 16
+  float v[8];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) v[i] = 0.f;
+  if (in) {
+    const size_t at = (size_t)row * (size_t)p.stride + (size_t)k;
+    load8<BF16>(p.x, at, v);
+    if (SILU) {
+      float u[8];
+      load8<BF16>(p.x, at + (size_t)p.K, u);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) v[i] = v[i] / (1.f + __expf(-v[i])) * u[i];
+    }
+  }
+  // Magnitudes compare as integers; NaN's is above every other.
+  uint32_t m = 0u;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) m = max(m, __float_as_uint(v[i]) & 0x7FFFFFFFu);
+#pragma unroll
+  for (int off = 8; off > 0; off >>= 1) m = max(m, __shfl_xor_sync(0xffffffffu, m, off));
+  float a = __uint_as_float(m);
+  if (a < Q_FLOOR) a = Q_FLOOR;  // false for NaN
+  const float scale = __fdiv_rn(a, E4M3_TOP), r = __fdiv_rn(E4M3_TOP, a);
+  uint32_t c[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) c[i] = e4m3x2(v[2 * i] * r, v[2 * i + 1] * r);
+  if (!in) return;
+  const uint2 code = make_uint2(c[0] | (c[1] << 16), c[2] | (c[3] << 16));
+  const int n = p.pos != nullptr ? p.top_k : 1;
+  for (int j = 0; j < n; ++j) {
+    const long long to = p.pos != nullptr ? __ldg(p.pos + (size_t)row * p.top_k + j) : row;
+    if (to < 0 || to >= p.places) continue;
+    *reinterpret_cast<uint2*>(p.q + (size_t)to * p.K + k) = code;
+    if (lane == 0) p.scales[(size_t)b * p.places + to] = scale;
+  }
+}
+
+struct CombineParams {
+  const void* rows;
+  long long n_rows;
+  const int32_t* pos;
+  const float* w;
+  const uint16_t* shared;
+  uint16_t* y;
+  int T, N, top_k;
+};
+
+// One thread per 8 outputs; the sum runs over the choices in order, then the
+// shared row, in fp32, and is rounded once to bf16.
+template <bool BF16>
+__global__ void __launch_bounds__(256) combine_kernel(const CombineParams p) {
+  pdl_wait();
+  pdl_trigger();
+  const int per = p.N / 8;
+  const long long u = (long long)blockIdx.x * 256 + threadIdx.x;
+  if (u >= (long long)p.T * per) return;
+  const int t = (int)(u / per), n = (int)(u % per) * 8;
+  float acc[8];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) acc[i] = 0.f;
+  for (int j = 0; j < p.top_k; ++j) {
+    const int r = __ldg(p.pos + (size_t)t * p.top_k + j);
+    if (r < 0 || r >= p.n_rows) continue;
+    const float w = __ldg(p.w + (size_t)t * p.top_k + j);
+    float v[8];
+    load8<BF16>(p.rows, (size_t)r * p.N + n, v);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) acc[i] = fmaf(w, v[i], acc[i]);
+  }
+  if (p.shared != nullptr) {
+    float v[8];
+    load8<true>(p.shared, (size_t)t * p.N + n, v);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) acc[i] += v[i];
+  }
+  uint32_t o[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const __nv_bfloat162 h = __floats2bfloat162_rn(acc[2 * i], acc[2 * i + 1]);
+    o[i] = *reinterpret_cast<const uint32_t*>(&h);
+  }
+  *reinterpret_cast<uint4*>(p.y + (size_t)t * p.N + n) = make_uint4(o[0], o[1], o[2], o[3]);
+}
+
+template <typename P>
+cudaError_t launch_pdl(void (*kernel)(const P), const P& p, long long ctas, int threads, cudaStream_t st) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)ctas);
+  cfg.blockDim = dim3(threads);
+  cfg.stream = st;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kernel, p);
+}
+
+}  // namespace
+
+cudaError_t launch_quantize_rows(const void* x, bool bf16, long long stride, int rows, int K, bool silu,
+                                 const int32_t* pos, int top_k, long long places, void* q, float* scales,
+                                 cudaStream_t st) {
+  QuantParams p;
+  p.x = x;
+  p.stride = stride;
+  p.rows = rows;
+  p.K = K;
+  p.kb = (K + 127) / 128;
+  p.pos = pos;
+  p.top_k = top_k;
+  p.places = places;
+  p.q = static_cast<uint8_t*>(q);
+  p.scales = scales;
+  const long long ctas = ((long long)rows * p.kb + 15) / 16;
+  if (bf16) return silu ? launch_pdl(quantize_kernel<true, true>, p, ctas, 256, st)
+                        : launch_pdl(quantize_kernel<true, false>, p, ctas, 256, st);
+  return silu ? launch_pdl(quantize_kernel<false, true>, p, ctas, 256, st)
+              : launch_pdl(quantize_kernel<false, false>, p, ctas, 256, st);
+}
+
+cudaError_t launch_combine(const void* rows, bool bf16, long long n_rows, const int32_t* pos, const float* w, int T,
+                           int top_k, int N, const void* shared, void* y, cudaStream_t st) {
+  CombineParams p;
+  p.rows = rows;
+  p.n_rows = n_rows;
+  p.pos = pos;
+  p.w = w;
+  p.shared = static_cast<const uint16_t*>(shared);
+  p.y = static_cast<uint16_t*>(y);
+  p.T = T;
+  p.N = N;
+  p.top_k = top_k;
+  const long long ctas = ((long long)T * (N / 8) + 255) / 256;
+  return bf16 ? launch_pdl(combine_kernel<true>, p, ctas, 256, st) : launch_pdl(combine_kernel<false>, p, ctas, 256, st);
+}
+
+}  // namespace flint

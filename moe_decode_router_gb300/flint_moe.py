@@ -29,6 +29,17 @@ W_BF16 = 1
 DECODE_CHAINED = 0
 DECODE_PERSISTENT = 1
 
+T_BF16 = 0
+T_F32 = 1
+
+SCORE_SIGMOID = 0
+SCORE_SOFTMAX = 1
+
+GROUP_MAX = 0
+GROUP_TOP2 = 1
+
+SCALE_BLOCK = 128  # elements of K that share a scale (and rows of a weight matrix)
+
 HIDDEN, N_EXPERTS, N_SHARED, INTER, TOP_K = 2048, 256, 1, 512, 6
 MAX_DECODE_BATCH = 8
 MAX_MEDIUM_BATCH = 64  # decode calls with 9..64 tokens take the medium-batch kernels (NVFP4)
@@ -46,6 +57,14 @@ class Dims(ctypes.Structure):
         ("hidden", ctypes.c_int), ("n_experts", ctypes.c_int), ("n_shared", ctypes.c_int),
         ("inter", ctypes.c_int), ("top_k", ctypes.c_int), ("weight_dtype", ctypes.c_int),
         ("rms_eps", ctypes.c_float),
+    ]
+
+
+class Routing(ctypes.Structure):
+    _fields_ = [
+        ("n_experts", ctypes.c_int), ("top_k", ctypes.c_int), ("score", ctypes.c_int), ("n_groups", ctypes.c_int),
+        ("top_groups", ctypes.c_int), ("group_score", ctypes.c_int), ("renormalise", ctypes.c_int),
+        ("scale", ctypes.c_float),
     ]
 
 
@@ -83,6 +102,20 @@ _SIGS = {
                                             ctypes.c_void_p, ctypes.c_size_t, ctypes.c_void_p]),
     "flint_moe_dense_gemv": (ctypes.c_int, [ctypes.c_void_p, ctypes.c_int, ctypes.c_int, ctypes.c_float,
                                             ctypes.c_void_p, ctypes.c_int, ctypes.c_void_p, ctypes.c_void_p]),
+    "flint_moe_route": (ctypes.c_int, [ctypes.POINTER(Routing), ctypes.c_void_p, ctypes.c_int, ctypes.c_longlong,
+                                       ctypes.c_int, ctypes.c_void_p, ctypes.c_void_p, ctypes.c_void_p,
+                                       ctypes.c_void_p]),
+    "flint_moe_group_pairs": (ctypes.c_int, [ctypes.c_void_p, ctypes.c_int, ctypes.c_int, ctypes.c_void_p,
+                                             ctypes.c_void_p, ctypes.c_void_p, ctypes.c_void_p]),
+    "flint_moe_quantize_rows": (ctypes.c_int, [ctypes.c_void_p, ctypes.c_int, ctypes.c_longlong, ctypes.c_int,
+                                               ctypes.c_int, ctypes.c_int, ctypes.c_void_p, ctypes.c_int, ctypes.c_int,
+                                               ctypes.c_void_p, ctypes.c_void_p, ctypes.c_void_p]),
+    "flint_moe_block_gemm": (ctypes.c_int, [ctypes.c_void_p, ctypes.c_void_p, ctypes.c_int, ctypes.c_void_p,
+                                            ctypes.c_void_p, ctypes.c_int, ctypes.c_void_p, ctypes.c_int, ctypes.c_int,
+                                            ctypes.c_void_p, ctypes.c_int, ctypes.c_void_p]),
+    "flint_moe_combine": (ctypes.c_int, [ctypes.c_void_p, ctypes.c_int, ctypes.c_int, ctypes.c_void_p, ctypes.c_void_p,
+                                         ctypes.c_int, ctypes.c_int, ctypes.c_int, ctypes.c_void_p, ctypes.c_void_p,
+                                         ctypes.c_void_p]),
     "flint_moe_release": (ctypes.c_int, []),
     "flint_moe_device_error": (ctypes.c_int, [ctypes.c_int]),
     "flint_moe_device_status": (ctypes.c_int, [ctypes.c_int]),
@@ -344,6 +377,126 @@ def dense_gemv(w: DenseNVFP4, x, y, stream=None):
     _expect(w.packed, "packed", torch.uint8, None)
     rc = _lib().flint_moe_dense_gemv(_ptr(w.packed), w.N, w.K, w.tensor_scale, _ptr(x), B, _ptr(y), _stream(stream))
     _check(rc, "flint_moe_dense_gemv")
+
+
+def _expect_rows(t, name, types, width):
+    """_expect for a matrix whose rows may lie apart: dtype one of `types`, last
+    dimension contiguous, on the current CUDA device.  Returns (type code, rows,
+    row stride in elements)."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name}: expected a torch.Tensor, got {type(t).__name__}")
+    if t.dtype not in types:
+        raise ValueError(f"{name}: dtype {t.dtype}, expected {' or '.join(str(d) for d in types)}")
+    shape = t.shape
+    if len(shape) != 2 or (width is not None and shape[1] != width):
+        raise ValueError(f"{name}: shape {tuple(shape)}, expected [rows][{'columns' if width is None else width}]")
+    rows = shape[0]
+    stride = t.stride()
+    if stride[1] != 1 and shape[1] != 1:
+        raise ValueError(f"{name}: the elements of a row must be contiguous")
+    if not t.is_cuda or t.get_device() != torch.cuda.current_device():
+        raise ValueError(f"{name}: must be on the current CUDA device")
+    return types[t.dtype], rows, (stride[0] if rows > 1 else shape[1])
+
+
+_ACT_TYPES = {torch.bfloat16: T_BF16, torch.float32: T_F32}
+
+
+def route(logits, ids, w, bias=None, score=SCORE_SIGMOID, n_groups=1, top_groups=1, group_score=GROUP_MAX,
+          renormalise=True, scale=1.0, stream=None):
+    """Chooses ids.shape[1] experts for every row of logits [T][E] (bf16 or fp32, rows may lie
+    apart): ids int32 [T][k], w fp32 [T][k].  bias fp32 [E] is added for the choice only."""
+    kind, T, stride = _expect_rows(logits, "logits", _ACT_TYPES, None)
+    E = logits.shape[1]
+    k = ids.shape[1] if isinstance(ids, torch.Tensor) and ids.dim() == 2 else 0
+    _expect(ids, "ids", torch.int32, (T, k))
+    _expect(w, "w", torch.float32, (T, k))
+    if bias is not None:
+        _expect(bias, "bias", torch.float32, (E,))
+    r = Routing(E, k, score, n_groups, top_groups, group_score, 1 if renormalise else 0, scale)
+    rc = _lib().flint_moe_route(ctypes.byref(r), logits.data_ptr(), kind, stride, T, _ptr(bias), ids.data_ptr(),
+                                w.data_ptr(), _stream(stream))
+    _check(rc, "flint_moe_route")
+
+
+def group_pairs(ids, offsets, order, pos, stream=None):
+    """Sorts the pairs of ids (int32, any shape) by expert: offsets int32 [E + 1], order int32
+    [pairs], pos int32 of the shape of ids."""
+    if not isinstance(ids, torch.Tensor) or not isinstance(offsets, torch.Tensor):
+        raise TypeError("ids, offsets: expected a torch.Tensor")
+    n, E = ids.numel(), offsets.numel() - 1
+    _expect(ids, "ids", torch.int32, ids.shape)
+    _expect(offsets, "offsets", torch.int32, (E + 1,))
+    _expect(order, "order", torch.int32, (n,))
+    _expect(pos, "pos", torch.int32, ids.shape)
+    rc = _lib().flint_moe_group_pairs(ids.data_ptr(), n, E, offsets.data_ptr(), order.data_ptr(), pos.data_ptr(),
+                                      _stream(stream))
+    _check(rc, "flint_moe_group_pairs")
+
+
+def quantize_rows(x, q, scales, pos=None, silu_mul=False, stream=None):
+    """Quantises x [rows][K] (bf16 or fp32; silu_mul: [rows][2K], silu(first half) * second
+    half) to q float8_e4m3fn [places][K] and scales fp32 [ceil(K / 128)][places]; pos int32
+    [rows][k] gives the places of each row, None: row i goes to place i."""
+    if not isinstance(q, torch.Tensor):
+        raise TypeError(f"q: expected a torch.Tensor, got {type(q).__name__}")
+    if q.dim() != 2:
+        raise ValueError(f"q: expected [places][K], got shape {tuple(q.shape)}")
+    places, K = q.shape
+    kind, rows, stride = _expect_rows(x, "x", _ACT_TYPES, 2 * K if silu_mul else K)
+    _expect(q, "q", torch.float8_e4m3fn, (places, K))
+    _expect(scales, "scales", torch.float32, (-(-K // SCALE_BLOCK), places))
+    k = 0
+    if pos is not None:
+        k = pos.shape[1] if isinstance(pos, torch.Tensor) and pos.dim() == 2 else 0
+        _expect(pos, "pos", torch.int32, (rows, k))
+    rc = _lib().flint_moe_quantize_rows(x.data_ptr(), kind, stride, rows, K, 1 if silu_mul else 0, _ptr(pos), k,
+                                        places, q.data_ptr(), scales.data_ptr(), _stream(stream))
+    _check(rc, "flint_moe_quantize_rows")
+
+
+def block_gemm(a, a_scales, b, b_scales, y, offsets=None, stream=None):
+    """y [M][N] (bf16 or fp32) = a @ b^T of E4M3 operands with block scales: a float8_e4m3fn
+    [M][K], a_scales fp32 [ceil(K / 128)][M], b [experts][N][K], b_scales
+    [experts][ceil(N / 128)][ceil(K / 128)].  offsets int32 [experts + 1] gives every expert
+    its rows of a; None: dense (b of one expert)."""
+    if not isinstance(b, torch.Tensor):
+        raise TypeError(f"b: expected a torch.Tensor, got {type(b).__name__}")
+    if b.dim() != 3:
+        raise ValueError(f"b: expected [experts][N][K], got shape {tuple(b.shape)}")
+    E, N, K = b.shape
+    kb = -(-K // SCALE_BLOCK)
+    kind, M, stride = _expect_rows(y, "y", _ACT_TYPES, N)
+    if stride != N:
+        raise ValueError("y: must be contiguous")
+    _expect(a, "a", torch.float8_e4m3fn, (M, K))
+    _expect(a_scales, "a_scales", torch.float32, (kb, M))
+    _expect(b, "b", torch.float8_e4m3fn, (E, N, K))
+    _expect(b_scales, "b_scales", torch.float32, (E, -(-N // SCALE_BLOCK), kb))
+    if offsets is not None:
+        _expect(offsets, "offsets", torch.int32, (E + 1,))
+    rc = _lib().flint_moe_block_gemm(a.data_ptr(), a_scales.data_ptr(), M, b.data_ptr(), b_scales.data_ptr(), E,
+                                     _ptr(offsets), N, K, y.data_ptr(), kind, _stream(stream))
+    _check(rc, "flint_moe_block_gemm")
+
+
+def combine(rows, pos, w, y, shared=None, stream=None):
+    """y [T][N] (bf16) = sum over j of w[t][j] * rows[pos[t][j]] (+ shared [T][N] bf16); rows
+    bf16 or fp32 [any][N], pos int32 and w fp32 [T][k]; pos outside the rows adds nothing."""
+    T = _rows(y, "y")
+    N = y.shape[1]
+    kind, n_rows, stride = _expect_rows(rows, "rows", _ACT_TYPES, N)
+    if stride != N:
+        raise ValueError("rows: must be contiguous")
+    k = pos.shape[1] if isinstance(pos, torch.Tensor) and pos.dim() == 2 else 0
+    _expect(y, "y", torch.bfloat16, (T, N))
+    _expect(pos, "pos", torch.int32, (T, k))
+    _expect(w, "w", torch.float32, (T, k))
+    if shared is not None:
+        _expect(shared, "shared", torch.bfloat16, (T, N))
+    rc = _lib().flint_moe_combine(rows.data_ptr(), kind, n_rows, pos.data_ptr(), w.data_ptr(), T, k, N, _ptr(shared),
+                                  y.data_ptr(), _stream(stream))
+    _check(rc, "flint_moe_combine")
 
 
 def release():
