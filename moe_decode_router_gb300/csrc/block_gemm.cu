@@ -374,7 +374,7 @@ __global__ void __launch_bounds__(TC_THREADS, 1)
             tc05::fence_after_sync();
             const uint64_t da = da0 + (uint64_t)(s * (C::STAGE >> 4)), db = db0 + (uint64_t)(s * (C::STAGE >> 4));
             const uint32_t d = tmem + b * NT;
-  #pragma unroll
+#pragma unroll
             for (int k = 0; k < 4; ++k) tc05::mma_e4m3_pair(d, da + 2 * k, db + 2 * k, idesc, k > 0 ? 1u : 0u);
             tc05::commit_pair(&empty[s]);
             tc05::commit_pair(&tfull[b]);
@@ -411,7 +411,7 @@ __global__ void __launch_bounds__(TC_THREADS, 1)
           }
           float* slot = ring + s * C::SLOT_FLOATS;
           const float* sa = p.sa + (size_t)kb * p.M + t.row0;
-  #pragma unroll
+#pragma unroll
           for (int i = 0; i < NT / 32; ++i) {
             const int c = lane + 32 * i;
             if (c < t.n) {
