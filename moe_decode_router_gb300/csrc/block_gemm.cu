@@ -6,6 +6,8 @@
 // and added in fp32.
 #include <cuda.h>
 
+#include <type_traits>
+
 #include "flint_common.cuh"
 #include "flint_internal.h"
 #include "tc05.cuh"
@@ -124,48 +126,63 @@ __global__ void __launch_bounds__(SK_WARPS * 32) block_gemm_skinny_kernel(const 
   }
 }
 
-// ---- many rows: tcgen05 over pairs of CTAs.
+// ---- many rows: tcgen05.
 //
-// The weights are the M side (256 weight rows per pair, 128 per CTA, always
-// full) and the activation rows the N side, which takes any multiple of 32 up
-// to NT: a ragged group of an expert wastes at most 31 columns.  The block
-// scales allow the tensor cores 128 of K at a time: every K block is a fresh
-// accumulator in tensor memory (NBUF of them in a ring), and eight warps per
-// CTA read it back and add it, scaled, into fp32 registers while the next
-// block is multiplied.
+// The block scales allow the tensor cores 128 of K at a time: every K block is
+// a fresh accumulator in tensor memory, and eight promotion warps read it back
+// and add it, scaled, into fp32 registers while the next blocks are multiplied.
+// The rate is set by how much tensor memory is under way: an accumulator is
+// free again only after its MMAs, a barrier, the read and a barrier back, so
+// accumulators are small (128 or 64 columns) and there are four or eight, and
+// the barriers stay inside one SM (with cta_group::2 each hand-over crosses
+// SMs: 1.1 us a round trip, 2.0 PFLOP/s where this reaches more).  Two
+// arrangements of the same pipeline:
 //
-// Per SM and K block at NT = 256: 512 cycles of MMA, against 128 KB of tensor
-// memory read and 16,384 packed fma for the promotion, about 256 cycles each,
-// that overlap with it; 32 KB of operands from L2 (64 B per cycle).
+// TALL (long groups).  128 rows of a are the M side and 256 weight rows the N
+// side.  A thread holds one row of a (its tensor-memory lane) and 128 outputs,
+// all with one scale a K block, the product of the row's and the weight
+// block's: per K block and SM 512 cycles of MMA, 256 of tensor-memory reads
+// (32x32b; the 16-lane forms read at half that rate) and 256 of packed fma,
+// which overlap.  Two CTAs with the same weight tile form a cluster: each
+// loads half of it for both (TMA multicast), 32 KB a K block from L2 per SM.
 //
-// Tensor memory is read in 16x256b form: a thread holds 4 weight rows x pairs
-// of neighbouring columns, so a pair of column scales, read once from shared
-// memory, serves 4 packed fma.
+// WIDE (short groups).  128 weight rows are the M side, always full, and up to
+// 64 rows of a the N side in steps of 16, so that a group of few rows costs
+// little more than its weights' bytes.  Scales differ by column: tensor memory
+// is read in 16x256b form, where a thread holds 4 weight rows x pairs of
+// neighbouring columns, so that a pair of column scales, read once from a ring
+// in shared memory, serves 4 packed fma.
 //
-// Warps: 0 TMA producer, 1 MMA issuer (even CTA), 2 scale loader, 3 tensor
-// memory; 4-7 and 8-11 promotion and output, one column half each.
+// Warps: 0-7 promotion and output, two column halves; 8 TMA producer; 9 and 11
+// MMA issuers; 10 loader of column scales (WIDE).
 constexpr int TC_THREADS = 384;
-constexpr int TC_A_BYTES = 128 * 128;
-// Registers at NT = 256: the promotion warps hold 128 accumulators each and
-// take what the other four warps give up.  Launched with 168 a thread.
-constexpr int TC_REGS = 168, TC_REGS_LOW = 56, TC_REGS_HIGH = 216;
+// Registers of TALL: the promotion warps hold 128 accumulators each and take
+// what the other four warps give up.  Launched with 168 a thread.
+constexpr int TC_REGS = 168, TC_REGS_LOW = 48, TC_REGS_HIGH = 224;
 static_assert(TC_REGS_HIGH * 256 + TC_REGS_LOW * 128 <= TC_REGS * TC_THREADS, "register shares");
 
-template <int NT>
+template <bool TALL>
 struct TcCfg {
-  static constexpr int NBUF = 512 / NT;
-  static constexpr int B_BYTES = NT / 2 * 128;
-  static constexpr int STAGE = TC_A_BYTES + B_BYTES;
-  static constexpr int STAGES = NT == 256 ? 6 : 9;
-  static constexpr int SLOTS = 4;                // scale ring
-  static constexpr int SLOT_FLOATS = NT + 4;     // column scales, then the weight scale
-  static constexpr int OUT_WARP = 16 * 80;       // 16 rows of y x 32 columns, 80-byte pitch
+  static constexpr int CTAS = TALL ? 2 : 1;        // of a cluster
+  static constexpr int ROWS = TALL ? 256 : 64;     // rows of a in a unit
+  static constexpr int WROWS = TALL ? 256 : 128;   // weight rows in a unit
+  static constexpr int ACC = TALL ? 128 : 64;      // columns of an accumulator
+  static constexpr int NBUF = 512 / ACC;
+  static constexpr int X_BYTES = TALL ? 128 * 128 : 64 * 128;  // rows of a in a stage
+  static constexpr int W_BYTES = WROWS * 128;
+  static constexpr int STAGE = X_BYTES + W_BYTES;
+  static constexpr int STAGES = TALL ? 3 : 8;
+  static constexpr int SLOTS = TALL ? 0 : 4;       // scale ring
+  static constexpr int SLOT_FLOATS = ACC + 4;      // column scales, then the weight scale
+  static constexpr int X_BOX = TALL ? 128 : 32;    // rows of a in one copy
+  static constexpr int OUT_WARP = TALL ? 8192 : 32 * 80;  // output staging: 32 rows a warp
   static constexpr int OFF_OUT = STAGES * STAGE;
   static constexpr int OFF_SCALE = OFF_OUT + 8 * OUT_WARP;
   static constexpr int OFF_BARS = OFF_SCALE + SLOTS * SLOT_FLOATS * 4;
   static constexpr int OFF_GROUPS = OFF_BARS + 512;
   static constexpr int smem(int E) { return OFF_GROUPS + (3 * E + 1) * 4; }
-  static_assert(OFF_GROUPS + (3 * 1024 + 1) * 4 <= 232448, "shared memory");
+  static_assert(OFF_GROUPS + (3 * ROUTE_MAX_E + 1) * 4 <= 232448, "shared memory");
+  static_assert(X_BYTES % 1024 == 0 && W_BYTES % 1024 == 0, "swizzle atoms");
 };
 
 struct TcArgs {
@@ -174,25 +191,33 @@ struct TcArgs {
   const int32_t* offsets;
   void* y;
   unsigned* err;
-  int M, N, E, kb, nb, n_tiles;  // n_tiles: weight tiles of 256 rows
+  int M, N, E, kb, nb, n_tiles;  // n_tiles: weight tiles
 };
 
 struct TcUnit {
-  int e, wt, row0, cnt, n;  // n: columns of the MMA
+  int e, wt, row0, cnt, n;  // n: columns of the MMAs
 };
 
-__device__ __forceinline__ void tma_pair_2d(uint32_t dst, const CUtensorMap* map, int x, int y, uint32_t bar) {
+__device__ __forceinline__ void tma_2d(uint32_t dst, const CUtensorMap* map, int x, int y, uint64_t* bar) {
   asm volatile(
-      "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes.cta_group::2 [%0], [%1, {%2, "
-      "%3}], [%4];" ::"r"(dst),
-      "l"(map), "r"(x), "r"(y), "r"(bar)
+      "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], [%4];" ::"r"(
+          dst),
+      "l"(map), "r"(x), "r"(y), "r"(smem_u32(bar))
       : "memory");
 }
-__device__ __forceinline__ void tma_pair_3d(uint32_t dst, const CUtensorMap* map, int x, int y, int z, uint32_t bar) {
+__device__ __forceinline__ void tma_3d(uint32_t dst, const CUtensorMap* map, int x, int y, int z, uint64_t* bar) {
   asm volatile(
-      "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes.cta_group::2 [%0], [%1, {%2, "
-      "%3, %4}], [%5];" ::"r"(dst),
-      "l"(map), "r"(x), "r"(y), "r"(z), "r"(bar)
+      "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], "
+      "[%5];" ::"r"(dst),
+      "l"(map), "r"(x), "r"(y), "r"(z), "r"(smem_u32(bar))
+      : "memory");
+}
+// The same box to this offset of both CTAs of the cluster, and its bytes to both CTAs' barriers.
+__device__ __forceinline__ void tma_3d_both(uint32_t dst, const CUtensorMap* map, int x, int y, int z, uint64_t* bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes.multicast::cluster [%0], [%1, "
+      "{%2, %3, %4}], [%5], %6;" ::"r"(dst),
+      "l"(map), "r"(x), "r"(y), "r"(z), "r"(smem_u32(bar)), "h"((uint16_t)3)
       : "memory");
 }
 __device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
@@ -205,41 +230,47 @@ __device__ __forceinline__ uint64_t pack2(uint32_t lo, uint32_t hi) {
   asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "r"(lo), "r"(hi));
   return r;
 }
+__device__ __forceinline__ uint32_t bf16_pair(uint64_t v) {
+  float lo, hi;
+  f2unpack(v, lo, hi);
+  const __nv_bfloat162 h = __floats2bfloat162_rn(lo, hi);
+  return *reinterpret_cast<const uint32_t*>(&h);
+}
 
-template <int NT, bool F32>
+template <bool TALL, bool F32>
 __global__ void __launch_bounds__(TC_THREADS, 1)
     block_gemm_tc_kernel(const TcArgs p, const __grid_constant__ CUtensorMap map_w,
-                         const __grid_constant__ CUtensorMap map_x) {
-  using C = TcCfg<NT>;
+                         const __grid_constant__ CUtensorMap map_x, const __grid_constant__ CUtensorMap map_y) {
+  using C = TcCfg<TALL>;
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   uint8_t* sm = smem_raw;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  const uint32_t rank = tc05::cluster_rank();
-  uint64_t* full = reinterpret_cast<uint64_t*>(sm + C::OFF_BARS);  // [STAGES] both CTAs' operands landed (even CTA's)
-  uint64_t* empty = full + C::STAGES;                              // [STAGES] stage consumed
+  const int rank = TALL ? (int)tc05::cluster_rank() : 0;
+  uint64_t* full = reinterpret_cast<uint64_t*>(sm + C::OFF_BARS);  // [STAGES] operands landed
+  uint64_t* empty = full + C::STAGES;                              // [STAGES] stage consumed, in every CTA of the cluster
   uint64_t* tfull = empty + C::STAGES;                             // [NBUF] accumulator complete
-  uint64_t* tempty = tfull + C::NBUF;                              // [NBUF] accumulator read, 16 warps (even CTA's)
+  uint64_t* tempty = tfull + C::NBUF;                              // [NBUF] accumulator read
   uint64_t* sfull = tempty + C::NBUF;                              // [SLOTS] scales landed
-  uint64_t* sempty = sfull + C::SLOTS;                             // [SLOTS] scales read, 8 warps
+  uint64_t* sempty = sfull + C::SLOTS;                             // [SLOTS] scales read
   uint32_t* tslot = reinterpret_cast<uint32_t*>(sempty + C::SLOTS);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tslot + 1);
   static_assert((2 * C::STAGES + 2 * C::NBUF + 2 * C::SLOTS) * 8 + 8 <= 512, "barriers");
-  int* g_tiles = reinterpret_cast<int*>(sm + C::OFF_GROUPS);  // [E + 1] column tiles before each group
+  int* g_tiles = reinterpret_cast<int*>(sm + C::OFF_GROUPS);  // [E + 1] row tiles before each group
   int* g_lo = g_tiles + p.E + 1;                              // [E] first row
   int* g_cnt = g_lo + p.E;                                    // [E] rows
 
-  if (warp == 3) {
-    tc05::tmem_alloc_pair(tslot, 512);
-    tc05::tmem_relinquish_pair();
+  if (warp == 8) {
+    tc05::tmem_alloc(tslot, 512);
+    tc05::tmem_relinquish();
   }
   if (tid == 0) {
     for (int i = 0; i < C::STAGES; ++i) {
       mbar_init(&full[i], 1);
-      mbar_init(&empty[i], 1);
+      mbar_init(&empty[i], TALL ? 4 : 1);  // TALL: two issuers in each of two CTAs
     }
     for (int i = 0; i < C::NBUF; ++i) {
       mbar_init(&tfull[i], 1);
-      mbar_init(&tempty[i], 16);
+      mbar_init(&tempty[i], TALL ? 4 : 8);  // TALL: an accumulator belongs to one column half
     }
     for (int i = 0; i < C::SLOTS; ++i) {
       mbar_init(&sfull[i], 32);
@@ -250,7 +281,7 @@ __global__ void __launch_bounds__(TC_THREADS, 1)
   }
   pdl_wait();
   pdl_trigger();
-  if (warp == 2) {  // groups: rows, and column tiles before each
+  if (warp == 8) {  // groups: rows, and row tiles before each
     int base = 0;
     for (int e0 = 0; e0 < p.E; e0 += 32) {
       const int e = e0 + lane;
@@ -261,7 +292,7 @@ __global__ void __launch_bounds__(TC_THREADS, 1)
         g_lo[e] = lo;
         g_cnt[e] = cnt;
       }
-      const int t = (cnt + NT - 1) / NT;
+      const int t = (cnt + C::ROWS - 1) / C::ROWS;
       int incl = t;
 #pragma unroll
       for (int off = 1; off < 32; off <<= 1) {
@@ -275,11 +306,11 @@ __global__ void __launch_bounds__(TC_THREADS, 1)
   }
   tc05::fence_before_sync();
   __syncthreads();
-  tc05::cluster_sync();  // both CTAs' barriers are ready
+  if (TALL) tc05::cluster_sync();  // the peer's barriers are ready too
   tc05::fence_after_sync();
   const uint32_t tmem = *tslot;
   const int n_units = g_tiles[p.E] * p.n_tiles;
-  const int u0 = blockIdx.x >> 1, ustep = gridDim.x >> 1;
+  const int u0 = blockIdx.x / C::CTAS, ustep = gridDim.x / C::CTAS;
 
   auto unit_of = [&](int u) -> TcUnit {
     TcUnit t;
@@ -292,12 +323,10 @@ __global__ void __launch_bounds__(TC_THREADS, 1)
       else hi = mid;
     }
     t.e = lo;
-    const int tiles = g_tiles[lo + 1] - g_tiles[lo], cnt = g_cnt[lo];
-    const int size = ((cnt + tiles - 1) / tiles + 31) & ~31;  // a group's tiles are of one size, to 32 rows
-    const int at = (tile - g_tiles[lo]) * size;
+    const int at = (tile - g_tiles[lo]) * C::ROWS;
     t.row0 = g_lo[lo] + at;
-    t.cnt = max(0, min(size, cnt - at));
-    t.n = max(32, (t.cnt + 31) & ~31);
+    t.cnt = min(C::ROWS, g_cnt[lo] - at);
+    t.n = TALL ? min(256, (p.N - t.wt * 256 + 15) & ~15) : (t.cnt + 15) & ~15;
     return t;
   };
   // Bounded wait.  Lanes of a warp that wait together agree on the result: the
@@ -311,28 +340,31 @@ __global__ void __launch_bounds__(TC_THREADS, 1)
     return false;
   };
 
-  if (warp < 4) {
-    if (NT == 256) tc05::regs_down<TC_REGS_LOW>();
-    if (warp == 0) {
-      // ---------------- producer: this CTA's 128 weight rows and its half of the columns
+  if (warp >= 8) {
+    if (TALL) tc05::regs_down<TC_REGS_LOW>();
+    if (warp == 8) {
+      // ---------------- producer
       if (lane == 0) {
         uint32_t s = 0, ph = 0, issued = 0;
         bool ok = true;
-        const uint32_t base = smem_u32(sm), full0 = tc05::map_rank(smem_u32(full), 0);
         for (int u = u0; u < n_units && ok; u += ustep) {
           const TcUnit t = unit_of(u);
-          const int nh = t.n >> 1, boxes = (nh + 31) >> 5;
-          const int wrow = t.wt * 256 + (int)rank * 128, xrow = t.row0 + (int)rank * nh;
-          const uint32_t bytes = 2u * (TC_A_BYTES + boxes * 4096);
+          const int boxes = TALL ? 1 : (t.n + 31) >> 5;
+          const uint32_t bytes = C::W_BYTES + boxes * C::X_BOX * 128;
           for (int kb = 0; kb < p.kb; ++kb) {
             if (!wait(&empty[s], ph ^ 1)) {
               ok = false;
               break;
             }
-            if (rank == 0) mbar_arrive_expect_tx(&full[s], bytes);
-            const uint32_t dst = base + s * C::STAGE, bar = full0 + s * 8;
-            tma_pair_3d(dst, &map_w, kb * 128, wrow, t.e, bar);
-            for (int i = 0; i < boxes; ++i) tma_pair_2d(dst + TC_A_BYTES + i * 4096, &map_x, kb * 128, xrow + 32 * i, bar);
+            mbar_arrive_expect_tx(&full[s], bytes);
+            const uint32_t w = smem_u32(sm) + s * C::STAGE, x = w + C::W_BYTES;
+            if (TALL) {
+              tma_3d_both(w + rank * 16384, &map_w, kb * 128, t.wt * 256 + rank * 128, t.e, &full[s]);
+              tma_2d(x, &map_x, kb * 128, t.row0 + rank * 128, &full[s]);
+            } else {
+              tma_3d(w, &map_w, kb * 128, t.wt * 128, t.e, &full[s]);
+              for (int i = 0; i < boxes; ++i) tma_2d(x + i * 4096, &map_x, kb * 128, t.row0 + 32 * i, &full[s]);
+            }
             ++issued;
             if (++s == C::STAGES) {
               s = 0;
@@ -340,61 +372,70 @@ __global__ void __launch_bounds__(TC_THREADS, 1)
             }
           }
         }
-        // Every stage's last phase: normally its release by the MMAs (nothing of
-        // the peer is then under way to this CTA); after a wait that ran out, the
-        // arrival of the copies.
+        // Every stage's last phase: normally its release by all MMAs, after
+        // which nothing is under way to this CTA; after a wait that ran out,
+        // the arrival of the copies (the peer's may come later: 1 ms covers any).
         const uint32_t n = issued < (uint32_t)C::STAGES ? issued : (uint32_t)C::STAGES;
         for (uint32_t q = issued - n; q < issued; ++q) {
-          if (ok) {
-            ok = wait(&empty[q % C::STAGES], (q / C::STAGES) & 1);
-          } else if (rank == 0) {
-            (void)mbar_wait(&full[q % C::STAGES], (q / C::STAGES) & 1);
-          }
+          if (ok) ok = wait(&empty[q % C::STAGES], (q / C::STAGES) & 1);
+          else (void)mbar_wait(&full[q % C::STAGES], (q / C::STAGES) & 1);
         }
-        if (!ok && rank != 0) {  // the peer's barriers cannot be waited on: 1 ms covers any copy
+        if (!ok && TALL) {
           const long long t0 = clock64();
           while (clock64() - t0 < 2000000) {
           }
         }
       }
-    } else if (warp == 1) {
-      // ---------------- MMA issuer
-      if (rank == 0 && lane == 0) {
-        uint32_t s = 0, ph = 0, b = 0, bph = 0, steps = 0;
-        bool ok = true;
-        const uint64_t da0 = tc05::sw128_desc(smem_u32(sm)), db0 = tc05::sw128_desc(smem_u32(sm) + TC_A_BYTES);
-        for (int u = u0; u < n_units && ok; u += ustep) {
-          const TcUnit t = unit_of(u);
-          const uint32_t idesc = tc05::idesc_e4m3(256, t.n);
-          for (int kb = 0; kb < p.kb; ++kb) {
-            if (!wait(&tempty[b], bph ^ 1) || !wait(&full[s], ph)) {
-              ok = false;
-              break;
-            }
-            tc05::fence_after_sync();
-            const uint64_t da = da0 + (uint64_t)(s * (C::STAGE >> 4)), db = db0 + (uint64_t)(s * (C::STAGE >> 4));
-            const uint32_t d = tmem + b * NT;
+    } else if (warp != 10) {
+      // ---------------- two MMA issuers: of one column half each (TALL), of
+      // the even and odd K blocks (WIDE).  Each commit costs its issuer about 100
+      // cycles, and each MMA 40 (70 if one lane runs the loop: its descriptors
+      // are not warp-uniform then), so that one issuer would need more than the
+      // 512 cycles of a block's MMAs.  A phase two ahead has the same parity, so
+      // an issuer has to see every phase of the barriers that it waits for: it
+      // takes part in every use of its stages and accumulators.
+      static_assert(TALL || (C::NBUF % 2 == 0 && C::STAGES % 2 == 0), "one issuer for each");
+      const uint32_t me = warp == 9 ? 0 : 1;
+      uint32_t g = 0;  // K blocks so far
+      bool ok = true;
+      const uint64_t dw0 = tc05::sw128_desc(smem_u32(sm)) + (TALL ? 1024 * me : 0);  // its 128 weight rows
+      const uint64_t dx0 = tc05::sw128_desc(smem_u32(sm) + C::W_BYTES);
+      for (int u = u0; u < n_units && ok; u += ustep) {
+        const TcUnit t = unit_of(u);
+        const int n = TALL ? min(128, t.n - 128 * (int)me) : t.n;  // <= 0: a narrow tile, nothing but the barriers
+        const uint32_t idesc = tc05::idesc_e4m3(128, n > 0 ? n : 16);
+        for (int kb = 0; kb < p.kb; ++kb, ++g) {
+          if (!TALL && g % 2 != me) continue;
+          const uint32_t s = g % C::STAGES, ph = (g / C::STAGES) & 1;
+          const uint32_t b = TALL ? 2 * me + (g & 1) : g % C::NBUF, bph = ((TALL ? g >> 1 : g / C::NBUF) & 1) ^ 1;
+          // every lane looks and waits, and all go on or none
+          const bool ready = mbar_test(&full[s], ph) & mbar_test(&tempty[b], bph);
+          if (!__all_sync(0xffffffffu, ready)) {
+            ok = wait(&full[s], ph) && wait(&tempty[b], bph);
+            ok = __all_sync(0xffffffffu, ok);
+            if (!ok) break;
+          }
+          tc05::fence_after_sync();
+          const uint64_t dw = dw0 + (uint64_t)(s * (C::STAGE >> 4)), dx = dx0 + (uint64_t)(s * (C::STAGE >> 4));
+          const uint32_t d = tmem + b * C::ACC;
+          if (n > 0) {
 #pragma unroll
-            for (int k = 0; k < 4; ++k) tc05::mma_e4m3_pair(d, da + 2 * k, db + 2 * k, idesc, k > 0 ? 1u : 0u);
-            tc05::commit_pair(&empty[s]);
-            tc05::commit_pair(&tfull[b]);
-            ++steps;
-            if (++s == C::STAGES) {
-              s = 0;
-              ph ^= 1;
-            }
-            if (++b == C::NBUF) {
-              b = 0;
-              bph ^= 1;
+            for (int k = 0; k < 4; ++k) {
+              if (TALL) tc05::mma_e4m3(d, dx + 2 * k, dw + 2 * k, idesc, k > 0 ? 1u : 0u);
+              else tc05::mma_e4m3(d, dw + 2 * k, dx + 2 * k, idesc, k > 0 ? 1u : 0u);
             }
           }
-        }
-        if (steps > 0) {  // the last MMAs have retired
-          const uint32_t q = steps - 1;
-          (void)mbar_wait(&empty[q % C::STAGES], (q / C::STAGES) & 1);
+          tc05::commit(&tfull[b]);
+          if (TALL) tc05::commit_both(&empty[s]);
+          else tc05::commit(&empty[s]);
         }
       }
-    } else if (warp == 2) {
+      if (!ok) {  // what has been issued retires before tensor memory goes
+        const long long t0 = clock64();
+        while (clock64() - t0 < 2000000) {
+        }
+      }
+    } else if (!TALL) {
       // ---------------- scales of each K block: one per column, and the weights' one
       uint32_t s = 0, ph = 0;
       float* ring = reinterpret_cast<float*>(sm + C::OFF_SCALE);
@@ -402,8 +443,7 @@ __global__ void __launch_bounds__(TC_THREADS, 1)
       for (int u = u0; u < n_units && ok; u += ustep) {
         const TcUnit t = unit_of(u);
         const int nh = t.n >> 1;
-        const int wblock = min(t.wt * 2 + (int)rank, p.nb - 1);
-        const float* sb = p.sb + ((size_t)t.e * p.nb + wblock) * p.kb;
+        const float* sb = p.sb + ((size_t)t.e * p.nb + t.wt) * p.kb;
         for (int kb = 0; kb < p.kb; ++kb) {
           if (!wait(&sempty[s], ph ^ 1)) {
             ok = false;
@@ -412,19 +452,20 @@ __global__ void __launch_bounds__(TC_THREADS, 1)
           float* slot = ring + s * C::SLOT_FLOATS;
           const float* sa = p.sa + (size_t)kb * p.M + t.row0;
 #pragma unroll
-          for (int i = 0; i < NT / 32; ++i) {
+          for (int i = 0; i < C::ACC / 32; ++i) {
             const int c = lane + 32 * i;
             if (c < t.n) {
-              // thread q of a promotion quad reads its pairs of 4 neighbouring 8-column groups together
+              // thread q of a promotion quad reads its pairs of the 4 neighbouring 8-column groups together
               const int h = c >= nh ? 1 : 0, cc = c - h * nh;
-              const int at = h * (NT / 2) + (cc & ~31) + ((cc & 7) >> 1) * 8 + ((cc >> 3) & 3) * 2 + (cc & 1);
+              const int at = h * (C::ACC / 2) + ((cc & 7) >> 1) * 8 + (cc >> 3) * 2 + (cc & 1);
               asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(smem_u32(slot + at)),
                            "l"(sa + min(c, t.cnt - 1))
                            : "memory");
             }
           }
           if (lane == 0)
-            asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(smem_u32(slot + NT)), "l"(sb + kb) : "memory");
+            asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(smem_u32(slot + C::ACC)), "l"(sb + kb)
+                         : "memory");
           asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(smem_u32(&sfull[s])) : "memory");
           if (++s == C::SLOTS) {
             s = 0;
@@ -435,80 +476,172 @@ __global__ void __launch_bounds__(TC_THREADS, 1)
       asm volatile("cp.async.wait_all;" ::: "memory");
     }
   } else {
-    if (NT == 256) tc05::regs_up<TC_REGS_HIGH>();
+    if (TALL) tc05::regs_up<TC_REGS_HIGH>();
     // ---------------- promotion: acc += scale * block, then the output
-    const int quad = warp & 3, half = warp >= 8 ? 1 : 0;
-    const int g = lane >> 2, q = lane & 3;
-    constexpr int CH = NT / 64;  // 32-column chunks of a half
-    uint32_t b = 0, bph = 0, s = 0, sph = 0;
-    const float* ring = reinterpret_cast<const float*>(sm + C::OFF_SCALE);
-    uint8_t* out = sm + C::OFF_OUT + (warp - 4) * C::OUT_WARP;
-    const uint32_t tempty0 = tc05::map_rank(smem_u32(tempty), 0);
+    const int quad = warp & 3, half = warp >> 2;
+    uint8_t* out = sm + C::OFF_OUT + warp * C::OUT_WARP;
+    const uint32_t lanes = tmem + ((uint32_t)(quad * 32) << 16);
+    uint32_t v = 0;  // accumulators so far
     bool ok = true;
-    for (int u = u0; u < n_units && ok; u += ustep) {
-      const TcUnit t = unit_of(u);
-      const int nh = t.n >> 1;
-      uint64_t acc[CH][2][8];  // [chunk][lane half][4 groups x (row g, row g + 8)]
+    // The accumulator is in registers: back to the MMAs.
+    auto give_back = [&](uint32_t b) {
+      tc05::fence_before_sync();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&tempty[b]);
+    };
+    if constexpr (TALL) {
+      for (int u = u0; u < n_units && ok; u += ustep) {
+        const TcUnit t = unit_of(u);
+        const int row = rank * 128 + quad * 32;      // first of the warp's 32 rows in the tile
+        const int live = t.n > 128 * half ? min(32, t.cnt - row) : 0;  // its rows of a, <= 0: none
+        const float* sa = p.sa + t.row0 + min(row + lane, t.cnt - 1);
+        const float* sb = p.sb + ((size_t)t.e * p.nb + min(t.wt * 2 + half, p.nb - 1)) * p.kb;
+        uint64_t acc[64];
 #pragma unroll
-      for (int c = 0; c < CH; ++c)
+        for (int i = 0; i < 64; ++i) acc[i] = 0ull;
+        // One K block with the scales a, w, which are then loaded for the block two further on.
+        auto promote = [&](int kb, float& a, float& w) -> bool {
+          const uint32_t b = 2 * half + (v & 1), bph = (v >> 1) & 1;
+          ++v;
+          if (!wait(&tfull[b], bph)) return false;
+          tc05::fence_after_sync();
+          if (live > 0) {
+            const uint32_t ta = lanes + b * C::ACC;
+            uint32_t r[2][16];
+            tc05::ld_32x32b_x16(ta, r[0]);
+            const float sc = a * w;
+            const uint64_t s2 = f2pack(sc, sc);
+            if (kb + 2 < p.kb) {
+              a = __ldg(sa + (size_t)(kb + 2) * p.M);
+              w = __ldg(sb + kb + 2);
+            }
 #pragma unroll
-        for (int i = 0; i < 8; ++i) acc[c][0][i] = acc[c][1][i] = 0ull;
-      for (int kb = 0; kb < p.kb; ++kb) {
-        if (!wait(&sfull[s], sph) || !wait(&tfull[b], bph)) {
-          ok = false;
-          break;
-        }
-        tc05::fence_after_sync();
-        const float* slot = ring + s * C::SLOT_FLOATS;
-        const float wsc = slot[NT];
-        const uint64_t w2 = f2pack(wsc, wsc);
-        const uint32_t ta = tmem + ((uint32_t)(quad * 32) << 16) + b * NT + (uint32_t)(half * nh);
-#pragma unroll
-        for (int c = 0; c < CH; ++c) {
-          if (32 * c < nh) {
-            uint32_t r[32];
-            tc05::ld_16x256b_x4(ta + 32 * c, r);
-            tc05::ld_16x256b_x4(ta + (16u << 16) + 32 * c, r + 16);
-            const float4* sc = reinterpret_cast<const float4*>(slot + half * (NT / 2) + 32 * c + q * 8);
-            const float4 s0 = sc[0], s1 = sc[1];
-            const uint64_t s2[4] = {f2mul(f2pack(s0.x, s0.y), w2), f2mul(f2pack(s0.z, s0.w), w2),
-                                    f2mul(f2pack(s1.x, s1.y), w2), f2mul(f2pack(s1.z, s1.w), w2)};
-            tc05::wait_ld32(r);
-#pragma unroll
-            for (int h = 0; h < 2; ++h)
+            for (int c = 0; c < 8; ++c) {
+              tc05::wait_ld16(r[c & 1]);
+              if (c < 7) tc05::ld_32x32b_x16(ta + 16 * (c + 1), r[(c + 1) & 1]);
+              else give_back(b);
 #pragma unroll
               for (int i = 0; i < 8; ++i)
-                acc[c][h][i] = fma2(pack2(r[16 * h + 2 * i], r[16 * h + 2 * i + 1]), s2[i >> 1], acc[c][h][i]);
+                acc[8 * c + i] = fma2(pack2(r[c & 1][2 * i], r[c & 1][2 * i + 1]), s2, acc[8 * c + i]);
+            }
+          } else {
+            give_back(b);
           }
+          return true;
+        };
+        float a0 = __ldg(sa), w0 = __ldg(sb), a1 = 0.f, w1 = 0.f;
+        if (p.kb > 1) {
+          a1 = __ldg(sa + p.M);
+          w1 = __ldg(sb + 1);
         }
-        tc05::fence_before_sync();
-        __syncwarp();
-        if (lane == 0) {
-          tc05::mbar_arrive_cluster(tempty0 + b * 8);
-          mbar_arrive(&sempty[s]);
+        for (int kb = 0; kb < p.kb && ok; kb += 2) {
+          ok = promote(kb, a0, w0);
+          if (ok && kb + 1 < p.kb) ok = promote(kb + 1, a1, w1);
         }
-        if (++b == C::NBUF) {
-          b = 0;
-          bph ^= 1;
-        }
-        if (++s == C::SLOTS) {
-          s = 0;
-          sph ^= 1;
+        if (!ok) break;
+        // Output: 128-byte pieces of 32 rows in the 128-byte swizzle, copied out by
+        // TMA while the next unit is multiplied.  Where a row behind the group's
+        // last belongs to another group, the rows are copied one by one.
+        constexpr int SIZE = F32 ? 4 : 2, COLS = 128 / SIZE;  // columns of a piece
+        const int n0 = t.wt * 256 + half * 128, row0 = t.row0 + row;
+        const bool box = live == 32 || t.row0 + t.cnt == p.M;  // TMA leaves out what lies outside y
+#pragma unroll
+        for (int r = 0; r < (F32 ? 2 : 1); ++r) {  // two pieces a round: 8 KB
+          asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
+          __syncwarp();
+#pragma unroll
+          for (int c = 0; c < 2; ++c)
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+              const uint64_t* src = acc + (2 * r + c) * (COLS / 2) + j * (F32 ? 2 : 4);
+              uint4 v;
+              if (F32) {
+                const ulonglong2 q = make_ulonglong2(src[0], src[1]);
+                v = *reinterpret_cast<const uint4*>(&q);
+              } else {
+                v = make_uint4(bf16_pair(src[0]), bf16_pair(src[1]), bf16_pair(src[2]), bf16_pair(src[3]));
+              }
+              // box: piece c as [32 rows][128 B], swizzled; else [32 rows][256 B]
+              const int at = box ? c * 4096 + lane * 128 + ((j ^ (lane & 7)) << 4) : lane * 256 + c * 128 + j * 16;
+              *reinterpret_cast<uint4*>(out + at) = v;
+            }
+          tc05::fence_proxy_async_smem();
+          __syncwarp();
+          const int nr = n0 + r * 2 * COLS;  // first column of the round
+          if (box) {
+            if (lane == 0 && live > 0) {
+#pragma unroll
+              for (int c = 0; c < 2; ++c)
+                if (nr + c * COLS < p.N)
+                  asm volatile("cp.async.bulk.tensor.2d.global.shared::cta.tile.bulk_group [%0, {%1, %2}], [%3];" ::"l"(
+                                   &map_y),
+                               "r"(nr + c * COLS), "r"(row0), "r"(smem_u32(out + c * 4096))
+                               : "memory");
+            }
+          } else if (lane < live && nr < p.N) {
+            asm volatile("cp.async.bulk.global.shared::cta.bulk_group [%0], [%1], %2;" ::"l"(
+                             static_cast<uint8_t*>(p.y) + ((size_t)(row0 + lane) * p.N + nr) * SIZE),
+                         "r"(smem_u32(out + lane * 256)), "r"(min(2 * COLS, p.N - nr) * SIZE)
+                         : "memory");
+          }
+          asm volatile("cp.async.bulk.commit_group;" ::: "memory");
         }
       }
-      if (!ok) break;
-      const int n0 = t.wt * 256 + (int)rank * 128 + quad * 32;  // first weight row of the warp
-      if (F32) {
-        float* y = static_cast<float*>(p.y);
+      asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
+    } else {
+      const int g = lane >> 2, q = lane & 3;
+      uint32_t s = 0, sph = 0;
+      const float* ring = reinterpret_cast<const float*>(sm + C::OFF_SCALE);
+      for (int u = u0; u < n_units && ok; u += ustep) {
+        const TcUnit t = unit_of(u);
+        const int nh = t.n >> 1;
+        uint64_t acc[2][8];  // [lane half][4 groups x (row g, row g + 8)]
 #pragma unroll
-        for (int c = 0; c < CH; ++c)
+        for (int i = 0; i < 8; ++i) acc[0][i] = acc[1][i] = 0ull;
+        for (int kb = 0; kb < p.kb; ++kb) {
+          const uint32_t b = v % C::NBUF, bph = (v / C::NBUF) & 1;
+          ++v;
+          if (!wait(&sfull[s], sph) || !wait(&tfull[b], bph)) {
+            ok = false;
+            break;
+          }
+          tc05::fence_after_sync();
+          const float* slot = ring + s * C::SLOT_FLOATS;
+          const uint32_t ta = lanes + b * C::ACC + (uint32_t)(half * nh);
+          uint32_t r[32];
+          tc05::ld_16x256b_x4(ta, r);
+          tc05::ld_16x256b_x4(ta + (16u << 16), r + 16);
+          const float wsc = slot[C::ACC];
+          const uint64_t w2 = f2pack(wsc, wsc);
+          const float4* sc = reinterpret_cast<const float4*>(slot + half * (C::ACC / 2) + q * 8);
+          const float4 s0 = sc[0], s1 = sc[1];
+          const uint64_t s2[4] = {f2mul(f2pack(s0.x, s0.y), w2), f2mul(f2pack(s0.z, s0.w), w2),
+                                  f2mul(f2pack(s1.x, s1.y), w2), f2mul(f2pack(s1.z, s1.w), w2)};
+          tc05::wait_ld32(r);
+          give_back(b);
+#pragma unroll
+          for (int h = 0; h < 2; ++h)
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+              acc[h][i] = fma2(pack2(r[16 * h + 2 * i], r[16 * h + 2 * i + 1]), s2[i >> 1], acc[h][i]);
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&sempty[s]);  // every lane has used its scales
+          if (++s == C::SLOTS) {
+            s = 0;
+            sph ^= 1;
+          }
+        }
+        if (!ok) break;
+        const int n0 = t.wt * 128 + quad * 32;  // first weight row of the warp
+        if (F32) {
+          float* y = static_cast<float*>(p.y);
 #pragma unroll
           for (int i = 0; i < 8; ++i) {
-            const int cl = 32 * c + (i >> 1) * 8 + 2 * q, col = half * nh + cl;
+            const int cl = (i >> 1) * 8 + 2 * q, col = half * nh + cl;
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
               float v0, v1;
-              f2unpack(acc[c][h][i], v0, v1);
+              f2unpack(acc[h][i], v0, v1);
               const int n = n0 + 16 * h + (i & 1) * 8 + g;
               if (n < p.N && cl < nh) {
                 if (col < t.cnt) y[(size_t)(t.row0 + col) * p.N + n] = v0;
@@ -516,40 +649,26 @@ __global__ void __launch_bounds__(TC_THREADS, 1)
               }
             }
           }
-      } else {
-        uint16_t* y = static_cast<uint16_t*>(p.y);
-        const uint32_t st = smem_u32(out) + (lane & 7) * 80 + (lane >> 3) * 16;  // row lane % 8 of matrix lane / 8
-        const uint4* ld = reinterpret_cast<const uint4*>(out + (lane >> 2) * 80 + (lane & 3) * 16);
-        const int n = n0 + (lane & 3) * 8;
+        } else {
+          // 8 x 8 transposes on the way into shared memory; four lanes store 32 columns of a row of y
+          uint16_t* y = static_cast<uint16_t*>(p.y);
+          const uint32_t st = smem_u32(out) + (lane & 7) * 80 + (lane >> 3) * 16;  // row lane % 8 of matrix lane / 8
+          const uint4* ld = reinterpret_cast<const uint4*>(out + (lane >> 2) * 80 + (lane & 3) * 16);
+          const int n = n0 + (lane & 3) * 8;
 #pragma unroll
-        for (int c = 0; c < CH; ++c) {
-          if (32 * c >= nh) break;
+          for (int k = 0; k < 4; ++k)  // weight rows 0-7, 8-15, 16-23, 24-31 of the warp x 8 rows of y
+            asm volatile("stmatrix.sync.aligned.m8n8.x4.trans.shared.b16 [%0], {%1, %2, %3, %4};" ::"r"(st + k * 640),
+                         "r"(bf16_pair(acc[0][2 * k])), "r"(bf16_pair(acc[0][2 * k + 1])), "r"(bf16_pair(acc[1][2 * k])),
+                         "r"(bf16_pair(acc[1][2 * k + 1]))
+                         : "memory");
+          __syncwarp();
 #pragma unroll
-          for (int gp = 0; gp < 4; gp += 2) {  // 16 rows of y at a time
-#pragma unroll
-            for (int k = 0; k < 2; ++k) {
-              uint32_t m[4];  // weight rows 0-7, 8-15, 16-23, 24-31 of the warp
-#pragma unroll
-              for (int i = 0; i < 4; ++i) {
-                float v0, v1;
-                f2unpack(acc[c][i >> 1][2 * (gp + k) + (i & 1)], v0, v1);
-                const __nv_bfloat162 hv = __floats2bfloat162_rn(v0, v1);
-                m[i] = *reinterpret_cast<const uint32_t*>(&hv);
-              }
-              asm volatile("stmatrix.sync.aligned.m8n8.x4.trans.shared.b16 [%0], {%1, %2, %3, %4};" ::"r"(st + k * 640),
-                           "r"(m[0]), "r"(m[1]), "r"(m[2]), "r"(m[3])
-                           : "memory");
-            }
-            __syncwarp();
-#pragma unroll
-            for (int k = 0; k < 2; ++k) {
-              const int cl = 32 * c + (gp + k) * 8 + (lane >> 2), col = half * nh + cl;
-              const uint4 v = ld[k * 40];
-              if (cl < nh && col < t.cnt && n < p.N)
-                *reinterpret_cast<uint4*>(y + (size_t)(t.row0 + col) * p.N + n) = v;
-            }
-            __syncwarp();
+          for (int k = 0; k < 4; ++k) {
+            const int cl = k * 8 + (lane >> 2), col = half * nh + cl;
+            if (cl < nh && col < t.cnt && n < p.N)
+              *reinterpret_cast<uint4*>(y + (size_t)(t.row0 + col) * p.N + n) = ld[40 * k];
           }
+          __syncwarp();
         }
       }
     }
@@ -557,10 +676,10 @@ __global__ void __launch_bounds__(TC_THREADS, 1)
   __syncwarp();
   tc05::fence_before_sync();
   __syncthreads();
-  tc05::cluster_sync();  // no arrival or copy is under way to either CTA any more
-  if (warp == 3) {
+  if (TALL) tc05::cluster_sync();  // no arrival or copy is under way to either CTA any more
+  if (warp == 8) {
     tc05::fence_after_sync();
-    tc05::tmem_dealloc_pair(tmem, 512);
+    tc05::tmem_dealloc(tmem, 512);
   }
 }
 
@@ -569,18 +688,23 @@ using EncodeTiled = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, 
                                  CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
 EncodeTiled g_encode = nullptr;  // set once, under the library's lock
 
-// A map of byte rows of length K, boxes of 128 bytes x `box` rows in the
-// 128-byte swizzle, zeros outside.
-bool row_map(CUtensorMap* m, const void* base, int rank, uint64_t K, uint64_t rows, uint64_t mats, uint32_t box) {
-  const cuuint64_t dims[3] = {K, rows, mats}, strides[2] = {K, K * rows};
-  const cuuint32_t boxes[3] = {128, box, 1}, steps[3] = {1, 1, 1};
-  return g_encode(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, (cuuint32_t)rank, const_cast<void*>(base), dims, strides, boxes,
-                  steps, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+// A map of rows of `cols` elements of `size` bytes, of one matrix (mats 0) or
+// `mats` of them; boxes of 128 bytes x `box` rows in the 128-byte swizzle, zeros
+// outside.
+bool row_map(CUtensorMap* m, const void* base, int size, uint64_t cols, uint64_t rows, uint64_t mats, uint32_t box) {
+  const cuuint64_t dims[3] = {cols, rows, mats}, strides[2] = {cols * size, cols * size * rows};
+  const cuuint32_t boxes[3] = {128u / (uint32_t)size, box, 1}, steps[3] = {1, 1, 1};
+  const CUtensorMapDataType type = size == 1   ? CU_TENSOR_MAP_DATA_TYPE_UINT8
+                                   : size == 2 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16
+                                               : CU_TENSOR_MAP_DATA_TYPE_FLOAT32;
+  return g_encode(m, type, mats ? 3 : 2, const_cast<void*>(base), dims, strides, boxes, steps,
+                  CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                   CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-template <int NT, bool F32>
+template <bool TALL, bool F32>
 cudaError_t launch_tc(const GemmArgs& p, int sm_count, unsigned* err, cudaStream_t st) {
+  using C = TcCfg<TALL>;
   TcArgs t;
   t.sa = p.sa;
   t.sb = p.sb;
@@ -592,26 +716,29 @@ cudaError_t launch_tc(const GemmArgs& p, int sm_count, unsigned* err, cudaStream
   t.E = p.E;
   t.kb = p.kb;
   t.nb = p.nb;
-  t.n_tiles = (p.N + 255) / 256;
-  CUtensorMap mw, mx;
-  if (!row_map(&mw, p.b, 3, p.K, p.N, p.E, 128) || !row_map(&mx, p.a, 2, p.K, p.M, 1, 32)) return cudaErrorInvalidValue;
-  const long long most = ((long long)(p.M + NT - 1) / NT + p.E) * t.n_tiles;  // units, at most
-  const int pairs = sm_count / 2;
+  t.n_tiles = (p.N + C::WROWS - 1) / C::WROWS;
+  CUtensorMap mw, mx, my;
+  const int size = F32 ? 4 : 2;
+  if (!row_map(&mw, p.b, 1, p.K, p.N, p.E, 128) || !row_map(&mx, p.a, 1, p.K, p.M, 0, C::X_BOX) ||
+      !row_map(&my, p.y, size, p.N, p.M, 0, 32))
+    return cudaErrorInvalidValue;
+  const long long most = ((long long)(p.M + C::ROWS - 1) / C::ROWS + p.E) * t.n_tiles;  // units, at most
+  const int clusters = sm_count / C::CTAS;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(2u * (unsigned)(most < pairs ? most : pairs));
+  cfg.gridDim = dim3((unsigned)(C::CTAS * (most < clusters ? most : clusters)));
   cfg.blockDim = dim3(TC_THREADS);
-  cfg.dynamicSmemBytes = TcCfg<NT>::smem(p.E);
+  cfg.dynamicSmemBytes = C::smem(p.E);
   cfg.stream = st;
   cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   attr[1].id = cudaLaunchAttributeClusterDimension;
-  attr[1].val.clusterDim.x = 2;
+  attr[1].val.clusterDim.x = C::CTAS;
   attr[1].val.clusterDim.y = 1;
   attr[1].val.clusterDim.z = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 2;
-  return cudaLaunchKernelEx(&cfg, block_gemm_tc_kernel<NT, F32>, t, mw, mx);
+  return cudaLaunchKernelEx(&cfg, block_gemm_tc_kernel<TALL, F32>, t, mw, mx, my);
 }
 
 }  // namespace
@@ -625,12 +752,12 @@ cudaError_t block_gemm_kernels_init() {
     if (q != cudaDriverEntryPointSuccess || fn == nullptr) return cudaErrorNotSupported;
     g_encode = reinterpret_cast<EncodeTiled>(fn);
   }
-  const void* k[4] = {reinterpret_cast<const void*>(block_gemm_tc_kernel<256, false>),
-                      reinterpret_cast<const void*>(block_gemm_tc_kernel<256, true>),
-                      reinterpret_cast<const void*>(block_gemm_tc_kernel<64, false>),
-                      reinterpret_cast<const void*>(block_gemm_tc_kernel<64, true>)};
+  const void* k[4] = {reinterpret_cast<const void*>(block_gemm_tc_kernel<true, false>),
+                      reinterpret_cast<const void*>(block_gemm_tc_kernel<true, true>),
+                      reinterpret_cast<const void*>(block_gemm_tc_kernel<false, false>),
+                      reinterpret_cast<const void*>(block_gemm_tc_kernel<false, true>)};
   for (int i = 0; i < 4; ++i) {
-    const int bytes = i < 2 ? TcCfg<256>::smem(ROUTE_MAX_E) : TcCfg<64>::smem(ROUTE_MAX_E);
+    const int bytes = i < 2 ? TcCfg<true>::smem(ROUTE_MAX_E) : TcCfg<false>::smem(ROUTE_MAX_E);
     cudaError_t e = cudaFuncSetAttribute(k[i], cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
     if (e != cudaSuccess) return e;
     cudaFuncAttributes fa;
@@ -657,8 +784,9 @@ cudaError_t launch_block_gemm(const void* a, const float* sa, int M, const void*
   p.kb = (K + 127) / 128;
   p.nb = (N + 127) / 128;
   if (M > (offsets != nullptr ? 64 : 8)) {
-    if ((long long)M <= 64LL * E) return f32 ? launch_tc<64, true>(p, sm_count, err, st) : launch_tc<64, false>(p, sm_count, err, st);
-    return f32 ? launch_tc<256, true>(p, sm_count, err, st) : launch_tc<256, false>(p, sm_count, err, st);
+    if ((long long)M > 64LL * E)
+      return f32 ? launch_tc<true, true>(p, sm_count, err, st) : launch_tc<true, false>(p, sm_count, err, st);
+    return f32 ? launch_tc<false, true>(p, sm_count, err, st) : launch_tc<false, false>(p, sm_count, err, st);
   }
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)M, (unsigned)((N + 15) / 16));
