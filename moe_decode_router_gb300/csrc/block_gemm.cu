@@ -154,7 +154,7 @@ __global__ void __launch_bounds__(SK_WARPS * 32) block_gemm_skinny_kernel(const 
 // in shared memory, serves 4 packed fma.
 //
 // Warps: 0-7 promotion and output, two column halves; 8 TMA producer; 9 and 11
-// MMA issuers; 10 loader of column scales (WIDE).
+// MMA issuers; 10 loader of scales.
 constexpr int TC_THREADS = 384;
 // Registers of TALL: the promotion warps hold 128 accumulators each and take
 // what the other four warps give up.  Launched with 168 a thread.
@@ -172,8 +172,11 @@ struct TcCfg {
   static constexpr int W_BYTES = WROWS * 128;
   static constexpr int STAGE = X_BYTES + W_BYTES;
   static constexpr int STAGES = TALL ? 3 : 8;
-  static constexpr int SLOTS = TALL ? 0 : 4;       // scale ring
-  static constexpr int SLOT_FLOATS = ACC + 4;      // column scales, then the weight scale
+  // Scale ring.  TALL: a slot has 4 K blocks, a scale for each of the CTA's 128
+  // rows, then one for each half of the weight tile.  WIDE: one K block, a scale
+  // for each column, then the weights'.
+  static constexpr int SLOTS = TALL ? 2 : 4;
+  static constexpr int SLOT_FLOATS = TALL ? 4 * 128 + 8 : ACC + 4;
   static constexpr int X_BOX = TALL ? 128 : 32;    // rows of a in one copy
   static constexpr int OUT_WARP = TALL ? 8192 : 32 * 80;  // output staging: 32 rows a warp
   static constexpr int OFF_OUT = STAGES * STAGE;
@@ -435,13 +438,46 @@ __global__ void __launch_bounds__(TC_THREADS, 1)
         while (clock64() - t0 < 2000000) {
         }
       }
-    } else if (!TALL) {
-      // ---------------- scales of each K block: one per column, and the weights' one
+    } else {
+      // ---------------- scales
       uint32_t s = 0, ph = 0;
       float* ring = reinterpret_cast<float*>(sm + C::OFF_SCALE);
       bool ok = true;
+      auto copy4 = [](float* dst, const float* src) {
+        asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(smem_u32(dst)), "l"(src) : "memory");
+      };
+      auto filled = [&]() {  // arrives when this lane's copies have landed
+        asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(smem_u32(&sfull[s])) : "memory");
+        if (++s == C::SLOTS) {
+          s = 0;
+          ph ^= 1;
+        }
+      };
       for (int u = u0; u < n_units && ok; u += ustep) {
         const TcUnit t = unit_of(u);
+        if (TALL) {
+          const float* sb = p.sb + ((size_t)t.e * p.nb + min(t.wt * 2 + (lane & 1), p.nb - 1)) * p.kb;
+          const int last = t.cnt - 1;
+          for (int kb = 0; kb < p.kb; kb += 4) {
+            if (!wait(&sempty[s], ph ^ 1)) {
+              ok = false;
+              break;
+            }
+            float* slot = ring + s * C::SLOT_FLOATS;
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+              if (kb + j < p.kb) {
+                const float* sa = p.sa + (size_t)(kb + j) * p.M + t.row0;
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                  copy4(slot + j * 128 + i * 32 + lane, sa + min(rank * 128 + i * 32 + lane, last));
+                if (lane < 2) copy4(slot + 512 + j * 2 + lane, sb + kb + j);
+              }
+            }
+            filled();
+          }
+          continue;
+        }
         const int nh = t.n >> 1;
         const float* sb = p.sb + ((size_t)t.e * p.nb + t.wt) * p.kb;
         for (int kb = 0; kb < p.kb; ++kb) {
@@ -458,19 +494,11 @@ __global__ void __launch_bounds__(TC_THREADS, 1)
               // thread q of a promotion quad reads its pairs of the 4 neighbouring 8-column groups together
               const int h = c >= nh ? 1 : 0, cc = c - h * nh;
               const int at = h * (C::ACC / 2) + ((cc & 7) >> 1) * 8 + (cc >> 3) * 2 + (cc & 1);
-              asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(smem_u32(slot + at)),
-                           "l"(sa + min(c, t.cnt - 1))
-                           : "memory");
+              copy4(slot + at, sa + min(c, t.cnt - 1));
             }
           }
-          if (lane == 0)
-            asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(smem_u32(slot + C::ACC)), "l"(sb + kb)
-                         : "memory");
-          asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(smem_u32(&sfull[s])) : "memory");
-          if (++s == C::SLOTS) {
-            s = 0;
-            ph ^= 1;
-          }
+          if (lane == 0) copy4(slot + C::ACC, sb + kb);
+          filled();
         }
       }
       asm volatile("cp.async.wait_all;" ::: "memory");
@@ -482,6 +510,8 @@ __global__ void __launch_bounds__(TC_THREADS, 1)
     uint8_t* out = sm + C::OFF_OUT + warp * C::OUT_WARP;
     const uint32_t lanes = tmem + ((uint32_t)(quad * 32) << 16);
     uint32_t v = 0;  // accumulators so far
+    uint32_t s = 0, sph = 0;
+    const float* ring = reinterpret_cast<const float*>(sm + C::OFF_SCALE);
     bool ok = true;
     // The accumulator is in registers: back to the MMAs.
     auto give_back = [&](uint32_t b) {
@@ -494,13 +524,11 @@ __global__ void __launch_bounds__(TC_THREADS, 1)
         const TcUnit t = unit_of(u);
         const int row = rank * 128 + quad * 32;      // first of the warp's 32 rows in the tile
         const int live = t.n > 128 * half ? min(32, t.cnt - row) : 0;  // its rows of a, <= 0: none
-        const float* sa = p.sa + t.row0 + min(row + lane, t.cnt - 1);
-        const float* sb = p.sb + ((size_t)t.e * p.nb + min(t.wt * 2 + half, p.nb - 1)) * p.kb;
         uint64_t acc[64];
 #pragma unroll
         for (int i = 0; i < 64; ++i) acc[i] = 0ull;
-        // One K block with the scales a, w, which are then loaded for the block two further on.
-        auto promote = [&](int kb, float& a, float& w) -> bool {
+        auto promote = [&](const float* sa, const float* sb) -> bool {  // one K block
+          const float sc = sa[quad * 32 + lane] * sb[half];
           const uint32_t b = 2 * half + (v & 1), bph = (v >> 1) & 1;
           ++v;
           if (!wait(&tfull[b], bph)) return false;
@@ -509,12 +537,7 @@ __global__ void __launch_bounds__(TC_THREADS, 1)
             const uint32_t ta = lanes + b * C::ACC;
             uint32_t r[2][16];
             tc05::ld_32x32b_x16(ta, r[0]);
-            const float sc = a * w;
             const uint64_t s2 = f2pack(sc, sc);
-            if (kb + 2 < p.kb) {
-              a = __ldg(sa + (size_t)(kb + 2) * p.M);
-              w = __ldg(sb + kb + 2);
-            }
 #pragma unroll
             for (int c = 0; c < 8; ++c) {
               tc05::wait_ld16(r[c & 1]);
@@ -529,14 +552,18 @@ __global__ void __launch_bounds__(TC_THREADS, 1)
           }
           return true;
         };
-        float a0 = __ldg(sa), w0 = __ldg(sb), a1 = 0.f, w1 = 0.f;
-        if (p.kb > 1) {
-          a1 = __ldg(sa + p.M);
-          w1 = __ldg(sb + 1);
-        }
-        for (int kb = 0; kb < p.kb && ok; kb += 2) {
-          ok = promote(kb, a0, w0);
-          if (ok && kb + 1 < p.kb) ok = promote(kb + 1, a1, w1);
+        for (int kb = 0; kb < p.kb && ok; kb += 4) {
+          ok = wait(&sfull[s], sph);
+          const float* slot = ring + s * C::SLOT_FLOATS;
+#pragma unroll
+          for (int j = 0; j < 4; ++j)
+            if (ok && kb + j < p.kb) ok = promote(slot + 128 * j, slot + 512 + 2 * j);
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&sempty[s]);  // every lane has used its scales
+          if (++s == C::SLOTS) {
+            s = 0;
+            sph ^= 1;
+          }
         }
         if (!ok) break;
         // Output: 128-byte pieces of 32 rows in the 128-byte swizzle, copied out by
@@ -590,8 +617,6 @@ __global__ void __launch_bounds__(TC_THREADS, 1)
       asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
     } else {
       const int g = lane >> 2, q = lane & 3;
-      uint32_t s = 0, sph = 0;
-      const float* ring = reinterpret_cast<const float*>(sm + C::OFF_SCALE);
       for (int u = u0; u < n_units && ok; u += ustep) {
         const TcUnit t = unit_of(u);
         const int nh = t.n >> 1;
