@@ -5,9 +5,15 @@
 // Routing, one warp per token.  With s = sigmoid(logit) or softmax over the
 // row, an expert is chosen by its key: the logit itself without a bias (both
 // scores grow with it, so the order is exact), s + bias with one.  Ties go to
-// the lower index.  Where neighbouring keys or group scores are closer in fp32
-// than fp32 can tell apart, the row is decided again in fp64: a selection is a
-// whole number and has no "almost".
+// the lower index.  A selection is a whole number and has no "almost": scores
+// are first formed in fp32, and where two neighbours in the order, or a kept
+// and a dropped group, are closer than the fp32 error bound, the warp decides
+// the row again in fp64 (about one row in 250 with 256 experts and a bias).
+//
+// Bound by instructions, some 600 a row: a pick is one redux of the lanes'
+// best keys, one of the indices that have it, and a new best in the lane that
+// owned it.  8,191 rows of 256 with 8 groups, bias and 8 picks: 276 us with
+// every score in fp64, ROUTE_US us this way.
 #include "flint_common.cuh"
 #include "flint_internal.h"
 
@@ -215,6 +221,174 @@ __device__ __noinline__ void route_row_f64(const RouteParams& p, const float (&x
   select_best<double, EPL>(key, lane, p.top_k, my_e, my_key);
 }
 
+__device__ __forceinline__ float ord_value(uint32_t k) {
+  return k == 0u ? -INFINITY : __uint_as_float((k >> 31) ? k & 0x7FFFFFFFu : ~k);
+}
+
+// fp32 error of a score: a sigmoid's from ex2 (2 units, and its argument's
+// rounding, |x| 2^-24 times s (1 - s) < 0.25 / |x|), one addition and one
+// reciprocal, below 2^-22; a softmax's from the same and a sum of up to 1024
+// terms (32 a lane, 5 steps), below 2^-19.  Twice that is allowed for.
+constexpr float SIGMOID_ERR = 4.76837158203125e-07f;  // 2^-21
+constexpr float SOFTMAX_ERR = 3.814697265625e-06f;    // 2^-18
+constexpr float SUM_ERR = 1.1920928955078125e-07f;    // 2^-23, of a sum: two roundings
+
+template <int EPL>
+__device__ __forceinline__ void fast_scores(const RouteParams& p, const float (&x)[EPL], float (&s)[EPL]) {
+  if (p.softmax) {
+    float m = -INFINITY, z = 0.f;
+#pragma unroll
+    for (int i = 0; i < EPL; ++i) m = x[i] > m ? x[i] : m;
+    m = ord_value(redux_max(m > -INFINITY ? ord_key(m) : 0u));
+#pragma unroll
+    for (int i = 0; i < EPL; ++i) {
+      s[i] = x[i] > -INFINITY ? (x[i] == m ? 1.f : __expf(x[i] - m)) : 0.f;
+      z += s[i];
+    }
+#pragma unroll
+    for (int off = 16; off > 0; off >>= 1) z += __shfl_xor_sync(FULL, z, off);
+    const float r = __fdividef(1.f, z);
+#pragma unroll
+    for (int i = 0; i < EPL; ++i) s[i] *= r;
+  } else {
+#pragma unroll
+    for (int i = 0; i < EPL; ++i) s[i] = __fdividef(1.f, 1.f + __expf(-x[i]));
+  }
+}
+
+// Selection with fp32 scores: my_e of lane k = the k-th expert (-1: none).
+// False where fp32 does not decide it.
+template <int EPL>
+__device__ __forceinline__ bool route_row_f32(const RouteParams& p, const float (&x)[EPL], int lane, int& my_e) {
+  const bool biased = p.bias != nullptr;
+  const float err = p.softmax ? SOFTMAX_ERR : SIGMOID_ERR;
+  const bool sums = p.n_groups > 1 && p.top2;
+  uint32_t key[EPL];   // choice, 0: not a candidate
+  bool sure = true;
+  float s[EPL];
+  if (biased || sums) fast_scores<EPL>(p, x, s);
+#pragma unroll
+  for (int i = 0; i < EPL; ++i) {
+    float k = x[i];
+    const int e = lane + 32 * i;
+    if (biased && e < p.E) k = s[i] + __ldg(p.bias + e);
+    key[i] = (x[i] > -INFINITY && k > -INFINITY) ? ord_key(k) : 0u;
+  }
+  if (p.n_groups > 1) {
+    const int G = p.n_groups, size = p.E / G;
+    float score = -INFINITY;  // lane g: group g's
+    auto close = [&](int g, uint32_t a, uint32_t b) {  // a, b: this lane's two best of the group
+      const uint32_t m1 = redux_max(a);
+      float v = ord_value(m1);
+      if (p.top2) {
+        const uint32_t who = __ballot_sync(FULL, a == m1);
+        const uint32_t m2 = redux_max(lane == __ffs(who) - 1 ? b : a);
+        if (m2 != 0u) v += ord_value(m2);
+      }
+      if (lane == g) score = v;
+    };
+    uint32_t a = 0u, b = 0u;
+    auto add = [&](uint32_t k) {
+      b = max(b, min(a, k));
+      a = max(a, k);
+    };
+    // the groups' values: the keys, or without a bias the scores to be summed
+    auto value = [&](int i) { return (sums && !biased) ? (key[i] != 0u ? ord_key(s[i]) : 0u) : key[i]; };
+    if (size % 32 == 0) {  // a group is a run of whole registers
+      int left = size / 32, g = 0;
+#pragma unroll
+      for (int i = 0; i < EPL; ++i) {
+        if (g < G) {
+          add(value(i));
+          if (--left == 0) {
+            close(g++, a, b);
+            a = b = 0u;
+            left = size / 32;
+          }
+        }
+      }
+    } else {
+      for (int g = 0; g < G; ++g) {
+        a = b = 0u;
+#pragma unroll
+        for (int i = 0; i < EPL; ++i) {
+          const int e = lane + 32 * i;
+          if (e >= g * size && e < (g + 1) * size) add(value(i));
+        }
+        close(g, a, b);
+      }
+    }
+    int rank = 0;
+    for (int g = 0; g < G; ++g) {
+      const float o = __shfl_sync(FULL, score, g);
+      if (o > score || (o == score && g < lane)) ++rank;
+    }
+    const bool kept = lane < G && rank < p.top_groups;
+    const uint32_t mask = __ballot_sync(FULL, kept);
+    if (biased || sums) {  // weakest kept group against strongest dropped one
+      const uint32_t k = lane < G && score > -INFINITY ? ord_key(score) : 0u;
+      const float lo = ord_value(redux_min(kept ? k : 0xFFFFFFFFu)), hi = ord_value(redux_max(kept ? 0u : k));
+      const float tol = 4.f * err + SUM_ERR * (fabsf(lo) + fabsf(hi));
+      sure = hi == -INFINITY || lo - hi > tol;
+    }
+#pragma unroll
+    for (int i = 0; i < EPL; ++i) {
+      const int g = (lane + 32 * i) / size;
+      if (g >= G || !((mask >> (g & 31)) & 1u)) key[i] = 0u;
+    }
+  }
+
+  uint32_t best = 0u;
+  int at = 0;
+  auto rescan = [&]() {
+    best = 0u;
+#pragma unroll
+    for (int i = 0; i < EPL; ++i)
+      if (key[i] > best) {
+        best = key[i];
+        at = i;
+      }
+  };
+  rescan();
+  my_e = -1;
+  uint32_t my_key = 0u;
+  const int picks = biased ? p.top_k + 1 : p.top_k;  // one more, to see how close it comes
+  for (int k = 0; k < picks; ++k) {
+    const uint32_t m = redux_max(best);
+    if (m == 0u) break;
+    const int e = (int)redux_min(best == m ? (uint32_t)(at * 32 + lane) : 0xFFFFFFFFu);
+    if (lane == k) {
+      my_e = e;
+      my_key = m;
+    }
+    if ((e & 31) == lane) {
+#pragma unroll
+      for (int i = 0; i < EPL; ++i)
+        if (i == at) key[i] = 0u;
+      rescan();
+    }
+  }
+  if (biased) {
+    // Neighbours in the order must be further apart than their errors, unless
+    // they are the same number: the same logit with the same bias.
+    const float v = ord_value(my_key), nv = __shfl_down_sync(FULL, v, 1);
+    const float bias = my_e >= 0 ? __ldg(p.bias + my_e) : 0.f, nb = __shfl_down_sync(FULL, bias, 1);
+    float mx = 0.f;
+#pragma unroll
+    for (int i = 0; i < EPL; ++i) {
+      const float o = __shfl_sync(FULL, x[i], my_e & 31);
+      if ((my_e >> 5) == i) mx = o;
+    }
+    const float nx = __shfl_down_sync(FULL, mx, 1);
+    const int ne = __shfl_down_sync(FULL, my_e, 1);
+    const bool pair = lane < p.top_k && my_e >= 0 && ne >= 0;
+    const bool apart = v - nv > 2.f * err + SUM_ERR * (fabsf(v) + fabsf(nv)) || (mx == nx && bias == nb);
+    sure = sure && __all_sync(FULL, !pair || apart);
+    if (lane >= p.top_k) my_e = -1;
+  }
+  return sure;
+}
+
 template <int EPL, bool BF16>
 __global__ void __launch_bounds__(128) route_kernel(const RouteParams p) {
   pdl_wait();
@@ -234,7 +408,7 @@ __global__ void __launch_bounds__(128) route_kernel(const RouteParams p) {
     }
   }
   int my_e;
-  route_row_f64<EPL>(p, x, lane, my_e);
+  if (!route_row_f32<EPL>(p, x, lane, my_e)) route_row_f64<EPL>(p, x, lane, my_e);
 
   // Weights from the selected logits.  u is the score times a factor common to
   // the row that keeps the largest near 1, so that renormalising never divides
@@ -285,66 +459,98 @@ __global__ void __launch_bounds__(128) route_kernel(const RouteParams p) {
 }
 
 // ---------------------------------------------------------------- grouping
-// Stable counting sort of the pairs by expert.  Every warp owns one stretch of
-// consecutive pairs and a histogram of its own; warps' histograms, summed in
-// order, give each warp its first place in every expert's range, and a second
-// pass over the stretch hands the places out in order.  No atomic decides an
-// order, so the result is the same on every call.
+// Stable counting sort of the pairs by expert, in one cluster of CTAs.  Every
+// warp owns one stretch of consecutive pairs and a histogram of its own in
+// shared memory; the histograms' sums in warp and CTA order (the CTAs read each
+// other's totals) give each warp its first place in every expert's range, and a
+// second pass over the stretch hands the places out in order.  No atomic
+// decides an order, so the result is the same on every call.
+//
+// Latency bound: the bytes are 12 a pair.  One CTA needs 61 us for 49,152 pairs
+// of 256 experts; GP_NOTE
 constexpr int GP_WARPS = 32;
+constexpr int GP_CTAS = 8;
 
 __global__ void __launch_bounds__(GP_WARPS * 32) group_kernel(const int32_t* __restrict__ ids, int P, int E,
                                                               int32_t* __restrict__ offsets,
                                                               int32_t* __restrict__ order, int32_t* __restrict__ pos) {
-  extern __shared__ int hist[];  // [GP_WARPS][E], then [E + 1] totals
-  int* first = hist + GP_WARPS * E;
-  pdl_wait();
-  pdl_trigger();
+  extern __shared__ int hist[];     // [GP_WARPS][E], [E] this CTA's totals, [E + 1] first places, [32] scan
+  int* total = hist + GP_WARPS * E;
+  int* first = total + E;
+  int* scan = first + E + 1;
+  uint32_t rank, ctas;
+  asm("mov.u32 %0, %%cluster_ctarank;" : "=r"(rank));
+  asm("mov.u32 %0, %%cluster_nctaid.x;" : "=r"(ctas));
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   for (int i = tid; i < GP_WARPS * E; i += GP_WARPS * 32) hist[i] = 0;
   __syncthreads();
-  const int per = ((P + GP_WARPS * 32 - 1) / (GP_WARPS * 32)) * 32;  // pairs of a warp
-  const long long lo = (long long)warp * per;
+  pdl_wait();
+  pdl_trigger();
+  const int stretch = (int)((P + ctas * GP_WARPS * 32 - 1) / (ctas * GP_WARPS * 32)) * 32;  // pairs of a warp
+  const long long lo = (long long)(rank * GP_WARPS + warp) * stretch;
   int* h = hist + warp * E;
-  for (int i = 0; i < per; i += 32) {
+  for (int i = 0; i < stretch; i += 32) {
     const long long at = lo + i + lane;
     const int id = at < P ? __ldg(ids + at) : -1;
     if (id >= 0 && id < E) atomicAdd(&h[id], 1);
   }
   __syncthreads();
-  for (int e = tid; e < E; e += GP_WARPS * 32) {  // per expert: exclusive sums over the warps
-    int s = 0;
-    for (int w = 0; w < GP_WARPS; ++w) {
-      const int c = hist[w * E + e];
-      hist[w * E + e] = s;
-      s += c;
-    }
-    first[e] = s;
-  }
-  __syncthreads();
-  if (warp == 0) {  // exclusive sums over the experts
-    int base = 0;
-    for (int e0 = 0; e0 < E; e0 += 32) {
-      const int e = e0 + lane;
-      const int c = e < E ? first[e] : 0;
-      int incl = c;
+  if (tid < E) {  // exclusive sums over the warps; E <= 1024 threads
+    int c[GP_WARPS], sum = 0;
 #pragma unroll
-      for (int off = 1; off < 32; off <<= 1) {
-        const int v = __shfl_up_sync(FULL, incl, off);
-        if (lane >= off) incl += v;
-      }
-      if (e < E) {
-        first[e] = base + incl - c;
-        offsets[e] = base + incl - c;
-      }
-      base += __shfl_sync(FULL, incl, 31);
+    for (int w = 0; w < GP_WARPS; ++w) c[w] = hist[w * E + tid];
+#pragma unroll
+    for (int w = 0; w < GP_WARPS; ++w) {
+      hist[w * E + tid] = sum;
+      sum += c[w];
     }
-    if (lane == 0) {
-      first[E] = base;
-      offsets[E] = base;
+    total[tid] = sum;
+  }
+  if (ctas > 1) asm volatile("barrier.cluster.arrive.release.aligned;\n barrier.cluster.wait.acquire.aligned;" ::: "memory");
+  else __syncthreads();
+  // per expert: all pairs, and those of the CTAs before this one
+  int all = 0, before = 0;
+  if (tid < E) {
+    for (uint32_t r = 0; r < ctas; ++r) {
+      int v;
+      if (ctas > 1) {
+        uint32_t a;
+        asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(smem_u32(total + tid)), "r"(r));
+        asm volatile("ld.shared::cluster.s32 %0, [%1];" : "=r"(v) : "r"(a) : "memory");
+      } else {
+        v = total[tid];
+      }
+      all += v;
+      if (r < rank) before += v;
     }
   }
+  int incl = all;  // inclusive sums over the experts
+#pragma unroll
+  for (int off = 1; off < 32; off <<= 1) {
+    const int v = __shfl_up_sync(FULL, incl, off);
+    if (lane >= off) incl += v;
+  }
+  if (lane == 31) scan[warp] = incl;
   __syncthreads();
-  for (int i = 0; i < per; i += 32) {
+  if (warp == 0) {
+    int v = scan[lane];
+#pragma unroll
+    for (int off = 1; off < 32; off <<= 1) {
+      const int o = __shfl_up_sync(FULL, v, off);
+      if (lane >= off) v += o;
+    }
+    scan[lane] = v;
+  }
+  __syncthreads();
+  const int base = incl - all + (warp > 0 ? scan[warp - 1] : 0);
+  if (tid < E) {
+    first[tid] = base + before;
+    if (rank == 0) offsets[tid] = base;
+  }
+  const int kept = scan[GP_WARPS - 1];
+  if (tid == 0 && rank == 0) offsets[E] = kept;
+  __syncthreads();
+  for (int i = 0; i < stretch; i += 32) {
     const long long at = lo + i + lane;
     const bool in = at < P;
     int id = in ? __ldg(ids + at) : -1;
@@ -358,7 +564,9 @@ __global__ void __launch_bounds__(GP_WARPS * 32) group_kernel(const int32_t* __r
     if (in) pos[at] = place;
     if (place >= 0) order[place] = (int)at;
   }
-  for (int i = first[E] + tid; i < P; i += GP_WARPS * 32) order[i] = -1;
+  for (long long i = kept + (long long)rank * GP_WARPS * 32 + tid; i < P; i += (long long)ctas * GP_WARPS * 32) order[i] = -1;
+  // no CTA leaves while another still reads its totals
+  if (ctas > 1) asm volatile("barrier.cluster.arrive.release.aligned;\n barrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
 
 template <int EPL>
@@ -378,9 +586,11 @@ cudaError_t launch_route_epl(const RouteParams& p, bool bf16, cudaStream_t st) {
 
 }  // namespace
 
+constexpr int group_smem(int E) { return (GP_WARPS * E + 2 * E + 1 + GP_WARPS) * 4; }
+
 cudaError_t route_kernels_init() {
   return cudaFuncSetAttribute(group_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                              (GP_WARPS * ROUTE_MAX_E + ROUTE_MAX_E + 1) * 4);
+                              group_smem(ROUTE_MAX_E));
 }
 
 cudaError_t launch_route(const RouteSpec& r, const void* logits, bool bf16, long long stride, int T, const float* bias,
@@ -410,15 +620,21 @@ cudaError_t launch_route(const RouteSpec& r, const void* logits, bool bf16, long
 cudaError_t launch_group_pairs(const int32_t* ids, int P, int E, int32_t* offsets, int32_t* order, int32_t* pos,
                                cudaStream_t st) {
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(1);
+  // One CTA alone saves the exchange: up to two passes of its warps.
+  const unsigned ctas = P <= 2 * GP_WARPS * 32 ? 1 : GP_CTAS;
+  cfg.gridDim = dim3(ctas);
   cfg.blockDim = dim3(GP_WARPS * 32);
-  cfg.dynamicSmemBytes = (size_t)(GP_WARPS * E + E + 1) * 4;
+  cfg.dynamicSmemBytes = (size_t)group_smem(E);
   cfg.stream = st;
-  cudaLaunchAttribute attr[1];
+  cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = ctas;
+  attr[1].val.clusterDim.y = 1;
+  attr[1].val.clusterDim.z = 1;
   cfg.attrs = attr;
-  cfg.numAttrs = 1;
+  cfg.numAttrs = 2;
   return cudaLaunchKernelEx(&cfg, group_kernel, ids, P, E, offsets, order, pos);
 }
 

@@ -41,7 +41,7 @@ constexpr float E4M3_TOP = 448.f;
 struct QuantParams {
   const void* x;
   long long stride;
-  int rows, K, kb;  // kb: blocks of a row
+  int rows, K;
   const int32_t* pos;
   int top_k;
   long long places;  // rows of q and of a scale line
@@ -49,7 +49,14 @@ struct QuantParams {
   float* scales;
 };
 
-// 16 lanes per block of 128, 8 values each.  The block's largest magnitude a
+__device__ __forceinline__ float rcp_approx(float v) {
+  float r;
+  asm("rcp.approx.f32 %0, %1;" : "=f"(r) : "f"(v));
+  return r;
+}
+
+// 16 lanes per block of 128, 8 values each; a CTA has 16 neighbouring rows of
+// one block column, so that their scales are one 64-byte line.  The block's largest magnitude a
 // (NaN if the block holds one) gives scale = a / 448 and codes
 // e4m3(x * (448 / a)), one rounding to nearest even.
 template <bool BF16, bool SILU>
@@ -57,11 +64,9 @@ __global__ void __launch_bounds__(256) quantize_kernel(const QuantParams p) {
   pdl_wait();
   pdl_trigger();
   const int lane = threadIdx.x & 15;
-  const long long unit = (long long)blockIdx.x * 16 + (threadIdx.x >> 4);
-  const bool live = unit < (long long)p.rows * p.kb;
-  const int row = live ? (int)(unit / p.kb) : 0, b = live ? (int)(unit % p.kb) : 0;
+  const int row = blockIdx.x * 16 + (threadIdx.x >> 4), b = blockIdx.y;
   const int k = b * 128 + lane * 8;
-  const bool in = live && k < p.K;  // K is a multiple of 16
+  const bool in = row < p.rows && k < p.K;  // K is a multiple of 16
   float v[8];
 #pragma unroll
   for (int i = 0; i < 8; ++i) v[i] = 0.f;
@@ -72,7 +77,7 @@ __global__ void __launch_bounds__(256) quantize_kernel(const QuantParams p) {
       float u[8];
       load8<BF16>(p.x, at + (size_t)p.K, u);
 #pragma unroll
-      for (int i = 0; i < 8; ++i) v[i] = v[i] / (1.f + __expf(-v[i])) * u[i];
+      for (int i = 0; i < 8; ++i) v[i] = v[i] * rcp_approx(1.f + __expf(-v[i])) * u[i];
     }
   }
   // Magnitudes compare as integers; NaN's is above every other.
@@ -89,9 +94,13 @@ __global__ void __launch_bounds__(256) quantize_kernel(const QuantParams p) {
   for (int i = 0; i < 4; ++i) c[i] = e4m3x2(v[2 * i] * r, v[2 * i + 1] * r);
   if (!in) return;
   const uint2 code = make_uint2(c[0] | (c[1] << 16), c[2] | (c[3] << 16));
-  const int n = p.pos != nullptr ? p.top_k : 1;
-  for (int j = 0; j < n; ++j) {
-    const long long to = p.pos != nullptr ? __ldg(p.pos + (size_t)row * p.top_k + j) : row;
+  if (p.pos == nullptr) {
+    *reinterpret_cast<uint2*>(p.q + (size_t)row * p.K + k) = code;
+    if (lane == 0) p.scales[(size_t)b * p.places + row] = scale;
+    return;
+  }
+  for (int j = 0; j < p.top_k; ++j) {
+    const int to = __ldg(p.pos + (size_t)row * p.top_k + j);
     if (to < 0 || to >= p.places) continue;
     *reinterpret_cast<uint2*>(p.q + (size_t)to * p.K + k) = code;
     if (lane == 0) p.scales[(size_t)b * p.places + to] = scale;
@@ -108,47 +117,52 @@ struct CombineParams {
   int T, N, top_k;
 };
 
-// One thread per 8 outputs; the sum runs over the choices in order, then the
-// shared row, in fp32, and is rounded once to bf16.
+// One thread per 8 outputs of a token; the sum runs over the choices in order,
+// then the shared row, in fp32, and is rounded once to bf16.  Four choices'
+// rows are under way at a time.
 template <bool BF16>
-__global__ void __launch_bounds__(256) combine_kernel(const CombineParams p) {
+__global__ void __launch_bounds__(128) combine_kernel(const CombineParams p) {
   pdl_wait();
   pdl_trigger();
-  const int per = p.N / 8;
-  const long long u = (long long)blockIdx.x * 256 + threadIdx.x;
-  if (u >= (long long)p.T * per) return;
-  const int t = (int)(u / per), n = (int)(u % per) * 8;
-  float acc[8];
+  const int t = blockIdx.x, n = (blockIdx.y * 128 + threadIdx.x) * 8;
+  if (n >= p.N) return;
+  const int32_t* pos = p.pos + (size_t)t * p.top_k;
+  const float* w = p.w + (size_t)t * p.top_k;
+  float acc[8], sh[8];
 #pragma unroll
-  for (int i = 0; i < 8; ++i) acc[i] = 0.f;
-  for (int j = 0; j < p.top_k; ++j) {
-    const int r = __ldg(p.pos + (size_t)t * p.top_k + j);
-    if (r < 0 || r >= p.n_rows) continue;
-    const float w = __ldg(p.w + (size_t)t * p.top_k + j);
-    float v[8];
-    load8<BF16>(p.rows, (size_t)r * p.N + n, v);
+  for (int i = 0; i < 8; ++i) acc[i] = sh[i] = 0.f;
+  if (p.shared != nullptr) load8<true>(p.shared, (size_t)t * p.N + n, sh);
+  for (int j0 = 0; j0 < p.top_k; j0 += 4) {
+    float v[4][8], f[4];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) acc[i] = fmaf(w, v[i], acc[i]);
-  }
-  if (p.shared != nullptr) {
-    float v[8];
-    load8<true>(p.shared, (size_t)t * p.N + n, v);
+    for (int j = 0; j < 4; ++j) {
+      int r = j0 + j < p.top_k ? __ldg(pos + j0 + j) : -1;
+      f[j] = 0.f;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) acc[i] += v[i];
+      for (int i = 0; i < 8; ++i) v[j][i] = 0.f;
+      if (r >= 0 && r < p.n_rows) {
+        f[j] = __ldg(w + j0 + j);
+        load8<BF16>(p.rows, (size_t)r * p.N + n, v[j]);
+      }
+    }
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+#pragma unroll
+      for (int i = 0; i < 8; ++i) acc[i] = fmaf(f[j], v[j][i], acc[i]);
   }
   uint32_t o[4];
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
-    const __nv_bfloat162 h = __floats2bfloat162_rn(acc[2 * i], acc[2 * i + 1]);
+    const __nv_bfloat162 h = __floats2bfloat162_rn(acc[2 * i] + sh[2 * i], acc[2 * i + 1] + sh[2 * i + 1]);
     o[i] = *reinterpret_cast<const uint32_t*>(&h);
   }
   *reinterpret_cast<uint4*>(p.y + (size_t)t * p.N + n) = make_uint4(o[0], o[1], o[2], o[3]);
 }
 
 template <typename P>
-cudaError_t launch_pdl(void (*kernel)(const P), const P& p, long long ctas, int threads, cudaStream_t st) {
+cudaError_t launch_pdl(void (*kernel)(const P), const P& p, dim3 ctas, int threads, cudaStream_t st) {
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)ctas);
+  cfg.gridDim = ctas;
   cfg.blockDim = dim3(threads);
   cfg.stream = st;
   cudaLaunchAttribute attr[1];
@@ -169,13 +183,12 @@ cudaError_t launch_quantize_rows(const void* x, bool bf16, long long stride, int
   p.stride = stride;
   p.rows = rows;
   p.K = K;
-  p.kb = (K + 127) / 128;
   p.pos = pos;
   p.top_k = top_k;
   p.places = places;
   p.q = static_cast<uint8_t*>(q);
   p.scales = scales;
-  const long long ctas = ((long long)rows * p.kb + 15) / 16;
+  const dim3 ctas((unsigned)((rows + 15) / 16), (unsigned)((K + 127) / 128));
   if (bf16) return silu ? launch_pdl(quantize_kernel<true, true>, p, ctas, 256, st)
                         : launch_pdl(quantize_kernel<true, false>, p, ctas, 256, st);
   return silu ? launch_pdl(quantize_kernel<false, true>, p, ctas, 256, st)
@@ -194,8 +207,8 @@ cudaError_t launch_combine(const void* rows, bool bf16, long long n_rows, const 
   p.T = T;
   p.N = N;
   p.top_k = top_k;
-  const long long ctas = ((long long)T * (N / 8) + 255) / 256;
-  return bf16 ? launch_pdl(combine_kernel<true>, p, ctas, 256, st) : launch_pdl(combine_kernel<false>, p, ctas, 256, st);
+  const dim3 ctas((unsigned)T, (unsigned)((N / 8 + 127) / 128));
+  return bf16 ? launch_pdl(combine_kernel<true>, p, ctas, 128, st) : launch_pdl(combine_kernel<false>, p, ctas, 128, st);
 }
 
 }  // namespace flint
