@@ -9,6 +9,7 @@ be built or loaded the import-time call ``load_library`` raises.
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 import threading
 
@@ -379,44 +380,85 @@ def dense_gemv(w: DenseNVFP4, x, y, stream=None):
     _check(rc, "flint_moe_dense_gemv")
 
 
+# The calls below are short beside their own marshalling, so each tensor is first
+# looked over with the few queries that decide it; the checks that name what is
+# wrong run only when that look fails.
+
+_ACT_TYPES = {torch.bfloat16: T_BF16, torch.float32: T_F32}
+
+
+def _fits(t, dtype, shape, device):
+    return t.dtype is dtype and t.shape == shape and t.get_device() == device and t.is_contiguous()
+
+
+def _on(device):
+    """Whether tensors on `device` (an index, -1: none) are on the current CUDA device."""
+    return device >= 0 and device == torch._C._cuda_getDevice()
+
+
+def _raw_stream(stream, device):
+    return torch._C._cuda_getCurrentRawStream(device) if stream is None else _stream(stream)
+
+
 def _expect_rows(t, name, types, width):
     """_expect for a matrix whose rows may lie apart: dtype one of `types`, last
-    dimension contiguous, on the current CUDA device.  Returns (type code, rows,
-    row stride in elements)."""
+    dimension contiguous, on the current CUDA device."""
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name}: expected a torch.Tensor, got {type(t).__name__}")
     if t.dtype not in types:
         raise ValueError(f"{name}: dtype {t.dtype}, expected {' or '.join(str(d) for d in types)}")
-    shape = t.shape
-    if len(shape) != 2 or (width is not None and shape[1] != width):
-        raise ValueError(f"{name}: shape {tuple(shape)}, expected [rows][{'columns' if width is None else width}]")
-    rows = shape[0]
-    stride = t.stride()
-    if stride[1] != 1 and shape[1] != 1:
+    if t.dim() != 2 or (width is not None and t.shape[1] != width):
+        raise ValueError(f"{name}: shape {tuple(t.shape)}, expected [rows][{'columns' if width is None else width}]")
+    if t.stride(1) != 1 and t.shape[1] != 1:
         raise ValueError(f"{name}: the elements of a row must be contiguous")
-    if not t.is_cuda or t.get_device() != torch.cuda.current_device():
+    if not t.is_cuda or t.device.index != torch.cuda.current_device():
         raise ValueError(f"{name}: must be on the current CUDA device")
-    return types[t.dtype], rows, (stride[0] if rows > 1 else shape[1])
 
 
-_ACT_TYPES = {torch.bfloat16: T_BF16, torch.float32: T_F32}
+def _matrix(t, name):
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name}: expected a torch.Tensor, got {type(t).__name__}")
+    if t.dim() != 2:
+        raise ValueError(f"{name}: shape {tuple(t.shape)}, expected a matrix")
+    return t.shape
+
+
+def _row_stride(t, rows, width):
+    """Elements between the rows of a matrix whose rows are contiguous, -1 otherwise."""
+    step, unit = t.stride()
+    if unit != 1 and width != 1:
+        return -1
+    return step if rows > 1 else width
+
+
+@functools.lru_cache(maxsize=64)
+def _routing(E, k, score, n_groups, top_groups, group_score, renormalise, scale):
+    r = Routing(E, k, score, n_groups, top_groups, group_score, renormalise, scale)
+    return ctypes.byref(r)
 
 
 def route(logits, ids, w, bias=None, score=SCORE_SIGMOID, n_groups=1, top_groups=1, group_score=GROUP_MAX,
           renormalise=True, scale=1.0, stream=None):
     """Chooses ids.shape[1] experts for every row of logits [T][E] (bf16 or fp32, rows may lie
     apart): ids int32 [T][k], w fp32 [T][k].  bias fp32 [E] is added for the choice only."""
-    kind, T, stride = _expect_rows(logits, "logits", _ACT_TYPES, None)
-    E = logits.shape[1]
-    k = ids.shape[1] if isinstance(ids, torch.Tensor) and ids.dim() == 2 else 0
-    _expect(ids, "ids", torch.int32, (T, k))
-    _expect(w, "w", torch.float32, (T, k))
-    if bias is not None:
-        _expect(bias, "bias", torch.float32, (E,))
-    r = Routing(E, k, score, n_groups, top_groups, group_score, 1 if renormalise else 0, scale)
-    rc = _lib().flint_moe_route(ctypes.byref(r), logits.data_ptr(), kind, stride, T, _ptr(bias), ids.data_ptr(),
-                                w.data_ptr(), _stream(stream))
-    _check(rc, "flint_moe_route")
+    T, E = _matrix(logits, "logits")
+    k = _matrix(ids, "ids")[1]
+    dev = logits.get_device()
+    kind = _ACT_TYPES.get(logits.dtype)
+    stride = _row_stride(logits, T, E)
+    if not (kind is not None and stride >= 0 and _on(dev) and _fits(ids, torch.int32, (T, k), dev)
+            and isinstance(w, torch.Tensor) and _fits(w, torch.float32, (T, k), dev)
+            and (bias is None or (isinstance(bias, torch.Tensor) and _fits(bias, torch.float32, (E,), dev)))):
+        _expect_rows(logits, "logits", _ACT_TYPES, None)
+        _expect(ids, "ids", torch.int32, (T, k))
+        _expect(w, "w", torch.float32, (T, k))
+        if bias is not None:
+            _expect(bias, "bias", torch.float32, (E,))
+    rc = _lib().flint_moe_route(_routing(E, k, score, n_groups, top_groups, group_score, 1 if renormalise else 0, scale),
+                                logits.data_ptr(), kind, stride, T, None if bias is None else bias.data_ptr(),
+                                ids.data_ptr(), w.data_ptr(), _raw_stream(stream, dev))
+    if rc:
+        _check(rc, "flint_moe_route")
 
 
 def group_pairs(ids, offsets, order, pos, stream=None):
@@ -424,35 +466,45 @@ def group_pairs(ids, offsets, order, pos, stream=None):
     [pairs], pos int32 of the shape of ids."""
     if not isinstance(ids, torch.Tensor) or not isinstance(offsets, torch.Tensor):
         raise TypeError("ids, offsets: expected a torch.Tensor")
-    n, E = ids.numel(), offsets.numel() - 1
-    _expect(ids, "ids", torch.int32, ids.shape)
-    _expect(offsets, "offsets", torch.int32, (E + 1,))
-    _expect(order, "order", torch.int32, (n,))
-    _expect(pos, "pos", torch.int32, ids.shape)
+    n, E, shape, dev = ids.numel(), offsets.numel() - 1, ids.shape, ids.get_device()
+    if not (_on(dev) and _fits(ids, torch.int32, shape, dev) and _fits(offsets, torch.int32, (E + 1,), dev)
+            and isinstance(order, torch.Tensor) and _fits(order, torch.int32, (n,), dev)
+            and isinstance(pos, torch.Tensor) and _fits(pos, torch.int32, shape, dev)):
+        _expect(ids, "ids", torch.int32, shape)
+        _expect(offsets, "offsets", torch.int32, (E + 1,))
+        _expect(order, "order", torch.int32, (n,))
+        _expect(pos, "pos", torch.int32, shape)
     rc = _lib().flint_moe_group_pairs(ids.data_ptr(), n, E, offsets.data_ptr(), order.data_ptr(), pos.data_ptr(),
-                                      _stream(stream))
-    _check(rc, "flint_moe_group_pairs")
+                                      _raw_stream(stream, dev))
+    if rc:
+        _check(rc, "flint_moe_group_pairs")
 
 
 def quantize_rows(x, q, scales, pos=None, silu_mul=False, stream=None):
     """Quantises x [rows][K] (bf16 or fp32; silu_mul: [rows][2K], silu(first half) * second
     half) to q float8_e4m3fn [places][K] and scales fp32 [ceil(K / 128)][places]; pos int32
     [rows][k] gives the places of each row, None: row i goes to place i."""
-    if not isinstance(q, torch.Tensor):
-        raise TypeError(f"q: expected a torch.Tensor, got {type(q).__name__}")
-    if q.dim() != 2:
-        raise ValueError(f"q: expected [places][K], got shape {tuple(q.shape)}")
-    places, K = q.shape
-    kind, rows, stride = _expect_rows(x, "x", _ACT_TYPES, 2 * K if silu_mul else K)
-    _expect(q, "q", torch.float8_e4m3fn, (places, K))
-    _expect(scales, "scales", torch.float32, (-(-K // SCALE_BLOCK), places))
-    k = 0
-    if pos is not None:
-        k = pos.shape[1] if isinstance(pos, torch.Tensor) and pos.dim() == 2 else 0
-        _expect(pos, "pos", torch.int32, (rows, k))
-    rc = _lib().flint_moe_quantize_rows(x.data_ptr(), kind, stride, rows, K, 1 if silu_mul else 0, _ptr(pos), k,
-                                        places, q.data_ptr(), scales.data_ptr(), _stream(stream))
-    _check(rc, "flint_moe_quantize_rows")
+    places, K = _matrix(q, "q")
+    rows, width = _matrix(x, "x")
+    k = 0 if pos is None else _matrix(pos, "pos")[1]
+    dev = x.get_device()
+    kind = _ACT_TYPES.get(x.dtype)
+    stride = _row_stride(x, rows, width)
+    lines = -(-K // SCALE_BLOCK)
+    if not (kind is not None and stride >= 0 and width == (2 * K if silu_mul else K) and _on(dev)
+            and _fits(q, torch.float8_e4m3fn, (places, K), dev) and isinstance(scales, torch.Tensor)
+            and _fits(scales, torch.float32, (lines, places), dev)
+            and (pos is None or _fits(pos, torch.int32, (rows, k), dev))):
+        _expect_rows(x, "x", _ACT_TYPES, 2 * K if silu_mul else K)
+        _expect(q, "q", torch.float8_e4m3fn, (places, K))
+        _expect(scales, "scales", torch.float32, (lines, places))
+        if pos is not None:
+            _expect(pos, "pos", torch.int32, (rows, k))
+    rc = _lib().flint_moe_quantize_rows(x.data_ptr(), kind, stride, rows, K, 1 if silu_mul else 0,
+                                        None if pos is None else pos.data_ptr(), k, places, q.data_ptr(),
+                                        scales.data_ptr(), _raw_stream(stream, dev))
+    if rc:
+        _check(rc, "flint_moe_quantize_rows")
 
 
 def block_gemm(a, a_scales, b, b_scales, y, offsets=None, stream=None):
@@ -465,38 +517,55 @@ def block_gemm(a, a_scales, b, b_scales, y, offsets=None, stream=None):
     if b.dim() != 3:
         raise ValueError(f"b: expected [experts][N][K], got shape {tuple(b.shape)}")
     E, N, K = b.shape
-    kb = -(-K // SCALE_BLOCK)
-    kind, M, stride = _expect_rows(y, "y", _ACT_TYPES, N)
-    if stride != N:
-        raise ValueError("y: must be contiguous")
-    _expect(a, "a", torch.float8_e4m3fn, (M, K))
-    _expect(a_scales, "a_scales", torch.float32, (kb, M))
-    _expect(b, "b", torch.float8_e4m3fn, (E, N, K))
-    _expect(b_scales, "b_scales", torch.float32, (E, -(-N // SCALE_BLOCK), kb))
-    if offsets is not None:
-        _expect(offsets, "offsets", torch.int32, (E + 1,))
+    M = _matrix(y, "y")[0]
+    dev = y.get_device()
+    kind = _ACT_TYPES.get(y.dtype)
+    kb, nb = -(-K // SCALE_BLOCK), -(-N // SCALE_BLOCK)
+    if not (kind is not None and _on(dev) and _fits(y, y.dtype, (M, N), dev) and isinstance(a, torch.Tensor)
+            and _fits(a, torch.float8_e4m3fn, (M, K), dev) and isinstance(a_scales, torch.Tensor)
+            and _fits(a_scales, torch.float32, (kb, M), dev) and _fits(b, torch.float8_e4m3fn, (E, N, K), dev)
+            and isinstance(b_scales, torch.Tensor) and _fits(b_scales, torch.float32, (E, nb, kb), dev)
+            and (offsets is None or (isinstance(offsets, torch.Tensor)
+                                     and _fits(offsets, torch.int32, (E + 1,), dev)))):
+        _expect_rows(y, "y", _ACT_TYPES, N)
+        _expect(y, "y", y.dtype, (M, N))
+        _expect(a, "a", torch.float8_e4m3fn, (M, K))
+        _expect(a_scales, "a_scales", torch.float32, (kb, M))
+        _expect(b, "b", torch.float8_e4m3fn, (E, N, K))
+        _expect(b_scales, "b_scales", torch.float32, (E, nb, kb))
+        if offsets is not None:
+            _expect(offsets, "offsets", torch.int32, (E + 1,))
     rc = _lib().flint_moe_block_gemm(a.data_ptr(), a_scales.data_ptr(), M, b.data_ptr(), b_scales.data_ptr(), E,
-                                     _ptr(offsets), N, K, y.data_ptr(), kind, _stream(stream))
-    _check(rc, "flint_moe_block_gemm")
+                                     None if offsets is None else offsets.data_ptr(), N, K, y.data_ptr(), kind,
+                                     _raw_stream(stream, dev))
+    if rc:
+        _check(rc, "flint_moe_block_gemm")
 
 
 def combine(rows, pos, w, y, shared=None, stream=None):
     """y [T][N] (bf16) = sum over j of w[t][j] * rows[pos[t][j]] (+ shared [T][N] bf16); rows
     bf16 or fp32 [any][N], pos int32 and w fp32 [T][k]; pos outside the rows adds nothing."""
-    T = _rows(y, "y")
-    N = y.shape[1]
-    kind, n_rows, stride = _expect_rows(rows, "rows", _ACT_TYPES, N)
-    if stride != N:
-        raise ValueError("rows: must be contiguous")
-    k = pos.shape[1] if isinstance(pos, torch.Tensor) and pos.dim() == 2 else 0
-    _expect(y, "y", torch.bfloat16, (T, N))
-    _expect(pos, "pos", torch.int32, (T, k))
-    _expect(w, "w", torch.float32, (T, k))
-    if shared is not None:
-        _expect(shared, "shared", torch.bfloat16, (T, N))
-    rc = _lib().flint_moe_combine(rows.data_ptr(), kind, n_rows, pos.data_ptr(), w.data_ptr(), T, k, N, _ptr(shared),
-                                  y.data_ptr(), _stream(stream))
-    _check(rc, "flint_moe_combine")
+    T, N = _matrix(y, "y")
+    n_rows = _matrix(rows, "rows")[0]
+    k = _matrix(pos, "pos")[1]
+    dev = y.get_device()
+    kind = _ACT_TYPES.get(rows.dtype)
+    if not (kind is not None and _on(dev) and _fits(rows, rows.dtype, (n_rows, N), dev)
+            and _fits(y, torch.bfloat16, (T, N), dev) and _fits(pos, torch.int32, (T, k), dev)
+            and isinstance(w, torch.Tensor) and _fits(w, torch.float32, (T, k), dev)
+            and (shared is None or (isinstance(shared, torch.Tensor) and _fits(shared, torch.bfloat16, (T, N), dev)))):
+        _expect_rows(rows, "rows", _ACT_TYPES, N)
+        _expect(rows, "rows", rows.dtype, (n_rows, N))
+        _expect(y, "y", torch.bfloat16, (T, N))
+        _expect(pos, "pos", torch.int32, (T, k))
+        _expect(w, "w", torch.float32, (T, k))
+        if shared is not None:
+            _expect(shared, "shared", torch.bfloat16, (T, N))
+    rc = _lib().flint_moe_combine(rows.data_ptr(), kind, n_rows, pos.data_ptr(), w.data_ptr(), T, k, N,
+                                  None if shared is None else shared.data_ptr(), y.data_ptr(),
+                                  _raw_stream(stream, dev))
+    if rc:
+        _check(rc, "flint_moe_combine")
 
 
 def release():
