@@ -26,6 +26,14 @@ struct GemmArgs {
   int M, N, K, E, kb, nb;
 };
 
+// 16 bytes of weights: read once, so not kept in L1.
+__device__ __forceinline__ uint4 ldg_stream(const uint8_t* p) {
+  uint4 v;
+  asm volatile("ld.global.nc.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
+               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+               : "l"(p));
+  return v;
+}
 __device__ __forceinline__ void mma_e4m3(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
                                          uint32_t b0, uint32_t b1) {
   asm("mma.sync.aligned.m16n8k32.row.col.f32.e4m3.e4m3.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};\n"
@@ -33,30 +41,32 @@ __device__ __forceinline__ void mma_e4m3(float (&d)[4], uint32_t a0, uint32_t a1
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 
-// ---- few rows: a CTA streams 16 weight rows once for up to 8 activation rows
-// of one expert.  Grid (M, ceil(N / 16)): the CTA of row r works when r is the
-// first of a run of 8 rows of its expert.  The K blocks go round the 8 warps.
-// Both operands are read straight from global memory into mma fragments: the
-// product of a block does not depend on the order of k, so lane t of a row's
-// four takes bytes 16t..16t+15 of each half block for either operand.
-constexpr int SK_WARPS = 8;
+// ---- few rows: weights are streamed once for up to 8 activation rows of one
+// expert.  Grid (M, N / rows of a CTA): the CTA of row r works when r is the
+// first of a run of 8 rows of its expert.  A warp takes 16 weight rows and every
+// SPLIT-th K block of them; SPLIT warps of a CTA share 16 rows, so that a small
+// product has enough warps (SPLIT 8) and a large one few sums across warps
+// (SPLIT 1).  Both operands are read straight from global memory into mma
+// fragments: the product of a block does not depend on the order of k, so lane
+// t of a row's four takes bytes 16t..16t+15 of each half block for either
+// operand.  Two K blocks (4 KB of weights a warp) are under way at a time.
+constexpr int SK_FULL_WARPS = 1024;
 
-template <bool F32>
-__global__ void __launch_bounds__(SK_WARPS * 32) block_gemm_skinny_kernel(const GemmArgs p) {
-  __shared__ float red[SK_WARPS][128];
+template <int SPLIT, int SK_WARPS, bool F32>
+__global__ void __launch_bounds__(SK_WARPS * 32, 24 / SK_WARPS) block_gemm_skinny_kernel(const GemmArgs p) {
+  __shared__ float red[SPLIT == 1 ? 1 : SK_WARPS][128];
   __shared__ int range[3];
   pdl_wait();
   pdl_trigger();
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int r = blockIdx.x;
-  int e = 0, r0 = r, r1 = p.M;
+  int e = 0, r0 = 0, r1 = p.M;
   if (p.offsets != nullptr) {
     // expert of row r: the number of groups that end at or before it
     if (warp == 0) {
       int ended = 0;
       for (int i = lane; i < p.E; i += 32) ended += __ldg(p.offsets + i + 1) <= r ? 1 : 0;
-#pragma unroll
-      for (int off = 16; off > 0; off >>= 1) ended += __shfl_xor_sync(0xffffffffu, ended, off);
+      ended = (int)__reduce_add_sync(0xffffffffu, (unsigned)ended);
       if (lane == 0) {
         range[0] = ended;
         range[1] = ended < p.E ? __ldg(p.offsets + ended) : 0;
@@ -69,53 +79,57 @@ __global__ void __launch_bounds__(SK_WARPS * 32) block_gemm_skinny_kernel(const 
     r0 = range[1];
     r1 = range[2];
     if (r < r0 || r >= r1) return;
-  } else {
-    r0 = 0;
   }
   if ((r - r0) & 7) return;
   const int n_rows = min(8, r1 - r);
-  const int n0 = blockIdx.y * 16;
+  const int n0 = (blockIdx.y * (SK_WARPS / SPLIT) + warp / SPLIT) * 16;
   const int g = lane >> 2, t = lane & 3;
-  const int na = n0 + g, nb = n0 + g + 8;
-  const uint8_t* b0 = p.b + ((size_t)e * p.N + min(na, p.N - 1)) * p.K;
-  const uint8_t* b1 = p.b + ((size_t)e * p.N + min(nb, p.N - 1)) * p.K;
-  const uint8_t* a0 = p.a + (size_t)(r + min(g, n_rows - 1)) * p.K;
-  const float* sb = p.sb + ((size_t)e * p.nb + n0 / 128) * p.kb;
-  const int c0 = min(2 * t, n_rows - 1), c1 = min(2 * t + 1, n_rows - 1);
   float acc[4] = {0.f, 0.f, 0.f, 0.f};
-  const uint4 zero = make_uint4(0, 0, 0, 0);
-  for (int kb = warp; kb < p.kb; kb += SK_WARPS) {
-    const int k0 = kb * 128 + 16 * t, k1 = k0 + 64;
-    const bool in0 = k0 < p.K, in1 = k1 < p.K;  // K is a multiple of 16
-    const uint4 wa0 = in0 ? __ldg(reinterpret_cast<const uint4*>(b0 + k0)) : zero;
-    const uint4 wb0 = in0 ? __ldg(reinterpret_cast<const uint4*>(b1 + k0)) : zero;
-    const uint4 xa0 = in0 ? __ldg(reinterpret_cast<const uint4*>(a0 + k0)) : zero;
-    const uint4 wa1 = in1 ? __ldg(reinterpret_cast<const uint4*>(b0 + k1)) : zero;
-    const uint4 wb1 = in1 ? __ldg(reinterpret_cast<const uint4*>(b1 + k1)) : zero;
-    const uint4 xa1 = in1 ? __ldg(reinterpret_cast<const uint4*>(a0 + k1)) : zero;
-    const float s = __ldg(sb + kb);
-    const float s0 = s * __ldg(p.sa + (size_t)kb * p.M + r + c0), s1 = s * __ldg(p.sa + (size_t)kb * p.M + r + c1);
-    float d[4] = {0.f, 0.f, 0.f, 0.f};
-    mma_e4m3(d, wa0.x, wb0.x, wa0.y, wb0.y, xa0.x, xa0.y);
-    mma_e4m3(d, wa0.z, wb0.z, wa0.w, wb0.w, xa0.z, xa0.w);
-    mma_e4m3(d, wa1.x, wb1.x, wa1.y, wb1.y, xa1.x, xa1.y);
-    mma_e4m3(d, wa1.z, wb1.z, wa1.w, wb1.w, xa1.z, xa1.w);
-    acc[0] = fmaf(s0, d[0], acc[0]);
-    acc[1] = fmaf(s1, d[1], acc[1]);
-    acc[2] = fmaf(s0, d[2], acc[2]);
-    acc[3] = fmaf(s1, d[3], acc[3]);
-  }
-  // red[warp][column * 16 + weight row]
-  red[warp][(2 * t) * 16 + g] = acc[0];
-  red[warp][(2 * t + 1) * 16 + g] = acc[1];
-  red[warp][(2 * t) * 16 + g + 8] = acc[2];
-  red[warp][(2 * t + 1) * 16 + g + 8] = acc[3];
-  __syncthreads();
-  if (tid < 128) {
-    float v = 0.f;
+  if (n0 < p.N) {
+    const int na = n0 + g, nb = n0 + g + 8;
+    const uint8_t* b0 = p.b + ((size_t)e * p.N + na) * p.K;
+    const uint8_t* b1 = p.b + ((size_t)e * p.N + min(nb, p.N - 1)) * p.K;  // N is a multiple of 8
+    const uint8_t* a0 = p.a + (size_t)(r + min(g, n_rows - 1)) * p.K;
+    const float* sb = p.sb + ((size_t)e * p.nb + n0 / 128) * p.kb;
+    const int c0 = min(2 * t, n_rows - 1), c1 = min(2 * t + 1, n_rows - 1);
+    constexpr int U = 2;
+    for (int kb0 = warp % SPLIT; kb0 < p.kb; kb0 += U * SPLIT) {
+      uint4 w[U][4], x[U][2];
+      float s0[U], s1[U];
 #pragma unroll
-    for (int w = 0; w < SK_WARPS; ++w) v += red[w][tid];
-    const int col = tid >> 4, n = n0 + (tid & 15);
+      for (int i = 0; i < U; ++i) {
+        const int kb = kb0 + i * SPLIT, k0 = kb * 128 + 16 * t, k1 = k0 + 64;
+        const uint4 zero = make_uint4(0, 0, 0, 0);
+        const bool in0 = k0 < p.K, in1 = k1 < p.K;  // K is a multiple of 16
+        w[i][0] = in0 ? ldg_stream(b0 + k0) : zero;
+        w[i][1] = in0 ? ldg_stream(b1 + k0) : zero;
+        w[i][2] = in1 ? ldg_stream(b0 + k1) : zero;
+        w[i][3] = in1 ? ldg_stream(b1 + k1) : zero;
+        x[i][0] = in0 ? __ldg(reinterpret_cast<const uint4*>(a0 + k0)) : zero;
+        x[i][1] = in1 ? __ldg(reinterpret_cast<const uint4*>(a0 + k1)) : zero;
+        s0[i] = s1[i] = 0.f;
+        if (kb < p.kb) {
+          const float s = __ldg(sb + kb);
+          s0[i] = s * __ldg(p.sa + (size_t)kb * p.M + r + c0);
+          s1[i] = s * __ldg(p.sa + (size_t)kb * p.M + r + c1);
+        }
+      }
+#pragma unroll
+      for (int i = 0; i < U; ++i) {
+        if (kb0 + i * SPLIT >= p.kb) break;
+        float d[4] = {0.f, 0.f, 0.f, 0.f};
+        mma_e4m3(d, w[i][0].x, w[i][1].x, w[i][0].y, w[i][1].y, x[i][0].x, x[i][0].y);
+        mma_e4m3(d, w[i][0].z, w[i][1].z, w[i][0].w, w[i][1].w, x[i][0].z, x[i][0].w);
+        mma_e4m3(d, w[i][2].x, w[i][3].x, w[i][2].y, w[i][3].y, x[i][1].x, x[i][1].y);
+        mma_e4m3(d, w[i][2].z, w[i][3].z, w[i][2].w, w[i][3].w, x[i][1].z, x[i][1].w);
+        acc[0] = fmaf(s0[i], d[0], acc[0]);
+        acc[1] = fmaf(s1[i], d[1], acc[1]);
+        acc[2] = fmaf(s0[i], d[2], acc[2]);
+        acc[3] = fmaf(s1[i], d[3], acc[3]);
+      }
+    }
+  }
+  auto store = [&](int col, int n, float v) {
     if (col < n_rows && n < p.N) {
       const size_t at = (size_t)(r + col) * p.N + n;
       if (F32)
@@ -123,7 +137,38 @@ __global__ void __launch_bounds__(SK_WARPS * 32) block_gemm_skinny_kernel(const 
       else
         static_cast<__nv_bfloat16*>(p.y)[at] = __float2bfloat16_rn(v);
     }
+  };
+  if constexpr (SPLIT == 1) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) store(2 * t + (i & 1), n0 + g + (i >> 1) * 8, acc[i]);
+  } else {
+    // red[warp][column * 16 + weight row]
+#pragma unroll
+    for (int i = 0; i < 4; ++i) red[warp][(2 * t + (i & 1)) * 16 + g + (i >> 1) * 8] = acc[i];
+    __syncthreads();
+    for (int o = tid; o < 128 * (SK_WARPS / SPLIT); o += SK_WARPS * 32) {
+      const int tile = o >> 7, c = o & 127;
+      float v = 0.f;
+#pragma unroll
+      for (int w = 0; w < SPLIT; ++w) v += red[tile * SPLIT + w][c];
+      store(c >> 4, (blockIdx.y * (SK_WARPS / SPLIT) + tile) * 16 + (c & 15), v);
+    }
   }
+}
+
+template <int SPLIT, int SK_WARPS, bool F32>
+cudaError_t launch_skinny(const GemmArgs& p, cudaStream_t st) {
+  constexpr int ROWS = SK_WARPS / SPLIT * 16;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)p.M, (unsigned)((p.N + ROWS - 1) / ROWS));
+  cfg.blockDim = dim3(SK_WARPS * 32);
+  cfg.stream = st;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, block_gemm_skinny_kernel<SPLIT, SK_WARPS, F32>, p);
 }
 
 // ---- many rows: tcgen05.
@@ -813,17 +858,10 @@ cudaError_t launch_block_gemm(const void* a, const float* sa, int M, const void*
       return f32 ? launch_tc<true, true>(p, sm_count, err, st) : launch_tc<true, false>(p, sm_count, err, st);
     return f32 ? launch_tc<false, true>(p, sm_count, err, st) : launch_tc<false, false>(p, sm_count, err, st);
   }
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)M, (unsigned)((N + 15) / 16));
-  cfg.blockDim = dim3(SK_WARPS * 32);
-  cfg.stream = st;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  return f32 ? cudaLaunchKernelEx(&cfg, block_gemm_skinny_kernel<true>, p)
-             : cudaLaunchKernelEx(&cfg, block_gemm_skinny_kernel<false>, p);
+  // Warps that the product would have with one warp to 16 weight rows.
+  const long long warps = (long long)M * ((N + 15) / 16);
+  if (warps >= SK_FULL_WARPS) return f32 ? launch_skinny<1, 4, true>(p, st) : launch_skinny<1, 4, false>(p, st);
+  return f32 ? launch_skinny<8, 8, true>(p, st) : launch_skinny<8, 8, false>(p, st);
 }
 
 }  // namespace flint

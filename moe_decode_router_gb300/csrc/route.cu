@@ -7,8 +7,9 @@
 // scores grow with it, so the order is exact), s + bias with one.  Ties go to
 // the lower index.  A selection is a whole number and has no "almost": scores
 // are first formed in fp32, and where two neighbours in the order, or a kept
-// and a dropped group, are closer than the fp32 error bound, the warp decides
-// the row again in fp64 (about one row in 250 with 256 experts and a bias).
+// and a dropped group, are closer than the fp32 error bound, the warp puts those
+// candidates in order in fp64 (about one row in 250 with 256 experts and a
+// bias), or the whole row where that needs more than the candidates.
 //
 // Bound by instructions, some 600 a row: a pick is one redux of the lanes'
 // best keys, one of the indices that have it, and a new best in the lane that
@@ -38,6 +39,7 @@ struct RouteParams {
   float* w;
   int T, E, top_k, n_groups, top_groups;
   int softmax, top2, renorm;
+  uint32_t recip;  // ceil(2^20 / experts of a group): e * recip >> 20 is expert e's group for e < 1024
   float scale;
 };
 
@@ -233,6 +235,12 @@ constexpr float SIGMOID_ERR = 4.76837158203125e-07f;  // 2^-21
 constexpr float SOFTMAX_ERR = 3.814697265625e-06f;    // 2^-18
 constexpr float SUM_ERR = 1.1920928955078125e-07f;    // 2^-23, of a sum: two roundings
 
+__device__ __forceinline__ float rcp_approx(float v) {
+  float r;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(v));
+  return r;
+}
+
 template <int EPL>
 __device__ __forceinline__ void fast_scores(const RouteParams& p, const float (&x)[EPL], float (&s)[EPL]) {
   if (p.softmax) {
@@ -247,13 +255,65 @@ __device__ __forceinline__ void fast_scores(const RouteParams& p, const float (&
     }
 #pragma unroll
     for (int off = 16; off > 0; off >>= 1) z += __shfl_xor_sync(FULL, z, off);
-    const float r = __fdividef(1.f, z);
+    const float r = rcp_approx(z);
 #pragma unroll
     for (int i = 0; i < EPL; ++i) s[i] *= r;
   } else {
 #pragma unroll
-    for (int i = 0; i < EPL; ++i) s[i] = __fdividef(1.f, 1.f + __expf(-x[i]));
+    for (int i = 0; i < EPL; ++i) s[i] = rcp_approx(1.f + __expf(-x[i]));
   }
+}
+
+// Decides the groups in fp64 from each group's two best experts (sigmoid scores),
+// one value a lane.  val: the fp32 values' keys.  False where fp32 does not
+// tell which experts those are, or where there are more than 32.
+template <int EPL>
+__device__ __noinline__ bool refine_groups(const RouteParams& p, const float (&x)[EPL], const uint32_t (&val)[EPL],
+                                           int lane, uint32_t& mask) {
+  const int G = p.n_groups, size = p.E / G, take = p.top2 ? 2 : 1;
+  if (G * take > 32) return false;
+  int mine = -1;  // expert of lane g * take + j
+  for (int g = 0; g < G; ++g) {
+    uint32_t done = 0u;
+    float last = 0.f;
+    for (int j = 0; j <= take; ++j) {  // one more than counts, to see how close it comes
+      uint32_t best = 0u;
+      int at = 0;
+#pragma unroll
+      for (int i = 0; i < EPL; ++i) {
+        const int e = lane + 32 * i;
+        if (e >= g * size && e < (g + 1) * size && !((done >> i) & 1u) && val[i] > best) {
+          best = val[i];
+          at = i;
+        }
+      }
+      const uint32_t m = redux_max(best);
+      if (m == 0u) break;
+      const float v = ord_value(m);
+      if (j == take) {
+        if (!(last - v > 2.f * SIGMOID_ERR + SUM_ERR * (fabsf(v) + fabsf(last)))) return false;
+        break;
+      }
+      last = v;
+      const int e = (int)redux_min(best == m ? (uint32_t)(at * 32 + lane) : 0xFFFFFFFFu);
+      if (lane == g * take + j) mine = e;
+      if ((e & 31) == lane) done |= 1u << at;
+    }
+  }
+  float mx = 0.f;
+#pragma unroll
+  for (int i = 0; i < EPL; ++i) {
+    const float o = __shfl_sync(FULL, x[i], mine & 31);
+    if ((mine >> 5) == i) mx = o;
+  }
+  double v = -INFINITY;
+  if (mine >= 0) v = 1.0 / (1.0 + exp(-(double)mx)) + (p.bias != nullptr ? (double)__ldg(p.bias + mine) : 0.0);
+  const double first = __shfl_sync(FULL, v, (lane * take) & 31), second = __shfl_sync(FULL, v, (lane * take + 1) & 31);
+  double score = lane < G ? first : -INFINITY;
+  if (lane < G && take == 2 && second > -INFINITY) score = first + second;
+  bool unsure;
+  mask = keep_groups<double>(score, lane, G, p.top_groups, 0.0, unsure);
+  return true;
 }
 
 // Selection with fp32 scores: my_e of lane k = the k-th expert (-1: none).
@@ -264,7 +324,6 @@ __device__ __forceinline__ bool route_row_f32(const RouteParams& p, const float 
   const float err = p.softmax ? SOFTMAX_ERR : SIGMOID_ERR;
   const bool sums = p.n_groups > 1 && p.top2;
   uint32_t key[EPL];   // choice, 0: not a candidate
-  bool sure = true;
   float s[EPL];
   if (biased || sums) fast_scores<EPL>(p, x, s);
 #pragma unroll
@@ -324,17 +383,28 @@ __device__ __forceinline__ bool route_row_f32(const RouteParams& p, const float 
       if (o > score || (o == score && g < lane)) ++rank;
     }
     const bool kept = lane < G && rank < p.top_groups;
-    const uint32_t mask = __ballot_sync(FULL, kept);
+    uint32_t mask = __ballot_sync(FULL, kept);
     if (biased || sums) {  // weakest kept group against strongest dropped one
       const uint32_t k = lane < G && score > -INFINITY ? ord_key(score) : 0u;
       const float lo = ord_value(redux_min(kept ? k : 0xFFFFFFFFu)), hi = ord_value(redux_max(kept ? 0u : k));
       const float tol = 4.f * err + SUM_ERR * (fabsf(lo) + fabsf(hi));
-      sure = hi == -INFINITY || lo - hi > tol;
+      if (!(hi == -INFINITY || lo - hi > tol)) {
+        float xc[EPL];  // copies: what a call takes by address does not stay in registers
+        uint32_t val[EPL];
+#pragma unroll
+        for (int i = 0; i < EPL; ++i) {
+          xc[i] = x[i];
+          val[i] = value(i);
+        }
+        uint32_t better;
+        if (p.softmax || !refine_groups<EPL>(p, xc, val, lane, better)) return false;
+        mask = better;
+      }
     }
 #pragma unroll
     for (int i = 0; i < EPL; ++i) {
-      const int g = (lane + 32 * i) / size;
-      if (g >= G || !((mask >> (g & 31)) & 1u)) key[i] = 0u;
+      const uint32_t g = ((uint32_t)(lane + 32 * i) * p.recip) >> 20;
+      if (!((mask >> (g & 31u)) & 1u)) key[i] = 0u;  // beyond the last expert the key is 0 already
     }
   }
 
@@ -352,12 +422,19 @@ __device__ __forceinline__ bool route_row_f32(const RouteParams& p, const float 
   rescan();
   my_e = -1;
   uint32_t my_key = 0u;
-  const int picks = biased ? p.top_k + 1 : p.top_k;  // one more, to see how close it comes
-  for (int k = 0; k < picks; ++k) {
+  // With a bias the picks go on as long as they could belong before the last
+  // one that counts: candidates beyond it are not in reach of fp32's error.
+  int n = 0;
+  float last = 0.f;
+  for (; n < 32; ++n) {
+    if (n >= p.top_k && !biased) break;
     const uint32_t m = redux_max(best);
     if (m == 0u) break;
+    const float v = ord_value(m);
+    if (n == p.top_k - 1) last = v;
+    if (n >= p.top_k && last - v > 2.f * err + SUM_ERR * (fabsf(v) + fabsf(last))) break;
     const int e = (int)redux_min(best == m ? (uint32_t)(at * 32 + lane) : 0xFFFFFFFFu);
-    if (lane == k) {
+    if (lane == n) {
       my_e = e;
       my_key = m;
     }
@@ -380,13 +457,27 @@ __device__ __forceinline__ bool route_row_f32(const RouteParams& p, const float 
       if ((my_e >> 5) == i) mx = o;
     }
     const float nx = __shfl_down_sync(FULL, mx, 1);
-    const int ne = __shfl_down_sync(FULL, my_e, 1);
-    const bool pair = lane < p.top_k && my_e >= 0 && ne >= 0;
     const bool apart = v - nv > 2.f * err + SUM_ERR * (fabsf(v) + fabsf(nv)) || (mx == nx && bias == nb);
-    sure = sure && __all_sync(FULL, !pair || apart);
+    if (!__all_sync(FULL, lane + 1 >= n || apart)) {
+      if (p.softmax || n == 32) return false;  // needs the row's sum, or more candidates
+      // the candidates, one a lane, in fp64, and their order
+      double k = -INFINITY;
+      if (lane < n) k = 1.0 / (1.0 + exp(-(double)mx)) + (double)bias;
+      int rank = 0, first = -1;
+      for (int j = 0; j < n; ++j) {
+        const double o = __shfl_sync(FULL, k, j);
+        const int oe = __shfl_sync(FULL, my_e, j);
+        if (o > k || (o == k && oe < my_e)) ++rank;
+      }
+      for (int j = 0; j < n; ++j) {
+        const int r = __shfl_sync(FULL, rank, j), oe = __shfl_sync(FULL, my_e, j);
+        if (r == lane) first = oe;
+      }
+      my_e = lane < n ? first : -1;
+    }
     if (lane >= p.top_k) my_e = -1;
   }
-  return sure;
+  return true;
 }
 
 template <int EPL, bool BF16>
@@ -408,7 +499,14 @@ __global__ void __launch_bounds__(128) route_kernel(const RouteParams p) {
     }
   }
   int my_e;
-  if (!route_row_f32<EPL>(p, x, lane, my_e)) route_row_f64<EPL>(p, x, lane, my_e);
+  if (!route_row_f32<EPL>(p, x, lane, my_e)) {
+    float xc[EPL];
+#pragma unroll
+    for (int i = 0; i < EPL; ++i) xc[i] = x[i];
+    int e;
+    route_row_f64<EPL>(p, xc, lane, e);
+    my_e = e;
+  }
 
   // Weights from the selected logits.  u is the score times a factor common to
   // the row that keeps the largest near 1, so that renormalising never divides
@@ -610,6 +708,7 @@ cudaError_t launch_route(const RouteSpec& r, const void* logits, bool bf16, long
   p.top2 = r.top2;
   p.renorm = r.renorm;
   p.scale = r.scale;
+  p.recip = (uint32_t)(((1 << 20) + r.E / r.n_groups - 1) / (r.E / r.n_groups));
   if (r.E <= 64) return launch_route_epl<2>(p, bf16, st);
   if (r.E <= 128) return launch_route_epl<4>(p, bf16, st);
   if (r.E <= 256) return launch_route_epl<8>(p, bf16, st);

@@ -44,7 +44,7 @@ struct QuantParams {
   int rows, K;
   const int32_t* pos;
   int top_k;
-  long long places;  // rows of q and of a scale line
+  int places;  // rows of q and of a scale line
   uint8_t* q;
   float* scales;
 };
@@ -55,56 +55,70 @@ __device__ __forceinline__ float rcp_approx(float v) {
   return r;
 }
 
-// 16 lanes per block of 128, 8 values each; a CTA has 16 neighbouring rows of
-// one block column, so that their scales are one 64-byte line.  The block's largest magnitude a
-// (NaN if the block holds one) gives scale = a / 448 and codes
-// e4m3(x * (448 / a)), one rounding to nearest even.
+// 8 lanes per block of 128, 16 values each; a CTA has 32 neighbouring rows of one
+// block column, so that their scales are one 128-byte line.  The block's
+// largest magnitude a (NaN if the block holds one) gives scale = a / 448 and
+// codes e4m3(x * (448 / a)), one rounding to nearest even.
 template <bool BF16, bool SILU>
 __global__ void __launch_bounds__(256) quantize_kernel(const QuantParams p) {
   pdl_wait();
   pdl_trigger();
-  const int lane = threadIdx.x & 15;
-  const int row = blockIdx.x * 16 + (threadIdx.x >> 4), b = blockIdx.y;
-  const int k = b * 128 + lane * 8;
+  const int lane = threadIdx.x & 7;
+  const int row = blockIdx.x * 32 + (threadIdx.x >> 3), b = blockIdx.y;
+  const int k = b * 128 + lane * 16;
   const bool in = row < p.rows && k < p.K;  // K is a multiple of 16
-  float v[8];
+  constexpr int AT_ONCE = 8;
+  int to[AT_ONCE];  // the first places, on their way while the row is
+  const int32_t* pos = p.pos + (size_t)row * p.top_k;
+  if (p.pos != nullptr) {
 #pragma unroll
-  for (int i = 0; i < 8; ++i) v[i] = 0.f;
+    for (int j = 0; j < AT_ONCE; ++j) to[j] = in && j < p.top_k ? __ldg(pos + j) : -1;
+  }
+  float v[16];
+#pragma unroll
+  for (int i = 0; i < 16; ++i) v[i] = 0.f;
   if (in) {
     const size_t at = (size_t)row * (size_t)p.stride + (size_t)k;
-    load8<BF16>(p.x, at, v);
+    float* lo = v;
+    load8<BF16>(p.x, at, *reinterpret_cast<float(*)[8]>(lo));
+    load8<BF16>(p.x, at + 8, *reinterpret_cast<float(*)[8]>(lo + 8));
     if (SILU) {
-      float u[8];
-      load8<BF16>(p.x, at + (size_t)p.K, u);
+      float u[16];
+      load8<BF16>(p.x, at + (size_t)p.K, *reinterpret_cast<float(*)[8]>(u));
+      load8<BF16>(p.x, at + (size_t)p.K + 8, *reinterpret_cast<float(*)[8]>(u + 8));
 #pragma unroll
-      for (int i = 0; i < 8; ++i) v[i] = v[i] * rcp_approx(1.f + __expf(-v[i])) * u[i];
+      for (int i = 0; i < 16; ++i) v[i] = v[i] * rcp_approx(1.f + __expf(-v[i])) * u[i];
     }
   }
   // Magnitudes compare as integers; NaN's is above every other.
   uint32_t m = 0u;
 #pragma unroll
-  for (int i = 0; i < 8; ++i) m = max(m, __float_as_uint(v[i]) & 0x7FFFFFFFu);
+  for (int i = 0; i < 16; ++i) m = max(m, __float_as_uint(v[i]) & 0x7FFFFFFFu);
 #pragma unroll
-  for (int off = 8; off > 0; off >>= 1) m = max(m, __shfl_xor_sync(0xffffffffu, m, off));
+  for (int off = 4; off > 0; off >>= 1) m = max(m, __shfl_xor_sync(0xffffffffu, m, off));
   float a = __uint_as_float(m);
   if (a < Q_FLOOR) a = Q_FLOOR;  // false for NaN
   const float scale = __fdiv_rn(a, E4M3_TOP), r = __fdiv_rn(E4M3_TOP, a);
   uint32_t c[4];
 #pragma unroll
-  for (int i = 0; i < 4; ++i) c[i] = e4m3x2(v[2 * i] * r, v[2 * i + 1] * r);
+  for (int i = 0; i < 4; ++i)
+    c[i] = e4m3x2(v[4 * i] * r, v[4 * i + 1] * r) | (e4m3x2(v[4 * i + 2] * r, v[4 * i + 3] * r) << 16);
   if (!in) return;
-  const uint2 code = make_uint2(c[0] | (c[1] << 16), c[2] | (c[3] << 16));
+  const uint4 code = make_uint4(c[0], c[1], c[2], c[3]);
+  uint8_t* q = p.q + k;
+  float* scales = p.scales + (size_t)b * p.places;
+  auto put = [&](int place) {
+    if (place < 0 || place >= p.places) return;
+    *reinterpret_cast<uint4*>(q + (size_t)place * p.K) = code;
+    if (lane == 0) scales[place] = scale;
+  };
   if (p.pos == nullptr) {
-    *reinterpret_cast<uint2*>(p.q + (size_t)row * p.K + k) = code;
-    if (lane == 0) p.scales[(size_t)b * p.places + row] = scale;
+    put(row);
     return;
   }
-  for (int j = 0; j < p.top_k; ++j) {
-    const int to = __ldg(p.pos + (size_t)row * p.top_k + j);
-    if (to < 0 || to >= p.places) continue;
-    *reinterpret_cast<uint2*>(p.q + (size_t)to * p.K + k) = code;
-    if (lane == 0) p.scales[(size_t)b * p.places + to] = scale;
-  }
+#pragma unroll
+  for (int j = 0; j < AT_ONCE; ++j) put(to[j]);
+  for (int j = AT_ONCE; j < p.top_k; ++j) put(__ldg(pos + j));
 }
 
 struct CombineParams {
@@ -185,10 +199,10 @@ cudaError_t launch_quantize_rows(const void* x, bool bf16, long long stride, int
   p.K = K;
   p.pos = pos;
   p.top_k = top_k;
-  p.places = places;
+  p.places = (int)places;
   p.q = static_cast<uint8_t*>(q);
   p.scales = scales;
-  const dim3 ctas((unsigned)((rows + 15) / 16), (unsigned)((K + 127) / 128));
+  const dim3 ctas((unsigned)((rows + 31) / 32), (unsigned)((K + 127) / 128));
   if (bf16) return silu ? launch_pdl(quantize_kernel<true, true>, p, ctas, 256, st)
                         : launch_pdl(quantize_kernel<true, false>, p, ctas, 256, st);
   return silu ? launch_pdl(quantize_kernel<false, true>, p, ctas, 256, st)
