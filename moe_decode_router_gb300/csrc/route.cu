@@ -408,16 +408,25 @@ __device__ __forceinline__ bool route_row_f32(const RouteParams& p, const float 
     }
   }
 
-  uint32_t best = 0u;
-  int at = 0;
+  // The lane's two best that are left.  A lane that wins twice looks for its
+  // next two among the rest; with the experts spread over the lanes that is rare.
+  uint32_t best = 0u, second = 0u, done = 0u;
+  int at = 0, at2 = 0;
   auto rescan = [&]() {
-    best = 0u;
+    best = second = 0u;
 #pragma unroll
-    for (int i = 0; i < EPL; ++i)
-      if (key[i] > best) {
-        best = key[i];
+    for (int i = 0; i < EPL; ++i) {
+      const uint32_t k = ((done >> i) & 1u) ? 0u : key[i];
+      if (k > best) {
+        second = best;
+        at2 = at;
+        best = k;
         at = i;
+      } else if (k > second) {
+        second = k;
+        at2 = i;
       }
+    }
   };
   rescan();
   my_e = -1;
@@ -438,12 +447,14 @@ __device__ __forceinline__ bool route_row_f32(const RouteParams& p, const float 
       my_e = e;
       my_key = m;
     }
-    if ((e & 31) == lane) {
-#pragma unroll
-      for (int i = 0; i < EPL; ++i)
-        if (i == at) key[i] = 0u;
-      rescan();
+    const bool won = (e & 31) == lane;
+    if (won) {
+      done |= 1u << at;
+      best = second;
+      at = at2;
+      second = 0u;
     }
+    if (EPL > 2 && __any_sync(FULL, won && best == 0u)) rescan();
   }
   if (biased) {
     // Neighbours in the order must be further apart than their errors, unless
@@ -568,6 +579,7 @@ __global__ void __launch_bounds__(128) route_kernel(const RouteParams p) {
 // of 256 experts; GP_NOTE
 constexpr int GP_WARPS = 32;
 constexpr int GP_CTAS = 8;
+constexpr int GP_HELD = 8;
 
 __global__ void __launch_bounds__(GP_WARPS * 32) group_kernel(const int32_t* __restrict__ ids, int P, int E,
                                                               int32_t* __restrict__ offsets,
@@ -587,10 +599,20 @@ __global__ void __launch_bounds__(GP_WARPS * 32) group_kernel(const int32_t* __r
   const int stretch = (int)((P + ctas * GP_WARPS * 32 - 1) / (ctas * GP_WARPS * 32)) * 32;  // pairs of a warp
   const long long lo = (long long)(rank * GP_WARPS + warp) * stretch;
   int* h = hist + warp * E;
-  for (int i = 0; i < stretch; i += 32) {
+  auto id_at = [&](int i) {  // of this lane's pair, -1: none or dropped
     const long long at = lo + i + lane;
     const int id = at < P ? __ldg(ids + at) : -1;
-    if (id >= 0 && id < E) atomicAdd(&h[id], 1);
+    return id >= 0 && id < E ? id : -1;
+  };
+  int held[GP_HELD];  // the first ids stay in registers for the second pass
+#pragma unroll
+  for (int i = 0; i < GP_HELD; ++i) held[i] = 32 * i < stretch ? id_at(32 * i) : -1;
+#pragma unroll
+  for (int i = 0; i < GP_HELD; ++i)
+    if (held[i] >= 0) atomicAdd(&h[held[i]], 1);
+  for (int i = 32 * GP_HELD; i < stretch; i += 32) {
+    const int id = id_at(i);
+    if (id >= 0) atomicAdd(&h[id], 1);
   }
   __syncthreads();
   if (tid < E) {  // exclusive sums over the warps; E <= 1024 threads
@@ -609,19 +631,25 @@ __global__ void __launch_bounds__(GP_WARPS * 32) group_kernel(const int32_t* __r
   // per expert: all pairs, and those of the CTAs before this one
   int all = 0, before = 0;
   if (tid < E) {
-    for (uint32_t r = 0; r < ctas; ++r) {
-      int v;
-      if (ctas > 1) {
+    int v[GP_CTAS] = {};
+    if (ctas > 1) {
+#pragma unroll
+      for (uint32_t r = 0; r < GP_CTAS; ++r) {
         uint32_t a;
         asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(smem_u32(total + tid)), "r"(r));
-        asm volatile("ld.shared::cluster.s32 %0, [%1];" : "=r"(v) : "r"(a) : "memory");
-      } else {
-        v = total[tid];
+        asm volatile("ld.shared::cluster.s32 %0, [%1];" : "=r"(v[r]) : "r"(a) : "memory");
       }
-      all += v;
-      if (r < rank) before += v;
+    } else {
+      v[0] = total[tid];
+    }
+#pragma unroll
+    for (uint32_t r = 0; r < GP_CTAS; ++r) {
+      all += v[r];
+      if (r < rank) before += v[r];
     }
   }
+  // this thread has read the other CTAs' totals; they may leave once all have
+  if (ctas > 1) asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
   int incl = all;  // inclusive sums over the experts
 #pragma unroll
   for (int off = 1; off < 32; off <<= 1) {
@@ -648,23 +676,31 @@ __global__ void __launch_bounds__(GP_WARPS * 32) group_kernel(const int32_t* __r
   const int kept = scan[GP_WARPS - 1];
   if (tid == 0 && rank == 0) offsets[E] = kept;
   __syncthreads();
-  for (int i = 0; i < stretch; i += 32) {
+  auto hand_out = [&](int i, int id) {
     const long long at = lo + i + lane;
-    const bool in = at < P;
-    int id = in ? __ldg(ids + at) : -1;
-    if (id < 0 || id >= E) id = -1;
-    const uint32_t peers = __match_any_sync(FULL, id);
+    // lanes with the same id, a ballot for each bit (match.any takes some 65
+    // cycles of the SM); a dropped pair's -1 meets nobody that looks
+    uint32_t peers = FULL;
+    for (int bit = 0; (1 << bit) < E; ++bit) {
+      const uint32_t on = __ballot_sync(FULL, (id >> bit) & 1);
+      peers &= ((id >> bit) & 1) ? on : ~on;
+    }
+    peers &= __ballot_sync(FULL, id >= 0);
     int place = -1;
     if (id >= 0) place = first[id] + h[id] + __popc(peers & ((1u << lane) - 1u));
     __syncwarp();
     if (id >= 0 && lane == __ffs(peers) - 1) h[id] += __popc(peers);
     __syncwarp();
-    if (in) pos[at] = place;
+    if (at < P) pos[at] = place;
     if (place >= 0) order[place] = (int)at;
-  }
+  };
+#pragma unroll
+  for (int i = 0; i < GP_HELD; ++i)
+    if (32 * i < stretch) hand_out(32 * i, held[i]);
+  for (int i = 32 * GP_HELD; i < stretch; i += 32) hand_out(i, id_at(i));
   for (long long i = kept + (long long)rank * GP_WARPS * 32 + tid; i < P; i += (long long)ctas * GP_WARPS * 32) order[i] = -1;
-  // no CTA leaves while another still reads its totals
-  if (ctas > 1) asm volatile("barrier.cluster.arrive.release.aligned;\n barrier.cluster.wait.acquire.aligned;" ::: "memory");
+  __syncwarp();
+  if (ctas > 1) asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
 
 template <int EPL>

@@ -380,20 +380,17 @@ def dense_gemv(w: DenseNVFP4, x, y, stream=None):
     _check(rc, "flint_moe_dense_gemv")
 
 
-# The calls below are short beside their own marshalling, so each tensor is first
-# looked over with the few queries that decide it; the checks that name what is
-# wrong run only when that look fails.
+# The calls below are short beside their own marshalling, so their tensors are
+# first looked over with the few queries that decide it, in line; the checks that
+# name what is wrong run only when that look fails, and always raise.
 
 _ACT_TYPES = {torch.bfloat16: T_BF16, torch.float32: T_F32}
+_I32, _F32, _BF16, _E4M3 = torch.int32, torch.float32, torch.bfloat16, torch.float8_e4m3fn
+_AMISS = (AttributeError, IndexError, KeyError, TypeError, ValueError)  # of the look at something else than a tensor
 
 
-def _fits(t, dtype, shape, device):
-    return t.dtype is dtype and t.shape == shape and t.get_device() == device and t.is_contiguous()
-
-
-def _on(device):
-    """Whether tensors on `device` (an index, -1: none) are on the current CUDA device."""
-    return device >= 0 and device == torch._C._cuda_getDevice()
+def _current_device():
+    return torch._C._cuda_getDevice()
 
 
 def _raw_stream(stream, device):
@@ -423,40 +420,47 @@ def _matrix(t, name):
     return t.shape
 
 
-def _row_stride(t, rows, width):
-    """Elements between the rows of a matrix whose rows are contiguous, -1 otherwise."""
-    step, unit = t.stride()
-    if unit != 1 and width != 1:
-        return -1
-    return step if rows > 1 else width
+def _refuse(where, *tensors):
+    """Raises for the first of (tensor, name, dtype, shape) that is not as expected; None is
+    an argument left out."""
+    for t, name, dtype, shape in tensors:
+        if t is not None:
+            _expect(t, name, dtype, shape)
+    raise ValueError(f"{where}: arguments do not fit together")
 
 
 @functools.lru_cache(maxsize=64)
 def _routing(E, k, score, n_groups, top_groups, group_score, renormalise, scale):
-    r = Routing(E, k, score, n_groups, top_groups, group_score, renormalise, scale)
-    return ctypes.byref(r)
+    return ctypes.byref(Routing(E, k, score, n_groups, top_groups, group_score, renormalise, scale))
 
 
 def route(logits, ids, w, bias=None, score=SCORE_SIGMOID, n_groups=1, top_groups=1, group_score=GROUP_MAX,
           renormalise=True, scale=1.0, stream=None):
     """Chooses ids.shape[1] experts for every row of logits [T][E] (bf16 or fp32, rows may lie
     apart): ids int32 [T][k], w fp32 [T][k].  bias fp32 [E] is added for the choice only."""
-    T, E = _matrix(logits, "logits")
-    k = _matrix(ids, "ids")[1]
-    dev = logits.get_device()
-    kind = _ACT_TYPES.get(logits.dtype)
-    stride = _row_stride(logits, T, E)
-    if not (kind is not None and stride >= 0 and _on(dev) and _fits(ids, torch.int32, (T, k), dev)
-            and isinstance(w, torch.Tensor) and _fits(w, torch.float32, (T, k), dev)
-            and (bias is None or (isinstance(bias, torch.Tensor) and _fits(bias, torch.float32, (E,), dev)))):
+    try:
+        T, E = logits.shape
+        step, unit = logits.stride()
+        sel = ids.shape
+        k = sel[1]
+        dev = logits.get_device()
+        kind = _ACT_TYPES[logits.dtype]
+        fits = (dev >= 0 and dev == _current_device() and (unit == 1 or E == 1) and len(sel) == 2 and sel[0] == T
+                and ids.dtype is _I32 and ids.get_device() == dev and ids.is_contiguous()
+                and w.shape == sel and w.dtype is _F32 and w.get_device() == dev and w.is_contiguous()
+                and (bias is None or (bias.shape == (E,) and bias.dtype is _F32 and bias.get_device() == dev
+                                      and bias.is_contiguous())))
+    except _AMISS:
+        fits = False
+    if not fits:
         _expect_rows(logits, "logits", _ACT_TYPES, None)
-        _expect(ids, "ids", torch.int32, (T, k))
-        _expect(w, "w", torch.float32, (T, k))
-        if bias is not None:
-            _expect(bias, "bias", torch.float32, (E,))
+        want = (logits.shape[0], _matrix(ids, "ids")[1])
+        _expect(w, "w", _F32, want)
+        _refuse("route", (ids, "ids", _I32, want), (bias, "bias", _F32, (logits.shape[1],)))
     rc = _lib().flint_moe_route(_routing(E, k, score, n_groups, top_groups, group_score, 1 if renormalise else 0, scale),
-                                logits.data_ptr(), kind, stride, T, None if bias is None else bias.data_ptr(),
-                                ids.data_ptr(), w.data_ptr(), _raw_stream(stream, dev))
+                                logits.data_ptr(), kind, step if T > 1 else E, T,
+                                None if bias is None else bias.data_ptr(), ids.data_ptr(), w.data_ptr(),
+                                _raw_stream(stream, dev))
     if rc:
         _check(rc, "flint_moe_route")
 
@@ -464,16 +468,22 @@ def route(logits, ids, w, bias=None, score=SCORE_SIGMOID, n_groups=1, top_groups
 def group_pairs(ids, offsets, order, pos, stream=None):
     """Sorts the pairs of ids (int32, any shape) by expert: offsets int32 [E + 1], order int32
     [pairs], pos int32 of the shape of ids."""
-    if not isinstance(ids, torch.Tensor) or not isinstance(offsets, torch.Tensor):
-        raise TypeError("ids, offsets: expected a torch.Tensor")
-    n, E, shape, dev = ids.numel(), offsets.numel() - 1, ids.shape, ids.get_device()
-    if not (_on(dev) and _fits(ids, torch.int32, shape, dev) and _fits(offsets, torch.int32, (E + 1,), dev)
-            and isinstance(order, torch.Tensor) and _fits(order, torch.int32, (n,), dev)
-            and isinstance(pos, torch.Tensor) and _fits(pos, torch.int32, shape, dev)):
-        _expect(ids, "ids", torch.int32, shape)
-        _expect(offsets, "offsets", torch.int32, (E + 1,))
-        _expect(order, "order", torch.int32, (n,))
-        _expect(pos, "pos", torch.int32, shape)
+    try:
+        n, E, dev = ids.numel(), offsets.numel() - 1, ids.get_device()
+        fits = (dev >= 0 and dev == _current_device() and ids.dtype is _I32 and ids.is_contiguous()
+                and offsets.dtype is _I32 and offsets.dim() == 1 and offsets.get_device() == dev
+                and offsets.is_contiguous()
+                and order.shape == (n,) and order.dtype is _I32 and order.get_device() == dev and order.is_contiguous()
+                and pos.shape == ids.shape and pos.dtype is _I32 and pos.get_device() == dev and pos.is_contiguous())
+    except _AMISS:
+        fits = False
+    if not fits:
+        if not isinstance(ids, torch.Tensor) or not isinstance(offsets, torch.Tensor):
+            raise TypeError("ids, offsets: expected a torch.Tensor")
+        _expect(ids, "ids", _I32, ids.shape)
+        _expect(order, "order", _I32, (ids.numel(),))
+        _expect(pos, "pos", _I32, ids.shape)
+        _refuse("group_pairs", (offsets, "offsets", _I32, (offsets.numel(),)))
     rc = _lib().flint_moe_group_pairs(ids.data_ptr(), n, E, offsets.data_ptr(), order.data_ptr(), pos.data_ptr(),
                                       _raw_stream(stream, dev))
     if rc:
@@ -484,23 +494,28 @@ def quantize_rows(x, q, scales, pos=None, silu_mul=False, stream=None):
     """Quantises x [rows][K] (bf16 or fp32; silu_mul: [rows][2K], silu(first half) * second
     half) to q float8_e4m3fn [places][K] and scales fp32 [ceil(K / 128)][places]; pos int32
     [rows][k] gives the places of each row, None: row i goes to place i."""
-    places, K = _matrix(q, "q")
-    rows, width = _matrix(x, "x")
-    k = 0 if pos is None else _matrix(pos, "pos")[1]
-    dev = x.get_device()
-    kind = _ACT_TYPES.get(x.dtype)
-    stride = _row_stride(x, rows, width)
-    lines = -(-K // SCALE_BLOCK)
-    if not (kind is not None and stride >= 0 and width == (2 * K if silu_mul else K) and _on(dev)
-            and _fits(q, torch.float8_e4m3fn, (places, K), dev) and isinstance(scales, torch.Tensor)
-            and _fits(scales, torch.float32, (lines, places), dev)
-            and (pos is None or _fits(pos, torch.int32, (rows, k), dev))):
+    try:
+        places, K = q.shape
+        rows, width = x.shape
+        step, unit = x.stride()
+        k = 0 if pos is None else pos.shape[1]
+        dev = x.get_device()
+        kind = _ACT_TYPES[x.dtype]
+        fits = (dev >= 0 and dev == _current_device() and unit == 1 and width == (2 * K if silu_mul else K)
+                and q.dtype is _E4M3 and q.get_device() == dev and q.is_contiguous()
+                and scales.shape == (-(-K // SCALE_BLOCK), places) and scales.dtype is _F32
+                and scales.get_device() == dev and scales.is_contiguous()
+                and (pos is None or (pos.shape == (rows, k) and pos.dtype is _I32 and pos.get_device() == dev
+                                     and pos.is_contiguous())))
+    except _AMISS:
+        fits = False
+    if not fits:
+        places, K = _matrix(q, "q")
         _expect_rows(x, "x", _ACT_TYPES, 2 * K if silu_mul else K)
-        _expect(q, "q", torch.float8_e4m3fn, (places, K))
-        _expect(scales, "scales", torch.float32, (lines, places))
-        if pos is not None:
-            _expect(pos, "pos", torch.int32, (rows, k))
-    rc = _lib().flint_moe_quantize_rows(x.data_ptr(), kind, stride, rows, K, 1 if silu_mul else 0,
+        _expect(scales, "scales", _F32, (-(-K // SCALE_BLOCK), places))
+        _refuse("quantize_rows", (q, "q", _E4M3, (places, K)),
+                (pos, "pos", _I32, (x.shape[0], 0 if pos is None else _matrix(pos, "pos")[1])))
+    rc = _lib().flint_moe_quantize_rows(x.data_ptr(), kind, step if rows > 1 else width, rows, K, 1 if silu_mul else 0,
                                         None if pos is None else pos.data_ptr(), k, places, q.data_ptr(),
                                         scales.data_ptr(), _raw_stream(stream, dev))
     if rc:
@@ -512,29 +527,36 @@ def block_gemm(a, a_scales, b, b_scales, y, offsets=None, stream=None):
     [M][K], a_scales fp32 [ceil(K / 128)][M], b [experts][N][K], b_scales
     [experts][ceil(N / 128)][ceil(K / 128)].  offsets int32 [experts + 1] gives every expert
     its rows of a; None: dense (b of one expert)."""
-    if not isinstance(b, torch.Tensor):
-        raise TypeError(f"b: expected a torch.Tensor, got {type(b).__name__}")
-    if b.dim() != 3:
-        raise ValueError(f"b: expected [experts][N][K], got shape {tuple(b.shape)}")
-    E, N, K = b.shape
-    M = _matrix(y, "y")[0]
-    dev = y.get_device()
-    kind = _ACT_TYPES.get(y.dtype)
-    kb, nb = -(-K // SCALE_BLOCK), -(-N // SCALE_BLOCK)
-    if not (kind is not None and _on(dev) and _fits(y, y.dtype, (M, N), dev) and isinstance(a, torch.Tensor)
-            and _fits(a, torch.float8_e4m3fn, (M, K), dev) and isinstance(a_scales, torch.Tensor)
-            and _fits(a_scales, torch.float32, (kb, M), dev) and _fits(b, torch.float8_e4m3fn, (E, N, K), dev)
-            and isinstance(b_scales, torch.Tensor) and _fits(b_scales, torch.float32, (E, nb, kb), dev)
-            and (offsets is None or (isinstance(offsets, torch.Tensor)
-                                     and _fits(offsets, torch.int32, (E + 1,), dev)))):
+    try:
+        E, N, K = b.shape
+        M = y.shape[0]
+        kb = -(-K // SCALE_BLOCK)
+        dev = y.get_device()
+        kind = _ACT_TYPES[y.dtype]
+        fits = (dev >= 0 and dev == _current_device() and y.shape == (M, N) and y.is_contiguous()
+                and a.shape == (M, K) and a.dtype is _E4M3 and a.get_device() == dev and a.is_contiguous()
+                and a_scales.shape == (kb, M) and a_scales.dtype is _F32 and a_scales.get_device() == dev
+                and a_scales.is_contiguous()
+                and b.dtype is _E4M3 and b.get_device() == dev and b.is_contiguous()
+                and b_scales.shape == (E, -(-N // SCALE_BLOCK), kb) and b_scales.dtype is _F32
+                and b_scales.get_device() == dev and b_scales.is_contiguous()
+                and (offsets is None or (offsets.shape == (E + 1,) and offsets.dtype is _I32
+                                         and offsets.get_device() == dev and offsets.is_contiguous())))
+    except _AMISS:
+        fits = False
+    if not fits:
+        if not isinstance(b, torch.Tensor):
+            raise TypeError(f"b: expected a torch.Tensor, got {type(b).__name__}")
+        if b.dim() != 3:
+            raise ValueError(f"b: expected [experts][N][K], got shape {tuple(b.shape)}")
+        E, N, K = b.shape
         _expect_rows(y, "y", _ACT_TYPES, N)
+        M, kb = y.shape[0], -(-K // SCALE_BLOCK)
         _expect(y, "y", y.dtype, (M, N))
-        _expect(a, "a", torch.float8_e4m3fn, (M, K))
-        _expect(a_scales, "a_scales", torch.float32, (kb, M))
-        _expect(b, "b", torch.float8_e4m3fn, (E, N, K))
-        _expect(b_scales, "b_scales", torch.float32, (E, nb, kb))
-        if offsets is not None:
-            _expect(offsets, "offsets", torch.int32, (E + 1,))
+        _expect(a, "a", _E4M3, (M, K))
+        _expect(a_scales, "a_scales", _F32, (kb, M))
+        _expect(b_scales, "b_scales", _F32, (E, -(-N // SCALE_BLOCK), kb))
+        _refuse("block_gemm", (b, "b", _E4M3, (E, N, K)), (offsets, "offsets", _I32, (E + 1,)))
     rc = _lib().flint_moe_block_gemm(a.data_ptr(), a_scales.data_ptr(), M, b.data_ptr(), b_scales.data_ptr(), E,
                                      None if offsets is None else offsets.data_ptr(), N, K, y.data_ptr(), kind,
                                      _raw_stream(stream, dev))
@@ -545,22 +567,30 @@ def block_gemm(a, a_scales, b, b_scales, y, offsets=None, stream=None):
 def combine(rows, pos, w, y, shared=None, stream=None):
     """y [T][N] (bf16) = sum over j of w[t][j] * rows[pos[t][j]] (+ shared [T][N] bf16); rows
     bf16 or fp32 [any][N], pos int32 and w fp32 [T][k]; pos outside the rows adds nothing."""
-    T, N = _matrix(y, "y")
-    n_rows = _matrix(rows, "rows")[0]
-    k = _matrix(pos, "pos")[1]
-    dev = y.get_device()
-    kind = _ACT_TYPES.get(rows.dtype)
-    if not (kind is not None and _on(dev) and _fits(rows, rows.dtype, (n_rows, N), dev)
-            and _fits(y, torch.bfloat16, (T, N), dev) and _fits(pos, torch.int32, (T, k), dev)
-            and isinstance(w, torch.Tensor) and _fits(w, torch.float32, (T, k), dev)
-            and (shared is None or (isinstance(shared, torch.Tensor) and _fits(shared, torch.bfloat16, (T, N), dev)))):
+    try:
+        T, N = y.shape
+        n_rows = rows.shape[0]
+        sel = pos.shape
+        k = sel[1]
+        dev = y.get_device()
+        kind = _ACT_TYPES[rows.dtype]
+        fits = (dev >= 0 and dev == _current_device() and y.dtype is _BF16 and y.is_contiguous()
+                and rows.shape == (n_rows, N) and rows.get_device() == dev and rows.is_contiguous()
+                and len(sel) == 2 and sel[0] == T and pos.dtype is _I32 and pos.get_device() == dev
+                and pos.is_contiguous()
+                and w.shape == sel and w.dtype is _F32 and w.get_device() == dev and w.is_contiguous()
+                and (shared is None or (shared.shape == (T, N) and shared.dtype is _BF16
+                                        and shared.get_device() == dev and shared.is_contiguous())))
+    except _AMISS:
+        fits = False
+    if not fits:
+        T, N = _matrix(y, "y")
         _expect_rows(rows, "rows", _ACT_TYPES, N)
-        _expect(rows, "rows", rows.dtype, (n_rows, N))
-        _expect(y, "y", torch.bfloat16, (T, N))
-        _expect(pos, "pos", torch.int32, (T, k))
-        _expect(w, "w", torch.float32, (T, k))
-        if shared is not None:
-            _expect(shared, "shared", torch.bfloat16, (T, N))
+        _expect(rows, "rows", rows.dtype, (rows.shape[0], N))
+        want = (T, _matrix(pos, "pos")[1])
+        _expect(pos, "pos", _I32, want)
+        _expect(w, "w", _F32, want)
+        _refuse("combine", (y, "y", _BF16, (T, N)), (shared, "shared", _BF16, (T, N)))
     rc = _lib().flint_moe_combine(rows.data_ptr(), kind, n_rows, pos.data_ptr(), w.data_ptr(), T, k, N,
                                   None if shared is None else shared.data_ptr(), y.data_ptr(),
                                   _raw_stream(stream, dev))
