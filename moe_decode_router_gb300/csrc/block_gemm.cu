@@ -190,6 +190,8 @@ cudaError_t launch_skinny(const GemmArgs& p, cudaStream_t st) {
 // (32x32b; the 16-lane forms read at half that rate) and 256 of packed fma,
 // which overlap.  Two CTAs with the same weight tile form a cluster: each
 // loads half of it for both (TMA multicast), 32 KB a K block from L2 per SM.
+// Where a group's last tile has at most 128 rows, both CTAs take those rows, with
+// a weight tile each: half the time that a tile with one idle CTA would take.
 //
 // WIDE (short groups).  128 weight rows are the M side, always full, and up to
 // 64 rows of a the N side in steps of 16, so that a group of few rows costs
@@ -243,7 +245,9 @@ struct TcArgs {
 };
 
 struct TcUnit {
-  int e, wt, row0, cnt, n;  // n: columns of the MMAs
+  int e, wt, row0, cnt, n;  // n: columns of the MMAs, <= 0: none for this CTA
+  int first;                // TALL: this CTA's first row in the tile
+  bool shared;              // TALL: both CTAs have the same rows
 };
 
 __device__ __forceinline__ void tma_2d(uint32_t dst, const CUtensorMap* map, int x, int y, uint64_t* bar) {
@@ -303,8 +307,8 @@ __global__ void __launch_bounds__(TC_THREADS, 1)
   uint32_t* tslot = reinterpret_cast<uint32_t*>(sempty + C::SLOTS);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tslot + 1);
   static_assert((2 * C::STAGES + 2 * C::NBUF + 2 * C::SLOTS) * 8 + 8 <= 512, "barriers");
-  int* g_tiles = reinterpret_cast<int*>(sm + C::OFF_GROUPS);  // [E + 1] row tiles before each group
-  int* g_lo = g_tiles + p.E + 1;                              // [E] first row
+  int* g_units = reinterpret_cast<int*>(sm + C::OFF_GROUPS);  // [E + 1] units before each group
+  int* g_lo = g_units + p.E + 1;                              // [E] first row
   int* g_cnt = g_lo + p.E;                                    // [E] rows
 
   if (warp == 8) {
@@ -329,7 +333,7 @@ __global__ void __launch_bounds__(TC_THREADS, 1)
   }
   pdl_wait();
   pdl_trigger();
-  if (warp == 8) {  // groups: rows, and row tiles before each
+  if (warp == 8) {  // groups: rows, and units before each
     int base = 0;
     for (int e0 = 0; e0 < p.E; e0 += 32) {
       const int e = e0 + lane;
@@ -340,40 +344,53 @@ __global__ void __launch_bounds__(TC_THREADS, 1)
         g_lo[e] = lo;
         g_cnt[e] = cnt;
       }
-      const int t = (cnt + C::ROWS - 1) / C::ROWS;
+      const int rest = cnt % C::ROWS, tiles = cnt / C::ROWS + (TALL ? rest > 128 : rest > 0);
+      int t = tiles * p.n_tiles + (TALL && rest > 0 && rest <= 128 ? (p.n_tiles + 1) / 2 : 0);
+      if (base > 1 << 29) t = 0;  // offsets that descend could count rows over and over: stay inside int
       int incl = t;
 #pragma unroll
       for (int off = 1; off < 32; off <<= 1) {
         const int v = __shfl_up_sync(0xffffffffu, incl, off);
         if (lane >= off) incl += v;
       }
-      if (e < p.E) g_tiles[e] = base + incl - t;
+      if (e < p.E) g_units[e] = base + incl - t;
       base += __shfl_sync(0xffffffffu, incl, 31);
     }
-    if (lane == 0) g_tiles[p.E] = base;
+    if (lane == 0) g_units[p.E] = base;
   }
   tc05::fence_before_sync();
   __syncthreads();
   if (TALL) tc05::cluster_sync();  // the peer's barriers are ready too
   tc05::fence_after_sync();
   const uint32_t tmem = *tslot;
-  const int n_units = g_tiles[p.E] * p.n_tiles;
+  const int n_units = g_units[p.E];
   const int u0 = blockIdx.x / C::CTAS, ustep = gridDim.x / C::CTAS;
 
   auto unit_of = [&](int u) -> TcUnit {
     TcUnit t;
-    const int tile = u / p.n_tiles;
-    t.wt = u - tile * p.n_tiles;
-    int lo = 0, hi = p.E;  // largest e with g_tiles[e] <= tile: the group that holds the tile
+    int lo = 0, hi = p.E;  // largest e with g_units[e] <= u: the group that holds the unit
     while (hi - lo > 1) {
       const int mid = (lo + hi) >> 1;
-      if (g_tiles[mid] <= tile) lo = mid;
+      if (g_units[mid] <= u) lo = mid;
       else hi = mid;
     }
     t.e = lo;
-    const int at = (tile - g_tiles[lo]) * C::ROWS;
-    t.row0 = g_lo[lo] + at;
-    t.cnt = min(C::ROWS, g_cnt[lo] - at);
+    const int cnt = g_cnt[lo], v = u - g_units[lo];
+    int tile = v / p.n_tiles;
+    t.wt = v - tile * p.n_tiles;
+    t.first = rank * 128;
+    t.shared = false;
+    if (TALL) {
+      const int whole = cnt / 256 + (cnt % 256 > 128 ? 1 : 0);
+      if (tile >= whole) {
+        t.wt = 2 * (v - whole * p.n_tiles) + rank;
+        tile = whole;
+        t.first = 0;
+        t.shared = true;
+      }
+    }
+    t.row0 = g_lo[lo] + tile * C::ROWS;
+    t.cnt = min(C::ROWS, cnt - tile * C::ROWS);
     t.n = TALL ? min(256, (p.N - t.wt * 256 + 15) & ~15) : (t.cnt + 15) & ~15;
     return t;
   };
@@ -407,8 +424,13 @@ __global__ void __launch_bounds__(TC_THREADS, 1)
             mbar_arrive_expect_tx(&full[s], bytes);
             const uint32_t w = smem_u32(sm) + s * C::STAGE, x = w + C::W_BYTES;
             if (TALL) {
-              tma_3d_both(w + rank * 16384, &map_w, kb * 128, t.wt * 256 + rank * 128, t.e, &full[s]);
-              tma_2d(x, &map_x, kb * 128, t.row0 + rank * 128, &full[s]);
+              if (t.shared) {
+                tma_3d(w, &map_w, kb * 128, t.wt * 256, t.e, &full[s]);
+                tma_3d(w + 16384, &map_w, kb * 128, t.wt * 256 + 128, t.e, &full[s]);
+              } else {
+                tma_3d_both(w + rank * 16384, &map_w, kb * 128, t.wt * 256 + rank * 128, t.e, &full[s]);
+              }
+              tma_2d(x, &map_x, kb * 128, t.row0 + t.first, &full[s]);
             } else {
               tma_3d(w, &map_w, kb * 128, t.wt * 128, t.e, &full[s]);
               for (int i = 0; i < boxes; ++i) tma_2d(x + i * 4096, &map_x, kb * 128, t.row0 + 32 * i, &full[s]);
@@ -515,7 +537,7 @@ __global__ void __launch_bounds__(TC_THREADS, 1)
                 const float* sa = p.sa + (size_t)(kb + j) * p.M + t.row0;
 #pragma unroll
                 for (int i = 0; i < 4; ++i)
-                  copy4(slot + j * 128 + i * 32 + lane, sa + min(rank * 128 + i * 32 + lane, last));
+                  copy4(slot + j * 128 + i * 32 + lane, sa + min(t.first + i * 32 + lane, last));
                 if (lane < 2) copy4(slot + 512 + j * 2 + lane, sb + kb + j);
               }
             }
@@ -567,7 +589,7 @@ __global__ void __launch_bounds__(TC_THREADS, 1)
     if constexpr (TALL) {
       for (int u = u0; u < n_units && ok; u += ustep) {
         const TcUnit t = unit_of(u);
-        const int row = rank * 128 + quad * 32;      // first of the warp's 32 rows in the tile
+        const int row = t.first + quad * 32;         // first of the warp's 32 rows in the tile
         const int live = t.n > 128 * half ? min(32, t.cnt - row) : 0;  // its rows of a, <= 0: none
         uint64_t acc[64];
 #pragma unroll
@@ -792,7 +814,8 @@ cudaError_t launch_tc(const GemmArgs& p, int sm_count, unsigned* err, cudaStream
   if (!row_map(&mw, p.b, 1, p.K, p.N, p.E, 128) || !row_map(&mx, p.a, 1, p.K, p.M, 0, C::X_BOX) ||
       !row_map(&my, p.y, size, p.N, p.M, 0, 32))
     return cudaErrorInvalidValue;
-  const long long most = ((long long)(p.M + C::ROWS - 1) / C::ROWS + p.E) * t.n_tiles;  // units, at most
+  const long long groups = p.M < p.E ? p.M : p.E;  // that can have rows
+  const long long most = ((long long)p.M / C::ROWS + groups) * t.n_tiles;  // units, at most
   const int clusters = sm_count / C::CTAS;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)(C::CTAS * (most < clusters ? most : clusters)));
