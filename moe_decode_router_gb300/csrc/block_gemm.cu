@@ -242,6 +242,7 @@ struct TcArgs {
   void* y;
   unsigned* err;
   int M, N, E, kb, nb, n_tiles;  // n_tiles: weight tiles
+  unsigned n_tiles_recip;        // ceil(2^32 / n_tiles)
 };
 
 struct TcUnit {
@@ -367,16 +368,21 @@ __global__ void __launch_bounds__(TC_THREADS, 1)
   const int u0 = blockIdx.x / C::CTAS, ustep = gridDim.x / C::CTAS;
 
   auto unit_of = [&](int u) -> TcUnit {
+    // The group is the last whose first unit is at or before u: the whole warp
+    // looks, at every 32nd group and then at 32 neighbours (a binary search of
+    // 256 groups takes 1,000 cycles).
     TcUnit t;
-    int lo = 0, hi = p.E;  // largest e with g_units[e] <= u: the group that holds the unit
-    while (hi - lo > 1) {
-      const int mid = (lo + hi) >> 1;
-      if (g_units[mid] <= u) lo = mid;
-      else hi = mid;
-    }
+    int from = 0;
+    if (p.E > 32) from = 32 * (__popc(__ballot_sync(0xffffffffu, 32 * lane < p.E && g_units[32 * lane] <= u)) - 1);
+    const int e = from + lane;
+    const int lo = from + __popc(__ballot_sync(0xffffffffu, e < p.E && g_units[e] <= u)) - 1;
     t.e = lo;
     const int cnt = g_cnt[lo], v = u - g_units[lo];
-    int tile = v / p.n_tiles;
+    int tile = v;  // v / n_tiles
+    if (p.n_tiles > 1) {
+      tile = (int)__umulhi((unsigned)v, p.n_tiles_recip);  // too large by one at most
+      if (tile * p.n_tiles > v) --tile;
+    }
     t.wt = v - tile * p.n_tiles;
     t.first = rank * 128;
     t.shared = false;
@@ -409,39 +415,40 @@ __global__ void __launch_bounds__(TC_THREADS, 1)
     if (TALL) tc05::regs_down<TC_REGS_LOW>();
     if (warp == 8) {
       // ---------------- producer
-      if (lane == 0) {
-        uint32_t s = 0, ph = 0, issued = 0;
-        bool ok = true;
-        for (int u = u0; u < n_units && ok; u += ustep) {
-          const TcUnit t = unit_of(u);
-          const int boxes = TALL ? 1 : (t.n + 31) >> 5;
-          const uint32_t bytes = C::W_BYTES + boxes * C::X_BOX * 128;
-          for (int kb = 0; kb < p.kb; ++kb) {
-            if (!wait(&empty[s], ph ^ 1)) {
-              ok = false;
-              break;
-            }
-            mbar_arrive_expect_tx(&full[s], bytes);
-            const uint32_t w = smem_u32(sm) + s * C::STAGE, x = w + C::W_BYTES;
-            if (TALL) {
-              if (t.shared) {
-                tma_3d(w, &map_w, kb * 128, t.wt * 256, t.e, &full[s]);
-                tma_3d(w + 16384, &map_w, kb * 128, t.wt * 256 + 128, t.e, &full[s]);
-              } else {
-                tma_3d_both(w + rank * 16384, &map_w, kb * 128, t.wt * 256 + rank * 128, t.e, &full[s]);
-              }
-              tma_2d(x, &map_x, kb * 128, t.row0 + t.first, &full[s]);
+      uint32_t s = 0, ph = 0, issued = 0;  // of lane 0, which copies
+      bool ok = true;
+      for (int u = u0; u < n_units && ok; u += ustep) {
+        const TcUnit t = unit_of(u);
+        const int boxes = TALL ? 1 : (t.n + 31) >> 5;
+        const uint32_t bytes = C::W_BYTES + boxes * C::X_BOX * 128;
+        for (int kb = 0; kb < p.kb && lane == 0; ++kb) {
+          if (!wait(&empty[s], ph ^ 1)) {
+            ok = false;
+            break;
+          }
+          mbar_arrive_expect_tx(&full[s], bytes);
+          const uint32_t w = smem_u32(sm) + s * C::STAGE, x = w + C::W_BYTES;
+          if (TALL) {
+            if (t.shared) {
+              tma_3d(w, &map_w, kb * 128, t.wt * 256, t.e, &full[s]);
+              tma_3d(w + 16384, &map_w, kb * 128, t.wt * 256 + 128, t.e, &full[s]);
             } else {
-              tma_3d(w, &map_w, kb * 128, t.wt * 128, t.e, &full[s]);
-              for (int i = 0; i < boxes; ++i) tma_2d(x + i * 4096, &map_x, kb * 128, t.row0 + 32 * i, &full[s]);
+              tma_3d_both(w + rank * 16384, &map_w, kb * 128, t.wt * 256 + rank * 128, t.e, &full[s]);
             }
-            ++issued;
-            if (++s == C::STAGES) {
-              s = 0;
-              ph ^= 1;
-            }
+            tma_2d(x, &map_x, kb * 128, t.row0 + t.first, &full[s]);
+          } else {
+            tma_3d(w, &map_w, kb * 128, t.wt * 128, t.e, &full[s]);
+            for (int i = 0; i < boxes; ++i) tma_2d(x + i * 4096, &map_x, kb * 128, t.row0 + 32 * i, &full[s]);
+          }
+          ++issued;
+          if (++s == C::STAGES) {
+            s = 0;
+            ph ^= 1;
           }
         }
+        ok = __all_sync(0xffffffffu, ok);
+      }
+      if (lane == 0) {
         // Every stage's last phase: normally its release by all MMAs, after
         // which nothing is under way to this CTA; after a wait that ran out,
         // the arrival of the copies (the peer's may come later: 1 ms covers any).
@@ -635,7 +642,7 @@ __global__ void __launch_bounds__(TC_THREADS, 1)
         if (!ok) break;
         // Output: 128-byte pieces of 32 rows in the 128-byte swizzle, copied out by
         // TMA while the next unit is multiplied.  Where a row behind the group's
-        // last belongs to another group, the rows are copied one by one.
+        // last belongs to another group, the warp stores its rows itself.
         constexpr int SIZE = F32 ? 4 : 2, COLS = 128 / SIZE;  // columns of a piece
         const int n0 = t.wt * 256 + half * 128, row0 = t.row0 + row;
         const bool box = live == 32 || t.row0 + t.cnt == p.M;  // TMA leaves out what lies outside y
@@ -655,9 +662,7 @@ __global__ void __launch_bounds__(TC_THREADS, 1)
               } else {
                 v = make_uint4(bf16_pair(src[0]), bf16_pair(src[1]), bf16_pair(src[2]), bf16_pair(src[3]));
               }
-              // box: piece c as [32 rows][128 B], swizzled; else [32 rows][256 B]
-              const int at = box ? c * 4096 + lane * 128 + ((j ^ (lane & 7)) << 4) : lane * 256 + c * 128 + j * 16;
-              *reinterpret_cast<uint4*>(out + at) = v;
+              *reinterpret_cast<uint4*>(out + c * 4096 + lane * 128 + ((j ^ (lane & 7)) << 4)) = v;
             }
           tc05::fence_proxy_async_smem();
           __syncwarp();
@@ -672,11 +677,15 @@ __global__ void __launch_bounds__(TC_THREADS, 1)
                                "r"(nr + c * COLS), "r"(row0), "r"(smem_u32(out + c * 4096))
                                : "memory");
             }
-          } else if (lane < live && nr < p.N) {
-            asm volatile("cp.async.bulk.global.shared::cta.bulk_group [%0], [%1], %2;" ::"l"(
-                             static_cast<uint8_t*>(p.y) + ((size_t)(row0 + lane) * p.N + nr) * SIZE),
-                         "r"(smem_u32(out + lane * 256)), "r"(min(2 * COLS, p.N - nr) * SIZE)
-                         : "memory");
+          } else {
+#pragma unroll 4
+            for (int i = 0; i < 16; ++i) {  // two rows at a time, 16 lanes each
+              const int rr = 2 * i + (lane >> 4), c = (lane >> 3) & 1, j = lane & 7;
+              const int n = nr + c * COLS + j * (16 / SIZE);
+              if (rr < live && n < p.N)
+                *reinterpret_cast<uint4*>(static_cast<uint8_t*>(p.y) + ((size_t)(row0 + rr) * p.N + n) * SIZE) =
+                    *reinterpret_cast<const uint4*>(out + c * 4096 + rr * 128 + ((j ^ (rr & 7)) << 4));
+            }
           }
           asm volatile("cp.async.bulk.commit_group;" ::: "memory");
         }
@@ -809,6 +818,7 @@ cudaError_t launch_tc(const GemmArgs& p, int sm_count, unsigned* err, cudaStream
   t.kb = p.kb;
   t.nb = p.nb;
   t.n_tiles = (p.N + C::WROWS - 1) / C::WROWS;
+  t.n_tiles_recip = 0xFFFFFFFFu / (unsigned)t.n_tiles + 1u;
   CUtensorMap mw, mx, my;
   const int size = F32 ? 4 : 2;
   if (!row_map(&mw, p.b, 1, p.K, p.N, p.E, 128) || !row_map(&mx, p.a, 1, p.K, p.M, 0, C::X_BOX) ||
