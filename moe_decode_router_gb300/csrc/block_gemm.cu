@@ -50,7 +50,6 @@ __device__ __forceinline__ void mma_e4m3(float (&d)[4], uint32_t a0, uint32_t a1
 // fragments: the product of a block does not depend on the order of k, so lane
 // t of a row's four takes bytes 16t..16t+15 of each half block for either
 // operand.  Two K blocks (4 KB of weights a warp) are under way at a time.
-constexpr int SK_FULL_WARPS = 1024;
 
 template <int SPLIT, int SK_WARPS, bool F32>
 __global__ void __launch_bounds__(SK_WARPS * 32, 24 / SK_WARPS) block_gemm_skinny_kernel(const GemmArgs p) {
@@ -62,15 +61,23 @@ __global__ void __launch_bounds__(SK_WARPS * 32, 24 / SK_WARPS) block_gemm_skinn
   const int r = blockIdx.x;
   int e = 0, r0 = 0, r1 = p.M;
   if (p.offsets != nullptr) {
-    // expert of row r: the number of groups that end at or before it
+    // expert of row r: the number of groups that end at or before it; its range:
+    // the offsets on either side of r
     if (warp == 0) {
-      int ended = 0;
-      for (int i = lane; i < p.E; i += 32) ended += __ldg(p.offsets + i + 1) <= r ? 1 : 0;
-      ended = (int)__reduce_add_sync(0xffffffffu, (unsigned)ended);
+      unsigned ended = 0, from = 0, to = (unsigned)p.M;
+      for (int i = lane; i <= p.E; i += 32) {
+        const int o = __ldg(p.offsets + i);
+        ended += i > 0 && o <= r ? 1 : 0;
+        if (o >= 0 && o <= r) from = max(from, (unsigned)o);
+        if (o > r) to = min(to, (unsigned)o);
+      }
+      ended = __reduce_add_sync(0xffffffffu, ended);
+      from = redux_max(from);
+      to = redux_min(to);
       if (lane == 0) {
-        range[0] = ended;
-        range[1] = ended < p.E ? __ldg(p.offsets + ended) : 0;
-        range[2] = ended < p.E ? min(__ldg(p.offsets + ended + 1), p.M) : 0;
+        range[0] = (int)ended;
+        range[1] = (int)from;
+        range[2] = (int)to;
       }
     }
     __syncthreads();
@@ -334,17 +341,22 @@ __global__ void __launch_bounds__(TC_THREADS, 1)
   }
   pdl_wait();
   pdl_trigger();
-  if (warp == 8) {  // groups: rows, and units before each
+  // groups: rows, and units before each
+  if (p.offsets != nullptr)
+    for (int e = tid; e <= p.E; e += TC_THREADS) g_units[e] = __ldg(p.offsets + e);  // all on their way at once
+  __syncthreads();
+  if (warp == 8) {
     int base = 0;
     for (int e0 = 0; e0 < p.E; e0 += 32) {
       const int e = e0 + lane;
       int lo = 0, cnt = 0;
       if (e < p.E) {
-        lo = p.offsets ? min(max(__ldg(p.offsets + e), 0), p.M) : 0;
-        cnt = p.offsets ? min(max(__ldg(p.offsets + e + 1), lo), p.M) - lo : p.M;
+        lo = p.offsets ? min(max(g_units[e], 0), p.M) : 0;
+        cnt = p.offsets ? min(max(g_units[e + 1], lo), p.M) - lo : p.M;
         g_lo[e] = lo;
         g_cnt[e] = cnt;
       }
+      __syncwarp();  // the offsets of these groups make room for their units; the next group's first is read below
       const int rest = cnt % C::ROWS, tiles = cnt / C::ROWS + (TALL ? rest > 128 : rest > 0);
       int t = tiles * p.n_tiles + (TALL && rest > 0 && rest <= 128 ? (p.n_tiles + 1) / 2 : 0);
       if (base > 1 << 29) t = 0;  // offsets that descend could count rows over and over: stay inside int
@@ -886,15 +898,21 @@ cudaError_t launch_block_gemm(const void* a, const float* sa, int M, const void*
   p.E = E;
   p.kb = (K + 127) / 128;
   p.nb = (N + 127) / 128;
-  if (M > (offsets != nullptr ? 64 : 8)) {
-    if ((long long)M > 64LL * E)
-      return f32 ? launch_tc<true, true>(p, sm_count, err, st) : launch_tc<true, false>(p, sm_count, err, st);
+  // Which kernel, measured (us) on 256 experts of 1024 x 2048, R rows in all, and
+  // on one matrix of 4096 x 2048:
+  //   up to 8 rows in all         few-row SPLIT 8  R 8: 8.5, WIDE 9.8
+  //   33 to 128 rows, at most one
+  //   an expert on average        few-row SPLIT 1  R 48: 20.0, WIDE 22.4; R 128: 35.2, 36.2; but R 32: 18.8, 16.6
+  //   one wave of WIDE's units,
+  //   or 36 rows an expert        WIDE             24 rows each: 89, TALL 93; 256 dense: 9.3, 11.9
+  //   else                        TALL             48 rows each: 98, WIDE 107; 512 dense: 12.2, 15.2
+  const long long groups = M < E ? M : E;  // that can have rows
+  const long long wide_units = (M / TcCfg<false>::ROWS + groups) * ((N + TcCfg<false>::WROWS - 1) / TcCfg<false>::WROWS);
+  if (M <= 8) return f32 ? launch_skinny<8, 8, true>(p, st) : launch_skinny<8, 8, false>(p, st);
+  if (M > 32 && M <= 128 && M <= E) return f32 ? launch_skinny<1, 4, true>(p, st) : launch_skinny<1, 4, false>(p, st);
+  if (M <= 36LL * E || wide_units <= sm_count)
     return f32 ? launch_tc<false, true>(p, sm_count, err, st) : launch_tc<false, false>(p, sm_count, err, st);
-  }
-  // Warps that the product would have with one warp to 16 weight rows.
-  const long long warps = (long long)M * ((N + 15) / 16);
-  if (warps >= SK_FULL_WARPS) return f32 ? launch_skinny<1, 4, true>(p, st) : launch_skinny<1, 4, false>(p, st);
-  return f32 ? launch_skinny<8, 8, true>(p, st) : launch_skinny<8, 8, false>(p, st);
+  return f32 ? launch_tc<true, true>(p, sm_count, err, st) : launch_tc<true, false>(p, sm_count, err, st);
 }
 
 }  // namespace flint
