@@ -42,6 +42,8 @@ struct QuantParams {
   const void* x;
   long long stride;
   int rows, K;
+  unsigned col_tiles;  // CTAs side by side
+  int wide;            // log2 of a CTA's block columns
   const int32_t* pos;
   int top_k;
   int places;  // rows of q and of a scale line
@@ -51,20 +53,31 @@ struct QuantParams {
 
 __device__ __forceinline__ float rcp_approx(float v) {
   float r;
-  asm("rcp.approx.f32 %0, %1;" : "=f"(r) : "f"(v));
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(v));
+  return r;
+}
+// The larger magnitude, NaN if either is.
+__device__ __forceinline__ float max_abs(float a, float b) {
+  float r;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(fabsf(a)), "f"(fabsf(b)));
   return r;
 }
 
-// 8 lanes per block of 128, 16 values each; a CTA has 32 neighbouring rows of one
-// block column, so that their scales are one 128-byte line.  The block's
-// largest magnitude a (NaN if the block holds one) gives scale = a / 448 and
-// codes e4m3(x * (448 / a)), one rounding to nearest even.
+// 8 lanes per block of 128, 16 values each.  A CTA has 32 blocks: 2^wide
+// neighbouring block columns of 32 / 2^wide rows, as wide as the row's blocks
+// divide evenly, so that a row's bytes are read and written together.  The
+// block's largest magnitude a (NaN if the block holds one) gives scale = a / 448
+// and codes e4m3(x * (448 / a)), one rounding to nearest even.
+//
+// Bound by HBM and by the instructions of the conversion.  QUANT_NOTE
 template <bool BF16, bool SILU>
 __global__ void __launch_bounds__(256) quantize_kernel(const QuantParams p) {
   pdl_wait();
   pdl_trigger();
   const int lane = threadIdx.x & 7;
-  const int row = blockIdx.x * 32 + (threadIdx.x >> 3), b = blockIdx.y;
+  const unsigned tile = blockIdx.x / p.col_tiles, u = threadIdx.x >> 3;
+  const int b = (int)(((blockIdx.x - tile * p.col_tiles) << p.wide) + (u & ((1u << p.wide) - 1u)));
+  const int row = (int)(tile * (32u >> p.wide) + (u >> p.wide));
   const int k = b * 128 + lane * 16;
   const bool in = row < p.rows && k < p.K;  // K is a multiple of 16
   constexpr int AT_ONCE = 8;
@@ -90,13 +103,11 @@ __global__ void __launch_bounds__(256) quantize_kernel(const QuantParams p) {
       for (int i = 0; i < 16; ++i) v[i] = v[i] * rcp_approx(1.f + __expf(-v[i])) * u[i];
     }
   }
-  // Magnitudes compare as integers; NaN's is above every other.
-  uint32_t m = 0u;
+  float a = 0.f;
 #pragma unroll
-  for (int i = 0; i < 16; ++i) m = max(m, __float_as_uint(v[i]) & 0x7FFFFFFFu);
+  for (int i = 0; i < 16; ++i) a = max_abs(a, v[i]);
 #pragma unroll
-  for (int off = 4; off > 0; off >>= 1) m = max(m, __shfl_xor_sync(0xffffffffu, m, off));
-  float a = __uint_as_float(m);
+  for (int off = 4; off > 0; off >>= 1) a = max_abs(a, __shfl_xor_sync(0xffffffffu, a, off));
   if (a < Q_FLOOR) a = Q_FLOOR;  // false for NaN
   const float scale = __fdiv_rn(a, E4M3_TOP), r = __fdiv_rn(E4M3_TOP, a);
   uint32_t c[4];
@@ -132,42 +143,58 @@ struct CombineParams {
 };
 
 // One thread per 8 outputs of a token; the sum runs over the choices in order,
-// then the shared row, in fp32, and is rounded once to bf16.  Four choices'
-// rows are under way at a time.
+// then the shared row, in fp32, and is rounded once to bf16.  Bound by HBM:
+// AT_ONCE choices' rows are under way at a time.  COMBINE_NOTE
 template <bool BF16>
 __global__ void __launch_bounds__(128) combine_kernel(const CombineParams p) {
+  constexpr int AT_ONCE = BF16 ? 8 : 4, WORDS = BF16 ? 1 : 2;
   pdl_wait();
   pdl_trigger();
   const int t = blockIdx.x, n = (blockIdx.y * 128 + threadIdx.x) * 8;
   if (n >= p.N) return;
   const int32_t* pos = p.pos + (size_t)t * p.top_k;
   const float* w = p.w + (size_t)t * p.top_k;
-  float acc[8], sh[8];
+  const uint4 zero = make_uint4(0, 0, 0, 0);
+  uint4 sh = zero;
+  if (p.shared != nullptr) sh = __ldg(reinterpret_cast<const uint4*>(p.shared + (size_t)t * p.N + n));
+  float acc[8];
 #pragma unroll
-  for (int i = 0; i < 8; ++i) acc[i] = sh[i] = 0.f;
-  if (p.shared != nullptr) load8<true>(p.shared, (size_t)t * p.N + n, sh);
-  for (int j0 = 0; j0 < p.top_k; j0 += 4) {
-    float v[4][8], f[4];
+  for (int i = 0; i < 8; ++i) acc[i] = 0.f;
+  for (int j0 = 0; j0 < p.top_k; j0 += AT_ONCE) {
+    uint4 raw[AT_ONCE][WORDS];
+    float f[AT_ONCE];
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      int r = j0 + j < p.top_k ? __ldg(pos + j0 + j) : -1;
-      f[j] = 0.f;
+    for (int j = 0; j < AT_ONCE; ++j) {
+      const int r = j0 + j < p.top_k ? __ldg(pos + j0 + j) : -1;
+      const bool on = r >= 0 && r < p.n_rows;
+      const uint4* src = reinterpret_cast<const uint4*>(static_cast<const uint8_t*>(p.rows) +
+                                                        ((size_t)(on ? r : 0) * p.N + n) * (BF16 ? 2 : 4));
+      f[j] = on ? __ldg(w + j0 + j) : 0.f;
 #pragma unroll
-      for (int i = 0; i < 8; ++i) v[j][i] = 0.f;
-      if (r >= 0 && r < p.n_rows) {
-        f[j] = __ldg(w + j0 + j);
-        load8<BF16>(p.rows, (size_t)r * p.N + n, v[j]);
-      }
+      for (int i = 0; i < WORDS; ++i) raw[j][i] = on ? __ldg(src + i) : zero;
     }
 #pragma unroll
-    for (int j = 0; j < 4; ++j)
+    for (int j = 0; j < AT_ONCE; ++j) {
+      if (j0 + j >= p.top_k) break;
+      float v[8];
+      if (BF16) {
+        bf16x8_to_f32(raw[j][0], v);
+      } else {
+        const uint32_t u[8] = {raw[j][0].x,         raw[j][0].y,         raw[j][0].z,         raw[j][0].w,
+                               raw[j][WORDS - 1].x, raw[j][WORDS - 1].y, raw[j][WORDS - 1].z, raw[j][WORDS - 1].w};
 #pragma unroll
-      for (int i = 0; i < 8; ++i) acc[i] = fmaf(f[j], v[j][i], acc[i]);
+        for (int i = 0; i < 8; ++i) v[i] = __uint_as_float(u[i]);
+      }
+#pragma unroll
+      for (int i = 0; i < 8; ++i) acc[i] = fmaf(f[j], v[i], acc[i]);
+    }
   }
+  float s[8];
+  bf16x8_to_f32(sh, s);
   uint32_t o[4];
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
-    const __nv_bfloat162 h = __floats2bfloat162_rn(acc[2 * i] + sh[2 * i], acc[2 * i + 1] + sh[2 * i + 1]);
+    const __nv_bfloat162 h = __floats2bfloat162_rn(acc[2 * i] + s[2 * i], acc[2 * i + 1] + s[2 * i + 1]);
     o[i] = *reinterpret_cast<const uint32_t*>(&h);
   }
   *reinterpret_cast<uint4*>(p.y + (size_t)t * p.N + n) = make_uint4(o[0], o[1], o[2], o[3]);
@@ -202,7 +229,13 @@ cudaError_t launch_quantize_rows(const void* x, bool bf16, long long stride, int
   p.places = (int)places;
   p.q = static_cast<uint8_t*>(q);
   p.scales = scales;
-  const dim3 ctas((unsigned)((rows + 31) / 32), (unsigned)((K + 127) / 128));
+  // As many block columns as leave at most an eighth of the CTA's places unused.
+  const int kb = (K + 127) / 128;
+  p.wide = 5;
+  while (p.wide > 0 && (((kb - 1) >> p.wide) + 1) * 8 << p.wide > kb * 9) --p.wide;
+  p.col_tiles = (unsigned)(((kb - 1) >> p.wide) + 1);
+  const unsigned row_tiles = ((unsigned)rows + (32u >> p.wide) - 1) / (32u >> p.wide);
+  const dim3 ctas(row_tiles * p.col_tiles);
   if (bf16) return silu ? launch_pdl(quantize_kernel<true, true>, p, ctas, 256, st)
                         : launch_pdl(quantize_kernel<true, false>, p, ctas, 256, st);
   return silu ? launch_pdl(quantize_kernel<false, true>, p, ctas, 256, st)
