@@ -4,6 +4,7 @@
 #include <atomic>
 #include <cmath>
 #include <cstring>
+#include <initializer_list>
 #include <map>
 #include <mutex>
 #include <vector>
@@ -146,6 +147,17 @@ bool outputs_overlap(const std::vector<Range>& outs, const std::vector<Range>& i
       if (overlap(outs[i], outs[j])) return true;
     for (const Range& r : ins)
       if (overlap(outs[i], r)) return true;
+  }
+  return false;
+}
+
+// The same for a fixed number of buffers, without allocating.
+bool any_overlap(std::initializer_list<Range> outs, std::initializer_list<Range> ins) {
+  for (auto o = outs.begin(); o != outs.end(); ++o) {
+    for (auto q = o + 1; q != outs.end(); ++q)
+      if (overlap(*o, *q)) return true;
+    for (const Range& r : ins)
+      if (overlap(*o, r)) return true;
   }
   return false;
 }
@@ -554,7 +566,7 @@ int flint_moe_route(const flint_moe_routing* r, const void* logits, int logits_t
   const bool bf16 = logits_type == FLINT_MOE_T_BF16;
   const size_t sel = (size_t)T * r->top_k * 4;
   const size_t in = ((size_t)(T - 1) * (size_t)row_stride + r->n_experts) * (bf16 ? 2 : 4);
-  if (outputs_overlap({{ids, sel}, {w, sel}}, {{logits, in}, {bias, (size_t)r->n_experts * 4}}))
+  if (any_overlap({{ids, sel}, {w, sel}}, {{logits, in}, {bias, (size_t)r->n_experts * 4}}))
     return FLINT_MOE_ERR_INVALID_ARG;
   RouteSpec s;
   s.E = r->n_experts;
@@ -580,7 +592,7 @@ int flint_moe_group_pairs(const int32_t* ids, int n_pairs, int n_experts, int32_
   if (!aligned(ids, 16) || !aligned(offsets, 16) || !aligned(order, 16) || !aligned(pos, 16))
     return FLINT_MOE_ERR_INVALID_ARG;
   const size_t n = (size_t)n_pairs * 4;
-  if (outputs_overlap({{offsets, (size_t)(n_experts + 1) * 4}, {order, n}, {pos, n}}, {{ids, n}}))
+  if (any_overlap({{offsets, (size_t)(n_experts + 1) * 4}, {order, n}, {pos, n}}, {{ids, n}}))
     return FLINT_MOE_ERR_INVALID_ARG;
   std::lock_guard<std::mutex> lk(g_mu);
   DeviceState* ds = nullptr;
@@ -605,7 +617,7 @@ int flint_moe_quantize_rows(const void* x, int x_type, long long row_stride, int
   if (x == nullptr || q == nullptr || scales == nullptr) return FLINT_MOE_ERR_INVALID_ARG;
   if (!aligned(x, 16) || !aligned(q, 16) || !aligned(scales, 16) || !opt_aligned(pos)) return FLINT_MOE_ERR_INVALID_ARG;
   const size_t in = (size_t)((rows - 1) * row_stride + width) * (size_t)size;
-  if (outputs_overlap({{q, (size_t)places * K}, {scales, (size_t)places * ((K + 127) / 128) * 4}},
+  if (any_overlap({{q, (size_t)places * K}, {scales, (size_t)places * ((K + 127) / 128) * 4}},
                       {{x, in}, {pos, (size_t)rows * (pos ? top_k : 0) * 4}}))
     return FLINT_MOE_ERR_INVALID_ARG;
   std::lock_guard<std::mutex> lk(g_mu);
@@ -630,7 +642,7 @@ int flint_moe_block_gemm(const void* a, const float* a_scales, int M, const void
       !opt_aligned(offsets))
     return FLINT_MOE_ERR_INVALID_ARG;
   const size_t kb = (size_t)(K + 127) / 128, nb = (size_t)(N + 127) / 128;
-  if (outputs_overlap({{y, (size_t)M * N * (y_type == FLINT_MOE_T_BF16 ? 2 : 4)}},
+  if (any_overlap({{y, (size_t)M * N * (y_type == FLINT_MOE_T_BF16 ? 2 : 4)}},
                       {{a, (size_t)M * K},
                        {a_scales, (size_t)M * kb * 4},
                        {b, (size_t)n_experts * N * K},
@@ -656,7 +668,7 @@ int flint_moe_combine(const void* rows, int rows_type, int n_rows, const int32_t
   if (!aligned(rows, 16) || !aligned(pos, 16) || !aligned(w, 16) || !aligned(y, 16) || !opt_aligned(shared))
     return FLINT_MOE_ERR_INVALID_ARG;
   const size_t act = (size_t)T * N * 2, sel = (size_t)T * top_k * 4;
-  if (outputs_overlap({{y, act}}, {{rows, (size_t)n_rows * N * (rows_type == FLINT_MOE_T_BF16 ? 2 : 4)},
+  if (any_overlap({{y, act}}, {{rows, (size_t)n_rows * N * (rows_type == FLINT_MOE_T_BF16 ? 2 : 4)},
                                    {pos, sel},
                                    {w, sel},
                                    {shared, act}}))

@@ -61,28 +61,31 @@ __global__ void __launch_bounds__(SK_WARPS * 32, 24 / SK_WARPS) block_gemm_skinn
   const int r = blockIdx.x;
   int e = 0, r0 = 0, r1 = p.M;
   if (p.offsets != nullptr) {
-    // expert of row r: the number of groups that end at or before it; its range:
-    // the offsets on either side of r
+    // expert of row r: the last group that starts at or before it; its range: the
+    // offsets on either side of r
     if (warp == 0) {
-      unsigned ended = 0, from = 0, to = (unsigned)p.M;
+      unsigned begun = 0, from = 0, to = (unsigned)p.M;
       for (int i = lane; i <= p.E; i += 32) {
         const int o = __ldg(p.offsets + i);
-        ended += i > 0 && o <= r ? 1 : 0;
-        if (o >= 0 && o <= r) from = max(from, (unsigned)o);
-        if (o > r) to = min(to, (unsigned)o);
+        if (o <= r) {
+          ++begun;
+          from = max(from, (unsigned)max(o, 0));
+        } else {
+          to = min(to, (unsigned)o);
+        }
       }
-      ended = __reduce_add_sync(0xffffffffu, ended);
+      begun = __reduce_add_sync(0xffffffffu, begun);
       from = redux_max(from);
       to = redux_min(to);
       if (lane == 0) {
-        range[0] = (int)ended;
+        range[0] = (int)begun - 1;
         range[1] = (int)from;
         range[2] = (int)to;
       }
     }
     __syncthreads();
     e = range[0];
-    if (e >= p.E) return;
+    if (e < 0 || e >= p.E) return;
     r0 = range[1];
     r1 = range[2];
     if (r < r0 || r >= r1) return;

@@ -136,6 +136,32 @@ def test_route_masked(dtype):
 
 
 @gpu
+@pytest.mark.parametrize("softmax", [False, True])
+def test_route_masked_with_bias(softmax):
+    """The same with keys that a bias decides: infinite and NaN biases, and logits so low or
+    high that the score is 0 or 1."""
+    d = dev()
+    E = 48
+    x = torch.randn(9, E, generator=gen(11))
+    x[0] = -float("inf")
+    x[1, ::3] = -float("inf")
+    x[2, 5:] = float("nan")
+    x[3] = torch.finfo(torch.float32).min
+    x[4, 7], x[4, 9] = float("inf"), float("inf")
+    x[5] = -200.0
+    x[6] = 60.0
+    x[7] = 0.5
+    b = 0.1 * torch.randn(E, generator=gen(12))
+    for case in range(3):
+        if case == 1:
+            b[3], b[4] = -float("inf"), float("nan")
+        if case == 2:
+            b[20], b[33] = float("inf"), float("inf")
+        for kw in (dict(), dict(n_groups=6, top_groups=2), dict(n_groups=6, top_groups=2, top2=True)):
+            check_route(x.to(d), 6, bias=b.to(d), softmax=softmax, **kw)
+
+
+@gpu
 def test_route_strided_rows():
     d = dev()
     big = torch.randn(50, 300, generator=gen(4)).to(d)
@@ -412,6 +438,72 @@ def test_combine_skips_what_pos_does_not_name():
     F.combine(rows, torch.tensor([[4, -1], [-1, -1]], dtype=torch.int32, device=d), torch.full((2, 2), 0.5, device=d), y)
     torch.cuda.synchronize()
     assert (y[0] == 1.0).all() and (y[1] == 0.0).all()
+
+
+# ------------------------------------------------------------------ beyond 32 bits
+
+
+@gpu
+def test_offsets_beyond_32_bits():
+    """Outputs and inputs of more than 2^31 elements: the last rows against the reference."""
+    d = dev()
+    rows, wide, n = 70016, 32768, 5
+    assert rows * wide > 2 ** 31
+    a, sa, b, sb = make_product(rows, wide, 16, 1, 3, d)
+    y = torch.empty(rows, wide, dtype=torch.bfloat16, device=d)
+    F.block_gemm(a, sa, b, sb, y)
+    torch.cuda.synchronize()
+    assert F.device_error() == 0
+    check_product(y[-n:], a[-n:], sa[:, -n:], b, sb)
+    q = torch.empty(rows, wide, dtype=torch.float8_e4m3fn, device=d)
+    s = torch.empty(wide // 128, rows, device=d)
+    F.quantize_rows(y, q, s)
+    torch.cuda.synchronize()
+    check_codes(f64(q[-n:]), f64(s[:, -n:]), f64(y[-n:]), np.zeros((n, wide)))
+    pos = torch.tensor([[rows - 1, 0], [rows - 2, -1]], dtype=torch.int32, device=d)
+    w, out = torch.tensor([[0.5, 2.0], [1.0, 1.0]], device=d), torch.empty(2, wide, dtype=torch.bfloat16, device=d)
+    F.combine(y, pos, w, out)
+    torch.cuda.synchronize()
+    ends = f64(torch.stack([y[0], y[-2], y[-1]]))
+    ry, mag = R.combine(ends, np.array([[2, 0], [1, -1]]), f64(w))
+    assert np.all(np.abs(f64(out) - ry) <= 4 * 2.0 ** -24 * mag + BF16 * np.abs(ry))
+
+
+@gpu
+def test_route_rows_beyond_32_bits():
+    """Rows so far apart that the last one starts beyond 2^31 elements."""
+    d = dev()
+    T, stride = 5, 1 << 29
+    big = torch.empty(T * stride, dtype=torch.bfloat16, device=d)
+    x = big.as_strided((T, 256), (stride, 1))
+    x.copy_(torch.randn(T, 256, generator=gen(2)).to(torch.bfloat16))
+    check_route(x, 6)
+
+
+@gpu
+@pytest.mark.parametrize("M,E", [(64, 16), (2000, 16), (6000, 16)])
+def test_block_gemm_on_two_streams(M, E):
+    """Calls that overlap on two streams give what each gives alone."""
+    d = dev()
+    N, K = 520, 656
+    counts = np.bincount(np.arange(M) * 7 % 13 % E, minlength=E)
+    off = torch.from_numpy(np.concatenate([[0], np.cumsum(counts)]).astype(np.int32)).to(d)
+    ins = [make_product(M, N, K, E, s, d) for s in (1, 2)]
+    alone = [torch.empty(M, N, device=d) for _ in ins]
+    for i, y in zip(ins, alone):
+        F.block_gemm(*i, y, offsets=off)
+    torch.cuda.synchronize()
+    ys = [torch.full((M, N), float("nan"), device=d) for _ in ins]
+    streams = [torch.cuda.Stream() for _ in ins]
+    torch.cuda.synchronize()
+    for _ in range(20):
+        for st, i, y in zip(streams, ins, ys):
+            F.block_gemm(*i, y, offsets=off, stream=st)
+    torch.cuda.synchronize()
+    assert F.device_error() == 0
+    for y, z in zip(ys, alone):
+        assert torch.equal(y, z)
+    check_product(alone[0], *ins[0], off.cpu().numpy())
 
 
 # ------------------------------------------------------------------ the run of them
