@@ -11,10 +11,11 @@
 // candidates in order in fp64 (about one row in 250 with 256 experts and a
 // bias), or the whole row where that needs more than the candidates.
 //
-// Bound by instructions, some 600 a row: a pick is one redux of the lanes'
-// best keys, one of the indices that have it, and a new best in the lane that
-// owned it.  8,191 rows of 256 with 8 groups, bias and 8 picks: 276 us with
-// every score in fp64, ROUTE_US us this way.
+// Bound by instructions, some 1,300 a row with groups and bias: a pick is one
+// redux of the lanes' best keys, one of the indices that have it, and the next
+// best in the lane that owned it (every lane keeps two at hand).  8,191 rows of
+// 256 with 8 groups, bias and 8 picks: 276 us with every score in fp64, 15.4 us
+// this way (the bytes alone: 1.3 us).
 #include "flint_common.cuh"
 #include "flint_internal.h"
 
@@ -28,7 +29,7 @@ constexpr unsigned FULL = 0xffffffffu;
 // share a key.
 __device__ __forceinline__ uint32_t ord_key(float f) {
   const uint32_t b = __float_as_uint(__fadd_rn(f, 0.0f));
-  return (b >> 31) ? ~b : (b | 0x80000000u);
+  return b ^ ((uint32_t)((int)b >> 31) | 0x80000000u);
 }
 
 struct RouteParams {
@@ -335,16 +336,18 @@ __device__ __forceinline__ bool route_row_f32(const RouteParams& p, const float 
   }
   if (p.n_groups > 1) {
     const int G = p.n_groups, size = p.E / G;
-    float score = -INFINITY;  // lane g: group g's
+    uint32_t g1 = 0u, g2 = 0u;  // lane g: group g's two best
     auto close = [&](int g, uint32_t a, uint32_t b) {  // a, b: this lane's two best of the group
       const uint32_t m1 = redux_max(a);
-      float v = ord_value(m1);
+      uint32_t m2 = 0u;
       if (p.top2) {
         const uint32_t who = __ballot_sync(FULL, a == m1);
-        const uint32_t m2 = redux_max(lane == __ffs(who) - 1 ? b : a);
-        if (m2 != 0u) v += ord_value(m2);
+        m2 = redux_max(lane == __ffs(who) - 1 ? b : a);
       }
-      if (lane == g) score = v;
+      if (lane == g) {
+        g1 = m1;
+        g2 = m2;
+      }
     };
     uint32_t a = 0u, b = 0u;
     auto add = [&](uint32_t k) {
@@ -377,6 +380,7 @@ __device__ __forceinline__ bool route_row_f32(const RouteParams& p, const float 
         close(g, a, b);
       }
     }
+    const float score = ord_value(g1) + (g2 != 0u ? ord_value(g2) : 0.f);
     int rank = 0;
     for (int g = 0; g < G; ++g) {
       const float o = __shfl_sync(FULL, score, g);
@@ -408,53 +412,67 @@ __device__ __forceinline__ bool route_row_f32(const RouteParams& p, const float 
     }
   }
 
-  // The lane's two best that are left.  A lane that wins twice looks for its
-  // next two among the rest; with the experts spread over the lanes that is rare.
+  // The lane's two best; a lane that wins twice looks for its next one among the
+  // rest.
   uint32_t best = 0u, second = 0u, done = 0u;
-  int at = 0, at2 = 0;
-  auto rescan = [&]() {
-    best = second = 0u;
+  int id = lane, id2 = lane;  // their experts
 #pragma unroll
-    for (int i = 0; i < EPL; ++i) {
-      const uint32_t k = ((done >> i) & 1u) ? 0u : key[i];
-      if (k > best) {
-        second = best;
-        at2 = at;
-        best = k;
-        at = i;
-      } else if (k > second) {
-        second = k;
-        at2 = i;
-      }
+  for (int i = 0; i < EPL; ++i) {
+    if (key[i] > best) {
+      second = best;
+      id2 = id;
+      best = key[i];
+      id = lane + 32 * i;
+    } else if (key[i] > second) {
+      second = key[i];
+      id2 = lane + 32 * i;
     }
-  };
-  rescan();
+  }
   my_e = -1;
   uint32_t my_key = 0u;
-  // With a bias the picks go on as long as they could belong before the last
-  // one that counts: candidates beyond it are not in reach of fp32's error.
   int n = 0;
-  float last = 0.f;
-  for (; n < 32; ++n) {
-    if (n >= p.top_k && !biased) break;
-    const uint32_t m = redux_max(best);
-    if (m == 0u) break;
-    const float v = ord_value(m);
-    if (n == p.top_k - 1) last = v;
-    if (n >= p.top_k && last - v > 2.f * err + SUM_ERR * (fabsf(v) + fabsf(last))) break;
-    const int e = (int)redux_min(best == m ? (uint32_t)(at * 32 + lane) : 0xFFFFFFFFu);
+  auto pick = [&](uint32_t m) {  // m: the warp's best key
+    const int e = (int)redux_min(best == m ? (uint32_t)id : 0xFFFFFFFFu);
     if (lane == n) {
       my_e = e;
       my_key = m;
     }
-    const bool won = (e & 31) == lane;
+    ++n;
+    const bool won = e == id && best == m;
     if (won) {
-      done |= 1u << at;
+      done |= 1u << (id >> 5);
       best = second;
-      at = at2;
+      id = id2;
       second = 0u;
     }
-    if (EPL > 2 && __any_sync(FULL, won && best == 0u)) rescan();
+    if (EPL > 2 && __any_sync(FULL, won && best == 0u)) {
+      if (won) {
+#pragma unroll
+        for (int i = 0; i < EPL; ++i) {
+          const uint32_t k = ((done >> i) & 1u) ? 0u : key[i];
+          if (k > best) {
+            best = k;
+            id = lane + 32 * i;
+          }
+        }
+      }
+    }
+  };
+  uint32_t m = redux_max(best);
+  while (n < p.top_k && m != 0u) {
+    pick(m);
+    m = redux_max(best);
+  }
+  if (biased && m != 0u) {
+    // The picks go on as long as they could belong before the last one that
+    // counts: candidates beyond are not in reach of fp32's error.
+    const float last = ord_value(__shfl_sync(FULL, my_key, n - 1));
+    while (n < 32 && m != 0u) {
+      const float v = ord_value(m);
+      if (last - v > 2.f * err + SUM_ERR * (fabsf(v) + fabsf(last))) break;
+      pick(m);
+      m = redux_max(best);
+    }
   }
   if (biased) {
     // Neighbours in the order must be further apart than their errors, unless
@@ -576,7 +594,7 @@ __global__ void __launch_bounds__(128) route_kernel(const RouteParams p) {
 // decides an order, so the result is the same on every call.
 //
 // Latency bound: the bytes are 12 a pair.  One CTA needs 61 us for 49,152 pairs
-// of 256 experts; GP_NOTE
+// of 256 experts, eight 8.6 us.  Up to 2,048 pairs one CTA is enough.
 constexpr int GP_WARPS = 32;
 constexpr int GP_CTAS = 8;
 constexpr int GP_HELD = 8;
@@ -755,7 +773,7 @@ cudaError_t launch_route(const RouteSpec& r, const void* logits, bool bf16, long
 cudaError_t launch_group_pairs(const int32_t* ids, int P, int E, int32_t* offsets, int32_t* order, int32_t* pos,
                                cudaStream_t st) {
   cudaLaunchConfig_t cfg = {};
-  // One CTA alone saves the exchange: up to two passes of its warps.
+  // One CTA alone saves the exchange with the others: up to two ids a thread.
   const unsigned ctas = P <= 2 * GP_WARPS * 32 ? 1 : GP_CTAS;
   cfg.gridDim = dim3(ctas);
   cfg.blockDim = dim3(GP_WARPS * 32);
