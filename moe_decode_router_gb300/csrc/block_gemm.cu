@@ -186,12 +186,12 @@ cudaError_t launch_skinny(const GemmArgs& p, cudaStream_t st) {
 // The block scales allow the tensor cores 128 of K at a time: every K block is
 // a fresh accumulator in tensor memory, and eight promotion warps read it back
 // and add it, scaled, into fp32 registers while the next blocks are multiplied.
-// The rate is set by how much tensor memory is under way: an accumulator is
-// free again only after its MMAs, a barrier, the read and a barrier back, so
-// accumulators are small (128 or 64 columns) and there are four or eight, and
-// the barriers stay inside one SM (with cta_group::2 each hand-over crosses
-// SMs: 1.1 us a round trip, 2.0 PFLOP/s where this reaches more).  Two
-// arrangements of the same pipeline:
+// An accumulator is free again only after its MMAs, a barrier, the read and a
+// barrier back, and a barrier costs some 100 cycles on either side: the hand-over
+// stays inside one SM (with cta_group::2 it crosses SMs, which took 1.2 times as
+// long), nothing else is waited for on the way (the scales come through a ring in
+// shared memory), and the MMAs of the next block cover it.  Two arrangements of
+// the same pipeline:
 //
 // TALL (long groups).  128 rows of a are the M side and 256 weight rows the N
 // side.  A thread holds one row of a (its tensor-memory lane) and 128 outputs,
@@ -210,8 +210,8 @@ cudaError_t launch_skinny(const GemmArgs& p, cudaStream_t st) {
 // neighbouring columns, so that a pair of column scales, read once from a ring
 // in shared memory, serves 4 packed fma.
 //
-// Warps: 0-7 promotion and output, two column halves; 8 TMA producer; 9 and 11
-// MMA issuers; 10 loader of scales.
+// Warps: 0-7 promotion and output, two column halves; 8 TMA producer; 9 MMA
+// issuer; 10 loader of scales; 11 nothing but its registers.
 constexpr int TC_THREADS = 384;
 // Registers of TALL: the promotion warps hold 128 accumulators each and take
 // what the other four warps give up.  Launched with 168 a thread.
@@ -223,7 +223,7 @@ struct TcCfg {
   static constexpr int CTAS = TALL ? 2 : 1;        // of a cluster
   static constexpr int ROWS = TALL ? 256 : 64;     // rows of a in a unit
   static constexpr int WROWS = TALL ? 256 : 128;   // weight rows in a unit
-  static constexpr int ACC = TALL ? 128 : 64;      // columns of an accumulator
+  static constexpr int ACC = TALL ? 256 : 64;      // columns of an accumulator
   static constexpr int NBUF = 512 / ACC;
   static constexpr int X_BYTES = TALL ? 128 * 128 : 64 * 128;  // rows of a in a stage
   static constexpr int W_BYTES = WROWS * 128;
@@ -329,11 +329,11 @@ __global__ void __launch_bounds__(TC_THREADS, 1)
   if (tid == 0) {
     for (int i = 0; i < C::STAGES; ++i) {
       mbar_init(&full[i], 1);
-      mbar_init(&empty[i], TALL ? 4 : 1);  // TALL: two issuers in each of two CTAs
+      mbar_init(&empty[i], C::CTAS);
     }
     for (int i = 0; i < C::NBUF; ++i) {
       mbar_init(&tfull[i], 1);
-      mbar_init(&tempty[i], TALL ? 4 : 8);  // TALL: an accumulator belongs to one column half
+      mbar_init(&tempty[i], 8);
     }
     for (int i = 0; i < C::SLOTS; ++i) {
       mbar_init(&sfull[i], 32);
@@ -478,28 +478,19 @@ __global__ void __launch_bounds__(TC_THREADS, 1)
           }
         }
       }
-    } else if (warp != 10) {
-      // ---------------- two MMA issuers: of one column half each (TALL), of
-      // the even and odd K blocks (WIDE).  Each commit costs its issuer about 100
-      // cycles, and each MMA 40 (70 if one lane runs the loop: its descriptors
-      // are not warp-uniform then), so that one issuer would need more than the
-      // 512 cycles of a block's MMAs.  A phase two ahead has the same parity, so
-      // an issuer has to see every phase of the barriers that it waits for: it
-      // takes part in every use of its stages and accumulators.
-      static_assert(TALL || (C::NBUF % 2 == 0 && C::STAGES % 2 == 0), "one issuer for each");
-      const uint32_t me = warp == 9 ? 0 : 1;
+    } else if (warp == 9) {
+      // ---------------- MMA issuer.  The whole warp runs the loop, so that the
+      // descriptors are warp-uniform values: 40 cycles an MMA, 70 from one lane's
+      // loop.
       uint32_t g = 0;  // K blocks so far
       bool ok = true;
-      const uint64_t dw0 = tc05::sw128_desc(smem_u32(sm)) + (TALL ? 1024 * me : 0);  // its 128 weight rows
-      const uint64_t dx0 = tc05::sw128_desc(smem_u32(sm) + C::W_BYTES);
+      const uint64_t dw0 = tc05::sw128_desc(smem_u32(sm)), dx0 = tc05::sw128_desc(smem_u32(sm) + C::W_BYTES);
       for (int u = u0; u < n_units && ok; u += ustep) {
         const TcUnit t = unit_of(u);
-        const int n = TALL ? min(128, t.n - 128 * (int)me) : t.n;  // <= 0: a narrow tile, nothing but the barriers
-        const uint32_t idesc = tc05::idesc_e4m3(128, n > 0 ? n : 16);
+        const uint32_t idesc = tc05::idesc_e4m3(128, t.n > 0 ? t.n : 16);
         for (int kb = 0; kb < p.kb; ++kb, ++g) {
-          if (!TALL && g % 2 != me) continue;
           const uint32_t s = g % C::STAGES, ph = (g / C::STAGES) & 1;
-          const uint32_t b = TALL ? 2 * me + (g & 1) : g % C::NBUF, bph = ((TALL ? g >> 1 : g / C::NBUF) & 1) ^ 1;
+          const uint32_t b = g % C::NBUF, bph = ((g / C::NBUF) & 1) ^ 1;
           // every lane looks and waits, and all go on or none
           const bool ready = mbar_test(&full[s], ph) & mbar_test(&tempty[b], bph);
           if (!__all_sync(0xffffffffu, ready)) {
@@ -510,7 +501,7 @@ __global__ void __launch_bounds__(TC_THREADS, 1)
           tc05::fence_after_sync();
           const uint64_t dw = dw0 + (uint64_t)(s * (C::STAGE >> 4)), dx = dx0 + (uint64_t)(s * (C::STAGE >> 4));
           const uint32_t d = tmem + b * C::ACC;
-          if (n > 0) {
+          if (t.n > 0) {  // else the last of an odd number of weight tiles: nothing but the barriers
 #pragma unroll
             for (int k = 0; k < 4; ++k) {
               if (TALL) tc05::mma_e4m3(d, dx + 2 * k, dw + 2 * k, idesc, k > 0 ? 1u : 0u);
@@ -527,7 +518,7 @@ __global__ void __launch_bounds__(TC_THREADS, 1)
         while (clock64() - t0 < 2000000) {
         }
       }
-    } else {
+    } else if (warp == 10) {
       // ---------------- scales
       uint32_t s = 0, ph = 0;
       float* ring = reinterpret_cast<float*>(sm + C::OFF_SCALE);
@@ -618,12 +609,12 @@ __global__ void __launch_bounds__(TC_THREADS, 1)
         for (int i = 0; i < 64; ++i) acc[i] = 0ull;
         auto promote = [&](const float* sa, const float* sb) -> bool {  // one K block
           const float sc = sa[quad * 32 + lane] * sb[half];
-          const uint32_t b = 2 * half + (v & 1), bph = (v >> 1) & 1;
+          const uint32_t b = v % C::NBUF, bph = (v / C::NBUF) & 1;
           ++v;
           if (!wait(&tfull[b], bph)) return false;
           tc05::fence_after_sync();
           if (live > 0) {
-            const uint32_t ta = lanes + b * C::ACC;
+            const uint32_t ta = lanes + b * C::ACC + half * 128;
             uint32_t r[2][16];
             tc05::ld_32x32b_x16(ta, r[0]);
             const uint64_t s2 = f2pack(sc, sc);
@@ -909,8 +900,10 @@ cudaError_t launch_block_gemm(const void* a, const float* sa, int M, const void*
   //   one wave of WIDE's units,
   //   or 36 rows an expert        WIDE             24 rows each: 89, TALL 93; 256 dense: 9.3, 11.9
   //   else                        TALL             48 rows each: 98, WIDE 107; 512 dense: 12.2, 15.2
+  constexpr int WIDE_ROWS = TcCfg<false>::ROWS, WIDE_W = TcCfg<false>::WROWS;
   const long long groups = M < E ? M : E;  // that can have rows
-  const long long wide_units = (M / TcCfg<false>::ROWS + groups) * ((N + TcCfg<false>::WROWS - 1) / TcCfg<false>::WROWS);
+  const long long wide_tiles = offsets == nullptr ? (M + WIDE_ROWS - 1) / WIDE_ROWS : M / WIDE_ROWS + groups;
+  const long long wide_units = wide_tiles * ((N + WIDE_W - 1) / WIDE_W);
   if (M <= 8) return f32 ? launch_skinny<8, 8, true>(p, st) : launch_skinny<8, 8, false>(p, st);
   if (M > 32 && M <= 128 && M <= E) return f32 ? launch_skinny<1, 4, true>(p, st) : launch_skinny<1, 4, false>(p, st);
   if (M <= 36LL * E || wide_units <= sm_count)
