@@ -340,7 +340,7 @@ int flint_moe_group_pairs(const int32_t *ids, int n_pairs, int n_experts, int32_
  * 128 does not divide K).
  *   x       [rows][K] of x_type (silu_mul != 0: [rows][2K], and the row
  *           quantised is silu(first half) * second half, formed in fp32 and not
- *           rounded before), rows row_stride elements apart
+ *           rounded before; below -87 the activation is 0), rows row_stride elements apart
  *   pos     int32 [rows][top_k]: the places that each row is written to
  *           (places outside 0..places-1 are skipped; two rows must not share
  *           one), or NULL: row i is written to place i, and places == rows

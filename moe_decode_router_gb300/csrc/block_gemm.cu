@@ -10,7 +10,7 @@
 
 #include "flint_common.cuh"
 #include "flint_internal.h"
-#include "tc05.cuh"
+#include "tc05_e4m3.cuh"
 
 namespace flint {
 
