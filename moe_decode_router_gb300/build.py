@@ -3,18 +3,22 @@
     python -m moe_decode_router_gb300.build [--force] [-v]
 
 Each .cu file under csrc/ compiles to its own object in parallel; the objects
-link into moe_decode_router_gb300/_lib/libflint_moe.so.  A rebuild happens
-only when a source or header is newer than the library.
+link into moe_decode_router_gb300/_lib/libflint_moe.so.  csrc/binding.cpp, the
+compiled marshalling of the short Python calls, becomes _flint_binding.so beside
+it (against the installed torch).  A rebuild happens only when a source or header
+is newer than what was built.
 """
 
 from __future__ import annotations
 
 import argparse
 import concurrent.futures as cf
+import importlib.util
 import os
 import shutil
 import subprocess
 import sys
+import sysconfig
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
@@ -22,6 +26,8 @@ CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 OUT_DIR = os.path.join(PKG, "_lib")
 LIB = os.path.join(OUT_DIR, "libflint_moe.so")
+BINDING = os.path.join(OUT_DIR, "_flint_binding.so")
+BINDING_SRC = os.path.join(CSRC, "binding.cpp")
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 
@@ -43,11 +49,31 @@ def _deps():
     return files
 
 
+def _torch_dir() -> str:
+    return importlib.util.find_spec("torch").submodule_search_locations[0]
+
+
+def _newer(out, deps) -> bool:
+    return os.path.exists(out) and all(os.path.getmtime(f) <= os.path.getmtime(out) for f in deps)
+
+
 def up_to_date() -> bool:
-    if not os.path.exists(LIB):
-        return False
-    t = os.path.getmtime(LIB)
-    return all(os.path.getmtime(f) <= t for f in _deps())
+    header = os.path.join(INCLUDE, "flint_moe.h")
+    return _newer(LIB, _deps()) and _newer(BINDING, [BINDING_SRC, header, os.path.join(_torch_dir(), "version.py")])
+
+
+def _build_binding(nvcc: str) -> None:
+    torch_dir = _torch_dir()
+    cuda = os.path.dirname(os.path.dirname(os.path.realpath(nvcc)))
+    tmp = BINDING + ".tmp"
+    cmd = [os.environ.get("CXX", "g++"), "-O2", "-std=c++17", "-fPIC", "-shared", BINDING_SRC, "-o", tmp,
+           "-I", INCLUDE, "-I", sysconfig.get_paths()["include"], "-I", os.path.join(torch_dir, "include"),
+           "-I", os.path.join(cuda, "include"), "-L", os.path.join(torch_dir, "lib"),
+           "-ltorch_python", "-ltorch_cpu", "-lc10", "-lc10_cuda"]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"g++ failed on {BINDING_SRC}:\n{r.stdout}\n{r.stderr}")
+    os.replace(tmp, BINDING)
 
 
 def build(force: bool = False, verbose: bool = False) -> str:
@@ -69,7 +95,9 @@ def build(force: bool = False, verbose: bool = False) -> str:
         return obj, r.stderr
 
     with cf.ThreadPoolExecutor(max_workers=min(8, os.cpu_count() or 1)) as ex:
+        binding = ex.submit(_build_binding, nvcc)
         results = list(ex.map(compile_one, _sources()))
+        binding.result()
     if verbose:
         for _, log in results:
             sys.stderr.write(log)

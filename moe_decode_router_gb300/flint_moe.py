@@ -9,7 +9,8 @@ be built or loaded the import-time call ``load_library`` raises.
 from __future__ import annotations
 
 import ctypes
-import functools
+import importlib.machinery
+import importlib.util
 import os
 import threading
 
@@ -145,8 +146,30 @@ def load_library(build_if_missing: bool = True) -> ctypes.CDLL:
             fn = getattr(lib, name)
             fn.restype = res
             fn.argtypes = args
+        _load_binding(lib)
         _LIB = lib
         return lib
+
+
+class _NotLoaded:
+    """Stands for the compiled marshalling until the library is loaded: no call fits it."""
+
+    def __getattr__(self, name):
+        return lambda *args: _LOOK
+
+
+_LOOK = 1  # the compiled look's "not taken": no status of the library is positive
+_FAST = _NotLoaded()
+
+
+def _load_binding(lib):
+    global _FAST
+    loader = importlib.machinery.ExtensionFileLoader("_flint_binding", _build.BINDING)
+    module = importlib.util.module_from_spec(importlib.util.spec_from_loader("_flint_binding", loader))
+    loader.exec_module(module)
+    module.bind(*(ctypes.cast(getattr(lib, f"flint_moe_{name}"), ctypes.c_void_p).value
+                  for name in ("route", "group_pairs", "quantize_rows", "block_gemm", "combine")))
+    _FAST = module
 
 
 def _lib():
@@ -380,36 +403,30 @@ def dense_gemv(w: DenseNVFP4, x, y, stream=None):
     _check(rc, "flint_moe_dense_gemv")
 
 
-# The calls below are short beside their own marshalling, so their tensors are
-# first looked over with the few queries that decide it, in line; the checks that
-# name what is wrong run only when that look fails, and always raise.
+# The calls below are short beside their own marshalling, so they go through the
+# compiled look at their tensors (csrc/binding.cpp), which makes the call or
+# answers _LOOK and has done nothing.  What it did not take comes back here: the
+# checks that name what is wrong, and the same call.
 
 _ACT_TYPES = {torch.bfloat16: T_BF16, torch.float32: T_F32}
-_I32, _F32, _BF16, _E4M3 = torch.int32, torch.float32, torch.bfloat16, torch.float8_e4m3fn
-_AMISS = (AttributeError, IndexError, KeyError, TypeError, ValueError)  # of the look at something else than a tensor
 
 
-def _current_device():
-    return torch._C._cuda_getDevice()
-
-
-def _raw_stream(stream, device):
-    return torch._C._cuda_getCurrentRawStream(device) if stream is None else _stream(stream)
-
-
-def _expect_rows(t, name, types, width):
-    """_expect for a matrix whose rows may lie apart: dtype one of `types`, last
-    dimension contiguous, on the current CUDA device."""
+def _expect_rows(t, name, width):
+    """_expect for a matrix of activations whose rows may lie apart: bf16 or fp32, last
+    dimension contiguous, on the current CUDA device.  Returns (type code, rows, columns,
+    elements between rows)."""
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name}: expected a torch.Tensor, got {type(t).__name__}")
-    if t.dtype not in types:
-        raise ValueError(f"{name}: dtype {t.dtype}, expected {' or '.join(str(d) for d in types)}")
+    if t.dtype not in _ACT_TYPES:
+        raise ValueError(f"{name}: dtype {t.dtype}, expected {' or '.join(str(d) for d in _ACT_TYPES)}")
     if t.dim() != 2 or (width is not None and t.shape[1] != width):
         raise ValueError(f"{name}: shape {tuple(t.shape)}, expected [rows][{'columns' if width is None else width}]")
-    if t.stride(1) != 1 and t.shape[1] != 1:
+    rows, cols = t.shape
+    if t.stride(1) != 1 and cols != 1:
         raise ValueError(f"{name}: the elements of a row must be contiguous")
     if not t.is_cuda or t.device.index != torch.cuda.current_device():
         raise ValueError(f"{name}: must be on the current CUDA device")
+    return _ACT_TYPES[t.dtype], rows, cols, t.stride(0) if rows > 1 else cols
 
 
 def _matrix(t, name):
@@ -420,47 +437,26 @@ def _matrix(t, name):
     return t.shape
 
 
-def _refuse(where, *tensors):
-    """Raises for the first of (tensor, name, dtype, shape) that is not as expected; None is
-    an argument left out."""
-    for t, name, dtype, shape in tensors:
-        if t is not None:
-            _expect(t, name, dtype, shape)
-    raise ValueError(f"{where}: arguments do not fit together")
-
-
-@functools.lru_cache(maxsize=64)
-def _routing(E, k, score, n_groups, top_groups, group_score, renormalise, scale):
-    return ctypes.byref(Routing(E, k, score, n_groups, top_groups, group_score, renormalise, scale))
+def _handle(stream):
+    return None if stream is None else _stream(stream)
 
 
 def route(logits, ids, w, bias=None, score=SCORE_SIGMOID, n_groups=1, top_groups=1, group_score=GROUP_MAX,
           renormalise=True, scale=1.0, stream=None):
     """Chooses ids.shape[1] experts for every row of logits [T][E] (bf16 or fp32, rows may lie
     apart): ids int32 [T][k], w fp32 [T][k].  bias fp32 [E] is added for the choice only."""
-    try:
-        T, E = logits.shape
-        step, unit = logits.stride()
-        sel = ids.shape
-        k = sel[1]
-        dev = logits.get_device()
-        kind = _ACT_TYPES[logits.dtype]
-        fits = (dev >= 0 and dev == _current_device() and (unit == 1 or E == 1) and len(sel) == 2 and sel[0] == T
-                and ids.dtype is _I32 and ids.get_device() == dev and ids.is_contiguous()
-                and w.shape == sel and w.dtype is _F32 and w.get_device() == dev and w.is_contiguous()
-                and (bias is None or (bias.shape == (E,) and bias.dtype is _F32 and bias.get_device() == dev
-                                      and bias.is_contiguous())))
-    except _AMISS:
-        fits = False
-    if not fits:
-        _expect_rows(logits, "logits", _ACT_TYPES, None)
-        want = (logits.shape[0], _matrix(ids, "ids")[1])
-        _expect(w, "w", _F32, want)
-        _refuse("route", (ids, "ids", _I32, want), (bias, "bias", _F32, (logits.shape[1],)))
-    rc = _lib().flint_moe_route(_routing(E, k, score, n_groups, top_groups, group_score, 1 if renormalise else 0, scale),
-                                logits.data_ptr(), kind, step if T > 1 else E, T,
-                                None if bias is None else bias.data_ptr(), ids.data_ptr(), w.data_ptr(),
-                                _raw_stream(stream, dev))
+    rc = _FAST.route(logits, ids, w, bias, score, n_groups, top_groups, group_score, renormalise, scale,
+                     _handle(stream))
+    if rc == _LOOK:
+        kind, T, E, stride = _expect_rows(logits, "logits", None)
+        k = _matrix(ids, "ids")[1]
+        _expect(ids, "ids", torch.int32, (T, k))
+        _expect(w, "w", torch.float32, (T, k))
+        if bias is not None:
+            _expect(bias, "bias", torch.float32, (E,))
+        r = Routing(E, k, score, n_groups, top_groups, group_score, 1 if renormalise else 0, scale)
+        rc = _lib().flint_moe_route(ctypes.byref(r), logits.data_ptr(), kind, stride, T, _ptr(bias), ids.data_ptr(),
+                                    w.data_ptr(), _stream(stream))
     if rc:
         _check(rc, "flint_moe_route")
 
@@ -468,24 +464,17 @@ def route(logits, ids, w, bias=None, score=SCORE_SIGMOID, n_groups=1, top_groups
 def group_pairs(ids, offsets, order, pos, stream=None):
     """Sorts the pairs of ids (int32, any shape) by expert: offsets int32 [E + 1], order int32
     [pairs], pos int32 of the shape of ids."""
-    try:
-        n, E, dev = ids.numel(), offsets.numel() - 1, ids.get_device()
-        fits = (dev >= 0 and dev == _current_device() and ids.dtype is _I32 and ids.is_contiguous()
-                and offsets.dtype is _I32 and offsets.dim() == 1 and offsets.get_device() == dev
-                and offsets.is_contiguous()
-                and order.shape == (n,) and order.dtype is _I32 and order.get_device() == dev and order.is_contiguous()
-                and pos.shape == ids.shape and pos.dtype is _I32 and pos.get_device() == dev and pos.is_contiguous())
-    except _AMISS:
-        fits = False
-    if not fits:
+    rc = _FAST.group_pairs(ids, offsets, order, pos, _handle(stream))
+    if rc == _LOOK:
         if not isinstance(ids, torch.Tensor) or not isinstance(offsets, torch.Tensor):
             raise TypeError("ids, offsets: expected a torch.Tensor")
-        _expect(ids, "ids", _I32, ids.shape)
-        _expect(order, "order", _I32, (ids.numel(),))
-        _expect(pos, "pos", _I32, ids.shape)
-        _refuse("group_pairs", (offsets, "offsets", _I32, (offsets.numel(),)))
-    rc = _lib().flint_moe_group_pairs(ids.data_ptr(), n, E, offsets.data_ptr(), order.data_ptr(), pos.data_ptr(),
-                                      _raw_stream(stream, dev))
+        n, E = ids.numel(), offsets.numel() - 1
+        _expect(ids, "ids", torch.int32, ids.shape)
+        _expect(offsets, "offsets", torch.int32, (E + 1,))
+        _expect(order, "order", torch.int32, (n,))
+        _expect(pos, "pos", torch.int32, ids.shape)
+        rc = _lib().flint_moe_group_pairs(ids.data_ptr(), n, E, offsets.data_ptr(), order.data_ptr(), pos.data_ptr(),
+                                          _stream(stream))
     if rc:
         _check(rc, "flint_moe_group_pairs")
 
@@ -494,30 +483,18 @@ def quantize_rows(x, q, scales, pos=None, silu_mul=False, stream=None):
     """Quantises x [rows][K] (bf16 or fp32; silu_mul: [rows][2K], silu(first half) * second
     half) to q float8_e4m3fn [places][K] and scales fp32 [ceil(K / 128)][places]; pos int32
     [rows][k] gives the places of each row, None: row i goes to place i."""
-    try:
-        places, K = q.shape
-        rows, width = x.shape
-        step, unit = x.stride()
-        k = 0 if pos is None else pos.shape[1]
-        dev = x.get_device()
-        kind = _ACT_TYPES[x.dtype]
-        fits = (dev >= 0 and dev == _current_device() and unit == 1 and width == (2 * K if silu_mul else K)
-                and q.dtype is _E4M3 and q.get_device() == dev and q.is_contiguous()
-                and scales.shape == (-(-K // SCALE_BLOCK), places) and scales.dtype is _F32
-                and scales.get_device() == dev and scales.is_contiguous()
-                and (pos is None or (pos.shape == (rows, k) and pos.dtype is _I32 and pos.get_device() == dev
-                                     and pos.is_contiguous())))
-    except _AMISS:
-        fits = False
-    if not fits:
+    rc = _FAST.quantize_rows(x, q, scales, pos, silu_mul, _handle(stream))
+    if rc == _LOOK:
         places, K = _matrix(q, "q")
-        _expect_rows(x, "x", _ACT_TYPES, 2 * K if silu_mul else K)
-        _expect(scales, "scales", _F32, (-(-K // SCALE_BLOCK), places))
-        _refuse("quantize_rows", (q, "q", _E4M3, (places, K)),
-                (pos, "pos", _I32, (x.shape[0], 0 if pos is None else _matrix(pos, "pos")[1])))
-    rc = _lib().flint_moe_quantize_rows(x.data_ptr(), kind, step if rows > 1 else width, rows, K, 1 if silu_mul else 0,
-                                        None if pos is None else pos.data_ptr(), k, places, q.data_ptr(),
-                                        scales.data_ptr(), _raw_stream(stream, dev))
+        kind, rows, _, stride = _expect_rows(x, "x", 2 * K if silu_mul else K)
+        _expect(q, "q", torch.float8_e4m3fn, (places, K))
+        _expect(scales, "scales", torch.float32, (-(-K // SCALE_BLOCK), places))
+        k = 0
+        if pos is not None:
+            k = _matrix(pos, "pos")[1]
+            _expect(pos, "pos", torch.int32, (rows, k))
+        rc = _lib().flint_moe_quantize_rows(x.data_ptr(), kind, stride, rows, K, 1 if silu_mul else 0, _ptr(pos), k,
+                                            places, q.data_ptr(), scales.data_ptr(), _stream(stream))
     if rc:
         _check(rc, "flint_moe_quantize_rows")
 
@@ -527,39 +504,24 @@ def block_gemm(a, a_scales, b, b_scales, y, offsets=None, stream=None):
     [M][K], a_scales fp32 [ceil(K / 128)][M], b [experts][N][K], b_scales
     [experts][ceil(N / 128)][ceil(K / 128)].  offsets int32 [experts + 1] gives every expert
     its rows of a; None: dense (b of one expert)."""
-    try:
-        E, N, K = b.shape
-        M = y.shape[0]
-        kb = -(-K // SCALE_BLOCK)
-        dev = y.get_device()
-        kind = _ACT_TYPES[y.dtype]
-        fits = (dev >= 0 and dev == _current_device() and y.shape == (M, N) and y.is_contiguous()
-                and a.shape == (M, K) and a.dtype is _E4M3 and a.get_device() == dev and a.is_contiguous()
-                and a_scales.shape == (kb, M) and a_scales.dtype is _F32 and a_scales.get_device() == dev
-                and a_scales.is_contiguous()
-                and b.dtype is _E4M3 and b.get_device() == dev and b.is_contiguous()
-                and b_scales.shape == (E, -(-N // SCALE_BLOCK), kb) and b_scales.dtype is _F32
-                and b_scales.get_device() == dev and b_scales.is_contiguous()
-                and (offsets is None or (offsets.shape == (E + 1,) and offsets.dtype is _I32
-                                         and offsets.get_device() == dev and offsets.is_contiguous())))
-    except _AMISS:
-        fits = False
-    if not fits:
+    rc = _FAST.block_gemm(a, a_scales, b, b_scales, y, offsets, _handle(stream))
+    if rc == _LOOK:
         if not isinstance(b, torch.Tensor):
             raise TypeError(f"b: expected a torch.Tensor, got {type(b).__name__}")
         if b.dim() != 3:
             raise ValueError(f"b: expected [experts][N][K], got shape {tuple(b.shape)}")
         E, N, K = b.shape
-        _expect_rows(y, "y", _ACT_TYPES, N)
-        M, kb = y.shape[0], -(-K // SCALE_BLOCK)
+        kind, M, _, _ = _expect_rows(y, "y", N)
+        kb = -(-K // SCALE_BLOCK)
         _expect(y, "y", y.dtype, (M, N))
-        _expect(a, "a", _E4M3, (M, K))
-        _expect(a_scales, "a_scales", _F32, (kb, M))
-        _expect(b_scales, "b_scales", _F32, (E, -(-N // SCALE_BLOCK), kb))
-        _refuse("block_gemm", (b, "b", _E4M3, (E, N, K)), (offsets, "offsets", _I32, (E + 1,)))
-    rc = _lib().flint_moe_block_gemm(a.data_ptr(), a_scales.data_ptr(), M, b.data_ptr(), b_scales.data_ptr(), E,
-                                     None if offsets is None else offsets.data_ptr(), N, K, y.data_ptr(), kind,
-                                     _raw_stream(stream, dev))
+        _expect(a, "a", torch.float8_e4m3fn, (M, K))
+        _expect(a_scales, "a_scales", torch.float32, (kb, M))
+        _expect(b, "b", torch.float8_e4m3fn, (E, N, K))
+        _expect(b_scales, "b_scales", torch.float32, (E, -(-N // SCALE_BLOCK), kb))
+        if offsets is not None:
+            _expect(offsets, "offsets", torch.int32, (E + 1,))
+        rc = _lib().flint_moe_block_gemm(a.data_ptr(), a_scales.data_ptr(), M, b.data_ptr(), b_scales.data_ptr(), E,
+                                         _ptr(offsets), N, K, y.data_ptr(), kind, _stream(stream))
     if rc:
         _check(rc, "flint_moe_block_gemm")
 
@@ -567,33 +529,19 @@ def block_gemm(a, a_scales, b, b_scales, y, offsets=None, stream=None):
 def combine(rows, pos, w, y, shared=None, stream=None):
     """y [T][N] (bf16) = sum over j of w[t][j] * rows[pos[t][j]] (+ shared [T][N] bf16); rows
     bf16 or fp32 [any][N], pos int32 and w fp32 [T][k]; pos outside the rows adds nothing."""
-    try:
-        T, N = y.shape
-        n_rows = rows.shape[0]
-        sel = pos.shape
-        k = sel[1]
-        dev = y.get_device()
-        kind = _ACT_TYPES[rows.dtype]
-        fits = (dev >= 0 and dev == _current_device() and y.dtype is _BF16 and y.is_contiguous()
-                and rows.shape == (n_rows, N) and rows.get_device() == dev and rows.is_contiguous()
-                and len(sel) == 2 and sel[0] == T and pos.dtype is _I32 and pos.get_device() == dev
-                and pos.is_contiguous()
-                and w.shape == sel and w.dtype is _F32 and w.get_device() == dev and w.is_contiguous()
-                and (shared is None or (shared.shape == (T, N) and shared.dtype is _BF16
-                                        and shared.get_device() == dev and shared.is_contiguous())))
-    except _AMISS:
-        fits = False
-    if not fits:
+    rc = _FAST.combine(rows, pos, w, y, shared, _handle(stream))
+    if rc == _LOOK:
         T, N = _matrix(y, "y")
-        _expect_rows(rows, "rows", _ACT_TYPES, N)
-        _expect(rows, "rows", rows.dtype, (rows.shape[0], N))
-        want = (T, _matrix(pos, "pos")[1])
-        _expect(pos, "pos", _I32, want)
-        _expect(w, "w", _F32, want)
-        _refuse("combine", (y, "y", _BF16, (T, N)), (shared, "shared", _BF16, (T, N)))
-    rc = _lib().flint_moe_combine(rows.data_ptr(), kind, n_rows, pos.data_ptr(), w.data_ptr(), T, k, N,
-                                  None if shared is None else shared.data_ptr(), y.data_ptr(),
-                                  _raw_stream(stream, dev))
+        kind, n_rows, _, _ = _expect_rows(rows, "rows", N)
+        k = _matrix(pos, "pos")[1]
+        _expect(rows, "rows", rows.dtype, (n_rows, N))
+        _expect(y, "y", torch.bfloat16, (T, N))
+        _expect(pos, "pos", torch.int32, (T, k))
+        _expect(w, "w", torch.float32, (T, k))
+        if shared is not None:
+            _expect(shared, "shared", torch.bfloat16, (T, N))
+        rc = _lib().flint_moe_combine(rows.data_ptr(), kind, n_rows, pos.data_ptr(), w.data_ptr(), T, k, N,
+                                      _ptr(shared), y.data_ptr(), _stream(stream))
     if rc:
         _check(rc, "flint_moe_combine")
 
