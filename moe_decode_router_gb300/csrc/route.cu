@@ -593,11 +593,11 @@ __global__ void __launch_bounds__(128) route_kernel(const RouteParams p) {
 // second pass over the stretch hands the places out in order.  No atomic
 // decides an order, so the result is the same on every call.
 //
-// Latency bound: the bytes are 12 a pair.  One CTA needs 61 us for 49,152 pairs
-// of 256 experts, eight 8.6 us.  Up to 2,048 pairs one CTA is enough.
+// Bound by latency and by the scattered stores of the order, one line a lane:
+// 49,152 pairs of 256 experts take one CTA 61 us, eight 8.4 us, sixteen 6.6 us.  Up to 2,048 pairs one CTA is enough.
 constexpr int GP_WARPS = 32;
-constexpr int GP_CTAS = 8;
-constexpr int GP_HELD = 8;
+constexpr int GP_CTAS = 16;  // more than the portable 8, within one GPC
+constexpr int GP_HELD = 4;
 
 __global__ void __launch_bounds__(GP_WARPS * 32) group_kernel(const int32_t* __restrict__ ids, int P, int E,
                                                               int32_t* __restrict__ offsets,
@@ -741,8 +741,9 @@ cudaError_t launch_route_epl(const RouteParams& p, bool bf16, cudaStream_t st) {
 constexpr int group_smem(int E) { return (GP_WARPS * E + 2 * E + 1 + GP_WARPS) * 4; }
 
 cudaError_t route_kernels_init() {
-  return cudaFuncSetAttribute(group_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                              group_smem(ROUTE_MAX_E));
+  const cudaError_t e = cudaFuncSetAttribute(group_kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+  if (e != cudaSuccess) return e;
+  return cudaFuncSetAttribute(group_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, group_smem(ROUTE_MAX_E));
 }
 
 cudaError_t launch_route(const RouteSpec& r, const void* logits, bool bf16, long long stride, int T, const float* bias,
