@@ -32,6 +32,7 @@ __device__ __forceinline__ uint32_t ord_key(float f) {
   return b ^ ((uint32_t)((int)b >> 31) | 0x80000000u);
 }
 
+// A lane holds EPL neighbouring experts: lane * EPL + i.
 struct RouteParams {
   const void* logits;
   long long stride;  // elements between rows
@@ -41,6 +42,8 @@ struct RouteParams {
   int T, E, top_k, n_groups, top_groups;
   int softmax, top2, renorm;
   uint32_t recip;  // ceil(2^20 / experts of a group): e * recip >> 20 is expert e's group for e < 1024
+  int group_lanes;  // lanes of a group where that is a power of two, else 0
+  bool wide_loads;  // rows start on 16-byte boundaries
   float scale;
 };
 
@@ -70,7 +73,7 @@ __device__ __forceinline__ F group_scores(const F (&v)[EPL], int lane, int E, in
     F a = -(F)INFINITY, b = -(F)INFINITY;
 #pragma unroll
     for (int i = 0; i < EPL; ++i) {
-      const int e = lane + 32 * i;
+      const int e = lane * EPL + i;
       if (e >= g * size && e < (g + 1) * size) {
         if (v[i] > a) {
           b = a;
@@ -146,7 +149,7 @@ __device__ __forceinline__ void keys_of(const RouteParams& p, const float (&x)[E
                                         F (&key)[EPL]) {
 #pragma unroll
   for (int i = 0; i < EPL; ++i) {
-    const int e = lane + 32 * i;
+    const int e = lane * EPL + i;
     F k = -(F)INFINITY;
     if (x[i] > -INFINITY) {
       k = (p.bias != nullptr && e < p.E) ? s[i] + (F)__ldg(p.bias + e) : (F)x[i];
@@ -161,7 +164,7 @@ template <typename F, int EPL>
 __device__ __forceinline__ void drop_groups(F (&key)[EPL], int lane, int size, uint32_t kept) {
 #pragma unroll
   for (int i = 0; i < EPL; ++i) {
-    const int g = (lane + 32 * i) / size;
+    const int g = (lane * EPL + i) / size;
     if (g >= 32 || !((kept >> g) & 1u)) key[i] = -(F)INFINITY;
   }
 }
@@ -180,7 +183,7 @@ __device__ __forceinline__ void select_best(const F (&key)[EPL], int lane, int n
     for (int i = 0; i < EPL; ++i)
       if (!((taken >> i) & 1u) && key[i] > best) {
         best = key[i];
-        at = lane + 32 * i;
+        at = lane * EPL + i;
       }
 #pragma unroll
     for (int off = 16; off > 0; off >>= 1) {
@@ -192,7 +195,7 @@ __device__ __forceinline__ void select_best(const F (&key)[EPL], int lane, int n
       }
     }
     if (!(best > -(F)INFINITY)) break;
-    if ((at & 31) == lane) taken |= 1u << (at >> 5);
+    if (at / EPL == lane) taken |= 1u << (at % EPL);
     if (lane == k) {
       my_e = at;
       my_key = best;
@@ -230,10 +233,11 @@ __device__ __forceinline__ float ord_value(uint32_t k) {
 
 // fp32 error of a score: a sigmoid's from ex2 (2 units, and its argument's
 // rounding, |x| 2^-24 times s (1 - s) < 0.25 / |x|), one addition and one
-// reciprocal, below 2^-22; a softmax's from the same and a sum of up to 1024
-// terms (32 a lane, 5 steps), below 2^-19.  Twice that is allowed for.
+// reciprocal, below 2^-22, of which twice is allowed for; a softmax's from the
+// same and a sum of up to 1024 terms (32 a lane, 5 steps: 36 roundings), below
+// 2.6e-6 of the row's largest score, of which 3.8e-6 is allowed for.
 constexpr float SIGMOID_ERR = 4.76837158203125e-07f;  // 2^-21
-constexpr float SOFTMAX_ERR = 3.814697265625e-06f;    // 2^-18
+constexpr float SOFTMAX_ERR = 3.814697265625e-06f;    // 2^-18, of the row's largest score
 constexpr float SUM_ERR = 1.1920928955078125e-07f;    // 2^-23, of a sum: two roundings
 
 __device__ __forceinline__ float rcp_approx(float v) {
@@ -242,8 +246,9 @@ __device__ __forceinline__ float rcp_approx(float v) {
   return r;
 }
 
+// Returns the scores' error bound.
 template <int EPL>
-__device__ __forceinline__ void fast_scores(const RouteParams& p, const float (&x)[EPL], float (&s)[EPL]) {
+__device__ __forceinline__ float fast_scores(const RouteParams& p, const float (&x)[EPL], float (&s)[EPL]) {
   if (p.softmax) {
     float m = -INFINITY, z = 0.f;
 #pragma unroll
@@ -259,18 +264,39 @@ __device__ __forceinline__ void fast_scores(const RouteParams& p, const float (&
     const float r = rcp_approx(z);
 #pragma unroll
     for (int i = 0; i < EPL; ++i) s[i] *= r;
-  } else {
-#pragma unroll
-    for (int i = 0; i < EPL; ++i) s[i] = rcp_approx(1.f + __expf(-x[i]));
+    return SOFTMAX_ERR * r;  // the largest score is 1 / z
   }
+#pragma unroll
+  for (int i = 0; i < EPL; ++i) s[i] = rcp_approx(1.f + __expf(-x[i]));
+  return SIGMOID_ERR;
 }
 
-// Decides the groups in fp64 from each group's two best experts (sigmoid scores),
-// one value a lane.  val: the fp32 values' keys.  False where fp32 does not
+// A softmax row's largest logit and the sum of exp(x - largest) in fp64.
+template <int EPL>
+__device__ __noinline__ void softmax_sum_f64(const float (&x)[EPL], float& m, double& z) {
+  m = -INFINITY;
+#pragma unroll
+  for (int i = 0; i < EPL; ++i) m = x[i] > m ? x[i] : m;
+  m = ord_value(redux_max(m > -INFINITY ? ord_key(m) : 0u));
+  z = 0.0;
+#pragma unroll
+  for (int i = 0; i < EPL; ++i)
+    if (x[i] > -INFINITY) z += x[i] == m ? 1.0 : exp((double)x[i] - (double)m);
+#pragma unroll
+  for (int off = 16; off > 0; off >>= 1) z += __shfl_xor_sync(FULL, z, off);
+}
+// One expert's score in fp64; m and z of its row, for a softmax.
+__device__ __forceinline__ double score_f64(const RouteParams& p, float x, float m, double z) {
+  if (p.softmax) return (x == m ? 1.0 : exp((double)x - (double)m)) / z;
+  return 1.0 / (1.0 + exp(-(double)x));
+}
+
+// Decides the groups in fp64 from each group's two best experts, one value a
+// lane.  val: the fp32 values' keys.  False where fp32 does not
 // tell which experts those are, or where there are more than 32.
 template <int EPL>
 __device__ __noinline__ bool refine_groups(const RouteParams& p, const float (&x)[EPL], const uint32_t (&val)[EPL],
-                                           int lane, uint32_t& mask) {
+                                           float err, int lane, uint32_t& mask) {
   const int G = p.n_groups, size = p.E / G, take = p.top2 ? 2 : 1;
   if (G * take > 32) return false;
   int mine = -1;  // expert of lane g * take + j
@@ -282,7 +308,7 @@ __device__ __noinline__ bool refine_groups(const RouteParams& p, const float (&x
       int at = 0;
 #pragma unroll
       for (int i = 0; i < EPL; ++i) {
-        const int e = lane + 32 * i;
+        const int e = lane * EPL + i;
         if (e >= g * size && e < (g + 1) * size && !((done >> i) & 1u) && val[i] > best) {
           best = val[i];
           at = i;
@@ -292,23 +318,25 @@ __device__ __noinline__ bool refine_groups(const RouteParams& p, const float (&x
       if (m == 0u) break;
       const float v = ord_value(m);
       if (j == take) {
-        if (!(last - v > 2.f * SIGMOID_ERR + SUM_ERR * (fabsf(v) + fabsf(last)))) return false;
+        if (!(last - v > 2.f * err + SUM_ERR * (fabsf(v) + fabsf(last)))) return false;
         break;
       }
       last = v;
-      const int e = (int)redux_min(best == m ? (uint32_t)(at * 32 + lane) : 0xFFFFFFFFu);
+      const int e = (int)redux_min(best == m ? (uint32_t)(lane * EPL + at) : 0xFFFFFFFFu);
       if (lane == g * take + j) mine = e;
-      if ((e & 31) == lane) done |= 1u << at;
+      if (e / EPL == lane) done |= 1u << at;
     }
   }
   float mx = 0.f;
 #pragma unroll
   for (int i = 0; i < EPL; ++i) {
-    const float o = __shfl_sync(FULL, x[i], mine & 31);
-    if ((mine >> 5) == i) mx = o;
+    const float o = __shfl_sync(FULL, x[i], mine / EPL);
+    if (mine % EPL == i) mx = o;
   }
-  double v = -INFINITY;
-  if (mine >= 0) v = 1.0 / (1.0 + exp(-(double)mx)) + (p.bias != nullptr ? (double)__ldg(p.bias + mine) : 0.0);
+  float m = 0.f;
+  double z = 1.0, v = -INFINITY;
+  if (p.softmax) softmax_sum_f64<EPL>(x, m, z);
+  if (mine >= 0) v = score_f64(p, mx, m, z) + (p.bias != nullptr ? (double)__ldg(p.bias + mine) : 0.0);
   const double first = __shfl_sync(FULL, v, (lane * take) & 31), second = __shfl_sync(FULL, v, (lane * take + 1) & 31);
   double score = lane < G ? first : -INFINITY;
   if (lane < G && take == 2 && second > -INFINITY) score = first + second;
@@ -317,79 +345,70 @@ __device__ __noinline__ bool refine_groups(const RouteParams& p, const float (&x
   return true;
 }
 
+__device__ __forceinline__ float as_f32(float v) { return v; }
+__device__ __forceinline__ float as_f32(__nv_bfloat16 v) { return __bfloat162float(v); }
+
+// The lane's EPL values of a row of E, `none` beyond it; up to 16 bytes a load
+// where the row is aligned for it.
+template <int EPL, typename V>
+__device__ __forceinline__ void load_experts(const V* row, bool aligned, int lane, int E, float none, float (&x)[EPL]) {
+  constexpr int N = EPL * sizeof(V) < 16 ? EPL : 16 / sizeof(V);  // of a load
+  struct alignas(N * sizeof(V)) Chunk {
+    V v[N];
+  };
+#pragma unroll
+  for (int c = 0; c < EPL; c += N) {
+    const int e = lane * EPL + c;
+    if (aligned && e + N <= E) {
+      const Chunk u = *reinterpret_cast<const Chunk*>(row + e);
+#pragma unroll
+      for (int i = 0; i < N; ++i) x[c + i] = as_f32(u.v[i]);
+    } else {
+#pragma unroll
+      for (int i = 0; i < N; ++i) x[c + i] = e + i < E ? as_f32(row[e + i]) : none;
+    }
+  }
+}
+
 // Selection with fp32 scores: my_e of lane k = the k-th expert (-1: none).
 // False where fp32 does not decide it.
 template <int EPL>
 __device__ __forceinline__ bool route_row_f32(const RouteParams& p, const float (&x)[EPL], int lane, int& my_e) {
   const bool biased = p.bias != nullptr;
-  const float err = p.softmax ? SOFTMAX_ERR : SIGMOID_ERR;
+  float err = 0.f;
   const bool sums = p.n_groups > 1 && p.top2;
-  uint32_t key[EPL];   // choice, 0: not a candidate
+  uint32_t key[EPL];  // choice, 0: not a candidate
   float s[EPL];
-  if (biased || sums) fast_scores<EPL>(p, x, s);
+  if (biased || sums) err = fast_scores<EPL>(p, x, s);
+  if (biased) {
+    float bias[EPL];
+    load_experts<EPL>(p.bias, true, lane, p.E, 0.f, bias);
 #pragma unroll
-  for (int i = 0; i < EPL; ++i) {
-    float k = x[i];
-    const int e = lane + 32 * i;
-    if (biased && e < p.E) k = s[i] + __ldg(p.bias + e);
-    key[i] = (x[i] > -INFINITY && k > -INFINITY) ? ord_key(k) : 0u;
-  }
-  if (p.n_groups > 1) {
-    const int G = p.n_groups, size = p.E / G;
-    uint32_t g1 = 0u, g2 = 0u;  // lane g: group g's two best
-    auto close = [&](int g, uint32_t a, uint32_t b) {  // a, b: this lane's two best of the group
-      const uint32_t m1 = redux_max(a);
-      uint32_t m2 = 0u;
-      if (p.top2) {
-        const uint32_t who = __ballot_sync(FULL, a == m1);
-        m2 = redux_max(lane == __ffs(who) - 1 ? b : a);
-      }
-      if (lane == g) {
-        g1 = m1;
-        g2 = m2;
-      }
-    };
-    uint32_t a = 0u, b = 0u;
-    auto add = [&](uint32_t k) {
-      b = max(b, min(a, k));
-      a = max(a, k);
-    };
-    // the groups' values: the keys, or without a bias the scores to be summed
-    auto value = [&](int i) { return (sums && !biased) ? (key[i] != 0u ? ord_key(s[i]) : 0u) : key[i]; };
-    if (size % 32 == 0) {  // a group is a run of whole registers
-      int left = size / 32, g = 0;
-#pragma unroll
-      for (int i = 0; i < EPL; ++i) {
-        if (g < G) {
-          add(value(i));
-          if (--left == 0) {
-            close(g++, a, b);
-            a = b = 0u;
-            left = size / 32;
-          }
-        }
-      }
-    } else {
-      for (int g = 0; g < G; ++g) {
-        a = b = 0u;
-#pragma unroll
-        for (int i = 0; i < EPL; ++i) {
-          const int e = lane + 32 * i;
-          if (e >= g * size && e < (g + 1) * size) add(value(i));
-        }
-        close(g, a, b);
-      }
+    for (int i = 0; i < EPL; ++i) {
+      const float k = s[i] + bias[i];
+      key[i] = (x[i] > -INFINITY && k > -INFINITY) ? ord_key(k) : 0u;
     }
-    const float score = ord_value(g1) + (g2 != 0u ? ord_value(g2) : 0.f);
+  } else {
+#pragma unroll
+    for (int i = 0; i < EPL; ++i) key[i] = x[i] > -INFINITY ? ord_key(x[i]) : 0u;
+  }
+  // the groups' values: the keys, or without a bias the scores to be summed
+  auto value = [&](int i) { return (sums && !biased) ? (key[i] != 0u ? ord_key(s[i]) : 0u) : key[i]; };
+  const int G = p.n_groups, size = p.E / G;
+  // Which groups stay, from their two best values g1, g2, held by lane `leader`
+  // of group g at g * step; `member` is the lane's own group.
+  auto decide = [&](uint32_t g1, uint32_t g2, int member, int step, uint32_t& mask) -> bool {
+    const bool leader = lane == member * step && member < G;
+    const float score = ord_value(g1) + (p.top2 && g2 != 0u ? ord_value(g2) : 0.f);
     int rank = 0;
     for (int g = 0; g < G; ++g) {
-      const float o = __shfl_sync(FULL, score, g);
-      if (o > score || (o == score && g < lane)) ++rank;
+      const float o = __shfl_sync(FULL, score, g * step);
+      if (o > score || (o == score && g < member)) ++rank;
     }
-    const bool kept = lane < G && rank < p.top_groups;
-    uint32_t mask = __ballot_sync(FULL, kept);
+    const bool kept = leader && rank < p.top_groups;
+    const uint32_t leaders = __ballot_sync(FULL, kept);  // bit g * step
     if (biased || sums) {  // weakest kept group against strongest dropped one
-      const uint32_t k = lane < G && score > -INFINITY ? ord_key(score) : 0u;
+      const uint32_t k = leader && score > -INFINITY ? ord_key(score) : 0u;
       const float lo = ord_value(redux_min(kept ? k : 0xFFFFFFFFu)), hi = ord_value(redux_max(kept ? 0u : k));
       const float tol = 4.f * err + SUM_ERR * (fabsf(lo) + fabsf(hi));
       if (!(hi == -INFINITY || lo - hi > tol)) {
@@ -401,13 +420,43 @@ __device__ __forceinline__ bool route_row_f32(const RouteParams& p, const float 
           val[i] = value(i);
         }
         uint32_t better;
-        if (p.softmax || !refine_groups<EPL>(p, xc, val, lane, better)) return false;
+        if (!refine_groups<EPL>(p, xc, val, err, lane, better)) return false;
         mask = better;
+        return true;
       }
     }
+    mask = 0u;
+    if (step == 1) mask = leaders;
+    else
+      for (int g = 0; g < G; ++g) mask |= ((leaders >> (g * step)) & 1u) << g;
+    return true;
+  };
+  if (G > 1 && p.group_lanes == 0) {  // groups that do not fall on whole lanes
+    uint32_t g1 = 0u, g2 = 0u;        // lane g: group g's two best
+    for (int g = 0; g < G; ++g) {
+      uint32_t a = 0u, b = 0u;
+#pragma unroll
+      for (int i = 0; i < EPL; ++i) {
+        const int e = lane * EPL + i;
+        if (e >= g * size && e < (g + 1) * size) {
+          const uint32_t k = value(i);
+          b = max(b, min(a, k));
+          a = max(a, k);
+        }
+      }
+      const uint32_t m1 = redux_max(a);
+      const uint32_t who = __ballot_sync(FULL, a == m1);
+      const uint32_t m2 = redux_max(lane == __ffs(who) - 1 ? b : a);
+      if (lane == g) {
+        g1 = m1;
+        g2 = m2;
+      }
+    }
+    uint32_t mask;
+    if (!decide(g1, g2, lane, 1, mask)) return false;
 #pragma unroll
     for (int i = 0; i < EPL; ++i) {
-      const uint32_t g = ((uint32_t)(lane + 32 * i) * p.recip) >> 20;
+      const uint32_t g = ((uint32_t)(lane * EPL + i) * p.recip) >> 20;
       if (!((mask >> (g & 31u)) & 1u)) key[i] = 0u;  // beyond the last expert the key is 0 already
     }
   }
@@ -415,18 +464,39 @@ __device__ __forceinline__ bool route_row_f32(const RouteParams& p, const float 
   // The lane's two best; a lane that wins twice looks for its next one among the
   // rest.
   uint32_t best = 0u, second = 0u, done = 0u;
-  int id = lane, id2 = lane;  // their experts
+  int id = lane * EPL, id2 = id;  // their experts
 #pragma unroll
   for (int i = 0; i < EPL; ++i) {
     if (key[i] > best) {
       second = best;
       id2 = id;
       best = key[i];
-      id = lane + 32 * i;
+      id = lane * EPL + i;
     } else if (key[i] > second) {
       second = key[i];
-      id2 = lane + 32 * i;
+      id2 = lane * EPL + i;
     }
+  }
+  if (G > 1 && p.group_lanes != 0) {  // a group is a run of whole lanes
+    uint32_t a = best, b = second;
+    if (sums && !biased) {
+      a = b = 0u;
+#pragma unroll
+      for (int i = 0; i < EPL; ++i) {
+        const uint32_t k = value(i);
+        b = max(b, min(a, k));
+        a = max(a, k);
+      }
+    }
+    for (int off = 1; off < p.group_lanes; off <<= 1) {
+      const uint32_t oa = __shfl_xor_sync(FULL, a, off), ob = __shfl_xor_sync(FULL, b, off);
+      b = max(min(a, oa), max(b, ob));
+      a = max(a, oa);
+    }
+    const int member = (int)(((uint32_t)(lane * EPL) * p.recip) >> 20);
+    uint32_t mask;
+    if (!decide(a, b, member, p.group_lanes, mask)) return false;
+    if (!((mask >> (member & 31)) & 1u)) best = second = 0u;  // never picked, so its keys are not looked at again
   }
   my_e = -1;
   uint32_t my_key = 0u;
@@ -440,7 +510,7 @@ __device__ __forceinline__ bool route_row_f32(const RouteParams& p, const float 
     ++n;
     const bool won = e == id && best == m;
     if (won) {
-      done |= 1u << (id >> 5);
+      done |= 1u << (id % EPL);
       best = second;
       id = id2;
       second = 0u;
@@ -452,7 +522,7 @@ __device__ __forceinline__ bool route_row_f32(const RouteParams& p, const float 
           const uint32_t k = ((done >> i) & 1u) ? 0u : key[i];
           if (k > best) {
             best = k;
-            id = lane + 32 * i;
+            id = lane * EPL + i;
           }
         }
       }
@@ -482,16 +552,23 @@ __device__ __forceinline__ bool route_row_f32(const RouteParams& p, const float 
     float mx = 0.f;
 #pragma unroll
     for (int i = 0; i < EPL; ++i) {
-      const float o = __shfl_sync(FULL, x[i], my_e & 31);
-      if ((my_e >> 5) == i) mx = o;
+      const float o = __shfl_sync(FULL, x[i], (uint32_t)my_e / EPL);
+      if ((uint32_t)my_e % EPL == i) mx = o;
     }
     const float nx = __shfl_down_sync(FULL, mx, 1);
     const bool apart = v - nv > 2.f * err + SUM_ERR * (fabsf(v) + fabsf(nv)) || (mx == nx && bias == nb);
     if (!__all_sync(FULL, lane + 1 >= n || apart)) {
-      if (p.softmax || n == 32) return false;  // needs the row's sum, or more candidates
+      if (n == 32) return false;  // more candidates than lanes
       // the candidates, one a lane, in fp64, and their order
-      double k = -INFINITY;
-      if (lane < n) k = 1.0 / (1.0 + exp(-(double)mx)) + (double)bias;
+      float top = 0.f;
+      double z = 1.0, k = -INFINITY;
+      if (p.softmax) {
+        float xc[EPL];
+#pragma unroll
+        for (int i = 0; i < EPL; ++i) xc[i] = x[i];
+        softmax_sum_f64<EPL>(xc, top, z);
+      }
+      if (lane < n) k = score_f64(p, mx, top, z) + (double)bias;
       int rank = 0, first = -1;
       for (int j = 0; j < n; ++j) {
         const double o = __shfl_sync(FULL, k, j);
@@ -517,16 +594,9 @@ __global__ void __launch_bounds__(128) route_kernel(const RouteParams p) {
   const int t = blockIdx.x * 4 + (threadIdx.x >> 5);
   if (t >= p.T) return;
   float x[EPL];
-#pragma unroll
-  for (int i = 0; i < EPL; ++i) {
-    const int e = lane + 32 * i;
-    x[i] = -INFINITY;
-    if (e < p.E) {
-      const size_t at = (size_t)t * (size_t)p.stride + (size_t)e;
-      x[i] = BF16 ? __bfloat162float(static_cast<const __nv_bfloat16*>(p.logits)[at])
-                  : static_cast<const float*>(p.logits)[at];
-    }
-  }
+  const size_t row = (size_t)t * (size_t)p.stride;
+  if (BF16) load_experts<EPL>(static_cast<const __nv_bfloat16*>(p.logits) + row, p.wide_loads, lane, p.E, -INFINITY, x);
+  else load_experts<EPL>(static_cast<const float*>(p.logits) + row, p.wide_loads, lane, p.E, -INFINITY, x);
   int my_e;
   if (!route_row_f32<EPL>(p, x, lane, my_e)) {
     float xc[EPL];
@@ -543,8 +613,8 @@ __global__ void __launch_bounds__(128) route_kernel(const RouteParams p) {
   float xs = -INFINITY;
 #pragma unroll
   for (int i = 0; i < EPL; ++i) {
-    const float v = __shfl_sync(FULL, x[i], my_e & 31);
-    if (my_e >= 0 && (my_e >> 5) == i) xs = v;
+    const float v = __shfl_sync(FULL, x[i], (uint32_t)my_e / EPL);
+    if (my_e >= 0 && (uint32_t)my_e % EPL == i) xs = v;
   }
   const bool on = my_e >= 0;
   float ref = on ? (p.softmax ? xs : fminf(xs, 0.f)) : -INFINITY;
@@ -722,7 +792,10 @@ __global__ void __launch_bounds__(GP_WARPS * 32) group_kernel(const int32_t* __r
 }
 
 template <int EPL>
-cudaError_t launch_route_epl(const RouteParams& p, bool bf16, cudaStream_t st) {
+cudaError_t launch_route_epl(RouteParams p, bool bf16, cudaStream_t st) {
+  const int size = p.E / p.n_groups, lanes = size % EPL == 0 ? size / EPL : 0;
+  p.group_lanes = (lanes & (lanes - 1)) == 0 ? lanes : 0;
+  p.wide_loads = p.stride * (bf16 ? 2 : 4) % 16 == 0;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)((p.T + 3) / 4));
   cfg.blockDim = dim3(128);
