@@ -77,12 +77,20 @@ bool to_stream(PyObject* o, int device, flint_moe_stream_t* st) {
   return true;
 }
 
+// Without the interpreter's lock while it lives; an exception (a tensor without
+// storage has no data pointer) takes the lock again on its way out.
+struct Unlocked {
+  PyThreadState* state = PyEval_SaveThread();
+  ~Unlocked() { PyEval_RestoreThread(state); }
+};
+
 template <typename F>
 PyObject* call(F&& f) {
   int rc;
-  Py_BEGIN_ALLOW_THREADS
-  rc = f();
-  Py_END_ALLOW_THREADS
+  {
+    Unlocked unlocked;
+    rc = f();
+  }
   return status(rc);
 }
 

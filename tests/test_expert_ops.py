@@ -737,3 +737,30 @@ def test_binding_refuses_what_it_can_see():
         F.block_gemm(None, None, z(1, 128, 128), None, z(4, 64))
     with pytest.raises(ValueError, match="rows: shape"):
         F.combine(z(4, 64), ids, w, z(4, 128, dtype=torch.bfloat16))
+
+
+@gpu
+def test_binding_refuses_tensors_without_storage():
+    """A tensor of the right kind that has no memory raises, from every call, and the
+    interpreter goes on."""
+    from torch._subclasses.fake_tensor import FakeTensorMode
+    d = dev()
+    with FakeTensorMode():
+        def e(*shape, dtype=torch.float32):
+            return torch.empty(shape, dtype=dtype, device=d)
+
+        i32, bf, f8 = torch.int32, torch.bfloat16, torch.float8_e4m3fn
+        ids, w = e(4, 6, dtype=i32), e(4, 6)
+        calls = [
+            lambda: F.route(e(4, 64), ids, w),
+            lambda: F.group_pairs(ids, e(65, dtype=i32), e(24, dtype=i32), e(4, 6, dtype=i32)),
+            lambda: F.quantize_rows(e(4, 256, dtype=bf), e(4, 256, dtype=f8), e(2, 4)),
+            lambda: F.block_gemm(e(4, 256, dtype=f8), e(2, 4), e(1, 128, 256, dtype=f8), e(1, 1, 2), e(4, 128, dtype=bf)),
+            lambda: F.combine(e(24, 128, dtype=bf), ids, w, e(4, 128, dtype=bf)),
+        ]
+        for f in calls:
+            with pytest.raises(RuntimeError):
+                f()
+    x = torch.ones(2, 64, device=d)
+    F.route(x, torch.empty(2, 6, dtype=i32, device=d), torch.empty(2, 6, device=d))
+    torch.cuda.synchronize()
