@@ -411,6 +411,12 @@ def dense_gemv(w: DenseNVFP4, x, y, stream=None):
 _ACT_TYPES = {torch.bfloat16: T_BF16, torch.float32: T_F32}
 
 
+def _counts(t, name):
+    """The C ABI counts in 32 bits, to which ctypes would cut a longer count without a word."""
+    if max(t.shape) > 0x7FFFFFFF:
+        raise ValueError(f"{name}: shape {tuple(t.shape)}, a count of more than 31 bits")
+
+
 def _expect_rows(t, name, width):
     """_expect for a matrix of activations whose rows may lie apart: bf16 or fp32, last
     dimension contiguous, on the current CUDA device.  Returns (type code, rows, columns,
@@ -421,6 +427,7 @@ def _expect_rows(t, name, width):
         raise ValueError(f"{name}: dtype {t.dtype}, expected {' or '.join(str(d) for d in _ACT_TYPES)}")
     if t.dim() != 2 or (width is not None and t.shape[1] != width):
         raise ValueError(f"{name}: shape {tuple(t.shape)}, expected [rows][{'columns' if width is None else width}]")
+    _counts(t, name)
     rows, cols = t.shape
     if t.stride(1) != 1 and cols != 1:
         raise ValueError(f"{name}: the elements of a row must be contiguous")
@@ -434,6 +441,7 @@ def _matrix(t, name):
         raise TypeError(f"{name}: expected a torch.Tensor, got {type(t).__name__}")
     if t.dim() != 2:
         raise ValueError(f"{name}: shape {tuple(t.shape)}, expected a matrix")
+    _counts(t, name)
     return t.shape
 
 
@@ -448,6 +456,10 @@ def route(logits, ids, w, bias=None, score=SCORE_SIGMOID, n_groups=1, top_groups
     rc = _FAST.route(logits, ids, w, bias, score, n_groups, top_groups, group_score, renormalise, scale,
                      _handle(stream))
     if rc == _LOOK:
+        for name, v in (("score", score), ("n_groups", n_groups), ("top_groups", top_groups),
+                        ("group_score", group_score)):
+            if abs(v) > 0x7FFFFFFF:
+                raise ValueError(f"{name}: {v}, more than 31 bits")
         kind, T, E, stride = _expect_rows(logits, "logits", None)
         k = _matrix(ids, "ids")[1]
         _expect(ids, "ids", torch.int32, (T, k))
@@ -469,6 +481,8 @@ def group_pairs(ids, offsets, order, pos, stream=None):
         if not isinstance(ids, torch.Tensor) or not isinstance(offsets, torch.Tensor):
             raise TypeError("ids, offsets: expected a torch.Tensor")
         n, E = ids.numel(), offsets.numel() - 1
+        if max(n, E) > 0x7FFFFFFF:
+            raise ValueError(f"ids, offsets: {n} pairs, {E} experts, a count of more than 31 bits")
         _expect(ids, "ids", torch.int32, ids.shape)
         _expect(offsets, "offsets", torch.int32, (E + 1,))
         _expect(order, "order", torch.int32, (n,))
@@ -510,6 +524,7 @@ def block_gemm(a, a_scales, b, b_scales, y, offsets=None, stream=None):
             raise TypeError(f"b: expected a torch.Tensor, got {type(b).__name__}")
         if b.dim() != 3:
             raise ValueError(f"b: expected [experts][N][K], got shape {tuple(b.shape)}")
+        _counts(b, "b")
         E, N, K = b.shape
         kind, M, _, _ = _expect_rows(y, "y", N)
         kb = -(-K // SCALE_BLOCK)

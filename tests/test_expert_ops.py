@@ -764,3 +764,31 @@ def test_binding_refuses_tensors_without_storage():
     x = torch.ones(2, 64, device=d)
     F.route(x, torch.empty(2, 6, dtype=i32, device=d), torch.empty(2, 6, device=d))
     torch.cuda.synchronize()
+
+
+def test_binding_refuses_counts_beyond_31_bits():
+    """What the C ABI's ints cannot hold raises; cut to 32 bits it would be a small count."""
+    n = (1 << 32) + 4
+
+    def m(*shape, dtype=torch.float32):
+        return torch.empty(shape, dtype=dtype, device="meta")
+
+    i32, f8 = torch.int32, torch.float8_e4m3fn
+    ids, w = torch.zeros(4, 6, dtype=i32), torch.zeros(4, 6)
+    for kw in (dict(score=1 << 32), dict(n_groups=n), dict(top_groups=n), dict(group_score=-(1 << 32))):
+        with pytest.raises(ValueError, match="31 bits"):
+            F.route(torch.zeros(4, 64), ids, w, **kw)
+    with pytest.raises(ValueError, match="logits: .*31 bits"):
+        F.route(m(n, 64), m(n, 6, dtype=i32), m(n, 6))
+    with pytest.raises(ValueError, match="ids, offsets: .*31 bits"):
+        F.group_pairs(m(n, dtype=i32), m(9, dtype=i32), m(n, dtype=i32), m(n, dtype=i32))
+    with pytest.raises(ValueError, match="q: .*31 bits"):
+        F.quantize_rows(m(4, 128), m(n, 128, dtype=f8), m(1, n))
+    with pytest.raises(ValueError, match="x: .*31 bits"):
+        F.quantize_rows(m(n, 128), m(4, 128, dtype=f8), m(1, 4))
+    with pytest.raises(ValueError, match="b: .*31 bits"):
+        F.block_gemm(m(4, 128, dtype=f8), m(1, 4), m(n, 128, 128, dtype=f8), m(n, 1, 1), m(4, 128))
+    with pytest.raises(ValueError, match="y: .*31 bits"):
+        F.block_gemm(m(n, 128, dtype=f8), m(1, n), m(1, 128, 128, dtype=f8), m(1, 1, 1), m(n, 128))
+    with pytest.raises(ValueError, match="rows: .*31 bits"):
+        F.combine(m(n, 128), ids, w, torch.zeros(4, 128, dtype=torch.bfloat16))
