@@ -11,11 +11,16 @@
 // candidates in order in fp64 (about one row in 250 with 256 experts and a
 // bias), or the whole row where that needs more than the candidates.
 //
-// Bound by instructions, some 1,300 a row with groups and bias: a pick is one
+// Bound by instructions, some 1,100 a row with groups and bias: a pick is one
 // redux of the lanes' best keys, one of the indices that have it, and the next
-// best in the lane that owned it (every lane keeps two at hand).  8,191 rows of
-// 256 with 8 groups, bias and 8 picks: 276 us with every score in fp64, 15.4 us
-// this way (the bytes alone: 1.3 us).
+// best in the lane that owned it (every lane keeps two at hand).  A lane's
+// experts are neighbours: the row comes in 16-byte loads, and a group of whole
+// lanes is scored by shuffles among them.  8,191 rows of 256 fp32 with 8 groups,
+// bias and 8 picks: 276 us with every score in fp64, 15.4 us with the experts
+// dealt out one by one, 14.6 us this way (the bytes alone: 1.3 us); 8,192 rows
+// of 256 bf16, softmax, no groups: 8.4 us.
+#include <type_traits>
+
 #include "flint_common.cuh"
 #include "flint_internal.h"
 
@@ -372,8 +377,9 @@ __device__ __forceinline__ void load_experts(const V* row, bool aligned, int lan
 
 // Selection with fp32 scores: my_e of lane k = the k-th expert (-1: none).
 // False where fp32 does not decide it.
-template <int EPL>
-__device__ __forceinline__ bool route_row_f32(const RouteParams& p, const float (&x)[EPL], int lane, int& my_e) {
+template <int EPL, typename V>
+__device__ __forceinline__ bool route_row_f32(const RouteParams& p, const float (&x)[EPL], const V* row, int lane,
+                                              int& my_e) {
   const bool biased = p.bias != nullptr;
   float err = 0.f;
   const bool sums = p.n_groups > 1 && p.top2;
@@ -395,8 +401,8 @@ __device__ __forceinline__ bool route_row_f32(const RouteParams& p, const float 
   // the groups' values: the keys, or without a bias the scores to be summed
   auto value = [&](int i) { return (sums && !biased) ? (key[i] != 0u ? ord_key(s[i]) : 0u) : key[i]; };
   const int G = p.n_groups, size = p.E / G;
-  // Which groups stay, from their two best values g1, g2, held by lane `leader`
-  // of group g at g * step; `member` is the lane's own group.
+  // Which groups stay (bit g * step of the mask), from their two best values g1,
+  // g2, held by lane `leader` of group g at g * step; `member` is the lane's own group.
   auto decide = [&](uint32_t g1, uint32_t g2, int member, int step, uint32_t& mask) -> bool {
     const bool leader = lane == member * step && member < G;
     const float score = ord_value(g1) + (p.top2 && g2 != 0u ? ord_value(g2) : 0.f);
@@ -421,14 +427,12 @@ __device__ __forceinline__ bool route_row_f32(const RouteParams& p, const float 
         }
         uint32_t better;
         if (!refine_groups<EPL>(p, xc, val, err, lane, better)) return false;
-        mask = better;
+        mask = 0u;
+        for (int g = 0; g < G; ++g) mask |= ((better >> g) & 1u) << (g * step);
         return true;
       }
     }
-    mask = 0u;
-    if (step == 1) mask = leaders;
-    else
-      for (int g = 0; g < G; ++g) mask |= ((leaders >> (g * step)) & 1u) << g;
+    mask = leaders;
     return true;
   };
   if (G > 1 && p.group_lanes == 0) {  // groups that do not fall on whole lanes
@@ -496,7 +500,7 @@ __device__ __forceinline__ bool route_row_f32(const RouteParams& p, const float 
     const int member = (int)(((uint32_t)(lane * EPL) * p.recip) >> 20);
     uint32_t mask;
     if (!decide(a, b, member, p.group_lanes, mask)) return false;
-    if (!((mask >> (member & 31)) & 1u)) best = second = 0u;  // never picked, so its keys are not looked at again
+    if (!((mask >> ((member * p.group_lanes) & 31)) & 1u)) best = second = 0u;  // never picked, so its keys are not looked at again
   }
   my_e = -1;
   uint32_t my_key = 0u;
@@ -549,12 +553,7 @@ __device__ __forceinline__ bool route_row_f32(const RouteParams& p, const float 
     // they are the same number: the same logit with the same bias.
     const float v = ord_value(my_key), nv = __shfl_down_sync(FULL, v, 1);
     const float bias = my_e >= 0 ? __ldg(p.bias + my_e) : 0.f, nb = __shfl_down_sync(FULL, bias, 1);
-    float mx = 0.f;
-#pragma unroll
-    for (int i = 0; i < EPL; ++i) {
-      const float o = __shfl_sync(FULL, x[i], (uint32_t)my_e / EPL);
-      if ((uint32_t)my_e % EPL == i) mx = o;
-    }
+    const float mx = my_e >= 0 ? as_f32(row[my_e]) : 0.f;  // again, from the L1
     const float nx = __shfl_down_sync(FULL, mx, 1);
     const bool apart = v - nv > 2.f * err + SUM_ERR * (fabsf(v) + fabsf(nv)) || (mx == nx && bias == nb);
     if (!__all_sync(FULL, lane + 1 >= n || apart)) {
@@ -594,11 +593,11 @@ __global__ void __launch_bounds__(128) route_kernel(const RouteParams p) {
   const int t = blockIdx.x * 4 + (threadIdx.x >> 5);
   if (t >= p.T) return;
   float x[EPL];
-  const size_t row = (size_t)t * (size_t)p.stride;
-  if (BF16) load_experts<EPL>(static_cast<const __nv_bfloat16*>(p.logits) + row, p.wide_loads, lane, p.E, -INFINITY, x);
-  else load_experts<EPL>(static_cast<const float*>(p.logits) + row, p.wide_loads, lane, p.E, -INFINITY, x);
+  using V = typename std::conditional<BF16, __nv_bfloat16, float>::type;
+  const V* row = static_cast<const V*>(p.logits) + (size_t)t * (size_t)p.stride;
+  load_experts<EPL>(row, p.wide_loads, lane, p.E, -INFINITY, x);
   int my_e;
-  if (!route_row_f32<EPL>(p, x, lane, my_e)) {
+  if (!route_row_f32<EPL>(p, x, row, lane, my_e)) {
     float xc[EPL];
 #pragma unroll
     for (int i = 0; i < EPL; ++i) xc[i] = x[i];
@@ -610,13 +609,8 @@ __global__ void __launch_bounds__(128) route_kernel(const RouteParams p) {
   // Weights from the selected logits.  u is the score times a factor common to
   // the row that keeps the largest near 1, so that renormalising never divides
   // by zero, however low the logits are.
-  float xs = -INFINITY;
-#pragma unroll
-  for (int i = 0; i < EPL; ++i) {
-    const float v = __shfl_sync(FULL, x[i], (uint32_t)my_e / EPL);
-    if (my_e >= 0 && (uint32_t)my_e % EPL == i) xs = v;
-  }
   const bool on = my_e >= 0;
+  const float xs = on ? as_f32(row[my_e]) : -INFINITY;
   float ref = on ? (p.softmax ? xs : fminf(xs, 0.f)) : -INFINITY;
   if (p.renorm) {
 #pragma unroll
