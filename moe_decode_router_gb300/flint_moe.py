@@ -1,7 +1,8 @@
 """ctypes binding of libflint_moe.so (include/flint_moe.h), same entry-point names.
 
 Argument marshalling only: tensors are passed as device pointers, the stream
-is torch's current CUDA stream unless one is given.  Every computation runs in
+is torch's current CUDA stream unless one is given.  The FP8 expert calls, a few
+microseconds each, are marshalled by compiled code (csrc/binding.cpp) first.  Every computation runs in
 the library's CUDA kernels; there is no fallback path.  If the library cannot
 be built or loaded the import-time call ``load_library`` raises.
 """
