@@ -43,13 +43,16 @@ __device__ __forceinline__ void mma_e4m3(float (&d)[4], uint32_t a0, uint32_t a1
 
 // ---- few rows: weights are streamed once for up to 8 activation rows of one
 // expert.  Grid (M, N / rows of a CTA): the CTA of row r works when r is the
-// first of a run of 8 rows of its expert.  A warp takes 16 weight rows and every
-// SPLIT-th K block of them; SPLIT warps of a CTA share 16 rows, so that a small
-// product has enough warps (SPLIT 8) and a large one few sums across warps
-// (SPLIT 1).  Both operands are read straight from global memory into mma
-// fragments: the product of a block does not depend on the order of k, so lane
-// t of a row's four takes bytes 16t..16t+15 of each half block for either
-// operand.  Two K blocks (4 KB of weights a warp) are under way at a time.
+// first of a run of 8 rows of its expert.  With SPLIT 8 a dense product has CTAs
+// for every eighth row alone (24 rows x 4096 x 2048 7.7 -> 6.8 us against the
+// tcgen05 kernel; SPLIT 1 sees grouped rows only, where this choice alone cost
+// 1.4 of 21 us).  A warp takes 16 weight rows and every SPLIT-th K block of
+// them; SPLIT warps of a CTA share 16 rows, so that a small product has enough
+// warps (SPLIT 8) and a large one few sums across warps (SPLIT 1).  Both operands
+// are read straight from global memory into mma fragments: the product of a
+// block does not depend on the order of k, so lane t of a row's four takes bytes
+// 16t..16t+15 of each half block for either operand.  Two K blocks (4 KB of
+// weights a warp) are under way at a time.
 
 template <int SPLIT, int SK_WARPS, bool F32>
 __global__ void __launch_bounds__(SK_WARPS * 32, 24 / SK_WARPS) block_gemm_skinny_kernel(const GemmArgs p) {
@@ -58,7 +61,7 @@ __global__ void __launch_bounds__(SK_WARPS * 32, 24 / SK_WARPS) block_gemm_skinn
   pdl_wait();
   pdl_trigger();
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  const int r = blockIdx.x;
+  const int r = SPLIT > 1 && p.offsets == nullptr ? blockIdx.x * 8 : blockIdx.x;
   int e = 0, r0 = 0, r1 = p.M;
   if (p.offsets != nullptr) {
     // expert of row r: the last group that starts at or before it; its range: the
@@ -170,7 +173,8 @@ template <int SPLIT, int SK_WARPS, bool F32>
 cudaError_t launch_skinny(const GemmArgs& p, cudaStream_t st) {
   constexpr int ROWS = SK_WARPS / SPLIT * 16;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)p.M, (unsigned)((p.N + ROWS - 1) / ROWS));
+  const bool eighths = SPLIT > 1 && p.offsets == nullptr;
+  cfg.gridDim = dim3((unsigned)(eighths ? (p.M + 7) / 8 : p.M), (unsigned)((p.N + ROWS - 1) / ROWS));
   cfg.blockDim = dim3(SK_WARPS * 32);
   cfg.stream = st;
   cudaLaunchAttribute attr[1];
@@ -894,7 +898,11 @@ cudaError_t launch_block_gemm(const void* a, const float* sa, int M, const void*
   p.nb = (N + 127) / 128;
   // Which kernel, measured (us) on 256 experts of 1024 x 2048, R rows in all, and
   // on one matrix of 4096 x 2048:
-  //   up to 8 rows in all         few-row SPLIT 8  R 8: 8.5, WIDE 9.8
+  //   up to 8 rows in all         few-row SPLIT 8  R 8: 7.9, WIDE 9.5
+  //   dense, passes of 8 rows
+  //   x N up to 14,336            few-row SPLIT 8  24 rows: 6.9, 7.7; 56 of 2048 x 4096: 11.1, 14.1; 192 of 512 x 512: 3.6, 4.3
+  //                                   (a pass reads the weights from L2 at some 8 TB/s; WIDE takes 0.3 us a K block, however
+  //                                   few its units.  Beyond: 32 rows 8.7, 7.7; 80 of 2048 x 4096 15.0, 14.1; 256 of 512 x 512 4.5, 4.3)
   //   33 to 128 rows, at most one
   //   an expert on average        few-row SPLIT 1  R 48: 20.0, WIDE 22.4; R 128: 35.2, 36.2; but R 32: 18.8, 16.6
   //   one wave of WIDE's units,
@@ -904,7 +912,8 @@ cudaError_t launch_block_gemm(const void* a, const float* sa, int M, const void*
   const long long groups = M < E ? M : E;  // that can have rows
   const long long wide_tiles = offsets == nullptr ? (M + WIDE_ROWS - 1) / WIDE_ROWS : M / WIDE_ROWS + groups;
   const long long wide_units = wide_tiles * ((N + WIDE_W - 1) / WIDE_W);
-  if (M <= 8) return f32 ? launch_skinny<8, 8, true>(p, st) : launch_skinny<8, 8, false>(p, st);
+  const bool few = M <= 8 || (offsets == nullptr && (M + 7LL) / 8 * N <= 14336);
+  if (few) return f32 ? launch_skinny<8, 8, true>(p, st) : launch_skinny<8, 8, false>(p, st);
   if (M > 32 && M <= 128 && M <= E) return f32 ? launch_skinny<1, 4, true>(p, st) : launch_skinny<1, 4, false>(p, st);
   if (M <= 36LL * E || wide_units <= sm_count)
     return f32 ? launch_tc<false, true>(p, sm_count, err, st) : launch_tc<false, false>(p, sm_count, err, st);

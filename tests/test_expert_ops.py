@@ -792,3 +792,20 @@ def test_binding_refuses_counts_beyond_31_bits():
         F.block_gemm(m(n, 128, dtype=f8), m(1, n), m(1, 128, 128, dtype=f8), m(1, 1, 1), m(n, 128))
     with pytest.raises(ValueError, match="rows: .*31 bits"):
         F.combine(m(n, 128), ids, w, torch.zeros(4, 128, dtype=torch.bfloat16))
+
+
+@gpu
+@pytest.mark.parametrize("out", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("M,N,K", [(16, 7168, 144), (16, 7176, 144), (41, 2568, 400), (60, 1792, 272), (70, 1640, 272),
+                                   (130, 1032, 1552), (193, 520, 272), (215, 8, 1040)])
+def test_block_gemm_dense_passes(out, M, N, K):
+    """Dense products on either side of what passes of eight rows take."""
+    d = dev()
+    a, sa, b, sb = make_product(M, N, K, 1, M + N + K, d)
+    guard = torch.full((M + 2, N), 7.0, dtype=out, device=d)
+    y = guard[1:-1]
+    F.block_gemm(a, sa, b, sb, y)
+    torch.cuda.synchronize()
+    assert F.device_error() == 0
+    assert bool((guard[0] == 7).all()) and bool((guard[-1] == 7).all())
+    check_product(y, a, sa, b, sb)
