@@ -212,7 +212,11 @@ cudaError_t launch_skinny(const GemmArgs& p, cudaStream_t st) {
 // little more than its weights' bytes.  Scales differ by column: tensor memory
 // is read in 16x256b form, where a thread holds 4 weight rows x pairs of
 // neighbouring columns, so that a pair of column scales, read once from a ring
-// in shared memory, serves 4 packed fma.
+// in shared memory, serves 4 packed fma.  A K block takes a CTA some 0.33 us
+// however few units there are, so where units leave SMs idle KS = 2 or 4 CTAs of
+// a cluster share a unit's K blocks.  Each leaves its partial sums in its own
+// stages, and after a cluster barrier adds its part of the unit's columns over
+// all of them, in the CTAs' order: the result is the same on every call.
 //
 // Warps: 0-7 promotion and output, two column halves; 8 TMA producer; 9 MMA
 // issuer; 10 loader of scales; 11 nothing but its registers.
@@ -304,11 +308,60 @@ __device__ __forceinline__ uint32_t bf16_pair(uint64_t v) {
   return *reinterpret_cast<const uint32_t*>(&h);
 }
 
-template <bool TALL, bool F32>
+// Output of WIDE: `groups` (up to 4, known when unrolled) groups of 8 columns of a
+// warp's half, the first the `first`-th; acc as the promotion warps hold them, from 0.
+template <bool F32>
+__device__ __forceinline__ void wide_output(const TcArgs& p, const TcUnit& t, const uint64_t (&acc)[2][8], int first,
+                                            int groups, uint8_t* out, int quad, int half, int lane) {
+  const int g = lane >> 2, q = lane & 3, nh = t.n >> 1;
+  const int n0 = t.wt * 128 + quad * 32;  // first weight row of the warp
+  if (F32) {
+    float* y = static_cast<float*>(p.y);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const int cl = (first + (i >> 1)) * 8 + 2 * q, col = half * nh + cl;
+      if ((i >> 1) >= groups) break;
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        float v0, v1;
+        f2unpack(acc[h][i], v0, v1);
+        const int n = n0 + 16 * h + (i & 1) * 8 + g;
+        if (n < p.N && cl < nh) {
+          if (col < t.cnt) y[(size_t)(t.row0 + col) * p.N + n] = v0;
+          if (col + 1 < t.cnt) y[(size_t)(t.row0 + col + 1) * p.N + n] = v1;
+        }
+      }
+    }
+  } else {
+    // 8 x 8 transposes on the way into shared memory; four lanes store 32 columns of a row of y
+    uint16_t* y = static_cast<uint16_t*>(p.y);
+    const uint32_t st = smem_u32(out) + (lane & 7) * 80 + (lane >> 3) * 16;  // row lane % 8 of matrix lane / 8
+    const uint4* ld = reinterpret_cast<const uint4*>(out + (lane >> 2) * 80 + (lane & 3) * 16);
+    const int n = n0 + (lane & 3) * 8;
+#pragma unroll
+    for (int k = 0; k < 4; ++k)  // weight rows 0-7, 8-15, 16-23, 24-31 of the warp x 8 rows of y
+      if (k < groups)
+        asm volatile("stmatrix.sync.aligned.m8n8.x4.trans.shared.b16 [%0], {%1, %2, %3, %4};" ::"r"(st + k * 640),
+                     "r"(bf16_pair(acc[0][2 * k])), "r"(bf16_pair(acc[0][2 * k + 1])), "r"(bf16_pair(acc[1][2 * k])),
+                     "r"(bf16_pair(acc[1][2 * k + 1]))
+                     : "memory");
+    __syncwarp();
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const int cl = (first + k) * 8 + (lane >> 2), col = half * nh + cl;
+      if (k < groups && cl < nh && col < t.cnt && n < p.N)
+        *reinterpret_cast<uint4*>(y + (size_t)(t.row0 + col) * p.N + n) = ld[40 * k];
+    }
+    __syncwarp();
+  }
+}
+
+template <bool TALL, bool F32, int KS>
 __global__ void __launch_bounds__(TC_THREADS, 1)
     block_gemm_tc_kernel(const TcArgs p, const __grid_constant__ CUtensorMap map_w,
                          const __grid_constant__ CUtensorMap map_x, const __grid_constant__ CUtensorMap map_y) {
   using C = TcCfg<TALL>;
+  static_assert(KS == 1 || !TALL, "K is split for WIDE alone");
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   uint8_t* sm = smem_raw;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -384,7 +437,12 @@ __global__ void __launch_bounds__(TC_THREADS, 1)
   tc05::fence_after_sync();
   const uint32_t tmem = *tslot;
   const int n_units = g_units[p.E];
-  const int u0 = blockIdx.x / C::CTAS, ustep = gridDim.x / C::CTAS;
+  constexpr int UNIT_CTAS = C::CTAS * KS;
+  // with K split one unit alone, whatever the offsets say
+  const int u0 = blockIdx.x / UNIT_CTAS, ustep = KS > 1 ? 1 << 30 : gridDim.x / UNIT_CTAS;
+  // this CTA's K blocks
+  const int split = KS > 1 ? (int)tc05::cluster_rank() : 0, share = (p.kb + KS - 1) / KS;
+  const int kb_from = KS > 1 ? min(split * share, p.kb) : 0, kb_to = KS > 1 ? min(kb_from + share, p.kb) : p.kb;
 
   auto unit_of = [&](int u) -> TcUnit {
     // The group is the last whose first unit is at or before u: the whole warp
@@ -440,7 +498,7 @@ __global__ void __launch_bounds__(TC_THREADS, 1)
         const TcUnit t = unit_of(u);
         const int boxes = TALL ? 1 : (t.n + 31) >> 5;
         const uint32_t bytes = C::W_BYTES + boxes * C::X_BOX * 128;
-        for (int kb = 0; kb < p.kb && lane == 0; ++kb) {
+        for (int kb = kb_from; kb < kb_to && lane == 0; ++kb) {
           if (!wait(&empty[s], ph ^ 1)) {
             ok = false;
             break;
@@ -492,7 +550,7 @@ __global__ void __launch_bounds__(TC_THREADS, 1)
       for (int u = u0; u < n_units && ok; u += ustep) {
         const TcUnit t = unit_of(u);
         const uint32_t idesc = tc05::idesc_e4m3(128, t.n > 0 ? t.n : 16);
-        for (int kb = 0; kb < p.kb; ++kb, ++g) {
+        for (int kb = kb_from; kb < kb_to; ++kb, ++g) {
           const uint32_t s = g % C::STAGES, ph = (g / C::STAGES) & 1;
           const uint32_t b = g % C::NBUF, bph = ((g / C::NBUF) & 1) ^ 1;
           // every lane looks and waits, and all go on or none
@@ -564,7 +622,7 @@ __global__ void __launch_bounds__(TC_THREADS, 1)
         }
         const int nh = t.n >> 1;
         const float* sb = p.sb + ((size_t)t.e * p.nb + t.wt) * p.kb;
-        for (int kb = 0; kb < p.kb; ++kb) {
+        for (int kb = kb_from; kb < kb_to; ++kb) {
           if (!wait(&sempty[s], ph ^ 1)) {
             ok = false;
             break;
@@ -702,14 +760,14 @@ __global__ void __launch_bounds__(TC_THREADS, 1)
       }
       asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
     } else {
-      const int g = lane >> 2, q = lane & 3;
+      const int q = lane & 3;
       for (int u = u0; u < n_units && ok; u += ustep) {
         const TcUnit t = unit_of(u);
         const int nh = t.n >> 1;
         uint64_t acc[2][8];  // [lane half][4 groups x (row g, row g + 8)]
 #pragma unroll
         for (int i = 0; i < 8; ++i) acc[0][i] = acc[1][i] = 0ull;
-        for (int kb = 0; kb < p.kb; ++kb) {
+        for (int kb = kb_from; kb < kb_to; ++kb) {
           const uint32_t b = v % C::NBUF, bph = (v / C::NBUF) & 1;
           ++v;
           if (!wait(&sfull[s], sph) || !wait(&tfull[b], bph)) {
@@ -743,46 +801,46 @@ __global__ void __launch_bounds__(TC_THREADS, 1)
           }
         }
         if (!ok) break;
-        const int n0 = t.wt * 128 + quad * 32;  // first weight row of the warp
-        if (F32) {
-          float* y = static_cast<float*>(p.y);
+        if constexpr (KS > 1) {
+          // The stages are free: every block of this CTA has landed and been multiplied.
+          uint64_t* part = reinterpret_cast<uint64_t*>(sm) + tid;
 #pragma unroll
-          for (int i = 0; i < 8; ++i) {
-            const int cl = (i >> 1) * 8 + 2 * q, col = half * nh + cl;
+          for (int k = 0; k < 4; ++k)
 #pragma unroll
-            for (int h = 0; h < 2; ++h) {
-              float v0, v1;
-              f2unpack(acc[h][i], v0, v1);
-              const int n = n0 + 16 * h + (i & 1) * 8 + g;
-              if (n < p.N && cl < nh) {
-                if (col < t.cnt) y[(size_t)(t.row0 + col) * p.N + n] = v0;
-                if (col + 1 < t.cnt) y[(size_t)(t.row0 + col + 1) * p.N + n] = v1;
-              }
-            }
-          }
+            for (int j = 0; j < 4; ++j) part[(4 * k + j) * 256] = acc[j >> 1][2 * k + (j & 1)];
         } else {
-          // 8 x 8 transposes on the way into shared memory; four lanes store 32 columns of a row of y
-          uint16_t* y = static_cast<uint16_t*>(p.y);
-          const uint32_t st = smem_u32(out) + (lane & 7) * 80 + (lane >> 3) * 16;  // row lane % 8 of matrix lane / 8
-          const uint4* ld = reinterpret_cast<const uint4*>(out + (lane >> 2) * 80 + (lane & 3) * 16);
-          const int n = n0 + (lane & 3) * 8;
-#pragma unroll
-          for (int k = 0; k < 4; ++k)  // weight rows 0-7, 8-15, 16-23, 24-31 of the warp x 8 rows of y
-            asm volatile("stmatrix.sync.aligned.m8n8.x4.trans.shared.b16 [%0], {%1, %2, %3, %4};" ::"r"(st + k * 640),
-                         "r"(bf16_pair(acc[0][2 * k])), "r"(bf16_pair(acc[0][2 * k + 1])), "r"(bf16_pair(acc[1][2 * k])),
-                         "r"(bf16_pair(acc[1][2 * k + 1]))
-                         : "memory");
-          __syncwarp();
-#pragma unroll
-          for (int k = 0; k < 4; ++k) {
-            const int cl = k * 8 + (lane >> 2), col = half * nh + cl;
-            if (cl < nh && col < t.cnt && n < p.N)
-              *reinterpret_cast<uint4*>(y + (size_t)(t.row0 + col) * p.N + n) = ld[40 * k];
-          }
-          __syncwarp();
+          wide_output<F32>(p, t, acc, 0, 4, out, quad, half, lane);
         }
       }
     }
+  }
+  if constexpr (KS > 1) {
+    // The partial sums, in the order of the CTAs; each CTA puts out 4 / KS of every
+    // warp's four groups of 8 columns.
+    __syncwarp();
+    tc05::cluster_sync();
+    if (warp < 8 && u0 < n_units) {
+      const TcUnit t = unit_of(u0);
+      constexpr int G = 4 / KS;
+      uint64_t v[KS][4 * G], acc[2][8];
+#pragma unroll
+      for (int r = 0; r < KS; ++r) {
+        uint32_t at;
+        asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(at) : "r"(smem_u32(sm) + (split * 4 * G * 256 + tid) * 8), "r"(r));
+#pragma unroll
+        for (int j = 0; j < 4 * G; ++j)
+          asm volatile("ld.shared::cluster.b64 %0, [%1];" : "=l"(v[r][j]) : "r"(at + j * 2048) : "memory");
+      }
+      const uint64_t one = f2pack(1.f, 1.f);
+#pragma unroll
+      for (int r = 1; r < KS; ++r)
+#pragma unroll
+        for (int j = 0; j < 4 * G; ++j) v[0][j] = fma2(v[r][j], one, v[0][j]);
+#pragma unroll
+      for (int j = 0; j < 4 * G; ++j) acc[(j >> 1) & 1][2 * (j >> 2) + (j & 1)] = v[0][j];
+      wide_output<F32>(p, t, acc, split * G, G, sm + C::OFF_OUT + warp * C::OUT_WARP, warp & 3, warp >> 2, lane);
+    }
+    tc05::cluster_sync();  // the other CTAs have read this one's
   }
   __syncwarp();
   tc05::fence_before_sync();
@@ -813,7 +871,7 @@ bool row_map(CUtensorMap* m, const void* base, int size, uint64_t cols, uint64_t
                   CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-template <bool TALL, bool F32>
+template <bool TALL, bool F32, int KS = 1>
 cudaError_t launch_tc(const GemmArgs& p, int sm_count, unsigned* err, cudaStream_t st) {
   using C = TcCfg<TALL>;
   TcArgs t;
@@ -835,10 +893,13 @@ cudaError_t launch_tc(const GemmArgs& p, int sm_count, unsigned* err, cudaStream
       !row_map(&my, p.y, size, p.N, p.M, 0, 32))
     return cudaErrorInvalidValue;
   const long long groups = p.M < p.E ? p.M : p.E;  // that can have rows
-  const long long most = ((long long)p.M / C::ROWS + groups) * t.n_tiles;  // units, at most
-  const int clusters = sm_count / C::CTAS;
+  const long long tiles = p.offsets == nullptr ? (p.M + C::ROWS - 1LL) / C::ROWS : (long long)p.M / C::ROWS + groups;
+  const long long most = tiles * t.n_tiles;  // units, at most
+  constexpr int UNIT_CTAS = C::CTAS * KS;
+  // With K split a cluster takes one unit and no more (its operands' memory holds the partial sums).
+  const long long clusters = KS > 1 ? most : sm_count / C::CTAS;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)(C::CTAS * (most < clusters ? most : clusters)));
+  cfg.gridDim = dim3((unsigned)(UNIT_CTAS * (most < clusters ? most : clusters)));
   cfg.blockDim = dim3(TC_THREADS);
   cfg.dynamicSmemBytes = C::smem(p.E);
   cfg.stream = st;
@@ -846,12 +907,12 @@ cudaError_t launch_tc(const GemmArgs& p, int sm_count, unsigned* err, cudaStream
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   attr[1].id = cudaLaunchAttributeClusterDimension;
-  attr[1].val.clusterDim.x = C::CTAS;
+  attr[1].val.clusterDim.x = UNIT_CTAS;
   attr[1].val.clusterDim.y = 1;
   attr[1].val.clusterDim.z = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 2;
-  return cudaLaunchKernelEx(&cfg, block_gemm_tc_kernel<TALL, F32>, t, mw, mx, my);
+  return cudaLaunchKernelEx(&cfg, block_gemm_tc_kernel<TALL, F32, KS>, t, mw, mx, my);
 }
 
 }  // namespace
@@ -865,11 +926,15 @@ cudaError_t block_gemm_kernels_init() {
     if (q != cudaDriverEntryPointSuccess || fn == nullptr) return cudaErrorNotSupported;
     g_encode = reinterpret_cast<EncodeTiled>(fn);
   }
-  const void* k[4] = {reinterpret_cast<const void*>(block_gemm_tc_kernel<true, false>),
-                      reinterpret_cast<const void*>(block_gemm_tc_kernel<true, true>),
-                      reinterpret_cast<const void*>(block_gemm_tc_kernel<false, false>),
-                      reinterpret_cast<const void*>(block_gemm_tc_kernel<false, true>)};
-  for (int i = 0; i < 4; ++i) {
+  const void* k[] = {reinterpret_cast<const void*>(block_gemm_tc_kernel<true, false, 1>),
+                     reinterpret_cast<const void*>(block_gemm_tc_kernel<true, true, 1>),
+                     reinterpret_cast<const void*>(block_gemm_tc_kernel<false, false, 1>),
+                     reinterpret_cast<const void*>(block_gemm_tc_kernel<false, true, 1>),
+                     reinterpret_cast<const void*>(block_gemm_tc_kernel<false, false, 2>),
+                     reinterpret_cast<const void*>(block_gemm_tc_kernel<false, true, 2>),
+                     reinterpret_cast<const void*>(block_gemm_tc_kernel<false, false, 4>),
+                     reinterpret_cast<const void*>(block_gemm_tc_kernel<false, true, 4>)};
+  for (int i = 0; i < 8; ++i) {
     const int bytes = i < 2 ? TcCfg<true>::smem(ROUTE_MAX_E) : TcCfg<false>::smem(ROUTE_MAX_E);
     cudaError_t e = cudaFuncSetAttribute(k[i], cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
     if (e != cudaSuccess) return e;
@@ -898,11 +963,17 @@ cudaError_t launch_block_gemm(const void* a, const float* sa, int M, const void*
   p.nb = (N + 127) / 128;
   // Which kernel, measured (us) on 256 experts of 1024 x 2048, R rows in all, and
   // on one matrix of 4096 x 2048:
-  //   up to 8 rows in all         few-row SPLIT 8  R 8: 7.9, WIDE 9.5
-  //   dense, passes of 8 rows
-  //   x N up to 14,336            few-row SPLIT 8  24 rows: 6.9, 7.7; 56 of 2048 x 4096: 11.1, 14.1; 192 of 512 x 512: 3.6, 4.3
-  //                                   (a pass reads the weights from L2 at some 8 TB/s; WIDE takes 0.3 us a K block, however
-  //                                   few its units.  Beyond: 32 rows 8.7, 7.7; 80 of 2048 x 4096 15.0, 14.1; 256 of 512 x 512 4.5, 4.3)
+  //   up to 8 grouped rows        few-row SPLIT 8  R 8: 7.9, WIDE 9.5
+  //   up to 8 dense rows, 28 M
+  //   weights                     few-row SPLIT 8  6144 x 4096: 7.2, WIDE in 2 9.6; but 8192 x 8192: 17.9, 16.3
+  //   more dense rows, passes of
+  //   8 x N up to 14,336, x K up
+  //   to 21 M                     few-row SPLIT 8  16 rows: 5.9, WIDE in 4 6.4; 40 of 2048 x 2048 5.9, 6.4; 192 of
+  //                                                512 x 512 3.6, 4.3; but 32 rows: 8.6, 6.4; 80 of 2048 x 1024 6.3, 5.7
+  //   a seventh of the SMs spare
+  //   with 4 CTAs a unit, K from
+  //   8 blocks                    WIDE in 4        32 rows: 6.4, in 2 7.4, whole 7.7; 64 of 2048 x 8192: 10.8, 15.9, 24.8
+  //   2 CTAs a unit, 12 blocks    WIDE in 2        64 of 4096 x 4096: 10.7, whole 14.2; but 128 of 2048 x 1024 6.3, 6.0
   //   33 to 128 rows, at most one
   //   an expert on average        few-row SPLIT 1  R 48: 20.0, WIDE 22.4; R 128: 35.2, 36.2; but R 32: 18.8, 16.6
   //   one wave of WIDE's units,
@@ -912,9 +983,17 @@ cudaError_t launch_block_gemm(const void* a, const float* sa, int M, const void*
   const long long groups = M < E ? M : E;  // that can have rows
   const long long wide_tiles = offsets == nullptr ? (M + WIDE_ROWS - 1) / WIDE_ROWS : M / WIDE_ROWS + groups;
   const long long wide_units = wide_tiles * ((N + WIDE_W - 1) / WIDE_W);
-  const bool few = M <= 8 || (offsets == nullptr && (M + 7LL) / 8 * N <= 14336);
+  const long long passes = (M + 7) / 8;
+  bool few;
+  if (offsets != nullptr) few = M <= 8;
+  else if (passes == 1) few = (long long)N * K <= 28 << 20;
+  else few = passes * N <= 14336 && passes * N * K <= 21 << 20;
   if (few) return f32 ? launch_skinny<8, 8, true>(p, st) : launch_skinny<8, 8, false>(p, st);
   if (M > 32 && M <= 128 && M <= E) return f32 ? launch_skinny<1, 4, true>(p, st) : launch_skinny<1, 4, false>(p, st);
+  if (p.kb >= 8 && 4 * wide_units <= 7 * sm_count / 8)
+    return f32 ? launch_tc<false, true, 4>(p, sm_count, err, st) : launch_tc<false, false, 4>(p, sm_count, err, st);
+  if (p.kb >= 12 && 2 * wide_units <= sm_count)
+    return f32 ? launch_tc<false, true, 2>(p, sm_count, err, st) : launch_tc<false, false, 2>(p, sm_count, err, st);
   if (M <= 36LL * E || wide_units <= sm_count)
     return f32 ? launch_tc<false, true>(p, sm_count, err, st) : launch_tc<false, false>(p, sm_count, err, st);
   return f32 ? launch_tc<true, true>(p, sm_count, err, st) : launch_tc<true, false>(p, sm_count, err, st);

@@ -809,3 +809,63 @@ def test_block_gemm_dense_passes(out, M, N, K):
     assert F.device_error() == 0
     assert bool((guard[0] == 7).all()) and bool((guard[-1] == 7).all())
     check_product(y, a, sa, b, sb)
+
+
+@gpu
+@pytest.mark.parametrize("out", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("counts,N,K", [
+    ([70], 1640, 1040),   # 9 blocks: three CTAs of three and one of none
+    ([130], 1032, 1552),  # 13 blocks
+    ([41], 2600, 1536),
+    ([64], 4096, 1024),   # 8 blocks
+    ([100], 2568, 2064),  # 17 blocks between two CTAs
+    ([8], 8192, 4112),
+    ([0, 33, 0, 37], 520, 1168),
+    ([5, 0, 65, 30], 1032, 1552),
+])
+def test_block_gemm_split_sums(out, counts, N, K):
+    """Products with too few units for the SMs, whose K blocks several blocks share; rows
+    behind and between stay as they were, and a second call gives the same bits."""
+    d = dev()
+    E, M = len(counts), sum(counts)
+    behind = 3 if E > 1 else 0
+    a, sa, b, sb = make_product(M + behind, N, K, E, M + N + K, d)
+    offsets = None if E == 1 else torch.tensor([0] + list(np.cumsum(counts)), dtype=torch.int32, device=d)
+    before = torch.randn(M + behind + 2, N, generator=gen(5)).to(out).to(d)
+    ys = []
+    for _ in range(2):
+        guard = before.clone()
+        F.block_gemm(a, sa, b, sb, guard[1:-1], offsets=offsets)
+        torch.cuda.synchronize()
+        assert F.device_error() == 0
+        assert torch.equal(guard[0], before[0]) and torch.equal(guard[-1], before[-1])
+        ys.append(guard[1:-1])
+    check_product(ys[0], a, sa, b, sb, None if offsets is None else offsets.cpu().numpy(), before[1:-1])
+    assert torch.equal(ys[0], ys[1])
+
+
+@gpu
+def test_block_gemm_split_sums_at_once():
+    """Captured and replayed on two streams at a time, each with its own inputs."""
+    d = dev()
+    ins = [make_product(48, 2048, 2560, 1, i, d) for i in range(2)]
+    want = [torch.empty(48, 2048, device=d) for _ in ins]
+    got = [torch.zeros(48, 2048, device=d) for _ in ins]
+    for i, y in zip(ins, want):
+        F.block_gemm(*i, y)
+    torch.cuda.synchronize()
+    streams, graphs = [torch.cuda.Stream() for _ in ins], []
+    for st, i, y in zip(streams, ins, got):
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g, stream=st):
+            for _ in range(8):
+                F.block_gemm(*i, y)
+        graphs.append(g)
+    for _ in range(5):
+        for st, g in zip(streams, graphs):
+            with torch.cuda.stream(st):
+                g.replay()
+    torch.cuda.synchronize()
+    assert F.device_error() == 0
+    for y, w in zip(got, want):
+        assert torch.equal(y, w)
