@@ -243,7 +243,7 @@ __device__ __forceinline__ float ord_value(uint32_t k) {
 // 2.6e-6 of the row's largest score, of which 3.8e-6 is allowed for.
 constexpr float SIGMOID_ERR = 4.76837158203125e-07f;  // 2^-21
 constexpr float SOFTMAX_ERR = 3.814697265625e-06f;    // 2^-18, of the row's largest score
-constexpr float SUM_ERR = 1.1920928955078125e-07f;    // 2^-23, of a sum: two roundings
+constexpr float SUM_ERR = 1.1920928955078125e-07f;    // 2^-23: two roundings
 
 __device__ __forceinline__ float rcp_approx(float v) {
   float r;
@@ -405,7 +405,7 @@ __device__ __forceinline__ bool route_row_f32(const RouteParams& p, const float 
   // g2, held by lane `leader` of group g at g * step; `member` is the lane's own group.
   auto decide = [&](uint32_t g1, uint32_t g2, int member, int step, uint32_t& mask) -> bool {
     const bool leader = lane == member * step && member < G;
-    const float score = ord_value(g1) + (p.top2 && g2 != 0u ? ord_value(g2) : 0.f);
+    const float v1 = ord_value(g1), v2 = p.top2 && g2 != 0u ? ord_value(g2) : 0.f, score = v1 + v2;
     int rank = 0;
     for (int g = 0; g < G; ++g) {
       const float o = __shfl_sync(FULL, score, g * step);
@@ -413,11 +413,15 @@ __device__ __forceinline__ bool route_row_f32(const RouteParams& p, const float 
     }
     const bool kept = leader && rank < p.top_groups;
     const uint32_t leaders = __ballot_sync(FULL, kept);  // bit g * step
-    if (biased || sums) {  // weakest kept group against strongest dropped one
-      const uint32_t k = leader && score > -INFINITY ? ord_key(score) : 0u;
-      const float lo = ord_value(redux_min(kept ? k : 0xFFFFFFFFu)), hi = ord_value(redux_max(kept ? 0u : k));
-      const float tol = 4.f * err + SUM_ERR * (fabsf(lo) + fabsf(hi));
-      if (!(hi == -INFINITY || lo - hi > tol)) {
+    if (biased || sums) {  // weakest kept group against strongest dropped one, each at its error's far end
+      // Both keys' errors and roundings, the sum's and this one's: by the size of the
+      // keys, which may nearly cancel.
+      const float tol = 2.f * err + 1.5f * SUM_ERR * (fabsf(v1) + fabsf(v2));
+      const bool some = leader && score > -INFINITY;
+      const uint32_t low = some ? ord_key(fmaxf(score - tol, -INFINITY)) : 0u;  // fmaxf, fminf: NaN of two infinities
+      const uint32_t high = some ? ord_key(fminf(score + tol, INFINITY)) : 0u;
+      const uint32_t lo = redux_min(kept ? low : 0xFFFFFFFFu), hi = redux_max(kept ? 0u : high);
+      if (hi != 0u && lo <= hi) {
         float xc[EPL];  // copies: what a call takes by address does not stay in registers
         uint32_t val[EPL];
 #pragma unroll

@@ -1,0 +1,44 @@
+"""Inputs of the FP8 expert operators where a shortcut can go wrong: routing rows whose
+fp32 scores do not decide.
+
+References and tolerances as in test_expert_ops.py.
+"""
+
+import numpy as np
+import pytest
+import torch
+
+import test_expert_ops as X
+from test_expert_ops import check_route, dev, gen, gpu
+
+# ------------------------------------------------------------------ groups whose two best cancel
+
+
+@gpu
+@pytest.mark.parametrize("softmax", [False, True])
+def test_route_group_sum_cancels(softmax):
+    """Two keys of opposite sign leave a small sum; what fp32 lost in the keys is as large as
+    the difference between the groups."""
+    d = dev()
+    x = torch.tensor([[-0.80, 0.58, 0.37, -0.58]], device=d)
+    b = torch.tensor([1e4, -1e4, 0.0, 0.0], device=d)
+    check_route(x, 2, bias=b, softmax=softmax, n_groups=2, top_groups=1, top2=True)
+
+
+@gpu
+@pytest.mark.parametrize("softmax", [False, True])
+@pytest.mark.parametrize("size", [4.0, 64.0, 1e4, 1e8])
+@pytest.mark.parametrize("E,G,top,k", [(16, 8, 3, 4), (256, 8, 4, 8), (160, 8, 3, 6), (96, 4, 1, 5), (64, 32, 3, 6)])
+def test_route_biases_of_both_signs(softmax, size, E, G, top, k):
+    """Every group has one expert forced by a large bias, one let through by its negative and
+    the rest forbidden, so that each group's sum is that of two scores."""
+    d = dev()
+    T = 400
+    g = gen(E + G)
+    x = (0.02 * torch.randn(T, E, generator=g)).to(d)
+    b = torch.full((G, E // G), -3 * size)
+    b[:, 0], b[:, -1] = size, -size
+    b = b.reshape(-1).to(d)
+    check_route(x, k, bias=b, softmax=softmax, n_groups=G, top_groups=top, top2=True)
+    mixed = (size * torch.randint(-1, 2, (E,), generator=g)).to(d)
+    check_route(x, k, bias=mixed, softmax=softmax, n_groups=G, top_groups=top, top2=True)
