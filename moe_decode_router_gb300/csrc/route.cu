@@ -417,7 +417,7 @@ __device__ __forceinline__ bool route_row_f32(const RouteParams& p, const float 
       // Both keys' errors and roundings, the sum's and this one's: by the size of the
       // keys, which may nearly cancel.
       const float tol = 2.f * err + 1.5f * SUM_ERR * (fabsf(v1) + fabsf(v2));
-      const bool some = leader && score > -INFINITY;
+      const bool some = leader && g1 != 0u;  // a group with candidates, also where their sum is beyond fp32
       const uint32_t low = some ? ord_key(fmaxf(score - tol, -INFINITY)) : 0u;  // fmaxf, fminf: NaN of two infinities
       const uint32_t high = some ? ord_key(fminf(score + tol, INFINITY)) : 0u;
       const uint32_t lo = redux_min(kept ? low : 0xFFFFFFFFu), hi = redux_max(kept ? 0u : high);

@@ -42,3 +42,23 @@ def test_route_biases_of_both_signs(softmax, size, E, G, top, k):
     check_route(x, k, bias=b, softmax=softmax, n_groups=G, top_groups=top, top2=True)
     mixed = (size * torch.randint(-1, 2, (E,), generator=g)).to(d)
     check_route(x, k, bias=mixed, softmax=softmax, n_groups=G, top_groups=top, top2=True)
+
+
+@gpu
+@pytest.mark.parametrize("softmax", [False, True])
+@pytest.mark.parametrize("E,G", [(16, 2), (64, 8), (160, 8)])
+def test_route_group_sum_beyond_fp32(softmax, E, G):
+    """Biases of the type's lowest value: the sum of two lies beyond fp32, but the group still
+    has candidates and comes before one that has none."""
+    d = dev()
+    low = torch.finfo(torch.float32).min
+    size = E // G
+    x = torch.randn(6, E, generator=gen(E))
+    b = torch.full((E,), low)
+    x[0, :size] = -float("inf")           # group 0 has no candidate
+    x[1, :(G - 1) * size] = -float("inf")  # only the last group has
+    x[2, size:] = float("nan")             # only the first has
+    check_route(x.to(d), 2, bias=b.to(d), softmax=softmax, n_groups=G, top_groups=1, top2=True)
+    b[-size:] = low / 2 * 1.5              # the last group's sum is the larger one, both beyond fp32
+    check_route(x.to(d), 2, bias=b.to(d), softmax=softmax, n_groups=G, top_groups=1, top2=True)
+    check_route(x.to(d), 2, bias=-b.to(d), softmax=softmax, n_groups=G, top_groups=1, top2=True)
