@@ -552,6 +552,20 @@ __device__ __forceinline__ bool route_row_f32(const RouteParams& p, const float 
       pick(m);
       m = redux_max(best);
     }
+    if (n == 32 && m != 0u) {
+      // More candidates than lanes.  What is left in reach is in its place behind
+      // the picks only where it is the same number as the last one that counts.
+      const int le = __shfl_sync(FULL, my_e, p.top_k - 1);
+      const float lx = as_f32(row[le]), lb = __ldg(p.bias + le);
+      bool other = false;
+#pragma unroll
+      for (int i = 0; i < EPL; ++i) {
+        const float v = ord_value(key[i]);
+        if (((done >> i) & 1u) || key[i] == 0u || last - v > 2.f * err + SUM_ERR * (fabsf(v) + fabsf(last))) continue;
+        other |= x[i] != lx || __ldg(p.bias + lane * EPL + i) != lb;
+      }
+      if (__any_sync(FULL, other)) return false;
+    }
   }
   if (biased) {
     // Neighbours in the order must be further apart than their errors, unless

@@ -62,3 +62,42 @@ def test_route_group_sum_beyond_fp32(softmax, E, G):
     b[-size:] = low / 2 * 1.5              # the last group's sum is the larger one, both beyond fp32
     check_route(x.to(d), 2, bias=b.to(d), softmax=softmax, n_groups=G, top_groups=1, top2=True)
     check_route(x.to(d), 2, bias=-b.to(d), softmax=softmax, n_groups=G, top_groups=1, top2=True)
+
+
+# ------------------------------------------------------------------ more equal candidates than lanes
+
+
+@gpu
+@pytest.mark.parametrize("softmax", [False, True])
+@pytest.mark.parametrize("E,odd", [(64, 40), (64, 63), (200, 33), (256, 255), (512, 300), (1024, 1023)])
+def test_route_best_behind_many_equal_ones(softmax, E, odd):
+    """One expert that fp32 cannot tell from the others, and that comes before them, at an index
+    behind the 32 that a warp looks at; by its bias, and by its logit."""
+    d = dev()
+    for k in (1, 8, 16):
+        x, b = torch.zeros(3, E), torch.zeros(E)
+        b[odd] = 1e-9
+        x[1] = 0.75
+        x[2] = -3.0
+        check_route(x.to(d), k, bias=b.to(d), softmax=softmax)
+        check_route(x.to(torch.bfloat16).to(d), k, bias=b.to(d), softmax=softmax)
+        check_route(x.to(d), k, bias=-b.to(d), softmax=softmax)
+        x = torch.zeros(2, E)
+        x[0, odd], x[1, odd] = 1e-9, -1e-9
+        check_route(x.to(d), k, bias=torch.zeros(E, device=d), softmax=softmax)
+
+
+@gpu
+@pytest.mark.parametrize("softmax", [False, True])
+@pytest.mark.parametrize("groups", [(1, 1, False), (4, 2, False), (4, 2, True), (8, 8, True)])
+def test_route_few_distinct_candidates(softmax, groups):
+    """Rows of a handful of values a few times 1e-9 apart, each held by dozens of experts, and
+    rows that are equal throughout."""
+    d = dev()
+    E, T = 256, 64
+    g = gen(13)
+    x = 1e-9 * torch.randint(0, 3, (T, E), generator=g)
+    x[::4] = 0.0
+    b = 1e-9 * (torch.rand(E, generator=g) < 0.02)
+    for bias in (b, torch.zeros(E), 0.5 + torch.zeros(E)):
+        check_route(x.to(d), 8, bias=bias.to(d), softmax=softmax, n_groups=groups[0], top_groups=groups[1], top2=groups[2])
