@@ -945,6 +945,44 @@ cudaError_t block_gemm_kernels_init() {
   return cudaSuccess;
 }
 
+// Which kernel a product takes, measured (us) on 256 experts of 1024 x 2048, R rows in all, and
+// on one matrix of 4096 x 2048:
+//   up to 8 grouped rows        few-row SPLIT 8  R 8: 7.9, WIDE 9.5
+//   up to 8 dense rows, 28 M
+//   weights                     few-row SPLIT 8  6144 x 4096: 7.2, WIDE in 2 9.6; but 8192 x 8192: 17.9, 16.3
+//   more dense rows, passes of
+//   8 x N up to 14,336, x K up
+//   to 21 M                     few-row SPLIT 8  16 rows: 5.9, WIDE in 4 6.4; 40 of 2048 x 2048 5.9, 6.4; 192 of
+//                                                512 x 512 3.6, 4.3; but 32 rows: 8.6, 6.4; 80 of 2048 x 1024 6.3, 5.7
+//   a seventh of the SMs spare
+//   with 4 CTAs a unit, K from
+//   8 blocks                    WIDE in 4        32 rows: 6.4, in 2 7.4, whole 7.7; 64 of 2048 x 8192: 10.8, 15.9, 24.8
+//   2 CTAs a unit, 12 blocks    WIDE in 2        64 of 4096 x 4096: 10.7, whole 14.2; but 128 of 2048 x 1024 6.3, 6.0
+//   33 to 128 rows, at most one
+//   an expert on average        few-row SPLIT 1  R 48: 20.0, WIDE 22.4; R 128: 35.2, 36.2; but R 32: 18.8, 16.6
+//   one wave of WIDE's units,
+//   or 36 rows an expert        WIDE             24 rows each: 89, TALL 93; 256 dense: 9.3, 11.9
+//   else                        TALL             48 rows each: 98, WIDE 107; 512 dense: 12.2, 15.2
+enum GemmKernel { GEMM_FEW_SPLIT, GEMM_FEW, GEMM_WIDE_IN_4, GEMM_WIDE_IN_2, GEMM_WIDE, GEMM_TALL };
+static GemmKernel choose_block_gemm(int M, int N, int K, int E, bool grouped, int sm_count) {
+  constexpr int WIDE_ROWS = TcCfg<false>::ROWS, WIDE_W = TcCfg<false>::WROWS;
+  const int kb = (K + 127) / 128;
+  const long long groups = M < E ? M : E;  // that can have rows
+  const long long wide_tiles = grouped ? M / WIDE_ROWS + groups : (M + WIDE_ROWS - 1) / WIDE_ROWS;
+  const long long wide_units = wide_tiles * ((N + WIDE_W - 1) / WIDE_W);
+  const long long passes = (M + 7) / 8;
+  bool few;
+  if (grouped) few = M <= 8;
+  else if (passes == 1) few = (long long)N * K <= 28 << 20;
+  else few = passes * N <= 14336 && passes * N * K <= 21 << 20;
+  if (few) return GEMM_FEW_SPLIT;
+  if (M > 32 && M <= 128 && M <= E) return GEMM_FEW;
+  if (kb >= 8 && 4 * wide_units <= 7 * sm_count / 8) return GEMM_WIDE_IN_4;
+  if (kb >= 12 && 2 * wide_units <= sm_count) return GEMM_WIDE_IN_2;
+  if (M <= 36LL * E || wide_units <= sm_count) return GEMM_WIDE;
+  return GEMM_TALL;
+}
+
 cudaError_t launch_block_gemm(const void* a, const float* sa, int M, const void* b, const float* sb, int E,
                               const int32_t* offsets, int N, int K, void* y, bool f32, int sm_count, unsigned* err,
                               cudaStream_t st) {
@@ -961,42 +999,24 @@ cudaError_t launch_block_gemm(const void* a, const float* sa, int M, const void*
   p.E = E;
   p.kb = (K + 127) / 128;
   p.nb = (N + 127) / 128;
-  // Which kernel, measured (us) on 256 experts of 1024 x 2048, R rows in all, and
-  // on one matrix of 4096 x 2048:
-  //   up to 8 grouped rows        few-row SPLIT 8  R 8: 7.9, WIDE 9.5
-  //   up to 8 dense rows, 28 M
-  //   weights                     few-row SPLIT 8  6144 x 4096: 7.2, WIDE in 2 9.6; but 8192 x 8192: 17.9, 16.3
-  //   more dense rows, passes of
-  //   8 x N up to 14,336, x K up
-  //   to 21 M                     few-row SPLIT 8  16 rows: 5.9, WIDE in 4 6.4; 40 of 2048 x 2048 5.9, 6.4; 192 of
-  //                                                512 x 512 3.6, 4.3; but 32 rows: 8.6, 6.4; 80 of 2048 x 1024 6.3, 5.7
-  //   a seventh of the SMs spare
-  //   with 4 CTAs a unit, K from
-  //   8 blocks                    WIDE in 4        32 rows: 6.4, in 2 7.4, whole 7.7; 64 of 2048 x 8192: 10.8, 15.9, 24.8
-  //   2 CTAs a unit, 12 blocks    WIDE in 2        64 of 4096 x 4096: 10.7, whole 14.2; but 128 of 2048 x 1024 6.3, 6.0
-  //   33 to 128 rows, at most one
-  //   an expert on average        few-row SPLIT 1  R 48: 20.0, WIDE 22.4; R 128: 35.2, 36.2; but R 32: 18.8, 16.6
-  //   one wave of WIDE's units,
-  //   or 36 rows an expert        WIDE             24 rows each: 89, TALL 93; 256 dense: 9.3, 11.9
-  //   else                        TALL             48 rows each: 98, WIDE 107; 512 dense: 12.2, 15.2
-  constexpr int WIDE_ROWS = TcCfg<false>::ROWS, WIDE_W = TcCfg<false>::WROWS;
-  const long long groups = M < E ? M : E;  // that can have rows
-  const long long wide_tiles = offsets == nullptr ? (M + WIDE_ROWS - 1) / WIDE_ROWS : M / WIDE_ROWS + groups;
-  const long long wide_units = wide_tiles * ((N + WIDE_W - 1) / WIDE_W);
-  const long long passes = (M + 7) / 8;
-  bool few;
-  if (offsets != nullptr) few = M <= 8;
-  else if (passes == 1) few = (long long)N * K <= 28 << 20;
-  else few = passes * N <= 14336 && passes * N * K <= 21 << 20;
-  if (few) return f32 ? launch_skinny<8, 8, true>(p, st) : launch_skinny<8, 8, false>(p, st);
-  if (M > 32 && M <= 128 && M <= E) return f32 ? launch_skinny<1, 4, true>(p, st) : launch_skinny<1, 4, false>(p, st);
-  if (p.kb >= 8 && 4 * wide_units <= 7 * sm_count / 8)
-    return f32 ? launch_tc<false, true, 4>(p, sm_count, err, st) : launch_tc<false, false, 4>(p, sm_count, err, st);
-  if (p.kb >= 12 && 2 * wide_units <= sm_count)
-    return f32 ? launch_tc<false, true, 2>(p, sm_count, err, st) : launch_tc<false, false, 2>(p, sm_count, err, st);
-  if (M <= 36LL * E || wide_units <= sm_count)
-    return f32 ? launch_tc<false, true>(p, sm_count, err, st) : launch_tc<false, false>(p, sm_count, err, st);
-  return f32 ? launch_tc<true, true>(p, sm_count, err, st) : launch_tc<true, false>(p, sm_count, err, st);
+  switch (choose_block_gemm(M, N, K, E, offsets != nullptr, sm_count)) {
+    case GEMM_FEW_SPLIT: return f32 ? launch_skinny<8, 8, true>(p, st) : launch_skinny<8, 8, false>(p, st);
+    case GEMM_FEW: return f32 ? launch_skinny<1, 4, true>(p, st) : launch_skinny<1, 4, false>(p, st);
+    case GEMM_WIDE_IN_4:
+      return f32 ? launch_tc<false, true, 4>(p, sm_count, err, st) : launch_tc<false, false, 4>(p, sm_count, err, st);
+    case GEMM_WIDE_IN_2:
+      return f32 ? launch_tc<false, true, 2>(p, sm_count, err, st) : launch_tc<false, false, 2>(p, sm_count, err, st);
+    case GEMM_WIDE:
+      return f32 ? launch_tc<false, true>(p, sm_count, err, st) : launch_tc<false, false>(p, sm_count, err, st);
+    case GEMM_TALL:
+      return f32 ? launch_tc<true, true>(p, sm_count, err, st) : launch_tc<true, false>(p, sm_count, err, st);
+  }
+  return cudaErrorInvalidValue;
 }
 
 }  // namespace flint
+
+// For the tests: which kernel a product takes on a GPU of so many SMs.
+extern "C" int flint_block_gemm_kernel(int M, int N, int K, int n_experts, int grouped, int sm_count) {
+  return flint::choose_block_gemm(M, N, K, n_experts, grouped != 0, sm_count);
+}
