@@ -202,10 +202,9 @@ cudaError_t launch_skinny(const GemmArgs& p, cudaStream_t st) {
 // all with one scale a K block, the product of the row's and the weight
 // block's: per K block and SM 512 cycles of MMA, 256 of tensor-memory reads
 // (32x32b; the 16-lane forms read at half that rate) and 256 of packed fma,
-// which overlap.  Two CTAs with the same weight tile form a cluster: each
-// loads half of it for both (TMA multicast), 32 KB a K block from L2 per SM.
-// Where a group's last tile has at most 128 rows, both CTAs take those rows, with
-// a weight tile each: half the time that a tile with one idle CTA would take.
+// which overlap.  Every CTA loads its own 48 KB a K block; sharing the weight tile
+// between two CTAs was no faster (8191 x 4096 x 4096 107 us either way, ragged
+// experts 146 shared, 144 alone) and ties their steps together.
 //
 // WIDE (short groups).  128 weight rows are the M side, always full, and up to
 // 64 rows of a the N side in steps of 16, so that a group of few rows costs
@@ -228,8 +227,7 @@ static_assert(TC_REGS_HIGH * 256 + TC_REGS_LOW * 128 <= TC_REGS * TC_THREADS, "r
 
 template <bool TALL>
 struct TcCfg {
-  static constexpr int CTAS = TALL ? 2 : 1;        // of a cluster
-  static constexpr int ROWS = TALL ? 256 : 64;     // rows of a in a unit
+  static constexpr int ROWS = TALL ? 128 : 64;     // rows of a in a unit
   static constexpr int WROWS = TALL ? 256 : 128;   // weight rows in a unit
   static constexpr int ACC = TALL ? 256 : 64;      // columns of an accumulator
   static constexpr int NBUF = 512 / ACC;
@@ -264,9 +262,7 @@ struct TcArgs {
 };
 
 struct TcUnit {
-  int e, wt, row0, cnt, n;  // n: columns of the MMAs, <= 0: none for this CTA
-  int first;                // TALL: this CTA's first row in the tile
-  bool shared;              // TALL: both CTAs have the same rows
+  int e, wt, row0, cnt, n;  // n: columns of the MMAs
 };
 
 __device__ __forceinline__ void tma_2d(uint32_t dst, const CUtensorMap* map, int x, int y, uint64_t* bar) {
@@ -281,14 +277,6 @@ __device__ __forceinline__ void tma_3d(uint32_t dst, const CUtensorMap* map, int
       "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], "
       "[%5];" ::"r"(dst),
       "l"(map), "r"(x), "r"(y), "r"(z), "r"(smem_u32(bar))
-      : "memory");
-}
-// The same box to this offset of both CTAs of the cluster, and its bytes to both CTAs' barriers.
-__device__ __forceinline__ void tma_3d_both(uint32_t dst, const CUtensorMap* map, int x, int y, int z, uint64_t* bar) {
-  asm volatile(
-      "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes.multicast::cluster [%0], [%1, "
-      "{%2, %3, %4}], [%5], %6;" ::"r"(dst),
-      "l"(map), "r"(x), "r"(y), "r"(z), "r"(smem_u32(bar)), "h"((uint16_t)3)
       : "memory");
 }
 __device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
@@ -365,9 +353,8 @@ __global__ void __launch_bounds__(TC_THREADS, 1)
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   uint8_t* sm = smem_raw;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  const int rank = TALL ? (int)tc05::cluster_rank() : 0;
   uint64_t* full = reinterpret_cast<uint64_t*>(sm + C::OFF_BARS);  // [STAGES] operands landed
-  uint64_t* empty = full + C::STAGES;                              // [STAGES] stage consumed, in every CTA of the cluster
+  uint64_t* empty = full + C::STAGES;                              // [STAGES] stage consumed
   uint64_t* tfull = empty + C::STAGES;                             // [NBUF] accumulator complete
   uint64_t* tempty = tfull + C::NBUF;                              // [NBUF] accumulator read
   uint64_t* sfull = tempty + C::NBUF;                              // [SLOTS] scales landed
@@ -386,7 +373,7 @@ __global__ void __launch_bounds__(TC_THREADS, 1)
   if (tid == 0) {
     for (int i = 0; i < C::STAGES; ++i) {
       mbar_init(&full[i], 1);
-      mbar_init(&empty[i], C::CTAS);
+      mbar_init(&empty[i], 1);
     }
     for (int i = 0; i < C::NBUF; ++i) {
       mbar_init(&tfull[i], 1);
@@ -417,8 +404,7 @@ __global__ void __launch_bounds__(TC_THREADS, 1)
         g_cnt[e] = cnt;
       }
       __syncwarp();  // the offsets of these groups make room for their units; the next group's first is read below
-      const int rest = cnt % C::ROWS, tiles = cnt / C::ROWS + (TALL ? rest > 128 : rest > 0);
-      int t = tiles * p.n_tiles + (TALL && rest > 0 && rest <= 128 ? (p.n_tiles + 1) / 2 : 0);
+      int t = (cnt + C::ROWS - 1) / C::ROWS * p.n_tiles;
       if (base > 1 << 29) t = 0;  // offsets that descend could count rows over and over: stay inside int
       int incl = t;
 #pragma unroll
@@ -433,13 +419,11 @@ __global__ void __launch_bounds__(TC_THREADS, 1)
   }
   tc05::fence_before_sync();
   __syncthreads();
-  if (TALL) tc05::cluster_sync();  // the peer's barriers are ready too
   tc05::fence_after_sync();
   const uint32_t tmem = *tslot;
   const int n_units = g_units[p.E];
-  constexpr int UNIT_CTAS = C::CTAS * KS;
   // with K split one unit alone, whatever the offsets say
-  const int u0 = blockIdx.x / UNIT_CTAS, ustep = KS > 1 ? 1 << 30 : gridDim.x / UNIT_CTAS;
+  const int u0 = blockIdx.x / KS, ustep = KS > 1 ? 1 << 30 : gridDim.x;
   // this CTA's K blocks
   const int split = KS > 1 ? (int)tc05::cluster_rank() : 0, share = (p.kb + KS - 1) / KS;
   const int kb_from = KS > 1 ? min(split * share, p.kb) : 0, kb_to = KS > 1 ? min(kb_from + share, p.kb) : p.kb;
@@ -461,17 +445,6 @@ __global__ void __launch_bounds__(TC_THREADS, 1)
       if (tile * p.n_tiles > v) --tile;
     }
     t.wt = v - tile * p.n_tiles;
-    t.first = rank * 128;
-    t.shared = false;
-    if (TALL) {
-      const int whole = cnt / 256 + (cnt % 256 > 128 ? 1 : 0);
-      if (tile >= whole) {
-        t.wt = 2 * (v - whole * p.n_tiles) + rank;
-        tile = whole;
-        t.first = 0;
-        t.shared = true;
-      }
-    }
     t.row0 = g_lo[lo] + tile * C::ROWS;
     t.cnt = min(C::ROWS, cnt - tile * C::ROWS);
     t.n = TALL ? min(256, (p.N - t.wt * 256 + 15) & ~15) : (t.cnt + 15) & ~15;
@@ -506,13 +479,9 @@ __global__ void __launch_bounds__(TC_THREADS, 1)
           mbar_arrive_expect_tx(&full[s], bytes);
           const uint32_t w = smem_u32(sm) + s * C::STAGE, x = w + C::W_BYTES;
           if (TALL) {
-            if (t.shared) {
-              tma_3d(w, &map_w, kb * 128, t.wt * 256, t.e, &full[s]);
-              tma_3d(w + 16384, &map_w, kb * 128, t.wt * 256 + 128, t.e, &full[s]);
-            } else {
-              tma_3d_both(w + rank * 16384, &map_w, kb * 128, t.wt * 256 + rank * 128, t.e, &full[s]);
-            }
-            tma_2d(x, &map_x, kb * 128, t.row0 + t.first, &full[s]);
+            tma_3d(w, &map_w, kb * 128, t.wt * 256, t.e, &full[s]);
+            tma_3d(w + 16384, &map_w, kb * 128, t.wt * 256 + 128, t.e, &full[s]);
+            tma_2d(x, &map_x, kb * 128, t.row0, &full[s]);
           } else {
             tma_3d(w, &map_w, kb * 128, t.wt * 128, t.e, &full[s]);
             for (int i = 0; i < boxes; ++i) tma_2d(x + i * 4096, &map_x, kb * 128, t.row0 + 32 * i, &full[s]);
@@ -528,16 +497,11 @@ __global__ void __launch_bounds__(TC_THREADS, 1)
       if (lane == 0) {
         // Every stage's last phase: normally its release by all MMAs, after
         // which nothing is under way to this CTA; after a wait that ran out,
-        // the arrival of the copies (the peer's may come later: 1 ms covers any).
+        // the arrival of the copies.
         const uint32_t n = issued < (uint32_t)C::STAGES ? issued : (uint32_t)C::STAGES;
         for (uint32_t q = issued - n; q < issued; ++q) {
           if (ok) ok = wait(&empty[q % C::STAGES], (q / C::STAGES) & 1);
           else (void)mbar_wait(&full[q % C::STAGES], (q / C::STAGES) & 1);
-        }
-        if (!ok && TALL) {
-          const long long t0 = clock64();
-          while (clock64() - t0 < 2000000) {
-          }
         }
       }
     } else if (warp == 9) {
@@ -549,7 +513,7 @@ __global__ void __launch_bounds__(TC_THREADS, 1)
       const uint64_t dw0 = tc05::sw128_desc(smem_u32(sm)), dx0 = tc05::sw128_desc(smem_u32(sm) + C::W_BYTES);
       for (int u = u0; u < n_units && ok; u += ustep) {
         const TcUnit t = unit_of(u);
-        const uint32_t idesc = tc05::idesc_e4m3(128, t.n > 0 ? t.n : 16);
+        const uint32_t idesc = tc05::idesc_e4m3(128, t.n);
         for (int kb = kb_from; kb < kb_to; ++kb, ++g) {
           const uint32_t s = g % C::STAGES, ph = (g / C::STAGES) & 1;
           const uint32_t b = g % C::NBUF, bph = ((g / C::NBUF) & 1) ^ 1;
@@ -563,16 +527,13 @@ __global__ void __launch_bounds__(TC_THREADS, 1)
           tc05::fence_after_sync();
           const uint64_t dw = dw0 + (uint64_t)(s * (C::STAGE >> 4)), dx = dx0 + (uint64_t)(s * (C::STAGE >> 4));
           const uint32_t d = tmem + b * C::ACC;
-          if (t.n > 0) {  // else the last of an odd number of weight tiles: nothing but the barriers
 #pragma unroll
-            for (int k = 0; k < 4; ++k) {
-              if (TALL) tc05::mma_e4m3(d, dx + 2 * k, dw + 2 * k, idesc, k > 0 ? 1u : 0u);
-              else tc05::mma_e4m3(d, dw + 2 * k, dx + 2 * k, idesc, k > 0 ? 1u : 0u);
-            }
+          for (int k = 0; k < 4; ++k) {
+            if (TALL) tc05::mma_e4m3(d, dx + 2 * k, dw + 2 * k, idesc, k > 0 ? 1u : 0u);
+            else tc05::mma_e4m3(d, dw + 2 * k, dx + 2 * k, idesc, k > 0 ? 1u : 0u);
           }
           tc05::commit(&tfull[b]);
-          if (TALL) tc05::commit_both(&empty[s]);
-          else tc05::commit(&empty[s]);
+          tc05::commit(&empty[s]);
         }
       }
       if (!ok) {  // what has been issued retires before tensor memory goes
@@ -612,7 +573,7 @@ __global__ void __launch_bounds__(TC_THREADS, 1)
                 const float* sa = p.sa + (size_t)(kb + j) * p.M + t.row0;
 #pragma unroll
                 for (int i = 0; i < 4; ++i)
-                  copy4(slot + j * 128 + i * 32 + lane, sa + min(t.first + i * 32 + lane, last));
+                  copy4(slot + j * 128 + i * 32 + lane, sa + min(i * 32 + lane, last));
                 if (lane < 2) copy4(slot + 512 + j * 2 + lane, sb + kb + j);
               }
             }
@@ -664,7 +625,7 @@ __global__ void __launch_bounds__(TC_THREADS, 1)
     if constexpr (TALL) {
       for (int u = u0; u < n_units && ok; u += ustep) {
         const TcUnit t = unit_of(u);
-        const int row = t.first + quad * 32;         // first of the warp's 32 rows in the tile
+        const int row = quad * 32;                   // first of the warp's 32 rows in the tile
         const int live = t.n > 128 * half ? min(32, t.cnt - row) : 0;  // its rows of a, <= 0: none
         uint64_t acc[64];
 #pragma unroll
@@ -845,7 +806,6 @@ __global__ void __launch_bounds__(TC_THREADS, 1)
   __syncwarp();
   tc05::fence_before_sync();
   __syncthreads();
-  if (TALL) tc05::cluster_sync();  // no arrival or copy is under way to either CTA any more
   if (warp == 8) {
     tc05::fence_after_sync();
     tc05::tmem_dealloc(tmem, 512);
@@ -895,11 +855,10 @@ cudaError_t launch_tc(const GemmArgs& p, int sm_count, unsigned* err, cudaStream
   const long long groups = p.M < p.E ? p.M : p.E;  // that can have rows
   const long long tiles = p.offsets == nullptr ? (p.M + C::ROWS - 1LL) / C::ROWS : (long long)p.M / C::ROWS + groups;
   const long long most = tiles * t.n_tiles;  // units, at most
-  constexpr int UNIT_CTAS = C::CTAS * KS;
   // With K split a cluster takes one unit and no more (its operands' memory holds the partial sums).
-  const long long clusters = KS > 1 ? most : sm_count / C::CTAS;
+  const long long clusters = KS > 1 ? most : sm_count;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)(UNIT_CTAS * (most < clusters ? most : clusters)));
+  cfg.gridDim = dim3((unsigned)(KS * (most < clusters ? most : clusters)));
   cfg.blockDim = dim3(TC_THREADS);
   cfg.dynamicSmemBytes = C::smem(p.E);
   cfg.stream = st;
@@ -907,7 +866,7 @@ cudaError_t launch_tc(const GemmArgs& p, int sm_count, unsigned* err, cudaStream
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   attr[1].id = cudaLaunchAttributeClusterDimension;
-  attr[1].val.clusterDim.x = UNIT_CTAS;
+  attr[1].val.clusterDim.x = KS;
   attr[1].val.clusterDim.y = 1;
   attr[1].val.clusterDim.z = 1;
   cfg.attrs = attr;

@@ -1,7 +1,6 @@
-// Helpers of the block-scaled FP8 product on top of tc05.cuh: clusters of two
-// CTAs, kind::f8f6f4 MMAs, tensor-memory loads whose registers pass through the
-// wait, register shares and a barrier test.  Written from the PTX ISA
-// description.
+// Helpers of the block-scaled FP8 product on top of tc05.cuh: clusters,
+// kind::f8f6f4 MMAs, tensor-memory loads whose registers pass through the wait,
+// register shares and a barrier test.  Written from the PTX ISA description.
 #pragma once
 
 #include <cstdint>
@@ -24,7 +23,7 @@ __device__ __forceinline__ bool mbar_test(uint64_t* bar, uint32_t parity) {
 
 namespace tc05 {
 
-// ---- clusters of two CTAs
+// ---- clusters
 __device__ __forceinline__ uint32_t cluster_rank() {
   uint32_t r;
   asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
@@ -51,18 +50,11 @@ __device__ __forceinline__ void mma_e4m3(uint32_t d_tmem, uint64_t a_desc, uint6
       : "memory");
 }
 // Arrives (once) on an mbarrier when all MMAs that the warp issued that way so
-// far have completed: on this CTA's, or on both CTAs' of the cluster.
+// far have completed.
 __device__ __forceinline__ void commit(uint64_t* bar) {
   asm volatile(
       "{\n .reg .pred e;\n elect.sync _|e, 0xffffffff;\n"
       " @e tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n}\n" ::"r"(smem_u32(bar))
-      : "memory");
-}
-__device__ __forceinline__ void commit_both(uint64_t* bar) {
-  asm volatile(
-      "{\n .reg .pred e;\n elect.sync _|e, 0xffffffff;\n @e tcgen05.commit.cta_group::1.mbarrier::arrive::one"
-      ".shared::cluster.multicast::cluster.b64 [%0], %1;\n}\n" ::"r"(smem_u32(bar)),
-      "h"((uint16_t)3)
       : "memory");
 }
 

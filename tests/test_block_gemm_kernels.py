@@ -3,11 +3,14 @@ them (asserted from the choice itself), with the group lengths, widths and types
 go wrong.  References and tolerances as in test_expert_ops.py.
 """
 
+import os
+
 import numpy as np
 import pytest
 import torch
 
 import expert_ops_reference as R
+from moe_decode_router_gb300 import build as _build
 from moe_decode_router_gb300 import flint_moe as F
 from test_expert_ops import check_product, dev, f64, gen, gpu, make_product
 
@@ -62,6 +65,15 @@ def test_every_kernel_is_chosen():
     assert kernel_of(256, 4096, 2048, sms=152) == WIDE
     assert kernel_of(8191, 4096, 4096, sms=152) == TALL
     assert kernel_of(49152, 1024, 2048, 256, True, 152) == TALL
+
+
+def test_no_copy_goes_to_several_blocks():
+    """Operands are copied into the memory of the block that asks for them and nowhere else, as any
+    caller's weights may lie in another GPU's memory."""
+    word = "multi" + "cast"
+    for name in sorted(os.listdir(_build.CSRC)):
+        with open(os.path.join(_build.CSRC, name)) as f:
+            assert word not in f.read().lower(), name
 
 
 # ------------------------------------------------------------------ long groups
