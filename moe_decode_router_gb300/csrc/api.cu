@@ -43,6 +43,7 @@ struct DeviceState {
   int sm_count = 0;
   int gu_grid = 0;     // three-kernel path: gate/up CTAs
   int fused_grid = 0;  // persistent kernel: one CTA per SM, at most one per router expert
+  int group_most = 0;  // CTAs of the largest cluster that grouping may use
   unsigned* err = nullptr;
   cudaStream_t capture_stream = nullptr;
   std::vector<GraphEntry> graphs;
@@ -94,7 +95,7 @@ int device_state(DeviceState** out) {
     if (dense_kernels_init() != cudaSuccess) return FLINT_MOE_ERR_CUDA;
     if (medium_kernels_init() != cudaSuccess) return FLINT_MOE_ERR_CUDA;
     if (prefill_kernels_init(dev) != cudaSuccess) return FLINT_MOE_ERR_CUDA;
-    if (route_kernels_init() != cudaSuccess) return FLINT_MOE_ERR_CUDA;
+    if (route_kernels_init(&s.group_most) != cudaSuccess) return FLINT_MOE_ERR_CUDA;
     if (block_gemm_kernels_init() != cudaSuccess) return FLINT_MOE_ERR_CUDA;
     if (cudaStreamCreateWithFlags(&s.capture_stream, cudaStreamNonBlocking) != cudaSuccess)
       return FLINT_MOE_ERR_CUDA;
@@ -599,7 +600,8 @@ int flint_moe_group_pairs(const int32_t* ids, int n_pairs, int n_experts, int32_
   int st = device_state(&ds);
   if (st != FLINT_MOE_OK) return st;
   return to_status(
-      launch_group_pairs(ids, n_pairs, n_experts, offsets, order, pos, reinterpret_cast<cudaStream_t>(stream)));
+      launch_group_pairs(ids, n_pairs, n_experts, offsets, order, pos, ds->group_most,
+                         reinterpret_cast<cudaStream_t>(stream)));
 }
 
 int flint_moe_quantize_rows(const void* x, int x_type, long long row_stride, int rows, int K, int silu_mul,

@@ -161,11 +161,11 @@ struct RouteSpec {
   int E, top_k, n_groups, top_groups, softmax, top2, renorm;
   float scale;
 };
-cudaError_t route_kernels_init();
+cudaError_t route_kernels_init(int* group_most);  // CTAs of the largest cluster that grouping may use
 cudaError_t launch_route(const RouteSpec& r, const void* logits, bool bf16, long long stride, int T, const float* bias,
                          int32_t* ids, float* w, cudaStream_t st);
 cudaError_t launch_group_pairs(const int32_t* ids, int P, int E, int32_t* offsets, int32_t* order, int32_t* pos,
-                               cudaStream_t st);
+                               int most, cudaStream_t st);
 
 // Quantisation of rows in blocks of 128, and the weighted combine (rows.cu).
 cudaError_t launch_quantize_rows(const void* x, bool bf16, long long stride, int rows, int K, bool silu,

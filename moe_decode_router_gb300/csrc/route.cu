@@ -678,11 +678,11 @@ __global__ void __launch_bounds__(128) route_kernel(const RouteParams p) {
 //
 // Bound by latency and by the scattered stores of the order, one line a lane:
 // 49,152 pairs of 256 experts take one CTA 61 us, eight 8.4 us, sixteen 6.3 us.
-// Up to 2,048 pairs one CTA is enough.
 constexpr int GP_WARPS = 32;
-constexpr int GP_CTAS = 16;  // more than the portable 8, within one GPC
+constexpr int GP_CTAS = 16;  // at most: more than the portable 8, within one GPC
 constexpr int GP_HELD = 4;
 
+template <int CTAS>  // of the cluster
 __global__ void __launch_bounds__(GP_WARPS * 32) group_kernel(const int32_t* __restrict__ ids, int P, int E,
                                                               int32_t* __restrict__ offsets,
                                                               int32_t* __restrict__ order, int32_t* __restrict__ pos) {
@@ -690,15 +690,14 @@ __global__ void __launch_bounds__(GP_WARPS * 32) group_kernel(const int32_t* __r
   int* total = hist + GP_WARPS * E;
   int* first = total + E;
   int* scan = first + E + 1;
-  uint32_t rank, ctas;
+  uint32_t rank;
   asm("mov.u32 %0, %%cluster_ctarank;" : "=r"(rank));
-  asm("mov.u32 %0, %%cluster_nctaid.x;" : "=r"(ctas));
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   for (int i = tid; i < GP_WARPS * E; i += GP_WARPS * 32) hist[i] = 0;
   __syncthreads();
   pdl_wait();
   pdl_trigger();
-  const int stretch = (int)((P + ctas * GP_WARPS * 32 - 1) / (ctas * GP_WARPS * 32)) * 32;  // pairs of a warp
+  const int stretch = (P + CTAS * GP_WARPS * 32 - 1) / (CTAS * GP_WARPS * 32) * 32;  // pairs of a warp
   const long long lo = (long long)(rank * GP_WARPS + warp) * stretch;
   int* h = hist + warp * E;
   auto id_at = [&](int i) {  // of this lane's pair, -1: none or dropped
@@ -728,15 +727,15 @@ __global__ void __launch_bounds__(GP_WARPS * 32) group_kernel(const int32_t* __r
     }
     total[tid] = sum;
   }
-  if (ctas > 1) asm volatile("barrier.cluster.arrive.release.aligned;\n barrier.cluster.wait.acquire.aligned;" ::: "memory");
+  if (CTAS > 1) asm volatile("barrier.cluster.arrive.release.aligned;\n barrier.cluster.wait.acquire.aligned;" ::: "memory");
   else __syncthreads();
   // per expert: all pairs, and those of the CTAs before this one
   int all = 0, before = 0;
   if (tid < E) {
-    int v[GP_CTAS] = {};
-    if (ctas > 1) {
+    int v[CTAS];
+    if (CTAS > 1) {
 #pragma unroll
-      for (uint32_t r = 0; r < GP_CTAS; ++r) {
+      for (uint32_t r = 0; r < CTAS; ++r) {
         uint32_t a;
         asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(smem_u32(total + tid)), "r"(r));
         asm volatile("ld.shared::cluster.s32 %0, [%1];" : "=r"(v[r]) : "r"(a) : "memory");
@@ -745,13 +744,13 @@ __global__ void __launch_bounds__(GP_WARPS * 32) group_kernel(const int32_t* __r
       v[0] = total[tid];
     }
 #pragma unroll
-    for (uint32_t r = 0; r < GP_CTAS; ++r) {
+    for (uint32_t r = 0; r < CTAS; ++r) {
       all += v[r];
       if (r < rank) before += v[r];
     }
   }
   // this thread has read the other CTAs' totals; they may leave once all have
-  if (ctas > 1) asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+  if (CTAS > 1) asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
   int incl = all;  // inclusive sums over the experts
 #pragma unroll
   for (int off = 1; off < 32; off <<= 1) {
@@ -800,9 +799,9 @@ __global__ void __launch_bounds__(GP_WARPS * 32) group_kernel(const int32_t* __r
   for (int i = 0; i < GP_HELD; ++i)
     if (32 * i < stretch) hand_out(32 * i, held[i]);
   for (int i = 32 * GP_HELD; i < stretch; i += 32) hand_out(i, id_at(i));
-  for (long long i = kept + (long long)rank * GP_WARPS * 32 + tid; i < P; i += (long long)ctas * GP_WARPS * 32) order[i] = -1;
+  for (long long i = kept + (long long)rank * GP_WARPS * 32 + tid; i < P; i += (long long)CTAS * GP_WARPS * 32) order[i] = -1;
   __syncwarp();
-  if (ctas > 1) asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+  if (CTAS > 1) asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
 
 template <int EPL>
@@ -827,10 +826,53 @@ cudaError_t launch_route_epl(RouteParams p, bool bf16, cudaStream_t st) {
 
 constexpr int group_smem(int E) { return (GP_WARPS * E + 2 * E + 1 + GP_WARPS) * 4; }
 
-cudaError_t route_kernels_init() {
-  const cudaError_t e = cudaFuncSetAttribute(group_kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
-  if (e != cudaSuccess) return e;
-  return cudaFuncSetAttribute(group_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, group_smem(ROUTE_MAX_E));
+// CTAs that group n_pairs where the device places clusters of up to `most`.  One
+// alone saves the exchange with the others (up to two ids a thread); few pairs
+// make a cluster's fixed costs count: 8,192 pairs of 64, 256, 1,024 experts 3.9,
+// 4.4, 6.3 us in eight, 4.0, 4.7, 8.4 in sixteen; 16,384 of 256 5.1 and 4.9.
+static int group_ctas(int n_pairs, int most) {
+  const int want = n_pairs <= 2 * GP_WARPS * 32 ? 1 : n_pairs <= 8192 ? 8 : GP_CTAS;
+  return want < most ? want : most;
+}
+
+static cudaLaunchConfig_t group_config(int ctas, int E, cudaLaunchAttribute (&attr)[2], cudaStream_t st) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)ctas);
+  cfg.blockDim = dim3(GP_WARPS * 32);
+  cfg.dynamicSmemBytes = (size_t)group_smem(E);
+  cfg.stream = st;
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = (unsigned)ctas;
+  attr[1].val.clusterDim.y = 1;
+  attr[1].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 2;
+  return cfg;
+}
+
+// Whether the device (it may be a part of one) places clusters of so many.
+template <int CTAS>
+static bool group_placed() {
+  if (CTAS > 8 &&
+      cudaFuncSetAttribute(group_kernel<CTAS>, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) != cudaSuccess)
+    return false;
+  if (cudaFuncSetAttribute(group_kernel<CTAS>, cudaFuncAttributeMaxDynamicSharedMemorySize, group_smem(ROUTE_MAX_E)) !=
+      cudaSuccess)
+    return false;
+  cudaLaunchAttribute attr[2];
+  const cudaLaunchConfig_t cfg = group_config(CTAS, ROUTE_MAX_E, attr, nullptr);
+  int n = 0;
+  return cudaOccupancyMaxActiveClusters(&n, group_kernel<CTAS>, &cfg) == cudaSuccess && n > 0;
+}
+
+cudaError_t route_kernels_init(int* group_most) {
+  *group_most = 1;
+  if (group_placed<8>()) *group_most = 8;
+  if (*group_most == 8 && group_placed<GP_CTAS>()) *group_most = GP_CTAS;
+  (void)cudaGetLastError();  // a size that is not placed is no error of a later call
+  return cudaFuncSetAttribute(group_kernel<1>, cudaFuncAttributeMaxDynamicSharedMemorySize, group_smem(ROUTE_MAX_E));
 }
 
 cudaError_t launch_route(const RouteSpec& r, const void* logits, bool bf16, long long stride, int T, const float* bias,
@@ -859,24 +901,16 @@ cudaError_t launch_route(const RouteSpec& r, const void* logits, bool bf16, long
 }
 
 cudaError_t launch_group_pairs(const int32_t* ids, int P, int E, int32_t* offsets, int32_t* order, int32_t* pos,
-                               cudaStream_t st) {
-  cudaLaunchConfig_t cfg = {};
-  // One CTA alone saves the exchange with the others: up to two ids a thread.
-  const unsigned ctas = P <= 2 * GP_WARPS * 32 ? 1 : GP_CTAS;
-  cfg.gridDim = dim3(ctas);
-  cfg.blockDim = dim3(GP_WARPS * 32);
-  cfg.dynamicSmemBytes = (size_t)group_smem(E);
-  cfg.stream = st;
+                               int most, cudaStream_t st) {
+  const int ctas = group_ctas(P, most);
   cudaLaunchAttribute attr[2];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  attr[1].id = cudaLaunchAttributeClusterDimension;
-  attr[1].val.clusterDim.x = ctas;
-  attr[1].val.clusterDim.y = 1;
-  attr[1].val.clusterDim.z = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = 2;
-  return cudaLaunchKernelEx(&cfg, group_kernel, ids, P, E, offsets, order, pos);
+  const cudaLaunchConfig_t cfg = group_config(ctas, E, attr, st);
+  return ctas == 1   ? cudaLaunchKernelEx(&cfg, group_kernel<1>, ids, P, E, offsets, order, pos)
+         : ctas == 8 ? cudaLaunchKernelEx(&cfg, group_kernel<8>, ids, P, E, offsets, order, pos)
+                     : cudaLaunchKernelEx(&cfg, group_kernel<GP_CTAS>, ids, P, E, offsets, order, pos);
 }
 
 }  // namespace flint
+
+// For the tests: the CTAs that group so many pairs where clusters of up to `most` are placed.
+extern "C" int flint_group_pairs_ctas(int n_pairs, int most) { return flint::group_ctas(n_pairs, most); }

@@ -1,5 +1,5 @@
 """Inputs of the FP8 expert operators where a shortcut can go wrong: routing rows whose
-fp32 scores do not decide.
+fp32 scores do not decide, and grouping in clusters of every size.
 
 References and tolerances as in test_expert_ops.py.
 """
@@ -8,7 +8,8 @@ import numpy as np
 import pytest
 import torch
 
-import test_expert_ops as X
+import expert_ops_reference as R
+from moe_decode_router_gb300 import flint_moe as F
 from test_expert_ops import check_route, dev, gen, gpu
 
 # ------------------------------------------------------------------ groups whose two best cancel
@@ -101,3 +102,28 @@ def test_route_few_distinct_candidates(softmax, groups):
     b = 1e-9 * (torch.rand(E, generator=g) < 0.02)
     for bias in (b, torch.zeros(E), 0.5 + torch.zeros(E)):
         check_route(x.to(d), 8, bias=bias.to(d), softmax=softmax, n_groups=groups[0], top_groups=groups[1], top2=groups[2])
+
+
+# ------------------------------------------------------------------ grouping by cluster size
+
+
+def test_group_ctas():
+    """One CTA, eight or sixteen by the number of pairs, and never more than the device places."""
+    ctas = F.load_library().flint_group_pairs_ctas
+    assert [ctas(n, 16) for n in (1, 2048, 2049, 8192, 8193, 1 << 24)] == [1, 1, 8, 8, 16, 16]
+    assert [ctas(n, 8) for n in (1, 2048, 2049, 8192, 8193, 1 << 24)] == [1, 1, 8, 8, 8, 8]
+    assert {ctas(n, 1) for n in (1, 2049, 8193, 1 << 24)} == {1}
+
+
+@gpu
+@pytest.mark.parametrize("E", [1, 5, 300, 1024])
+@pytest.mark.parametrize("pairs", [2048, 2049, 5000, 8191, 8192, 8193, 16385])
+def test_group_pairs_of_every_cluster(pairs, E):
+    d = dev()
+    ids = torch.randint(-1, E + 1, (pairs,), generator=gen(pairs + E), dtype=torch.int32)
+    offsets = torch.full((E + 1,), -9, dtype=torch.int32, device=d)
+    order, pos = (torch.full((pairs,), -9, dtype=torch.int32, device=d) for _ in range(2))
+    F.group_pairs(ids.to(d), offsets, order, pos)
+    torch.cuda.synchronize()
+    for got, want in zip((offsets, order, pos), R.group(ids.numpy(), E)):
+        assert np.array_equal(got.cpu().numpy(), want)
