@@ -43,6 +43,8 @@ struct DeviceState {
   int sm_count = 0;
   int gu_grid = 0;     // three-kernel path: gate/up CTAs
   int fused_grid = 0;  // persistent kernel: one CTA per SM, at most one per router expert
+  bool group_ready = false;       // grouping of pairs
+  bool block_gemm_ready = false;  // the block-scaled product
   int group_most = 0;  // CTAs of the largest cluster that grouping may use
   unsigned* err = nullptr;
   cudaStream_t capture_stream = nullptr;
@@ -95,8 +97,10 @@ int device_state(DeviceState** out) {
     if (dense_kernels_init() != cudaSuccess) return FLINT_MOE_ERR_CUDA;
     if (medium_kernels_init() != cudaSuccess) return FLINT_MOE_ERR_CUDA;
     if (prefill_kernels_init(dev) != cudaSuccess) return FLINT_MOE_ERR_CUDA;
-    if (route_kernels_init(&s.group_most) != cudaSuccess) return FLINT_MOE_ERR_CUDA;
-    if (block_gemm_kernels_init() != cudaSuccess) return FLINT_MOE_ERR_CUDA;
+    // What these need no other call does: a device that refuses it has the rest.
+    s.group_ready = route_kernels_init(&s.group_most) == cudaSuccess;
+    s.block_gemm_ready = block_gemm_kernels_init() == cudaSuccess;
+    if (!s.group_ready || !s.block_gemm_ready) (void)cudaGetLastError();  // theirs alone
     if (cudaStreamCreateWithFlags(&s.capture_stream, cudaStreamNonBlocking) != cudaSuccess)
       return FLINT_MOE_ERR_CUDA;
     s.ready = true;
@@ -599,6 +603,7 @@ int flint_moe_group_pairs(const int32_t* ids, int n_pairs, int n_experts, int32_
   DeviceState* ds = nullptr;
   int st = device_state(&ds);
   if (st != FLINT_MOE_OK) return st;
+  if (!ds->group_ready) return FLINT_MOE_ERR_CUDA;
   return to_status(
       launch_group_pairs(ids, n_pairs, n_experts, offsets, order, pos, ds->group_most,
                          reinterpret_cast<cudaStream_t>(stream)));
@@ -655,6 +660,7 @@ int flint_moe_block_gemm(const void* a, const float* a_scales, int M, const void
   DeviceState* ds = nullptr;
   int st = device_state(&ds);
   if (st != FLINT_MOE_OK) return st;
+  if (!ds->block_gemm_ready) return FLINT_MOE_ERR_CUDA;
   return to_status(launch_block_gemm(a, a_scales, M, b, b_scales, n_experts, offsets, N, K, y,
                                      y_type == FLINT_MOE_T_F32, ds->sm_count, ds->err,
                                      reinterpret_cast<cudaStream_t>(stream)));

@@ -871,7 +871,7 @@ cudaError_t route_kernels_init(int* group_most) {
   *group_most = 1;
   if (group_placed<8>()) *group_most = 8;
   if (*group_most == 8 && group_placed<GP_CTAS>()) *group_most = GP_CTAS;
-  (void)cudaGetLastError();  // a size that is not placed is no error of a later call
+  if (*group_most < GP_CTAS) (void)cudaGetLastError();  // a size that is not placed is no error of a later call
   return cudaFuncSetAttribute(group_kernel<1>, cudaFuncAttributeMaxDynamicSharedMemorySize, group_smem(ROUTE_MAX_E));
 }
 
