@@ -4,9 +4,11 @@
 
 Each .cu file under csrc/ compiles to its own object in parallel; the objects
 link into moe_decode_router_gb300/_lib/libflint_moe.so.  csrc/binding.cpp, the
-compiled marshalling of the short Python calls, becomes _flint_binding.so beside
-it (against the installed torch).  A rebuild happens only when a source or header
-is newer than what was built.
+compiled marshalling of the short Python calls, becomes an extension module beside
+it, whose name holds what it was built against: the interpreter and the installed
+torch.  A rebuild happens only when a source or header is newer than what was
+built.  Every build works in a folder of its own and moves what it made into place,
+so that several processes may build at once.
 """
 
 from __future__ import annotations
@@ -15,10 +17,12 @@ import argparse
 import concurrent.futures as cf
 import importlib.util
 import os
+import re
 import shutil
 import subprocess
 import sys
 import sysconfig
+import tempfile
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
@@ -26,7 +30,6 @@ CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 OUT_DIR = os.path.join(PKG, "_lib")
 LIB = os.path.join(OUT_DIR, "libflint_moe.so")
-BINDING = os.path.join(OUT_DIR, "_flint_binding.so")
 BINDING_SRC = os.path.join(CSRC, "binding.cpp")
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
@@ -53,19 +56,29 @@ def _torch_dir() -> str:
     return importlib.util.find_spec("torch").submodule_search_locations[0]
 
 
+def _torch_version() -> str:
+    with open(os.path.join(_torch_dir(), "version.py")) as f:
+        return re.search(r"""^__version__ = ['"]([^'"]+)""", f.read(), re.M).group(1)
+
+
+def binding_path() -> str:
+    """The compiled marshalling for this interpreter and this torch; one built for others is another file."""
+    return os.path.join(OUT_DIR, f"_flint_binding-torch{_torch_version()}{sysconfig.get_config_var('EXT_SUFFIX')}")
+
+
 def _newer(out, deps) -> bool:
     return os.path.exists(out) and all(os.path.getmtime(f) <= os.path.getmtime(out) for f in deps)
 
 
 def up_to_date() -> bool:
     header = os.path.join(INCLUDE, "flint_moe.h")
-    return _newer(LIB, _deps()) and _newer(BINDING, [BINDING_SRC, header, os.path.join(_torch_dir(), "version.py")])
+    return _newer(LIB, _deps()) and _newer(binding_path(), [BINDING_SRC, header, os.path.join(_torch_dir(), "version.py")])
 
 
-def _build_binding(nvcc: str) -> None:
+def _build_binding(nvcc: str, work: str) -> None:
     torch_dir = _torch_dir()
     cuda = os.path.dirname(os.path.dirname(os.path.realpath(nvcc)))
-    tmp = BINDING + ".tmp"
+    tmp = os.path.join(work, "binding.so")
     cmd = [os.environ.get("CXX", "g++"), "-O2", "-std=c++17", "-fPIC", "-shared", BINDING_SRC, "-o", tmp,
            "-I", INCLUDE, "-I", sysconfig.get_paths()["include"], "-I", os.path.join(torch_dir, "include"),
            "-I", os.path.join(cuda, "include"), "-L", os.path.join(torch_dir, "lib"),
@@ -73,21 +86,25 @@ def _build_binding(nvcc: str) -> None:
     r = subprocess.run(cmd, capture_output=True, text=True)
     if r.returncode != 0:
         raise RuntimeError(f"g++ failed on {BINDING_SRC}:\n{r.stdout}\n{r.stderr}")
-    os.replace(tmp, BINDING)
+    os.replace(tmp, binding_path())
 
 
 def build(force: bool = False, verbose: bool = False) -> str:
     if not force and up_to_date():
         return LIB
     nvcc = nvcc_path()
-    obj_dir = os.path.join(OUT_DIR, "obj")
-    os.makedirs(obj_dir, exist_ok=True)
+    os.makedirs(OUT_DIR, exist_ok=True)
+    with tempfile.TemporaryDirectory(prefix="build-", dir=OUT_DIR) as work:
+        return _build_in(work, nvcc, verbose)
+
+
+def _build_in(work: str, nvcc: str, verbose: bool) -> str:
     common = ARCH + ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "-I", INCLUDE, "-I", CSRC]
     if verbose:
         common += ["-Xptxas", "-v"]
 
     def compile_one(src):
-        obj = os.path.join(obj_dir, os.path.basename(src)[:-3] + ".o")
+        obj = os.path.join(work, os.path.basename(src)[:-3] + ".o")
         cmd = [nvcc, *common, "-c", src, "-o", obj]
         r = subprocess.run(cmd, capture_output=True, text=True)
         if r.returncode != 0:
@@ -95,14 +112,14 @@ def build(force: bool = False, verbose: bool = False) -> str:
         return obj, r.stderr
 
     with cf.ThreadPoolExecutor(max_workers=min(8, os.cpu_count() or 1)) as ex:
-        binding = ex.submit(_build_binding, nvcc)
+        binding = ex.submit(_build_binding, nvcc, work)
         results = list(ex.map(compile_one, _sources()))
         binding.result()
     if verbose:
         for _, log in results:
             sys.stderr.write(log)
     objs = [o for o, _ in results]
-    tmp = LIB + ".tmp"
+    tmp = os.path.join(work, "lib.so")
     cmd = [nvcc, *ARCH, "-shared", "-o", tmp, *objs]
     r = subprocess.run(cmd, capture_output=True, text=True)
     if r.returncode != 0:

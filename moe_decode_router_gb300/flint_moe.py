@@ -165,7 +165,7 @@ _FAST = _NotLoaded()
 
 def _load_binding(lib):
     global _FAST
-    loader = importlib.machinery.ExtensionFileLoader("_flint_binding", _build.BINDING)
+    loader = importlib.machinery.ExtensionFileLoader("_flint_binding", _build.binding_path())
     module = importlib.util.module_from_spec(importlib.util.spec_from_loader("_flint_binding", loader))
     loader.exec_module(module)
     module.bind(*(ctypes.cast(getattr(lib, f"flint_moe_{name}"), ctypes.c_void_p).value
