@@ -8,7 +8,8 @@ compiled marshalling of the short Python calls, becomes an extension module besi
 it, whose name holds what it was built against: the interpreter and the installed
 torch.  A rebuild happens only when a source or header is newer than what was
 built.  Every build works in a folder of its own and moves what it made into place,
-so that several processes may build at once.
+so that several processes may build at once.  Without the module (no host compiler,
+no torch headers) every call is marshalled by Python: a warning, not an error.
 """
 
 from __future__ import annotations
@@ -23,6 +24,7 @@ import subprocess
 import sys
 import sysconfig
 import tempfile
+import warnings
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
@@ -70,61 +72,72 @@ def _newer(out, deps) -> bool:
     return os.path.exists(out) and all(os.path.getmtime(f) <= os.path.getmtime(out) for f in deps)
 
 
-def up_to_date() -> bool:
+def library_up_to_date() -> bool:
+    return _newer(LIB, _deps())
+
+
+def binding_up_to_date() -> bool:
     header = os.path.join(INCLUDE, "flint_moe.h")
-    return _newer(LIB, _deps()) and _newer(binding_path(), [BINDING_SRC, header, os.path.join(_torch_dir(), "version.py")])
+    return _newer(binding_path(), [BINDING_SRC, header, os.path.join(_torch_dir(), "version.py")])
 
 
-def _build_binding(nvcc: str, work: str) -> None:
-    torch_dir = _torch_dir()
-    cuda = os.path.dirname(os.path.dirname(os.path.realpath(nvcc)))
-    tmp = os.path.join(work, "binding.so")
-    cmd = [os.environ.get("CXX", "g++"), "-O2", "-std=c++17", "-fPIC", "-shared", BINDING_SRC, "-o", tmp,
-           "-I", INCLUDE, "-I", sysconfig.get_paths()["include"], "-I", os.path.join(torch_dir, "include"),
-           "-I", os.path.join(cuda, "include"), "-L", os.path.join(torch_dir, "lib"),
-           "-ltorch_python", "-ltorch_cpu", "-lc10", "-lc10_cuda"]
+def up_to_date() -> bool:
+    return library_up_to_date() and binding_up_to_date()
+
+
+def _run(cmd, what):
     r = subprocess.run(cmd, capture_output=True, text=True)
     if r.returncode != 0:
-        raise RuntimeError(f"g++ failed on {BINDING_SRC}:\n{r.stdout}\n{r.stderr}")
+        raise RuntimeError(f"{what} failed:\n{r.stdout}\n{r.stderr}")
+    return r
+
+
+def _build_binding(work: str) -> None:
+    torch_dir = _torch_dir()
+    cuda = os.path.dirname(os.path.dirname(os.path.realpath(nvcc_path())))
+    tmp = os.path.join(work, "binding.so")
+    _run([os.environ.get("CXX", "g++"), "-O2", "-std=c++17", "-fPIC", "-shared", BINDING_SRC, "-o", tmp,
+          "-I", INCLUDE, "-I", sysconfig.get_paths()["include"], "-I", os.path.join(torch_dir, "include"),
+          "-I", os.path.join(cuda, "include"), "-L", os.path.join(torch_dir, "lib"),
+          "-ltorch_python", "-ltorch_cpu", "-lc10", "-lc10_cuda"], f"g++ on {BINDING_SRC}")
     os.replace(tmp, binding_path())
 
 
-def build(force: bool = False, verbose: bool = False) -> str:
-    if not force and up_to_date():
-        return LIB
+def _build_library(work: str, verbose: bool) -> None:
     nvcc = nvcc_path()
-    os.makedirs(OUT_DIR, exist_ok=True)
-    with tempfile.TemporaryDirectory(prefix="build-", dir=OUT_DIR) as work:
-        return _build_in(work, nvcc, verbose)
-
-
-def _build_in(work: str, nvcc: str, verbose: bool) -> str:
     common = ARCH + ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "-I", INCLUDE, "-I", CSRC]
     if verbose:
         common += ["-Xptxas", "-v"]
 
     def compile_one(src):
         obj = os.path.join(work, os.path.basename(src)[:-3] + ".o")
-        cmd = [nvcc, *common, "-c", src, "-o", obj]
-        r = subprocess.run(cmd, capture_output=True, text=True)
-        if r.returncode != 0:
-            raise RuntimeError(f"nvcc failed on {src}:\n{r.stdout}\n{r.stderr}")
-        return obj, r.stderr
+        return obj, _run([nvcc, *common, "-c", src, "-o", obj], f"nvcc on {src}").stderr
 
     with cf.ThreadPoolExecutor(max_workers=min(8, os.cpu_count() or 1)) as ex:
-        binding = ex.submit(_build_binding, nvcc, work)
         results = list(ex.map(compile_one, _sources()))
-        binding.result()
     if verbose:
         for _, log in results:
             sys.stderr.write(log)
-    objs = [o for o, _ in results]
     tmp = os.path.join(work, "lib.so")
-    cmd = [nvcc, *ARCH, "-shared", "-o", tmp, *objs]
-    r = subprocess.run(cmd, capture_output=True, text=True)
-    if r.returncode != 0:
-        raise RuntimeError(f"link failed:\n{r.stdout}\n{r.stderr}")
+    _run([nvcc, *ARCH, "-shared", "-o", tmp, *(o for o, _ in results)], "the link")
     os.replace(tmp, LIB)
+
+
+def build(force: bool = False, verbose: bool = False) -> str:
+    library, binding = force or not library_up_to_date(), force or not binding_up_to_date()
+    if not library and not binding:
+        return LIB
+    os.makedirs(OUT_DIR, exist_ok=True)
+    with tempfile.TemporaryDirectory(prefix="build-", dir=OUT_DIR) as work, cf.ThreadPoolExecutor(1) as ex:
+        made = ex.submit(_build_binding, work) if binding else None
+        if library:
+            _build_library(work, verbose)
+        try:
+            if made:
+                made.result()
+        except Exception as e:
+            warnings.warn(f"the compiled marshalling could not be built; Python marshals every call instead: {e}",
+                          RuntimeWarning)
     return LIB
 
 

@@ -14,6 +14,7 @@ import importlib.machinery
 import importlib.util
 import os
 import threading
+import warnings
 
 import torch
 
@@ -153,7 +154,7 @@ def load_library(build_if_missing: bool = True) -> ctypes.CDLL:
 
 
 class _NotLoaded:
-    """Stands for the compiled marshalling until the library is loaded: no call fits it."""
+    """Stands for the compiled marshalling until the library is loaded, and where there is none: no call fits it."""
 
     def __getattr__(self, name):
         return lambda *args: _LOOK
@@ -164,13 +165,22 @@ _FAST = _NotLoaded()
 
 
 def _load_binding(lib):
+    """The compiled marshalling is a shortcut: without it the calls below make their own way."""
     global _FAST
+    try:
+        _FAST = _binding(lib)
+    except (ImportError, OSError, RuntimeError) as e:
+        warnings.warn(f"the compiled marshalling could not be loaded; Python marshals every call instead: {e}",
+                      RuntimeWarning)
+
+
+def _binding(lib):
     loader = importlib.machinery.ExtensionFileLoader("_flint_binding", _build.binding_path())
     module = importlib.util.module_from_spec(importlib.util.spec_from_loader("_flint_binding", loader))
     loader.exec_module(module)
     module.bind(*(ctypes.cast(getattr(lib, f"flint_moe_{name}"), ctypes.c_void_p).value
                   for name in ("route", "group_pairs", "quantize_rows", "block_gemm", "combine")))
-    _FAST = module
+    return module
 
 
 def _lib():
