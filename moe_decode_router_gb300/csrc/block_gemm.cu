@@ -44,9 +44,8 @@ __device__ __forceinline__ void mma_e4m3(float (&d)[4], uint32_t a0, uint32_t a1
 // ---- few rows: weights are streamed once for up to 8 activation rows of one
 // expert.  Grid (M, N / rows of a CTA): the CTA of row r works when r is the
 // first of a run of 8 rows of its expert.  With SPLIT 8 a dense product has CTAs
-// for every eighth row alone (24 rows x 4096 x 2048 7.7 -> 6.8 us against the
-// tcgen05 kernel; SPLIT 1 sees grouped rows only, where this choice alone cost
-// 1.4 of 21 us).  A warp takes 16 weight rows and every SPLIT-th K block of
+// for every eighth row alone (SPLIT 1 sees grouped rows only, where this choice
+// alone cost 1.4 of 21 us).  A warp takes 16 weight rows and every SPLIT-th K block of
 // them; SPLIT warps of a CTA share 16 rows, so that a small product has enough
 // warps (SPLIT 8) and a large one few sums across warps (SPLIT 1).  Both operands
 // are read straight from global memory into mma fragments: the product of a
@@ -203,8 +202,8 @@ cudaError_t launch_skinny(const GemmArgs& p, cudaStream_t st) {
 // block's: per K block and SM 512 cycles of MMA, 256 of tensor-memory reads
 // (32x32b; the 16-lane forms read at half that rate) and 256 of packed fma,
 // which overlap.  Every CTA loads its own 48 KB a K block; sharing the weight tile
-// between two CTAs was no faster (8191 x 4096 x 4096 107 us either way, ragged
-// experts 146 shared, 144 alone) and ties their steps together.
+// between two CTAs gains little (8191 x 4096 x 4096 107 us either way, ragged
+// experts 146 shared, 147 alone with weights from HBM) and ties their steps together.
 //
 // WIDE (short groups).  128 weight rows are the M side, always full, and up to
 // 64 rows of a the N side in steps of 16, so that a group of few rows costs
@@ -445,6 +444,16 @@ __global__ void __launch_bounds__(TC_THREADS, 1)
       if (tile * p.n_tiles > v) --tile;
     }
     t.wt = v - tile * p.n_tiles;
+    if (TALL) {
+      // Two row tiles of a group go side by side, so that both ask for a weight tile at
+      // about the same time: ragged experts 142.2 -> 141.4 us against one after the other.
+      const int first = tile & ~1;
+      if ((first + 1) * C::ROWS < cnt) {
+        const int r = v - first * p.n_tiles;
+        t.wt = r >> 1;
+        tile = first + (r & 1);
+      }
+    }
     t.row0 = g_lo[lo] + tile * C::ROWS;
     t.cnt = min(C::ROWS, cnt - tile * C::ROWS);
     t.n = TALL ? min(256, (p.N - t.wt * 256 + 15) & ~15) : (t.cnt + 15) & ~15;
@@ -904,24 +913,24 @@ cudaError_t block_gemm_kernels_init() {
   return cudaSuccess;
 }
 
-// Which kernel a product takes, measured (us) on 256 experts of 1024 x 2048, R rows in all, and
-// on one matrix of 4096 x 2048:
-//   up to 8 grouped rows        few-row SPLIT 8  R 8: 7.9, WIDE 9.5
+// Which kernel a product takes, measured (us, calls in a graph) on 256 experts of
+// 1024 x 2048, R rows in all, and on one matrix of 4096 x 2048:
+//   up to 8 grouped rows        few-row SPLIT 8  R 8: 6.2, WIDE 9.4
 //   up to 8 dense rows, 28 M
-//   weights                     few-row SPLIT 8  6144 x 4096: 7.2, WIDE in 2 9.6; but 8192 x 8192: 17.9, 16.3
+//   weights                     few-row SPLIT 8  8 of 6144 x 4096: 6.2, WIDE in 2 9.0; but 8192 x 8192: 14.6, 13.4
 //   more dense rows, passes of
 //   8 x N up to 14,336, x K up
-//   to 21 M                     few-row SPLIT 8  16 rows: 5.9, WIDE in 4 6.4; 40 of 2048 x 2048 5.9, 6.4; 192 of
-//                                                512 x 512 3.6, 4.3; but 32 rows: 8.6, 6.4; 80 of 2048 x 1024 6.3, 5.7
+//   to 21 M                     few-row SPLIT 8  16 rows: 5.2, WIDE in 4 5.8; 40 of 2048 x 2048 5.8, 5.8; 192 of
+//                                                512 x 512 3.5, 4.1; but 32 rows: 7.9, 5.8; 80 of 2048 x 1024 6.1, 5.2
+//   33 to 128 rows, at most one
+//   an expert on average        few-row SPLIT 1  R 48: 17.3, WIDE 19.1; R 128: 36.6, 34.5; but R 32: 16.5, 14.3
 //   a seventh of the SMs spare
 //   with 4 CTAs a unit, K from
-//   8 blocks                    WIDE in 4        32 rows: 6.4, in 2 7.4, whole 7.7; 64 of 2048 x 8192: 10.8, 15.9, 24.8
-//   2 CTAs a unit, 12 blocks    WIDE in 2        64 of 4096 x 4096: 10.7, whole 14.2; but 128 of 2048 x 1024 6.3, 6.0
-//   33 to 128 rows, at most one
-//   an expert on average        few-row SPLIT 1  R 48: 20.0, WIDE 22.4; R 128: 35.2, 36.2; but R 32: 18.8, 16.6
+//   8 blocks                    WIDE in 4        32 rows: 5.8, in 2 6.9, whole 7.6; 64 of 2048 x 8192: 10.3, 15.2, 24.6
+//   2 CTAs a unit, 12 blocks    WIDE in 2        100 of 4096 x 4096: 10.4, whole 14.0
 //   one wave of WIDE's units,
-//   or 36 rows an expert        WIDE             24 rows each: 89, TALL 93; 256 dense: 9.3, 11.9
-//   else                        TALL             48 rows each: 98, WIDE 107; 512 dense: 12.2, 15.2
+//   or 36 rows an expert        WIDE             24 rows each: 85.7, TALL 87.8; 256 dense: 9.0, 10.5
+//   else                        TALL             48 rows each: 91.5, WIDE 102.7; 512 dense: 10.7, 14.9
 enum GemmKernel { GEMM_FEW_SPLIT, GEMM_FEW, GEMM_WIDE_IN_4, GEMM_WIDE_IN_2, GEMM_WIDE, GEMM_TALL };
 static GemmKernel choose_block_gemm(int M, int N, int K, int E, bool grouped, int sm_count) {
   constexpr int WIDE_ROWS = TcCfg<false>::ROWS, WIDE_W = TcCfg<false>::WROWS;
