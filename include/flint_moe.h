@@ -307,7 +307,8 @@ typedef struct {
 
 /*
  * Routing of T tokens (1..2^20).
- *   logits  [T][E] of logits_type, rows row_stride >= E elements apart
+ *   logits  [T][E] of logits_type, rows row_stride elements apart (E to 2^31;
+ *           what lies between two rows counts as the buffer's)
  *   bias    fp32 [E] added to the scores for the choice only, or NULL
  *   ids     int32 [T][top_k] in descending order of key, w fp32 [T][top_k]
  * The key of an expert is its logit, or score + bias when a bias is given.  An
@@ -346,10 +347,11 @@ int flint_moe_group_pairs(const int32_t *ids, int n_pairs, int n_experts, int32_
  *           one), or NULL: row i is written to place i, and places == rows
  *   q       E4M3 [places][K]; scales fp32 [ceil(K / 128)][places]
  * With a = max(largest magnitude of the block, 2^-96): scale = a / 448 and
- * code = e4m3(x * (448 / a)), round to nearest even; a block that holds an
- * infinity or NaN gets a scale that is not finite.  Places that no row names
- * are left as they were.  K a multiple of 16, at most 2^17; row_stride a
- * multiple of 16 bytes; at most 2^24 rows and places.
+ * code = e4m3(x * (448 / a)), quotient and product in fp32, then to nearest
+ * even; a block that holds an infinity or NaN gets a scale that is not finite.
+ * Places that no row names are left as they were.  K a multiple of 16, at most
+ * 2^17; row_stride a multiple of 16 bytes, at most 2^31 elements; at most 2^24
+ * rows and places.  What lies between two rows counts as x's.
  */
 int flint_moe_quantize_rows(const void *x, int x_type, long long row_stride, int rows, int K,
                             int silu_mul, const int32_t *pos, int top_k, int places, void *q,

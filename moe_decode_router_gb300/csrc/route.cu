@@ -11,14 +11,16 @@
 // candidates in order in fp64 (about one row in 250 with 256 experts and a
 // bias), or the whole row where that needs more than the candidates.
 //
-// Bound by instructions, some 1,100 a row with groups and bias: a pick is one
-// redux of the lanes' best keys, one of the indices that have it, and the next
-// best in the lane that owned it (every lane keeps two at hand).  A lane's
+// Bound by dependent steps: a pick is one redux of the lanes' best keys, one of the
+// indices that have it, and the next best in the lane that owned it (every lane
+// keeps two at hand), one pick after another; and by a last wave that is mostly
+// empty (2,048 blocks are 2.25 waves).  Some 1,000 instructions a row with groups
+// and bias use 55 % of the issue slots while the SMs are busy, 39 % in all.  A lane's
 // experts are neighbours: the row comes in 16-byte loads, and a group of whole
 // lanes is scored by shuffles among them.  8,191 rows of 256 fp32 with 8 groups,
 // bias and 8 picks: 276 us with every score in fp64, 15.4 us with the experts
-// dealt out one by one, 14.6 us this way (the bytes alone: 1.3 us); 8,192 rows
-// of 256 bf16, softmax, no groups: 8.4 us.
+// dealt out one by one, 13.1 us this way (the bytes alone: 1.3 us); 8,192 rows
+// of 256 bf16, softmax, no groups: 8.1 us.
 #include <type_traits>
 
 #include "flint_common.cuh"
@@ -677,7 +679,8 @@ __global__ void __launch_bounds__(128) route_kernel(const RouteParams p) {
 // decides an order, so the result is the same on every call.
 //
 // Bound by latency and by the scattered stores of the order, one line a lane:
-// 49,152 pairs of 256 experts take one CTA 61 us, eight 8.4 us, sixteen 6.3 us.
+// 49,152 pairs of 256 experts take one CTA 61 us, eight 8.4 us, sixteen 6.2 us; one
+// cluster does all, so 2^20 pairs take 66 us.
 constexpr int GP_WARPS = 32;
 constexpr int GP_CTAS = 16;  // at most: more than the portable 8, within one GPC
 constexpr int GP_HELD = 4;
