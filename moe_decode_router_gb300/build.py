@@ -60,7 +60,8 @@ def _torch_dir() -> str:
 
 def _torch_version() -> str:
     with open(os.path.join(_torch_dir(), "version.py")) as f:
-        return re.search(r"""^__version__ = ['"]([^'"]+)""", f.read(), re.M).group(1)
+        found = re.search(r"""^__version__ = ['"]([^'"]+)""", f.read(), re.M)
+    return found.group(1) if found else "unknown"
 
 
 def binding_path() -> str:
