@@ -177,10 +177,10 @@ def _own(s):
     c = s["case"]
     act = {"none": F.ACT_NONE, "silu": F.ACT_SILU, "gelu": F.ACT_GELU}[c.get("act", "none")]
     if c["op"] == "quantise":
-        F.quantize_rows_int8(s["x"], s["q"], s["scales"], pos=s["pos"])
+        F.integer_quantize_rows(s["x"], s["q"], s["scales"], pos=s["pos"])
         return s["q"], s["scales"]
     if c["op"] == "int8":
-        F.int8_gemm(s["a"], s["a_scales"], s["b"], s["b_scales"], s["y"], offsets=s["offsets"], act=act)
+        F.integer_gemm(s["a"], s["a_scales"], s["b"], s["b_scales"], s["y"], offsets=s["offsets"], act=act)
         return s["y"]
     if c["op"] == "gated":
         F.gated_linear(s["x"], s["w"], s["h"], gu=s["gu"], offsets=s["offsets"], act=act)
