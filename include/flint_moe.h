@@ -30,7 +30,8 @@
  *     routed experts, 1 shared expert, intermediate 512, top-6.  Anything else
  *     returns FLINT_MOE_ERR_UNSUPPORTED (there is no generic fallback path).
  *     The parts of an FP8 expert layer (flint_moe_route and the calls after
- *     it) take any shape within their limits.
+ *     it) and the linear, gated and 8-bit integer products take any shape
+ *     within their limits.
  */
 #ifndef FLINT_MOE_H
 #define FLINT_MOE_H
@@ -388,6 +389,107 @@ int flint_moe_block_gemm(const void *a, const float *a_scales, int M, const void
 int flint_moe_combine(const void *rows, int rows_type, int n_rows, const int32_t *pos,
                       const float *w, int T, int top_k, int N, const void *shared, void *y,
                       flint_moe_stream_t stream);
+
+/*
+ * ---- Feed-forward blocks of any shape: bf16 with gradients, 8-bit integers ----
+ *
+ * The two products of a gated feed-forward block in bf16, with their gradients,
+ * and in 8-bit integers with one scale for each row (token) and each output
+ * (channel); dense, or grouped by expert with the offsets of
+ * flint_moe_group_pairs.  A block, for P rows in expert order:
+ *   flint_moe_gated_linear     x  [P][K]  -> h [P][I], and gu [P][2I] to train
+ *   flint_moe_linear           h  [P][I]  -> y [P][N]
+ *   flint_moe_linear_backward  dy [P][N]  -> dh [P][I], dw of the second product
+ *   flint_moe_gated_linear_backward  dh   -> dgu [P][2I], dx [P][K], dw of the first
+ * and the same block served in 8-bit integers:
+ *   flint_moe_integer_quantize_rows  x, pos -> q [P][K], scales
+ *   flint_moe_integer_gemm           gated  -> h [P][I] in bf16
+ *   flint_moe_integer_quantize_rows  h      -> q [P][I], scales
+ *   flint_moe_integer_gemm                  -> y [P][N], for flint_moe_combine
+ * Weights are quantised by the same call, their matrices' rows being outputs.
+ * Limits of all: M 1..2^24 rows, N a multiple of 8, I (half a gated matrix) a
+ * multiple of 16, K a multiple of 16, N, 2 I and K at most 2^17, up to 1024
+ * experts; every buffer contiguous.  offsets int32 [n_experts + 1] on the device:
+ * rows offsets[e] .. offsets[e + 1] - 1 belong to expert e.  They must start at 0, not
+ * descend and not pass M; rows of outputs behind the last are left as they were,
+ * and what the inputs hold there is not used.  NULL: dense, n_experts == 1.
+ * No workspace is needed, every call is deterministic, and all may be captured
+ * into a CUDA graph (the first call of a process on a device sets up the library
+ * and must come before the capture).  Sums are fp32 (integer: exact).
+ */
+
+/* Activation of a gated product: none (a plain product), x / (1 + exp(-x)), or
+ * x / 2 * (1 + tanh(sqrt(2 / pi) * (x + 0.044715 x^3))).  Below -87 the first, and
+ * below -9 the second, may be 0. */
+enum { FLINT_MOE_ACT_NONE = 0, FLINT_MOE_ACT_SILU = 1, FLINT_MOE_ACT_GELU = 2 };
+
+/*
+ * y[m][n] = sum over k of x[m][k] * w[e][n][k], e the expert of row m.
+ *   x bf16 [M][K], w bf16 [n_experts][N][K], y [M][N] of y_type (FLINT_MOE_T_*)
+ */
+int flint_moe_linear(const void *x, int M, const void *w, int n_experts, const int32_t *offsets,
+                     int N, int K, void *y, int y_type, flint_moe_stream_t stream);
+
+/*
+ * Gradients of flint_moe_linear: dx = dy w, dw[e] = dy^T x over the rows of expert e
+ * (zeros for an expert of no rows).
+ *   dy bf16 [M][N], x and w as they were; dx bf16 [M][K] or NULL; dw
+ *   [n_experts][N][K] of dw_type or NULL; not both NULL
+ */
+int flint_moe_linear_backward(const void *dy, const void *x, int M, const void *w, int n_experts,
+                              const int32_t *offsets, int N, int K, void *dx, void *dw, int dw_type,
+                              flint_moe_stream_t stream);
+
+/*
+ * Gated projections in one kernel: with g and u the sums of x[m] with rows i and
+ * I + i of w[e],  h[m][i] = act(g) * u, formed from the fp32 sums.
+ *   x bf16 [M][K], w bf16 [n_experts][2I][K], h bf16 [M][I]
+ *   gu bf16 [M][2I] or NULL: the sums, g then u, for the gradient
+ */
+int flint_moe_gated_linear(const void *x, int M, const void *w, int n_experts, const int32_t *offsets,
+                           int I, int K, int act, void *h, void *gu, flint_moe_stream_t stream);
+
+/*
+ * Gradients of flint_moe_gated_linear: dg = dh * u * act'(g) and du = dh * act(g),
+ * formed in fp32 from gu and rounded to bf16 (dgu), then dx = dgu w and
+ * dw[e] = dgu^T x over the rows of expert e.
+ *   dh bf16 [M][I], gu bf16 [M][2I], x and w as they were; dgu bf16 [M][2I] is
+ *   written; dx and dw as for flint_moe_linear_backward, both may be NULL
+ */
+int flint_moe_gated_linear_backward(const void *dh, const void *gu, const void *x, int M, const void *w,
+                                    int n_experts, const int32_t *offsets, int I, int K, int act,
+                                    void *dgu, void *dx, void *dw, int dw_type,
+                                    flint_moe_stream_t stream);
+
+/*
+ * Rows to 8-bit integers: with a = max(largest magnitude of the row, 2^-96),
+ * scale = a / 127 in fp32, code = the whole number next to the real number
+ * x / scale, ties to even.  A row that holds an infinity or NaN gets a scale that is
+ * not finite, and codes of 0.
+ *   x [rows][K] of x_type, rows row_stride elements apart (a multiple of 16 bytes,
+ *   at most 2^31; what lies between two rows counts as x's); pos int32 [rows][top_k],
+ *   top_k 1..16: the places that each row is written to (places outside
+ *   0..places-1 are skipped; two rows must not share one), or NULL: row i is
+ *   written to place i, and places == rows
+ *   q int8 [places][K], scales fp32 [places]; places that no row names are left
+ *   as they were.  At most 2^24 rows and places.
+ */
+int flint_moe_integer_quantize_rows(const void *x, int x_type, long long row_stride, int rows, int K,
+                                    const int32_t *pos, int top_k, int places, int8_t *q, float *scales,
+                                    flint_moe_stream_t stream);
+
+/*
+ * 8-bit integer product: with s[m][n] = the exact sum over k of a[m][k] * b[e][n][k],
+ *   y[m][n] = a_scales[m] * b_scales[e][n] * s[m][n]
+ * in fp32 with one rounding to y's type.  act other than FLINT_MOE_ACT_NONE: N is 2I, and
+ * y [M][I] = act(value of i) * (value of I + i).
+ *   a int8 [M][K], a_scales fp32 [M], b int8 [n_experts][N][K], b_scales fp32
+ *   [n_experts][N]; y [M][N] or [M][I] of y_type.  All 256 codes are numbers.
+ *   K below 2^17.
+ */
+int flint_moe_integer_gemm(const int8_t *a, const float *a_scales, int M, const int8_t *b,
+                           const float *b_scales, int n_experts, const int32_t *offsets, int N, int K,
+                           int act, void *y, int y_type, flint_moe_stream_t stream);
 
 /* Frees cached CUDA graphs of every device the calling thread used.  Call
  * before freeing buffers whose addresses a cached stack graph holds. */

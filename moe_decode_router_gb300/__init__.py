@@ -5,6 +5,9 @@ The compute path is libflint_moe.so (csrc/, declared in include/flint_moe.h);
 """
 
 from .flint_moe import (  # noqa: F401
+    ACT_GELU,
+    ACT_NONE,
+    ACT_SILU,
     W_NVFP4,
     W_BF16,
     FlintLayer,
@@ -15,7 +18,13 @@ from .flint_moe import (  # noqa: F401
     decode_layer,
     decode_stack,
     device_error,
+    gated_linear,
+    gated_linear_backward,
     group_pairs,
+    integer_gemm,
+    integer_quantize_rows,
+    linear,
+    linear_backward,
     load_library,
     pack_layer,
     pack_weights,

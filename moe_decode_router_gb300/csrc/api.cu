@@ -258,6 +258,16 @@ int launch_one_layer(const flint_moe_dims* dims, const flint_moe_layer& layer, c
 }
 
 }  // namespace
+
+int device_info(int* sm_count, unsigned** err) {
+  std::lock_guard<std::mutex> lk(g_mu);
+  DeviceState* s = nullptr;
+  const int st = device_state(&s);
+  if (st != FLINT_MOE_OK) return st;
+  *sm_count = s->sm_count;
+  *err = s->err;
+  return FLINT_MOE_OK;
+}
 }  // namespace flint
 
 using namespace flint;

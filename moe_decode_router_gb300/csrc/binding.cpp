@@ -1,5 +1,5 @@
-// Compiled marshalling of the FP8 expert operators' Python calls: the same look
-// at the tensors as in flint_moe.py (type, shape, layout, device), then the C
+// Compiled marshalling of the Python calls of the FP8 expert operators and of the
+// linear, gated and integer products: the same look at the tensors as in flint_moe.py (type, shape, layout, device), then the C
 // ABI.  Those calls last a few microseconds, and a look of interpreted code as
 // long again.  A call that does not fit returns LOOK and has done nothing: the
 // interpreted path then names what is wrong, or takes the call.
@@ -26,6 +26,15 @@ struct Entry {
   decltype(&flint_moe_block_gemm) block_gemm = nullptr;
   decltype(&flint_moe_combine) combine = nullptr;
 } g_entry;
+
+struct LinearEntry {
+  decltype(&flint_moe_linear) linear = nullptr;
+  decltype(&flint_moe_linear_backward) linear_backward = nullptr;
+  decltype(&flint_moe_gated_linear) gated_linear = nullptr;
+  decltype(&flint_moe_gated_linear_backward) gated_linear_backward = nullptr;
+  decltype(&flint_moe_integer_quantize_rows) integer_quantize_rows = nullptr;
+  decltype(&flint_moe_integer_gemm) integer_gemm = nullptr;
+} g_linear;
 
 PyObject* status(long v) { return PyLong_FromLong(v); }
 
@@ -237,6 +246,186 @@ PyObject* py_combine(PyObject*, PyObject* const* a, Py_ssize_t n) try {
   return status(LOOK);
 }
 
+// A weight tensor [E][N][K] of this type on the current device (`dev` takes it).
+bool weights(const at::Tensor* w, at::ScalarType type, int* dev, int64_t* E, int64_t* N, int64_t* K) {
+  if (w == nullptr || w->dim() != 3 || (*dev = device_of(*w)) < 0) return false;
+  *E = w->size(0);
+  *N = w->size(1);
+  *K = w->size(2);
+  return fits_int(*E) && fits_int(*N) && fits_int(*K) && plain(w, type, *dev);
+}
+bool plain3(const at::Tensor* t, at::ScalarType type, int device, int64_t a, int64_t b, int64_t c) {
+  return plain(t, type, device) && t->dim() == 3 && t->size(0) == a && t->size(1) == b && t->size(2) == c;
+}
+// An optional argument: None, or what `fits` takes.
+template <typename F>
+bool optional(PyObject* o, const at::Tensor** t, F&& fits) {
+  *t = o == Py_None ? nullptr : tensor(o);
+  return o == Py_None || (*t != nullptr && fits(*t));
+}
+const void* in(const at::Tensor* t) { return t ? t->const_data_ptr() : nullptr; }
+void* out(const at::Tensor* t) { return t ? t->data_ptr() : nullptr; }
+const int32_t* places(const at::Tensor* t) { return static_cast<const int32_t*>(in(t)); }
+
+// linear(x, w, y, offsets | None, stream)
+PyObject* py_linear(PyObject*, PyObject* const* a, Py_ssize_t n) try {
+  if (n != 5 || g_linear.linear == nullptr) return status(LOOK);
+  const at::Tensor *x = tensor(a[0]), *w = tensor(a[1]), *y = tensor(a[2]), *offsets;
+  int dev;
+  int64_t E, N, K;
+  if (x == nullptr || y == nullptr || x->dim() != 2 || !weights(w, at::kBFloat16, &dev, &E, &N, &K)) return status(LOOK);
+  const int64_t M = x->size(0);
+  const int type = act_type(*y);
+  if (!fits_int(M) || type < 0 || !plain2(x, at::kBFloat16, dev, M, K) || !plain2(y, y->scalar_type(), dev, M, N) ||
+      !optional(a[3], &offsets, [&](const at::Tensor* t) { return plain1(t, at::kInt, dev, E + 1); }))
+    return status(LOOK);
+  flint_moe_stream_t st;
+  if (!to_stream(a[4], dev, &st)) return status(LOOK);
+  return call([&] {
+    return g_linear.linear(in(x), (int)M, in(w), (int)E, places(offsets), (int)N, (int)K, out(y), type, st);
+  });
+} catch (...) {
+  return status(LOOK);
+}
+
+// linear_backward(dy, x, w, dx | None, dw | None, offsets | None, stream)
+PyObject* py_linear_backward(PyObject*, PyObject* const* a, Py_ssize_t n) try {
+  if (n != 7 || g_linear.linear_backward == nullptr) return status(LOOK);
+  const at::Tensor *dy = tensor(a[0]), *x = tensor(a[1]), *w = tensor(a[2]), *dx, *dw, *offsets;
+  int dev;
+  int64_t E, N, K;
+  if (dy == nullptr || dy->dim() != 2 || !weights(w, at::kBFloat16, &dev, &E, &N, &K)) return status(LOOK);
+  const int64_t M = dy->size(0);
+  if (!fits_int(M) || !plain2(dy, at::kBFloat16, dev, M, N) || !plain2(x, at::kBFloat16, dev, M, K) ||
+      !optional(a[3], &dx, [&](const at::Tensor* t) { return plain2(t, at::kBFloat16, dev, M, K); }) ||
+      !optional(a[4], &dw, [&](const at::Tensor* t) { return act_type(*t) >= 0 && plain3(t, t->scalar_type(), dev, E, N, K); }) ||
+      !optional(a[5], &offsets, [&](const at::Tensor* t) { return plain1(t, at::kInt, dev, E + 1); }))
+    return status(LOOK);
+  flint_moe_stream_t st;
+  if (!to_stream(a[6], dev, &st)) return status(LOOK);
+  const int type = dw ? act_type(*dw) : FLINT_MOE_T_BF16;
+  return call([&] {
+    return g_linear.linear_backward(in(dy), in(x), (int)M, in(w), (int)E, places(offsets), (int)N, (int)K, out(dx),
+                                    out(dw), type, st);
+  });
+} catch (...) {
+  return status(LOOK);
+}
+
+// gated_linear(x, w, h, gu | None, offsets | None, act, stream)
+PyObject* py_gated_linear(PyObject*, PyObject* const* a, Py_ssize_t n) try {
+  if (n != 7 || g_linear.gated_linear == nullptr) return status(LOOK);
+  const at::Tensor *x = tensor(a[0]), *w = tensor(a[1]), *h = tensor(a[2]), *gu, *offsets;
+  int dev, act;
+  int64_t E, N, K;
+  if (x == nullptr || x->dim() != 2 || !weights(w, at::kBFloat16, &dev, &E, &N, &K) || N % 2) return status(LOOK);
+  const int64_t M = x->size(0);
+  if (!fits_int(M) || !plain2(x, at::kBFloat16, dev, M, K) || !plain2(h, at::kBFloat16, dev, M, N / 2) ||
+      !optional(a[3], &gu, [&](const at::Tensor* t) { return plain2(t, at::kBFloat16, dev, M, N); }) ||
+      !optional(a[4], &offsets, [&](const at::Tensor* t) { return plain1(t, at::kInt, dev, E + 1); }) ||
+      !to_int(a[5], &act))
+    return status(LOOK);
+  flint_moe_stream_t st;
+  if (!to_stream(a[6], dev, &st)) return status(LOOK);
+  return call([&] {
+    return g_linear.gated_linear(in(x), (int)M, in(w), (int)E, places(offsets), (int)(N / 2), (int)K, act, out(h),
+                                 out(gu), st);
+  });
+} catch (...) {
+  return status(LOOK);
+}
+
+// gated_linear_backward(dh, gu, x, w, dgu, dx | None, dw | None, offsets | None, act, stream)
+PyObject* py_gated_linear_backward(PyObject*, PyObject* const* a, Py_ssize_t n) try {
+  if (n != 10 || g_linear.gated_linear_backward == nullptr) return status(LOOK);
+  const at::Tensor *dh = tensor(a[0]), *gu = tensor(a[1]), *x = tensor(a[2]), *w = tensor(a[3]), *dgu = tensor(a[4]);
+  const at::Tensor *dx, *dw, *offsets;
+  int dev, act;
+  int64_t E, N, K;
+  if (dh == nullptr || dh->dim() != 2 || !weights(w, at::kBFloat16, &dev, &E, &N, &K) || N % 2) return status(LOOK);
+  const int64_t M = dh->size(0);
+  if (!fits_int(M) || !plain2(dh, at::kBFloat16, dev, M, N / 2) || !plain2(gu, at::kBFloat16, dev, M, N) ||
+      !plain2(x, at::kBFloat16, dev, M, K) || !plain2(dgu, at::kBFloat16, dev, M, N) ||
+      !optional(a[5], &dx, [&](const at::Tensor* t) { return plain2(t, at::kBFloat16, dev, M, K); }) ||
+      !optional(a[6], &dw, [&](const at::Tensor* t) { return act_type(*t) >= 0 && plain3(t, t->scalar_type(), dev, E, N, K); }) ||
+      !optional(a[7], &offsets, [&](const at::Tensor* t) { return plain1(t, at::kInt, dev, E + 1); }) ||
+      !to_int(a[8], &act))
+    return status(LOOK);
+  flint_moe_stream_t st;
+  if (!to_stream(a[9], dev, &st)) return status(LOOK);
+  const int type = dw ? act_type(*dw) : FLINT_MOE_T_BF16;
+  return call([&] {
+    return g_linear.gated_linear_backward(in(dh), in(gu), in(x), (int)M, in(w), (int)E, places(offsets), (int)(N / 2),
+                                          (int)K, act, out(dgu), out(dx), out(dw), type, st);
+  });
+} catch (...) {
+  return status(LOOK);
+}
+
+// integer_quantize_rows(x, q, scales, pos | None, stream)
+PyObject* py_integer_quantize_rows(PyObject*, PyObject* const* a, Py_ssize_t n) try {
+  if (n != 5 || g_linear.integer_quantize_rows == nullptr) return status(LOOK);
+  const at::Tensor *x = tensor(a[0]), *q = tensor(a[1]), *s = tensor(a[2]), *pos;
+  if (x == nullptr || q == nullptr || x->dim() != 2 || q->dim() != 2) return status(LOOK);
+  const int dev = device_of(*x), type = act_type(*x);
+  const int64_t rows = x->size(0), K = x->size(1), to = q->size(0);
+  if (dev < 0 || type < 0 || !fits_int(rows) || !fits_int(K) || !fits_int(to) || x->stride(1) != 1) return status(LOOK);
+  if (!plain2(q, at::kChar, dev, to, K) || !plain1(s, at::kFloat, dev, to)) return status(LOOK);
+  if (!optional(a[3], &pos, [&](const at::Tensor* t) {
+        return t->dim() == 2 && fits_int(t->size(1)) && plain2(t, at::kInt, dev, rows, t->size(1));
+      }))
+    return status(LOOK);
+  flint_moe_stream_t st;
+  if (!to_stream(a[4], dev, &st)) return status(LOOK);
+  return call([&] {
+    return g_linear.integer_quantize_rows(in(x), type, rows > 1 ? x->stride(0) : K, (int)rows, (int)K, places(pos),
+                                          pos ? (int)pos->size(1) : 0, (int)to, static_cast<int8_t*>(out(q)),
+                                          static_cast<float*>(out(s)), st);
+  });
+} catch (...) {
+  return status(LOOK);
+}
+
+// integer_gemm(a, a_scales, b, b_scales, y, offsets | None, act, stream)
+PyObject* py_integer_gemm(PyObject*, PyObject* const* a, Py_ssize_t n) try {
+  if (n != 8 || g_linear.integer_gemm == nullptr) return status(LOOK);
+  const at::Tensor *x = tensor(a[0]), *xs = tensor(a[1]), *w = tensor(a[2]), *ws = tensor(a[3]), *y = tensor(a[4]);
+  const at::Tensor* offsets;
+  int dev, act;
+  int64_t E, N, K;
+  if (x == nullptr || y == nullptr || x->dim() != 2 || !weights(w, at::kChar, &dev, &E, &N, &K) || !to_int(a[6], &act))
+    return status(LOOK);
+  const int64_t M = x->size(0), width = act == FLINT_MOE_ACT_NONE ? N : N / 2;
+  const int type = act_type(*y);
+  if (act != FLINT_MOE_ACT_NONE && N % 2) return status(LOOK);
+  if (!fits_int(M) || type < 0 || !plain2(x, at::kChar, dev, M, K) || !plain1(xs, at::kFloat, dev, M) ||
+      !plain2(ws, at::kFloat, dev, E, N) || !plain2(y, y->scalar_type(), dev, M, width) ||
+      !optional(a[5], &offsets, [&](const at::Tensor* t) { return plain1(t, at::kInt, dev, E + 1); }))
+    return status(LOOK);
+  flint_moe_stream_t st;
+  if (!to_stream(a[7], dev, &st)) return status(LOOK);
+  return call([&] {
+    return g_linear.integer_gemm(static_cast<const int8_t*>(in(x)), static_cast<const float*>(in(xs)), (int)M,
+                                 static_cast<const int8_t*>(in(w)), static_cast<const float*>(in(ws)), (int)E,
+                                 places(offsets), (int)N, (int)K, act, out(y), type, st);
+  });
+} catch (...) {
+  return status(LOOK);
+}
+
+// bind_linear(linear, linear_backward, gated_linear, gated_linear_backward, integer_quantize_rows, integer_gemm)
+PyObject* py_bind_linear(PyObject*, PyObject* args) {
+  unsigned long long f[6];
+  if (!PyArg_ParseTuple(args, "KKKKKK", &f[0], &f[1], &f[2], &f[3], &f[4], &f[5])) return nullptr;
+  g_linear.linear = reinterpret_cast<decltype(g_linear.linear)>(f[0]);
+  g_linear.linear_backward = reinterpret_cast<decltype(g_linear.linear_backward)>(f[1]);
+  g_linear.gated_linear = reinterpret_cast<decltype(g_linear.gated_linear)>(f[2]);
+  g_linear.gated_linear_backward = reinterpret_cast<decltype(g_linear.gated_linear_backward)>(f[3]);
+  g_linear.integer_quantize_rows = reinterpret_cast<decltype(g_linear.integer_quantize_rows)>(f[4]);
+  g_linear.integer_gemm = reinterpret_cast<decltype(g_linear.integer_gemm)>(f[5]);
+  Py_RETURN_NONE;
+}
+
 // bind(route, group_pairs, quantize_rows, block_gemm, combine): addresses of the library's entry points
 PyObject* py_bind(PyObject*, PyObject* args) {
   unsigned long long f[5];
@@ -252,6 +441,9 @@ PyObject* py_bind(PyObject*, PyObject* args) {
 #define FAST(name) {#name, reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(py_##name)), METH_FASTCALL, nullptr}
 PyMethodDef methods[] = {FAST(route),      FAST(group_pairs), FAST(quantize_rows),
                          FAST(block_gemm), FAST(combine),     {"bind", py_bind, METH_VARARGS, nullptr},
+                         FAST(linear),     FAST(linear_backward), FAST(gated_linear), FAST(gated_linear_backward),
+                         FAST(integer_quantize_rows), FAST(integer_gemm),
+                         {"bind_linear", py_bind_linear, METH_VARARGS, nullptr},
                          {nullptr, nullptr, 0, nullptr}};
 PyModuleDef module_def = {PyModuleDef_HEAD_INIT, "_flint_binding", nullptr, -1, methods, nullptr, nullptr, nullptr, nullptr};
 

@@ -180,6 +180,38 @@ cudaError_t launch_block_gemm(const void* a, const float* sa, int M, const void*
                               const int32_t* offsets, int N, int K, void* y, bool f32, int sm_count, unsigned* err,
                               cudaStream_t st);
 
+// Linear, gated and 8-bit integer products of any shape (linear_api.cu and the
+// kernels' files).  What the calls need of the library's set-up of the current device:
+int device_info(int* sm_count, unsigned** err);  // a status; takes the library's lock
+enum { FFN_NONE = 0, FFN_SILU = 1, FFN_GELU = 2 };
+struct ProductArgs {
+  const void* x;           // [M][K]
+  const void* w;           // [E][N][K]
+  const int32_t* offsets;  // [E + 1], or null: dense
+  void* y;                 // [M][N], gated [M][N / 2]
+  void* keep;              // gated, bf16: [M][N] sums, or null
+  const float* sx;         // 8-bit integers: scales [M] and [E][N]
+  const float* sw;
+  int M, N, K, E, act, f32;  // f32: y is fp32
+};
+cudaError_t launch_few_rows(const ProductArgs& p, bool int8, cudaStream_t st);  // few_rows.cu
+// dgu [M][2 I] from dh [M][I] and the kept sums gu [M][2 I] (gradients.cu)
+cudaError_t launch_gate_backward(const void* dh, const void* gu, const int32_t* offsets, int M, int I, int E, int act,
+                                 void* dgu, cudaStream_t st);
+// dx [M][K] = dy [M][N] w, or dw [E][N][K] = dy^T x by expert (gradients.cu)
+struct GradArgs {
+  const void* dy;
+  const void* other;  // w or x
+  const int32_t* offsets;
+  void* out;
+  int M, N, K, E, f32;
+};
+cudaError_t launch_input_gradient(const GradArgs& p, cudaStream_t st);
+cudaError_t launch_weight_gradient(const GradArgs& p, cudaStream_t st);
+// Rows to 8-bit integers with one scale each (integer_rows.cu)
+cudaError_t launch_integer_rows(const void* x, bool bf16, long long stride, int rows, int K, const int32_t* pos,
+                                int top_k, int places, void* q, float* scales, cudaStream_t st);
+
 cudaError_t launch_pack(int fmt, const void* gate_up, const uint8_t* gu_scales, const void* down,
                         const uint8_t* dn_scales, void* packed, cudaStream_t st);
 

@@ -1,0 +1,184 @@
+// Rows to 8-bit integers with one scale each, written to every place that the routing
+// gives a row.
+#include "product_common.cuh"
+
+namespace flint {
+
+namespace {
+
+// Smallest row maximum that a scale is made for.
+constexpr float ROW_FLOOR = 1.262177448353618888658765704e-29f;  // 2^-96
+
+struct IntRowsArgs {
+  const void* x;
+  long long stride;
+  int rows, K;
+  const int32_t* pos;
+  int top_k, places;
+  uint8_t* q;
+  float* scales;
+};
+
+// The larger magnitude, NaN if either is.
+__device__ __forceinline__ float max_magnitude(float a, float b) {
+  float r;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(fabsf(a)), "f"(fabsf(b)));
+  return r;
+}
+
+// 16 values of a row as they lie: 2 (bf16) or 4 (fp32) pieces of 16 bytes.
+template <bool BF16>
+struct Raw16 {
+  uint4 v[BF16 ? 2 : 4];
+  __device__ __forceinline__ void load(const void* base, size_t at) {
+    const uint4* s = reinterpret_cast<const uint4*>(static_cast<const uint8_t*>(base) + at * (BF16 ? 2 : 4));
+#pragma unroll
+    for (int i = 0; i < (BF16 ? 2 : 4); ++i) v[i] = __ldg(s + i);
+  }
+  __device__ __forceinline__ void zero() {
+#pragma unroll
+    for (int i = 0; i < (BF16 ? 2 : 4); ++i) v[i] = make_uint4(0, 0, 0, 0);
+  }
+  __device__ __forceinline__ float value(int i) const {
+    const uint4& w = v[BF16 ? i >> 3 : i >> 2];
+    const int c = BF16 ? (i >> 1) & 3 : i & 3;
+    const uint32_t b = c == 0 ? w.x : c == 1 ? w.y : c == 2 ? w.z : w.w;
+    if (!BF16) return __uint_as_float(b);
+    return __uint_as_float(i & 1 ? b & 0xFFFF0000u : b << 16);
+  }
+  __device__ __forceinline__ float top() const {
+    float a = 0.f;
+#pragma unroll
+    for (int i = 0; i < 16; ++i) a = max_magnitude(a, value(i));
+    return a;
+  }
+};
+
+// The whole number next to v / s, ties to even, in the low byte.  v * (1 / s) is off by
+// 2^-16 of a step at most, so only next to a border (one bf16 value in 200 is a tie) does
+// the exact remainder v - n * s, a multiple of the scale's last bit, decide.
+__device__ __forceinline__ uint32_t code(float v, float s, float inv) {
+  constexpr float MAGIC = 12582912.f;  // 1.5 * 2^23: its unit is 1
+  const float t = v * inv;
+  float m = t + MAGIC;
+  const float n = m - MAGIC;
+  if (fabsf(t - n) > 0.4999f) {
+    const float rest = fmaf(-n, s, v), twice = 2.f * fabsf(rest);
+    if (twice > s || (twice == s && (__float_as_uint(m) & 1u))) m += copysignf(1.f, rest);
+  }
+  return __float_as_uint(m);
+}
+
+// a = max(largest magnitude of the row, 2^-96), scale = a / 127, code = the whole number
+// next to x / scale.  THREADS lanes of a CTA of 256 have a row: each 16 neighbouring
+// values at a time, the first HELD x 16 of them kept in registers between the two passes
+// (a longer row is read a second time).  Bound by HBM.
+template <bool BF16, int THREADS>
+__global__ void __launch_bounds__(256) integer_rows_kernel(const IntRowsArgs p) {
+  constexpr int HELD = 4;
+  __shared__ float tops[8];
+  pdl_wait();
+  pdl_trigger();
+  const int lane = threadIdx.x % THREADS, warp = threadIdx.x >> 5;
+  const int row = blockIdx.x * (256 / THREADS) + threadIdx.x / THREADS;
+  const bool in = row < p.rows;
+  const size_t base = (size_t)row * (size_t)p.stride;
+  Raw16<BF16> held[HELD];
+#pragma unroll
+  for (int i = 0; i < HELD; ++i) {
+    const int k = (i * THREADS + lane) * 16;
+    if (in && k < p.K) held[i].load(p.x, base + k);  // K is a multiple of 16
+    else held[i].zero();
+  }
+  float a = 0.f;
+#pragma unroll
+  for (int i = 0; i < HELD; ++i) a = max_magnitude(a, held[i].top());
+  if (in)
+    for (int k = (HELD * THREADS + lane) * 16; k < p.K; k += THREADS * 16) {
+      Raw16<BF16> v;
+      v.load(p.x, base + k);
+      a = max_magnitude(a, v.top());
+    }
+#pragma unroll
+  for (int off = 16; off > 0; off >>= 1) a = max_magnitude(a, __shfl_xor_sync(0xffffffffu, a, off));
+  if (THREADS > 32) {
+    if ((threadIdx.x & 31) == 0) tops[warp] = a;
+    __syncthreads();
+    constexpr int WARPS = THREADS / 32;
+#pragma unroll
+    for (int i = 0; i < WARPS; ++i) a = max_magnitude(a, tops[warp / WARPS * WARPS + i]);
+  }
+  if (!in) return;
+  if (a < ROW_FLOOR) a = ROW_FLOOR;  // false for NaN
+  const float scale = __fdiv_rn(a, 127.f), inv = __frcp_rn(scale);
+  const bool fine = scale < INFINITY;  // false for NaN: the codes of such a row are 0
+  const int32_t* pos = p.pos + (size_t)row * p.top_k;
+  auto put = [&](const Raw16<BF16>& v, int k) {
+    uint32_t c[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const uint32_t lo = __byte_perm(code(v.value(4 * i), scale, inv), code(v.value(4 * i + 1), scale, inv), 0x0040);
+      const uint32_t hi = __byte_perm(code(v.value(4 * i + 2), scale, inv), code(v.value(4 * i + 3), scale, inv), 0x0040);
+      c[i] = fine ? __byte_perm(lo, hi, 0x5410) : 0u;
+    }
+    const uint4 codes = make_uint4(c[0], c[1], c[2], c[3]);
+    if (p.pos == nullptr) {
+      *reinterpret_cast<uint4*>(p.q + (size_t)row * p.K + k) = codes;
+      return;
+    }
+    for (int j = 0; j < p.top_k; ++j) {
+      const int place = __ldg(pos + j);
+      if (place >= 0 && place < p.places) *reinterpret_cast<uint4*>(p.q + (size_t)place * p.K + k) = codes;
+    }
+  };
+#pragma unroll
+  for (int i = 0; i < HELD; ++i) {
+    const int k = (i * THREADS + lane) * 16;
+    if (k < p.K) put(held[i], k);
+  }
+  for (int k = (HELD * THREADS + lane) * 16; k < p.K; k += THREADS * 16) {
+    Raw16<BF16> v;
+    v.load(p.x, base + k);
+    put(v, k);
+  }
+  if (p.pos == nullptr) {
+    if (lane == 0) p.scales[row] = scale;
+  } else if (lane < p.top_k) {
+    const int place = __ldg(pos + lane);
+    if (place >= 0 && place < p.places) p.scales[place] = scale;
+  }
+}
+
+template <bool BF16, int THREADS>
+cudaError_t launch(const IntRowsArgs& p, cudaStream_t st) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)((p.rows + 256 / THREADS - 1) / (256 / THREADS)));
+  cfg.blockDim = dim3(256);
+  cfg.stream = st;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, integer_rows_kernel<BF16, THREADS>, p);
+}
+
+}  // namespace
+
+cudaError_t launch_integer_rows(const void* x, bool bf16, long long stride, int rows, int K, const int32_t* pos,
+                                int top_k, int places, void* q, float* scales, cudaStream_t st) {
+  IntRowsArgs p;
+  p.x = x;
+  p.stride = stride;
+  p.rows = rows;
+  p.K = K;
+  p.pos = pos;
+  p.top_k = top_k;
+  p.places = places;
+  p.q = static_cast<uint8_t*>(q);
+  p.scales = scales;
+  if (K <= 2048) return bf16 ? launch<true, 32>(p, st) : launch<false, 32>(p, st);
+  return bf16 ? launch<true, 256>(p, st) : launch<false, 256>(p, st);
+}
+
+}  // namespace flint

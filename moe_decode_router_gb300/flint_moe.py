@@ -1,8 +1,9 @@
 """ctypes binding of libflint_moe.so (include/flint_moe.h), same entry-point names.
 
 Argument marshalling only: tensors are passed as device pointers, the stream
-is torch's current CUDA stream unless one is given.  The FP8 expert calls, a few
-microseconds each, are marshalled by compiled code (csrc/binding.cpp) first.  Every computation runs in
+is torch's current CUDA stream unless one is given.  The FP8 expert calls and the linear,
+gated and integer products, a few microseconds each, are marshalled by compiled code
+(csrc/binding.cpp) first.  Every computation runs in
 the library's CUDA kernels; there is no fallback path.  If the library cannot
 be built or loaded the import-time call ``load_library`` raises.
 """
@@ -41,6 +42,10 @@ SCORE_SOFTMAX = 1
 
 GROUP_MAX = 0
 GROUP_TOP2 = 1
+
+ACT_NONE = 0
+ACT_SILU = 1
+ACT_GELU = 2
 
 SCALE_BLOCK = 128  # elements of K that share a scale (and rows of a weight matrix)
 
@@ -128,7 +133,17 @@ _SIGS = {
     "flint_moe_status_string": (ctypes.c_char_p, [ctypes.c_int]),
 }
 
-EXPORTED = tuple(_SIGS)
+_P, _I = ctypes.c_void_p, ctypes.c_int
+_LINEAR_SIGS = {  # csrc/linear_api.cu
+    "flint_moe_linear": (_I, [_P, _I, _P, _I, _P, _I, _I, _P, _I, _P]),
+    "flint_moe_linear_backward": (_I, [_P, _P, _I, _P, _I, _P, _I, _I, _P, _P, _I, _P]),
+    "flint_moe_gated_linear": (_I, [_P, _I, _P, _I, _P, _I, _I, _I, _P, _P, _P]),
+    "flint_moe_gated_linear_backward": (_I, [_P, _P, _P, _I, _P, _I, _P, _I, _I, _I, _P, _P, _P, _I, _P]),
+    "flint_moe_integer_quantize_rows": (_I, [_P, _I, ctypes.c_longlong, _I, _I, _P, _I, _I, _P, _P, _P]),
+    "flint_moe_integer_gemm": (_I, [_P, _P, _I, _P, _P, _I, _P, _I, _I, _I, _P, _I, _P]),
+}
+
+EXPORTED = (*_SIGS, *_LINEAR_SIGS)
 
 
 def load_library(build_if_missing: bool = True) -> ctypes.CDLL:
@@ -144,7 +159,7 @@ def load_library(build_if_missing: bool = True) -> ctypes.CDLL:
             raise RuntimeError(f"libflint_moe.so not found at {path}; build it with "
                                "python -m moe_decode_router_gb300.build")
         lib = ctypes.CDLL(path)
-        for name, (res, args) in _SIGS.items():
+        for name, (res, args) in (_SIGS | _LINEAR_SIGS).items():
             fn = getattr(lib, name)
             fn.restype = res
             fn.argtypes = args
@@ -180,6 +195,7 @@ def _binding(lib):
     loader.exec_module(module)
     module.bind(*(ctypes.cast(getattr(lib, f"flint_moe_{name}"), ctypes.c_void_p).value
                   for name in ("route", "group_pairs", "quantize_rows", "block_gemm", "combine")))
+    module.bind_linear(*(ctypes.cast(getattr(lib, name), ctypes.c_void_p).value for name in _LINEAR_SIGS))
     return module
 
 
@@ -570,6 +586,149 @@ def combine(rows, pos, w, y, shared=None, stream=None):
                                       _ptr(shared), y.data_ptr(), _stream(stream))
     if rc:
         _check(rc, "flint_moe_combine")
+
+
+def _products(w, name, dtype, gated=False):
+    """Experts, N and K of a weight tensor [experts][N][K]; gated: N is even."""
+    if not isinstance(w, torch.Tensor):
+        raise TypeError(f"{name}: expected a torch.Tensor, got {type(w).__name__}")
+    if w.dim() != 3 or (gated and w.shape[1] % 2):
+        raise ValueError(f"{name}: expected [experts][{'2I' if gated else 'N'}][K], got shape {tuple(w.shape)}")
+    _counts(w, name)
+    _expect(w, name, dtype, w.shape)
+    return w.shape
+
+
+def _offsets(offsets, E):
+    if offsets is not None:
+        _expect(offsets, "offsets", torch.int32, (E + 1,))
+    return _ptr(offsets)
+
+
+def _output(t, name, shape):
+    """_expect for an output of bf16 or fp32; returns its type code."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name}: expected a torch.Tensor, got {type(t).__name__}")
+    if t.dtype not in _ACT_TYPES:
+        raise ValueError(f"{name}: dtype {t.dtype}, expected {' or '.join(str(d) for d in _ACT_TYPES)}")
+    _expect(t, name, t.dtype, shape)
+    return _ACT_TYPES[t.dtype]
+
+
+def _code(act):
+    if abs(act) > 0x7FFFFFFF:
+        raise ValueError(f"act: {act}, more than 31 bits")
+    return act
+
+
+def linear(x, w, y, offsets=None, stream=None):
+    """y [M][N] (bf16 or fp32) = x [M][K] @ w[e]^T in bf16, w [experts][N][K].  offsets int32
+    [experts + 1] gives every expert its rows; None: dense (w of one expert)."""
+    rc = _FAST.linear(x, w, y, offsets, _handle(stream))
+    if rc == _LOOK:
+        M = _matrix(x, "x")[0]
+        E, N, K = _products(w, "w", torch.bfloat16)
+        _expect(x, "x", torch.bfloat16, (M, K))
+        kind = _output(y, "y", (M, N))
+        rc = _lib().flint_moe_linear(x.data_ptr(), M, w.data_ptr(), E, _offsets(offsets, E), N, K, y.data_ptr(), kind,
+                                     _stream(stream))
+    if rc:
+        _check(rc, "flint_moe_linear")
+
+
+def linear_backward(dy, x, w, dx=None, dw=None, offsets=None, stream=None):
+    """Gradients of linear from dy bf16 [M][N]: dx bf16 [M][K] and dw [experts][N][K] (bf16 or
+    fp32), either of which may be None."""
+    rc = _FAST.linear_backward(dy, x, w, dx, dw, offsets, _handle(stream))
+    if rc == _LOOK:
+        M = _matrix(dy, "dy")[0]
+        E, N, K = _products(w, "w", torch.bfloat16)
+        _expect(dy, "dy", torch.bfloat16, (M, N))
+        _expect(x, "x", torch.bfloat16, (M, K))
+        if dx is not None:
+            _expect(dx, "dx", torch.bfloat16, (M, K))
+        kind = T_BF16 if dw is None else _output(dw, "dw", (E, N, K))
+        rc = _lib().flint_moe_linear_backward(dy.data_ptr(), x.data_ptr(), M, w.data_ptr(), E, _offsets(offsets, E), N,
+                                              K, _ptr(dx), _ptr(dw), kind, _stream(stream))
+    if rc:
+        _check(rc, "flint_moe_linear_backward")
+
+
+def gated_linear(x, w, h, gu=None, offsets=None, act=ACT_SILU, stream=None):
+    """h [M][I] = act(x @ gate^T) * (x @ up^T), all bf16: x [M][K], w [experts][2I][K] (the gate's
+    rows, then the other factor's); gu bf16 [M][2I] takes the sums that the gradient needs."""
+    rc = _FAST.gated_linear(x, w, h, gu, offsets, act, _handle(stream))
+    if rc == _LOOK:
+        M = _matrix(x, "x")[0]
+        E, N, K = _products(w, "w", torch.bfloat16, gated=True)
+        _expect(x, "x", torch.bfloat16, (M, K))
+        _expect(h, "h", torch.bfloat16, (M, N // 2))
+        if gu is not None:
+            _expect(gu, "gu", torch.bfloat16, (M, N))
+        rc = _lib().flint_moe_gated_linear(x.data_ptr(), M, w.data_ptr(), E, _offsets(offsets, E), N // 2, K,
+                                           _code(act), h.data_ptr(), _ptr(gu), _stream(stream))
+    if rc:
+        _check(rc, "flint_moe_gated_linear")
+
+
+def gated_linear_backward(dh, gu, x, w, dgu, dx=None, dw=None, offsets=None, act=ACT_SILU, stream=None):
+    """Gradients of gated_linear from dh bf16 [M][I] and the kept gu: dgu bf16 [M][2I], and dx bf16
+    [M][K] and dw [experts][2I][K] (bf16 or fp32) where they are given."""
+    rc = _FAST.gated_linear_backward(dh, gu, x, w, dgu, dx, dw, offsets, act, _handle(stream))
+    if rc == _LOOK:
+        M = _matrix(dh, "dh")[0]
+        E, N, K = _products(w, "w", torch.bfloat16, gated=True)
+        _expect(dh, "dh", torch.bfloat16, (M, N // 2))
+        _expect(gu, "gu", torch.bfloat16, (M, N))
+        _expect(x, "x", torch.bfloat16, (M, K))
+        _expect(dgu, "dgu", torch.bfloat16, (M, N))
+        if dx is not None:
+            _expect(dx, "dx", torch.bfloat16, (M, K))
+        kind = T_BF16 if dw is None else _output(dw, "dw", (E, N, K))
+        rc = _lib().flint_moe_gated_linear_backward(dh.data_ptr(), gu.data_ptr(), x.data_ptr(), M, w.data_ptr(), E,
+                                                    _offsets(offsets, E), N // 2, K, _code(act), dgu.data_ptr(),
+                                                    _ptr(dx), _ptr(dw), kind, _stream(stream))
+    if rc:
+        _check(rc, "flint_moe_gated_linear_backward")
+
+
+def integer_quantize_rows(x, q, scales, pos=None, stream=None):
+    """Quantises x [rows][K] (bf16 or fp32, rows may lie apart) to q int8 [places][K] with one scale
+    a row, fp32 [places]; pos int32 [rows][k] gives the places of each row, None: row i goes to
+    place i."""
+    rc = _FAST.integer_quantize_rows(x, q, scales, pos, _handle(stream))
+    if rc == _LOOK:
+        places, K = _matrix(q, "q")
+        kind, rows, _, stride = _expect_rows(x, "x", K)
+        _expect(q, "q", torch.int8, (places, K))
+        _expect(scales, "scales", torch.float32, (places,))
+        k = 0
+        if pos is not None:
+            k = _matrix(pos, "pos")[1]
+            _expect(pos, "pos", torch.int32, (rows, k))
+        rc = _lib().flint_moe_integer_quantize_rows(x.data_ptr(), kind, stride, rows, K, _ptr(pos), k, places,
+                                                    q.data_ptr(), scales.data_ptr(), _stream(stream))
+    if rc:
+        _check(rc, "flint_moe_integer_quantize_rows")
+
+
+def integer_gemm(a, a_scales, b, b_scales, y, offsets=None, act=ACT_NONE, stream=None):
+    """y [M][N] (bf16 or fp32) = a @ b[e]^T of int8 operands, times a_scales fp32 [M] and b_scales
+    fp32 [experts][N]: a [M][K], b [experts][N][K].  With an activation N is 2I and y [M][I] =
+    act(first half) * second half.  offsets int32 [experts + 1] gives every expert its rows; None:
+    dense (b of one expert)."""
+    rc = _FAST.integer_gemm(a, a_scales, b, b_scales, y, offsets, act, _handle(stream))
+    if rc == _LOOK:
+        M = _matrix(a, "a")[0]
+        E, N, K = _products(b, "b", torch.int8, gated=act != ACT_NONE)
+        _expect(a, "a", torch.int8, (M, K))
+        _expect(a_scales, "a_scales", torch.float32, (M,))
+        _expect(b_scales, "b_scales", torch.float32, (E, N))
+        kind = _output(y, "y", (M, N if act == ACT_NONE else N // 2))
+        rc = _lib().flint_moe_integer_gemm(a.data_ptr(), a_scales.data_ptr(), M, b.data_ptr(), b_scales.data_ptr(), E,
+                                           _offsets(offsets, E), N, K, _code(act), y.data_ptr(), kind, _stream(stream))
+    if rc:
+        _check(rc, "flint_moe_integer_gemm")
 
 
 def release():
