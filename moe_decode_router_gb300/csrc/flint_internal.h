@@ -198,7 +198,7 @@ cudaError_t launch_few_rows(const ProductArgs& p, bool int8, cudaStream_t st);  
 // dgu [M][2 I] from dh [M][I] and the kept sums gu [M][2 I] (gradients.cu)
 cudaError_t launch_gate_backward(const void* dh, const void* gu, const int32_t* offsets, int M, int I, int E, int act,
                                  void* dgu, cudaStream_t st);
-// dx [M][K] = dy [M][N] w, or dw [E][N][K] = dy^T x by expert (gradients.cu)
+// dx [M][K] = dy [M][N] w, or dw [E][N][K] = dy^T x by expert
 struct GradArgs {
   const void* dy;
   const void* other;  // w or x
@@ -206,8 +206,11 @@ struct GradArgs {
   void* out;
   int M, N, K, E, f32;
 };
-cudaError_t launch_input_gradient(const GradArgs& p, cudaStream_t st);
-cudaError_t launch_weight_gradient(const GradArgs& p, cudaStream_t st);
+// tcgen05 over pairs of CTAs (pair_gemm.cu)
+cudaError_t pair_gemm_kernels_init();
+cudaError_t launch_pair_forward(const ProductArgs& p, int sm_count, unsigned* err, cudaStream_t st);
+cudaError_t launch_pair_input(const GradArgs& p, int sm_count, unsigned* err, cudaStream_t st);
+cudaError_t launch_pair_weights(const GradArgs& p, int sm_count, unsigned* err, cudaStream_t st);
 // Rows to 8-bit integers with one scale each (integer_rows.cu)
 cudaError_t launch_integer_rows(const void* x, bool bf16, long long stride, int rows, int K, const int32_t* pos,
                                 int top_k, int places, void* q, float* scales, cudaStream_t st);

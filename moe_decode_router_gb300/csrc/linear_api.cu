@@ -1,6 +1,8 @@
 // C ABI of the linear, gated and 8-bit integer products: argument validation and the
 // choice of kernels.  See include/flint_moe.h.
 #include <initializer_list>
+#include <map>
+#include <mutex>
 
 #include "flint_internal.h"
 #include "flint_moe.h"
@@ -63,16 +65,39 @@ static_assert((int)FFN_NONE == (int)FLINT_MOE_ACT_NONE && (int)FFN_SILU == (int)
                   (int)FFN_GELU == (int)FLINT_MOE_ACT_GELU,
               "activations");
 
-int product(const ProductArgs& p, bool int8, flint_moe_stream_t stream) {
+// The current device's set-up: the library's, and once that of the tensor-core kernels, whose
+// failure is these calls' alone.
+struct Device {
   int sms = 0;
   unsigned* err = nullptr;
-  const int st = device_info(&sms, &err);
+};
+int set_up(Device* d) {
+  const int st = device_info(&d->sms, &d->err);
   if (st != FLINT_MOE_OK) return st;
-  return to_status(launch_few_rows(p, int8, reinterpret_cast<cudaStream_t>(stream)));
+  static std::mutex mu;
+  static std::map<int, bool> ready;
+  int dev = -1;
+  if (cudaGetDevice(&dev) != cudaSuccess) return FLINT_MOE_ERR_CUDA;
+  std::lock_guard<std::mutex> lk(mu);
+  auto it = ready.find(dev);
+  if (it == ready.end()) {
+    it = ready.emplace(dev, pair_gemm_kernels_init() == cudaSuccess).first;
+    if (!it->second) (void)cudaGetLastError();
+  }
+  return it->second ? FLINT_MOE_OK : FLINT_MOE_ERR_CUDA;
+}
+
+int product(const ProductArgs& p, bool int8, flint_moe_stream_t stream) {
+  Device d;
+  const int rc = set_up(&d);
+  if (rc != FLINT_MOE_OK) return rc;
+  cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+  if (int8 || p.M <= 8) return to_status(launch_few_rows(p, int8, st));
+  return to_status(launch_pair_forward(p, d.sms, d.err, st));
 }
 
 int gradients(const void* dy, const void* x, int M, const void* w, int E, const int32_t* offsets, int N, int K,
-              void* dx, void* dw, int dw_type, cudaStream_t st) {
+              void* dx, void* dw, int dw_type, const Device& d, cudaStream_t st) {
   GradArgs p;
   p.dy = dy;
   p.offsets = offsets;
@@ -85,13 +110,13 @@ int gradients(const void* dy, const void* x, int M, const void* w, int E, const 
     p.other = w;
     p.out = dx;
     p.f32 = 0;
-    e = launch_input_gradient(p, st);
+    e = launch_pair_input(p, d.sms, d.err, st);
   }
   if (e == cudaSuccess && dw != nullptr) {
     p.other = x;
     p.out = dw;
     p.f32 = dw_type == FLINT_MOE_T_F32;
-    e = launch_weight_gradient(p, st);
+    e = launch_pair_weights(p, d.sms, d.err, st);
   }
   return to_status(e);
 }
@@ -142,10 +167,10 @@ int flint_moe_linear_backward(const void* dy, const void* x, int M, const void* 
   if (bad_buffers({}, {{dy, (size_t)M * N * 2}, {x, (size_t)M * K * 2}, {w, weights * 2}},
                   {{dx, (size_t)M * K * 2}, {dw, weights * type_size(dw_type)}}, {{offsets, offset_bytes(n_experts)}}))
     return FLINT_MOE_ERR_INVALID_ARG;
-  int sms = 0;
-  unsigned* err = nullptr;
-  if ((st = device_info(&sms, &err)) != FLINT_MOE_OK) return st;
-  return gradients(dy, x, M, w, n_experts, offsets, N, K, dx, dw, dw_type, reinterpret_cast<cudaStream_t>(stream));
+  Device d;
+  if ((st = set_up(&d)) != FLINT_MOE_OK) return st;
+  return gradients(dy, x, M, w, n_experts, offsets, N, K, dx, dw, dw_type, d,
+                   reinterpret_cast<cudaStream_t>(stream));
 }
 
 int flint_moe_gated_linear_backward(const void* dh, const void* gu, const void* x, int M, const void* w, int n_experts,
@@ -160,12 +185,11 @@ int flint_moe_gated_linear_backward(const void* dh, const void* gu, const void* 
   if (bad_buffers({{dgu, sums}}, {{dh, (size_t)M * I * 2}, {gu, sums}, {x, (size_t)M * K * 2}, {w, weights * 2}},
                   {{dx, (size_t)M * K * 2}, {dw, weights * type_size(dw_type)}}, {{offsets, offset_bytes(n_experts)}}))
     return FLINT_MOE_ERR_INVALID_ARG;
-  int sms = 0;
-  unsigned* err = nullptr;
-  if ((st = device_info(&sms, &err)) != FLINT_MOE_OK) return st;
+  Device d;
+  if ((st = set_up(&d)) != FLINT_MOE_OK) return st;
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   if (launch_gate_backward(dh, gu, offsets, M, I, n_experts, act, dgu, s) != cudaSuccess) return FLINT_MOE_ERR_CUDA;
-  return gradients(dgu, x, M, w, n_experts, offsets, 2 * I, K, dx, dw, dw_type, s);
+  return gradients(dgu, x, M, w, n_experts, offsets, 2 * I, K, dx, dw, dw_type, d, s);
 }
 
 int flint_moe_integer_quantize_rows(const void* x, int x_type, long long row_stride, int rows, int K,
@@ -183,9 +207,8 @@ int flint_moe_integer_quantize_rows(const void* x, int x_type, long long row_str
                   {{x, ((size_t)(rows - 1) * (size_t)row_stride + K) * size}}, {},
                   {{pos, (size_t)rows * (pos ? top_k : 0) * 4}}))
     return FLINT_MOE_ERR_INVALID_ARG;
-  int sms = 0;
-  unsigned* err = nullptr;
-  const int st = device_info(&sms, &err);
+  Device d;
+  const int st = set_up(&d);
   if (st != FLINT_MOE_OK) return st;
   return to_status(launch_integer_rows(x, x_type == FLINT_MOE_T_BF16, row_stride, rows, K, pos, top_k, places, q,
                                        scales, reinterpret_cast<cudaStream_t>(stream)));

@@ -1,0 +1,578 @@
+// bf16 products on the tensor cores (tcgen05 over pairs of CTAs), dense or grouped by
+// expert: linear and gated products and their gradients.
+//
+// One kernel for three products.  The M side of the MMA is the dimension that lies
+// contiguous in the output (i), always 256 of it a unit; the N side (o), up to 256 in
+// steps of 32, is what is ragged:
+//   FORWARD  y[m][n]     i = n: weights by rows       o = m: rows of x       sum over k
+//   INPUT    dx[m][k]    i = k: weights by columns    o = m: rows of dy      sum over n
+//   WEIGHTS  dw[e][n][k] i = k: columns of x          o = n: columns of dy   sum over the rows m of e
+// An operand whose M or N dimension is contiguous in memory is taken as it lies (the
+// descriptors' other major order), so nothing is transposed on the way in; on the way out
+// the accumulator (lanes i, columns o) is turned by stmatrix into rows of the output.
+//
+// A gated unit has 8 strips of 16 gate rows and the 16 rows of the other factor that
+// belong to them, so that a warp's 32 lanes hold both and the thread that reads a gate's
+// sum reads its partner's.
+//
+// Each CTA loads its 128 rows of A and half of B, 64 of the contracted dimension at a time
+// (128 bytes, 128-byte swizzle): 32 KB a stage and CTA against 512 cycles of MMA, 64 bytes
+// a cycle and SM; a CTA by itself would load 96.  The accumulator is double-buffered in
+// tensor memory, so that a unit's output overlaps the next one's products.
+//
+// WEIGHTS contracts over an expert's rows, which end anywhere: whole steps of 16 rows are
+// multiplied, and in the last a warp of each CTA overwrites the rows behind the end (another
+// expert's, perhaps infinite) with zeros before the stage is handed on.
+//
+// Warps: 0-7 output, two halves of the columns; 8 TMA producer; 9 MMA issuer (of the even
+// CTA); 10 rows behind the end (WEIGHTS); 11 none.
+#include <initializer_list>
+
+#include "product_common.cuh"
+#include "tc05_pair.cuh"
+
+namespace flint {
+
+namespace {
+
+enum { FORWARD, INPUT, WEIGHTS };
+
+constexpr int PAIR_THREADS = 384;
+constexpr int A_BYTES = 128 * 128, B_BYTES = 128 * 128, STAGE = A_BYTES + B_BYTES, STAGES = 6;
+constexpr int OUT_WARP = 32 * 80;  // output staging of a warp: 32 rows of 64 bytes, 80 apart
+constexpr int OFF_OUT = STAGES * STAGE;
+constexpr int OFF_BARS = OFF_OUT + 8 * OUT_WARP;
+constexpr int OFF_GROUPS = OFF_BARS + 256;
+constexpr int pair_smem(int E) { return OFF_GROUPS + (3 * E + 1) * 4; }
+static_assert(pair_smem(ROUTE_MAX_E) <= 232448, "shared memory");
+static_assert((3 * STAGES + 4) * 8 + 8 <= 256, "barriers");
+
+struct PairArgs {
+  const int32_t* offsets;
+  void* y;
+  uint16_t* keep;  // gated: the sums, or null
+  unsigned* err;
+  int M, E;
+  int I;        // width of the output (i)
+  int O;        // WEIGHTS: N
+  int steps;    // FORWARD, INPUT: steps of 64 of the contracted dimension
+  int a_tiles;  // units side by side in i
+  int tile;     // o's of a unit, at most: a multiple of 32
+  int o_tiles;  // WEIGHTS: units side by side in o
+  int box;      // rows of B in one copy
+  int band;     // tiles of o that go side by side
+  int act;
+};
+
+struct Unit {
+  int e, at, o0, cnt, n;  // tile of i; first o and how many; columns of the MMAs
+  int c0, clen;           // WEIGHTS: the expert's rows
+};
+
+template <int MODE, bool GATED, bool F32>
+__global__ void __launch_bounds__(PAIR_THREADS, 1)
+    pair_gemm_kernel(const PairArgs p, const __grid_constant__ CUtensorMap map_a,
+                     const __grid_constant__ CUtensorMap map_b) {
+  extern __shared__ __align__(1024) uint8_t smem_raw[];
+  uint8_t* sm = smem_raw;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const uint32_t rank = tc05::cluster_rank();
+  uint64_t* full = reinterpret_cast<uint64_t*>(sm + OFF_BARS);  // [STAGES] both CTAs' operands landed (even CTA's)
+  uint64_t* empty = full + STAGES;                              // [STAGES] stage consumed
+  uint64_t* landed = empty + STAGES;                            // [STAGES] WEIGHTS: a last stage of this CTA landed
+  uint64_t* tfull = landed + STAGES;                            // [2] accumulator complete
+  uint64_t* tempty = tfull + 2;                                 // [2] accumulator read, 16 warps (even CTA's)
+  uint32_t* tslot = reinterpret_cast<uint32_t*>(tempty + 2);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(tslot + 1);
+  int* g_units = reinterpret_cast<int*>(sm + OFF_GROUPS);  // [E + 1] units before each group
+  int* g_lo = g_units + p.E + 1;                           // [E] first row
+  int* g_cnt = g_lo + p.E;                                 // [E] rows
+
+  if (tid == 0) {
+    for (int i = 0; i < STAGES; ++i) {
+      mbar_init(&full[i], MODE == WEIGHTS ? 2 : 1);
+      mbar_init(&empty[i], 1);
+      mbar_init(&landed[i], 1);
+    }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&tfull[i], 1);
+      mbar_init(&tempty[i], 16);
+    }
+    *abort_flag = 0;
+    fence_mbar_init();
+  }
+  pdl_wait();
+  // Tensor memory is taken when the grid before this one is gone and (below) given back
+  // before either CTA of a pair ends: taking it may wait without a limit for another's.
+  if (warp == 8) {
+    tc05::alloc_pair(tslot, 512);
+    tc05::relinquish_pair();
+  }
+  pdl_trigger();
+  if (p.offsets != nullptr)
+    for (int e = tid; e <= p.E; e += PAIR_THREADS) g_units[e] = __ldg(p.offsets + e);  // all on their way at once
+  __syncthreads();
+  if (warp == 8) {
+    int base = 0;
+    for (int e0 = 0; e0 < p.E; e0 += 32) {
+      const int e = e0 + lane;
+      int lo = 0, cnt = 0;
+      if (e < p.E) {
+        lo = p.offsets ? min(max(g_units[e], 0), p.M) : 0;
+        cnt = p.offsets ? min(max(g_units[e + 1], lo), p.M) - lo : p.M;
+        g_lo[e] = lo;
+        g_cnt[e] = cnt;
+      }
+      __syncwarp();  // the offsets of these groups make room for their units; the next group's first is read below
+      int t = MODE == WEIGHTS ? (e < p.E ? p.o_tiles * p.a_tiles : 0) : (cnt + p.tile - 1) / p.tile * p.a_tiles;
+      if (base > 1 << 29) t = 0;  // offsets that descend could count rows over and over: stay inside int
+      int incl = t;
+#pragma unroll
+      for (int off = 1; off < 32; off <<= 1) {
+        const int v = __shfl_up_sync(0xffffffffu, incl, off);
+        if (lane >= off) incl += v;
+      }
+      if (e < p.E) g_units[e] = base + incl - t;
+      base += __shfl_sync(0xffffffffu, incl, 31);
+    }
+    if (lane == 0) g_units[p.E] = base;
+  }
+  tc05::fence_before_sync();
+  __syncthreads();
+  tc05::cluster_sync();  // both CTAs' barriers are ready
+  tc05::fence_after_sync();
+  const uint32_t tmem = *tslot;
+  const int n_units = g_units[p.E];
+  const int u0 = blockIdx.x >> 1, ustep = gridDim.x >> 1;
+
+  auto unit_of = [&](int u) -> Unit {
+    // The group is the last whose first unit is at or before u: the whole warp looks, at
+    // every 32nd group and then at 32 neighbours.
+    Unit t;
+    int from = 0;
+    if (p.E > 32) from = 32 * (__popc(__ballot_sync(0xffffffffu, 32 * lane < p.E && g_units[32 * lane] <= u)) - 1);
+    const int e = from + lane;
+    t.e = from + __popc(__ballot_sync(0xffffffffu, e < p.E && g_units[e] <= u)) - 1;
+    const int v = u - g_units[t.e], rows = g_cnt[t.e];
+    const int tiles = MODE == WEIGHTS ? p.o_tiles : (rows + p.tile - 1) / p.tile;
+    // bands of neighbouring tiles of o, all of i within a band: what runs at a time shares both operands
+    const int per = p.band * p.a_tiles, first = v / per * p.band, rest = v - v / per * per;
+    const int high = min(p.band, tiles - first);
+    t.at = rest / high;
+    const int tile = first + rest - t.at * high;
+    if (MODE == WEIGHTS) {
+      t.o0 = tile * p.tile;
+      t.cnt = min(p.tile, p.O - t.o0);
+      t.c0 = g_lo[t.e];
+      t.clen = rows;
+    } else {
+      const int size = ((rows + tiles - 1) / tiles + 31) & ~31;  // a group's tiles are of one size, to 32 rows
+      t.o0 = g_lo[t.e] + tile * size;
+      t.cnt = max(0, min(size, rows - tile * size));
+      t.c0 = t.clen = 0;
+    }
+    t.n = max(32, (t.cnt + 31) & ~31);
+    return t;
+  };
+  auto steps_of = [&](const Unit& t) { return MODE == WEIGHTS ? (t.clen + 63) >> 6 : p.steps; };
+  // Bounded wait.  Lanes of a warp that wait together agree on the result: the awaited
+  // phase cannot move on without a later arrival of this same warp.
+  auto wait = [&](uint64_t* bar, uint32_t parity) -> bool {
+    if (mbar_try_wait(bar, parity)) return true;
+    if (*abort_flag) return false;
+    if (mbar_wait(bar, parity)) return true;
+    atomicOr(p.err, ERR_WAIT_FULL);
+    *abort_flag = 1;
+    return false;
+  };
+  const uint32_t base = smem_u32(sm), full0 = tc05::map_rank(smem_u32(full), 0);
+
+  if (warp == 8) {
+    // ---------------- producer: this CTA's 128 of i and its half of the columns
+    uint32_t s = 0, ph = 0, issued = 0;  // of lane 0, which copies
+    bool ok = true;
+    for (int u = u0; u < n_units && ok; u += ustep) {
+      const Unit t = unit_of(u);
+      const int nh = t.n >> 1, steps = steps_of(t);
+      const int i0 = t.at * 256 + (int)rank * 128, oh = t.o0 + (int)rank * nh;
+      const int boxes = MODE == WEIGHTS ? (nh + 63) >> 6 : (nh + p.box - 1) / p.box;
+      const uint32_t bytes = A_BYTES + boxes * (MODE == WEIGHTS ? 8192 : p.box * 128);
+      for (int k = 0; k < steps && lane == 0; ++k) {
+        if (!wait(&empty[s], ph ^ 1)) {
+          ok = false;
+          break;
+        }
+        uint32_t bar = full0 + s * 8;
+        const uint32_t a = base + s * STAGE, b = a + A_BYTES;
+        if (MODE == WEIGHTS) {
+          if (k == steps - 1 && (t.clen & 15)) {  // handed on by the warp that zeroes what lies behind the end
+            mbar_arrive_expect_tx(&landed[s], bytes);
+            bar = smem_u32(&landed[s]);
+          } else {
+            tc05::arrive_expect_cluster(bar, bytes);
+          }
+        } else if (rank == 0) {
+          mbar_arrive_expect_tx(&full[s], 2 * bytes);
+        }
+        if (MODE == FORWARD) {
+          if (GATED) tc05::tma_pair_5d(a, &map_a, k * 64, 0, 0, t.at * 8 + (int)rank * 4, t.e, bar);
+          else tc05::tma_pair_3d(a, &map_a, k * 64, i0, t.e, bar);
+          for (int i = 0; i < boxes; ++i)
+            tc05::tma_pair_2d(b + i * p.box * 128, &map_b, k * 64, oh + i * p.box, bar);
+        } else if (MODE == INPUT) {
+          tc05::tma_pair_3d(a, &map_a, i0, k * 64, t.e, bar);
+          tc05::tma_pair_3d(a + 8192, &map_a, i0 + 64, k * 64, t.e, bar);
+          for (int i = 0; i < boxes; ++i)
+            tc05::tma_pair_2d(b + i * p.box * 128, &map_b, k * 64, oh + i * p.box, bar);
+        } else {
+          const int c = t.c0 + k * 64;
+          tc05::tma_pair_2d(a, &map_a, i0, c, bar);
+          tc05::tma_pair_2d(a + 8192, &map_a, i0 + 64, c, bar);
+          for (int i = 0; i < boxes; ++i) tc05::tma_pair_2d(b + i * 8192, &map_b, oh + i * 64, c, bar);
+        }
+        ++issued;
+        if (++s == STAGES) {
+          s = 0;
+          ph ^= 1;
+        }
+      }
+      ok = __all_sync(0xffffffffu, ok);
+    }
+    if (lane == 0) {
+      // Every stage's last phase: normally its release by the MMAs (nothing of the peer
+      // is then under way to this CTA); after a wait that ran out, time for the copies.
+      const uint32_t n = issued < (uint32_t)STAGES ? issued : (uint32_t)STAGES;
+      for (uint32_t q = issued - n; q < issued && ok; ++q) ok = wait(&empty[q % STAGES], (q / STAGES) & 1);
+      if (!ok) {  // 1 ms covers any copy
+        const long long t0 = clock64();
+        while (clock64() - t0 < 2000000) {
+        }
+      }
+    }
+  } else if (warp == 9) {
+    // ---------------- MMA issuer.  The whole warp runs the loop, so that the descriptors
+    // are warp-uniform values.
+    if (rank == 0) {
+      uint32_t s = 0, ph = 0, v = 0;
+      bool ok = true;
+      constexpr bool A_ROWS = MODE != FORWARD, B_ROWS = MODE == WEIGHTS;
+      const uint64_t da0 = A_ROWS ? tc05::sw128_rows_desc(base, 8192) : tc05::sw128_desc(base);
+      const uint64_t db0 = B_ROWS ? tc05::sw128_rows_desc(base + A_BYTES, 8192) : tc05::sw128_desc(base + A_BYTES);
+      constexpr uint32_t DA = A_ROWS ? 128 : 2, DB = B_ROWS ? 128 : 2;  // 16 of the contracted dimension
+      for (int u = u0; u < n_units && ok; u += ustep) {
+        const Unit t = unit_of(u);
+        const int steps = steps_of(t);
+        if (steps == 0) continue;
+        const uint32_t idesc = tc05::idesc_f16(256, t.n, 1) | (A_ROWS ? tc05::A_ROWS_CONTIGUOUS : 0u) |
+                               (B_ROWS ? tc05::B_ROWS_CONTIGUOUS : 0u);
+        const uint32_t b = v & 1, d = tmem + b * 256;
+        ok = __all_sync(0xffffffffu, wait(&tempty[b], ((v >> 1) & 1) ^ 1));
+        ++v;
+        for (int k = 0; k < steps && ok; ++k) {
+          ok = __all_sync(0xffffffffu, wait(&full[s], ph));
+          if (!ok) break;
+          tc05::fence_after_sync();
+          const uint64_t da = da0 + s * (STAGE >> 4), db = db0 + s * (STAGE >> 4);
+          const int parts = MODE == WEIGHTS && k == steps - 1 ? (((t.clen - 1) & 63) >> 4) + 1 : 4;
+#pragma unroll
+          for (int j = 0; j < 4; ++j)
+            if (j < parts) tc05::mma_pair(d, da + j * DA, db + j * DB, idesc, k > 0 || j > 0 ? 1u : 0u);
+          tc05::commit_pair(&empty[s]);
+          if (++s == STAGES) {
+            s = 0;
+            ph ^= 1;
+          }
+        }
+        if (ok) tc05::commit_pair(&tfull[b]);
+      }
+      if (!ok) {  // what has been issued retires before tensor memory goes
+        const long long t0 = clock64();
+        while (clock64() - t0 < 2000000) {
+        }
+      }
+    }
+  } else if (warp == 10) {
+    // ---------------- WEIGHTS: zeros for the rows of a last step that are not the expert's
+    if (MODE == WEIGHTS) {
+      uint32_t g = 0, parity = 0;  // steps so far; of `landed`, a bit a stage
+      bool ok = true;
+      for (int u = u0; u < n_units && ok; u += ustep) {
+        const Unit t = unit_of(u);
+        const int steps = steps_of(t);
+        g += steps;
+        if (!(t.clen & 15)) continue;
+        const uint32_t s = (g - 1) % STAGES;
+        ok = __all_sync(0xffffffffu, wait(&landed[s], (parity >> s) & 1));
+        if (!ok) break;
+        parity ^= 1u << s;
+        const int from = t.clen & 63, to = (from + 15) & ~15, pieces = 2 + ((t.n / 2 + 63) >> 6);
+        uint8_t* stage = sm + s * STAGE;
+        for (int i = lane; i < (to - from) * pieces * 8; i += 32) {
+          const int row = from + i / (pieces * 8), c = i % (pieces * 8);
+          *reinterpret_cast<uint4*>(stage + (c >> 3) * 8192 + row * 128 + (c & 7) * 16) = make_uint4(0, 0, 0, 0);
+        }
+        tc05::fence_async();
+        __syncwarp();
+        if (lane == 0) tc05::arrive_cluster(full0 + s * 8);
+      }
+    }
+  } else if (warp < 8) {
+    // ---------------- output
+    const int quad = warp & 3, half = warp >> 2;
+    uint8_t* out = sm + OFF_OUT + warp * OUT_WARP;
+    const uint32_t lanes = tmem + ((uint32_t)(quad * 32) << 16);
+    const uint32_t tempty0 = tc05::map_rank(smem_u32(tempty), 0);
+    const int g = lane >> 2, q = lane & 3;
+    uint32_t v = 0;
+    bool ok = true;
+    for (int u = u0; u < n_units && ok; u += ustep) {
+      const Unit t = unit_of(u);
+      const int nh = t.n >> 1;
+      const bool any = steps_of(t) > 0;
+      const uint32_t b = v & 1;
+      if (any) {
+        ok = __all_sync(0xffffffffu, wait(&tfull[b], (v >> 1) & 1));
+        if (!ok) break;
+        ++v;
+        tc05::fence_after_sync();
+      }
+      // first i of the warp's lanes (gated: of its 16 pairs), and the row of the output that o 0 of the unit is
+      const int i0 = GATED ? (t.at * 8 + (int)rank * 4 + quad) * 16 : t.at * 256 + (int)rank * 128 + quad * 32;
+      const size_t row0 = MODE == WEIGHTS ? (size_t)t.e * p.O + t.o0 : (size_t)t.o0;
+      const int live = min(nh, t.cnt - half * nh);  // columns of this half that are outputs
+      for (int c = 0; 32 * c < live; ++c) {
+        uint32_t r[32];
+        if (any) {
+          const uint32_t ta = lanes + b * 256 + (uint32_t)(half * nh + 32 * c);
+          tc05::ld_16x256b_x4(ta, r);
+          tc05::ld_16x256b_x4(ta + (16u << 16), r + 16);
+          tc05::wait_ld32(r);
+        } else {
+#pragma unroll
+          for (int i = 0; i < 32; ++i) r[i] = 0;
+        }
+        const int left = live - 32 * c;  // columns of the chunk that are outputs
+        const size_t row = row0 + half * nh + 32 * c;
+        auto f = [&](int h, int k, int j) { return __uint_as_float(r[16 * h + 4 * k + j]); };
+        if (GATED) {
+          // A tile of 16 i's x 32 columns, through shared memory: rows of 32 bytes
+          auto put = [&](uint16_t* to, size_t width, auto&& pair) {
+            const uint32_t st = smem_u32(out) + ((lane >> 4) * 8 + (lane & 7)) * 48 + ((lane >> 3) & 1) * 16;
+#pragma unroll
+            for (int k = 0; k < 4; k += 2)
+              asm volatile("stmatrix.sync.aligned.m8n8.x4.trans.shared.b16 [%0], {%1, %2, %3, %4};" ::"r"(
+                               st + k * 8 * 48),
+                           "r"(pair(k, 0)), "r"(pair(k, 2)), "r"(pair(k + 1, 0)), "r"(pair(k + 1, 2))
+                           : "memory");
+            __syncwarp();
+#pragma unroll
+            for (int k = 0; k < 2; ++k) {
+              const int col = 16 * k + (lane >> 1);
+              if (col < left && i0 < p.I)
+                *reinterpret_cast<uint4*>(to + (row + col) * width + i0 + (lane & 1) * 8) =
+                    *reinterpret_cast<const uint4*>(out + col * 48 + (lane & 1) * 16);
+            }
+            __syncwarp();
+          };
+          if (p.keep != nullptr) {
+            put(p.keep, (size_t)2 * p.I, [&](int k, int j) { return bf16x2_bits(f(0, k, j), f(0, k, j + 1)); });
+            put(p.keep + p.I, (size_t)2 * p.I, [&](int k, int j) { return bf16x2_bits(f(1, k, j), f(1, k, j + 1)); });
+          }
+          put(static_cast<uint16_t*>(p.y), (size_t)p.I, [&](int k, int j) {
+            return bf16x2_bits(activation(f(0, k, j), p.act) * f(1, k, j),
+                               activation(f(0, k, j + 1), p.act) * f(1, k, j + 1));
+          });
+        } else if (F32) {
+          float* y = static_cast<float*>(p.y);
+#pragma unroll
+          for (int k = 0; k < 4; ++k)
+#pragma unroll
+            for (int h = 0; h < 2; ++h)
+#pragma unroll
+              for (int j = 0; j < 4; ++j) {
+                const int col = 8 * k + 2 * q + (j & 1), i = i0 + 16 * h + (j >> 1) * 8 + g;
+                if (col < left && i < p.I) y[(row + col) * p.I + i] = f(h, k, j);
+              }
+        } else {
+          uint16_t* y = static_cast<uint16_t*>(p.y);
+          const uint32_t st = smem_u32(out) + (lane & 7) * 80 + (lane >> 3) * 16;  // row lane % 8 of matrix lane / 8
+#pragma unroll
+          for (int k = 0; k < 4; ++k)
+            asm volatile("stmatrix.sync.aligned.m8n8.x4.trans.shared.b16 [%0], {%1, %2, %3, %4};" ::"r"(st + k * 640),
+                         "r"(bf16x2_bits(f(0, k, 0), f(0, k, 1))), "r"(bf16x2_bits(f(0, k, 2), f(0, k, 3))),
+                         "r"(bf16x2_bits(f(1, k, 0), f(1, k, 1))), "r"(bf16x2_bits(f(1, k, 2), f(1, k, 3)))
+                         : "memory");
+          __syncwarp();
+          const int i = i0 + (lane & 3) * 8;
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            const int col = 8 * k + (lane >> 2);
+            if (col < left && i < p.I)  // the width is a multiple of 8
+              *reinterpret_cast<uint4*>(y + (row + col) * p.I + i) =
+                  *reinterpret_cast<const uint4*>(out + col * 80 + (lane & 3) * 16);
+          }
+          __syncwarp();
+        }
+      }
+      if (any) {
+        tc05::fence_before_sync();
+        __syncwarp();
+        if (lane == 0) tc05::arrive_cluster(tempty0 + b * 8);
+      }
+    }
+  }
+  __syncwarp();
+  tc05::fence_before_sync();
+  __syncthreads();
+  tc05::cluster_sync();  // no arrival or copy is under way to either CTA any more
+  if (warp == 8) {
+    tc05::fence_after_sync();
+    tc05::dealloc_pair(tmem, 512);
+  }
+  __syncwarp();
+  tc05::cluster_sync();
+}
+
+EncodeTiled g_encode = nullptr;  // set once, under the caller's lock
+
+// A map of bf16 elements in the 128-byte swizzle, zeros outside.  dims from the innermost,
+// strides in elements from the second dimension on.
+bool encode(CUtensorMap* m, const void* base, std::initializer_list<uint64_t> dims,
+            std::initializer_list<uint64_t> strides, std::initializer_list<uint32_t> box) {
+  cuuint64_t d[5], s[4];
+  cuuint32_t b[5], one[5] = {1, 1, 1, 1, 1};
+  int n = 0;
+  for (uint64_t v : dims) d[n++] = v;
+  n = 0;
+  for (uint64_t v : strides) s[n++] = v * 2;
+  n = 0;
+  for (uint32_t v : box) b[n++] = v;
+  return g_encode(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, (cuuint32_t)n, const_cast<void*>(base), d, s, b, one,
+                  CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                  CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+template <int MODE, bool GATED, bool F32>
+cudaError_t launch(const PairArgs& p, const CUtensorMap& ma, const CUtensorMap& mb, long long most, int sm_count,
+                   cudaStream_t st) {
+  const int pairs = sm_count / 2;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(2u * (unsigned)(most < pairs ? most : pairs));
+  cfg.blockDim = dim3(PAIR_THREADS);
+  cfg.dynamicSmemBytes = pair_smem(p.E);
+  cfg.stream = st;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = 2;
+  attr[1].val.clusterDim.y = 1;
+  attr[1].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 2;
+  return cudaLaunchKernelEx(&cfg, pair_gemm_kernel<MODE, GATED, F32>, p, ma, mb);
+}
+
+// Tiles of rows that a grouped (or dense) product may have, at most.
+long long row_tiles(int M, int E, bool grouped, int tile) {
+  if (!grouped) return (M + tile - 1LL) / tile;
+  return (long long)M / tile + (M < E ? M : E);
+}
+
+}  // namespace
+
+cudaError_t pair_gemm_kernels_init() {
+  if (g_encode == nullptr) {
+    void* fn = nullptr;
+    cudaDriverEntryPointQueryResult q;
+    const cudaError_t e = cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &fn, 12000, cudaEnableDefault, &q);
+    if (e != cudaSuccess) return e;
+    if (q != cudaDriverEntryPointSuccess || fn == nullptr) return cudaErrorNotSupported;
+    g_encode = reinterpret_cast<EncodeTiled>(fn);
+  }
+  const void* k[] = {reinterpret_cast<const void*>(pair_gemm_kernel<FORWARD, true, false>),
+                     reinterpret_cast<const void*>(pair_gemm_kernel<FORWARD, false, false>),
+                     reinterpret_cast<const void*>(pair_gemm_kernel<FORWARD, false, true>),
+                     reinterpret_cast<const void*>(pair_gemm_kernel<INPUT, false, false>),
+                     reinterpret_cast<const void*>(pair_gemm_kernel<WEIGHTS, false, false>),
+                     reinterpret_cast<const void*>(pair_gemm_kernel<WEIGHTS, false, true>)};
+  for (const void* f : k) {
+    const cudaError_t e =
+        cudaFuncSetAttribute(f, cudaFuncAttributeMaxDynamicSharedMemorySize, pair_smem(ROUTE_MAX_E));
+    if (e != cudaSuccess) return e;
+  }
+  return cudaSuccess;
+}
+
+cudaError_t launch_pair_forward(const ProductArgs& a, int sm_count, unsigned* err, cudaStream_t st) {
+  const bool gated = a.act != FFN_NONE;
+  const uint64_t M = a.M, N = a.N, K = a.K, E = a.E;
+  PairArgs p = {};
+  p.offsets = a.offsets;
+  p.y = a.y;
+  p.keep = static_cast<uint16_t*>(a.keep);
+  p.err = err;
+  p.M = a.M;
+  p.E = a.E;
+  p.I = gated ? a.N / 2 : a.N;
+  p.steps = (a.K + 63) / 64;
+  p.a_tiles = (a.N + 255) / 256;
+  p.tile = 256;
+  p.box = 32;
+  p.band = 8;
+  p.act = a.act;
+  CUtensorMap ma, mb;
+  const bool ok =
+      gated ? encode(&ma, a.w, {K, 16, 2, N / 32, E}, {K, N / 2 * K, 16 * K, N * K}, {64, 16, 2, 4, 1})
+            : encode(&ma, a.w, {K, N, E}, {K, N * K}, {64, 128, 1});
+  if (!ok || !encode(&mb, a.x, {K, M}, {K}, {64, (uint32_t)p.box})) return cudaErrorInvalidValue;
+  const long long most = row_tiles(a.M, a.E, a.offsets != nullptr, p.tile) * p.a_tiles;
+  if (gated) return launch<FORWARD, true, false>(p, ma, mb, most, sm_count, st);
+  return a.f32 ? launch<FORWARD, false, true>(p, ma, mb, most, sm_count, st)
+               : launch<FORWARD, false, false>(p, ma, mb, most, sm_count, st);
+}
+
+cudaError_t launch_pair_input(const GradArgs& a, int sm_count, unsigned* err, cudaStream_t st) {
+  const uint64_t M = a.M, N = a.N, K = a.K, E = a.E;
+  PairArgs p = {};
+  p.offsets = a.offsets;
+  p.y = a.out;
+  p.err = err;
+  p.M = a.M;
+  p.E = a.E;
+  p.I = a.K;
+  p.steps = (a.N + 63) / 64;
+  p.a_tiles = (a.K + 255) / 256;
+  p.tile = 256;
+  p.box = 32;
+  p.band = 8;
+  CUtensorMap ma, mb;
+  if (!encode(&ma, a.other, {K, N, E}, {K, N * K}, {64, 64, 1}) || !encode(&mb, a.dy, {N, M}, {N}, {64, (uint32_t)p.box}))
+    return cudaErrorInvalidValue;
+  return launch<INPUT, false, false>(p, ma, mb, row_tiles(a.M, a.E, a.offsets != nullptr, p.tile) * p.a_tiles, sm_count, st);
+}
+
+cudaError_t launch_pair_weights(const GradArgs& a, int sm_count, unsigned* err, cudaStream_t st) {
+  const uint64_t M = a.M, N = a.N, K = a.K;
+  PairArgs p = {};
+  p.offsets = a.offsets;
+  p.y = a.out;
+  p.err = err;
+  p.M = a.M;
+  p.E = a.E;
+  p.I = a.K;
+  p.O = a.N;
+  p.a_tiles = (a.K + 255) / 256;
+  p.tile = 256;
+  p.o_tiles = (a.N + p.tile - 1) / p.tile;
+  p.box = 64;
+  p.band = 8;
+  CUtensorMap ma, mb;
+  if (!encode(&ma, a.other, {K, M}, {K}, {64, 64}) || !encode(&mb, a.dy, {N, M}, {N}, {64, 64}))
+    return cudaErrorInvalidValue;
+  const long long most = (long long)a.E * p.a_tiles * p.o_tiles;
+  return a.f32 ? launch<WEIGHTS, false, true>(p, ma, mb, most, sm_count, st)
+               : launch<WEIGHTS, false, false>(p, ma, mb, most, sm_count, st);
+}
+
+}  // namespace flint
