@@ -463,8 +463,8 @@ int flint_moe_gated_linear_backward(const void *dh, const void *gu, const void *
 
 /*
  * Rows to 8-bit integers: with a = max(largest magnitude of the row, 2^-96),
- * scale = a / 127 in fp32, code = the whole number next to the real number
- * x / scale, ties to even.  A row that holds an infinity or NaN gets a scale that is
+ * scale = a * (1 / 127), factor and product in fp32, and code = the whole number next
+ * to the real number x / scale, ties to even.  A row that holds an infinity or NaN gets a scale that is
  * not finite, and codes of 0.
  *   x [rows][K] of x_type, rows row_stride elements apart (a multiple of 16 bytes,
  *   at most 2^31; what lies between two rows counts as x's); pos int32 [rows][top_k],

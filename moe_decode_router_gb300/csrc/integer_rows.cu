@@ -69,8 +69,8 @@ __device__ __forceinline__ uint32_t code(float v, float s, float inv) {
   return __float_as_uint(m);
 }
 
-// a = max(largest magnitude of the row, 2^-96), scale = a / 127, code = the whole number
-// next to x / scale.  THREADS lanes of a CTA of 256 have a row: each 16 neighbouring
+// a = max(largest magnitude of the row, 2^-96), scale = a * (1 / 127) (both in fp32), code =
+// the whole number next to x / scale.  THREADS lanes of a CTA of 256 have a row: each 16 neighbouring
 // values at a time, the first HELD x 16 of them kept in registers between the two passes
 // (a longer row is read a second time).  Bound by HBM.
 template <bool BF16, int THREADS>
@@ -110,7 +110,7 @@ __global__ void __launch_bounds__(256) integer_rows_kernel(const IntRowsArgs p) 
   }
   if (!in) return;
   if (a < ROW_FLOOR) a = ROW_FLOOR;  // false for NaN
-  const float scale = __fdiv_rn(a, 127.f), inv = __frcp_rn(scale);
+  const float scale = __fmul_rn(a, 1.f / 127.f), inv = __frcp_rn(scale);
   const bool fine = scale < INFINITY;  // false for NaN: the codes of such a row are 0
   const int32_t* pos = p.pos + (size_t)row * p.top_k;
   auto put = [&](const Raw16<BF16>& v, int k) {

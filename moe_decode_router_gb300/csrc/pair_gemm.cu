@@ -1,5 +1,5 @@
-// bf16 products on the tensor cores (tcgen05 over pairs of CTAs), dense or grouped by
-// expert: linear and gated products and their gradients.
+// Products on the tensor cores (tcgen05 over pairs of CTAs), dense or grouped by expert:
+// linear and gated products in bf16 and their gradients, and 8-bit integer products.
 //
 // One kernel for three products.  The M side of the MMA is the dimension that lies
 // contiguous in the output (i), always 256 of it a unit; the N side (o), up to 256 in
@@ -24,8 +24,16 @@
 // multiplied, and in the last a warp of each CTA overwrites the rows behind the end (another
 // expert's, perhaps infinite) with zeros before the stage is handed on.
 //
+// 8-bit integers.  This GPU's tensor cores take none at a rate worth using, but a code is
+// exact in fp16, a product of two in fp32, and a sum of 1,024 products stays within 2^24,
+// where fp32 holds every whole number.  Codes land in a ring of their own (128 of K a
+// stage); four warps turn them into fp16 operands (code + 1152 is put together from the
+// bits, 1152 taken off) and every 1,024 of K the accumulator is added to 32-bit integers in
+// registers.  fp32 outputs of bf16 operands are promoted the same way every 512 of the
+// contracted dimension: the tensor cores cut a sum instead of rounding it, which adds up.
+//
 // Warps: 0-7 output, two halves of the columns; 8 TMA producer; 9 MMA issuer (of the even
-// CTA); 10 rows behind the end (WEIGHTS); 11 none.
+// CTA); 10 rows behind the end (WEIGHTS); 11 none; 12-15 codes to fp16 (integers).
 #include <initializer_list>
 
 #include "product_common.cuh"
@@ -37,20 +45,33 @@ namespace {
 
 enum { FORWARD, INPUT, WEIGHTS };
 
-constexpr int PAIR_THREADS = 384;
-constexpr int A_BYTES = 128 * 128, B_BYTES = 128 * 128, STAGE = A_BYTES + B_BYTES, STAGES = 6;
+constexpr int A_BYTES = 128 * 128, B_BYTES = 128 * 128, STAGE = A_BYTES + B_BYTES;
+constexpr int RING = 6;            // stages of operands; of integers 3, and 3 of codes (128 of K each) behind them
+constexpr int CODES = 3;
 constexpr int OUT_WARP = 32 * 80;  // output staging of a warp: 32 rows of 64 bytes, 80 apart
-constexpr int OFF_OUT = STAGES * STAGE;
+constexpr int OFF_OUT = RING * STAGE;
 constexpr int OFF_BARS = OFF_OUT + 8 * OUT_WARP;
+constexpr int SEG_F32 = 8, SEG_INT = 16;  // steps of 64 between promotions
+
+// Registers a thread: the output warps of a promoting kernel hold 128 sums each and take what
+// the others give up; a block is launched with LAUNCH of them.
+template <bool INT8>
+struct Regs {
+  static constexpr int THREADS = INT8 ? 512 : 384, LAUNCH = INT8 ? 128 : 168;
+  static constexpr int HIGH = INT8 ? 192 : 224, LOW = INT8 ? 64 : 48;
+  static_assert(HIGH * 256 + LOW * (THREADS - 256) <= LAUNCH * THREADS, "register shares");
+};
 constexpr int OFF_GROUPS = OFF_BARS + 256;
 constexpr int pair_smem(int E) { return OFF_GROUPS + (3 * E + 1) * 4; }
 static_assert(pair_smem(ROUTE_MAX_E) <= 232448, "shared memory");
-static_assert((3 * STAGES + 4) * 8 + 8 <= 256, "barriers");
+static_assert((3 * RING + CODES + 4) * 8 + 8 <= 256, "barriers");
 
 struct PairArgs {
   const int32_t* offsets;
   void* y;
   uint16_t* keep;  // gated: the sums, or null
+  const float* sx;  // integers: scales
+  const float* sw;
   unsigned* err;
   int M, E;
   int I;        // width of the output (i)
@@ -69,18 +90,47 @@ struct Unit {
   int c0, clen;           // WEIGHTS: the expert's rows
 };
 
-template <int MODE, bool GATED, bool F32>
-__global__ void __launch_bounds__(PAIR_THREADS, 1)
+// Sums of a promoting kernel.
+template <bool INT8>
+struct Held {
+  using type = float;
+};
+template <>
+struct Held<true> {
+  using type = int;
+};
+
+// 16 codes to 16 fp16 values: code + 1152 is 0x6400 with the code, its sign bit turned, in the low byte.
+__device__ __forceinline__ void codes_to_f16(const uint4 c, uint4& lo, uint4& hi) {
+  const uint32_t w[4] = {c.x ^ 0x80808080u, c.y ^ 0x80808080u, c.z ^ 0x80808080u, c.w ^ 0x80808080u};
+  uint32_t o[8];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    const uint32_t u = __byte_perm(w[i >> 1], 0x64646464u, i & 1 ? 0x4342 : 0x4140);
+    const __half2 v = __hsub2(*reinterpret_cast<const __half2*>(&u), __float2half2_rn(1152.f));
+    o[i] = *reinterpret_cast<const uint32_t*>(&v);
+  }
+  lo = make_uint4(o[0], o[1], o[2], o[3]);
+  hi = make_uint4(o[4], o[5], o[6], o[7]);
+}
+
+template <int MODE, bool GATED, bool F32, bool INT8>
+__global__ void __launch_bounds__(Regs<INT8>::THREADS, 1)
     pair_gemm_kernel(const PairArgs p, const __grid_constant__ CUtensorMap map_a,
                      const __grid_constant__ CUtensorMap map_b) {
+  constexpr int STAGES = INT8 ? RING - CODES : RING, THREADS = Regs<INT8>::THREADS;
+  constexpr bool PROMOTE = F32 || INT8;
+  static_assert(!INT8 || MODE == FORWARD, "integers have no gradient");
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   uint8_t* sm = smem_raw;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const uint32_t rank = tc05::cluster_rank();
   uint64_t* full = reinterpret_cast<uint64_t*>(sm + OFF_BARS);  // [STAGES] both CTAs' operands landed (even CTA's)
   uint64_t* empty = full + STAGES;                              // [STAGES] stage consumed
-  uint64_t* landed = empty + STAGES;                            // [STAGES] WEIGHTS: a last stage of this CTA landed
-  uint64_t* tfull = landed + STAGES;                            // [2] accumulator complete
+  uint64_t* landed = empty + STAGES;                            // [STAGES] WEIGHTS: a last stage of this CTA landed;
+                                                                // [CODES] integers: codes of this CTA landed
+  uint64_t* taken = landed + RING;                              // [CODES] integers: codes turned
+  uint64_t* tfull = taken + CODES;                              // [2] accumulator complete
   uint64_t* tempty = tfull + 2;                                 // [2] accumulator read, 16 warps (even CTA's)
   uint32_t* tslot = reinterpret_cast<uint32_t*>(tempty + 2);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tslot + 1);
@@ -90,10 +140,11 @@ __global__ void __launch_bounds__(PAIR_THREADS, 1)
 
   if (tid == 0) {
     for (int i = 0; i < STAGES; ++i) {
-      mbar_init(&full[i], MODE == WEIGHTS ? 2 : 1);
+      mbar_init(&full[i], INT8 ? 8 : MODE == WEIGHTS ? 2 : 1);
       mbar_init(&empty[i], 1);
-      mbar_init(&landed[i], 1);
     }
+    for (int i = 0; i < RING; ++i) mbar_init(&landed[i], 1);
+    for (int i = 0; i < CODES; ++i) mbar_init(&taken[i], 4);
     for (int i = 0; i < 2; ++i) {
       mbar_init(&tfull[i], 1);
       mbar_init(&tempty[i], 16);
@@ -110,7 +161,7 @@ __global__ void __launch_bounds__(PAIR_THREADS, 1)
   }
   pdl_trigger();
   if (p.offsets != nullptr)
-    for (int e = tid; e <= p.E; e += PAIR_THREADS) g_units[e] = __ldg(p.offsets + e);  // all on their way at once
+    for (int e = tid; e <= p.E; e += THREADS) g_units[e] = __ldg(p.offsets + e);  // all on their way at once
   __syncthreads();
   if (warp == 8) {
     int base = 0;
@@ -186,137 +237,232 @@ __global__ void __launch_bounds__(PAIR_THREADS, 1)
     return false;
   };
   const uint32_t base = smem_u32(sm), full0 = tc05::map_rank(smem_u32(full), 0);
-
-  if (warp == 8) {
-    // ---------------- producer: this CTA's 128 of i and its half of the columns
-    uint32_t s = 0, ph = 0, issued = 0;  // of lane 0, which copies
-    bool ok = true;
-    for (int u = u0; u < n_units && ok; u += ustep) {
-      const Unit t = unit_of(u);
-      const int nh = t.n >> 1, steps = steps_of(t);
-      const int i0 = t.at * 256 + (int)rank * 128, oh = t.o0 + (int)rank * nh;
-      const int boxes = MODE == WEIGHTS ? (nh + 63) >> 6 : (nh + p.box - 1) / p.box;
-      const uint32_t bytes = A_BYTES + boxes * (MODE == WEIGHTS ? 8192 : p.box * 128);
-      for (int k = 0; k < steps && lane == 0; ++k) {
-        if (!wait(&empty[s], ph ^ 1)) {
-          ok = false;
-          break;
-        }
-        uint32_t bar = full0 + s * 8;
-        const uint32_t a = base + s * STAGE, b = a + A_BYTES;
-        if (MODE == WEIGHTS) {
-          if (k == steps - 1 && (t.clen & 15)) {  // handed on by the warp that zeroes what lies behind the end
-            mbar_arrive_expect_tx(&landed[s], bytes);
-            bar = smem_u32(&landed[s]);
-          } else {
-            tc05::arrive_expect_cluster(bar, bytes);
-          }
-        } else if (rank == 0) {
-          mbar_arrive_expect_tx(&full[s], 2 * bytes);
-        }
-        if (MODE == FORWARD) {
-          if (GATED) tc05::tma_pair_5d(a, &map_a, k * 64, 0, 0, t.at * 8 + (int)rank * 4, t.e, bar);
-          else tc05::tma_pair_3d(a, &map_a, k * 64, i0, t.e, bar);
-          for (int i = 0; i < boxes; ++i)
-            tc05::tma_pair_2d(b + i * p.box * 128, &map_b, k * 64, oh + i * p.box, bar);
-        } else if (MODE == INPUT) {
-          tc05::tma_pair_3d(a, &map_a, i0, k * 64, t.e, bar);
-          tc05::tma_pair_3d(a + 8192, &map_a, i0 + 64, k * 64, t.e, bar);
-          for (int i = 0; i < boxes; ++i)
-            tc05::tma_pair_2d(b + i * p.box * 128, &map_b, k * 64, oh + i * p.box, bar);
-        } else {
-          const int c = t.c0 + k * 64;
-          tc05::tma_pair_2d(a, &map_a, i0, c, bar);
-          tc05::tma_pair_2d(a + 8192, &map_a, i0 + 64, c, bar);
-          for (int i = 0; i < boxes; ++i) tc05::tma_pair_2d(b + i * 8192, &map_b, oh + i * 64, c, bar);
-        }
-        ++issued;
-        if (++s == STAGES) {
-          s = 0;
-          ph ^= 1;
-        }
-      }
-      ok = __all_sync(0xffffffffu, ok);
-    }
-    if (lane == 0) {
-      // Every stage's last phase: normally its release by the MMAs (nothing of the peer
-      // is then under way to this CTA); after a wait that ran out, time for the copies.
-      const uint32_t n = issued < (uint32_t)STAGES ? issued : (uint32_t)STAGES;
-      for (uint32_t q = issued - n; q < issued && ok; ++q) ok = wait(&empty[q % STAGES], (q / STAGES) & 1);
-      if (!ok) {  // 1 ms covers any copy
-        const long long t0 = clock64();
-        while (clock64() - t0 < 2000000) {
-        }
-      }
-    }
-  } else if (warp == 9) {
-    // ---------------- MMA issuer.  The whole warp runs the loop, so that the descriptors
-    // are warp-uniform values.
-    if (rank == 0) {
-      uint32_t s = 0, ph = 0, v = 0;
+  if (warp >= 8) {
+    if (PROMOTE) tc05::regs_down<Regs<INT8>::LOW>();
+    if (INT8 && warp == 8) {
+      // ---------------- producer of codes: stages of 128 of K
+      uint32_t r = 0, ph = 0, issued = 0;
       bool ok = true;
-      constexpr bool A_ROWS = MODE != FORWARD, B_ROWS = MODE == WEIGHTS;
-      const uint64_t da0 = A_ROWS ? tc05::sw128_rows_desc(base, 8192) : tc05::sw128_desc(base);
-      const uint64_t db0 = B_ROWS ? tc05::sw128_rows_desc(base + A_BYTES, 8192) : tc05::sw128_desc(base + A_BYTES);
-      constexpr uint32_t DA = A_ROWS ? 128 : 2, DB = B_ROWS ? 128 : 2;  // 16 of the contracted dimension
       for (int u = u0; u < n_units && ok; u += ustep) {
         const Unit t = unit_of(u);
-        const int steps = steps_of(t);
-        if (steps == 0) continue;
-        const uint32_t idesc = tc05::idesc_f16(256, t.n, 1) | (A_ROWS ? tc05::A_ROWS_CONTIGUOUS : 0u) |
-                               (B_ROWS ? tc05::B_ROWS_CONTIGUOUS : 0u);
-        const uint32_t b = v & 1, d = tmem + b * 256;
-        ok = __all_sync(0xffffffffu, wait(&tempty[b], ((v >> 1) & 1) ^ 1));
-        ++v;
-        for (int k = 0; k < steps && ok; ++k) {
-          ok = __all_sync(0xffffffffu, wait(&full[s], ph));
+        const int nh = t.n >> 1, oh = t.o0 + (int)rank * nh, boxes = (nh + p.box - 1) / p.box;
+        const uint32_t bytes = A_BYTES + boxes * p.box * 128;
+        for (int k = 0; k < (p.steps + 1) >> 1 && lane == 0; ++k) {
+          if (!wait(&taken[r], ph ^ 1)) {
+            ok = false;
+            break;
+          }
+          const uint32_t a = base + (STAGES + r) * STAGE, b = a + A_BYTES, bar = smem_u32(&landed[r]);
+          mbar_arrive_expect_tx(&landed[r], bytes);
+          if (GATED) tc05::tma_pair_5d(a, &map_a, k * 128, 0, 0, t.at * 8 + (int)rank * 4, t.e, bar);
+          else tc05::tma_pair_3d(a, &map_a, k * 128, t.at * 256 + (int)rank * 128, t.e, bar);
+          for (int i = 0; i < boxes; ++i) tc05::tma_pair_2d(b + i * p.box * 128, &map_b, k * 128, oh + i * p.box, bar);
+          ++issued;
+          if (++r == CODES) {
+            r = 0;
+            ph ^= 1;
+          }
+        }
+        ok = __all_sync(0xffffffffu, ok);
+      }
+      if (lane == 0) {
+        const uint32_t n = min(issued, (uint32_t)CODES);
+        for (uint32_t q = issued - n; q < issued && ok; ++q) ok = wait(&taken[q % CODES], (q / CODES) & 1);
+        if (!ok) {  // 1 ms covers any copy
+          const long long t0 = clock64();
+          while (clock64() - t0 < 2000000) {
+          }
+        }
+      }
+    } else if (INT8 && warp >= 12) {
+      // ---------------- codes to fp16: 64 of K at a time.  A warp takes 8 rows (a swizzle
+      // atom) at once, a lane 16 codes of a row; the 8 lanes that shared memory serves
+      // together have two rows r and r ^ 5, whose swizzled places differ on the way in
+      // (bit 2) and on the way out (bit 0).
+      constexpr int AT_ONCE = 4;
+      uint32_t s = 0, ph = 0, r = 0, rph = 0;
+      bool ok = true;
+      const int q = lane & 3, row = (lane >> 3) ^ (lane & 4 ? 5 : 0);
+      for (int u = u0; u < n_units && ok; u += ustep) {
+        const Unit t = unit_of(u);
+        const int atoms = 16 + (t.n >> 4);  // of A, then of B's half
+        for (int k = 0; k < p.steps; ++k) {
+          if ((k & 1) == 0) ok = __all_sync(0xffffffffu, wait(&landed[r], rph));
+          ok = ok && __all_sync(0xffffffffu, wait(&empty[s], ph ^ 1));
           if (!ok) break;
-          tc05::fence_after_sync();
-          const uint64_t da = da0 + s * (STAGE >> 4), db = db0 + s * (STAGE >> 4);
-          const int parts = MODE == WEIGHTS && k == steps - 1 ? (((t.clen - 1) & 63) >> 4) + 1 : 4;
-#pragma unroll
-          for (int j = 0; j < 4; ++j)
-            if (j < parts) tc05::mma_pair(d, da + j * DA, db + j * DB, idesc, k > 0 || j > 0 ? 1u : 0u);
-          tc05::commit_pair(&empty[s]);
+          const uint8_t* from = sm + (STAGES + r) * STAGE + row * 128 + ((((k & 1) * 4 + q) ^ row) << 4);
+          uint8_t* to = sm + s * STAGE + row * 128;
+          const int lo = ((2 * q) ^ row) << 4, hi = ((2 * q + 1) ^ row) << 4;
+          for (int a = warp - 12; a < atoms; a += 4 * AT_ONCE) {
+            uint4 c[AT_ONCE];
+  #pragma unroll
+            for (int i = 0; i < AT_ONCE; ++i)
+              if (a + 4 * i < atoms) c[i] = *reinterpret_cast<const uint4*>(from + (a + 4 * i) * 1024);
+  #pragma unroll
+            for (int i = 0; i < AT_ONCE; ++i)
+              if (a + 4 * i < atoms) {
+                uint4 v0, v1;
+                codes_to_f16(c[i], v0, v1);
+                uint8_t* at = to + (a + 4 * i) * 1024;
+                *reinterpret_cast<uint4*>(at + lo) = v0;
+                *reinterpret_cast<uint4*>(at + hi) = v1;
+              }
+          }
+          tc05::fence_proxy_async_smem();
+          __syncwarp();
+          if (lane == 0) tc05::arrive_cluster(full0 + s * 8);
+          if (++s == STAGES) {
+            s = 0;
+            ph ^= 1;
+          }
+          if ((k & 1) || k == p.steps - 1) {
+            if (lane == 0) mbar_arrive(&taken[r]);
+            if (++r == CODES) {
+              r = 0;
+              rph ^= 1;
+            }
+          }
+        }
+      }
+    } else if (warp == 8) {
+      // ---------------- producer: this CTA's 128 of i and its half of the columns
+      uint32_t s = 0, ph = 0, issued = 0;  // of lane 0, which copies
+      bool ok = true;
+      for (int u = u0; u < n_units && ok; u += ustep) {
+        const Unit t = unit_of(u);
+        const int nh = t.n >> 1, steps = steps_of(t);
+        const int i0 = t.at * 256 + (int)rank * 128, oh = t.o0 + (int)rank * nh;
+        const int boxes = MODE == WEIGHTS ? (nh + 63) >> 6 : (nh + p.box - 1) / p.box;
+        const uint32_t bytes = A_BYTES + boxes * (MODE == WEIGHTS ? 8192 : p.box * 128);
+        for (int k = 0; k < steps && lane == 0; ++k) {
+          if (!wait(&empty[s], ph ^ 1)) {
+            ok = false;
+            break;
+          }
+          uint32_t bar = full0 + s * 8;
+          const uint32_t a = base + s * STAGE, b = a + A_BYTES;
+          if (MODE == WEIGHTS) {
+            if (k == steps - 1 && (t.clen & 15)) {  // handed on by the warp that zeroes what lies behind the end
+              mbar_arrive_expect_tx(&landed[s], bytes);
+              bar = smem_u32(&landed[s]);
+            } else {
+              tc05::arrive_expect_cluster(bar, bytes);
+            }
+          } else if (rank == 0) {
+            mbar_arrive_expect_tx(&full[s], 2 * bytes);
+          }
+          if (MODE == FORWARD) {
+            if (GATED) tc05::tma_pair_5d(a, &map_a, k * 64, 0, 0, t.at * 8 + (int)rank * 4, t.e, bar);
+            else tc05::tma_pair_3d(a, &map_a, k * 64, i0, t.e, bar);
+            for (int i = 0; i < boxes; ++i)
+              tc05::tma_pair_2d(b + i * p.box * 128, &map_b, k * 64, oh + i * p.box, bar);
+          } else if (MODE == INPUT) {
+            tc05::tma_pair_3d(a, &map_a, i0, k * 64, t.e, bar);
+            tc05::tma_pair_3d(a + 8192, &map_a, i0 + 64, k * 64, t.e, bar);
+            for (int i = 0; i < boxes; ++i)
+              tc05::tma_pair_2d(b + i * p.box * 128, &map_b, k * 64, oh + i * p.box, bar);
+          } else {
+            const int c = t.c0 + k * 64;
+            tc05::tma_pair_2d(a, &map_a, i0, c, bar);
+            tc05::tma_pair_2d(a + 8192, &map_a, i0 + 64, c, bar);
+            for (int i = 0; i < boxes; ++i) tc05::tma_pair_2d(b + i * 8192, &map_b, oh + i * 64, c, bar);
+          }
+          ++issued;
           if (++s == STAGES) {
             s = 0;
             ph ^= 1;
           }
         }
-        if (ok) tc05::commit_pair(&tfull[b]);
+        ok = __all_sync(0xffffffffu, ok);
       }
-      if (!ok) {  // what has been issued retires before tensor memory goes
-        const long long t0 = clock64();
-        while (clock64() - t0 < 2000000) {
+      if (lane == 0) {
+        // Every stage's last phase: normally its release by the MMAs (nothing of the peer
+        // is then under way to this CTA); after a wait that ran out, time for the copies.
+        const uint32_t n = issued < (uint32_t)STAGES ? issued : (uint32_t)STAGES;
+        for (uint32_t q = issued - n; q < issued && ok; ++q) ok = wait(&empty[q % STAGES], (q / STAGES) & 1);
+        if (!ok) {  // 1 ms covers any copy
+          const long long t0 = clock64();
+          while (clock64() - t0 < 2000000) {
+          }
+        }
+      }
+    } else if (warp == 9) {
+      // ---------------- MMA issuer.  The whole warp runs the loop, so that the descriptors
+      // are warp-uniform values.
+      if (rank == 0) {
+        uint32_t s = 0, ph = 0, v = 0;
+        bool ok = true;
+        constexpr bool A_ROWS = MODE != FORWARD, B_ROWS = MODE == WEIGHTS;
+        constexpr int SEG = INT8 ? SEG_INT : SEG_F32;
+        constexpr uint32_t TFULL = (2 * STAGES + RING + CODES) * 8;
+        const uint32_t bars[2] = {full0, tc05::map_rank(smem_u32(full), 1)};  // of either CTA
+        const uint64_t da0 = A_ROWS ? tc05::sw128_rows_desc(base, 8192) : tc05::sw128_desc(base);
+        const uint64_t db0 = B_ROWS ? tc05::sw128_rows_desc(base + A_BYTES, 8192) : tc05::sw128_desc(base + A_BYTES);
+        constexpr uint32_t DA = A_ROWS ? 128 : 2, DB = B_ROWS ? 128 : 2;  // 16 of the contracted dimension
+        for (int u = u0; u < n_units && ok; u += ustep) {
+          const Unit t = unit_of(u);
+          const int steps = steps_of(t);
+          const uint32_t idesc = tc05::idesc_f16(256, t.n, INT8 ? 0 : 1) | (A_ROWS ? tc05::A_ROWS_CONTIGUOUS : 0u) |
+                                 (B_ROWS ? tc05::B_ROWS_CONTIGUOUS : 0u);
+          for (int k = 0; k < steps; ++k) {
+            const bool fresh = PROMOTE ? k % SEG == 0 : k == 0;
+            const bool last = k == steps - 1 || (PROMOTE && k % SEG == SEG - 1);
+            const uint32_t b = v & 1, d = tmem + b * 256;
+            // every lane waits, and all go on or none
+            ok = !fresh || __all_sync(0xffffffffu, wait(&tempty[b], ((v >> 1) & 1) ^ 1));
+            ok = ok && __all_sync(0xffffffffu, wait(&full[s], ph));
+            if (!ok) break;
+            tc05::fence_after_sync();
+            const uint64_t da = da0 + s * (STAGE >> 4), db = db0 + s * (STAGE >> 4);
+            const int parts = MODE == WEIGHTS && k == steps - 1 ? (((t.clen - 1) & 63) >> 4) + 1 : 4;
+  #pragma unroll
+            for (int j = 0; j < 4; ++j)
+              if (j < parts) tc05::mma_pair(d, da + j * DA, db + j * DB, idesc, !fresh || j > 0 ? 1u : 0u);
+            for (int c = 0; c < 2; ++c) tc05::commit_pair(bars[c] + STAGES * 8 + s * 8);  // empty
+            if (last) {
+              for (int c = 0; c < 2; ++c) tc05::commit_pair(bars[c] + TFULL + b * 8);
+              ++v;
+            }
+            if (++s == STAGES) {
+              s = 0;
+              ph ^= 1;
+            }
+          }
+        }
+        if (!ok) {  // what has been issued retires before tensor memory goes
+          const long long t0 = clock64();
+          while (clock64() - t0 < 2000000) {
+          }
+        }
+      }
+    } else if (warp == 10) {
+      // ---------------- WEIGHTS: zeros for the rows of a last step that are not the expert's
+      if (MODE == WEIGHTS) {
+        uint32_t g = 0, parity = 0;  // steps so far; of `landed`, a bit a stage
+        bool ok = true;
+        for (int u = u0; u < n_units && ok; u += ustep) {
+          const Unit t = unit_of(u);
+          const int steps = steps_of(t);
+          g += steps;
+          if (!(t.clen & 15)) continue;
+          const uint32_t s = (g - 1) % STAGES;
+          ok = __all_sync(0xffffffffu, wait(&landed[s], (parity >> s) & 1));
+          if (!ok) break;
+          parity ^= 1u << s;
+          const int from = t.clen & 63, to = (from + 15) & ~15, pieces = 2 + ((t.n / 2 + 63) >> 6);
+          uint8_t* stage = sm + s * STAGE;
+          for (int i = lane; i < (to - from) * pieces * 8; i += 32) {
+            const int row = from + i / (pieces * 8), c = i % (pieces * 8);
+            *reinterpret_cast<uint4*>(stage + (c >> 3) * 8192 + row * 128 + (c & 7) * 16) = make_uint4(0, 0, 0, 0);
+          }
+          tc05::fence_async();
+          __syncwarp();
+          if (lane == 0) tc05::arrive_cluster(full0 + s * 8);
         }
       }
     }
-  } else if (warp == 10) {
-    // ---------------- WEIGHTS: zeros for the rows of a last step that are not the expert's
-    if (MODE == WEIGHTS) {
-      uint32_t g = 0, parity = 0;  // steps so far; of `landed`, a bit a stage
-      bool ok = true;
-      for (int u = u0; u < n_units && ok; u += ustep) {
-        const Unit t = unit_of(u);
-        const int steps = steps_of(t);
-        g += steps;
-        if (!(t.clen & 15)) continue;
-        const uint32_t s = (g - 1) % STAGES;
-        ok = __all_sync(0xffffffffu, wait(&landed[s], (parity >> s) & 1));
-        if (!ok) break;
-        parity ^= 1u << s;
-        const int from = t.clen & 63, to = (from + 15) & ~15, pieces = 2 + ((t.n / 2 + 63) >> 6);
-        uint8_t* stage = sm + s * STAGE;
-        for (int i = lane; i < (to - from) * pieces * 8; i += 32) {
-          const int row = from + i / (pieces * 8), c = i % (pieces * 8);
-          *reinterpret_cast<uint4*>(stage + (c >> 3) * 8192 + row * 128 + (c & 7) * 16) = make_uint4(0, 0, 0, 0);
-        }
-        tc05::fence_async();
-        __syncwarp();
-        if (lane == 0) tc05::arrive_cluster(full0 + s * 8);
-      }
-    }
-  } else if (warp < 8) {
+  } else {
+    if (PROMOTE) tc05::regs_up<Regs<INT8>::HIGH>();
     // ---------------- output
     const int quad = warp & 3, half = warp >> 2;
     uint8_t* out = sm + OFF_OUT + warp * OUT_WARP;
@@ -325,12 +471,52 @@ __global__ void __launch_bounds__(PAIR_THREADS, 1)
     const int g = lane >> 2, q = lane & 3;
     uint32_t v = 0;
     bool ok = true;
+    // The accumulator is in registers (or in shared memory): back to the MMAs.
+    auto give_back = [&](uint32_t b) {
+      tc05::fence_before_sync();
+      __syncwarp();
+      if (lane == 0) tc05::arrive_cluster(tempty0 + b * 8);
+    };
     for (int u = u0; u < n_units && ok; u += ustep) {
       const Unit t = unit_of(u);
-      const int nh = t.n >> 1;
-      const bool any = steps_of(t) > 0;
-      const uint32_t b = v & 1;
-      if (any) {
+      const int nh = t.n >> 1, steps = steps_of(t);
+      const int live = min(nh, t.cnt - half * nh);  // columns of this half that are outputs
+      using S = typename Held<INT8>::type;
+      constexpr int CHUNKS = PROMOTE ? 4 : 1;
+      S held[CHUNKS][32];
+      uint32_t b = 0;
+      if (PROMOTE) {
+#pragma unroll
+        for (int c = 0; c < CHUNKS; ++c)
+#pragma unroll
+          for (int i = 0; i < 32; ++i) held[c][i] = 0;
+        constexpr int SEG = INT8 ? SEG_INT : SEG_F32;
+        for (int k = 0; k < steps; k += SEG) {
+          b = v & 1;
+          ok = __all_sync(0xffffffffu, wait(&tfull[b], (v >> 1) & 1));
+          if (!ok) break;
+          ++v;
+          tc05::fence_after_sync();
+#pragma unroll
+          for (int c = 0; c < CHUNKS; ++c) {
+            if (32 * c < live) {
+              uint32_t r[32];
+              const uint32_t ta = lanes + b * 256 + (uint32_t)(half * nh + 32 * c);
+              tc05::ld_16x256b_x4(ta, r);
+              tc05::ld_16x256b_x4(ta + (16u << 16), r + 16);
+              tc05::wait_ld32(r);
+#pragma unroll
+              for (int i = 0; i < 32; ++i) {
+                const float x = __uint_as_float(r[i]);
+                held[c][i] += INT8 ? (S)__float2int_rn(x) : (S)x;
+              }
+            }
+          }
+          give_back(b);
+        }
+        if (!ok) break;
+      } else if (steps > 0) {
+        b = v & 1;
         ok = __all_sync(0xffffffffu, wait(&tfull[b], (v >> 1) & 1));
         if (!ok) break;
         ++v;
@@ -339,22 +525,57 @@ __global__ void __launch_bounds__(PAIR_THREADS, 1)
       // first i of the warp's lanes (gated: of its 16 pairs), and the row of the output that o 0 of the unit is
       const int i0 = GATED ? (t.at * 8 + (int)rank * 4 + quad) * 16 : t.at * 256 + (int)rank * 128 + quad * 32;
       const size_t row0 = MODE == WEIGHTS ? (size_t)t.e * p.O + t.o0 : (size_t)t.o0;
-      const int live = min(nh, t.cnt - half * nh);  // columns of this half that are outputs
-      for (int c = 0; 32 * c < live; ++c) {
+      float sw[4] = {1.f, 1.f, 1.f, 1.f};  // integers: scales of lanes g, g + 8, g + 16, g + 24
+      if (INT8) {
+        const float* w = p.sw + (size_t)t.e * p.I * (GATED ? 2 : 1);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const int n = i0 + g + 8 * (GATED ? i & 1 : i);
+          sw[i] = __ldg(w + min(n, p.I - 1) + (GATED && i >= 2 ? p.I : 0));
+        }
+      }
+#pragma unroll
+      for (int c = 0; c < (PROMOTE ? CHUNKS : 4); ++c) {
+        if (32 * c >= live) break;
         uint32_t r[32];
-        if (any) {
+        if (!PROMOTE && steps > 0) {
           const uint32_t ta = lanes + b * 256 + (uint32_t)(half * nh + 32 * c);
           tc05::ld_16x256b_x4(ta, r);
           tc05::ld_16x256b_x4(ta + (16u << 16), r + 16);
           tc05::wait_ld32(r);
-        } else {
+        } else if (!PROMOTE) {
 #pragma unroll
           for (int i = 0; i < 32; ++i) r[i] = 0;
+        } else {
+          const size_t row = row0 + half * nh + 32 * c;
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            float sx[2] = {1.f, 1.f};
+            if (INT8) {
+#pragma unroll
+              for (int j = 0; j < 2; ++j) sx[j] = __ldg(p.sx + min(row + 8 * k + 2 * q + j, (size_t)p.M - 1));
+            }
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+              const int at = (j >> 2) * 16 + 4 * k + (j & 3);
+              const float x = (float)held[PROMOTE ? c : 0][at];
+              r[at] = __float_as_uint(INT8 ? x * (sx[j & 1] * sw[(j >> 2) * 2 + ((j >> 1) & 1)]) : x);
+            }
+          }
         }
         const int left = live - 32 * c;  // columns of the chunk that are outputs
         const size_t row = row0 + half * nh + 32 * c;
         auto f = [&](int h, int k, int j) { return __uint_as_float(r[16 * h + 4 * k + j]); };
-        if (GATED) {
+        if (GATED && F32) {
+          float* y = static_cast<float*>(p.y);
+#pragma unroll
+          for (int k = 0; k < 4; ++k)
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+              const int col = 8 * k + 2 * q + (j & 1), i = i0 + (j >> 1) * 8 + g;
+              if (col < left && i < p.I) y[(row + col) * p.I + i] = activation(f(0, k, j), p.act) * f(1, k, j);
+            }
+        } else if (GATED) {
           // A tile of 16 i's x 32 columns, through shared memory: rows of 32 bytes
           auto put = [&](uint16_t* to, size_t width, auto&& pair) {
             const uint32_t st = smem_u32(out) + ((lane >> 4) * 8 + (lane & 7)) * 48 + ((lane >> 3) & 1) * 16;
@@ -414,11 +635,7 @@ __global__ void __launch_bounds__(PAIR_THREADS, 1)
           __syncwarp();
         }
       }
-      if (any) {
-        tc05::fence_before_sync();
-        __syncwarp();
-        if (lane == 0) tc05::arrive_cluster(tempty0 + b * 8);
-      }
+      if (!PROMOTE && steps > 0) give_back(b);
     }
   }
   __syncwarp();
@@ -435,30 +652,30 @@ __global__ void __launch_bounds__(PAIR_THREADS, 1)
 
 EncodeTiled g_encode = nullptr;  // set once, under the caller's lock
 
-// A map of bf16 elements in the 128-byte swizzle, zeros outside.  dims from the innermost,
-// strides in elements from the second dimension on.
-bool encode(CUtensorMap* m, const void* base, std::initializer_list<uint64_t> dims,
+// A map of bf16 elements (size 2) or bytes in the 128-byte swizzle, zeros outside.  dims
+// from the innermost, strides in elements from the second dimension on.
+bool encode(CUtensorMap* m, int size, const void* base, std::initializer_list<uint64_t> dims,
             std::initializer_list<uint64_t> strides, std::initializer_list<uint32_t> box) {
   cuuint64_t d[5], s[4];
   cuuint32_t b[5], one[5] = {1, 1, 1, 1, 1};
   int n = 0;
   for (uint64_t v : dims) d[n++] = v;
   n = 0;
-  for (uint64_t v : strides) s[n++] = v * 2;
+  for (uint64_t v : strides) s[n++] = v * size;
   n = 0;
   for (uint32_t v : box) b[n++] = v;
-  return g_encode(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, (cuuint32_t)n, const_cast<void*>(base), d, s, b, one,
+  return g_encode(m, size == 2 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_UINT8, (cuuint32_t)n, const_cast<void*>(base), d, s, b, one,
                   CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                   CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-template <int MODE, bool GATED, bool F32>
+template <int MODE, bool GATED, bool F32, bool INT8 = false>
 cudaError_t launch(const PairArgs& p, const CUtensorMap& ma, const CUtensorMap& mb, long long most, int sm_count,
                    cudaStream_t st) {
   const int pairs = sm_count / 2;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(2u * (unsigned)(most < pairs ? most : pairs));
-  cfg.blockDim = dim3(PAIR_THREADS);
+  cfg.blockDim = dim3(Regs<INT8>::THREADS);
   cfg.dynamicSmemBytes = pair_smem(p.E);
   cfg.stream = st;
   cudaLaunchAttribute attr[2];
@@ -470,7 +687,7 @@ cudaError_t launch(const PairArgs& p, const CUtensorMap& ma, const CUtensorMap& 
   attr[1].val.clusterDim.z = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 2;
-  return cudaLaunchKernelEx(&cfg, pair_gemm_kernel<MODE, GATED, F32>, p, ma, mb);
+  return cudaLaunchKernelEx(&cfg, pair_gemm_kernel<MODE, GATED, F32, INT8>, p, ma, mb);
 }
 
 // Tiles of rows that a grouped (or dense) product may have, at most.
@@ -490,21 +707,30 @@ cudaError_t pair_gemm_kernels_init() {
     if (q != cudaDriverEntryPointSuccess || fn == nullptr) return cudaErrorNotSupported;
     g_encode = reinterpret_cast<EncodeTiled>(fn);
   }
-  const void* k[] = {reinterpret_cast<const void*>(pair_gemm_kernel<FORWARD, true, false>),
-                     reinterpret_cast<const void*>(pair_gemm_kernel<FORWARD, false, false>),
-                     reinterpret_cast<const void*>(pair_gemm_kernel<FORWARD, false, true>),
-                     reinterpret_cast<const void*>(pair_gemm_kernel<INPUT, false, false>),
-                     reinterpret_cast<const void*>(pair_gemm_kernel<WEIGHTS, false, false>),
-                     reinterpret_cast<const void*>(pair_gemm_kernel<WEIGHTS, false, true>)};
-  for (const void* f : k) {
-    const cudaError_t e =
-        cudaFuncSetAttribute(f, cudaFuncAttributeMaxDynamicSharedMemorySize, pair_smem(ROUTE_MAX_E));
+  const struct {
+    const void* f;
+    int regs;  // that its shares are counted from
+  } k[] = {{reinterpret_cast<const void*>(pair_gemm_kernel<FORWARD, true, false, false>), 0},
+           {reinterpret_cast<const void*>(pair_gemm_kernel<FORWARD, false, false, false>), 0},
+           {reinterpret_cast<const void*>(pair_gemm_kernel<INPUT, false, false, false>), 0},
+           {reinterpret_cast<const void*>(pair_gemm_kernel<WEIGHTS, false, false, false>), 0},
+           {reinterpret_cast<const void*>(pair_gemm_kernel<FORWARD, false, true, false>), Regs<false>::LAUNCH},
+           {reinterpret_cast<const void*>(pair_gemm_kernel<WEIGHTS, false, true, false>), Regs<false>::LAUNCH},
+           {reinterpret_cast<const void*>(pair_gemm_kernel<FORWARD, false, false, true>), Regs<true>::LAUNCH},
+           {reinterpret_cast<const void*>(pair_gemm_kernel<FORWARD, false, true, true>), Regs<true>::LAUNCH},
+           {reinterpret_cast<const void*>(pair_gemm_kernel<FORWARD, true, false, true>), Regs<true>::LAUNCH},
+           {reinterpret_cast<const void*>(pair_gemm_kernel<FORWARD, true, true, true>), Regs<true>::LAUNCH}};
+  for (const auto& x : k) {
+    cudaError_t e = cudaFuncSetAttribute(x.f, cudaFuncAttributeMaxDynamicSharedMemorySize, pair_smem(ROUTE_MAX_E));
     if (e != cudaSuccess) return e;
+    cudaFuncAttributes fa;
+    if ((e = cudaFuncGetAttributes(&fa, x.f)) != cudaSuccess) return e;
+    if (fa.numRegs < x.regs) return cudaErrorInvalidConfiguration;  // the shares would never be met
   }
   return cudaSuccess;
 }
 
-cudaError_t launch_pair_forward(const ProductArgs& a, int sm_count, unsigned* err, cudaStream_t st) {
+cudaError_t launch_pair_forward(const ProductArgs& a, bool int8, int sm_count, unsigned* err, cudaStream_t st) {
   const bool gated = a.act != FFN_NONE;
   const uint64_t M = a.M, N = a.N, K = a.K, E = a.E;
   PairArgs p = {};
@@ -521,12 +747,22 @@ cudaError_t launch_pair_forward(const ProductArgs& a, int sm_count, unsigned* er
   p.box = 32;
   p.band = 8;
   p.act = a.act;
+  p.sx = a.sx;
+  p.sw = a.sw;
   CUtensorMap ma, mb;
+  const int size = int8 ? 1 : 2;
+  const uint32_t inner = 128 / size;
   const bool ok =
-      gated ? encode(&ma, a.w, {K, 16, 2, N / 32, E}, {K, N / 2 * K, 16 * K, N * K}, {64, 16, 2, 4, 1})
-            : encode(&ma, a.w, {K, N, E}, {K, N * K}, {64, 128, 1});
-  if (!ok || !encode(&mb, a.x, {K, M}, {K}, {64, (uint32_t)p.box})) return cudaErrorInvalidValue;
+      gated ? encode(&ma, size, a.w, {K, 16, 2, N / 32, E}, {K, N / 2 * K, 16 * K, N * K}, {inner, 16, 2, 4, 1})
+            : encode(&ma, size, a.w, {K, N, E}, {K, N * K}, {inner, 128, 1});
+  if (!ok || !encode(&mb, size, a.x, {K, M}, {K}, {inner, (uint32_t)p.box})) return cudaErrorInvalidValue;
   const long long most = row_tiles(a.M, a.E, a.offsets != nullptr, p.tile) * p.a_tiles;
+  if (int8) {
+    if (gated) return a.f32 ? launch<FORWARD, true, true, true>(p, ma, mb, most, sm_count, st)
+                            : launch<FORWARD, true, false, true>(p, ma, mb, most, sm_count, st);
+    return a.f32 ? launch<FORWARD, false, true, true>(p, ma, mb, most, sm_count, st)
+                 : launch<FORWARD, false, false, true>(p, ma, mb, most, sm_count, st);
+  }
   if (gated) return launch<FORWARD, true, false>(p, ma, mb, most, sm_count, st);
   return a.f32 ? launch<FORWARD, false, true>(p, ma, mb, most, sm_count, st)
                : launch<FORWARD, false, false>(p, ma, mb, most, sm_count, st);
@@ -547,7 +783,7 @@ cudaError_t launch_pair_input(const GradArgs& a, int sm_count, unsigned* err, cu
   p.box = 32;
   p.band = 8;
   CUtensorMap ma, mb;
-  if (!encode(&ma, a.other, {K, N, E}, {K, N * K}, {64, 64, 1}) || !encode(&mb, a.dy, {N, M}, {N}, {64, (uint32_t)p.box}))
+  if (!encode(&ma, 2, a.other, {K, N, E}, {K, N * K}, {64, 64, 1}) || !encode(&mb, 2, a.dy, {N, M}, {N}, {64, (uint32_t)p.box}))
     return cudaErrorInvalidValue;
   return launch<INPUT, false, false>(p, ma, mb, row_tiles(a.M, a.E, a.offsets != nullptr, p.tile) * p.a_tiles, sm_count, st);
 }
@@ -568,7 +804,7 @@ cudaError_t launch_pair_weights(const GradArgs& a, int sm_count, unsigned* err, 
   p.box = 64;
   p.band = 8;
   CUtensorMap ma, mb;
-  if (!encode(&ma, a.other, {K, M}, {K}, {64, 64}) || !encode(&mb, a.dy, {N, M}, {N}, {64, 64}))
+  if (!encode(&ma, 2, a.other, {K, M}, {K}, {64, 64}) || !encode(&mb, 2, a.dy, {N, M}, {N}, {64, 64}))
     return cudaErrorInvalidValue;
   const long long most = (long long)a.E * p.a_tiles * p.o_tiles;
   return a.f32 ? launch<WEIGHTS, false, true>(p, ma, mb, most, sm_count, st)

@@ -66,14 +66,12 @@ __device__ __forceinline__ void mma_pair(uint32_t d_tmem, uint64_t a_desc, uint6
       "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate)
       : "memory");
 }
-// Arrives (once) on the mbarrier at this offset in both CTAs of the pair when all MMAs
-// that the warp issued that way so far have completed.
-__device__ __forceinline__ void commit_pair(uint64_t* bar) {
+// Arrives (once) on an mbarrier of either CTA, given by its shared-cluster address, when all
+// MMAs that the warp issued that way so far have completed.
+__device__ __forceinline__ void commit_pair(uint32_t cluster_addr) {
   asm volatile(
       "{\n .reg .pred e;\n elect.sync _|e, 0xffffffff;\n"
-      " @e tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;\n}\n" ::"r"(
-          smem_u32(bar)),
-      "h"((uint16_t)3)
+      " @e tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.b64 [%0];\n}\n" ::"r"(cluster_addr)
       : "memory");
 }
 

@@ -61,7 +61,7 @@ def slope(g, act):
 def integer_rows(x):
     """codes [rows][K] and fp32 scales [rows] of finite rows."""
     top = x.double().abs().amax(1).clamp(min=FLOOR)
-    scale = (top / 127).float()
+    scale = (top * torch.tensor(1 / 127, dtype=torch.float32).double()).float()  # a product of two fp32 is exact in 64 bits
     z = x.double() / scale.double()[:, None]
     q = torch.floor(z)
     rest = z - q
