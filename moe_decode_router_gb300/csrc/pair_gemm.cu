@@ -27,13 +27,15 @@
 // 8-bit integers.  This GPU's tensor cores take none at a rate worth using, but a code is
 // exact in fp16, a product of two in fp32, and a sum of 1,024 products stays within 2^24,
 // where fp32 holds every whole number.  Codes land in a ring of their own (128 of K a
-// stage); four warps turn them into fp16 operands (code + 1152 is put together from the
-// bits, 1152 taken off) and every 1,024 of K the accumulator is added to 32-bit integers in
-// registers.  fp32 outputs of bf16 operands are promoted the same way every 512 of the
+// stage); eight warps turn them into fp16 (code + 1152 is put together from the bits,
+// 1152 taken off), the weights' into tensor memory and the others into shared memory, whose
+// bandwidth would be the bound with both: 96 KB for 64 of K, 768 cycles against 512 of MMA.
+// Every 1,024 of K the accumulator (one alone, beside the weights) is added to 32-bit
+// integers in registers.  fp32 outputs of bf16 operands are promoted the same way every 512 of the
 // contracted dimension: the tensor cores cut a sum instead of rounding it, which adds up.
 //
 // Warps: 0-7 output, two halves of the columns; 8 TMA producer; 9 MMA issuer (of the even
-// CTA); 10 rows behind the end (WEIGHTS); 11 none; 12-15 codes to fp16 (integers).
+// CTA); 10 rows behind the end (WEIGHTS); 11 none; 12-15 and 16-19 codes to fp16 (integers).
 #include <initializer_list>
 
 #include "product_common.cuh"
@@ -46,8 +48,10 @@ namespace {
 enum { FORWARD, INPUT, WEIGHTS };
 
 constexpr int A_BYTES = 128 * 128, B_BYTES = 128 * 128, STAGE = A_BYTES + B_BYTES;
-constexpr int RING = 6;            // stages of operands; of integers 3, and 3 of codes (128 of K each) behind them
-constexpr int CODES = 3;
+constexpr int RING = 6;            // stages of operands
+constexpr int CODES = 4;           // integers: stages of codes, 128 of K each, then
+constexpr int TURNED = 4;          //   stages of one operand in fp16, and as many in tensor memory behind the sums
+static_assert(CODES * STAGE + TURNED * B_BYTES <= RING * STAGE, "rings");
 constexpr int OUT_WARP = 32 * 80;  // output staging of a warp: 32 rows of 64 bytes, 80 apart
 constexpr int OFF_OUT = RING * STAGE;
 constexpr int OFF_BARS = OFF_OUT + 8 * OUT_WARP;
@@ -57,8 +61,8 @@ constexpr int SEG_F32 = 8, SEG_INT = 16;  // steps of 64 between promotions
 // the others give up; a block is launched with LAUNCH of them.
 template <bool INT8>
 struct Regs {
-  static constexpr int THREADS = INT8 ? 512 : 384, LAUNCH = INT8 ? 128 : 168;
-  static constexpr int HIGH = INT8 ? 192 : 224, LOW = INT8 ? 64 : 48;
+  static constexpr int THREADS = INT8 ? 640 : 384, LAUNCH = INT8 ? 96 : 168;
+  static constexpr int HIGH = INT8 ? 168 : 224, LOW = 48;
   static_assert(HIGH * 256 + LOW * (THREADS - 256) <= LAUNCH * THREADS, "register shares");
 };
 constexpr int OFF_GROUPS = OFF_BARS + 256;
@@ -118,7 +122,7 @@ template <int MODE, bool GATED, bool F32, bool INT8>
 __global__ void __launch_bounds__(Regs<INT8>::THREADS, 1)
     pair_gemm_kernel(const PairArgs p, const __grid_constant__ CUtensorMap map_a,
                      const __grid_constant__ CUtensorMap map_b) {
-  constexpr int STAGES = INT8 ? RING - CODES : RING, THREADS = Regs<INT8>::THREADS;
+  constexpr int STAGES = INT8 ? TURNED : RING, BUFS = INT8 ? 1 : 2, THREADS = Regs<INT8>::THREADS;
   constexpr bool PROMOTE = F32 || INT8;
   static_assert(!INT8 || MODE == FORWARD, "integers have no gradient");
   extern __shared__ __align__(1024) uint8_t smem_raw[];
@@ -140,11 +144,11 @@ __global__ void __launch_bounds__(Regs<INT8>::THREADS, 1)
 
   if (tid == 0) {
     for (int i = 0; i < STAGES; ++i) {
-      mbar_init(&full[i], INT8 ? 8 : MODE == WEIGHTS ? 2 : 1);
+      mbar_init(&full[i], INT8 ? 16 : MODE == WEIGHTS ? 2 : 1);
       mbar_init(&empty[i], 1);
     }
     for (int i = 0; i < RING; ++i) mbar_init(&landed[i], 1);
-    for (int i = 0; i < CODES; ++i) mbar_init(&taken[i], 4);
+    for (int i = 0; i < CODES; ++i) mbar_init(&taken[i], 8);
     for (int i = 0; i < 2; ++i) {
       mbar_init(&tfull[i], 1);
       mbar_init(&tempty[i], 16);
@@ -252,7 +256,7 @@ __global__ void __launch_bounds__(Regs<INT8>::THREADS, 1)
             ok = false;
             break;
           }
-          const uint32_t a = base + (STAGES + r) * STAGE, b = a + A_BYTES, bar = smem_u32(&landed[r]);
+          const uint32_t a = base + r * STAGE, b = a + A_BYTES, bar = smem_u32(&landed[r]);
           mbar_arrive_expect_tx(&landed[r], bytes);
           if (GATED) tc05::tma_pair_5d(a, &map_a, k * 128, 0, 0, t.at * 8 + (int)rank * 4, t.e, bar);
           else tc05::tma_pair_3d(a, &map_a, k * 128, t.at * 256 + (int)rank * 128, t.e, bar);
@@ -275,40 +279,58 @@ __global__ void __launch_bounds__(Regs<INT8>::THREADS, 1)
         }
       }
     } else if (INT8 && warp >= 12) {
-      // ---------------- codes to fp16: 64 of K at a time.  A warp takes 8 rows (a swizzle
-      // atom) at once, a lane 16 codes of a row; the 8 lanes that shared memory serves
-      // together have two rows r and r ^ 5, whose swizzled places differ on the way in
-      // (bit 2) and on the way out (bit 0).
-      constexpr int AT_ONCE = 4;
+      // ---------------- codes to fp16, 64 of K at a time
       uint32_t s = 0, ph = 0, r = 0, rph = 0;
       bool ok = true;
+      // Warps 12-15, the weights: a lane has a row, that of its lane of tensor memory (the
+      // swizzle puts 8 neighbouring rows' pieces in different places).
+      const int arow = (warp & 3) * 32 + lane;
+      const uint32_t a_to = tmem + 256 + ((uint32_t)((warp & 3) * 32) << 16);
+      // Warps 16-19, the other operand: a warp takes 8 rows (a swizzle atom) at once, a lane
+      // 16 codes of a row; the 8 lanes that shared memory serves together have two rows r and
+      // r ^ 5, whose swizzled places differ on the way in (bit 2) and on the way out (bit 0).
       const int q = lane & 3, row = (lane >> 3) ^ (lane & 4 ? 5 : 0);
+      const int lo = ((2 * q) ^ row) << 4, hi = ((2 * q + 1) ^ row) << 4;
       for (int u = u0; u < n_units && ok; u += ustep) {
         const Unit t = unit_of(u);
-        const int atoms = 16 + (t.n >> 4);  // of A, then of B's half
+        const int atoms = t.n >> 4;
         for (int k = 0; k < p.steps; ++k) {
           if ((k & 1) == 0) ok = __all_sync(0xffffffffu, wait(&landed[r], rph));
           ok = ok && __all_sync(0xffffffffu, wait(&empty[s], ph ^ 1));
           if (!ok) break;
-          const uint8_t* from = sm + (STAGES + r) * STAGE + row * 128 + ((((k & 1) * 4 + q) ^ row) << 4);
-          uint8_t* to = sm + s * STAGE + row * 128;
-          const int lo = ((2 * q) ^ row) << 4, hi = ((2 * q + 1) ^ row) << 4;
-          for (int a = warp - 12; a < atoms; a += 4 * AT_ONCE) {
-            uint4 c[AT_ONCE];
-  #pragma unroll
-            for (int i = 0; i < AT_ONCE; ++i)
-              if (a + 4 * i < atoms) c[i] = *reinterpret_cast<const uint4*>(from + (a + 4 * i) * 1024);
-  #pragma unroll
-            for (int i = 0; i < AT_ONCE; ++i)
-              if (a + 4 * i < atoms) {
+          const uint8_t* from = sm + r * STAGE;
+          if (warp < 16) {
+            tc05::fence_after_sync();
+            const uint8_t* at = from + arow * 128;
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+              const uint4 c0 = *reinterpret_cast<const uint4*>(at + ((((k & 1) * 4 + 2 * h) ^ (arow & 7)) << 4));
+              const uint4 c1 = *reinterpret_cast<const uint4*>(at + ((((k & 1) * 4 + 2 * h + 1) ^ (arow & 7)) << 4));
+              uint4 v[4];
+              codes_to_f16(c0, v[0], v[1]);
+              codes_to_f16(c1, v[2], v[3]);
+              tc05::st_32x32b_x16(a_to + s * 32 + h * 16, v);
+            }
+            tc05::wait_st();
+            tc05::fence_before_sync();
+          } else {
+            const uint8_t* at = from + A_BYTES + row * 128 + ((((k & 1) * 4 + q) ^ row) << 4);
+            uint8_t* to = sm + CODES * STAGE + s * B_BYTES + row * 128;
+            uint4 c[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+              if (warp - 16 + 4 * i < atoms) c[i] = *reinterpret_cast<const uint4*>(at + (warp - 16 + 4 * i) * 1024);
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+              if (warp - 16 + 4 * i < atoms) {
                 uint4 v0, v1;
                 codes_to_f16(c[i], v0, v1);
-                uint8_t* at = to + (a + 4 * i) * 1024;
-                *reinterpret_cast<uint4*>(at + lo) = v0;
-                *reinterpret_cast<uint4*>(at + hi) = v1;
+                uint8_t* d = to + (warp - 16 + 4 * i) * 1024;
+                *reinterpret_cast<uint4*>(d + lo) = v0;
+                *reinterpret_cast<uint4*>(d + hi) = v1;
               }
+            tc05::fence_proxy_async_smem();
           }
-          tc05::fence_proxy_async_smem();
           __syncwarp();
           if (lane == 0) tc05::arrive_cluster(full0 + s * 8);
           if (++s == STAGES) {
@@ -398,6 +420,7 @@ __global__ void __launch_bounds__(Regs<INT8>::THREADS, 1)
         const uint32_t bars[2] = {full0, tc05::map_rank(smem_u32(full), 1)};  // of either CTA
         const uint64_t da0 = A_ROWS ? tc05::sw128_rows_desc(base, 8192) : tc05::sw128_desc(base);
         const uint64_t db0 = B_ROWS ? tc05::sw128_rows_desc(base + A_BYTES, 8192) : tc05::sw128_desc(base + A_BYTES);
+        const uint64_t db8 = tc05::sw128_desc(base + CODES * STAGE);
         constexpr uint32_t DA = A_ROWS ? 128 : 2, DB = B_ROWS ? 128 : 2;  // 16 of the contracted dimension
         for (int u = u0; u < n_units && ok; u += ustep) {
           const Unit t = unit_of(u);
@@ -407,17 +430,20 @@ __global__ void __launch_bounds__(Regs<INT8>::THREADS, 1)
           for (int k = 0; k < steps; ++k) {
             const bool fresh = PROMOTE ? k % SEG == 0 : k == 0;
             const bool last = k == steps - 1 || (PROMOTE && k % SEG == SEG - 1);
-            const uint32_t b = v & 1, d = tmem + b * 256;
+            const uint32_t b = v % BUFS, d = tmem + b * 256;
             // every lane waits, and all go on or none
-            ok = !fresh || __all_sync(0xffffffffu, wait(&tempty[b], ((v >> 1) & 1) ^ 1));
+            ok = !fresh || __all_sync(0xffffffffu, wait(&tempty[b], ((v / BUFS) & 1) ^ 1));
             ok = ok && __all_sync(0xffffffffu, wait(&full[s], ph));
             if (!ok) break;
             tc05::fence_after_sync();
             const uint64_t da = da0 + s * (STAGE >> 4), db = db0 + s * (STAGE >> 4);
             const int parts = MODE == WEIGHTS && k == steps - 1 ? (((t.clen - 1) & 63) >> 4) + 1 : 4;
   #pragma unroll
-            for (int j = 0; j < 4; ++j)
-              if (j < parts) tc05::mma_pair(d, da + j * DA, db + j * DB, idesc, !fresh || j > 0 ? 1u : 0u);
+            for (int j = 0; j < 4; ++j) {
+              const uint32_t more = !fresh || j > 0 ? 1u : 0u;
+              if (INT8) tc05::mma_pair_ts(d, tmem + 256 + s * 32 + j * 8, db8 + s * (B_BYTES >> 4) + j * DB, idesc, more);
+              else if (j < parts) tc05::mma_pair(d, da + j * DA, db + j * DB, idesc, more);
+            }
             for (int c = 0; c < 2; ++c) tc05::commit_pair(bars[c] + STAGES * 8 + s * 8);  // empty
             if (last) {
               for (int c = 0; c < 2; ++c) tc05::commit_pair(bars[c] + TFULL + b * 8);
@@ -492,8 +518,8 @@ __global__ void __launch_bounds__(Regs<INT8>::THREADS, 1)
           for (int i = 0; i < 32; ++i) held[c][i] = 0;
         constexpr int SEG = INT8 ? SEG_INT : SEG_F32;
         for (int k = 0; k < steps; k += SEG) {
-          b = v & 1;
-          ok = __all_sync(0xffffffffu, wait(&tfull[b], (v >> 1) & 1));
+          b = v % BUFS;
+          ok = __all_sync(0xffffffffu, wait(&tfull[b], (v / BUFS) & 1));
           if (!ok) break;
           ++v;
           tc05::fence_after_sync();
@@ -516,8 +542,8 @@ __global__ void __launch_bounds__(Regs<INT8>::THREADS, 1)
         }
         if (!ok) break;
       } else if (steps > 0) {
-        b = v & 1;
-        ok = __all_sync(0xffffffffu, wait(&tfull[b], (v >> 1) & 1));
+        b = v % BUFS;
+        ok = __all_sync(0xffffffffu, wait(&tfull[b], (v / BUFS) & 1));
         if (!ok) break;
         ++v;
         tc05::fence_after_sync();
