@@ -198,19 +198,20 @@ cudaError_t launch_few_rows(const ProductArgs& p, bool int8, cudaStream_t st);  
 // dgu [M][2 I] from dh [M][I] and the kept sums gu [M][2 I] (gradients.cu)
 cudaError_t launch_gate_backward(const void* dh, const void* gu, const int32_t* offsets, int M, int I, int E, int act,
                                  void* dgu, cudaStream_t st);
-// dx [M][K] = dy [M][N] w, or dw [E][N][K] = dy^T x by expert
+// dx [M][K] = dy [M][N] w and dw [E][N][K] = dy^T x by expert; either may be null
 struct GradArgs {
   const void* dy;
-  const void* other;  // w or x
+  const void* x;
+  const void* w;
   const int32_t* offsets;
-  void* out;
-  int M, N, K, E, f32;
+  void* dx;
+  void* dw;
+  int M, N, K, E, f32;  // f32: dw is fp32
 };
 // tcgen05 over pairs of CTAs (pair_gemm.cu)
 cudaError_t pair_gemm_kernels_init();
 cudaError_t launch_pair_forward(const ProductArgs& p, bool int8, int sm_count, unsigned* err, cudaStream_t st);
-cudaError_t launch_pair_input(const GradArgs& p, int sm_count, unsigned* err, cudaStream_t st);
-cudaError_t launch_pair_weights(const GradArgs& p, int sm_count, unsigned* err, cudaStream_t st);
+cudaError_t launch_pair_backward(const GradArgs& p, int sm_count, unsigned* err, cudaStream_t st);
 // Rows to 8-bit integers with one scale each (integer_rows.cu)
 cudaError_t launch_integer_rows(const void* x, bool bf16, long long stride, int rows, int K, const int32_t* pos,
                                 int top_k, int places, void* q, float* scales, cudaStream_t st);

@@ -98,27 +98,9 @@ int product(const ProductArgs& p, bool int8, flint_moe_stream_t stream) {
 
 int gradients(const void* dy, const void* x, int M, const void* w, int E, const int32_t* offsets, int N, int K,
               void* dx, void* dw, int dw_type, const Device& d, cudaStream_t st) {
-  GradArgs p;
-  p.dy = dy;
-  p.offsets = offsets;
-  p.M = M;
-  p.N = N;
-  p.K = K;
-  p.E = E;
-  cudaError_t e = cudaSuccess;
-  if (dx != nullptr) {
-    p.other = w;
-    p.out = dx;
-    p.f32 = 0;
-    e = launch_pair_input(p, d.sms, d.err, st);
-  }
-  if (e == cudaSuccess && dw != nullptr) {
-    p.other = x;
-    p.out = dw;
-    p.f32 = dw_type == FLINT_MOE_T_F32;
-    e = launch_pair_weights(p, d.sms, d.err, st);
-  }
-  return to_status(e);
+  const GradArgs p = {dy, x, w, offsets, dx, dw, M, N, K, E, dw_type == FLINT_MOE_T_F32};
+  if (dx == nullptr && dw == nullptr) return FLINT_MOE_OK;
+  return to_status(launch_pair_backward(p, d.sms, d.err, st));
 }
 
 }  // namespace

@@ -1,12 +1,12 @@
 // Products on the tensor cores (tcgen05 over pairs of CTAs), dense or grouped by expert:
 // linear and gated products in bf16 and their gradients, and 8-bit integer products.
 //
-// One kernel for three products.  The M side of the MMA is the dimension that lies
-// contiguous in the output (i), always 256 of it a unit; the N side (o), up to 256 in
-// steps of 32, is what is ragged:
-//   FORWARD  y[m][n]     i = n: weights by rows       o = m: rows of x       sum over k
-//   INPUT    dx[m][k]    i = k: weights by columns    o = m: rows of dy      sum over n
-//   WEIGHTS  dw[e][n][k] i = k: columns of x          o = n: columns of dy   sum over the rows m of e
+// Three products in one kernel (both gradients in one launch, an expert's after one another).  The M
+// side of the MMA is the dimension that lies contiguous in the output (i), always 256 of it a
+// unit; the N side (o), up to 256 in steps of 32, is what is ragged:
+//   forward  y[m][n]     i = n: weights by rows       o = m: rows of x       sum over k
+//   input    dx[m][k]    i = k: weights by columns    o = m: rows of dy      sum over n
+//   weights  dw[e][n][k] i = k: columns of x          o = n: columns of dy   sum over the rows m of e
 // An operand whose M or N dimension is contiguous in memory is taken as it lies (the
 // descriptors' other major order), so nothing is transposed on the way in; on the way out
 // the accumulator (lanes i, columns o) is turned by stmatrix into rows of the output.
@@ -17,10 +17,11 @@
 //
 // Each CTA loads its 128 rows of A and half of B, 64 of the contracted dimension at a time
 // (128 bytes, 128-byte swizzle): 32 KB a stage and CTA against 512 cycles of MMA, 64 bytes
-// a cycle and SM; a CTA by itself would load 96.  The accumulator is double-buffered in
+// a cycle and SM; a CTA by itself would load 96.  A stage is two copies, as large as they may be: with
+// boxes of 32 rows of B (five copies a stage) 8192 x 8192 x 8192 took 693 us, with 128 574.  The accumulator is double-buffered in
 // tensor memory, so that a unit's output overlaps the next one's products.
 //
-// WEIGHTS contracts over an expert's rows, which end anywhere: whole steps of 16 rows are
+// The weights' gradient contracts over an expert's rows, which end anywhere: whole steps of 16 rows are
 // multiplied, and in the last a warp of each CTA overwrites the rows behind the end (another
 // expert's, perhaps infinite) with zeros before the stage is handed on.
 //
@@ -35,7 +36,7 @@
 // contracted dimension: the tensor cores cut a sum instead of rounding it, which adds up.
 //
 // Warps: 0-7 output, two halves of the columns; 8 TMA producer; 9 MMA issuer (of the even
-// CTA); 10 rows behind the end (WEIGHTS); 11 none; 12-15 and 16-19 codes to fp16 (integers).
+// CTA); 10 rows behind the end; 11 none; 12-15 and 16-19 codes to fp16 (integers).
 #include <initializer_list>
 
 #include "product_common.cuh"
@@ -45,7 +46,7 @@ namespace flint {
 
 namespace {
 
-enum { FORWARD, INPUT, WEIGHTS };
+enum { FORWARD, BACKWARD };
 
 constexpr int A_BYTES = 128 * 128, B_BYTES = 128 * 128, STAGE = A_BYTES + B_BYTES;
 constexpr int RING = 6;            // stages of operands
@@ -72,26 +73,38 @@ static_assert((3 * RING + CODES + 4) * 8 + 8 <= 256, "barriers");
 
 struct PairArgs {
   const int32_t* offsets;
-  void* y;
-  uint16_t* keep;  // gated: the sums, or null
+  void* y;          // forward: y; backward: dx, or null
+  void* dw;         // backward: or null
+  uint16_t* keep;   // gated: the sums, or null
   const float* sx;  // integers: scales
   const float* sw;
   unsigned* err;
   int M, E;
-  int I;        // width of the output (i)
-  int O;        // WEIGHTS: N
-  int steps;    // FORWARD, INPUT: steps of 64 of the contracted dimension
-  int a_tiles;  // units side by side in i
-  int tile;     // o's of a unit, at most: a multiple of 32
-  int o_tiles;  // WEIGHTS: units side by side in o
-  int box;      // rows of B in one copy
-  int band;     // tiles of o that go side by side
+  int I;          // width of the outputs (i)
+  int O;          // backward: N, rows of an expert's dw
+  int steps;      // forward, input: steps of 64 of the contracted dimension
+  int a_tiles;    // units side by side in i
+  int tile;       // forward, input: o's of a unit, at most (a multiple of 32)
+  int tile_w;     // weights: the same
+  int o_tiles;    // weights: units side by side in o, 0: not wanted
+  int band;       // tiles of o that go side by side
   int act;
+  bool pieces_k, pieces_n;  // K, N are multiples of 64: two pieces of 64 make one copy
+};
+
+// Boxes of operands in shared memory: rows of 128 bytes.
+struct Maps {
+  CUtensorMap a;     // forward: 128 rows of weights; input: 64 columns of 64 rows of weights (or 2 x 64 columns)
+  CUtensorMap b[4];  // 16, 32, 64 or 128 rows of x (dy)
+  CUtensorMap aw;    // weights: 64 columns of 64 rows of x (or 2 x 64)
+  CUtensorMap bw;    // weights: 64 columns of 64 rows of dy
+  CUtensorMap bw2;   // weights: 2 x 64
 };
 
 struct Unit {
   int e, at, o0, cnt, n;  // tile of i; first o and how many; columns of the MMAs
-  int c0, clen;           // WEIGHTS: the expert's rows
+  bool weights;
+  int c0, clen;           // weights: the expert's rows
 };
 
 // Sums of a promoting kernel.
@@ -120,8 +133,7 @@ __device__ __forceinline__ void codes_to_f16(const uint4 c, uint4& lo, uint4& hi
 
 template <int MODE, bool GATED, bool F32, bool INT8>
 __global__ void __launch_bounds__(Regs<INT8>::THREADS, 1)
-    pair_gemm_kernel(const PairArgs p, const __grid_constant__ CUtensorMap map_a,
-                     const __grid_constant__ CUtensorMap map_b) {
+    pair_gemm_kernel(const PairArgs p, const __grid_constant__ Maps maps) {
   constexpr int STAGES = INT8 ? TURNED : RING, BUFS = INT8 ? 1 : 2, THREADS = Regs<INT8>::THREADS;
   constexpr bool PROMOTE = F32 || INT8;
   static_assert(!INT8 || MODE == FORWARD, "integers have no gradient");
@@ -131,7 +143,7 @@ __global__ void __launch_bounds__(Regs<INT8>::THREADS, 1)
   const uint32_t rank = tc05::cluster_rank();
   uint64_t* full = reinterpret_cast<uint64_t*>(sm + OFF_BARS);  // [STAGES] both CTAs' operands landed (even CTA's)
   uint64_t* empty = full + STAGES;                              // [STAGES] stage consumed
-  uint64_t* landed = empty + STAGES;                            // [STAGES] WEIGHTS: a last stage of this CTA landed;
+  uint64_t* landed = empty + STAGES;                            // [STAGES] weights: a last stage of this CTA landed;
                                                                 // [CODES] integers: codes of this CTA landed
   uint64_t* taken = landed + RING;                              // [CODES] integers: codes turned
   uint64_t* tfull = taken + CODES;                              // [2] accumulator complete
@@ -144,7 +156,7 @@ __global__ void __launch_bounds__(Regs<INT8>::THREADS, 1)
 
   if (tid == 0) {
     for (int i = 0; i < STAGES; ++i) {
-      mbar_init(&full[i], INT8 ? 16 : MODE == WEIGHTS ? 2 : 1);
+      mbar_init(&full[i], INT8 ? 16 : MODE == BACKWARD ? 2 : 1);
       mbar_init(&empty[i], 1);
     }
     for (int i = 0; i < RING; ++i) mbar_init(&landed[i], 1);
@@ -179,7 +191,9 @@ __global__ void __launch_bounds__(Regs<INT8>::THREADS, 1)
         g_cnt[e] = cnt;
       }
       __syncwarp();  // the offsets of these groups make room for their units; the next group's first is read below
-      int t = MODE == WEIGHTS ? (e < p.E ? p.o_tiles * p.a_tiles : 0) : (cnt + p.tile - 1) / p.tile * p.a_tiles;
+      int t = MODE == BACKWARD && p.y == nullptr ? 0 : (cnt + p.tile - 1) / p.tile;
+      if (MODE == BACKWARD && e < p.E) t += p.o_tiles;
+      t *= p.a_tiles;
       if (base > 1 << 29) t = 0;  // offsets that descend could count rows over and over: stay inside int
       int incl = t;
 #pragma unroll
@@ -208,16 +222,21 @@ __global__ void __launch_bounds__(Regs<INT8>::THREADS, 1)
     if (p.E > 32) from = 32 * (__popc(__ballot_sync(0xffffffffu, 32 * lane < p.E && g_units[32 * lane] <= u)) - 1);
     const int e = from + lane;
     t.e = from + __popc(__ballot_sync(0xffffffffu, e < p.E && g_units[e] <= u)) - 1;
-    const int v = u - g_units[t.e], rows = g_cnt[t.e];
-    const int tiles = MODE == WEIGHTS ? p.o_tiles : (rows + p.tile - 1) / p.tile;
+    const int rows = g_cnt[t.e];
+    int v = u - g_units[t.e], tiles = MODE == BACKWARD && p.y == nullptr ? 0 : (rows + p.tile - 1) / p.tile;
+    t.weights = MODE == BACKWARD && v >= tiles * p.a_tiles;
+    if (t.weights) {
+      v -= tiles * p.a_tiles;
+      tiles = p.o_tiles;
+    }
     // bands of neighbouring tiles of o, all of i within a band: what runs at a time shares both operands
     const int per = p.band * p.a_tiles, first = v / per * p.band, rest = v - v / per * per;
     const int high = min(p.band, tiles - first);
     t.at = rest / high;
     const int tile = first + rest - t.at * high;
-    if (MODE == WEIGHTS) {
-      t.o0 = tile * p.tile;
-      t.cnt = min(p.tile, p.O - t.o0);
+    if (t.weights) {
+      t.o0 = tile * p.tile_w;
+      t.cnt = min(p.tile_w, p.O - t.o0);
       t.c0 = g_lo[t.e];
       t.clen = rows;
     } else {
@@ -229,7 +248,7 @@ __global__ void __launch_bounds__(Regs<INT8>::THREADS, 1)
     t.n = max(32, (t.cnt + 31) & ~31);
     return t;
   };
-  auto steps_of = [&](const Unit& t) { return MODE == WEIGHTS ? (t.clen + 63) >> 6 : p.steps; };
+  auto steps_of = [&](const Unit& t) { return t.weights ? (t.clen + 63) >> 6 : p.steps; };
   // Bounded wait.  Lanes of a warp that wait together agree on the result: the awaited
   // phase cannot move on without a later arrival of this same warp.
   auto wait = [&](uint64_t* bar, uint32_t parity) -> bool {
@@ -240,6 +259,8 @@ __global__ void __launch_bounds__(Regs<INT8>::THREADS, 1)
     *abort_flag = 1;
     return false;
   };
+  // the smallest box of B that holds so many rows: 16 << box_of
+  auto box_of = [](int rows) { return rows <= 16 ? 0 : rows <= 32 ? 1 : rows <= 64 ? 2 : 3; };
   const uint32_t base = smem_u32(sm), full0 = tc05::map_rank(smem_u32(full), 0);
   if (warp >= 8) {
     if (PROMOTE) tc05::regs_down<Regs<INT8>::LOW>();
@@ -249,8 +270,8 @@ __global__ void __launch_bounds__(Regs<INT8>::THREADS, 1)
       bool ok = true;
       for (int u = u0; u < n_units && ok; u += ustep) {
         const Unit t = unit_of(u);
-        const int nh = t.n >> 1, oh = t.o0 + (int)rank * nh, boxes = (nh + p.box - 1) / p.box;
-        const uint32_t bytes = A_BYTES + boxes * p.box * 128;
+        const int nh = t.n >> 1, oh = t.o0 + (int)rank * nh, sel = box_of(nh);
+        const uint32_t bytes = A_BYTES + (2048u << sel);
         for (int k = 0; k < (p.steps + 1) >> 1 && lane == 0; ++k) {
           if (!wait(&taken[r], ph ^ 1)) {
             ok = false;
@@ -258,9 +279,9 @@ __global__ void __launch_bounds__(Regs<INT8>::THREADS, 1)
           }
           const uint32_t a = base + r * STAGE, b = a + A_BYTES, bar = smem_u32(&landed[r]);
           mbar_arrive_expect_tx(&landed[r], bytes);
-          if (GATED) tc05::tma_pair_5d(a, &map_a, k * 128, 0, 0, t.at * 8 + (int)rank * 4, t.e, bar);
-          else tc05::tma_pair_3d(a, &map_a, k * 128, t.at * 256 + (int)rank * 128, t.e, bar);
-          for (int i = 0; i < boxes; ++i) tc05::tma_pair_2d(b + i * p.box * 128, &map_b, k * 128, oh + i * p.box, bar);
+          if (GATED) tc05::tma_pair_5d(a, &maps.a, k * 128, 0, 0, t.at * 8 + (int)rank * 4, t.e, bar);
+          else tc05::tma_pair_3d(a, &maps.a, k * 128, t.at * 256 + (int)rank * 128, t.e, bar);
+          tc05::tma_pair_2d(b, &maps.b[sel], k * 128, oh, bar);
           ++issued;
           if (++r == CODES) {
             r = 0;
@@ -354,8 +375,9 @@ __global__ void __launch_bounds__(Regs<INT8>::THREADS, 1)
         const Unit t = unit_of(u);
         const int nh = t.n >> 1, steps = steps_of(t);
         const int i0 = t.at * 256 + (int)rank * 128, oh = t.o0 + (int)rank * nh;
-        const int boxes = MODE == WEIGHTS ? (nh + 63) >> 6 : (nh + p.box - 1) / p.box;
-        const uint32_t bytes = A_BYTES + boxes * (MODE == WEIGHTS ? 8192 : p.box * 128);
+        const int sel = box_of(nh), boxes = (nh + 63) >> 6;
+        const bool both = p.pieces_n && nh == 128;  // weights: two pieces of B at once
+        const uint32_t bytes = A_BYTES + (t.weights ? (uint32_t)boxes * 8192u : 2048u << sel);
         for (int k = 0; k < steps && lane == 0; ++k) {
           if (!wait(&empty[s], ph ^ 1)) {
             ok = false;
@@ -363,31 +385,37 @@ __global__ void __launch_bounds__(Regs<INT8>::THREADS, 1)
           }
           uint32_t bar = full0 + s * 8;
           const uint32_t a = base + s * STAGE, b = a + A_BYTES;
-          if (MODE == WEIGHTS) {
-            if (k == steps - 1 && (t.clen & 15)) {  // handed on by the warp that zeroes what lies behind the end
-              mbar_arrive_expect_tx(&landed[s], bytes);
-              bar = smem_u32(&landed[s]);
-            } else {
-              tc05::arrive_expect_cluster(bar, bytes);
-            }
-          } else if (rank == 0) {
-            mbar_arrive_expect_tx(&full[s], 2 * bytes);
+          if (MODE == FORWARD) {
+            if (rank == 0) mbar_arrive_expect_tx(&full[s], 2 * bytes);
+          } else if (t.weights && k == steps - 1 && (t.clen & 15)) {
+            mbar_arrive_expect_tx(&landed[s], bytes);  // handed on by the warp that zeroes what lies behind the end
+            bar = smem_u32(&landed[s]);
+          } else {
+            tc05::arrive_expect_cluster(bar, bytes);
           }
           if (MODE == FORWARD) {
-            if (GATED) tc05::tma_pair_5d(a, &map_a, k * 64, 0, 0, t.at * 8 + (int)rank * 4, t.e, bar);
-            else tc05::tma_pair_3d(a, &map_a, k * 64, i0, t.e, bar);
-            for (int i = 0; i < boxes; ++i)
-              tc05::tma_pair_2d(b + i * p.box * 128, &map_b, k * 64, oh + i * p.box, bar);
-          } else if (MODE == INPUT) {
-            tc05::tma_pair_3d(a, &map_a, i0, k * 64, t.e, bar);
-            tc05::tma_pair_3d(a + 8192, &map_a, i0 + 64, k * 64, t.e, bar);
-            for (int i = 0; i < boxes; ++i)
-              tc05::tma_pair_2d(b + i * p.box * 128, &map_b, k * 64, oh + i * p.box, bar);
+            if (GATED) tc05::tma_pair_5d(a, &maps.a, k * 64, 0, 0, t.at * 8 + (int)rank * 4, t.e, bar);
+            else tc05::tma_pair_3d(a, &maps.a, k * 64, i0, t.e, bar);
+            tc05::tma_pair_2d(b, &maps.b[sel], k * 64, oh, bar);
+          } else if (!t.weights) {
+            if (p.pieces_k) {
+              tc05::tma_pair_4d(a, &maps.a, 0, k * 64, i0 >> 6, t.e, bar);
+            } else {
+              tc05::tma_pair_3d(a, &maps.a, i0, k * 64, t.e, bar);
+              tc05::tma_pair_3d(a + 8192, &maps.a, i0 + 64, k * 64, t.e, bar);
+            }
+            tc05::tma_pair_2d(b, &maps.b[sel], k * 64, oh, bar);
           } else {
             const int c = t.c0 + k * 64;
-            tc05::tma_pair_2d(a, &map_a, i0, c, bar);
-            tc05::tma_pair_2d(a + 8192, &map_a, i0 + 64, c, bar);
-            for (int i = 0; i < boxes; ++i) tc05::tma_pair_2d(b + i * 8192, &map_b, oh + i * 64, c, bar);
+            if (p.pieces_k) {
+              tc05::tma_pair_3d(a, &maps.aw, 0, c, i0 >> 6, bar);
+            } else {
+              tc05::tma_pair_2d(a, &maps.aw, i0, c, bar);
+              tc05::tma_pair_2d(a + 8192, &maps.aw, i0 + 64, c, bar);
+            }
+            if (both) tc05::tma_pair_3d(b, &maps.bw2, 0, c, oh >> 6, bar);
+            else
+              for (int i = 0; i < boxes; ++i) tc05::tma_pair_2d(b + i * 8192, &maps.bw, oh + i * 64, c, bar);
           }
           ++issued;
           if (++s == STAGES) {
@@ -414,19 +442,21 @@ __global__ void __launch_bounds__(Regs<INT8>::THREADS, 1)
       if (rank == 0) {
         uint32_t s = 0, ph = 0, v = 0;
         bool ok = true;
-        constexpr bool A_ROWS = MODE != FORWARD, B_ROWS = MODE == WEIGHTS;
+        constexpr bool A_ROWS = MODE == BACKWARD;
         constexpr int SEG = INT8 ? SEG_INT : SEG_F32;
         constexpr uint32_t TFULL = (2 * STAGES + RING + CODES) * 8;
         const uint32_t bars[2] = {full0, tc05::map_rank(smem_u32(full), 1)};  // of either CTA
         const uint64_t da0 = A_ROWS ? tc05::sw128_rows_desc(base, 8192) : tc05::sw128_desc(base);
-        const uint64_t db0 = B_ROWS ? tc05::sw128_rows_desc(base + A_BYTES, 8192) : tc05::sw128_desc(base + A_BYTES);
+        const uint64_t db_k = tc05::sw128_desc(base + A_BYTES), db_w = tc05::sw128_rows_desc(base + A_BYTES, 8192);
         const uint64_t db8 = tc05::sw128_desc(base + CODES * STAGE);
-        constexpr uint32_t DA = A_ROWS ? 128 : 2, DB = B_ROWS ? 128 : 2;  // 16 of the contracted dimension
+        constexpr uint32_t DA = A_ROWS ? 128 : 2;  // 16 of the contracted dimension
         for (int u = u0; u < n_units && ok; u += ustep) {
           const Unit t = unit_of(u);
           const int steps = steps_of(t);
           const uint32_t idesc = tc05::idesc_f16(256, t.n, INT8 ? 0 : 1) | (A_ROWS ? tc05::A_ROWS_CONTIGUOUS : 0u) |
-                                 (B_ROWS ? tc05::B_ROWS_CONTIGUOUS : 0u);
+                                 (t.weights ? tc05::B_ROWS_CONTIGUOUS : 0u);
+          const uint64_t db0 = t.weights ? db_w : db_k;
+          const uint32_t DB = t.weights ? 128 : 2;
           for (int k = 0; k < steps; ++k) {
             const bool fresh = PROMOTE ? k % SEG == 0 : k == 0;
             const bool last = k == steps - 1 || (PROMOTE && k % SEG == SEG - 1);
@@ -437,7 +467,7 @@ __global__ void __launch_bounds__(Regs<INT8>::THREADS, 1)
             if (!ok) break;
             tc05::fence_after_sync();
             const uint64_t da = da0 + s * (STAGE >> 4), db = db0 + s * (STAGE >> 4);
-            const int parts = MODE == WEIGHTS && k == steps - 1 ? (((t.clen - 1) & 63) >> 4) + 1 : 4;
+            const int parts = t.weights && k == steps - 1 ? (((t.clen - 1) & 63) >> 4) + 1 : 4;
   #pragma unroll
             for (int j = 0; j < 4; ++j) {
               const uint32_t more = !fresh || j > 0 ? 1u : 0u;
@@ -462,15 +492,15 @@ __global__ void __launch_bounds__(Regs<INT8>::THREADS, 1)
         }
       }
     } else if (warp == 10) {
-      // ---------------- WEIGHTS: zeros for the rows of a last step that are not the expert's
-      if (MODE == WEIGHTS) {
+      // ---------------- weights: zeros for the rows of a last step that are not the expert's
+      if (MODE == BACKWARD) {
         uint32_t g = 0, parity = 0;  // steps so far; of `landed`, a bit a stage
         bool ok = true;
         for (int u = u0; u < n_units && ok; u += ustep) {
           const Unit t = unit_of(u);
           const int steps = steps_of(t);
           g += steps;
-          if (!(t.clen & 15)) continue;
+          if (!(t.clen & 15)) continue;  // 0 of what are not weights
           const uint32_t s = (g - 1) % STAGES;
           ok = __all_sync(0xffffffffu, wait(&landed[s], (parity >> s) & 1));
           if (!ok) break;
@@ -550,7 +580,8 @@ __global__ void __launch_bounds__(Regs<INT8>::THREADS, 1)
       }
       // first i of the warp's lanes (gated: of its 16 pairs), and the row of the output that o 0 of the unit is
       const int i0 = GATED ? (t.at * 8 + (int)rank * 4 + quad) * 16 : t.at * 256 + (int)rank * 128 + quad * 32;
-      const size_t row0 = MODE == WEIGHTS ? (size_t)t.e * p.O + t.o0 : (size_t)t.o0;
+      const size_t row0 = t.weights ? (size_t)t.e * p.O + t.o0 : (size_t)t.o0;
+      void* to = t.weights ? p.dw : p.y;
       float sw[4] = {1.f, 1.f, 1.f, 1.f};  // integers: scales of lanes g, g + 8, g + 16, g + 24
       if (INT8) {
         const float* w = p.sw + (size_t)t.e * p.I * (GATED ? 2 : 1);
@@ -629,8 +660,8 @@ __global__ void __launch_bounds__(Regs<INT8>::THREADS, 1)
             return bf16x2_bits(activation(f(0, k, j), p.act) * f(1, k, j),
                                activation(f(0, k, j + 1), p.act) * f(1, k, j + 1));
           });
-        } else if (F32) {
-          float* y = static_cast<float*>(p.y);
+        } else if (F32 && (MODE == FORWARD || t.weights)) {
+          float* y = static_cast<float*>(to);
 #pragma unroll
           for (int k = 0; k < 4; ++k)
 #pragma unroll
@@ -641,7 +672,7 @@ __global__ void __launch_bounds__(Regs<INT8>::THREADS, 1)
                 if (col < left && i < p.I) y[(row + col) * p.I + i] = f(h, k, j);
               }
         } else {
-          uint16_t* y = static_cast<uint16_t*>(p.y);
+          uint16_t* y = static_cast<uint16_t*>(to);
           const uint32_t st = smem_u32(out) + (lane & 7) * 80 + (lane >> 3) * 16;  // row lane % 8 of matrix lane / 8
 #pragma unroll
           for (int k = 0; k < 4; ++k)
@@ -696,8 +727,7 @@ bool encode(CUtensorMap* m, int size, const void* base, std::initializer_list<ui
 }
 
 template <int MODE, bool GATED, bool F32, bool INT8 = false>
-cudaError_t launch(const PairArgs& p, const CUtensorMap& ma, const CUtensorMap& mb, long long most, int sm_count,
-                   cudaStream_t st) {
+cudaError_t launch(const PairArgs& p, const Maps& maps, long long most, int sm_count, cudaStream_t st) {
   const int pairs = sm_count / 2;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(2u * (unsigned)(most < pairs ? most : pairs));
@@ -713,13 +743,65 @@ cudaError_t launch(const PairArgs& p, const CUtensorMap& ma, const CUtensorMap& 
   attr[1].val.clusterDim.z = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 2;
-  return cudaLaunchKernelEx(&cfg, pair_gemm_kernel<MODE, GATED, F32, INT8>, p, ma, mb);
+  return cudaLaunchKernelEx(&cfg, pair_gemm_kernel<MODE, GATED, F32, INT8>, p, maps);
 }
 
 // Tiles of rows that a grouped (or dense) product may have, at most.
 long long row_tiles(int M, int E, bool grouped, int tile) {
   if (!grouped) return (M + tile - 1LL) / tile;
   return (long long)M / tile + (M < E ? M : E);
+}
+
+// A unit takes about so many cycles: its operands' bytes at 64 a cycle, which for 256 columns is the
+// MMAs' time too, and what its start and end leave uncovered.
+long long unit_cycles(long long steps, int n) { return steps * (256 + n) + 1500; }
+
+// Tile of a dense product's rows, so that the units fill the pairs of SMs evenly.
+int choose_tile(int M, long long a_tiles, long long steps, int pairs) {
+  int best = 256;
+  long long least = -1;
+  for (int tile = 256; tile >= 32; tile -= 32) {
+    const long long units = (M + tile - 1LL) / tile * a_tiles;
+    const long long c = (units + pairs - 1) / pairs * unit_cycles(steps, M < tile ? (M + 31) & ~31 : tile);
+    if (least < 0 || c < least) {
+      least = c;
+      best = tile;
+    }
+  }
+  return best;
+}
+
+// The same for both gradients in one launch: units of dx first, then of dw, dealt out in turn.
+void choose_tiles(PairArgs& p, bool dx, bool dw, int pairs) {
+  const long long rows_steps = (p.M + 63) / 64;
+  long long least = -1;
+  int best = 256, best_w = 256;
+  for (int tile = 256; tile >= (dx ? 64 : 256); tile -= 32)
+    for (int tile_w = 256; tile_w >= (dw ? 64 : 256); tile_w -= 32) {
+      const long long a = dx ? (p.M + tile - 1LL) / tile * p.a_tiles : 0, ca = unit_cycles(p.steps, tile);
+      const long long b = dw ? (p.O + tile_w - 1LL) / tile_w * p.a_tiles : 0, cb = unit_cycles(rows_steps, tile_w);
+      const long long edge = a % pairs, end = (a + b) % pairs;  // pairs below an edge have one unit more
+      long long most = 0;
+      for (long long q : {0LL, edge, end}) {
+        if (q >= pairs) continue;
+        const long long na = a / pairs + (q < edge), n = (a + b) / pairs + (q < end);
+        const long long c = na * ca + (n - na) * cb;
+        if (c > most) most = c;
+      }
+      if (least < 0 || most < least) {
+        least = most;
+        best = tile;
+        best_w = tile_w;
+      }
+    }
+  p.tile = best;
+  p.tile_w = best_w;
+}
+
+bool encode_rows(Maps& m, int size, const void* x, uint64_t rows, uint64_t K) {
+  for (uint32_t i = 0; i < 4; ++i)
+    if (!encode(&m.b[i], size, x, {K, rows}, {K}, {128u / size, 16u << i})) return false;
+  return true;
 }
 
 }  // namespace
@@ -738,10 +820,9 @@ cudaError_t pair_gemm_kernels_init() {
     int regs;  // that its shares are counted from
   } k[] = {{reinterpret_cast<const void*>(pair_gemm_kernel<FORWARD, true, false, false>), 0},
            {reinterpret_cast<const void*>(pair_gemm_kernel<FORWARD, false, false, false>), 0},
-           {reinterpret_cast<const void*>(pair_gemm_kernel<INPUT, false, false, false>), 0},
-           {reinterpret_cast<const void*>(pair_gemm_kernel<WEIGHTS, false, false, false>), 0},
+           {reinterpret_cast<const void*>(pair_gemm_kernel<BACKWARD, false, false, false>), 0},
            {reinterpret_cast<const void*>(pair_gemm_kernel<FORWARD, false, true, false>), Regs<false>::LAUNCH},
-           {reinterpret_cast<const void*>(pair_gemm_kernel<WEIGHTS, false, true, false>), Regs<false>::LAUNCH},
+           {reinterpret_cast<const void*>(pair_gemm_kernel<BACKWARD, false, true, false>), Regs<false>::LAUNCH},
            {reinterpret_cast<const void*>(pair_gemm_kernel<FORWARD, false, false, true>), Regs<true>::LAUNCH},
            {reinterpret_cast<const void*>(pair_gemm_kernel<FORWARD, false, true, true>), Regs<true>::LAUNCH},
            {reinterpret_cast<const void*>(pair_gemm_kernel<FORWARD, true, false, true>), Regs<true>::LAUNCH},
@@ -763,78 +844,70 @@ cudaError_t launch_pair_forward(const ProductArgs& a, bool int8, int sm_count, u
   p.offsets = a.offsets;
   p.y = a.y;
   p.keep = static_cast<uint16_t*>(a.keep);
+  p.sx = a.sx;
+  p.sw = a.sw;
   p.err = err;
   p.M = a.M;
   p.E = a.E;
   p.I = gated ? a.N / 2 : a.N;
   p.steps = (a.K + 63) / 64;
   p.a_tiles = (a.N + 255) / 256;
-  p.tile = 256;
-  p.box = 32;
+  p.tile = a.offsets == nullptr ? choose_tile(a.M, p.a_tiles, p.steps, sm_count / 2) : 256;
   p.band = 8;
   p.act = a.act;
-  p.sx = a.sx;
-  p.sw = a.sw;
-  CUtensorMap ma, mb;
+  Maps m;
   const int size = int8 ? 1 : 2;
   const uint32_t inner = 128 / size;
   const bool ok =
-      gated ? encode(&ma, size, a.w, {K, 16, 2, N / 32, E}, {K, N / 2 * K, 16 * K, N * K}, {inner, 16, 2, 4, 1})
-            : encode(&ma, size, a.w, {K, N, E}, {K, N * K}, {inner, 128, 1});
-  if (!ok || !encode(&mb, size, a.x, {K, M}, {K}, {inner, (uint32_t)p.box})) return cudaErrorInvalidValue;
+      gated ? encode(&m.a, size, a.w, {K, 16, 2, N / 32, E}, {K, N / 2 * K, 16 * K, N * K}, {inner, 16, 2, 4, 1})
+            : encode(&m.a, size, a.w, {K, N, E}, {K, N * K}, {inner, 128, 1});
+  if (!ok || !encode_rows(m, size, a.x, M, K)) return cudaErrorInvalidValue;
+  m.aw = m.bw = m.bw2 = m.a;
   const long long most = row_tiles(a.M, a.E, a.offsets != nullptr, p.tile) * p.a_tiles;
   if (int8) {
-    if (gated) return a.f32 ? launch<FORWARD, true, true, true>(p, ma, mb, most, sm_count, st)
-                            : launch<FORWARD, true, false, true>(p, ma, mb, most, sm_count, st);
-    return a.f32 ? launch<FORWARD, false, true, true>(p, ma, mb, most, sm_count, st)
-                 : launch<FORWARD, false, false, true>(p, ma, mb, most, sm_count, st);
+    if (gated) return a.f32 ? launch<FORWARD, true, true, true>(p, m, most, sm_count, st)
+                            : launch<FORWARD, true, false, true>(p, m, most, sm_count, st);
+    return a.f32 ? launch<FORWARD, false, true, true>(p, m, most, sm_count, st)
+                 : launch<FORWARD, false, false, true>(p, m, most, sm_count, st);
   }
-  if (gated) return launch<FORWARD, true, false>(p, ma, mb, most, sm_count, st);
-  return a.f32 ? launch<FORWARD, false, true>(p, ma, mb, most, sm_count, st)
-               : launch<FORWARD, false, false>(p, ma, mb, most, sm_count, st);
+  if (gated) return launch<FORWARD, true, false>(p, m, most, sm_count, st);
+  return a.f32 ? launch<FORWARD, false, true>(p, m, most, sm_count, st)
+               : launch<FORWARD, false, false>(p, m, most, sm_count, st);
 }
 
-cudaError_t launch_pair_input(const GradArgs& a, int sm_count, unsigned* err, cudaStream_t st) {
+cudaError_t launch_pair_backward(const GradArgs& a, int sm_count, unsigned* err, cudaStream_t st) {
   const uint64_t M = a.M, N = a.N, K = a.K, E = a.E;
   PairArgs p = {};
   p.offsets = a.offsets;
-  p.y = a.out;
-  p.err = err;
-  p.M = a.M;
-  p.E = a.E;
-  p.I = a.K;
-  p.steps = (a.N + 63) / 64;
-  p.a_tiles = (a.K + 255) / 256;
-  p.tile = 256;
-  p.box = 32;
-  p.band = 8;
-  CUtensorMap ma, mb;
-  if (!encode(&ma, 2, a.other, {K, N, E}, {K, N * K}, {64, 64, 1}) || !encode(&mb, 2, a.dy, {N, M}, {N}, {64, (uint32_t)p.box}))
-    return cudaErrorInvalidValue;
-  return launch<INPUT, false, false>(p, ma, mb, row_tiles(a.M, a.E, a.offsets != nullptr, p.tile) * p.a_tiles, sm_count, st);
-}
-
-cudaError_t launch_pair_weights(const GradArgs& a, int sm_count, unsigned* err, cudaStream_t st) {
-  const uint64_t M = a.M, N = a.N, K = a.K;
-  PairArgs p = {};
-  p.offsets = a.offsets;
-  p.y = a.out;
+  p.y = a.dx;
+  p.dw = a.dw;
   p.err = err;
   p.M = a.M;
   p.E = a.E;
   p.I = a.K;
   p.O = a.N;
+  p.steps = (a.N + 63) / 64;
   p.a_tiles = (a.K + 255) / 256;
-  p.tile = 256;
-  p.o_tiles = (a.N + p.tile - 1) / p.tile;
-  p.box = 64;
+  p.tile = p.tile_w = 256;
   p.band = 8;
-  CUtensorMap ma, mb;
-  if (!encode(&ma, 2, a.other, {K, M}, {K}, {64, 64}) || !encode(&mb, 2, a.dy, {N, M}, {N}, {64, 64}))
-    return cudaErrorInvalidValue;
-  const long long most = (long long)a.E * p.a_tiles * p.o_tiles;
-  return a.f32 ? launch<WEIGHTS, false, true>(p, ma, mb, most, sm_count, st)
-               : launch<WEIGHTS, false, false>(p, ma, mb, most, sm_count, st);
+  p.pieces_k = a.K % 64 == 0;
+  p.pieces_n = a.N % 64 == 0;
+  if (a.offsets == nullptr) choose_tiles(p, a.dx != nullptr, a.dw != nullptr, sm_count / 2);
+  if (a.dw != nullptr) p.o_tiles = (a.N + p.tile_w - 1) / p.tile_w;
+  Maps m;
+  bool ok = encode_rows(m, 2, a.dy, M, N);
+  ok = ok && (p.pieces_k ? encode(&m.a, 2, a.w, {64, N, K / 64, E}, {K, 64, N * K}, {64, 64, 2, 1})
+                         : encode(&m.a, 2, a.w, {K, N, E}, {K, N * K}, {64, 64, 1}));
+  ok = ok && (p.pieces_k ? encode(&m.aw, 2, a.x, {64, M, K / 64}, {K, 64}, {64, 64, 2})
+                         : encode(&m.aw, 2, a.x, {K, M}, {K}, {64, 64}));
+  ok = ok && encode(&m.bw, 2, a.dy, {N, M}, {N}, {64, 64});
+  m.bw2 = m.bw;
+  if (p.pieces_n) ok = ok && encode(&m.bw2, 2, a.dy, {64, M, N / 64}, {N, 64}, {64, 64, 2});
+  if (!ok) return cudaErrorInvalidValue;
+  long long most = (long long)a.E * p.o_tiles * p.a_tiles;
+  if (a.dx != nullptr) most += row_tiles(a.M, a.E, a.offsets != nullptr, p.tile) * p.a_tiles;
+  return a.f32 ? launch<BACKWARD, false, true>(p, m, most, sm_count, st)
+               : launch<BACKWARD, false, false>(p, m, most, sm_count, st);
 }
 
 }  // namespace flint
