@@ -1,7 +1,7 @@
 // Products on the tensor cores (tcgen05 over pairs of CTAs), dense or grouped by expert:
 // linear and gated products in bf16 and their gradients, and 8-bit integer products.
 //
-// Three products in one kernel (both gradients in one launch, an expert's after one another).  The M
+// Three products in one kernel (both gradients in one launch, the weights' behind).  The M
 // side of the MMA is the dimension that lies contiguous in the output (i), always 256 of it a
 // unit; the N side (o), up to 256 in steps of 32, is what is ragged:
 //   forward  y[m][n]     i = n: weights by rows       o = m: rows of x       sum over k
@@ -84,13 +84,28 @@ struct PairArgs {
   int O;          // backward: N, rows of an expert's dw
   int steps;      // forward, input: steps of 64 of the contracted dimension
   int a_tiles;    // units side by side in i
-  int tile;       // forward, input: o's of a unit, at most (a multiple of 32)
-  int tile_w;     // weights: the same
+  int tile;       // forward, input: o's of a unit, at most (a multiple of 32); grouped: 256
+  int row_tiles;  // dense: units side by side in o
+  int tile_w;     // weights: o's of a unit, at most
   int o_tiles;    // weights: units side by side in o, 0: not wanted
-  int band;       // tiles of o that go side by side
+  unsigned per_band, per_expert;  // reciprocals of BAND * a_tiles and of o_tiles * a_tiles
   int act;
   bool pieces_k, pieces_n;  // K, N are multiples of 64: two pieces of 64 make one copy
 };
+
+// Tiles of o that go side by side, with all of i: what runs at a time shares both operands.
+constexpr int BAND = 8;
+// x / n for x below 9,000 is x * SMALL[n] >> 16.
+__constant__ unsigned SMALL[BAND + 1] = {0,         65536,         65536 / 2 + 1, 65536 / 3 + 1, 65536 / 4 + 1,
+                                         65536 / 5 + 1, 65536 / 6 + 1, 65536 / 7 + 1, 65536 / 8 + 1};
+static_assert(BAND * ((1 << 17) / 256) < 9000, "a band's units");
+// x / n from n's reciprocal, 2^32 / n rounded up (0 for n = 1): too large by one at most.
+__device__ __forceinline__ int quotient(int x, unsigned recip, int n) {
+  if (n == 1) return x;
+  const int q = (int)__umulhi((unsigned)x, recip);
+  return q * n > x ? q - 1 : q;
+}
+unsigned reciprocal(int n) { return 0xFFFFFFFFu / (unsigned)n + 1u; }
 
 // Boxes of operands in shared memory: rows of 128 bytes.
 struct Maps {
@@ -152,7 +167,7 @@ __global__ void __launch_bounds__(Regs<INT8>::THREADS, 1)
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tslot + 1);
   int* g_units = reinterpret_cast<int*>(sm + OFF_GROUPS);  // [E + 1] units before each group
   int* g_lo = g_units + p.E + 1;                           // [E] first row
-  int* g_cnt = g_lo + p.E;                                 // [E] rows
+  int* g_cnt = g_lo + p.E;                                 // [E] rows, and from bit 26 a tile's rows / 32
 
   if (tid == 0) {
     for (int i = 0; i < STAGES; ++i) {
@@ -187,12 +202,13 @@ __global__ void __launch_bounds__(Regs<INT8>::THREADS, 1)
       if (e < p.E) {
         lo = p.offsets ? min(max(g_units[e], 0), p.M) : 0;
         cnt = p.offsets ? min(max(g_units[e + 1], lo), p.M) - lo : p.M;
+        // a group's tiles are of one size, to 32 rows
+        const int tiles = (cnt + p.tile - 1) / p.tile;
         g_lo[e] = lo;
-        g_cnt[e] = cnt;
+        g_cnt[e] = cnt | (cnt > 0 ? ((cnt + tiles - 1) / tiles + 31) >> 5 : 0) << 26;
       }
       __syncwarp();  // the offsets of these groups make room for their units; the next group's first is read below
       int t = MODE == BACKWARD && p.y == nullptr ? 0 : (cnt + p.tile - 1) / p.tile;
-      if (MODE == BACKWARD && e < p.E) t += p.o_tiles;
       t *= p.a_tiles;
       if (base > 1 << 29) t = 0;  // offsets that descend could count rows over and over: stay inside int
       int incl = t;
@@ -211,36 +227,45 @@ __global__ void __launch_bounds__(Regs<INT8>::THREADS, 1)
   tc05::cluster_sync();  // both CTAs' barriers are ready
   tc05::fence_after_sync();
   const uint32_t tmem = *tslot;
-  const int n_units = g_units[p.E];
+  const int n_rows_units = g_units[p.E];  // forward, input; behind them the weights'
+  const int n_units = n_rows_units + (MODE == BACKWARD ? p.E * p.o_tiles * p.a_tiles : 0);
   const int u0 = blockIdx.x >> 1, ustep = gridDim.x >> 1;
 
+  // Few divisions: every role looks its units up, and a weights' unit may be three steps long.
   auto unit_of = [&](int u) -> Unit {
-    // The group is the last whose first unit is at or before u: the whole warp looks, at
-    // every 32nd group and then at 32 neighbours.
     Unit t;
-    int from = 0;
-    if (p.E > 32) from = 32 * (__popc(__ballot_sync(0xffffffffu, 32 * lane < p.E && g_units[32 * lane] <= u)) - 1);
-    const int e = from + lane;
-    t.e = from + __popc(__ballot_sync(0xffffffffu, e < p.E && g_units[e] <= u)) - 1;
-    const int rows = g_cnt[t.e];
-    int v = u - g_units[t.e], tiles = MODE == BACKWARD && p.y == nullptr ? 0 : (rows + p.tile - 1) / p.tile;
-    t.weights = MODE == BACKWARD && v >= tiles * p.a_tiles;
+    int v, tiles;
+    t.weights = MODE == BACKWARD && u >= n_rows_units;
+    t.e = 0;
     if (t.weights) {
-      v -= tiles * p.a_tiles;
+      const int per = p.o_tiles * p.a_tiles;
+      t.e = quotient(u - n_rows_units, p.per_expert, per);
+      v = u - n_rows_units - t.e * per;
       tiles = p.o_tiles;
+    } else {
+      // The group is the last whose first unit is at or before u: the whole warp looks, at
+      // every 32nd group and then at 32 neighbours.
+      if (p.E > 1) {
+        int from = 0;
+        if (p.E > 32) from = 32 * (__popc(__ballot_sync(0xffffffffu, 32 * lane < p.E && g_units[32 * lane] <= u)) - 1);
+        const int e = from + lane;
+        t.e = from + __popc(__ballot_sync(0xffffffffu, e < p.E && g_units[e] <= u)) - 1;
+      }
+      v = u - g_units[t.e];
     }
-    // bands of neighbouring tiles of o, all of i within a band: what runs at a time shares both operands
-    const int per = p.band * p.a_tiles, first = v / per * p.band, rest = v - v / per * per;
-    const int high = min(p.band, tiles - first);
-    t.at = rest / high;
-    const int tile = first + rest - t.at * high;
+    const int g = g_cnt[t.e], rows = g & ((1 << 26) - 1);
+    if (!t.weights) tiles = p.offsets != nullptr ? (rows + 255) >> 8 : p.row_tiles;
+    const int per = BAND * p.a_tiles, band = quotient(v, p.per_band, per), rest = v - band * per;
+    const int high = min(BAND, tiles - band * BAND);
+    t.at = (int)((unsigned)rest * SMALL[high] >> 16);
+    const int tile = band * BAND + rest - t.at * high;
     if (t.weights) {
       t.o0 = tile * p.tile_w;
       t.cnt = min(p.tile_w, p.O - t.o0);
       t.c0 = g_lo[t.e];
       t.clen = rows;
     } else {
-      const int size = ((rows + tiles - 1) / tiles + 31) & ~31;  // a group's tiles are of one size, to 32 rows
+      const int size = g >> 26 << 5;
       t.o0 = g_lo[t.e] + tile * size;
       t.cnt = max(0, min(size, rows - tile * size));
       t.c0 = t.clen = 0;
@@ -685,9 +710,12 @@ __global__ void __launch_bounds__(Regs<INT8>::THREADS, 1)
 #pragma unroll
           for (int k = 0; k < 4; ++k) {
             const int col = 8 * k + (lane >> 2);
-            if (col < left && i < p.I)  // the width is a multiple of 8
-              *reinterpret_cast<uint4*>(y + (row + col) * p.I + i) =
-                  *reinterpret_cast<const uint4*>(out + col * 80 + (lane & 3) * 16);
+            if (col < left && i < p.I) {  // the width is a multiple of 8
+              uint4* dst = reinterpret_cast<uint4*>(y + (row + col) * p.I + i);
+              const uint4 x = *reinterpret_cast<const uint4*>(out + col * 80 + (lane & 3) * 16);
+              if (t.weights) __stcs(dst, x);  // read again by no kernel soon: operands stay in L2
+              else *dst = x;
+            }
           }
           __syncwarp();
         }
@@ -853,8 +881,9 @@ cudaError_t launch_pair_forward(const ProductArgs& a, bool int8, int sm_count, u
   p.steps = (a.K + 63) / 64;
   p.a_tiles = (a.N + 255) / 256;
   p.tile = a.offsets == nullptr ? choose_tile(a.M, p.a_tiles, p.steps, sm_count / 2) : 256;
-  p.band = 8;
   p.act = a.act;
+  p.row_tiles = (a.M + p.tile - 1) / p.tile;
+  p.per_band = reciprocal(BAND * p.a_tiles);
   Maps m;
   const int size = int8 ? 1 : 2;
   const uint32_t inner = 128 / size;
@@ -889,11 +918,13 @@ cudaError_t launch_pair_backward(const GradArgs& a, int sm_count, unsigned* err,
   p.steps = (a.N + 63) / 64;
   p.a_tiles = (a.K + 255) / 256;
   p.tile = p.tile_w = 256;
-  p.band = 8;
   p.pieces_k = a.K % 64 == 0;
   p.pieces_n = a.N % 64 == 0;
   if (a.offsets == nullptr) choose_tiles(p, a.dx != nullptr, a.dw != nullptr, sm_count / 2);
   if (a.dw != nullptr) p.o_tiles = (a.N + p.tile_w - 1) / p.tile_w;
+  p.row_tiles = (a.M + p.tile - 1) / p.tile;
+  p.per_band = reciprocal(BAND * p.a_tiles);
+  p.per_expert = reciprocal(a.dw != nullptr ? p.o_tiles * p.a_tiles : 1);
   Maps m;
   bool ok = encode_rows(m, 2, a.dy, M, N);
   ok = ok && (p.pieces_k ? encode(&m.a, 2, a.w, {64, N, K / 64, E}, {K, 64, N * K}, {64, 64, 2, 1})
