@@ -8,9 +8,11 @@
 // partner's too.  Both operands are read straight from global memory into fragments:
 // a sum does not depend on the order of k, so lane t of a row's four takes bytes
 // 16 t .. 16 t + 15 of each 64 for either operand (8 bf16 or 16 integers: two mma).
-// Two pieces of 128 bytes a row (4 KB of weights a warp) are under way at a time.
+// DEEP pieces of 128 bytes a row (2 KB of weights a warp each) are under way at a time.
 // Every SPLIT-th piece of K is a warp's; SPLIT warps of a CTA share their rows and add
-// their sums in the warps' order, so that a small product has enough warps.
+// their sums in the warps' order, so that a small product has enough warps.  A dense
+// product asks for its first weights before it waits for the kernel before it: into L2
+// alone, where a write of that kernel would still reach them.
 //
 // Grid (M, weight rows / rows of a CTA): the CTA of row r works when r is the first of a
 // run of 8 rows of its expert; a dense product has CTAs for every eighth row alone.
@@ -44,15 +46,29 @@ struct Sum<true> {
   using type = int;
 };
 
-template <bool INT8, bool GATED, int SPLIT, int WARPS>
-__global__ void __launch_bounds__(WARPS * 32, 24 / WARPS) few_rows_kernel(const ProductArgs p) {
+template <bool INT8, bool GATED, int SPLIT, int WARPS, int DEEP>
+__global__ void __launch_bounds__(WARPS * 32, (DEEP > 2 ? 16 : 24) / WARPS) few_rows_kernel(const ProductArgs p) {
   using S = typename Sum<INT8>::type;
   constexpr int SIZE = INT8 ? 1 : 2;
   __shared__ S red[SPLIT == 1 ? 1 : WARPS][128];
   __shared__ int range[3];
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int outs = GATED ? p.N / 2 : p.N;          // outputs of a row
+  constexpr int STEP = GATED ? 8 : 16;             // of them, a warp's
+  const int tile = blockIdx.y * (WARPS / SPLIT) + warp / SPLIT, n0 = tile * STEP;
+  const int g = lane >> 2, t = lane & 3;
+  const size_t kbytes = (size_t)p.K * SIZE;
+  const int pieces = (int)((kbytes + 127) / 128);
+  if (p.offsets == nullptr && n0 < outs) {
+    const uint8_t* w = static_cast<const uint8_t*>(p.w);
+    for (int i = t; i < 2 * DEEP; i += 4) {  // lanes t of a row: its two halves of 16 and the pieces
+      const int row = i & 1 ? (GATED ? outs + n0 + g : min(n0 + g + 8, p.N - 1)) : n0 + g;
+      const int piece = warp % SPLIT + (i >> 1) * SPLIT;
+      if (piece < pieces) prefetch_l2(w + (size_t)row * kbytes + (size_t)piece * 128);
+    }
+  }
   pdl_wait();
   pdl_trigger();
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int r = p.offsets == nullptr ? blockIdx.x * 8 : blockIdx.x;
   int e = 0, r0 = 0, r1 = p.M;
   if (p.offsets != nullptr) {
@@ -73,19 +89,13 @@ __global__ void __launch_bounds__(WARPS * 32, 24 / WARPS) few_rows_kernel(const 
   }
   if ((r - r0) & 7) return;
   const int n_rows = min(8, r1 - r);
-  const int outs = GATED ? p.N / 2 : p.N;          // outputs of a row
-  constexpr int STEP = GATED ? 8 : 16;             // of them, a warp's
-  const int tile = blockIdx.y * (WARPS / SPLIT) + warp / SPLIT, n0 = tile * STEP;
-  const int g = lane >> 2, t = lane & 3;
-  const size_t kbytes = (size_t)p.K * SIZE;
   S acc[4] = {0, 0, 0, 0};
   if (n0 < outs) {  // outs is a multiple of 8
     const uint8_t* w = static_cast<const uint8_t*>(p.w) + (size_t)e * p.N * kbytes;
     const uint8_t* b0 = w + (size_t)(n0 + g) * kbytes;
     const uint8_t* b1 = w + (size_t)(GATED ? outs + n0 + g : min(n0 + g + 8, p.N - 1)) * kbytes;
     const uint8_t* a0 = static_cast<const uint8_t*>(p.x) + (size_t)(r + min(g, n_rows - 1)) * kbytes;
-    constexpr int U = 2;
-    const int pieces = (int)((kbytes + 127) / 128);
+    constexpr int U = DEEP;
     for (int q0 = warp % SPLIT; q0 < pieces; q0 += U * SPLIT) {
       uint4 v[U][4], x[U][2];
 #pragma unroll
@@ -157,7 +167,7 @@ __global__ void __launch_bounds__(WARPS * 32, 24 / WARPS) few_rows_kernel(const 
   }
 }
 
-template <bool INT8, bool GATED, int SPLIT, int WARPS>
+template <bool INT8, bool GATED, int SPLIT, int WARPS, int DEEP>
 cudaError_t launch(const ProductArgs& p, cudaStream_t st) {
   constexpr int ROWS = WARPS / SPLIT * (GATED ? 8 : 16);
   const int outs = GATED ? p.N / 2 : p.N;
@@ -170,18 +180,32 @@ cudaError_t launch(const ProductArgs& p, cudaStream_t st) {
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, few_rows_kernel<INT8, GATED, SPLIT, WARPS>, p);
+  return cudaLaunchKernelEx(&cfg, few_rows_kernel<INT8, GATED, SPLIT, WARPS, DEEP>, p);
 }
 
-template <bool INT8>
-cudaError_t launch_type(const ProductArgs& p, cudaStream_t st) {
-  return p.act != FFN_NONE ? launch<INT8, true, 8, 8>(p, st) : launch<INT8, false, 8, 8>(p, st);
+// Warps that share K and pieces under way, measured (us; calls in a graph, weights from HBM; the
+// second digits are the next best).  256 experts of 1024 x 2048, and dense N x K:
+//   up to 16 rows by expert   8 of 8, 2    bf16 6 rows 6.5 (4 of 4: 7.2)
+//   up to 128                 4 of 4, 2    integers 48 rows 19.2 (8 of 8: 21.9), bf16 96 rows 54.7 (55.7)
+//   more                      1 of 4, 4    integers 384 rows 67.0 (4 of 4: 70.1), bf16 123.0 (126.3), floors 60 and 125
+//   dense, a warp's share of  8 of 8, 4    bf16 4 x 2048 x 8192 8.8 (2 pieces: 9.8), 1 x 2048 x 2048 3.3 (3.6)
+//     K is 4 pieces and more
+//   dense, less               8 of 8, 2    integers 8 x 8192 x 2048 5.5 (4 pieces: 7.5)
+template <bool INT8, bool GATED>
+cudaError_t launch_shape(const ProductArgs& p, cudaStream_t st) {
+  if (p.offsets == nullptr)
+    return (long long)p.K * (INT8 ? 1 : 2) >= 8 * 4 * 128 ? launch<INT8, GATED, 8, 8, 4>(p, st)
+                                                           : launch<INT8, GATED, 8, 8, 2>(p, st);
+  if (p.M <= 16) return launch<INT8, GATED, 8, 8, 2>(p, st);
+  if (p.M <= 128) return launch<INT8, GATED, 4, 4, 2>(p, st);
+  return launch<INT8, GATED, 1, 4, 4>(p, st);
 }
 
 }  // namespace
 
 cudaError_t launch_few_rows(const ProductArgs& p, bool int8, cudaStream_t st) {
-  return int8 ? launch_type<true>(p, st) : launch_type<false>(p, st);
+  if (int8) return p.act != FFN_NONE ? launch_shape<true, true>(p, st) : launch_shape<true, false>(p, st);
+  return p.act != FFN_NONE ? launch_shape<false, true>(p, st) : launch_shape<false, false>(p, st);
 }
 
 }  // namespace flint

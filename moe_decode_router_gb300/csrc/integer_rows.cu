@@ -73,9 +73,8 @@ __device__ __forceinline__ uint32_t code(float v, float s, float inv) {
 // the whole number next to x / scale.  THREADS lanes of a CTA of 256 have a row: each 16 neighbouring
 // values at a time, the first HELD x 16 of them kept in registers between the two passes
 // (a longer row is read a second time).  Bound by HBM.
-template <bool BF16, int THREADS>
-__global__ void __launch_bounds__(256) integer_rows_kernel(const IntRowsArgs p) {
-  constexpr int HELD = 4;
+template <bool BF16, int THREADS, int HELD>
+__global__ void __launch_bounds__(256, 3) integer_rows_kernel(const IntRowsArgs p) {
   __shared__ float tops[8];
   pdl_wait();
   pdl_trigger();
@@ -83,6 +82,11 @@ __global__ void __launch_bounds__(256) integer_rows_kernel(const IntRowsArgs p) 
   const int row = blockIdx.x * (256 / THREADS) + threadIdx.x / THREADS;
   const bool in = row < p.rows;
   const size_t base = (size_t)row * (size_t)p.stride;
+  constexpr int AT_ONCE = 8;
+  int to[AT_ONCE];  // the first places, on their way while the row is
+  const int32_t* pos = p.pos + (size_t)row * p.top_k;
+#pragma unroll
+  for (int j = 0; j < AT_ONCE; ++j) to[j] = in && p.pos != nullptr && j < p.top_k ? __ldg(pos + j) : -1;
   Raw16<BF16> held[HELD];
 #pragma unroll
   for (int i = 0; i < HELD; ++i) {
@@ -112,7 +116,6 @@ __global__ void __launch_bounds__(256) integer_rows_kernel(const IntRowsArgs p) 
   if (a < ROW_FLOOR) a = ROW_FLOOR;  // false for NaN
   const float scale = __fmul_rn(a, 1.f / 127.f), inv = __frcp_rn(scale);
   const bool fine = scale < INFINITY;  // false for NaN: the codes of such a row are 0
-  const int32_t* pos = p.pos + (size_t)row * p.top_k;
   auto put = [&](const Raw16<BF16>& v, int k) {
     uint32_t c[4];
 #pragma unroll
@@ -126,10 +129,12 @@ __global__ void __launch_bounds__(256) integer_rows_kernel(const IntRowsArgs p) 
       *reinterpret_cast<uint4*>(p.q + (size_t)row * p.K + k) = codes;
       return;
     }
-    for (int j = 0; j < p.top_k; ++j) {
-      const int place = __ldg(pos + j);
+    auto store = [&](int place) {
       if (place >= 0 && place < p.places) *reinterpret_cast<uint4*>(p.q + (size_t)place * p.K + k) = codes;
-    }
+    };
+#pragma unroll
+    for (int j = 0; j < AT_ONCE; ++j) store(to[j]);
+    for (int j = AT_ONCE; j < p.top_k; ++j) store(__ldg(pos + j));
   };
 #pragma unroll
   for (int i = 0; i < HELD; ++i) {
@@ -149,7 +154,7 @@ __global__ void __launch_bounds__(256) integer_rows_kernel(const IntRowsArgs p) 
   }
 }
 
-template <bool BF16, int THREADS>
+template <bool BF16, int THREADS, int HELD>
 cudaError_t launch(const IntRowsArgs& p, cudaStream_t st) {
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)((p.rows + 256 / THREADS - 1) / (256 / THREADS)));
@@ -160,7 +165,7 @@ cudaError_t launch(const IntRowsArgs& p, cudaStream_t st) {
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, integer_rows_kernel<BF16, THREADS>, p);
+  return cudaLaunchKernelEx(&cfg, integer_rows_kernel<BF16, THREADS, HELD>, p);
 }
 
 }  // namespace
@@ -177,8 +182,10 @@ cudaError_t launch_integer_rows(const void* x, bool bf16, long long stride, int 
   p.places = places;
   p.q = static_cast<uint8_t*>(q);
   p.scales = scales;
-  if (K <= 2048) return bf16 ? launch<true, 32>(p, st) : launch<false, 32>(p, st);
-  return bf16 ? launch<true, 256>(p, st) : launch<false, 256>(p, st);
+  // few rows: more threads for each, or most SMs idle
+  if (K <= 2048 && rows <= 1024) return bf16 ? launch<true, 128, 1>(p, st) : launch<false, 128, 1>(p, st);
+  if (K <= 2048) return bf16 ? launch<true, 32, 4>(p, st) : launch<false, 32, 4>(p, st);
+  return bf16 ? launch<true, 256, 4>(p, st) : launch<false, 256, 4>(p, st);
 }
 
 }  // namespace flint

@@ -50,13 +50,13 @@ enum { FORWARD, BACKWARD };
 
 constexpr int A_BYTES = 128 * 128, B_BYTES = 128 * 128, STAGE = A_BYTES + B_BYTES;
 constexpr int RING = 6;            // stages of operands
-constexpr int CODES = 4;           // integers: stages of codes, 128 of K each, then
-constexpr int TURNED = 4;          //   stages of one operand in fp16, and as many in tensor memory behind the sums
-static_assert(CODES * STAGE + TURNED * B_BYTES <= RING * STAGE, "rings");
+constexpr int CODES = 3;           // integers: stages of codes, 128 of K each, then
+constexpr int TURNED = 3;          //   stages of one operand in fp16, and as many in tensor memory behind the sums
+static_assert(CODES * STAGE + TURNED * 2 * B_BYTES <= RING * STAGE && 256 + TURNED * 64 <= 512, "rings");
 constexpr int OUT_WARP = 32 * 80;  // output staging of a warp: 32 rows of 64 bytes, 80 apart
 constexpr int OFF_OUT = RING * STAGE;
 constexpr int OFF_BARS = OFF_OUT + 8 * OUT_WARP;
-constexpr int SEG_F32 = 8, SEG_INT = 16;  // steps of 64 between promotions
+constexpr int SEG_F32 = 8, SEG_INT = 8;  // steps (of 64; integers: of 128) between promotions
 
 // Registers a thread: the output warps of a promoting kernel hold 128 sums each and take what
 // the others give up; a block is launched with LAUNCH of them.
@@ -82,7 +82,7 @@ struct PairArgs {
   int M, E;
   int I;          // width of the outputs (i)
   int O;          // backward: N, rows of an expert's dw
-  int steps;      // forward, input: steps of 64 of the contracted dimension
+  int steps;      // forward, input: steps of 64 of the contracted dimension (integers: of 128)
   int a_tiles;    // units side by side in i
   int tile;       // forward, input: o's of a unit, at most (a multiple of 32); grouped: 256
   int row_tiles;  // dense: units side by side in o
@@ -297,7 +297,7 @@ __global__ void __launch_bounds__(Regs<INT8>::THREADS, 1)
         const Unit t = unit_of(u);
         const int nh = t.n >> 1, oh = t.o0 + (int)rank * nh, sel = box_of(nh);
         const uint32_t bytes = A_BYTES + (2048u << sel);
-        for (int k = 0; k < (p.steps + 1) >> 1 && lane == 0; ++k) {
+        for (int k = 0; k < p.steps && lane == 0; ++k) {
           if (!wait(&taken[r], ph ^ 1)) {
             ok = false;
             break;
@@ -325,7 +325,7 @@ __global__ void __launch_bounds__(Regs<INT8>::THREADS, 1)
         }
       }
     } else if (INT8 && warp >= 12) {
-      // ---------------- codes to fp16, 64 of K at a time
+      // ---------------- codes to fp16, 128 of K at a time
       uint32_t s = 0, ph = 0, r = 0, rph = 0;
       bool ok = true;
       // Warps 12-15, the weights: a lane has a row, that of its lane of tensor memory (the
@@ -341,40 +341,47 @@ __global__ void __launch_bounds__(Regs<INT8>::THREADS, 1)
         const Unit t = unit_of(u);
         const int atoms = t.n >> 4;
         for (int k = 0; k < p.steps; ++k) {
-          if ((k & 1) == 0) ok = __all_sync(0xffffffffu, wait(&landed[r], rph));
-          ok = ok && __all_sync(0xffffffffu, wait(&empty[s], ph ^ 1));
+          ok = __all_sync(0xffffffffu, wait(&landed[r], rph)) && __all_sync(0xffffffffu, wait(&empty[s], ph ^ 1));
           if (!ok) break;
           const uint8_t* from = sm + r * STAGE;
           if (warp < 16) {
             tc05::fence_after_sync();
             const uint8_t* at = from + arow * 128;
 #pragma unroll
-            for (int h = 0; h < 2; ++h) {
-              const uint4 c0 = *reinterpret_cast<const uint4*>(at + ((((k & 1) * 4 + 2 * h) ^ (arow & 7)) << 4));
-              const uint4 c1 = *reinterpret_cast<const uint4*>(at + ((((k & 1) * 4 + 2 * h + 1) ^ (arow & 7)) << 4));
+            for (int h = 0; h < 4; ++h) {
+              const uint4 c0 = *reinterpret_cast<const uint4*>(at + (((2 * h) ^ (arow & 7)) << 4));
+              const uint4 c1 = *reinterpret_cast<const uint4*>(at + (((2 * h + 1) ^ (arow & 7)) << 4));
               uint4 v[4];
               codes_to_f16(c0, v[0], v[1]);
               codes_to_f16(c1, v[2], v[3]);
-              tc05::st_32x32b_x16(a_to + s * 32 + h * 16, v);
+              tc05::st_32x32b_x16(a_to + s * 64 + h * 16, v);
             }
+          } else {
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+              const uint8_t* at = from + A_BYTES + row * 128 + (((h * 4 + q) ^ row) << 4);
+              uint8_t* to = sm + CODES * STAGE + (2 * s + h) * B_BYTES + row * 128;
+              uint4 c[4];
+#pragma unroll
+              for (int i = 0; i < 4; ++i)
+                if (warp - 16 + 4 * i < atoms) c[i] = *reinterpret_cast<const uint4*>(at + (warp - 16 + 4 * i) * 1024);
+#pragma unroll
+              for (int i = 0; i < 4; ++i)
+                if (warp - 16 + 4 * i < atoms) {
+                  uint4 v0, v1;
+                  codes_to_f16(c[i], v0, v1);
+                  uint8_t* d = to + (warp - 16 + 4 * i) * 1024;
+                  *reinterpret_cast<uint4*>(d + lo) = v0;
+                  *reinterpret_cast<uint4*>(d + hi) = v1;
+                }
+            }
+          }
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&taken[r]);  // the codes are in registers or beyond
+          if (warp < 16) {
             tc05::wait_st();
             tc05::fence_before_sync();
           } else {
-            const uint8_t* at = from + A_BYTES + row * 128 + ((((k & 1) * 4 + q) ^ row) << 4);
-            uint8_t* to = sm + CODES * STAGE + s * B_BYTES + row * 128;
-            uint4 c[4];
-#pragma unroll
-            for (int i = 0; i < 4; ++i)
-              if (warp - 16 + 4 * i < atoms) c[i] = *reinterpret_cast<const uint4*>(at + (warp - 16 + 4 * i) * 1024);
-#pragma unroll
-            for (int i = 0; i < 4; ++i)
-              if (warp - 16 + 4 * i < atoms) {
-                uint4 v0, v1;
-                codes_to_f16(c[i], v0, v1);
-                uint8_t* d = to + (warp - 16 + 4 * i) * 1024;
-                *reinterpret_cast<uint4*>(d + lo) = v0;
-                *reinterpret_cast<uint4*>(d + hi) = v1;
-              }
             tc05::fence_proxy_async_smem();
           }
           __syncwarp();
@@ -383,12 +390,9 @@ __global__ void __launch_bounds__(Regs<INT8>::THREADS, 1)
             s = 0;
             ph ^= 1;
           }
-          if ((k & 1) || k == p.steps - 1) {
-            if (lane == 0) mbar_arrive(&taken[r]);
-            if (++r == CODES) {
-              r = 0;
-              rph ^= 1;
-            }
+          if (++r == CODES) {
+            r = 0;
+            rph ^= 1;
           }
         }
       }
@@ -493,10 +497,12 @@ __global__ void __launch_bounds__(Regs<INT8>::THREADS, 1)
             tc05::fence_after_sync();
             const uint64_t da = da0 + s * (STAGE >> 4), db = db0 + s * (STAGE >> 4);
             const int parts = t.weights && k == steps - 1 ? (((t.clen - 1) & 63) >> 4) + 1 : 4;
-  #pragma unroll
-            for (int j = 0; j < 4; ++j) {
+#pragma unroll
+            for (int j = 0; j < (INT8 ? 8 : 4); ++j) {
               const uint32_t more = !fresh || j > 0 ? 1u : 0u;
-              if (INT8) tc05::mma_pair_ts(d, tmem + 256 + s * 32 + j * 8, db8 + s * (B_BYTES >> 4) + j * DB, idesc, more);
+              if (INT8)
+                tc05::mma_pair_ts(d, tmem + 256 + s * 64 + j * 8,
+                                  db8 + (2 * s + (j >> 2)) * (B_BYTES >> 4) + (j & 3) * DB, idesc, more);
               else if (j < parts) tc05::mma_pair(d, da + j * DA, db + j * DB, idesc, more);
             }
             for (int c = 0; c < 2; ++c) tc05::commit_pair(bars[c] + STAGES * 8 + s * 8);  // empty
@@ -878,9 +884,9 @@ cudaError_t launch_pair_forward(const ProductArgs& a, bool int8, int sm_count, u
   p.M = a.M;
   p.E = a.E;
   p.I = gated ? a.N / 2 : a.N;
-  p.steps = (a.K + 63) / 64;
+  p.steps = int8 ? (a.K + 127) / 128 : (a.K + 63) / 64;
   p.a_tiles = (a.N + 255) / 256;
-  p.tile = a.offsets == nullptr ? choose_tile(a.M, p.a_tiles, p.steps, sm_count / 2) : 256;
+  p.tile = a.offsets == nullptr ? choose_tile(a.M, p.a_tiles, (a.K + 63) / 64, sm_count / 2) : 256;
   p.act = a.act;
   p.row_tiles = (a.M + p.tile - 1) / p.tile;
   p.per_band = reciprocal(BAND * p.a_tiles);
