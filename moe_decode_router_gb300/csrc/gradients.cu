@@ -20,6 +20,8 @@ struct GateArgs {
   const int32_t* offsets;
   uint16_t* dgu;
   int M, I, E, act;
+  unsigned col_tiles;  // CTAs side by side
+  int wide;            // log2 of a CTA's threads on a row
 };
 
 // dg = dh * u * act'(g), du = dh * act(g), formed in fp32 from the kept bf16 sums and
@@ -28,12 +30,11 @@ struct GateArgs {
 __global__ void __launch_bounds__(256) gate_backward_kernel(const GateArgs p) {
   pdl_wait();
   pdl_trigger();
-  const unsigned per_row = (unsigned)p.I / 8;
   const int live = p.offsets == nullptr ? p.M : min(max(__ldg(p.offsets + p.E), 0), p.M);
-  const size_t at = (size_t)blockIdx.x * 256 + threadIdx.x;
-  const size_t row = at / per_row;
-  if (row >= (size_t)live) return;
-  const int i = (int)(at - row * per_row) * 8;
+  const unsigned tile = blockIdx.x / p.col_tiles, at = blockIdx.x - tile * p.col_tiles;
+  const size_t row = (size_t)tile * (256u >> p.wide) + (threadIdx.x >> p.wide);
+  const int i = (int)((at << p.wide) + (threadIdx.x & ((1u << p.wide) - 1u))) * 8;
+  if (row >= (size_t)live || i >= p.I) return;
   const uint16_t* gu = p.gu + row * 2 * p.I + i;
   const uint4 rd = ldg_once(p.dh + row * p.I + i), rg = ldg_once(gu), ru = ldg_once(gu + p.I);
   float d[8], g[8], u[8], dg[8], du[8];
@@ -81,8 +82,13 @@ cudaError_t launch_gate_backward(const void* dh, const void* gu, const int32_t* 
   p.I = I;
   p.E = E;
   p.act = act;
-  const size_t pieces = (size_t)M * (I / 8);
-  return launch_pdl(gate_backward_kernel, p, dim3((unsigned)((pieces + 255) / 256)), 256, st);
+  // as many threads on a row as leave at most an eighth of them without work
+  const int per_row = I / 8;
+  p.wide = 8;
+  while (p.wide > 0 && (((per_row - 1) >> p.wide) + 1) * 8 << p.wide > per_row * 9) --p.wide;
+  p.col_tiles = (unsigned)(((per_row - 1) >> p.wide) + 1);
+  const unsigned row_tiles = (unsigned)(((long long)M + (256 >> p.wide) - 1) / (256 >> p.wide));
+  return launch_pdl(gate_backward_kernel, p, dim3(row_tiles * p.col_tiles), 256, st);
 }
 
 }  // namespace flint

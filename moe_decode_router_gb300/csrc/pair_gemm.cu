@@ -113,6 +113,7 @@ struct Maps {
   CUtensorMap b[4];  // 16, 32, 64 or 128 rows of x (dy)
   CUtensorMap aw;    // weights: 64 columns of 64 rows of x (or 2 x 64)
   CUtensorMap bw;    // weights: 64 columns of 64 rows of dy
+  CUtensorMap bw1;   // weights: the same as pieces of 64 columns
   CUtensorMap bw2;   // weights: 2 x 64
 };
 
@@ -405,7 +406,7 @@ __global__ void __launch_bounds__(Regs<INT8>::THREADS, 1)
         const int nh = t.n >> 1, steps = steps_of(t);
         const int i0 = t.at * 256 + (int)rank * 128, oh = t.o0 + (int)rank * nh;
         const int sel = box_of(nh), boxes = (nh + 63) >> 6;
-        const bool both = p.pieces_n && nh == 128;  // weights: two pieces of B at once
+        const bool both = p.pieces_n && nh == 128, one = p.pieces_n && nh == 64;  // weights: pieces of 64 columns of B
         const uint32_t bytes = A_BYTES + (t.weights ? (uint32_t)boxes * 8192u : 2048u << sel);
         for (int k = 0; k < steps && lane == 0; ++k) {
           if (!wait(&empty[s], ph ^ 1)) {
@@ -442,7 +443,7 @@ __global__ void __launch_bounds__(Regs<INT8>::THREADS, 1)
               tc05::tma_pair_2d(a, &maps.aw, i0, c, bar);
               tc05::tma_pair_2d(a + 8192, &maps.aw, i0 + 64, c, bar);
             }
-            if (both) tc05::tma_pair_3d(b, &maps.bw2, 0, c, oh >> 6, bar);
+            if (both || one) tc05::tma_pair_3d(b, both ? &maps.bw2 : &maps.bw1, 0, c, oh >> 6, bar);
             else
               for (int i = 0; i < boxes; ++i) tc05::tma_pair_2d(b + i * 8192, &maps.bw, oh + i * 64, c, bar);
           }
@@ -478,7 +479,7 @@ __global__ void __launch_bounds__(Regs<INT8>::THREADS, 1)
         const uint64_t da0 = A_ROWS ? tc05::sw128_rows_desc(base, 8192) : tc05::sw128_desc(base);
         const uint64_t db_k = tc05::sw128_desc(base + A_BYTES), db_w = tc05::sw128_rows_desc(base + A_BYTES, 8192);
         const uint64_t db8 = tc05::sw128_desc(base + CODES * STAGE);
-        constexpr uint32_t DA = A_ROWS ? 128 : 2;  // 16 of the contracted dimension
+        constexpr int DA = A_ROWS ? 128 : 2;  // 16 of the contracted dimension
         for (int u = u0; u < n_units && ok; u += ustep) {
           const Unit t = unit_of(u);
           const int steps = steps_of(t);
@@ -492,20 +493,24 @@ __global__ void __launch_bounds__(Regs<INT8>::THREADS, 1)
             const uint32_t b = v % BUFS, d = tmem + b * 256;
             // every lane waits, and all go on or none
             ok = !fresh || __all_sync(0xffffffffu, wait(&tempty[b], ((v / BUFS) & 1) ^ 1));
-            ok = ok && __all_sync(0xffffffffu, wait(&full[s], ph));
+            if (ok && !__all_sync(0xffffffffu, mbar_test(&full[s], ph))) ok = __all_sync(0xffffffffu, wait(&full[s], ph));
             if (!ok) break;
             tc05::fence_after_sync();
             const uint64_t da = da0 + s * (STAGE >> 4), db = db0 + s * (STAGE >> 4);
             const int parts = t.weights && k == steps - 1 ? (((t.clen - 1) & 63) >> 4) + 1 : 4;
-#pragma unroll
-            for (int j = 0; j < (INT8 ? 8 : 4); ++j) {
-              const uint32_t more = !fresh || j > 0 ? 1u : 0u;
-              if (INT8)
-                tc05::mma_pair_ts(d, tmem + 256 + s * 64 + j * 8,
-                                  db8 + (2 * s + (j >> 2)) * (B_BYTES >> 4) + (j & 3) * DB, idesc, more);
-              else if (j < parts) tc05::mma_pair(d, da + j * DA, db + j * DB, idesc, more);
+            const uint32_t more = fresh ? 0u : 1u, free0 = bars[0] + STAGES * 8 + s * 8, free1 = bars[1] + STAGES * 8 + s * 8;
+            if (INT8) {
+              tc05::mma_pair_ts(d, tmem + 256 + s * 64, db8 + 2 * s * (B_BYTES >> 4), idesc, more);
+              tc05::mma_pair_ts(d, tmem + 256 + s * 64 + 32, db8 + (2 * s + 1) * (B_BYTES >> 4), idesc, 1);
+              tc05::commit_pair(free0);
+              tc05::commit_pair(free1);
+            } else if (parts == 4) {
+              tc05::mma_pair_step<DA>(d, da, db, DB, idesc, more, free0, free1);
+            } else {
+              for (int j = 0; j < parts; ++j) tc05::mma_pair(d, da + j * DA, db + j * DB, idesc, j > 0 ? 1u : more);
+              tc05::commit_pair(free0);
+              tc05::commit_pair(free1);
             }
-            for (int c = 0; c < 2; ++c) tc05::commit_pair(bars[c] + STAGES * 8 + s * 8);  // empty
             if (last) {
               for (int c = 0; c < 2; ++c) tc05::commit_pair(bars[c] + TFULL + b * 8);
               ++v;
@@ -569,10 +574,10 @@ __global__ void __launch_bounds__(Regs<INT8>::THREADS, 1)
       const int nh = t.n >> 1, steps = steps_of(t);
       const int live = min(nh, t.cnt - half * nh);  // columns of this half that are outputs
       using S = typename Held<INT8>::type;
-      constexpr int CHUNKS = PROMOTE ? 4 : 1;
-      S held[CHUNKS][32];
+      constexpr int CHUNKS = 4;
+      S held[PROMOTE ? CHUNKS : 1][32];
       uint32_t b = 0;
-      if (PROMOTE) {
+      if constexpr (PROMOTE) {
 #pragma unroll
         for (int c = 0; c < CHUNKS; ++c)
 #pragma unroll
@@ -622,18 +627,28 @@ __global__ void __launch_bounds__(Regs<INT8>::THREADS, 1)
           sw[i] = __ldg(w + min(n, p.I - 1) + (GATED && i >= 2 ? p.I : 0));
         }
       }
+      // Chunk c of the accumulator, on its way to registers while the one before is put out.
+      uint32_t next[PROMOTE ? 1 : 32];
+      auto fetch = [&](int c) {
+        if constexpr (!PROMOTE) {
+          if (steps > 0 && 32 * c < live) {
+            const uint32_t ta = lanes + b * 256 + (uint32_t)(half * nh + 32 * c);
+            tc05::ld_16x256b_x4(ta, next);
+            tc05::ld_16x256b_x4(ta + (16u << 16), next + 16);
+          }
+        }
+      };
+      fetch(0);
 #pragma unroll
-      for (int c = 0; c < (PROMOTE ? CHUNKS : 4); ++c) {
+      for (int c = 0; c < 4; ++c) {
         if (32 * c >= live) break;
         uint32_t r[32];
-        if (!PROMOTE && steps > 0) {
-          const uint32_t ta = lanes + b * 256 + (uint32_t)(half * nh + 32 * c);
-          tc05::ld_16x256b_x4(ta, r);
-          tc05::ld_16x256b_x4(ta + (16u << 16), r + 16);
-          tc05::wait_ld32(r);
-        } else if (!PROMOTE) {
+        if constexpr (!PROMOTE) {
+          if (steps > 0) tc05::wait_ld32(next);
 #pragma unroll
-          for (int i = 0; i < 32; ++i) r[i] = 0;
+          for (int i = 0; i < 32; ++i) r[i] = steps > 0 ? next[i] : 0u;
+          fetch(c + 1);
+          if (steps > 0 && 32 * (c + 1) >= live) give_back(b);
         } else {
           const size_t row = row0 + half * nh + 32 * c;
 #pragma unroll
@@ -646,7 +661,7 @@ __global__ void __launch_bounds__(Regs<INT8>::THREADS, 1)
 #pragma unroll
             for (int j = 0; j < 8; ++j) {
               const int at = (j >> 2) * 16 + 4 * k + (j & 3);
-              const float x = (float)held[PROMOTE ? c : 0][at];
+              const float x = (float)held[c][at];
               r[at] = __float_as_uint(INT8 ? x * (sx[j & 1] * sw[(j >> 2) * 2 + ((j >> 1) & 1)]) : x);
             }
           }
@@ -726,7 +741,7 @@ __global__ void __launch_bounds__(Regs<INT8>::THREADS, 1)
           __syncwarp();
         }
       }
-      if (!PROMOTE && steps > 0) give_back(b);
+      if (!PROMOTE && steps > 0 && live <= 0) give_back(b);
     }
   }
   __syncwarp();
@@ -786,9 +801,17 @@ long long row_tiles(int M, int E, bool grouped, int tile) {
   return (long long)M / tile + (M < E ? M : E);
 }
 
-// A unit takes about so many cycles: its operands' bytes at 64 a cycle, which for 256 columns is the
-// MMAs' time too, and what its start and end leave uncovered.
-long long unit_cycles(long long steps, int n) { return steps * (256 + n) + 1500; }
+// What a step of 64 of the contracted dimension takes, measured (ns, 64 units of 256 x n on 76 pairs):
+//   n          256  192  128   64   32
+//   forward    287  234  201  201  199     below 160 columns the way of a stage through the ring
+//   input      289  250  241  241  239
+//   weights    285    -  304  304    -
+// and a unit's start and end, where nothing else covers them, some 3,000 + 10 n.
+enum { STEP_FORWARD = 200, STEP_INPUT = 240, STEP_WEIGHTS = 285 };
+long long unit_ns(long long steps, int n, int least) {
+  const int by_columns = n * 9 / 8;
+  return steps * (by_columns > least ? by_columns : least) + 3000 + 10 * n;
+}
 
 // Tile of a dense product's rows, so that the units fill the pairs of SMs evenly.
 int choose_tile(int M, long long a_tiles, long long steps, int pairs) {
@@ -796,7 +819,7 @@ int choose_tile(int M, long long a_tiles, long long steps, int pairs) {
   long long least = -1;
   for (int tile = 256; tile >= 32; tile -= 32) {
     const long long units = (M + tile - 1LL) / tile * a_tiles;
-    const long long c = (units + pairs - 1) / pairs * unit_cycles(steps, M < tile ? (M + 31) & ~31 : tile);
+    const long long c = (units + pairs - 1) / pairs * unit_ns(steps, M < tile ? (M + 31) & ~31 : tile, STEP_FORWARD);
     if (least < 0 || c < least) {
       least = c;
       best = tile;
@@ -811,9 +834,9 @@ void choose_tiles(PairArgs& p, bool dx, bool dw, int pairs) {
   long long least = -1;
   int best = 256, best_w = 256;
   for (int tile = 256; tile >= (dx ? 64 : 256); tile -= 32)
-    for (int tile_w = 256; tile_w >= (dw ? 64 : 256); tile_w -= 32) {
-      const long long a = dx ? (p.M + tile - 1LL) / tile * p.a_tiles : 0, ca = unit_cycles(p.steps, tile);
-      const long long b = dw ? (p.O + tile_w - 1LL) / tile_w * p.a_tiles : 0, cb = unit_cycles(rows_steps, tile_w);
+    for (int tile_w = 256; tile_w >= (dw ? 128 : 256); tile_w -= 128) {  // whole pieces of 64 columns
+      const long long a = dx ? (p.M + tile - 1LL) / tile * p.a_tiles : 0, ca = unit_ns(p.steps, tile, STEP_INPUT);
+      const long long b = dw ? (p.O + tile_w - 1LL) / tile_w * p.a_tiles : 0, cb = unit_ns(rows_steps, tile_w, STEP_WEIGHTS);
       const long long edge = a % pairs, end = (a + b) % pairs;  // pairs below an edge have one unit more
       long long most = 0;
       for (long long q : {0LL, edge, end}) {
@@ -897,7 +920,7 @@ cudaError_t launch_pair_forward(const ProductArgs& a, bool int8, int sm_count, u
       gated ? encode(&m.a, size, a.w, {K, 16, 2, N / 32, E}, {K, N / 2 * K, 16 * K, N * K}, {inner, 16, 2, 4, 1})
             : encode(&m.a, size, a.w, {K, N, E}, {K, N * K}, {inner, 128, 1});
   if (!ok || !encode_rows(m, size, a.x, M, K)) return cudaErrorInvalidValue;
-  m.aw = m.bw = m.bw2 = m.a;
+  m.aw = m.bw = m.bw1 = m.bw2 = m.a;
   const long long most = row_tiles(a.M, a.E, a.offsets != nullptr, p.tile) * p.a_tiles;
   if (int8) {
     if (gated) return a.f32 ? launch<FORWARD, true, true, true>(p, m, most, sm_count, st)
@@ -938,8 +961,10 @@ cudaError_t launch_pair_backward(const GradArgs& a, int sm_count, unsigned* err,
   ok = ok && (p.pieces_k ? encode(&m.aw, 2, a.x, {64, M, K / 64}, {K, 64}, {64, 64, 2})
                          : encode(&m.aw, 2, a.x, {K, M}, {K}, {64, 64}));
   ok = ok && encode(&m.bw, 2, a.dy, {N, M}, {N}, {64, 64});
-  m.bw2 = m.bw;
-  if (p.pieces_n) ok = ok && encode(&m.bw2, 2, a.dy, {64, M, N / 64}, {N, 64}, {64, 64, 2});
+  m.bw1 = m.bw2 = m.bw;
+  if (p.pieces_n)
+    ok = ok && encode(&m.bw1, 2, a.dy, {64, M, N / 64}, {N, 64}, {64, 64, 1}) &&
+         encode(&m.bw2, 2, a.dy, {64, M, N / 64}, {N, 64}, {64, 64, 2});
   if (!ok) return cudaErrorInvalidValue;
   long long most = (long long)a.E * p.o_tiles * p.a_tiles;
   if (a.dx != nullptr) most += row_tiles(a.M, a.E, a.offsets != nullptr, p.tile) * p.a_tiles;

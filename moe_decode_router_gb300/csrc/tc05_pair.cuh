@@ -59,8 +59,30 @@ __device__ __forceinline__ uint64_t sw128_rows_desc(uint32_t smem_addr, uint32_t
          (uint64_t)1u << 46 | (uint64_t)2u << 61;
 }
 
-// D (+)= A * B^T over both CTAs of the pair, one instruction (256 x N x 16) of the lane that
-// elect.sync picks of a whole converged warp of the even CTA.
+// D (+)= A * B^T over both CTAs of the pair, 256 x N x 64: four instructions whose operands lie
+// DA and DB (in descriptor units) apart, of the lane that elect.sync picks of a whole
+// converged warp of the even CTA; then the stage's release: an arrival on an mbarrier of
+// either CTA (shared-cluster addresses) when all MMAs that the lane issued so far have
+// completed.  In one piece, as an election for every instruction made a step 350 cycles long.
+template <int DA>
+__device__ __forceinline__ void mma_pair_step(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t db,
+                                              uint32_t idesc, uint32_t accumulate, uint32_t bar0, uint32_t bar1) {
+  asm volatile(
+      "{\n .reg .pred p, q, e;\n .reg .b64 a1, a2, a3, b1, b2, b3, db;\n"
+      " setp.ne.b32 p, %4, 0;\n setp.eq.b32 q, %4, %4;\n cvt.u64.u32 db, %5;\n"
+      " add.s64 a1, %1, %8;\n add.s64 a2, a1, %8;\n add.s64 a3, a2, %8;\n"
+      " add.s64 b1, %2, db;\n add.s64 b2, b1, db;\n add.s64 b3, b2, db;\n"
+      " elect.sync _|e, 0xffffffff;\n"
+      " @e tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n"
+      " @e tcgen05.mma.cta_group::2.kind::f16 [%0], a1, b1, %3, q;\n"
+      " @e tcgen05.mma.cta_group::2.kind::f16 [%0], a2, b2, %3, q;\n"
+      " @e tcgen05.mma.cta_group::2.kind::f16 [%0], a3, b3, %3, q;\n"
+      " @e tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.b64 [%6];\n"
+      " @e tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.b64 [%7];\n}\n" ::"r"(d_tmem),
+      "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate), "r"(db), "r"(bar0), "r"(bar1), "n"(DA)
+      : "memory");
+}
+// One of its instructions (256 x N x 16).
 __device__ __forceinline__ void mma_pair(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc,
                                          uint32_t accumulate) {
   asm volatile(
@@ -69,12 +91,19 @@ __device__ __forceinline__ void mma_pair(uint32_t d_tmem, uint64_t a_desc, uint6
       "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate)
       : "memory");
 }
-// The same with A in tensor memory: lanes are its rows, a column holds two neighbours of K.
+// Four with A in tensor memory, 8 columns each: lanes are its rows, a column holds two neighbours of K.
 __device__ __forceinline__ void mma_pair_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_t b_desc, uint32_t idesc,
                                             uint32_t accumulate) {
   asm volatile(
-      "{\n .reg .pred p, e;\n setp.ne.b32 p, %4, 0;\n elect.sync _|e, 0xffffffff;\n"
-      " @e tcgen05.mma.cta_group::2.kind::f16 [%0], [%1], %2, %3, p;\n}\n" ::"r"(d_tmem),
+      "{\n .reg .pred p, q, e;\n .reg .b64 b1, b2, b3;\n .reg .b32 a1, a2, a3;\n"
+      " setp.ne.b32 p, %4, 0;\n setp.eq.b32 q, %4, %4;\n"
+      " add.u32 a1, %1, 8;\n add.u32 a2, %1, 16;\n add.u32 a3, %1, 24;\n"
+      " add.s64 b1, %2, 2;\n add.s64 b2, %2, 4;\n add.s64 b3, %2, 6;\n"
+      " elect.sync _|e, 0xffffffff;\n"
+      " @e tcgen05.mma.cta_group::2.kind::f16 [%0], [%1], %2, %3, p;\n"
+      " @e tcgen05.mma.cta_group::2.kind::f16 [%0], [a1], b1, %3, q;\n"
+      " @e tcgen05.mma.cta_group::2.kind::f16 [%0], [a2], b2, %3, q;\n"
+      " @e tcgen05.mma.cta_group::2.kind::f16 [%0], [a3], b3, %3, q;\n}\n" ::"r"(d_tmem),
       "r"(a_tmem), "l"(b_desc), "r"(idesc), "r"(accumulate)
       : "memory");
 }
