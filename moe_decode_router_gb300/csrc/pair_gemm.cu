@@ -35,8 +35,9 @@
 // integers in registers.  fp32 outputs of bf16 operands are promoted the same way every 512 of the
 // contracted dimension: the tensor cores cut a sum instead of rounding it, which adds up.
 //
-// Warps: 0-7 output, two halves of the columns; 8 TMA producer; 9 MMA issuer (of the even
-// CTA); 10 rows behind the end; 11 none; 12-15 and 16-19 codes to fp16 (integers).
+// Warps: output (the first 8 or 16, a quarter of the lanes and a part of the columns each); then the
+// TMA producer; the MMA issuer (of the even CTA); rows behind the end; none; integers: four
+// and four that turn codes to fp16.
 #include <initializer_list>
 
 #include "product_common.cuh"
@@ -53,23 +54,28 @@ constexpr int RING = 6;            // stages of operands
 constexpr int CODES = 3;           // integers: stages of codes, 128 of K each, then
 constexpr int TURNED = 3;          //   stages of one operand in fp16, and as many in tensor memory behind the sums
 static_assert(CODES * STAGE + TURNED * 2 * B_BYTES <= RING * STAGE && 256 + TURNED * 64 <= 512, "rings");
-constexpr int OUT_WARP = 32 * 80;  // output staging of a warp: 32 rows of 64 bytes, 80 apart
+constexpr int OUT_BYTES = 8 * 32 * 80;  // output staging: rows of 64 bytes, 80 apart, 32 a warp (16 of 16 warps)
 constexpr int OFF_OUT = RING * STAGE;
-constexpr int OFF_BARS = OFF_OUT + 8 * OUT_WARP;
+constexpr int OFF_BARS = OFF_OUT + OUT_BYTES;
 constexpr int SEG_F32 = 8, SEG_INT = 8;  // steps (of 64; integers: of 128) between promotions
 
-// Registers a thread: the output warps of a promoting kernel hold 128 sums each and take what
-// the others give up; a block is launched with LAUNCH of them.
-template <bool INT8>
-struct Regs {
-  static constexpr int THREADS = INT8 ? 640 : 384, LAUNCH = INT8 ? 96 : 168;
-  static constexpr int HIGH = INT8 ? 168 : 224, LOW = 48;
-  static_assert(HIGH * 256 + LOW * (THREADS - 256) <= LAUNCH * THREADS, "register shares");
-};
 constexpr int OFF_GROUPS = OFF_BARS + 256;
 constexpr int pair_smem(int E) { return OFF_GROUPS + (3 * E + 1) * 4; }
 static_assert(pair_smem(ROUTE_MAX_E) <= 232448, "shared memory");
 static_assert((3 * RING + CODES + 4) * 8 + 8 <= 256, "barriers");
+
+// Warps and registers.  A kernel that adds up its accumulators has 8 output warps, which hold
+// 128 sums a thread and take registers that the others give up (a block is launched with LAUNCH
+// a thread); the others have 16, as a tile's way out is a chain of short steps: the weights'
+// gradient of 256 experts (49,152 rows, 1024 x 2048) took 284 us with 8.
+template <bool PROMOTE, bool INT8>
+struct Shape {
+  static constexpr int OUT_WARPS = PROMOTE ? 8 : 16, PARTS = OUT_WARPS / 4;  // parts of the columns
+  static constexpr int CHUNK = PROMOTE ? 32 : 16;                            // columns on their way at a time
+  static constexpr int THREADS = PROMOTE && !INT8 ? 384 : 640;
+  static constexpr int LAUNCH = INT8 ? 96 : 168, HIGH = INT8 ? 168 : 224, LOW = 48;
+  static_assert(!PROMOTE || HIGH * 256 + LOW * (THREADS - 256) <= LAUNCH * THREADS, "register shares");
+};
 
 struct PairArgs {
   const int32_t* offsets;
@@ -148,10 +154,12 @@ __device__ __forceinline__ void codes_to_f16(const uint4 c, uint4& lo, uint4& hi
 }
 
 template <int MODE, bool GATED, bool F32, bool INT8>
-__global__ void __launch_bounds__(Regs<INT8>::THREADS, 1)
+__global__ void __launch_bounds__(Shape<F32 || INT8, INT8>::THREADS, 1)
     pair_gemm_kernel(const PairArgs p, const __grid_constant__ Maps maps) {
-  constexpr int STAGES = INT8 ? TURNED : RING, BUFS = INT8 ? 1 : 2, THREADS = Regs<INT8>::THREADS;
+  constexpr int STAGES = INT8 ? TURNED : RING, BUFS = INT8 ? 1 : 2;
   constexpr bool PROMOTE = F32 || INT8;
+  using W = Shape<PROMOTE, INT8>;
+  constexpr int THREADS = W::THREADS, PRODUCER = W::OUT_WARPS, ISSUER = PRODUCER + 1, ZEROS = PRODUCER + 2;
   static_assert(!INT8 || MODE == FORWARD, "integers have no gradient");
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   uint8_t* sm = smem_raw;
@@ -163,7 +171,7 @@ __global__ void __launch_bounds__(Regs<INT8>::THREADS, 1)
                                                                 // [CODES] integers: codes of this CTA landed
   uint64_t* taken = landed + RING;                              // [CODES] integers: codes turned
   uint64_t* tfull = taken + CODES;                              // [2] accumulator complete
-  uint64_t* tempty = tfull + 2;                                 // [2] accumulator read, 16 warps (even CTA's)
+  uint64_t* tempty = tfull + 2;                                 // [2] accumulator read, by both CTAs' output warps (even CTA's)
   uint32_t* tslot = reinterpret_cast<uint32_t*>(tempty + 2);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tslot + 1);
   int* g_units = reinterpret_cast<int*>(sm + OFF_GROUPS);  // [E + 1] units before each group
@@ -179,7 +187,7 @@ __global__ void __launch_bounds__(Regs<INT8>::THREADS, 1)
     for (int i = 0; i < CODES; ++i) mbar_init(&taken[i], 8);
     for (int i = 0; i < 2; ++i) {
       mbar_init(&tfull[i], 1);
-      mbar_init(&tempty[i], 16);
+      mbar_init(&tempty[i], 2 * W::OUT_WARPS);
     }
     *abort_flag = 0;
     fence_mbar_init();
@@ -187,7 +195,7 @@ __global__ void __launch_bounds__(Regs<INT8>::THREADS, 1)
   pdl_wait();
   // Tensor memory is taken when the grid before this one is gone and (below) given back
   // before either CTA of a pair ends: taking it may wait without a limit for another's.
-  if (warp == 8) {
+  if (warp == PRODUCER) {
     tc05::alloc_pair(tslot, 512);
     tc05::relinquish_pair();
   }
@@ -195,7 +203,7 @@ __global__ void __launch_bounds__(Regs<INT8>::THREADS, 1)
   if (p.offsets != nullptr)
     for (int e = tid; e <= p.E; e += THREADS) g_units[e] = __ldg(p.offsets + e);  // all on their way at once
   __syncthreads();
-  if (warp == 8) {
+  if (warp == PRODUCER) {
     int base = 0;
     for (int e0 = 0; e0 < p.E; e0 += 32) {
       const int e = e0 + lane;
@@ -288,9 +296,9 @@ __global__ void __launch_bounds__(Regs<INT8>::THREADS, 1)
   // the smallest box of B that holds so many rows: 16 << box_of
   auto box_of = [](int rows) { return rows <= 16 ? 0 : rows <= 32 ? 1 : rows <= 64 ? 2 : 3; };
   const uint32_t base = smem_u32(sm), full0 = tc05::map_rank(smem_u32(full), 0);
-  if (warp >= 8) {
-    if (PROMOTE) tc05::regs_down<Regs<INT8>::LOW>();
-    if (INT8 && warp == 8) {
+  if (warp >= W::OUT_WARPS) {
+    if (PROMOTE) tc05::regs_down<W::LOW>();
+    if (INT8 && warp == PRODUCER) {
       // ---------------- producer of codes: stages of 128 of K
       uint32_t r = 0, ph = 0, issued = 0;
       bool ok = true;
@@ -397,7 +405,7 @@ __global__ void __launch_bounds__(Regs<INT8>::THREADS, 1)
           }
         }
       }
-    } else if (warp == 8) {
+    } else if (warp == PRODUCER) {
       // ---------------- producer: this CTA's 128 of i and its half of the columns
       uint32_t s = 0, ph = 0, issued = 0;  // of lane 0, which copies
       bool ok = true;
@@ -466,7 +474,7 @@ __global__ void __launch_bounds__(Regs<INT8>::THREADS, 1)
           }
         }
       }
-    } else if (warp == 9) {
+    } else if (warp == ISSUER) {
       // ---------------- MMA issuer.  The whole warp runs the loop, so that the descriptors
       // are warp-uniform values.
       if (rank == 0) {
@@ -527,7 +535,7 @@ __global__ void __launch_bounds__(Regs<INT8>::THREADS, 1)
           }
         }
       }
-    } else if (warp == 10) {
+    } else if (warp == ZEROS) {
       // ---------------- weights: zeros for the rows of a last step that are not the expert's
       if (MODE == BACKWARD) {
         uint32_t g = 0, parity = 0;  // steps so far; of `landed`, a bit a stage
@@ -541,23 +549,22 @@ __global__ void __launch_bounds__(Regs<INT8>::THREADS, 1)
           ok = __all_sync(0xffffffffu, wait(&landed[s], (parity >> s) & 1));
           if (!ok) break;
           parity ^= 1u << s;
+          // a row of every piece of both operands: 8 lanes each
           const int from = t.clen & 63, to = (from + 15) & ~15, pieces = 2 + ((t.n / 2 + 63) >> 6);
-          uint8_t* stage = sm + s * STAGE;
-          for (int i = lane; i < (to - from) * pieces * 8; i += 32) {
-            const int row = from + i / (pieces * 8), c = i % (pieces * 8);
-            *reinterpret_cast<uint4*>(stage + (c >> 3) * 8192 + row * 128 + (c & 7) * 16) = make_uint4(0, 0, 0, 0);
-          }
-          tc05::fence_async();
+          uint8_t* at = sm + s * STAGE + (lane >> 3) * 8192 + (lane & 7) * 16;
+          if (lane < pieces * 8)
+            for (int row = from; row < to; ++row) *reinterpret_cast<uint4*>(at + row * 128) = make_uint4(0, 0, 0, 0);
+          tc05::fence_proxy_async_smem();
           __syncwarp();
           if (lane == 0) tc05::arrive_cluster(full0 + s * 8);
         }
       }
     }
   } else {
-    if (PROMOTE) tc05::regs_up<Regs<INT8>::HIGH>();
+    if (PROMOTE) tc05::regs_up<W::HIGH>();
     // ---------------- output
-    const int quad = warp & 3, half = warp >> 2;
-    uint8_t* out = sm + OFF_OUT + warp * OUT_WARP;
+    const int quad = warp & 3, part = warp >> 2;
+    uint8_t* out = sm + OFF_OUT + warp * (OUT_BYTES / W::OUT_WARPS);
     const uint32_t lanes = tmem + ((uint32_t)(quad * 32) << 16);
     const uint32_t tempty0 = tc05::map_rank(smem_u32(tempty), 0);
     const int g = lane >> 2, q = lane & 3;
@@ -571,8 +578,8 @@ __global__ void __launch_bounds__(Regs<INT8>::THREADS, 1)
     };
     for (int u = u0; u < n_units && ok; u += ustep) {
       const Unit t = unit_of(u);
-      const int nh = t.n >> 1, steps = steps_of(t);
-      const int live = min(nh, t.cnt - half * nh);  // columns of this half that are outputs
+      const int np = t.n / W::PARTS, first = part * np, steps = steps_of(t);
+      const int live = min(np, t.cnt - first);  // columns of this part that are outputs
       using S = typename Held<INT8>::type;
       constexpr int CHUNKS = 4;
       S held[PROMOTE ? CHUNKS : 1][32];
@@ -593,7 +600,7 @@ __global__ void __launch_bounds__(Regs<INT8>::THREADS, 1)
           for (int c = 0; c < CHUNKS; ++c) {
             if (32 * c < live) {
               uint32_t r[32];
-              const uint32_t ta = lanes + b * 256 + (uint32_t)(half * nh + 32 * c);
+              const uint32_t ta = lanes + b * 256 + (uint32_t)(first + 32 * c);
               tc05::ld_16x256b_x4(ta, r);
               tc05::ld_16x256b_x4(ta + (16u << 16), r + 16);
               tc05::wait_ld32(r);
@@ -628,29 +635,30 @@ __global__ void __launch_bounds__(Regs<INT8>::THREADS, 1)
         }
       }
       // Chunk c of the accumulator, on its way to registers while the one before is put out.
-      uint32_t next[PROMOTE ? 1 : 32];
+      constexpr int CW = W::CHUNK, GROUPS = CW / 8;  // groups of 8 columns
+      uint32_t next[PROMOTE ? 1 : 16];
       auto fetch = [&](int c) {
         if constexpr (!PROMOTE) {
-          if (steps > 0 && 32 * c < live) {
-            const uint32_t ta = lanes + b * 256 + (uint32_t)(half * nh + 32 * c);
-            tc05::ld_16x256b_x4(ta, next);
-            tc05::ld_16x256b_x4(ta + (16u << 16), next + 16);
+          if (steps > 0 && CW * c < live) {
+            const uint32_t ta = lanes + b * 256 + (uint32_t)(first + CW * c);
+            tc05::ld_16x256b_x2(ta, next);
+            tc05::ld_16x256b_x2(ta + (16u << 16), next + 8);
           }
         }
       };
       fetch(0);
 #pragma unroll
       for (int c = 0; c < 4; ++c) {
-        if (32 * c >= live) break;
-        uint32_t r[32];
+        if (CW * c >= live) break;
+        uint32_t r[CW];
+        const size_t row = row0 + first + CW * c;
         if constexpr (!PROMOTE) {
-          if (steps > 0) tc05::wait_ld32(next);
+          if (steps > 0) tc05::wait_ld16(next);
 #pragma unroll
-          for (int i = 0; i < 32; ++i) r[i] = steps > 0 ? next[i] : 0u;
+          for (int i = 0; i < CW; ++i) r[i] = steps > 0 ? next[i] : 0u;
           fetch(c + 1);
-          if (steps > 0 && 32 * (c + 1) >= live) give_back(b);
+          if (steps > 0 && CW * (c + 1) >= live) give_back(b);
         } else {
-          const size_t row = row0 + half * nh + 32 * c;
 #pragma unroll
           for (int k = 0; k < 4; ++k) {
             float sx[2] = {1.f, 1.f};
@@ -666,31 +674,30 @@ __global__ void __launch_bounds__(Regs<INT8>::THREADS, 1)
             }
           }
         }
-        const int left = live - 32 * c;  // columns of the chunk that are outputs
-        const size_t row = row0 + half * nh + 32 * c;
-        auto f = [&](int h, int k, int j) { return __uint_as_float(r[16 * h + 4 * k + j]); };
+        const int left = live - CW * c;  // columns of the chunk that are outputs
+        auto f = [&](int h, int k, int j) { return __uint_as_float(r[CW / 2 * h + 4 * k + j]); };
         if (GATED && F32) {
           float* y = static_cast<float*>(p.y);
 #pragma unroll
-          for (int k = 0; k < 4; ++k)
+          for (int k = 0; k < GROUPS; ++k)
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
               const int col = 8 * k + 2 * q + (j & 1), i = i0 + (j >> 1) * 8 + g;
               if (col < left && i < p.I) y[(row + col) * p.I + i] = activation(f(0, k, j), p.act) * f(1, k, j);
             }
         } else if (GATED) {
-          // A tile of 16 i's x 32 columns, through shared memory: rows of 32 bytes
+          // 16 i's x the chunk's columns, through shared memory: rows of 32 bytes
           auto put = [&](uint16_t* to, size_t width, auto&& pair) {
             const uint32_t st = smem_u32(out) + ((lane >> 4) * 8 + (lane & 7)) * 48 + ((lane >> 3) & 1) * 16;
 #pragma unroll
-            for (int k = 0; k < 4; k += 2)
+            for (int k = 0; k < GROUPS; k += 2)
               asm volatile("stmatrix.sync.aligned.m8n8.x4.trans.shared.b16 [%0], {%1, %2, %3, %4};" ::"r"(
                                st + k * 8 * 48),
                            "r"(pair(k, 0)), "r"(pair(k, 2)), "r"(pair(k + 1, 0)), "r"(pair(k + 1, 2))
                            : "memory");
             __syncwarp();
 #pragma unroll
-            for (int k = 0; k < 2; ++k) {
+            for (int k = 0; k < GROUPS / 2; ++k) {
               const int col = 16 * k + (lane >> 1);
               if (col < left && i0 < p.I)
                 *reinterpret_cast<uint4*>(to + (row + col) * width + i0 + (lane & 1) * 8) =
@@ -709,7 +716,7 @@ __global__ void __launch_bounds__(Regs<INT8>::THREADS, 1)
         } else if (F32 && (MODE == FORWARD || t.weights)) {
           float* y = static_cast<float*>(to);
 #pragma unroll
-          for (int k = 0; k < 4; ++k)
+          for (int k = 0; k < GROUPS; ++k)
 #pragma unroll
             for (int h = 0; h < 2; ++h)
 #pragma unroll
@@ -721,7 +728,7 @@ __global__ void __launch_bounds__(Regs<INT8>::THREADS, 1)
           uint16_t* y = static_cast<uint16_t*>(to);
           const uint32_t st = smem_u32(out) + (lane & 7) * 80 + (lane >> 3) * 16;  // row lane % 8 of matrix lane / 8
 #pragma unroll
-          for (int k = 0; k < 4; ++k)
+          for (int k = 0; k < GROUPS; ++k)
             asm volatile("stmatrix.sync.aligned.m8n8.x4.trans.shared.b16 [%0], {%1, %2, %3, %4};" ::"r"(st + k * 640),
                          "r"(bf16x2_bits(f(0, k, 0), f(0, k, 1))), "r"(bf16x2_bits(f(0, k, 2), f(0, k, 3))),
                          "r"(bf16x2_bits(f(1, k, 0), f(1, k, 1))), "r"(bf16x2_bits(f(1, k, 2), f(1, k, 3)))
@@ -729,7 +736,7 @@ __global__ void __launch_bounds__(Regs<INT8>::THREADS, 1)
           __syncwarp();
           const int i = i0 + (lane & 3) * 8;
 #pragma unroll
-          for (int k = 0; k < 4; ++k) {
+          for (int k = 0; k < GROUPS; ++k) {
             const int col = 8 * k + (lane >> 2);
             if (col < left && i < p.I) {  // the width is a multiple of 8
               uint4* dst = reinterpret_cast<uint4*>(y + (row + col) * p.I + i);
@@ -748,7 +755,7 @@ __global__ void __launch_bounds__(Regs<INT8>::THREADS, 1)
   tc05::fence_before_sync();
   __syncthreads();
   tc05::cluster_sync();  // no arrival or copy is under way to either CTA any more
-  if (warp == 8) {
+  if (warp == PRODUCER) {
     tc05::fence_after_sync();
     tc05::dealloc_pair(tmem, 512);
   }
@@ -780,7 +787,7 @@ cudaError_t launch(const PairArgs& p, const Maps& maps, long long most, int sm_c
   const int pairs = sm_count / 2;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(2u * (unsigned)(most < pairs ? most : pairs));
-  cfg.blockDim = dim3(Regs<INT8>::THREADS);
+  cfg.blockDim = dim3(Shape<F32 || INT8, INT8>::THREADS);
   cfg.dynamicSmemBytes = pair_smem(p.E);
   cfg.stream = st;
   cudaLaunchAttribute attr[2];
@@ -878,12 +885,12 @@ cudaError_t pair_gemm_kernels_init() {
   } k[] = {{reinterpret_cast<const void*>(pair_gemm_kernel<FORWARD, true, false, false>), 0},
            {reinterpret_cast<const void*>(pair_gemm_kernel<FORWARD, false, false, false>), 0},
            {reinterpret_cast<const void*>(pair_gemm_kernel<BACKWARD, false, false, false>), 0},
-           {reinterpret_cast<const void*>(pair_gemm_kernel<FORWARD, false, true, false>), Regs<false>::LAUNCH},
-           {reinterpret_cast<const void*>(pair_gemm_kernel<BACKWARD, false, true, false>), Regs<false>::LAUNCH},
-           {reinterpret_cast<const void*>(pair_gemm_kernel<FORWARD, false, false, true>), Regs<true>::LAUNCH},
-           {reinterpret_cast<const void*>(pair_gemm_kernel<FORWARD, false, true, true>), Regs<true>::LAUNCH},
-           {reinterpret_cast<const void*>(pair_gemm_kernel<FORWARD, true, false, true>), Regs<true>::LAUNCH},
-           {reinterpret_cast<const void*>(pair_gemm_kernel<FORWARD, true, true, true>), Regs<true>::LAUNCH}};
+           {reinterpret_cast<const void*>(pair_gemm_kernel<FORWARD, false, true, false>), Shape<true, false>::LAUNCH},
+           {reinterpret_cast<const void*>(pair_gemm_kernel<BACKWARD, false, true, false>), Shape<true, false>::LAUNCH},
+           {reinterpret_cast<const void*>(pair_gemm_kernel<FORWARD, false, false, true>), Shape<true, true>::LAUNCH},
+           {reinterpret_cast<const void*>(pair_gemm_kernel<FORWARD, false, true, true>), Shape<true, true>::LAUNCH},
+           {reinterpret_cast<const void*>(pair_gemm_kernel<FORWARD, true, false, true>), Shape<true, true>::LAUNCH},
+           {reinterpret_cast<const void*>(pair_gemm_kernel<FORWARD, true, true, true>), Shape<true, true>::LAUNCH}};
   for (const auto& x : k) {
     cudaError_t e = cudaFuncSetAttribute(x.f, cudaFuncAttributeMaxDynamicSharedMemorySize, pair_smem(ROUTE_MAX_E));
     if (e != cudaSuccess) return e;

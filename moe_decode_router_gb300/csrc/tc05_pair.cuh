@@ -45,9 +45,6 @@ __device__ __forceinline__ void relinquish_pair() {
 __device__ __forceinline__ void dealloc_pair(uint32_t taddr, uint32_t ncols) {
   asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(taddr), "r"(ncols) : "memory");
 }
-// Generic-proxy writes to shared memory before this become visible to the async proxy (either CTA's MMA).
-__device__ __forceinline__ void fence_async() { asm volatile("fence.proxy.async;" ::: "memory"); }
-
 // Bits of the instruction descriptor: an operand whose M or N dimension is contiguous in memory.
 constexpr uint32_t A_ROWS_CONTIGUOUS = 1u << 15, B_ROWS_CONTIGUOUS = 1u << 16;
 
@@ -106,6 +103,13 @@ __device__ __forceinline__ void mma_pair_ts(uint32_t d_tmem, uint32_t a_tmem, ui
       " @e tcgen05.mma.cta_group::2.kind::f16 [%0], [a3], b3, %3, q;\n}\n" ::"r"(d_tmem),
       "r"(a_tmem), "l"(b_desc), "r"(idesc), "r"(accumulate)
       : "memory");
+}
+// 16 TMEM lanes x 16 consecutive 32-bit columns, laid out as by ld_16x256b_x4.
+__device__ __forceinline__ void ld_16x256b_x2(uint32_t taddr, uint32_t* r) {
+  asm volatile("tcgen05.ld.sync.aligned.16x256b.x2.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
+               : "r"(taddr)
+               : "memory");
 }
 // 16 32-bit columns of the warp's 32 lanes (thread i -> lane i), and the wait for such stores.
 __device__ __forceinline__ void st_32x32b_x16(uint32_t taddr, const uint4 (&v)[4]) {
