@@ -82,8 +82,8 @@ __global__ void __launch_bounds__(256, 3) integer_rows_kernel(const IntRowsArgs 
   const int row = blockIdx.x * (256 / THREADS) + threadIdx.x / THREADS;
   const bool in = row < p.rows;
   const size_t base = (size_t)row * (size_t)p.stride;
-  constexpr int AT_ONCE = 8;
-  int to[AT_ONCE];  // the first places, on their way while the row is
+  constexpr int AT_ONCE = HELD == 1 ? 8 : 0;
+  int to[8];  // the first places, on their way while the row is
   const int32_t* pos = p.pos + (size_t)row * p.top_k;
 #pragma unroll
   for (int j = 0; j < AT_ONCE; ++j) to[j] = in && p.pos != nullptr && j < p.top_k ? __ldg(pos + j) : -1;

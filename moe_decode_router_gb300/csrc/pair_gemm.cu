@@ -35,6 +35,11 @@
 // integers in registers.  fp32 outputs of bf16 operands are promoted the same way every 512 of the
 // contracted dimension: the tensor cores cut a sum instead of rounding it, which adds up.
 //
+// Where a dense product has units for few pairs alone, KS = 2 or 4 pairs of a cluster share a
+// unit's contraction.  Each leaves its sums in its stages, and after a cluster barrier adds its
+// part of the unit's columns over all of them, in the pairs' order: the result is the same on
+// every call.
+//
 // Warps: output (the first 8 or 16, a quarter of the lanes and a part of the columns each); then the
 // TMA producer; the MMA issuer (of the even CTA); rows behind the end; none; integers: four
 // and four that turn codes to fp16.
@@ -153,7 +158,7 @@ __device__ __forceinline__ void codes_to_f16(const uint4 c, uint4& lo, uint4& hi
   hi = make_uint4(o[4], o[5], o[6], o[7]);
 }
 
-template <int MODE, bool GATED, bool F32, bool INT8>
+template <int MODE, bool GATED, bool F32, bool INT8, int KS>
 __global__ void __launch_bounds__(Shape<F32 || INT8, INT8>::THREADS, 1)
     pair_gemm_kernel(const PairArgs p, const __grid_constant__ Maps maps) {
   constexpr int STAGES = INT8 ? TURNED : RING, BUFS = INT8 ? 1 : 2;
@@ -164,7 +169,9 @@ __global__ void __launch_bounds__(Shape<F32 || INT8, INT8>::THREADS, 1)
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   uint8_t* sm = smem_raw;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  const uint32_t rank = tc05::cluster_rank();
+  // of the cluster's pairs this one's contraction; of the pair this CTA's half
+  const uint32_t rank = tc05::cluster_rank() & 1u, lead = tc05::cluster_rank() & ~1u;
+  const int split = KS > 1 ? (int)(tc05::cluster_rank() >> 1) : 0;
   uint64_t* full = reinterpret_cast<uint64_t*>(sm + OFF_BARS);  // [STAGES] both CTAs' operands landed (even CTA's)
   uint64_t* empty = full + STAGES;                              // [STAGES] stage consumed
   uint64_t* landed = empty + STAGES;                            // [STAGES] weights: a last stage of this CTA landed;
@@ -191,6 +198,16 @@ __global__ void __launch_bounds__(Shape<F32 || INT8, INT8>::THREADS, 1)
     }
     *abort_flag = 0;
     fence_mbar_init();
+  }
+  if (tid == 32) {  // the copies' descriptors, on their way while the grid before this one ends
+    tc05::prefetch_map(&maps.a);
+    for (int i = 0; i < 4; ++i) tc05::prefetch_map(&maps.b[i]);
+    if (MODE == BACKWARD) {
+      tc05::prefetch_map(&maps.aw);
+      tc05::prefetch_map(&maps.bw);
+      tc05::prefetch_map(&maps.bw1);
+      tc05::prefetch_map(&maps.bw2);
+    }
   }
   pdl_wait();
   // Tensor memory is taken when the grid before this one is gone and (below) given back
@@ -238,7 +255,8 @@ __global__ void __launch_bounds__(Shape<F32 || INT8, INT8>::THREADS, 1)
   const uint32_t tmem = *tslot;
   const int n_rows_units = g_units[p.E];  // forward, input; behind them the weights'
   const int n_units = n_rows_units + (MODE == BACKWARD ? p.E * p.o_tiles * p.a_tiles : 0);
-  const int u0 = blockIdx.x >> 1, ustep = gridDim.x >> 1;
+  // with the contraction shared one unit alone (its operands' memory takes the sums)
+  const int u0 = blockIdx.x / (2 * KS), ustep = KS > 1 ? 1 << 30 : gridDim.x >> 1;
 
   // Few divisions: every role looks its units up, and a weights' unit may be three steps long.
   auto unit_of = [&](int u) -> Unit {
@@ -282,7 +300,18 @@ __global__ void __launch_bounds__(Shape<F32 || INT8, INT8>::THREADS, 1)
     t.n = max(32, (t.cnt + 31) & ~31);
     return t;
   };
-  auto steps_of = [&](const Unit& t) { return t.weights ? (t.clen + 63) >> 6 : p.steps; };
+  // this pair's steps of a unit
+  struct Steps {
+    int from, to, all;
+  };
+  auto steps_of = [&](const Unit& t) {
+    Steps s;
+    s.all = t.weights ? (t.clen + 63) >> 6 : p.steps;
+    const int share = (s.all + KS - 1) / KS;
+    s.from = KS > 1 ? min(split * share, s.all) : 0;
+    s.to = KS > 1 ? min(s.from + share, s.all) : s.all;
+    return s;
+  };
   // Bounded wait.  Lanes of a warp that wait together agree on the result: the awaited
   // phase cannot move on without a later arrival of this same warp.
   auto wait = [&](uint64_t* bar, uint32_t parity) -> bool {
@@ -295,7 +324,7 @@ __global__ void __launch_bounds__(Shape<F32 || INT8, INT8>::THREADS, 1)
   };
   // the smallest box of B that holds so many rows: 16 << box_of
   auto box_of = [](int rows) { return rows <= 16 ? 0 : rows <= 32 ? 1 : rows <= 64 ? 2 : 3; };
-  const uint32_t base = smem_u32(sm), full0 = tc05::map_rank(smem_u32(full), 0);
+  const uint32_t base = smem_u32(sm), full0 = tc05::map_rank(smem_u32(full), lead);
   if (warp >= W::OUT_WARPS) {
     if (PROMOTE) tc05::regs_down<W::LOW>();
     if (INT8 && warp == PRODUCER) {
@@ -306,7 +335,8 @@ __global__ void __launch_bounds__(Shape<F32 || INT8, INT8>::THREADS, 1)
         const Unit t = unit_of(u);
         const int nh = t.n >> 1, oh = t.o0 + (int)rank * nh, sel = box_of(nh);
         const uint32_t bytes = A_BYTES + (2048u << sel);
-        for (int k = 0; k < p.steps && lane == 0; ++k) {
+        const Steps steps = steps_of(t);
+        for (int k = steps.from; k < steps.to && lane == 0; ++k) {
           if (!wait(&taken[r], ph ^ 1)) {
             ok = false;
             break;
@@ -349,7 +379,8 @@ __global__ void __launch_bounds__(Shape<F32 || INT8, INT8>::THREADS, 1)
       for (int u = u0; u < n_units && ok; u += ustep) {
         const Unit t = unit_of(u);
         const int atoms = t.n >> 4;
-        for (int k = 0; k < p.steps; ++k) {
+        const Steps steps = steps_of(t);
+        for (int k = steps.from; k < steps.to; ++k) {
           ok = __all_sync(0xffffffffu, wait(&landed[r], rph)) && __all_sync(0xffffffffu, wait(&empty[s], ph ^ 1));
           if (!ok) break;
           const uint8_t* from = sm + r * STAGE;
@@ -411,12 +442,13 @@ __global__ void __launch_bounds__(Shape<F32 || INT8, INT8>::THREADS, 1)
       bool ok = true;
       for (int u = u0; u < n_units && ok; u += ustep) {
         const Unit t = unit_of(u);
-        const int nh = t.n >> 1, steps = steps_of(t);
+        const int nh = t.n >> 1;
+        const Steps steps = steps_of(t);
         const int i0 = t.at * 256 + (int)rank * 128, oh = t.o0 + (int)rank * nh;
         const int sel = box_of(nh), boxes = (nh + 63) >> 6;
         const bool both = p.pieces_n && nh == 128, one = p.pieces_n && nh == 64;  // weights: pieces of 64 columns of B
         const uint32_t bytes = A_BYTES + (t.weights ? (uint32_t)boxes * 8192u : 2048u << sel);
-        for (int k = 0; k < steps && lane == 0; ++k) {
+        for (int k = steps.from; k < steps.to && lane == 0; ++k) {
           if (!wait(&empty[s], ph ^ 1)) {
             ok = false;
             break;
@@ -425,7 +457,7 @@ __global__ void __launch_bounds__(Shape<F32 || INT8, INT8>::THREADS, 1)
           const uint32_t a = base + s * STAGE, b = a + A_BYTES;
           if (MODE == FORWARD) {
             if (rank == 0) mbar_arrive_expect_tx(&full[s], 2 * bytes);
-          } else if (t.weights && k == steps - 1 && (t.clen & 15)) {
+          } else if (t.weights && k == steps.all - 1 && (t.clen & 15)) {
             mbar_arrive_expect_tx(&landed[s], bytes);  // handed on by the warp that zeroes what lies behind the end
             bar = smem_u32(&landed[s]);
           } else {
@@ -483,21 +515,22 @@ __global__ void __launch_bounds__(Shape<F32 || INT8, INT8>::THREADS, 1)
         constexpr bool A_ROWS = MODE == BACKWARD;
         constexpr int SEG = INT8 ? SEG_INT : SEG_F32;
         constexpr uint32_t TFULL = (2 * STAGES + RING + CODES) * 8;
-        const uint32_t bars[2] = {full0, tc05::map_rank(smem_u32(full), 1)};  // of either CTA
+        const uint32_t bars[2] = {full0, tc05::map_rank(smem_u32(full), lead | 1u)};  // of either CTA
         const uint64_t da0 = A_ROWS ? tc05::sw128_rows_desc(base, 8192) : tc05::sw128_desc(base);
         const uint64_t db_k = tc05::sw128_desc(base + A_BYTES), db_w = tc05::sw128_rows_desc(base + A_BYTES, 8192);
         const uint64_t db8 = tc05::sw128_desc(base + CODES * STAGE);
         constexpr int DA = A_ROWS ? 128 : 2;  // 16 of the contracted dimension
         for (int u = u0; u < n_units && ok; u += ustep) {
           const Unit t = unit_of(u);
-          const int steps = steps_of(t);
+          const Steps steps = steps_of(t);
           const uint32_t idesc = tc05::idesc_f16(256, t.n, INT8 ? 0 : 1) | (A_ROWS ? tc05::A_ROWS_CONTIGUOUS : 0u) |
                                  (t.weights ? tc05::B_ROWS_CONTIGUOUS : 0u);
           const uint64_t db0 = t.weights ? db_w : db_k;
           const uint32_t DB = t.weights ? 128 : 2;
-          for (int k = 0; k < steps; ++k) {
-            const bool fresh = PROMOTE ? k % SEG == 0 : k == 0;
-            const bool last = k == steps - 1 || (PROMOTE && k % SEG == SEG - 1);
+          for (int k = steps.from; k < steps.to; ++k) {
+            const int at = k - steps.from;
+            const bool fresh = PROMOTE ? at % SEG == 0 : at == 0;
+            const bool last = k == steps.to - 1 || (PROMOTE && at % SEG == SEG - 1);
             const uint32_t b = v % BUFS, d = tmem + b * 256;
             // every lane waits, and all go on or none
             ok = !fresh || __all_sync(0xffffffffu, wait(&tempty[b], ((v / BUFS) & 1) ^ 1));
@@ -505,7 +538,7 @@ __global__ void __launch_bounds__(Shape<F32 || INT8, INT8>::THREADS, 1)
             if (!ok) break;
             tc05::fence_after_sync();
             const uint64_t da = da0 + s * (STAGE >> 4), db = db0 + s * (STAGE >> 4);
-            const int parts = t.weights && k == steps - 1 ? (((t.clen - 1) & 63) >> 4) + 1 : 4;
+            const int parts = t.weights && k == steps.all - 1 ? (((t.clen - 1) & 63) >> 4) + 1 : 4;
             const uint32_t more = fresh ? 0u : 1u, free0 = bars[0] + STAGES * 8 + s * 8, free1 = bars[1] + STAGES * 8 + s * 8;
             if (INT8) {
               tc05::mma_pair_ts(d, tmem + 256 + s * 64, db8 + 2 * s * (B_BYTES >> 4), idesc, more);
@@ -542,9 +575,9 @@ __global__ void __launch_bounds__(Shape<F32 || INT8, INT8>::THREADS, 1)
         bool ok = true;
         for (int u = u0; u < n_units && ok; u += ustep) {
           const Unit t = unit_of(u);
-          const int steps = steps_of(t);
-          g += steps;
-          if (!(t.clen & 15)) continue;  // 0 of what are not weights
+          const Steps steps = steps_of(t);
+          g += steps.to - steps.from;
+          if (!(t.clen & 15) || steps.from == steps.to || steps.to < steps.all) continue;  // clen: 0 of what are not weights
           const uint32_t s = (g - 1) % STAGES;
           ok = __all_sync(0xffffffffu, wait(&landed[s], (parity >> s) & 1));
           if (!ok) break;
@@ -560,13 +593,18 @@ __global__ void __launch_bounds__(Shape<F32 || INT8, INT8>::THREADS, 1)
         }
       }
     }
+    if constexpr (KS > 1) {  // the output warps' two barriers
+      __syncwarp();
+      tc05::cluster_sync();
+      tc05::cluster_sync();
+    }
   } else {
     if (PROMOTE) tc05::regs_up<W::HIGH>();
     // ---------------- output
     const int quad = warp & 3, part = warp >> 2;
     uint8_t* out = sm + OFF_OUT + warp * (OUT_BYTES / W::OUT_WARPS);
     const uint32_t lanes = tmem + ((uint32_t)(quad * 32) << 16);
-    const uint32_t tempty0 = tc05::map_rank(smem_u32(tempty), 0);
+    const uint32_t tempty0 = tc05::map_rank(smem_u32(tempty), lead);
     const int g = lane >> 2, q = lane & 3;
     uint32_t v = 0;
     bool ok = true;
@@ -576,28 +614,139 @@ __global__ void __launch_bounds__(Shape<F32 || INT8, INT8>::THREADS, 1)
       __syncwarp();
       if (lane == 0) tc05::arrive_cluster(tempty0 + b * 8);
     };
+    using S = typename Held<INT8>::type;
+    constexpr int CW = W::CHUNK, GROUPS = CW / 8;  // columns of a chunk, and groups of 8
+    // Puts out chunk c of the warp's part of unit t: its sums x, as tensor memory is read.  With the
+    // contraction shared every KS-th group is this pair's.
+    auto put_out = [&](const Unit& t, int c, const S* x) {
+      const int np = t.n / W::PARTS, first = part * np, live = min(np, t.cnt - first);
+      // first i of the warp's lanes (gated: of its 16 pairs), and the row of the output that o 0 of the unit is
+      const int i0 = GATED ? (t.at * 8 + (int)rank * 4 + quad) * 16 : t.at * 256 + (int)rank * 128 + quad * 32;
+      const size_t row0 = t.weights ? (size_t)t.e * p.O + t.o0 : (size_t)t.o0, row = row0 + first + CW * c;
+      void* to = t.weights ? p.dw : p.y;
+      const int left = live - CW * c;  // columns of the chunk that are outputs
+      auto mine = [&](int col) { return KS == 1 || (c * GROUPS + (col >> 3)) % KS == split; };
+      float r[CW];
+      if constexpr (INT8) {
+        float sw[4];  // scales of lanes g, g + 8, g + 16, g + 24
+        const float* w = p.sw + (size_t)t.e * p.I * (GATED ? 2 : 1);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const int n = i0 + g + 8 * (GATED ? i & 1 : i);
+          sw[i] = __ldg(w + min(n, p.I - 1) + (GATED && i >= 2 ? p.I : 0));
+        }
+#pragma unroll
+        for (int k = 0; k < GROUPS; ++k) {
+          float sx[2];
+#pragma unroll
+          for (int j = 0; j < 2; ++j) sx[j] = __ldg(p.sx + min(row + 8 * k + 2 * q + j, (size_t)p.M - 1));
+#pragma unroll
+          for (int j = 0; j < 8; ++j) {
+            const int at = (j >> 2) * (CW / 2) + 4 * k + (j & 3);
+            r[at] = (float)x[at] * (sx[j & 1] * sw[(j >> 2) * 2 + ((j >> 1) & 1)]);
+          }
+        }
+      } else {
+#pragma unroll
+        for (int i = 0; i < CW; ++i) r[i] = x[i];
+      }
+      auto f = [&](int h, int k, int j) { return r[CW / 2 * h + 4 * k + j]; };
+      if (GATED && F32) {
+        float* y = static_cast<float*>(p.y);
+#pragma unroll
+        for (int k = 0; k < GROUPS; ++k)
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            const int col = 8 * k + 2 * q + (j & 1), i = i0 + (j >> 1) * 8 + g;
+            if (mine(col) && col < left && i < p.I) y[(row + col) * p.I + i] = activation(f(0, k, j), p.act) * f(1, k, j);
+          }
+      } else if (GATED) {
+        // 16 i's x the chunk's columns, through shared memory: rows of 32 bytes
+        auto put = [&](uint16_t* to, size_t width, auto&& pair) {
+          const uint32_t st = smem_u32(out) + ((lane >> 4) * 8 + (lane & 7)) * 48 + ((lane >> 3) & 1) * 16;
+#pragma unroll
+          for (int k = 0; k < GROUPS; k += 2)
+            asm volatile("stmatrix.sync.aligned.m8n8.x4.trans.shared.b16 [%0], {%1, %2, %3, %4};" ::"r"(
+                             st + k * 8 * 48),
+                         "r"(pair(k, 0)), "r"(pair(k, 2)), "r"(pair(k + 1, 0)), "r"(pair(k + 1, 2))
+                         : "memory");
+          __syncwarp();
+#pragma unroll
+          for (int k = 0; k < GROUPS / 2; ++k) {
+            const int col = 16 * k + (lane >> 1);
+            if (mine(col) && col < left && i0 < p.I)
+              *reinterpret_cast<uint4*>(to + (row + col) * width + i0 + (lane & 1) * 8) =
+                  *reinterpret_cast<const uint4*>(out + col * 48 + (lane & 1) * 16);
+          }
+          __syncwarp();
+        };
+        if (p.keep != nullptr) {
+          put(p.keep, (size_t)2 * p.I, [&](int k, int j) { return bf16x2_bits(f(0, k, j), f(0, k, j + 1)); });
+          put(p.keep + p.I, (size_t)2 * p.I, [&](int k, int j) { return bf16x2_bits(f(1, k, j), f(1, k, j + 1)); });
+        }
+        put(static_cast<uint16_t*>(p.y), (size_t)p.I, [&](int k, int j) {
+          return bf16x2_bits(activation(f(0, k, j), p.act) * f(1, k, j),
+                             activation(f(0, k, j + 1), p.act) * f(1, k, j + 1));
+        });
+      } else if (F32 && (MODE == FORWARD || t.weights)) {
+        float* y = static_cast<float*>(to);
+#pragma unroll
+        for (int k = 0; k < GROUPS; ++k)
+#pragma unroll
+          for (int h = 0; h < 2; ++h)
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+              const int col = 8 * k + 2 * q + (j & 1), i = i0 + 16 * h + (j >> 1) * 8 + g;
+              if (mine(col) && col < left && i < p.I) y[(row + col) * p.I + i] = f(h, k, j);
+            }
+      } else {
+        uint16_t* y = static_cast<uint16_t*>(to);
+        const uint32_t st = smem_u32(out) + (lane & 7) * 80 + (lane >> 3) * 16;  // row lane % 8 of matrix lane / 8
+#pragma unroll
+        for (int k = 0; k < GROUPS; ++k)
+          asm volatile("stmatrix.sync.aligned.m8n8.x4.trans.shared.b16 [%0], {%1, %2, %3, %4};" ::"r"(st + k * 640),
+                       "r"(bf16x2_bits(f(0, k, 0), f(0, k, 1))), "r"(bf16x2_bits(f(0, k, 2), f(0, k, 3))),
+                       "r"(bf16x2_bits(f(1, k, 0), f(1, k, 1))), "r"(bf16x2_bits(f(1, k, 2), f(1, k, 3)))
+                       : "memory");
+        __syncwarp();
+        const int i = i0 + (lane & 3) * 8;
+#pragma unroll
+        for (int k = 0; k < GROUPS; ++k) {
+          const int col = 8 * k + (lane >> 2);
+          if (mine(col) && col < left && i < p.I) {  // the width is a multiple of 8
+            uint4* dst = reinterpret_cast<uint4*>(y + (row + col) * p.I + i);
+            const uint4 x = *reinterpret_cast<const uint4*>(out + col * 80 + (lane & 3) * 16);
+            if (t.weights) __stcs(dst, x);  // read again by no kernel soon: operands stay in L2
+            else *dst = x;
+          }
+        }
+        __syncwarp();
+      }
+    };
+    // Partial sums of a shared contraction: of register i of chunk c.
+    S* parts = reinterpret_cast<S*>(sm) + tid;
+    auto part_at = [&](int c, int i) { return (c * CW + i) * (W::OUT_WARPS * 32); };
     for (int u = u0; u < n_units && ok; u += ustep) {
       const Unit t = unit_of(u);
-      const int np = t.n / W::PARTS, first = part * np, steps = steps_of(t);
+      const int np = t.n / W::PARTS, first = part * np;
+      const Steps steps = steps_of(t);
       const int live = min(np, t.cnt - first);  // columns of this part that are outputs
-      using S = typename Held<INT8>::type;
-      constexpr int CHUNKS = 4;
-      S held[PROMOTE ? CHUNKS : 1][32];
       uint32_t b = 0;
       if constexpr (PROMOTE) {
+        S held[4][32];
 #pragma unroll
-        for (int c = 0; c < CHUNKS; ++c)
+        for (int c = 0; c < 4; ++c)
 #pragma unroll
           for (int i = 0; i < 32; ++i) held[c][i] = 0;
         constexpr int SEG = INT8 ? SEG_INT : SEG_F32;
-        for (int k = 0; k < steps; k += SEG) {
+        for (int k = steps.from; k < steps.to; k += SEG) {
           b = v % BUFS;
           ok = __all_sync(0xffffffffu, wait(&tfull[b], (v / BUFS) & 1));
           if (!ok) break;
           ++v;
           tc05::fence_after_sync();
 #pragma unroll
-          for (int c = 0; c < CHUNKS; ++c) {
+          for (int c = 0; c < 4; ++c) {
             if (32 * c < live) {
               uint32_t r[32];
               const uint32_t ta = lanes + b * 256 + (uint32_t)(first + 32 * c);
@@ -614,141 +763,85 @@ __global__ void __launch_bounds__(Shape<F32 || INT8, INT8>::THREADS, 1)
           give_back(b);
         }
         if (!ok) break;
-      } else if (steps > 0) {
-        b = v % BUFS;
-        ok = __all_sync(0xffffffffu, wait(&tfull[b], (v / BUFS) & 1));
-        if (!ok) break;
-        ++v;
-        tc05::fence_after_sync();
-      }
-      // first i of the warp's lanes (gated: of its 16 pairs), and the row of the output that o 0 of the unit is
-      const int i0 = GATED ? (t.at * 8 + (int)rank * 4 + quad) * 16 : t.at * 256 + (int)rank * 128 + quad * 32;
-      const size_t row0 = t.weights ? (size_t)t.e * p.O + t.o0 : (size_t)t.o0;
-      void* to = t.weights ? p.dw : p.y;
-      float sw[4] = {1.f, 1.f, 1.f, 1.f};  // integers: scales of lanes g, g + 8, g + 16, g + 24
-      if (INT8) {
-        const float* w = p.sw + (size_t)t.e * p.I * (GATED ? 2 : 1);
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const int n = i0 + g + 8 * (GATED ? i & 1 : i);
-          sw[i] = __ldg(w + min(n, p.I - 1) + (GATED && i >= 2 ? p.I : 0));
+        for (int c = 0; c < 4; ++c) {
+          if (32 * c >= live) break;
+          if constexpr (KS == 1) {
+            put_out(t, c, held[c]);
+          } else {
+#pragma unroll
+            for (int i = 0; i < 32; ++i) parts[part_at(c, i)] = held[c][i];
+          }
         }
-      }
-      // Chunk c of the accumulator, on its way to registers while the one before is put out.
-      constexpr int CW = W::CHUNK, GROUPS = CW / 8;  // groups of 8 columns
-      uint32_t next[PROMOTE ? 1 : 16];
-      auto fetch = [&](int c) {
-        if constexpr (!PROMOTE) {
-          if (steps > 0 && CW * c < live) {
+      } else {
+        const bool any = steps.from < steps.to;
+        if (any) {
+          b = v % BUFS;
+          ok = __all_sync(0xffffffffu, wait(&tfull[b], (v / BUFS) & 1));
+          if (!ok) break;
+          ++v;
+          tc05::fence_after_sync();
+        }
+        // Chunk c of the accumulator, on its way to registers while the one before is put out.
+        uint32_t next[16];
+        auto fetch = [&](int c) {
+          if (any && CW * c < live) {
             const uint32_t ta = lanes + b * 256 + (uint32_t)(first + CW * c);
             tc05::ld_16x256b_x2(ta, next);
             tc05::ld_16x256b_x2(ta + (16u << 16), next + 8);
           }
-        }
-      };
-      fetch(0);
+        };
+        fetch(0);
 #pragma unroll
-      for (int c = 0; c < 4; ++c) {
-        if (CW * c >= live) break;
-        uint32_t r[CW];
-        const size_t row = row0 + first + CW * c;
-        if constexpr (!PROMOTE) {
-          if (steps > 0) tc05::wait_ld16(next);
+        for (int c = 0; c < 4; ++c) {
+          if (CW * c >= live) break;
+          S x[CW];
+          if (any) tc05::wait_ld16(next);
 #pragma unroll
-          for (int i = 0; i < CW; ++i) r[i] = steps > 0 ? next[i] : 0u;
+          for (int i = 0; i < CW; ++i) x[i] = any ? __uint_as_float(next[i & 15]) : 0.f;
           fetch(c + 1);
-          if (steps > 0 && CW * (c + 1) >= live) give_back(b);
-        } else {
+          if (any && CW * (c + 1) >= live) give_back(b);
+          if constexpr (KS == 1) {
+            put_out(t, c, x);
+          } else {
 #pragma unroll
-          for (int k = 0; k < 4; ++k) {
-            float sx[2] = {1.f, 1.f};
-            if (INT8) {
-#pragma unroll
-              for (int j = 0; j < 2; ++j) sx[j] = __ldg(p.sx + min(row + 8 * k + 2 * q + j, (size_t)p.M - 1));
-            }
-#pragma unroll
-            for (int j = 0; j < 8; ++j) {
-              const int at = (j >> 2) * 16 + 4 * k + (j & 3);
-              const float x = (float)held[c][at];
-              r[at] = __float_as_uint(INT8 ? x * (sx[j & 1] * sw[(j >> 2) * 2 + ((j >> 1) & 1)]) : x);
-            }
+            for (int i = 0; i < CW; ++i) parts[part_at(c, i)] = x[i];
           }
         }
-        const int left = live - CW * c;  // columns of the chunk that are outputs
-        auto f = [&](int h, int k, int j) { return __uint_as_float(r[CW / 2 * h + 4 * k + j]); };
-        if (GATED && F32) {
-          float* y = static_cast<float*>(p.y);
+        if (any && live <= 0) give_back(b);
+      }
+    }
+    if constexpr (KS > 1) {
+      __syncwarp();
+      tc05::cluster_sync();  // every pair's sums are there
+      if (u0 < n_units) {
+        const Unit t = unit_of(u0);
+        const int live = min(t.n / W::PARTS, t.cnt - part * (t.n / W::PARTS));
+#pragma unroll 1
+        for (int c = 0; CW * c < live; ++c) {
+          S x[CW];
 #pragma unroll
-          for (int k = 0; k < GROUPS; ++k)
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-              const int col = 8 * k + 2 * q + (j & 1), i = i0 + (j >> 1) * 8 + g;
-              if (col < left && i < p.I) y[(row + col) * p.I + i] = activation(f(0, k, j), p.act) * f(1, k, j);
-            }
-        } else if (GATED) {
-          // 16 i's x the chunk's columns, through shared memory: rows of 32 bytes
-          auto put = [&](uint16_t* to, size_t width, auto&& pair) {
-            const uint32_t st = smem_u32(out) + ((lane >> 4) * 8 + (lane & 7)) * 48 + ((lane >> 3) & 1) * 16;
-#pragma unroll
-            for (int k = 0; k < GROUPS; k += 2)
-              asm volatile("stmatrix.sync.aligned.m8n8.x4.trans.shared.b16 [%0], {%1, %2, %3, %4};" ::"r"(
-                               st + k * 8 * 48),
-                           "r"(pair(k, 0)), "r"(pair(k, 2)), "r"(pair(k + 1, 0)), "r"(pair(k + 1, 2))
-                           : "memory");
-            __syncwarp();
-#pragma unroll
-            for (int k = 0; k < GROUPS / 2; ++k) {
-              const int col = 16 * k + (lane >> 1);
-              if (col < left && i0 < p.I)
-                *reinterpret_cast<uint4*>(to + (row + col) * width + i0 + (lane & 1) * 8) =
-                    *reinterpret_cast<const uint4*>(out + col * 48 + (lane & 1) * 16);
-            }
-            __syncwarp();
-          };
-          if (p.keep != nullptr) {
-            put(p.keep, (size_t)2 * p.I, [&](int k, int j) { return bf16x2_bits(f(0, k, j), f(0, k, j + 1)); });
-            put(p.keep + p.I, (size_t)2 * p.I, [&](int k, int j) { return bf16x2_bits(f(1, k, j), f(1, k, j + 1)); });
-          }
-          put(static_cast<uint16_t*>(p.y), (size_t)p.I, [&](int k, int j) {
-            return bf16x2_bits(activation(f(0, k, j), p.act) * f(1, k, j),
-                               activation(f(0, k, j + 1), p.act) * f(1, k, j + 1));
-          });
-        } else if (F32 && (MODE == FORWARD || t.weights)) {
-          float* y = static_cast<float*>(to);
-#pragma unroll
-          for (int k = 0; k < GROUPS; ++k)
-#pragma unroll
-            for (int h = 0; h < 2; ++h)
-#pragma unroll
-              for (int j = 0; j < 4; ++j) {
-                const int col = 8 * k + 2 * q + (j & 1), i = i0 + 16 * h + (j >> 1) * 8 + g;
-                if (col < left && i < p.I) y[(row + col) * p.I + i] = f(h, k, j);
-              }
-        } else {
-          uint16_t* y = static_cast<uint16_t*>(to);
-          const uint32_t st = smem_u32(out) + (lane & 7) * 80 + (lane >> 3) * 16;  // row lane % 8 of matrix lane / 8
-#pragma unroll
-          for (int k = 0; k < GROUPS; ++k)
-            asm volatile("stmatrix.sync.aligned.m8n8.x4.trans.shared.b16 [%0], {%1, %2, %3, %4};" ::"r"(st + k * 640),
-                         "r"(bf16x2_bits(f(0, k, 0), f(0, k, 1))), "r"(bf16x2_bits(f(0, k, 2), f(0, k, 3))),
-                         "r"(bf16x2_bits(f(1, k, 0), f(1, k, 1))), "r"(bf16x2_bits(f(1, k, 2), f(1, k, 3)))
-                         : "memory");
-          __syncwarp();
-          const int i = i0 + (lane & 3) * 8;
+          for (int i = 0; i < CW; ++i) x[i] = 0;
 #pragma unroll
           for (int k = 0; k < GROUPS; ++k) {
-            const int col = 8 * k + (lane >> 2);
-            if (col < left && i < p.I) {  // the width is a multiple of 8
-              uint4* dst = reinterpret_cast<uint4*>(y + (row + col) * p.I + i);
-              const uint4 x = *reinterpret_cast<const uint4*>(out + col * 80 + (lane & 3) * 16);
-              if (t.weights) __stcs(dst, x);  // read again by no kernel soon: operands stay in L2
-              else *dst = x;
+            if ((c * GROUPS + k) % KS != split) continue;
+#pragma unroll
+            for (int j = 0; j < KS; ++j) {
+              const uint32_t from = tc05::map_rank(smem_u32(parts), 2 * j + rank);
+#pragma unroll
+              for (int i = 0; i < 8; ++i) {
+                const int at = (i >> 2) * (CW / 2) + 4 * k + (i & 3);
+                uint32_t word;
+                asm volatile("ld.shared::cluster.b32 %0, [%1];" : "=r"(word) : "r"(from + (uint32_t)part_at(c, at) * 4u) : "memory");
+                x[at] += *reinterpret_cast<const S*>(&word);
+              }
             }
           }
-          __syncwarp();
+          put_out(t, c, x);
         }
       }
-      if (!PROMOTE && steps > 0 && live <= 0) give_back(b);
+      __syncwarp();
+      tc05::cluster_sync();  // the other pairs have read this one's
     }
   }
   __syncwarp();
@@ -782,11 +875,11 @@ bool encode(CUtensorMap* m, int size, const void* base, std::initializer_list<ui
                   CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-template <int MODE, bool GATED, bool F32, bool INT8 = false>
-cudaError_t launch(const PairArgs& p, const Maps& maps, long long most, int sm_count, cudaStream_t st) {
-  const int pairs = sm_count / 2;
+template <int MODE, bool GATED, bool F32, bool INT8, int KS>
+cudaError_t launch_split(const PairArgs& p, const Maps& maps, long long most, int sm_count, cudaStream_t st) {
+  const long long pairs = KS > 1 ? most : sm_count / 2;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(2u * (unsigned)(most < pairs ? most : pairs));
+  cfg.gridDim = dim3(2u * KS * (unsigned)(most < pairs ? most : pairs));
   cfg.blockDim = dim3(Shape<F32 || INT8, INT8>::THREADS);
   cfg.dynamicSmemBytes = pair_smem(p.E);
   cfg.stream = st;
@@ -794,12 +887,18 @@ cudaError_t launch(const PairArgs& p, const Maps& maps, long long most, int sm_c
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   attr[1].id = cudaLaunchAttributeClusterDimension;
-  attr[1].val.clusterDim.x = 2;
+  attr[1].val.clusterDim.x = 2 * KS;
   attr[1].val.clusterDim.y = 1;
   attr[1].val.clusterDim.z = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 2;
-  return cudaLaunchKernelEx(&cfg, pair_gemm_kernel<MODE, GATED, F32, INT8>, p, maps);
+  return cudaLaunchKernelEx(&cfg, pair_gemm_kernel<MODE, GATED, F32, INT8, KS>, p, maps);
+}
+template <int MODE, bool GATED, bool F32, bool INT8 = false>
+cudaError_t launch(const PairArgs& p, const Maps& maps, int ks, long long most, int sm_count, cudaStream_t st) {
+  if (ks == 4) return launch_split<MODE, GATED, F32, INT8, 4>(p, maps, most, sm_count, st);
+  if (ks == 2) return launch_split<MODE, GATED, F32, INT8, 2>(p, maps, most, sm_count, st);
+  return launch_split<MODE, GATED, F32, INT8, 1>(p, maps, most, sm_count, st);
 }
 
 // Tiles of rows that a grouped (or dense) product may have, at most.
@@ -820,46 +919,63 @@ long long unit_ns(long long steps, int n, int least) {
   return steps * (by_columns > least ? by_columns : least) + 3000 + 10 * n;
 }
 
-// Tile of a dense product's rows, so that the units fill the pairs of SMs evenly.
-int choose_tile(int M, long long a_tiles, long long steps, int pairs) {
-  int best = 256;
+// Clusters of KS pairs that run at a time: a pair has two neighbouring SMs, and a cluster lies in
+// one of the GPU's parts of 18 to 20 SMs.
+long long clusters_of(int ks, int pairs) { return ks == 4 ? pairs / 5 : ks == 2 ? pairs * 2 / 5 : pairs; }
+// What joining a shared contraction takes.
+long long join_ns(int ks) { return ks > 1 ? 1500 : 0; }
+
+struct Plan {
+  int tile, tile_w, ks;
+};
+
+// Tile of a dense product's rows, and pairs that share its contraction, so that the units fill the
+// pairs of SMs evenly.
+Plan plan_forward(int M, long long a_tiles, long long steps, int pairs) {
+  Plan best = {256, 256, 1};
   long long least = -1;
-  for (int tile = 256; tile >= 32; tile -= 32) {
-    const long long units = (M + tile - 1LL) / tile * a_tiles;
-    const long long c = (units + pairs - 1) / pairs * unit_ns(steps, M < tile ? (M + 31) & ~31 : tile, STEP_FORWARD);
-    if (least < 0 || c < least) {
-      least = c;
-      best = tile;
+  for (int ks = 1; ks <= 4; ks *= 2)
+    for (int tile = 256; tile >= 32; tile -= 32) {
+      const long long units = (M + tile - 1LL) / tile * a_tiles, room = clusters_of(ks, pairs);
+      if (ks > 1 && (units > room || steps < 4 * ks)) continue;
+      const int n = M < tile ? (M + 31) & ~31 : tile;
+      const long long c = (units + room - 1) / room * (unit_ns((steps + ks - 1) / ks, n, STEP_FORWARD) + join_ns(ks));
+      if (least < 0 || c < least) {
+        least = c;
+        best = {tile, 256, ks};
+      }
     }
-  }
   return best;
 }
 
 // The same for both gradients in one launch: units of dx first, then of dw, dealt out in turn.
-void choose_tiles(PairArgs& p, bool dx, bool dw, int pairs) {
-  const long long rows_steps = (p.M + 63) / 64;
+Plan plan_backward(int M, int N, long long a_tiles, bool dx, bool dw, int pairs) {
+  const long long dx_steps = (N + 63) / 64, dw_steps = (M + 63) / 64;
+  Plan best = {256, 256, 1};
   long long least = -1;
-  int best = 256, best_w = 256;
-  for (int tile = 256; tile >= (dx ? 64 : 256); tile -= 32)
-    for (int tile_w = 256; tile_w >= (dw ? 128 : 256); tile_w -= 128) {  // whole pieces of 64 columns
-      const long long a = dx ? (p.M + tile - 1LL) / tile * p.a_tiles : 0, ca = unit_ns(p.steps, tile, STEP_INPUT);
-      const long long b = dw ? (p.O + tile_w - 1LL) / tile_w * p.a_tiles : 0, cb = unit_ns(rows_steps, tile_w, STEP_WEIGHTS);
-      const long long edge = a % pairs, end = (a + b) % pairs;  // pairs below an edge have one unit more
-      long long most = 0;
-      for (long long q : {0LL, edge, end}) {
-        if (q >= pairs) continue;
-        const long long na = a / pairs + (q < edge), n = (a + b) / pairs + (q < end);
-        const long long c = na * ca + (n - na) * cb;
-        if (c > most) most = c;
+  for (int ks = 1; ks <= 4; ks *= 2)
+    for (int tile = 256; tile >= (dx ? 64 : 256); tile -= 32)
+      for (int tile_w = 256; tile_w >= (dw ? 128 : 256); tile_w -= 128) {  // whole pieces of 64 columns
+        const long long a = dx ? (M + tile - 1LL) / tile * a_tiles : 0, b = dw ? (N + tile_w - 1LL) / tile_w * a_tiles : 0;
+        const long long room = clusters_of(ks, pairs);
+        if (ks > 1 && (a + b > room || (dx ? dx_steps : 0) + (dw ? dw_steps : 0) < 8 * ks)) continue;
+        const int n = M < tile ? (M + 31) & ~31 : tile;
+        const long long ca = unit_ns((dx_steps + ks - 1) / ks, n, STEP_INPUT) + join_ns(ks);
+        const long long cb = unit_ns((dw_steps + ks - 1) / ks, tile_w, STEP_WEIGHTS) + join_ns(ks);
+        const long long edge = a % room, end = (a + b) % room;  // pairs below an edge have one unit more
+        long long most = 0;
+        for (long long q : {0LL, edge, end}) {
+          if (q >= room) continue;
+          const long long na = a / room + (q < edge), all = (a + b) / room + (q < end);
+          const long long c = na * ca + (all - na) * cb;
+          if (c > most) most = c;
+        }
+        if (least < 0 || most < least) {
+          least = most;
+          best = {tile, tile_w, ks};
+        }
       }
-      if (least < 0 || most < least) {
-        least = most;
-        best = tile;
-        best_w = tile_w;
-      }
-    }
-  p.tile = best;
-  p.tile_w = best_w;
+  return best;
 }
 
 bool encode_rows(Maps& m, int size, const void* x, uint64_t rows, uint64_t K) {
@@ -879,18 +995,22 @@ cudaError_t pair_gemm_kernels_init() {
     if (q != cudaDriverEntryPointSuccess || fn == nullptr) return cudaErrorNotSupported;
     g_encode = reinterpret_cast<EncodeTiled>(fn);
   }
+#define PAIR_KERNELS(ks)                                                                               \
+  {reinterpret_cast<const void*>(pair_gemm_kernel<FORWARD, true, false, false, ks>), 0},               \
+      {reinterpret_cast<const void*>(pair_gemm_kernel<FORWARD, false, false, false, ks>), 0},          \
+      {reinterpret_cast<const void*>(pair_gemm_kernel<BACKWARD, false, false, false, ks>), 0},         \
+      {reinterpret_cast<const void*>(pair_gemm_kernel<FORWARD, false, true, false, ks>), LAUNCH},      \
+      {reinterpret_cast<const void*>(pair_gemm_kernel<BACKWARD, false, true, false, ks>), LAUNCH},     \
+      {reinterpret_cast<const void*>(pair_gemm_kernel<FORWARD, false, false, true, ks>), LAUNCH_INT},  \
+      {reinterpret_cast<const void*>(pair_gemm_kernel<FORWARD, false, true, true, ks>), LAUNCH_INT},   \
+      {reinterpret_cast<const void*>(pair_gemm_kernel<FORWARD, true, false, true, ks>), LAUNCH_INT},   \
+      {reinterpret_cast<const void*>(pair_gemm_kernel<FORWARD, true, true, true, ks>), LAUNCH_INT}
+  constexpr int LAUNCH = Shape<true, false>::LAUNCH, LAUNCH_INT = Shape<true, true>::LAUNCH;
   const struct {
     const void* f;
     int regs;  // that its shares are counted from
-  } k[] = {{reinterpret_cast<const void*>(pair_gemm_kernel<FORWARD, true, false, false>), 0},
-           {reinterpret_cast<const void*>(pair_gemm_kernel<FORWARD, false, false, false>), 0},
-           {reinterpret_cast<const void*>(pair_gemm_kernel<BACKWARD, false, false, false>), 0},
-           {reinterpret_cast<const void*>(pair_gemm_kernel<FORWARD, false, true, false>), Shape<true, false>::LAUNCH},
-           {reinterpret_cast<const void*>(pair_gemm_kernel<BACKWARD, false, true, false>), Shape<true, false>::LAUNCH},
-           {reinterpret_cast<const void*>(pair_gemm_kernel<FORWARD, false, false, true>), Shape<true, true>::LAUNCH},
-           {reinterpret_cast<const void*>(pair_gemm_kernel<FORWARD, false, true, true>), Shape<true, true>::LAUNCH},
-           {reinterpret_cast<const void*>(pair_gemm_kernel<FORWARD, true, false, true>), Shape<true, true>::LAUNCH},
-           {reinterpret_cast<const void*>(pair_gemm_kernel<FORWARD, true, true, true>), Shape<true, true>::LAUNCH}};
+  } k[] = {PAIR_KERNELS(1), PAIR_KERNELS(2), PAIR_KERNELS(4)};
+#undef PAIR_KERNELS
   for (const auto& x : k) {
     cudaError_t e = cudaFuncSetAttribute(x.f, cudaFuncAttributeMaxDynamicSharedMemorySize, pair_smem(ROUTE_MAX_E));
     if (e != cudaSuccess) return e;
@@ -916,7 +1036,8 @@ cudaError_t launch_pair_forward(const ProductArgs& a, bool int8, int sm_count, u
   p.I = gated ? a.N / 2 : a.N;
   p.steps = int8 ? (a.K + 127) / 128 : (a.K + 63) / 64;
   p.a_tiles = (a.N + 255) / 256;
-  p.tile = a.offsets == nullptr ? choose_tile(a.M, p.a_tiles, (a.K + 63) / 64, sm_count / 2) : 256;
+  const Plan plan = a.offsets == nullptr ? plan_forward(a.M, p.a_tiles, (a.K + 63) / 64, sm_count / 2) : Plan{256, 256, 1};
+  p.tile = plan.tile;
   p.act = a.act;
   p.row_tiles = (a.M + p.tile - 1) / p.tile;
   p.per_band = reciprocal(BAND * p.a_tiles);
@@ -930,14 +1051,14 @@ cudaError_t launch_pair_forward(const ProductArgs& a, bool int8, int sm_count, u
   m.aw = m.bw = m.bw1 = m.bw2 = m.a;
   const long long most = row_tiles(a.M, a.E, a.offsets != nullptr, p.tile) * p.a_tiles;
   if (int8) {
-    if (gated) return a.f32 ? launch<FORWARD, true, true, true>(p, m, most, sm_count, st)
-                            : launch<FORWARD, true, false, true>(p, m, most, sm_count, st);
-    return a.f32 ? launch<FORWARD, false, true, true>(p, m, most, sm_count, st)
-                 : launch<FORWARD, false, false, true>(p, m, most, sm_count, st);
+    if (gated) return a.f32 ? launch<FORWARD, true, true, true>(p, m, plan.ks, most, sm_count, st)
+                            : launch<FORWARD, true, false, true>(p, m, plan.ks, most, sm_count, st);
+    return a.f32 ? launch<FORWARD, false, true, true>(p, m, plan.ks, most, sm_count, st)
+                 : launch<FORWARD, false, false, true>(p, m, plan.ks, most, sm_count, st);
   }
-  if (gated) return launch<FORWARD, true, false>(p, m, most, sm_count, st);
-  return a.f32 ? launch<FORWARD, false, true>(p, m, most, sm_count, st)
-               : launch<FORWARD, false, false>(p, m, most, sm_count, st);
+  if (gated) return launch<FORWARD, true, false>(p, m, plan.ks, most, sm_count, st);
+  return a.f32 ? launch<FORWARD, false, true>(p, m, plan.ks, most, sm_count, st)
+               : launch<FORWARD, false, false>(p, m, plan.ks, most, sm_count, st);
 }
 
 cudaError_t launch_pair_backward(const GradArgs& a, int sm_count, unsigned* err, cudaStream_t st) {
@@ -953,10 +1074,12 @@ cudaError_t launch_pair_backward(const GradArgs& a, int sm_count, unsigned* err,
   p.O = a.N;
   p.steps = (a.N + 63) / 64;
   p.a_tiles = (a.K + 255) / 256;
-  p.tile = p.tile_w = 256;
   p.pieces_k = a.K % 64 == 0;
   p.pieces_n = a.N % 64 == 0;
-  if (a.offsets == nullptr) choose_tiles(p, a.dx != nullptr, a.dw != nullptr, sm_count / 2);
+  const Plan plan = a.offsets == nullptr ? plan_backward(a.M, a.N, p.a_tiles, a.dx != nullptr, a.dw != nullptr, sm_count / 2)
+                                         : Plan{256, 256, 1};
+  p.tile = plan.tile;
+  p.tile_w = plan.tile_w;
   if (a.dw != nullptr) p.o_tiles = (a.N + p.tile_w - 1) / p.tile_w;
   p.row_tiles = (a.M + p.tile - 1) / p.tile;
   p.per_band = reciprocal(BAND * p.a_tiles);
@@ -975,8 +1098,8 @@ cudaError_t launch_pair_backward(const GradArgs& a, int sm_count, unsigned* err,
   if (!ok) return cudaErrorInvalidValue;
   long long most = (long long)a.E * p.o_tiles * p.a_tiles;
   if (a.dx != nullptr) most += row_tiles(a.M, a.E, a.offsets != nullptr, p.tile) * p.a_tiles;
-  return a.f32 ? launch<BACKWARD, false, true>(p, m, most, sm_count, st)
-               : launch<BACKWARD, false, false>(p, m, most, sm_count, st);
+  return a.f32 ? launch<BACKWARD, false, true>(p, m, plan.ks, most, sm_count, st)
+               : launch<BACKWARD, false, false>(p, m, plan.ks, most, sm_count, st);
 }
 
 }  // namespace flint

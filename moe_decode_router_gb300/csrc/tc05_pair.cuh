@@ -130,6 +130,9 @@ __device__ __forceinline__ void commit_pair(uint32_t cluster_addr) {
       : "memory");
 }
 
+__device__ __forceinline__ void prefetch_map(const CUtensorMap* map) {
+  asm volatile("prefetch.tensormap [%0];" ::"l"(map) : "memory");
+}
 // Copies of a tile into this CTA's shared memory, counted on an mbarrier of either CTA of the pair.
 __device__ __forceinline__ void tma_pair_2d(uint32_t dst, const CUtensorMap* map, int x, int y, uint32_t bar) {
   asm volatile(
