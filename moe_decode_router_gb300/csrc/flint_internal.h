@@ -210,6 +210,7 @@ struct GradArgs {
 };
 // tcgen05 over pairs of CTAs (pair_gemm.cu)
 cudaError_t pair_gemm_kernels_init();
+bool few_rows_take(const ProductArgs& p, bool int8, int sm_count);  // rather than launch_pair_forward
 cudaError_t launch_pair_forward(const ProductArgs& p, bool int8, int sm_count, unsigned* err, cudaStream_t st);
 cudaError_t launch_pair_backward(const GradArgs& p, int sm_count, unsigned* err, cudaStream_t st);
 // Rows to 8-bit integers with one scale each (integer_rows.cu)

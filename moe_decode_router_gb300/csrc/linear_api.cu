@@ -92,7 +92,7 @@ int product(const ProductArgs& p, bool int8, flint_moe_stream_t stream) {
   const int rc = set_up(&d);
   if (rc != FLINT_MOE_OK) return rc;
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
-  if (p.M <= 8 || (p.offsets != nullptr && p.M <= 8LL * p.E)) return to_status(launch_few_rows(p, int8, st));
+  if (few_rows_take(p, int8, d.sms)) return to_status(launch_few_rows(p, int8, st));
   return to_status(launch_pair_forward(p, int8, d.sms, d.err, st));
 }
 

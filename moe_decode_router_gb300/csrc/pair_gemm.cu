@@ -912,12 +912,16 @@ long long row_tiles(int M, int E, bool grouped, int tile) {
 //   forward    287  234  201  201  199     below 160 columns the way of a stage through the ring
 //   input      289  250  241  241  239
 //   weights    285    -  304  304    -
-// and a unit's start and end, where nothing else covers them, some 3,000 + 10 n.
-enum { STEP_FORWARD = 200, STEP_INPUT = 240, STEP_WEIGHTS = 285 };
-long long unit_ns(long long steps, int n, int least) {
-  const int by_columns = n * 9 / 8;
-  return steps * (by_columns > least ? by_columns : least) + 3000 + 10 * n;
+//   integers   512    -    -    -  370
+// A unit takes its steps, or its way out; a launch 4.5 us and the last unit's way out besides.
+enum Kind { K_FORWARD, K_INPUT, K_WEIGHTS, K_INTEGERS };
+long long unit_ns(long long steps, int n, Kind kind) {
+  constexpr int LEAST[] = {200, 240, 285, 370};
+  const int by_columns = kind == K_INTEGERS ? 228 + n * 10 / 9 : 75 + n * 5 / 6;
+  const long long loop = steps * (by_columns > LEAST[kind] ? by_columns : LEAST[kind]), out = 5 * n;
+  return loop > out ? loop : out;
 }
+long long launch_ns(int n) { return 4500 + 8 * n; }
 
 // Clusters of KS pairs that run at a time: a pair has two neighbouring SMs, and a cluster lies in
 // one of the GPU's parts of 18 to 20 SMs.
@@ -927,32 +931,29 @@ long long join_ns(int ks) { return ks > 1 ? 1500 : 0; }
 
 struct Plan {
   int tile, tile_w, ks;
+  long long ns;
 };
 
 // Tile of a dense product's rows, and pairs that share its contraction, so that the units fill the
 // pairs of SMs evenly.
-Plan plan_forward(int M, long long a_tiles, long long steps, int pairs) {
-  Plan best = {256, 256, 1};
-  long long least = -1;
+Plan plan_forward(int M, long long a_tiles, long long steps, bool int8, int pairs) {
+  Plan best = {256, 256, 1, -1};
   for (int ks = 1; ks <= 4; ks *= 2)
     for (int tile = 256; tile >= 32; tile -= 32) {
       const long long units = (M + tile - 1LL) / tile * a_tiles, room = clusters_of(ks, pairs);
       if (ks > 1 && (units > room || steps < 4 * ks)) continue;
       const int n = M < tile ? (M + 31) & ~31 : tile;
-      const long long c = (units + room - 1) / room * (unit_ns((steps + ks - 1) / ks, n, STEP_FORWARD) + join_ns(ks));
-      if (least < 0 || c < least) {
-        least = c;
-        best = {tile, 256, ks};
-      }
+      const long long c = (units + room - 1) / room * unit_ns((steps + ks - 1) / ks, n, int8 ? K_INTEGERS : K_FORWARD) +
+                          launch_ns(n) + join_ns(ks);
+      if (best.ns < 0 || c < best.ns) best = {tile, 256, ks, c};
     }
   return best;
 }
 
-// The same for both gradients in one launch: units of dx first, then of dw, dealt out in turn.
+// The same for both gradients in one launch (or one alone): units of dx first, then of dw, dealt out in turn.
 Plan plan_backward(int M, int N, long long a_tiles, bool dx, bool dw, int pairs) {
   const long long dx_steps = (N + 63) / 64, dw_steps = (M + 63) / 64;
-  Plan best = {256, 256, 1};
-  long long least = -1;
+  Plan best = {256, 256, 1, -1};
   for (int ks = 1; ks <= 4; ks *= 2)
     for (int tile = 256; tile >= (dx ? 64 : 256); tile -= 32)
       for (int tile_w = 256; tile_w >= (dw ? 128 : 256); tile_w -= 128) {  // whole pieces of 64 columns
@@ -960,8 +961,8 @@ Plan plan_backward(int M, int N, long long a_tiles, bool dx, bool dw, int pairs)
         const long long room = clusters_of(ks, pairs);
         if (ks > 1 && (a + b > room || (dx ? dx_steps : 0) + (dw ? dw_steps : 0) < 8 * ks)) continue;
         const int n = M < tile ? (M + 31) & ~31 : tile;
-        const long long ca = unit_ns((dx_steps + ks - 1) / ks, n, STEP_INPUT) + join_ns(ks);
-        const long long cb = unit_ns((dw_steps + ks - 1) / ks, tile_w, STEP_WEIGHTS) + join_ns(ks);
+        const long long ca = unit_ns((dx_steps + ks - 1) / ks, n, K_INPUT);
+        const long long cb = unit_ns((dw_steps + ks - 1) / ks, tile_w, K_WEIGHTS);
         const long long edge = a % room, end = (a + b) % room;  // pairs below an edge have one unit more
         long long most = 0;
         for (long long q : {0LL, edge, end}) {
@@ -970,10 +971,8 @@ Plan plan_backward(int M, int N, long long a_tiles, bool dx, bool dw, int pairs)
           const long long c = na * ca + (all - na) * cb;
           if (c > most) most = c;
         }
-        if (least < 0 || most < least) {
-          least = most;
-          best = {tile, tile_w, ks};
-        }
+        most += launch_ns(dw ? tile_w : n) + join_ns(ks);
+        if (best.ns < 0 || most < best.ns) best = {tile, tile_w, ks, most};
       }
   return best;
 }
@@ -1036,7 +1035,8 @@ cudaError_t launch_pair_forward(const ProductArgs& a, bool int8, int sm_count, u
   p.I = gated ? a.N / 2 : a.N;
   p.steps = int8 ? (a.K + 127) / 128 : (a.K + 63) / 64;
   p.a_tiles = (a.N + 255) / 256;
-  const Plan plan = a.offsets == nullptr ? plan_forward(a.M, p.a_tiles, (a.K + 63) / 64, sm_count / 2) : Plan{256, 256, 1};
+  const Plan plan = a.offsets == nullptr ? plan_forward(a.M, p.a_tiles, (a.K + 63) / 64, int8, sm_count / 2)
+                                         : Plan{256, 256, 1, 0};
   p.tile = plan.tile;
   p.act = a.act;
   p.row_tiles = (a.M + p.tile - 1) / p.tile;
@@ -1061,7 +1061,9 @@ cudaError_t launch_pair_forward(const ProductArgs& a, bool int8, int sm_count, u
                : launch<FORWARD, false, false>(p, m, plan.ks, most, sm_count, st);
 }
 
-cudaError_t launch_pair_backward(const GradArgs& a, int sm_count, unsigned* err, cudaStream_t st) {
+namespace {
+
+cudaError_t launch_backward(const GradArgs& a, const Plan& plan, int sm_count, unsigned* err, cudaStream_t st) {
   const uint64_t M = a.M, N = a.N, K = a.K, E = a.E;
   PairArgs p = {};
   p.offsets = a.offsets;
@@ -1076,8 +1078,6 @@ cudaError_t launch_pair_backward(const GradArgs& a, int sm_count, unsigned* err,
   p.a_tiles = (a.K + 255) / 256;
   p.pieces_k = a.K % 64 == 0;
   p.pieces_n = a.N % 64 == 0;
-  const Plan plan = a.offsets == nullptr ? plan_backward(a.M, a.N, p.a_tiles, a.dx != nullptr, a.dw != nullptr, sm_count / 2)
-                                         : Plan{256, 256, 1};
   p.tile = plan.tile;
   p.tile_w = plan.tile_w;
   if (a.dw != nullptr) p.o_tiles = (a.N + p.tile_w - 1) / p.tile_w;
@@ -1102,4 +1102,63 @@ cudaError_t launch_pair_backward(const GradArgs& a, int sm_count, unsigned* err,
                : launch<BACKWARD, false, false>(p, m, plan.ks, most, sm_count, st);
 }
 
+}  // namespace
+
+cudaError_t launch_pair_backward(const GradArgs& a, int sm_count, unsigned* err, cudaStream_t st) {
+  const int a_tiles = (a.K + 255) / 256, pairs = sm_count / 2;
+  const bool dx = a.dx != nullptr, dw = a.dw != nullptr;
+  if (a.offsets != nullptr) return launch_backward(a, Plan{256, 256, 1, 0}, sm_count, err, st);
+  const Plan plan = plan_backward(a.M, a.N, a_tiles, dx, dw, pairs);
+  if (dx && dw) {
+    // Long units of one and short ones of the other fill a launch badly: 16 rows of 8192 x 2048 take 43
+    // us in one and 28 in two, each with its own share of the contraction a cluster.
+    const Plan one = plan_backward(a.M, a.N, a_tiles, true, false, pairs), two = plan_backward(a.M, a.N, a_tiles, false, true, pairs);
+    if (one.ns + two.ns < plan.ns) {
+      GradArgs g = a;
+      g.dw = nullptr;
+      const cudaError_t e = launch_backward(g, one, sm_count, err, st);
+      if (e != cudaSuccess) return e;
+      g.dw = a.dw;
+      g.dx = nullptr;
+      return launch_backward(g, two, sm_count, err, st);
+    }
+  }
+  return launch_backward(a, plan, sm_count, err, st);
+}
+
+// Whether the few-row kernel takes a product.  By expert: up to 8 rows an expert on average (1,536 rows
+// of 256 experts 162 us, pairs 171; integers 102 and 250).  Dense: its passes of 8 rows over the weights,
+// from L2 at 10.5 TB/s (integers 6.8), against the pairs' plan:
+//   rows of N x K      few, pairs (us)
+//   48 of 2048 x 2048   7.9,  8.5    but 64:  9.2,  8.5    integers  96: 10.3, 12.2
+//   16 of 8192 x 2048  10.0, 12.1    but 24: 13.2, 12.2    integers  48: 17.4, 17.5
+//   24 of 4096 x 4096  13.1, 13.9    but 32: 16.1, 14.1    integers  48: 15.8, 18.7
+bool few_rows_take(const ProductArgs& a, bool int8, int sm_count) {
+  if (a.offsets != nullptr) return a.M <= 8LL * a.E;
+  if (a.M <= 8) return true;
+  if (a.M > 256) return false;
+  const long long bytes = (long long)a.N * a.K * (int8 ? 1 : 2), passes = (a.M + 7) / 8;
+  return 3000 + passes * bytes / (int8 ? 6800 : 10500) <=
+         plan_forward(a.M, (a.N + 255) / 256, (a.K + 63) / 64, int8, sm_count / 2).ns;
+}
+
 }  // namespace flint
+
+// For the tests: what a dense product (what 0: forward, 1: integers, 2: dx, 3: dw, 4: both) takes on a GPU
+// of so many SMs: 0 the few-row kernel, else the pairs' KS * 1000000 + tile * 1000 + tile of dw.
+extern "C" int flint_linear_plan(int what, int M, int N, int K, int sm_count) {
+  using namespace flint;
+  Plan plan;
+  if (what < 2) {
+    ProductArgs a = {};
+    a.M = M;
+    a.N = N;
+    a.K = K;
+    a.E = 1;
+    if (few_rows_take(a, what == 1, sm_count)) return 0;
+    plan = plan_forward(M, (N + 255) / 256, (K + 63) / 64, what == 1, sm_count / 2);
+  } else {
+    plan = plan_backward(M, N, (K + 255) / 256, what != 3, what != 2, sm_count / 2);
+  }
+  return plan.ks * 1000000 + plan.tile * 1000 + plan.tile_w;
+}
