@@ -365,7 +365,7 @@ __global__ void __launch_bounds__(Shape<F32 || INT8, INT8>::THREADS, 1)
       }
     } else if (INT8 && warp >= 12) {
       // ---------------- codes to fp16, 128 of K at a time
-      uint32_t s = 0, ph = 0, r = 0, rph = 0;
+      uint32_t s = 0, ph = 0, r = 0, rph = 0, turned = 0;
       bool ok = true;
       // Warps 12-15, the weights: a lane has a row, that of its lane of tensor memory (the
       // swizzle puts 8 neighbouring rows' pieces in different places).
@@ -434,8 +434,12 @@ __global__ void __launch_bounds__(Shape<F32 || INT8, INT8>::THREADS, 1)
             r = 0;
             rph ^= 1;
           }
+          ++turned;
         }
       }
+      // The last releases of the stages have arrived: no arrival is under way to this CTA when it ends.
+      for (uint32_t q = turned - min(turned, (uint32_t)STAGES); q < turned && ok; ++q)
+        ok = __all_sync(0xffffffffu, wait(&empty[q % STAGES], (q / STAGES) & 1));
     } else if (warp == PRODUCER) {
       // ---------------- producer: this CTA's 128 of i and its half of the columns
       uint32_t s = 0, ph = 0, issued = 0;  // of lane 0, which copies
