@@ -209,10 +209,14 @@ struct GradArgs {
   int M, N, K, E, f32;  // f32: dw is fp32
 };
 // tcgen05 over pairs of CTAs (pair_gemm.cu)
-cudaError_t pair_gemm_kernels_init();
-bool few_rows_take(const ProductArgs& p, bool int8, int sm_count);  // rather than launch_pair_forward
-cudaError_t launch_pair_forward(const ProductArgs& p, bool int8, int sm_count, unsigned* err, cudaStream_t st);
-cudaError_t launch_pair_backward(const GradArgs& p, int sm_count, unsigned* err, cudaStream_t st);
+struct PairDevice {
+  int sms, most_ks;  // most_ks: pairs of the largest cluster that may share a contraction
+  unsigned* err;
+};
+cudaError_t pair_gemm_kernels_init(int* most_ks);
+bool few_rows_take(const ProductArgs& p, bool int8, const PairDevice& dev);  // rather than launch_pair_forward
+cudaError_t launch_pair_forward(const ProductArgs& p, bool int8, const PairDevice& dev, cudaStream_t st);
+cudaError_t launch_pair_backward(const GradArgs& p, const PairDevice& dev, cudaStream_t st);
 // Rows to 8-bit integers with one scale each (integer_rows.cu)
 cudaError_t launch_integer_rows(const void* x, bool bf16, long long stride, int rows, int K, const int32_t* pos,
                                 int top_k, int places, void* q, float* scales, cudaStream_t st);

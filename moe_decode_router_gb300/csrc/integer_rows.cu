@@ -46,7 +46,18 @@ struct Raw16 {
     if (!BF16) return __uint_as_float(b);
     return __uint_as_float(i & 1 ? b & 0xFFFF0000u : b << 16);
   }
+  // The largest magnitude, NaN if there is one: of bf16 two at a time.
   __device__ __forceinline__ float top() const {
+    if (BF16) {
+      uint32_t a = 0;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const uint4& w = v[i >> 2];
+        const uint32_t b = ((i & 3) == 0 ? w.x : (i & 3) == 1 ? w.y : (i & 3) == 2 ? w.z : w.w) & 0x7FFF7FFFu;
+        asm("max.NaN.bf16x2 %0, %0, %1;" : "+r"(a) : "r"(b));
+      }
+      return max_magnitude(__uint_as_float(a << 16), __uint_as_float(a & 0xFFFF0000u));
+    }
     float a = 0.f;
 #pragma unroll
     for (int i = 0; i < 16; ++i) a = max_magnitude(a, value(i));
@@ -54,19 +65,36 @@ struct Raw16 {
   }
 };
 
-// The whole number next to v / s, ties to even, in the low byte.  v * (1 / s) is off by
-// 2^-16 of a step at most, so only next to a border (one bf16 value in 200 is a tie) does
-// the exact remainder v - n * s, a multiple of the scale's last bit, decide.
-__device__ __forceinline__ uint32_t code(float v, float s, float inv) {
-  constexpr float MAGIC = 12582912.f;  // 1.5 * 2^23: its unit is 1
-  const float t = v * inv;
-  float m = t + MAGIC;
-  const float n = m - MAGIC;
-  if (fabsf(t - n) > 0.4999f) {
-    const float rest = fmaf(-n, s, v), twice = 2.f * fabsf(rest);
-    if (twice > s || (twice == s && (__float_as_uint(m) & 1u))) m += copysignf(1.f, rest);
+__device__ __forceinline__ uint64_t fma_pair(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t d;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
+  return d;
+}
+// The whole numbers next to v / s of two values, ties to even, in the low bytes.  v * (1 / s) is off
+// by 2^-16 of a step at most, so only next to a border (one bf16 value in 200 is a tie) does the
+// exact remainder v - n * s, a multiple of the scale's last bit, decide.  The kernel is bound by its
+// instructions: in pairs, 8,192 rows of
+// 4,096 take 19 us, one by one they took 25.
+struct Scale {
+  float s, near;               // near: remainders above are next to a border
+  uint64_t inv, minus, magic;  // pairs of 1 / s, -s and 1.5 * 2^23, whose unit is 1
+};
+__device__ __forceinline__ float settle(float m, float rest, float s) {
+  const float twice = 2.f * fabsf(rest);
+  return twice > s || (twice == s && (__float_as_uint(m) & 1u)) ? m + copysignf(1.f, rest) : m;
+}
+__device__ __forceinline__ void codes_of(float v0, float v1, const Scale& k, uint32_t& c0, uint32_t& c1) {
+  constexpr float MAGIC = 12582912.f;
+  const uint64_t v = f2pack(v0, v1), m = fma_pair(v, k.inv, k.magic), n = f2add(m, f2pack(-MAGIC, -MAGIC));
+  float m0, m1, r0, r1;
+  f2unpack(m, m0, m1);
+  f2unpack(fma_pair(n, k.minus, v), r0, r1);
+  if (fmaxf(fabsf(r0), fabsf(r1)) > k.near) {
+    m0 = settle(m0, r0, k.s);
+    m1 = settle(m1, r1, k.s);
   }
-  return __float_as_uint(m);
+  c0 = __float_as_uint(m0);
+  c1 = __float_as_uint(m1);
 }
 
 // a = max(largest magnitude of the row, 2^-96), scale = a * (1 / 127) (both in fp32), code =
@@ -74,7 +102,7 @@ __device__ __forceinline__ uint32_t code(float v, float s, float inv) {
 // values at a time, the first HELD x 16 of them kept in registers between the two passes
 // (a longer row is read a second time).  Bound by HBM.
 template <bool BF16, int THREADS, int HELD>
-__global__ void __launch_bounds__(256, 3) integer_rows_kernel(const IntRowsArgs p) {
+__global__ void __launch_bounds__(256, HELD == 1 ? 5 : HELD == 2 ? 4 : 2) integer_rows_kernel(const IntRowsArgs p) {
   __shared__ float tops[8];
   pdl_wait();
   pdl_trigger();
@@ -115,14 +143,16 @@ __global__ void __launch_bounds__(256, 3) integer_rows_kernel(const IntRowsArgs 
   if (!in) return;
   if (a < ROW_FLOOR) a = ROW_FLOOR;  // false for NaN
   const float scale = __fmul_rn(a, 1.f / 127.f), inv = __frcp_rn(scale);
+  const Scale steps = {scale, 0.4999f * scale, f2pack(inv, inv), f2pack(-scale, -scale), f2pack(12582912.f, 12582912.f)};
   const bool fine = scale < INFINITY;  // false for NaN: the codes of such a row are 0
   auto put = [&](const Raw16<BF16>& v, int k) {
     uint32_t c[4];
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      const uint32_t lo = __byte_perm(code(v.value(4 * i), scale, inv), code(v.value(4 * i + 1), scale, inv), 0x0040);
-      const uint32_t hi = __byte_perm(code(v.value(4 * i + 2), scale, inv), code(v.value(4 * i + 3), scale, inv), 0x0040);
-      c[i] = fine ? __byte_perm(lo, hi, 0x5410) : 0u;
+      uint32_t b0, b1, b2, b3;
+      codes_of(v.value(4 * i), v.value(4 * i + 1), steps, b0, b1);
+      codes_of(v.value(4 * i + 2), v.value(4 * i + 3), steps, b2, b3);
+      c[i] = fine ? __byte_perm(__byte_perm(b0, b1, 0x0040), __byte_perm(b2, b3, 0x0040), 0x5410) : 0u;
     }
     const uint4 codes = make_uint4(c[0], c[1], c[2], c[3]);
     if (p.pos == nullptr) {
@@ -182,9 +212,19 @@ cudaError_t launch_integer_rows(const void* x, bool bf16, long long stride, int 
   p.places = places;
   p.q = static_cast<uint8_t*>(q);
   p.scales = scales;
-  // few rows: more threads for each, or most SMs idle
-  if (K <= 2048 && rows <= 1024) return bf16 ? launch<true, 128, 1>(p, st) : launch<false, 128, 1>(p, st);
-  if (K <= 2048) return bf16 ? launch<true, 32, 4>(p, st) : launch<false, 32, 4>(p, st);
+  // Threads on a row and pieces of 16 each of them keeps, measured (us, bf16; the second digits the next best):
+  //   K 512, 49,152 rows             32, 1   15.0 (32, 2: 16.3)
+  //   K 1024, 8,192 rows to 2 places  32, 2    6.4 (64, 1: 7.3)
+  //   K 1408, 49,152 rows            64, 2   48.8 (32, 4: 53.7)
+  //   K 2048, 8,191 rows to 6 places 128, 1   22.7 (64, 2: 24.5); 300 rows 2.7 (3.6)
+  //   K 4096, 8,192 rows            128, 2   19.2 (256, 1: 23.3)
+  //   K 8192, 4,096 rows            256, 2   19.0 (256, 4: 34)
+  if (K <= 512) return bf16 ? launch<true, 32, 1>(p, st) : launch<false, 32, 1>(p, st);
+  if (K <= 1024) return bf16 ? launch<true, 32, 2>(p, st) : launch<false, 32, 2>(p, st);
+  if (K <= 1792 && rows > 1024) return bf16 ? launch<true, 64, 2>(p, st) : launch<false, 64, 2>(p, st);
+  if (K <= 2048) return bf16 ? launch<true, 128, 1>(p, st) : launch<false, 128, 1>(p, st);
+  if (K <= 4096) return bf16 ? launch<true, 128, 2>(p, st) : launch<false, 128, 2>(p, st);
+  if (K <= 8192) return bf16 ? launch<true, 256, 2>(p, st) : launch<false, 256, 2>(p, st);
   return bf16 ? launch<true, 256, 4>(p, st) : launch<false, 256, 4>(p, st);
 }
 

@@ -66,41 +66,42 @@ static_assert((int)FFN_NONE == (int)FLINT_MOE_ACT_NONE && (int)FFN_SILU == (int)
               "activations");
 
 // The current device's set-up: the library's, and once that of the tensor-core kernels, whose
-// failure is these calls' alone.
-struct Device {
-  int sms = 0;
-  unsigned* err = nullptr;
-};
-int set_up(Device* d) {
+// failure is the products' alone.
+int set_up(PairDevice* d) {
   const int st = device_info(&d->sms, &d->err);
   if (st != FLINT_MOE_OK) return st;
   static std::mutex mu;
-  static std::map<int, bool> ready;
+  static std::map<int, int> most;  // pairs of a cluster, 0: the kernels are not to be had
   int dev = -1;
   if (cudaGetDevice(&dev) != cudaSuccess) return FLINT_MOE_ERR_CUDA;
   std::lock_guard<std::mutex> lk(mu);
-  auto it = ready.find(dev);
-  if (it == ready.end()) {
-    it = ready.emplace(dev, pair_gemm_kernels_init() == cudaSuccess).first;
-    if (!it->second) (void)cudaGetLastError();
+  auto it = most.find(dev);
+  if (it == most.end()) {
+    int ks = 0;
+    if (pair_gemm_kernels_init(&ks) != cudaSuccess) {
+      ks = 0;
+      (void)cudaGetLastError();
+    }
+    it = most.emplace(dev, ks).first;
   }
-  return it->second ? FLINT_MOE_OK : FLINT_MOE_ERR_CUDA;
+  d->most_ks = it->second;
+  return d->most_ks > 0 ? FLINT_MOE_OK : FLINT_MOE_ERR_CUDA;
 }
 
 int product(const ProductArgs& p, bool int8, flint_moe_stream_t stream) {
-  Device d;
+  PairDevice d;
   const int rc = set_up(&d);
   if (rc != FLINT_MOE_OK) return rc;
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
-  if (few_rows_take(p, int8, d.sms)) return to_status(launch_few_rows(p, int8, st));
-  return to_status(launch_pair_forward(p, int8, d.sms, d.err, st));
+  if (few_rows_take(p, int8, d)) return to_status(launch_few_rows(p, int8, st));
+  return to_status(launch_pair_forward(p, int8, d, st));
 }
 
 int gradients(const void* dy, const void* x, int M, const void* w, int E, const int32_t* offsets, int N, int K,
-              void* dx, void* dw, int dw_type, const Device& d, cudaStream_t st) {
+              void* dx, void* dw, int dw_type, const PairDevice& d, cudaStream_t st) {
   const GradArgs p = {dy, x, w, offsets, dx, dw, M, N, K, E, dw_type == FLINT_MOE_T_F32};
   if (dx == nullptr && dw == nullptr) return FLINT_MOE_OK;
-  return to_status(launch_pair_backward(p, d.sms, d.err, st));
+  return to_status(launch_pair_backward(p, d, st));
 }
 
 }  // namespace
@@ -149,7 +150,7 @@ int flint_moe_linear_backward(const void* dy, const void* x, int M, const void* 
   if (bad_buffers({}, {{dy, (size_t)M * N * 2}, {x, (size_t)M * K * 2}, {w, weights * 2}},
                   {{dx, (size_t)M * K * 2}, {dw, weights * type_size(dw_type)}}, {{offsets, offset_bytes(n_experts)}}))
     return FLINT_MOE_ERR_INVALID_ARG;
-  Device d;
+  PairDevice d;
   if ((st = set_up(&d)) != FLINT_MOE_OK) return st;
   return gradients(dy, x, M, w, n_experts, offsets, N, K, dx, dw, dw_type, d,
                    reinterpret_cast<cudaStream_t>(stream));
@@ -167,7 +168,7 @@ int flint_moe_gated_linear_backward(const void* dh, const void* gu, const void* 
   if (bad_buffers({{dgu, sums}}, {{dh, (size_t)M * I * 2}, {gu, sums}, {x, (size_t)M * K * 2}, {w, weights * 2}},
                   {{dx, (size_t)M * K * 2}, {dw, weights * type_size(dw_type)}}, {{offsets, offset_bytes(n_experts)}}))
     return FLINT_MOE_ERR_INVALID_ARG;
-  Device d;
+  PairDevice d;
   if ((st = set_up(&d)) != FLINT_MOE_OK) return st;
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   if (launch_gate_backward(dh, gu, offsets, M, I, n_experts, act, dgu, s) != cudaSuccess) return FLINT_MOE_ERR_CUDA;
@@ -189,8 +190,9 @@ int flint_moe_integer_quantize_rows(const void* x, int x_type, long long row_str
                   {{x, ((size_t)(rows - 1) * (size_t)row_stride + K) * size}}, {},
                   {{pos, (size_t)rows * (pos ? top_k : 0) * 4}}))
     return FLINT_MOE_ERR_INVALID_ARG;
-  Device d;
-  const int st = set_up(&d);
+  int sms = 0;
+  unsigned* err = nullptr;
+  const int st = device_info(&sms, &err);
   if (st != FLINT_MOE_OK) return st;
   return to_status(launch_integer_rows(x, x_type == FLINT_MOE_T_BF16, row_stride, rows, K, pos, top_k, places, q,
                                        scales, reinterpret_cast<cudaStream_t>(stream)));

@@ -940,9 +940,9 @@ struct Plan {
 
 // Tile of a dense product's rows, and pairs that share its contraction, so that the units fill the
 // pairs of SMs evenly.
-Plan plan_forward(int M, long long a_tiles, long long steps, bool int8, int pairs) {
+Plan plan_forward(int M, long long a_tiles, long long steps, bool int8, int pairs, int most_ks) {
   Plan best = {256, 256, 1, -1};
-  for (int ks = 1; ks <= 4; ks *= 2)
+  for (int ks = 1; ks <= most_ks; ks *= 2)
     for (int tile = 256; tile >= 32; tile -= 32) {
       const long long units = (M + tile - 1LL) / tile * a_tiles, room = clusters_of(ks, pairs);
       if (ks > 1 && (units > room || steps < 4 * ks)) continue;
@@ -955,10 +955,10 @@ Plan plan_forward(int M, long long a_tiles, long long steps, bool int8, int pair
 }
 
 // The same for both gradients in one launch (or one alone): units of dx first, then of dw, dealt out in turn.
-Plan plan_backward(int M, int N, long long a_tiles, bool dx, bool dw, int pairs) {
+Plan plan_backward(int M, int N, long long a_tiles, bool dx, bool dw, int pairs, int most_ks) {
   const long long dx_steps = (N + 63) / 64, dw_steps = (M + 63) / 64;
   Plan best = {256, 256, 1, -1};
-  for (int ks = 1; ks <= 4; ks *= 2)
+  for (int ks = 1; ks <= most_ks; ks *= 2)
     for (int tile = 256; tile >= (dx ? 64 : 256); tile -= 32)
       for (int tile_w = 256; tile_w >= (dw ? 128 : 256); tile_w -= 128) {  // whole pieces of 64 columns
         const long long a = dx ? (M + tile - 1LL) / tile * a_tiles : 0, b = dw ? (N + tile_w - 1LL) / tile_w * a_tiles : 0;
@@ -989,7 +989,7 @@ bool encode_rows(Maps& m, int size, const void* x, uint64_t rows, uint64_t K) {
 
 }  // namespace
 
-cudaError_t pair_gemm_kernels_init() {
+cudaError_t pair_gemm_kernels_init(int* most_ks) {
   if (g_encode == nullptr) {
     void* fn = nullptr;
     cudaDriverEntryPointQueryResult q;
@@ -1021,10 +1021,31 @@ cudaError_t pair_gemm_kernels_init() {
     if ((e = cudaFuncGetAttributes(&fa, x.f)) != cudaSuccess) return e;
     if (fa.numRegs < x.regs) return cudaErrorInvalidConfiguration;  // the shares would never be met
   }
+  // Pairs of a cluster that share a contraction, as many as the device places.
+  *most_ks = 1;
+  for (int ks = 2; ks <= 4; ks *= 2) {
+    cudaLaunchAttribute attr;
+    attr.id = cudaLaunchAttributeClusterDimension;
+    attr.val.clusterDim.x = 2 * ks;
+    attr.val.clusterDim.y = 1;
+    attr.val.clusterDim.z = 1;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(2 * ks);
+    cfg.blockDim = dim3(Shape<true, true>::THREADS);
+    cfg.dynamicSmemBytes = pair_smem(ROUTE_MAX_E);
+    cfg.attrs = &attr;
+    cfg.numAttrs = 1;
+    int fit = 0;
+    const cudaError_t e = ks == 2 ? cudaOccupancyMaxActiveClusters(&fit, pair_gemm_kernel<FORWARD, true, true, true, 2>, &cfg)
+                                  : cudaOccupancyMaxActiveClusters(&fit, pair_gemm_kernel<FORWARD, true, true, true, 4>, &cfg);
+    if (e != cudaSuccess) (void)cudaGetLastError();
+    if (e != cudaSuccess || fit < 1) break;
+    *most_ks = ks;
+  }
   return cudaSuccess;
 }
 
-cudaError_t launch_pair_forward(const ProductArgs& a, bool int8, int sm_count, unsigned* err, cudaStream_t st) {
+cudaError_t launch_pair_forward(const ProductArgs& a, bool int8, const PairDevice& dev, cudaStream_t st) {
   const bool gated = a.act != FFN_NONE;
   const uint64_t M = a.M, N = a.N, K = a.K, E = a.E;
   PairArgs p = {};
@@ -1033,13 +1054,13 @@ cudaError_t launch_pair_forward(const ProductArgs& a, bool int8, int sm_count, u
   p.keep = static_cast<uint16_t*>(a.keep);
   p.sx = a.sx;
   p.sw = a.sw;
-  p.err = err;
+  p.err = dev.err;
   p.M = a.M;
   p.E = a.E;
   p.I = gated ? a.N / 2 : a.N;
   p.steps = int8 ? (a.K + 127) / 128 : (a.K + 63) / 64;
   p.a_tiles = (a.N + 255) / 256;
-  const Plan plan = a.offsets == nullptr ? plan_forward(a.M, p.a_tiles, (a.K + 63) / 64, int8, sm_count / 2)
+  const Plan plan = a.offsets == nullptr ? plan_forward(a.M, p.a_tiles, (a.K + 63) / 64, int8, dev.sms / 2, dev.most_ks)
                                          : Plan{256, 256, 1, 0};
   p.tile = plan.tile;
   p.act = a.act;
@@ -1055,25 +1076,25 @@ cudaError_t launch_pair_forward(const ProductArgs& a, bool int8, int sm_count, u
   m.aw = m.bw = m.bw1 = m.bw2 = m.a;
   const long long most = row_tiles(a.M, a.E, a.offsets != nullptr, p.tile) * p.a_tiles;
   if (int8) {
-    if (gated) return a.f32 ? launch<FORWARD, true, true, true>(p, m, plan.ks, most, sm_count, st)
-                            : launch<FORWARD, true, false, true>(p, m, plan.ks, most, sm_count, st);
-    return a.f32 ? launch<FORWARD, false, true, true>(p, m, plan.ks, most, sm_count, st)
-                 : launch<FORWARD, false, false, true>(p, m, plan.ks, most, sm_count, st);
+    if (gated) return a.f32 ? launch<FORWARD, true, true, true>(p, m, plan.ks, most, dev.sms, st)
+                            : launch<FORWARD, true, false, true>(p, m, plan.ks, most, dev.sms, st);
+    return a.f32 ? launch<FORWARD, false, true, true>(p, m, plan.ks, most, dev.sms, st)
+                 : launch<FORWARD, false, false, true>(p, m, plan.ks, most, dev.sms, st);
   }
-  if (gated) return launch<FORWARD, true, false>(p, m, plan.ks, most, sm_count, st);
-  return a.f32 ? launch<FORWARD, false, true>(p, m, plan.ks, most, sm_count, st)
-               : launch<FORWARD, false, false>(p, m, plan.ks, most, sm_count, st);
+  if (gated) return launch<FORWARD, true, false>(p, m, plan.ks, most, dev.sms, st);
+  return a.f32 ? launch<FORWARD, false, true>(p, m, plan.ks, most, dev.sms, st)
+               : launch<FORWARD, false, false>(p, m, plan.ks, most, dev.sms, st);
 }
 
 namespace {
 
-cudaError_t launch_backward(const GradArgs& a, const Plan& plan, int sm_count, unsigned* err, cudaStream_t st) {
+cudaError_t launch_backward(const GradArgs& a, const Plan& plan, const PairDevice& dev, cudaStream_t st) {
   const uint64_t M = a.M, N = a.N, K = a.K, E = a.E;
   PairArgs p = {};
   p.offsets = a.offsets;
   p.y = a.dx;
   p.dw = a.dw;
-  p.err = err;
+  p.err = dev.err;
   p.M = a.M;
   p.E = a.E;
   p.I = a.K;
@@ -1102,32 +1123,33 @@ cudaError_t launch_backward(const GradArgs& a, const Plan& plan, int sm_count, u
   if (!ok) return cudaErrorInvalidValue;
   long long most = (long long)a.E * p.o_tiles * p.a_tiles;
   if (a.dx != nullptr) most += row_tiles(a.M, a.E, a.offsets != nullptr, p.tile) * p.a_tiles;
-  return a.f32 ? launch<BACKWARD, false, true>(p, m, plan.ks, most, sm_count, st)
-               : launch<BACKWARD, false, false>(p, m, plan.ks, most, sm_count, st);
+  return a.f32 ? launch<BACKWARD, false, true>(p, m, plan.ks, most, dev.sms, st)
+               : launch<BACKWARD, false, false>(p, m, plan.ks, most, dev.sms, st);
 }
 
 }  // namespace
 
-cudaError_t launch_pair_backward(const GradArgs& a, int sm_count, unsigned* err, cudaStream_t st) {
-  const int a_tiles = (a.K + 255) / 256, pairs = sm_count / 2;
+cudaError_t launch_pair_backward(const GradArgs& a, const PairDevice& dev, cudaStream_t st) {
+  const int a_tiles = (a.K + 255) / 256, pairs = dev.sms / 2;
   const bool dx = a.dx != nullptr, dw = a.dw != nullptr;
-  if (a.offsets != nullptr) return launch_backward(a, Plan{256, 256, 1, 0}, sm_count, err, st);
-  const Plan plan = plan_backward(a.M, a.N, a_tiles, dx, dw, pairs);
+  if (a.offsets != nullptr) return launch_backward(a, Plan{256, 256, 1, 0}, dev, st);
+  const Plan plan = plan_backward(a.M, a.N, a_tiles, dx, dw, pairs, dev.most_ks);
   if (dx && dw) {
     // Long units of one and short ones of the other fill a launch badly: 16 rows of 8192 x 2048 take 43
     // us in one and 28 in two, each with its own share of the contraction a cluster.
-    const Plan one = plan_backward(a.M, a.N, a_tiles, true, false, pairs), two = plan_backward(a.M, a.N, a_tiles, false, true, pairs);
+    const Plan one = plan_backward(a.M, a.N, a_tiles, true, false, pairs, dev.most_ks);
+    const Plan two = plan_backward(a.M, a.N, a_tiles, false, true, pairs, dev.most_ks);
     if (one.ns + two.ns < plan.ns) {
       GradArgs g = a;
       g.dw = nullptr;
-      const cudaError_t e = launch_backward(g, one, sm_count, err, st);
+      const cudaError_t e = launch_backward(g, one, dev, st);
       if (e != cudaSuccess) return e;
       g.dw = a.dw;
       g.dx = nullptr;
-      return launch_backward(g, two, sm_count, err, st);
+      return launch_backward(g, two, dev, st);
     }
   }
-  return launch_backward(a, plan, sm_count, err, st);
+  return launch_backward(a, plan, dev, st);
 }
 
 // Whether the few-row kernel takes a product.  By expert: up to 8 rows an expert on average (1,536 rows
@@ -1137,13 +1159,13 @@ cudaError_t launch_pair_backward(const GradArgs& a, int sm_count, unsigned* err,
 //   48 of 2048 x 2048   7.9,  8.5    but 64:  9.2,  8.5    integers  96: 10.3, 12.2
 //   16 of 8192 x 2048  10.0, 12.1    but 24: 13.2, 12.2    integers  48: 17.4, 17.5
 //   24 of 4096 x 4096  13.1, 13.9    but 32: 16.1, 14.1    integers  48: 15.8, 18.7
-bool few_rows_take(const ProductArgs& a, bool int8, int sm_count) {
+bool few_rows_take(const ProductArgs& a, bool int8, const PairDevice& dev) {
   if (a.offsets != nullptr) return a.M <= 8LL * a.E;
   if (a.M <= 8) return true;
   if (a.M > 256) return false;
   const long long bytes = (long long)a.N * a.K * (int8 ? 1 : 2), passes = (a.M + 7) / 8;
   return 3000 + passes * bytes / (int8 ? 6800 : 10500) <=
-         plan_forward(a.M, (a.N + 255) / 256, (a.K + 63) / 64, int8, sm_count / 2).ns;
+         plan_forward(a.M, (a.N + 255) / 256, (a.K + 63) / 64, int8, dev.sms / 2, dev.most_ks).ns;
 }
 
 }  // namespace flint
@@ -1159,10 +1181,10 @@ extern "C" int flint_linear_plan(int what, int M, int N, int K, int sm_count) {
     a.N = N;
     a.K = K;
     a.E = 1;
-    if (few_rows_take(a, what == 1, sm_count)) return 0;
-    plan = plan_forward(M, (N + 255) / 256, (K + 63) / 64, what == 1, sm_count / 2);
+    if (few_rows_take(a, what == 1, PairDevice{sm_count, 4, nullptr})) return 0;
+    plan = plan_forward(M, (N + 255) / 256, (K + 63) / 64, what == 1, sm_count / 2, 4);
   } else {
-    plan = plan_backward(M, N, (K + 255) / 256, what != 3, what != 2, sm_count / 2);
+    plan = plan_backward(M, N, (K + 255) / 256, what != 3, what != 2, sm_count / 2, 4);
   }
   return plan.ks * 1000000 + plan.tile * 1000 + plan.tile_w;
 }

@@ -120,11 +120,10 @@ def test_dense_gradients(out, what, M, N, K, ks):
 
 
 @gpu
-@pytest.mark.parametrize("high,N,K", [(9, 544, 272), (90, 1056, 528), (600, 544, 1040)])
-def test_many_groups(high, N, K):
-    """Groups of 0 to `high` rows of 70 experts: several units a pair, every length of a last step,
-    and the few-row kernel by experts."""
-    E = 70
+@pytest.mark.parametrize("E,high,N,K", [(70, 9, 544, 272), (70, 90, 1056, 528), (70, 600, 544, 1040), (1024, 24, 96, 80)])
+def test_many_groups(E, high, N, K):
+    """Groups of 0 to `high` rows: several units a pair, every length of a last step, and the
+    few-row kernel by experts."""
     counts = torch.randint(0, high + 1, (E,), generator=gen(high)).tolist()
     counts[3] = counts[E - 1] = 0
     M, offsets, I = sum(counts), groups(counts), N // 2

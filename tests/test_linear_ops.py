@@ -329,7 +329,8 @@ def test_integer_sums_are_exact(M, K):
 @gpu
 @pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
 @pytest.mark.parametrize("rows,K,pad", [(1, 16, 0), (3, 128, 8), (7, 144, 0), (129, 2048, 0), (1000, 512, 16),
-                                        (5, 2064, 0), (2, 16400, 8), (3, 131072, 0)])
+                                        (5, 2064, 0), (2, 16400, 8), (3, 131072, 0), (1025, 1040, 0), (33, 1024, 8),
+                                        (1030, 1808, 0), (70, 4096, 0), (3, 8208, 0), (9, 5136, 16)])
 def test_integer_quantize_rows(dtype, rows, K, pad):
     x = (3 * torch.randn(rows, K + pad, generator=gen(rows + K))).to(dtype).to(dev())[:, :K]
     q_whole, q, q_before = framed((rows, K), torch.int8)
