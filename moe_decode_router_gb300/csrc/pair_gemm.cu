@@ -364,82 +364,97 @@ __global__ void __launch_bounds__(Shape<F32 || INT8, INT8>::THREADS, 1)
         }
       }
     } else if (INT8 && warp >= 12) {
-      // ---------------- codes to fp16, 128 of K at a time
-      uint32_t s = 0, ph = 0, r = 0, rph = 0, turned = 0;
-      bool ok = true;
-      // Warps 12-15, the weights: a lane has a row, that of its lane of tensor memory (the
-      // swizzle puts 8 neighbouring rows' pieces in different places).
-      const int arow = (warp & 3) * 32 + lane;
-      const uint32_t a_to = tmem + 256 + ((uint32_t)((warp & 3) * 32) << 16);
-      // Warps 16-19, the other operand: a warp takes 8 rows (a swizzle atom) at once, a lane
-      // 16 codes of a row; the 8 lanes that shared memory serves together have two rows r and
-      // r ^ 5, whose swizzled places differ on the way in (bit 2) and on the way out (bit 0).
-      const int q = lane & 3, row = (lane >> 3) ^ (lane & 4 ? 5 : 0);
-      const int lo = ((2 * q) ^ row) << 4, hi = ((2 * q + 1) ^ row) << 4;
-      for (int u = u0; u < n_units && ok; u += ustep) {
-        const Unit t = unit_of(u);
-        const int atoms = t.n >> 4;
-        const Steps steps = steps_of(t);
-        for (int k = steps.from; k < steps.to; ++k) {
-          ok = __all_sync(0xffffffffu, wait(&landed[r], rph)) && __all_sync(0xffffffffu, wait(&empty[s], ph ^ 1));
-          if (!ok) break;
-          const uint8_t* from = sm + r * STAGE;
-          if (warp < 16) {
-            tc05::fence_after_sync();
-            const uint8_t* at = from + arow * 128;
-#pragma unroll
-            for (int h = 0; h < 4; ++h) {
-              const uint4 c0 = *reinterpret_cast<const uint4*>(at + (((2 * h) ^ (arow & 7)) << 4));
-              const uint4 c1 = *reinterpret_cast<const uint4*>(at + (((2 * h + 1) ^ (arow & 7)) << 4));
-              uint4 v[4];
-              codes_to_f16(c0, v[0], v[1]);
-              codes_to_f16(c1, v[2], v[3]);
-              tc05::st_32x32b_x16(a_to + s * 64 + h * 16, v);
+      // ---------------- codes to fp16, 128 of K at a time: take(stage of codes, stage, unit) turns this
+      // warp's part of them, done() makes what it wrote visible to the MMAs.
+      auto turn = [&](auto&& take, auto&& done) {
+        uint32_t s = 0, ph = 0, r = 0, rph = 0, turned = 0;
+        bool ok = true;
+        for (int u = u0; u < n_units && ok; u += ustep) {
+          const Unit t = unit_of(u);
+          const Steps steps = steps_of(t);
+          for (int k = steps.from; k < steps.to; ++k) {
+            // every lane looks, and all go on or none
+            if (!__all_sync(0xffffffffu, mbar_test(&landed[r], rph) & mbar_test(&empty[s], ph ^ 1)))
+              ok = __all_sync(0xffffffffu, wait(&landed[r], rph)) && __all_sync(0xffffffffu, wait(&empty[s], ph ^ 1));
+            if (!ok) break;
+            take(r, s, t);
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&taken[r]);  // the codes are in registers or beyond
+            done();
+            __syncwarp();
+            if (lane == 0) tc05::arrive_cluster(full0 + s * 8);
+            if (++s == STAGES) {
+              s = 0;
+              ph ^= 1;
             }
-          } else {
-#pragma unroll
-            for (int h = 0; h < 2; ++h) {
-              const uint8_t* at = from + A_BYTES + row * 128 + (((h * 4 + q) ^ row) << 4);
-              uint8_t* to = sm + CODES * STAGE + (2 * s + h) * B_BYTES + row * 128;
-              uint4 c[4];
-#pragma unroll
-              for (int i = 0; i < 4; ++i)
-                if (warp - 16 + 4 * i < atoms) c[i] = *reinterpret_cast<const uint4*>(at + (warp - 16 + 4 * i) * 1024);
-#pragma unroll
-              for (int i = 0; i < 4; ++i)
-                if (warp - 16 + 4 * i < atoms) {
-                  uint4 v0, v1;
-                  codes_to_f16(c[i], v0, v1);
-                  uint8_t* d = to + (warp - 16 + 4 * i) * 1024;
-                  *reinterpret_cast<uint4*>(d + lo) = v0;
-                  *reinterpret_cast<uint4*>(d + hi) = v1;
-                }
+            if (++r == CODES) {
+              r = 0;
+              rph ^= 1;
             }
+            ++turned;
           }
-          __syncwarp();
-          if (lane == 0) mbar_arrive(&taken[r]);  // the codes are in registers or beyond
-          if (warp < 16) {
-            tc05::wait_st();
-            tc05::fence_before_sync();
-          } else {
-            tc05::fence_proxy_async_smem();
-          }
-          __syncwarp();
-          if (lane == 0) tc05::arrive_cluster(full0 + s * 8);
-          if (++s == STAGES) {
-            s = 0;
-            ph ^= 1;
-          }
-          if (++r == CODES) {
-            r = 0;
-            rph ^= 1;
-          }
-          ++turned;
         }
+        // The last releases of the stages have arrived: no arrival is under way to this CTA when it ends.
+        for (uint32_t q = turned - min(turned, (uint32_t)STAGES); q < turned && ok; ++q)
+          ok = __all_sync(0xffffffffu, wait(&empty[q % STAGES], (q / STAGES) & 1));
+      };
+      if (warp < 16) {
+        // The weights: a lane has a row, that of its lane of tensor memory (the swizzle puts 8
+        // neighbouring rows' pieces in different places).
+        const int arow = (warp & 3) * 32 + lane;
+        const uint32_t to = tmem + 256 + ((uint32_t)((warp & 3) * 32) << 16);
+        turn(
+            [&](uint32_t r, uint32_t s, const Unit&) {
+              tc05::fence_after_sync();
+              const uint8_t* at = sm + r * STAGE + arow * 128;
+#pragma unroll
+              for (int g = 0; g < 2; ++g) {
+                uint4 c[4];
+#pragma unroll
+                for (int h = 0; h < 4; ++h) c[h] = *reinterpret_cast<const uint4*>(at + (((4 * g + h) ^ (arow & 7)) << 4));
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                  uint4 v[4];
+                  codes_to_f16(c[2 * h], v[0], v[1]);
+                  codes_to_f16(c[2 * h + 1], v[2], v[3]);
+                  tc05::st_32x32b_x16(to + s * 64 + (2 * g + h) * 16, v);
+                }
+              }
+            },
+            [&] {
+              tc05::wait_st();
+              tc05::fence_before_sync();
+            });
+      } else {
+        // The other operand: a warp takes 8 rows (a swizzle atom) at once, a lane 16 codes of a row;
+        // the 8 lanes that shared memory serves together have two rows r and r ^ 5, whose
+        // swizzled places differ on the way in (bit 2) and on the way out (bit 0).
+        const int q = lane & 3, row = (lane >> 3) ^ (lane & 4 ? 5 : 0), first = warp - 16;
+        const int in = A_BYTES + row * 128 + first * 1024, near = (q ^ row) << 4;  // the second 64 of K: near ^ 64
+        const int out = CODES * STAGE + row * 128 + first * 1024, lo = ((2 * q) ^ row) << 4;  // the upper half: lo ^ 16
+        turn(
+            [&](uint32_t r, uint32_t s, const Unit& t) {
+              const int atoms = t.n >> 4;
+#pragma unroll
+              for (int h = 0; h < 2; ++h) {
+                const uint8_t* at = sm + r * STAGE + in + (near ^ (h * 64));
+                uint8_t* to = sm + (2 * s + h) * B_BYTES + out;
+                uint4 c[4];
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                  if (first + 4 * i < atoms) c[i] = *reinterpret_cast<const uint4*>(at + i * 4096);
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                  if (first + 4 * i < atoms) {
+                    uint4 v0, v1;
+                    codes_to_f16(c[i], v0, v1);
+                    *reinterpret_cast<uint4*>(to + i * 4096 + lo) = v0;
+                    *reinterpret_cast<uint4*>(to + i * 4096 + (lo ^ 16)) = v1;
+                  }
+              }
+            },
+            [&] { tc05::fence_proxy_async_smem(); });
       }
-      // The last releases of the stages have arrived: no arrival is under way to this CTA when it ends.
-      for (uint32_t q = turned - min(turned, (uint32_t)STAGES); q < turned && ok; ++q)
-        ok = __all_sync(0xffffffffu, wait(&empty[q % STAGES], (q / STAGES) & 1));
     } else if (warp == PRODUCER) {
       // ---------------- producer: this CTA's 128 of i and its half of the columns
       uint32_t s = 0, ph = 0, issued = 0;  // of lane 0, which copies
