@@ -67,7 +67,7 @@ static_assert((int)FFN_NONE == (int)FLINT_MOE_ACT_NONE && (int)FFN_SILU == (int)
 
 // The current device's set-up: the library's, and once that of the tensor-core kernels, whose
 // failure is the products' alone.
-int set_up(PairDevice* d) {
+int set_up(PairDevice* d) try {
   const int st = device_info(&d->sms, &d->err);
   if (st != FLINT_MOE_OK) return st;
   static std::mutex mu;
@@ -86,6 +86,8 @@ int set_up(PairDevice* d) {
   }
   d->most_ks = it->second;
   return d->most_ks > 0 ? FLINT_MOE_OK : FLINT_MOE_ERR_CUDA;
+} catch (...) {  // no memory for the map, no mutex
+  return FLINT_MOE_ERR_CUDA;
 }
 
 int product(const ProductArgs& p, bool int8, flint_moe_stream_t stream) {
