@@ -26,14 +26,17 @@
 // expert's, perhaps infinite) with zeros before the stage is handed on.
 //
 // 8-bit integers.  This GPU's tensor cores take none at a rate worth using, but a code is
-// exact in fp16, a product of two in fp32, and a sum of 1,024 products stays within 2^24,
-// where fp32 holds every whole number.  Codes land in a ring of their own (128 of K a
+// exact in fp16, a product of two in fp32, and a sum of 896 products stays below 2^24 - 2^21
+// (up to 2^24 fp32 holds every whole number).  Codes land in a ring of their own (128 of K a
 // stage); eight warps turn them into fp16 (code + 1152 is put together from the bits,
 // 1152 taken off), the weights' into tensor memory and the others into shared memory, whose
 // bandwidth would be the bound with both: 96 KB for 64 of K, 768 cycles against 512 of MMA.
-// Every 1,024 of K the accumulator (one alone, beside the weights) is added to 32-bit
-// integers in registers.  fp32 outputs of bf16 operands are promoted the same way every 512 of the
-// contracted dimension: the tensor cores cut a sum instead of rounding it, which adds up.
+// Every 896 of K the accumulator (one alone, beside the weights: no MMA runs meanwhile) is added to
+// sums in registers: in fp32 while they are at most 2^21, and once one of a warp's has passed that in
+// 32-bit integers, whose conversions (16 lanes a cycle) are most of the time of the hand-over: 8191 x
+// 4096 x 4096 takes 173 us, 194 with integers from the start.  fp32 outputs of bf16 operands are
+// promoted the same way every 512 of the contracted dimension: the tensor cores cut a sum instead of
+// rounding it, which adds up.
 //
 // Where a dense product has units for few pairs alone, KS = 2 or 4 pairs of a cluster share a
 // unit's contraction.  Each leaves its sums in its stages, and after a cluster barrier adds its
@@ -62,7 +65,7 @@ static_assert(CODES * STAGE + TURNED * 2 * B_BYTES <= RING * STAGE && 256 + TURN
 constexpr int OUT_BYTES = 8 * 32 * 80;  // output staging: rows of 64 bytes, 80 apart, 32 a warp (16 of 16 warps)
 constexpr int OFF_OUT = RING * STAGE;
 constexpr int OFF_BARS = OFF_OUT + OUT_BYTES;
-constexpr int SEG_F32 = 8, SEG_INT = 8;  // steps (of 64; integers: of 128) between promotions
+constexpr int SEG_F32 = 8, SEG_INT = 7;  // steps (of 64; integers: of 128) between promotions
 
 constexpr int OFF_GROUPS = OFF_BARS + 256;
 constexpr int pair_smem(int E) { return OFF_GROUPS + (3 * E + 1) * 4; }
@@ -134,6 +137,9 @@ struct Unit {
   int c0, clen;           // weights: the expert's rows
 };
 
+// fp32 adds whole numbers exactly up to 2^24: a segment's sum to one of ROOM at most.
+constexpr float ROOM = (float)((1 << 24) - SEG_INT * 128 * (1 << 14));
+static_assert(SEG_INT * 128 * (1 << 14) < 1 << 24, "exact sums");
 // Sums of a promoting kernel.
 template <bool INT8>
 struct Held {
@@ -637,7 +643,7 @@ __global__ void __launch_bounds__(Shape<F32 || INT8, INT8>::THREADS, 1)
     constexpr int CW = W::CHUNK, GROUPS = CW / 8;  // columns of a chunk, and groups of 8
     // Puts out chunk c of the warp's part of unit t: its sums x, as tensor memory is read.  With the
     // contraction shared every KS-th group is this pair's.
-    auto put_out = [&](const Unit& t, int c, const S* x) {
+    auto put_out = [&](const Unit& t, int c, const float* x) {
       const int np = t.n / W::PARTS, first = part * np, live = min(np, t.cnt - first);
       // first i of the warp's lanes (gated: of its 16 pairs), and the row of the output that o 0 of the unit is
       const int i0 = GATED ? (t.at * 8 + (int)rank * 4 + quad) * 16 : t.at * 256 + (int)rank * 128 + quad * 32;
@@ -662,7 +668,7 @@ __global__ void __launch_bounds__(Shape<F32 || INT8, INT8>::THREADS, 1)
 #pragma unroll
           for (int j = 0; j < 8; ++j) {
             const int at = (j >> 2) * (CW / 2) + 4 * k + (j & 3);
-            r[at] = (float)x[at] * (sx[j & 1] * sw[(j >> 2) * 2 + ((j >> 1) & 1)]);
+            r[at] = x[at] * (sx[j & 1] * sw[(j >> 2) * 2 + ((j >> 1) & 1)]);
           }
         }
       } else {
@@ -752,44 +758,87 @@ __global__ void __launch_bounds__(Shape<F32 || INT8, INT8>::THREADS, 1)
       const int live = min(np, t.cnt - first);  // columns of this part that are outputs
       uint32_t b = 0;
       if constexpr (PROMOTE) {
-        S held[4][32];
+        float held[4][32];  // integers: as `whole` says, their bits
 #pragma unroll
         for (int c = 0; c < 4; ++c)
 #pragma unroll
-          for (int i = 0; i < 32; ++i) held[c][i] = 0;
+          for (int i = 0; i < 32; ++i) held[c][i] = 0.f;
         constexpr int SEG = INT8 ? SEG_INT : SEG_F32;
+        bool whole = false;
+        // Adds the accumulator, 16 columns at a time; with registers to spare (not of integers) the next
+        // ones are on their way meanwhile (4095 rows of 2048 x 1408, both gradients: 36.9 us, 37.9 without).
+        auto add = [&](auto&& sum) {
+          constexpr int AHEAD = INT8 ? 0 : 1;
+          uint32_t r[1 + AHEAD][16];
+          auto fetch = [&](int c) {
+            const uint32_t ta = lanes + b * 256 + (uint32_t)(first + 16 * c);
+            tc05::ld_16x256b_x2(ta, r[c & AHEAD]);
+            tc05::ld_16x256b_x2(ta + (16u << 16), r[c & AHEAD] + 8);
+          };
+          if (AHEAD && live > 0) fetch(0);
+#pragma unroll
+          for (int c = 0; c < 8; ++c) {
+            if (16 * c >= live) break;
+            if (!AHEAD) fetch(c);
+            tc05::wait_ld16(r[c & AHEAD]);
+            if (AHEAD && c < 7 && 16 * (c + 1) < live) fetch(c + 1);
+#pragma unroll
+            for (int i = 0; i < 16; i += 2)
+              sum(held[c >> 1] + (i >> 3) * 16 + (c & 1) * 8 + (i & 7), __uint_as_float(r[c & AHEAD][i]),
+                  __uint_as_float(r[c & AHEAD][i + 1]));
+          }
+        };
         for (int k = steps.from; k < steps.to; k += SEG) {
           b = v % BUFS;
           ok = __all_sync(0xffffffffu, wait(&tfull[b], (v / BUFS) & 1));
           if (!ok) break;
           ++v;
           tc05::fence_after_sync();
-#pragma unroll
-          for (int c = 0; c < 4; ++c) {
-            if (32 * c < live) {
-              uint32_t r[32];
-              const uint32_t ta = lanes + b * 256 + (uint32_t)(first + 32 * c);
-              tc05::ld_16x256b_x4(ta, r);
-              tc05::ld_16x256b_x4(ta + (16u << 16), r + 16);
-              tc05::wait_ld32(r);
-#pragma unroll
-              for (int i = 0; i < 32; ++i) {
-                const float x = __uint_as_float(r[i]);
-                held[c][i] += INT8 ? (S)__float2int_rn(x) : (S)x;
-              }
-            }
+          if (INT8 && whole) {
+            add([](float* h, float x0, float x1) {
+              h[0] = __int_as_float(__float_as_int(h[0]) + __float2int_rn(x0));
+              h[1] = __int_as_float(__float_as_int(h[1]) + __float2int_rn(x1));
+            });
+          } else if (INT8) {
+            add([](float* h, float x0, float x1) { f2unpack(f2add(f2pack(h[0], h[1]), f2pack(x0, x1)), h[0], h[1]); });
+          } else {
+            add([](float* h, float x0, float x1) {
+              h[0] += x0;
+              h[1] += x1;
+            });
           }
           give_back(b);
+          if (INT8 && !whole) {
+            // While the MMAs go on: may the next segment be added in fp32?
+            const bool end = k + SEG >= steps.to;
+            float top = 0.f;
+            if (!end)
+#pragma unroll
+              for (int c = 0; c < 4; ++c)
+                if (32 * c < live)
+#pragma unroll
+                  for (int i = 0; i < 32; ++i) top = fmaxf(top, fabsf(held[c][i]));
+            whole = __any_sync(0xffffffffu, top > ROOM) || (KS > 1 && end);  // several pairs' sums may be large
+            if (whole)
+#pragma unroll
+              for (int c = 0; c < 4; ++c)
+                if (32 * c < live)
+#pragma unroll
+                  for (int i = 0; i < 32; ++i) held[c][i] = __int_as_float(__float2int_rn(held[c][i]));
+          }
         }
         if (!ok) break;
 #pragma unroll
         for (int c = 0; c < 4; ++c) {
           if (32 * c >= live) break;
           if constexpr (KS == 1) {
+            if (INT8 && whole)
+#pragma unroll
+              for (int i = 0; i < 32; ++i) held[c][i] = (float)__float_as_int(held[c][i]);
             put_out(t, c, held[c]);
           } else {
 #pragma unroll
-            for (int i = 0; i < 32; ++i) parts[part_at(c, i)] = held[c][i];
+            for (int i = 0; i < 32; ++i) parts[part_at(c, i)] = reinterpret_cast<const S&>(held[c][i]);
           }
         }
       } else {
@@ -856,7 +905,10 @@ __global__ void __launch_bounds__(Shape<F32 || INT8, INT8>::THREADS, 1)
               }
             }
           }
-          put_out(t, c, x);
+          float sums[CW];
+#pragma unroll
+          for (int i = 0; i < CW; ++i) sums[i] = (float)x[i];
+          put_out(t, c, sums);
         }
       }
       __syncwarp();
@@ -931,22 +983,22 @@ long long row_tiles(int M, int E, bool grouped, int tile) {
 //   forward    287  234  201  201  199     below 160 columns the way of a stage through the ring
 //   input      289  250  241  241  239
 //   weights    285    -  304  304    -
-//   integers   512    -    -    -  370
-// A unit takes its steps, or its way out; a launch 4.5 us and the last unit's way out besides.
+//   integers   356  308  285    -  269
+// A unit takes its steps, or its way out; a launch 4.5 us (integers 5.5) and the last unit's way out besides.
 enum Kind { K_FORWARD, K_INPUT, K_WEIGHTS, K_INTEGERS };
 long long unit_ns(long long steps, int n, Kind kind) {
-  constexpr int LEAST[] = {200, 240, 285, 370};
-  const int by_columns = kind == K_INTEGERS ? 228 + n * 10 / 9 : 75 + n * 5 / 6;
+  constexpr int LEAST[] = {200, 240, 285, 269};
+  const int by_columns = kind == K_INTEGERS ? 190 + n * 2 / 3 : 75 + n * 5 / 6;
   const long long loop = steps * (by_columns > LEAST[kind] ? by_columns : LEAST[kind]), out = 5 * n;
   return loop > out ? loop : out;
 }
-long long launch_ns(int n) { return 4500 + 8 * n; }
+long long launch_ns(int n, bool int8 = false) { return int8 ? 5500 + 10 * n : 4500 + 8 * n; }
 
 // Clusters of KS pairs that run at a time: a pair has two neighbouring SMs, and a cluster lies in
 // one of the GPU's parts of 18 to 20 SMs.
 long long clusters_of(int ks, int pairs) { return ks == 4 ? pairs / 5 : ks == 2 ? pairs * 2 / 5 : pairs; }
-// What joining a shared contraction takes.
-long long join_ns(int ks) { return ks > 1 ? 1500 : 0; }
+// What joining a shared contraction takes (integers: 32 rows of 2048 x 8192 2.4 us, 256 rows 5.3).
+long long join_ns(int ks, int n = 0) { return ks > 1 ? (n ? 1700 + 13 * n : 1500) : 0; }
 
 struct Plan {
   int tile, tile_w, ks;
@@ -963,7 +1015,7 @@ Plan plan_forward(int M, long long a_tiles, long long steps, bool int8, int pair
       if (ks > 1 && (units > room || steps < 4 * ks)) continue;
       const int n = M < tile ? (M + 31) & ~31 : tile;
       const long long c = (units + room - 1) / room * unit_ns((steps + ks - 1) / ks, n, int8 ? K_INTEGERS : K_FORWARD) +
-                          launch_ns(n) + join_ns(ks);
+                          launch_ns(n, int8) + join_ns(ks, int8 ? n : 0);
       if (best.ns < 0 || c < best.ns) best = {tile, 256, ks, c};
     }
   return best;
@@ -1168,12 +1220,12 @@ cudaError_t launch_pair_backward(const GradArgs& a, const PairDevice& dev, cudaS
 }
 
 // Whether the few-row kernel takes a product.  By expert: up to 8 rows an expert on average (1,536 rows
-// of 256 experts 162 us, pairs 171; integers 102 and 250).  Dense: its passes of 8 rows over the weights,
+// of 256 experts 162 us, pairs 171; integers 108 and 130).  Dense: its passes of 8 rows over the weights,
 // from L2 at 10.5 TB/s (integers 6.8), against the pairs' plan:
 //   rows of N x K      few, pairs (us)
-//   48 of 2048 x 2048   7.9,  8.5    but 64:  9.2,  8.5    integers  96: 10.3, 12.2
-//   16 of 8192 x 2048  10.0, 12.1    but 24: 13.2, 12.2    integers  48: 17.4, 17.5
-//   24 of 4096 x 4096  13.1, 13.9    but 32: 16.1, 14.1    integers  48: 15.8, 18.7
+//   48 of 2048 x 2048   7.9,  8.5    but 64:  9.2,  8.5    integers 128: 12.7, 12.9
+//   16 of 8192 x 2048  10.0, 12.1    but 24: 13.2, 12.2    integers  32: 12.2, 13.9 but 48: 17.2, 14.1
+//   24 of 4096 x 4096  13.1, 13.9    but 32: 16.1, 14.1    integers  32: 12.8, 16.1 but 48: 17.9, 16.4
 bool few_rows_take(const ProductArgs& a, bool int8, const PairDevice& dev) {
   if (a.offsets != nullptr) return a.M <= 8LL * a.E;
   if (a.M <= 8) return true;

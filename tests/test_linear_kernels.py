@@ -2,6 +2,9 @@
 and each of them against the 64-bit references, with the tolerances of test_linear_ops.py."""
 
 import math
+import pathlib
+import subprocess
+import sys
 
 import pytest
 import torch
@@ -82,7 +85,7 @@ def test_dense_gated(what, M, N, K, ks):
 @gpu
 @pytest.mark.parametrize("out", [torch.bfloat16, torch.float32])
 @pytest.mark.parametrize("act", ["none", "silu"])
-@pytest.mark.parametrize("M,N,K,ks", [(300, 1024, 1040, 4), (200, 1056, 4112, 4), (130, 4096, 4096, 2), (800, 1056, 2064, 2),
+@pytest.mark.parametrize("M,N,K,ks", [(300, 1024, 1552, 4), (200, 1056, 4112, 4), (130, 4096, 4096, 2), (800, 1056, 2576, 2),
                                       (100, 8192, 2064, 1), (1000, 1056, 272, 1)])
 def test_dense_integers(out, act, M, N, K, ks):
     assert plan(INTEGERS, M, N, K)[0] == ks
@@ -97,6 +100,26 @@ def test_dense_integers(out, act, M, N, K, ks):
         near(y, v, off + half_step(y, v.abs() + off))
     else:
         near(y, *check_gated(y, v[:, :width], v[:, width:], off[:, :width], off[:, width:], act))
+
+
+@gpu
+@pytest.mark.parametrize("M,N,K,ks", [(300, 1024, 8208, 4), (800, 1056, 4112, 2), (2100, 2048, 4112, 1)])
+def test_integer_sums_small_and_large(M, N, K, ks):
+    """Sums that stay below 2^21, pass it in the first or in a later segment, or return, side by side."""
+    d = dev()
+    assert plan(INTEGERS, M, N, K)[0] == ks
+    level = torch.tensor([3, 18, -18, 40, 127, -128, 18], dtype=torch.int8)
+    a = level[torch.arange(M) // 64 % 7][:, None].repeat(1, K)
+    a[64 * 6:64 * 7, K // 2:] *= -1
+    a[::5] = torch.randint(-128, 128, (len(a[::5]), K), generator=gen(M), dtype=torch.int8)
+    b = torch.randint(0, 128, (1, N, K), generator=gen(N), dtype=torch.int8)
+    b[0, ::3] = torch.randint(-128, 128, (len(b[0, ::3]), K), generator=gen(K), dtype=torch.int8)
+    b[0, 40:44] = -128
+    a, b = a.to(d), b.to(d)
+    y, ones = torch.empty(M, N, device=d), torch.ones(max(M, N), device=d)
+    F.integer_gemm(a, ones[:M], b, ones[None, :N].contiguous(), y)
+    done()
+    assert torch.equal(y, R.integer_sums(a, b).float())
 
 
 @gpu
@@ -183,3 +206,47 @@ def test_captured_shared_contractions_at_once():
     for o, w in zip(outs, want):
         for a, b in zip(o, w):
             assert torch.equal(a, b)
+
+
+FIRST_CALL_CAPTURED = """
+import torch
+from moe_decode_router_gb300 import flint_moe as F
+d = torch.device("cuda:0")
+bf = dict(device=d, dtype=torch.bfloat16)
+F.load_library()
+ids = torch.tensor([[0], [1], [1], [0]], dtype=torch.int32, device=d)
+offsets, order, pos = (torch.empty(s, dtype=torch.int32, device=d) for s in (3, 4, (4, 1)))
+F.group_pairs(ids, offsets, order, pos)  # sets up the library
+x, w, dy = torch.randn(300, 256, **bf), torch.randn(1, 512, 256, **bf), torch.randn(300, 512, **bf)
+outs = [torch.zeros(300, 512, **bf), torch.zeros(300, 256, **bf), torch.zeros(1, 512, 256, **bf),
+        torch.zeros(300, 256, **bf), torch.zeros(2, 512, **bf), torch.zeros(300, 256, dtype=torch.int8, device=d),
+        torch.zeros(300, device=d)]
+
+
+def run():
+    F.linear(x, w, outs[0])
+    F.linear_backward(dy, x, w, outs[1], outs[2])
+    F.gated_linear(x, w, outs[3])
+    F.linear(x[:2], w, outs[4])
+    F.integer_quantize_rows(x, outs[5], outs[6])
+
+
+g = torch.cuda.CUDAGraph()
+with torch.cuda.graph(g):
+    run()
+assert not any(bool(o.any()) for o in outs)
+g.replay()
+torch.cuda.synchronize()
+got = [o.clone() for o in outs]
+run()
+torch.cuda.synchronize()
+assert all(torch.equal(a, b) and bool(a.any()) for a, b in zip(got, outs)) and F.device_error() == 0
+"""
+
+
+@gpu
+def test_first_products_may_be_captured():
+    """Once any call has set up the library, the first call of every product may be on a capturing stream."""
+    r = subprocess.run([sys.executable, "-c", FIRST_CALL_CAPTURED], capture_output=True, text=True, timeout=300,
+                       cwd=pathlib.Path(__file__).resolve().parents[1])
+    assert r.returncode == 0, r.stderr
