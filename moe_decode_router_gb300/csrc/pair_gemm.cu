@@ -70,7 +70,7 @@ constexpr int SEG_F32 = 8, SEG_INT = 7;  // steps (of 64; integers: of 128) betw
 constexpr int OFF_GROUPS = OFF_BARS + 256;
 constexpr int pair_smem(int E) { return OFF_GROUPS + (3 * E + 1) * 4; }
 static_assert(pair_smem(ROUTE_MAX_E) <= 232448, "shared memory");
-static_assert((3 * RING + CODES + 4) * 8 + 8 <= 256, "barriers");
+static_assert((3 * RING + CODES + 5) * 8 + 8 <= 256, "barriers");
 
 // Warps and registers.  A kernel that adds up its accumulators has 8 output warps, which hold
 // 128 sums a thread and take registers that the others give up (a block is launched with LAUNCH
@@ -170,7 +170,8 @@ __global__ void __launch_bounds__(Shape<F32 || INT8, INT8>::THREADS, 1)
   constexpr int STAGES = INT8 ? TURNED : RING, BUFS = INT8 ? 1 : 2;
   constexpr bool PROMOTE = F32 || INT8;
   using W = Shape<PROMOTE, INT8>;
-  constexpr int THREADS = W::THREADS, PRODUCER = W::OUT_WARPS, ISSUER = PRODUCER + 1, ZEROS = PRODUCER + 2;
+  constexpr int THREADS = W::THREADS, PRODUCER = W::OUT_WARPS, ISSUER = PRODUCER + 1, ZEROS = PRODUCER + 2,
+                KEEPER = PRODUCER + 3;
   static_assert(!INT8 || MODE == FORWARD, "integers have no gradient");
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   uint8_t* sm = smem_raw;
@@ -185,7 +186,8 @@ __global__ void __launch_bounds__(Shape<F32 || INT8, INT8>::THREADS, 1)
   uint64_t* taken = landed + RING;                              // [CODES] integers: codes turned
   uint64_t* tfull = taken + CODES;                              // [2] accumulator complete
   uint64_t* tempty = tfull + 2;                                 // [2] accumulator read, by both CTAs' output warps (even CTA's)
-  uint32_t* tslot = reinterpret_cast<uint32_t*>(tempty + 2);
+  uint64_t* taken_mem = tempty + 2;                             // tensor memory taken, by both CTAs
+  uint32_t* tslot = reinterpret_cast<uint32_t*>(taken_mem + 1);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tslot + 1);
   int* g_units = reinterpret_cast<int*>(sm + OFF_GROUPS);  // [E + 1] units before each group
   int* g_lo = g_units + p.E + 1;                           // [E] first row
@@ -202,6 +204,7 @@ __global__ void __launch_bounds__(Shape<F32 || INT8, INT8>::THREADS, 1)
       mbar_init(&tfull[i], 1);
       mbar_init(&tempty[i], 2 * W::OUT_WARPS);
     }
+    mbar_init(taken_mem, 2);
     *abort_flag = 0;
     fence_mbar_init();
   }
@@ -215,18 +218,8 @@ __global__ void __launch_bounds__(Shape<F32 || INT8, INT8>::THREADS, 1)
       tc05::prefetch_map(&maps.bw2);
     }
   }
-  pdl_wait();
-  // Tensor memory is taken when the grid before this one is gone and (below) given back
-  // before either CTA of a pair ends: taking it may wait without a limit for another's.
-  if (warp == PRODUCER) {
-    tc05::alloc_pair(tslot, 512);
-    tc05::relinquish_pair();
-  }
-  pdl_trigger();
-  if (p.offsets != nullptr)
-    for (int e = tid; e <= p.E; e += THREADS) g_units[e] = __ldg(p.offsets + e);  // all on their way at once
-  __syncthreads();
-  if (warp == PRODUCER) {
+  // The groups' units, by one warp.
+  auto count_units = [&] {
     int base = 0;
     for (int e0 = 0; e0 < p.E; e0 += 32) {
       const int e = e0 + lane;
@@ -253,12 +246,23 @@ __global__ void __launch_bounds__(Shape<F32 || INT8, INT8>::THREADS, 1)
       base += __shfl_sync(0xffffffffu, incl, 31);
     }
     if (lane == 0) g_units[p.E] = base;
-  }
-  tc05::fence_before_sync();
+  };
+  if (p.offsets == nullptr && warp == PRODUCER) count_units();
   __syncthreads();
   tc05::cluster_sync();  // both CTAs' barriers are ready
-  tc05::fence_after_sync();
-  const uint32_t tmem = *tslot;
+  // A dense product's first copies are worked out before the wait.
+  const bool early = p.offsets == nullptr && warp == PRODUCER;
+  auto follow = [] {
+    pdl_wait();
+    pdl_trigger();
+  };
+  if (!early) follow();
+  if (p.offsets != nullptr) {
+    for (int e = tid; e <= p.E; e += THREADS) g_units[e] = __ldg(p.offsets + e);  // all on their way at once
+    __syncthreads();
+    if (warp == PRODUCER) count_units();
+    __syncthreads();
+  }
   const int n_rows_units = g_units[p.E];  // forward, input; behind them the weights'
   const int n_units = n_rows_units + (MODE == BACKWARD ? p.E * p.o_tiles * p.a_tiles : 0);
   // with the contraction shared one unit alone (its operands' memory takes the sums)
@@ -330,6 +334,12 @@ __global__ void __launch_bounds__(Shape<F32 || INT8, INT8>::THREADS, 1)
   };
   // the smallest box of B that holds so many rows: 16 << box_of
   auto box_of = [](int rows) { return rows <= 16 ? 0 : rows <= 32 ? 1 : rows <= 64 ? 2 : 3; };
+  // Tensor memory, when a warp of either CTA has taken it: the copies start meanwhile.
+  auto tensor_memory = [&](bool& ok) -> uint32_t {
+    ok = __all_sync(0xffffffffu, wait(taken_mem, 0));
+    tc05::fence_after_sync();
+    return *reinterpret_cast<volatile uint32_t*>(tslot);
+  };
   const uint32_t base = smem_u32(sm), full0 = tc05::map_rank(smem_u32(full), lead);
   if (warp >= W::OUT_WARPS) {
     if (PROMOTE) tc05::regs_down<W::LOW>();
@@ -342,6 +352,7 @@ __global__ void __launch_bounds__(Shape<F32 || INT8, INT8>::THREADS, 1)
         const int nh = t.n >> 1, oh = t.o0 + (int)rank * nh, sel = box_of(nh);
         const uint32_t bytes = A_BYTES + (2048u << sel);
         const Steps steps = steps_of(t);
+        if (early && u == u0) follow();
         for (int k = steps.from; k < steps.to && lane == 0; ++k) {
           if (!wait(&taken[r], ph ^ 1)) {
             ok = false;
@@ -408,8 +419,9 @@ __global__ void __launch_bounds__(Shape<F32 || INT8, INT8>::THREADS, 1)
         // The weights: a lane has a row, that of its lane of tensor memory (the swizzle puts 8
         // neighbouring rows' pieces in different places).
         const int arow = (warp & 3) * 32 + lane;
-        const uint32_t to = tmem + 256 + ((uint32_t)((warp & 3) * 32) << 16);
-        turn(
+        bool had;
+        const uint32_t to = tensor_memory(had) + 256 + ((uint32_t)((warp & 3) * 32) << 16);
+        if (had) turn(
             [&](uint32_t r, uint32_t s, const Unit&) {
               tc05::fence_after_sync();
               const uint8_t* at = sm + r * STAGE + arow * 128;
@@ -473,6 +485,7 @@ __global__ void __launch_bounds__(Shape<F32 || INT8, INT8>::THREADS, 1)
         const int sel = box_of(nh), boxes = (nh + 63) >> 6;
         const bool both = p.pieces_n && nh == 128, one = p.pieces_n && nh == 64;  // weights: pieces of 64 columns of B
         const uint32_t bytes = A_BYTES + (t.weights ? (uint32_t)boxes * 8192u : 2048u << sel);
+        if (early && u == u0) follow();
         for (int k = steps.from; k < steps.to && lane == 0; ++k) {
           if (!wait(&empty[s], ph ^ 1)) {
             ok = false;
@@ -536,7 +549,8 @@ __global__ void __launch_bounds__(Shape<F32 || INT8, INT8>::THREADS, 1)
       // are warp-uniform values.
       if (rank == 0) {
         uint32_t s = 0, ph = 0, v = 0;
-        bool ok = true;
+        bool ok;
+        const uint32_t tmem = tensor_memory(ok);
         constexpr bool A_ROWS = MODE == BACKWARD;
         constexpr int SEG = INT8 ? SEG_INT : SEG_F32;
         constexpr uint32_t TFULL = (2 * STAGES + RING + CODES) * 8;
@@ -587,6 +601,9 @@ __global__ void __launch_bounds__(Shape<F32 || INT8, INT8>::THREADS, 1)
             }
           }
         }
+        // The last accumulators are given back: no arrival is under way to this CTA when it ends.
+        for (uint32_t j = v - min(v, (uint32_t)BUFS); j < v && ok; ++j)
+          ok = __all_sync(0xffffffffu, wait(&tempty[j % BUFS], (j / BUFS) & 1));
         if (!ok) {  // what has been issued retires before tensor memory goes
           const long long t0 = clock64();
           while (clock64() - t0 < 2000000) {
@@ -618,9 +635,18 @@ __global__ void __launch_bounds__(Shape<F32 || INT8, INT8>::THREADS, 1)
         }
       }
     }
-    if constexpr (KS > 1) {  // the output warps' two barriers
+    if (warp == KEEPER) {
+      // ---------------- tensor memory: taken when the grid before this one is gone and (below) given
+      // back before either CTA of a pair ends, as taking it may wait without a limit for another's.
+      tc05::alloc_pair(tslot, 512);
+      tc05::relinquish_pair();
+      tc05::fence_before_sync();
       __syncwarp();
-      tc05::cluster_sync();
+      if (lane == 0)
+        for (uint32_t c = 0; c < 2; ++c) tc05::arrive_cluster(tc05::map_rank(smem_u32(taken_mem), lead | c));
+    }
+    if constexpr (KS > 1) {  // the output warps' barrier
+      __syncwarp();
       tc05::cluster_sync();
     }
   } else {
@@ -628,11 +654,11 @@ __global__ void __launch_bounds__(Shape<F32 || INT8, INT8>::THREADS, 1)
     // ---------------- output
     const int quad = warp & 3, part = warp >> 2;
     uint8_t* out = sm + OFF_OUT + warp * (OUT_BYTES / W::OUT_WARPS);
-    const uint32_t lanes = tmem + ((uint32_t)(quad * 32) << 16);
+    bool ok;
+    const uint32_t lanes = tensor_memory(ok) + ((uint32_t)(quad * 32) << 16);
     const uint32_t tempty0 = tc05::map_rank(smem_u32(tempty), lead);
     const int g = lane >> 2, q = lane & 3;
     uint32_t v = 0;
-    bool ok = true;
     // The accumulator is in registers (or in shared memory): back to the MMAs.
     auto give_back = [&](uint32_t b) {
       tc05::fence_before_sync();
@@ -911,20 +937,20 @@ __global__ void __launch_bounds__(Shape<F32 || INT8, INT8>::THREADS, 1)
           put_out(t, c, sums);
         }
       }
-      __syncwarp();
-      tc05::cluster_sync();  // the other pairs have read this one's
     }
   }
+  // Nothing is under way to either CTA any more: every arrival and copy has been waited for.  So the
+  // barriers publish nothing (a release would wait for the outputs to land): all sums have been
+  // read, by the other pairs too; tensor memory is given back.
   __syncwarp();
   tc05::fence_before_sync();
-  __syncthreads();
-  tc05::cluster_sync();  // no arrival or copy is under way to either CTA any more
-  if (warp == PRODUCER) {
+  tc05::cluster_meet();
+  if (warp == KEEPER) {
     tc05::fence_after_sync();
-    tc05::dealloc_pair(tmem, 512);
+    tc05::dealloc_pair(*tslot, 512);
   }
   __syncwarp();
-  tc05::cluster_sync();
+  tc05::cluster_meet();
 }
 
 EncodeTiled g_encode = nullptr;  // set once, under the caller's lock
@@ -984,7 +1010,7 @@ long long row_tiles(int M, int E, bool grouped, int tile) {
 //   input      289  250  241  241  239
 //   weights    285    -  304  304    -
 //   integers   356  308  285    -  269
-// A unit takes its steps, or its way out; a launch 4.5 us (integers 5.5) and the last unit's way out besides.
+// A unit takes its steps, or its way out; a launch 3 us (integers 3.5) and the last unit's way out besides.
 enum Kind { K_FORWARD, K_INPUT, K_WEIGHTS, K_INTEGERS };
 long long unit_ns(long long steps, int n, Kind kind) {
   constexpr int LEAST[] = {200, 240, 285, 269};
@@ -992,13 +1018,13 @@ long long unit_ns(long long steps, int n, Kind kind) {
   const long long loop = steps * (by_columns > LEAST[kind] ? by_columns : LEAST[kind]), out = 5 * n;
   return loop > out ? loop : out;
 }
-long long launch_ns(int n, bool int8 = false) { return int8 ? 5500 + 10 * n : 4500 + 8 * n; }
+long long launch_ns(int n, bool int8 = false) { return int8 ? 3500 + 10 * n : 3000 + 8 * n; }
 
 // Clusters of KS pairs that run at a time: a pair has two neighbouring SMs, and a cluster lies in
 // one of the GPU's parts of 18 to 20 SMs.
 long long clusters_of(int ks, int pairs) { return ks == 4 ? pairs / 5 : ks == 2 ? pairs * 2 / 5 : pairs; }
-// What joining a shared contraction takes (integers: 32 rows of 2048 x 8192 2.4 us, 256 rows 5.3).
-long long join_ns(int ks, int n = 0) { return ks > 1 ? (n ? 1700 + 13 * n : 1500) : 0; }
+// What joining a shared contraction takes (integers: 32 rows of 2048 x 8192 1.7 us, 256 rows 4.2).
+long long join_ns(int ks, int n = 0) { return ks > 1 ? (n ? 1300 + 11 * n : 2000) : 0; }
 
 struct Plan {
   int tile, tile_w, ks;
@@ -1202,8 +1228,8 @@ cudaError_t launch_pair_backward(const GradArgs& a, const PairDevice& dev, cudaS
   if (a.offsets != nullptr) return launch_backward(a, Plan{256, 256, 1, 0}, dev, st);
   const Plan plan = plan_backward(a.M, a.N, a_tiles, dx, dw, pairs, dev.most_ks);
   if (dx && dw) {
-    // Long units of one and short ones of the other fill a launch badly: 16 rows of 8192 x 2048 take 43
-    // us in one and 28 in two, each with its own share of the contraction a cluster.
+    // Long units of one and short ones of the other fill a launch badly: 16 rows of 8192 x 2048 take 41
+    // us in one and 25 in two, each with its own share of the contraction a cluster.
     const Plan one = plan_backward(a.M, a.N, a_tiles, true, false, pairs, dev.most_ks);
     const Plan two = plan_backward(a.M, a.N, a_tiles, false, true, pairs, dev.most_ks);
     if (one.ns + two.ns < plan.ns) {
@@ -1223,9 +1249,9 @@ cudaError_t launch_pair_backward(const GradArgs& a, const PairDevice& dev, cudaS
 // of 256 experts 162 us, pairs 171; integers 108 and 130).  Dense: its passes of 8 rows over the weights,
 // from L2 at 10.5 TB/s (integers 6.8), against the pairs' plan:
 //   rows of N x K      few, pairs (us)
-//   48 of 2048 x 2048   7.9,  8.5    but 64:  9.2,  8.5    integers 128: 12.7, 12.9
-//   16 of 8192 x 2048  10.0, 12.1    but 24: 13.2, 12.2    integers  32: 12.2, 13.9 but 48: 17.2, 14.1
-//   24 of 4096 x 4096  13.1, 13.9    but 32: 16.1, 14.1    integers  32: 12.8, 16.1 but 48: 17.9, 16.4
+//   32 of 2048 x 2048   6.3,  7.3    but 48:  8.3,  7.0    integers  64:  7.1,  8.5 but 128: 12.6, 10.3
+//   16 of 8192 x 2048   9.8, 10.1    but 24: 13.8, 10.1    integers  24:  9.7, 11.7 but  40: 14.7, 12.4
+//   16 of 4096 x 4096  10.4, 11.1    but 24: 14.2, 11.3    integers  32: 12.7, 13.4 but  40: 15.5, 13.5
 bool few_rows_take(const ProductArgs& a, bool int8, const PairDevice& dev) {
   if (a.offsets != nullptr) return a.M <= 8LL * a.E;
   if (a.M <= 8) return true;

@@ -28,7 +28,7 @@ def plan(what, M, N, K, sms=None):
 def test_every_plan_is_chosen():
     """On 152 SMs, by the cases below and the measured crossings."""
     assert plan(FORWARD, 8, 8192, 2048, 152) == 0 and plan(INTEGERS, 8, 64, 16, 152) == 0
-    assert plan(FORWARD, 48, 2048, 2048, 152) == 0 and plan(FORWARD, 64, 2048, 2048, 152)[0] == 4
+    assert plan(FORWARD, 24, 2048, 2048, 152) == 0 and plan(FORWARD, 64, 2048, 2048, 152)[0] == 4
     assert plan(INTEGERS, 64, 2048, 2048, 152) == 0 and plan(INTEGERS, 128, 2048, 2048, 152)[0] == 4
     assert plan(FORWARD, 64, 4096, 4096, 152)[0] == 2 and plan(INTEGERS, 96, 4096, 4096, 152)[0] == 2
     assert plan(FORWARD, 64, 8192, 2048, 152)[0] == 1
@@ -55,8 +55,8 @@ def twice(call, outs):
 
 
 # what, rows, N, K, pairs that share a contraction
-SHARED = [(FORWARD, 256, 1032, 1040, 4), (FORWARD, 70, 2048, 2064, 4), (FORWARD, 300, 416, 4112, 4), (FORWARD, 129, 4104, 4096, 2),
-          (FORWARD, 700, 1032, 1552, 2), (FORWARD, 90, 8192, 2064, 1), (FORWARD, 1000, 1056, 272, 1)]
+SHARED = [(FORWARD, 256, 1032, 1552, 4), (FORWARD, 70, 2048, 2064, 4), (FORWARD, 300, 416, 4112, 4), (FORWARD, 129, 4104, 4096, 2),
+          (FORWARD, 700, 1032, 2064, 2), (FORWARD, 256, 1032, 1040, 1), (FORWARD, 90, 8192, 2064, 1), (FORWARD, 1000, 1056, 272, 1)]
 
 
 @gpu
