@@ -44,8 +44,8 @@
 // every call.
 //
 // Warps: output (the first 8 or 16, a quarter of the lanes and a part of the columns each); then the
-// TMA producer; the MMA issuer (of the even CTA); rows behind the end; none; integers: four
-// and four that turn codes to fp16.
+// TMA producer; the MMA issuer (of the even CTA); rows behind the end; tensor memory;
+// integers: four and four that turn codes to fp16.
 #include <initializer_list>
 
 #include "product_common.cuh"
