@@ -100,6 +100,8 @@ struct PairArgs {
   int a_tiles;    // units side by side in i
   int tile;       // forward, input: o's of a unit, at most (a multiple of 32); grouped: 256
   int row_tiles;  // dense: units side by side in o
+  int units;      // dense: of the forward product or dx
+  int rows;       // dense: rows, and from bit 26 a tile's rows / 32
   int tile_w;     // weights: o's of a unit, at most
   int o_tiles;    // weights: units side by side in o, 0: not wanted
   unsigned per_band, per_expert;  // reciprocals of BAND * a_tiles and of o_tiles * a_tiles
@@ -109,10 +111,9 @@ struct PairArgs {
 
 // Tiles of o that go side by side, with all of i: what runs at a time shares both operands.
 constexpr int BAND = 8;
-// x / n for x below 9,000 is x * SMALL[n] >> 16.
-__constant__ unsigned SMALL[BAND + 1] = {0,         65536,         65536 / 2 + 1, 65536 / 3 + 1, 65536 / 4 + 1,
-                                         65536 / 5 + 1, 65536 / 6 + 1, 65536 / 7 + 1, 65536 / 8 + 1};
-static_assert(BAND * ((1 << 17) / 256) < 9000, "a band's units");
+// x / n for n up to BAND: (x + 1/2) / n is 1/16 at least from a whole number, and off by less than 2^-20 of itself.
+__device__ __forceinline__ int small_quotient(int x, int n) { return (int)__fdividef((float)x + 0.5f, (float)n); }
+static_assert(BAND <= 8 && BAND * ((1 << 17) / 256) < 1 << 14, "a band's units");
 // x / n from n's reciprocal, 2^32 / n rounded up (0 for n = 1): too large by one at most.
 __device__ __forceinline__ int quotient(int x, unsigned recip, int n) {
   if (n == 1) return x;
@@ -225,8 +226,8 @@ __global__ void __launch_bounds__(Shape<F32 || INT8, INT8>::THREADS, 1)
       const int e = e0 + lane;
       int lo = 0, cnt = 0;
       if (e < p.E) {
-        lo = p.offsets ? min(max(g_units[e], 0), p.M) : 0;
-        cnt = p.offsets ? min(max(g_units[e + 1], lo), p.M) - lo : p.M;
+        lo = min(max(g_units[e], 0), p.M);
+        cnt = min(max(g_units[e + 1], lo), p.M) - lo;
         // a group's tiles are of one size, to 32 rows
         const int tiles = (cnt + p.tile - 1) / p.tile;
         g_lo[e] = lo;
@@ -247,7 +248,12 @@ __global__ void __launch_bounds__(Shape<F32 || INT8, INT8>::THREADS, 1)
     }
     if (lane == 0) g_units[p.E] = base;
   };
-  if (p.offsets == nullptr && warp == PRODUCER) count_units();
+  if (p.offsets == nullptr && tid == 64) {
+    g_units[0] = 0;
+    g_units[1] = p.units;
+    g_lo[0] = 0;
+    g_cnt[0] = p.rows;
+  }
   __syncthreads();
   tc05::cluster_sync();  // both CTAs' barriers are ready
   // A dense product's first copies are worked out before the wait.
@@ -294,7 +300,7 @@ __global__ void __launch_bounds__(Shape<F32 || INT8, INT8>::THREADS, 1)
     if (!t.weights) tiles = p.offsets != nullptr ? (rows + 255) >> 8 : p.row_tiles;
     const int per = BAND * p.a_tiles, band = quotient(v, p.per_band, per), rest = v - band * per;
     const int high = min(BAND, tiles - band * BAND);
-    t.at = (int)((unsigned)rest * SMALL[high] >> 16);
+    t.at = small_quotient(rest, high);
     const int tile = band * BAND + rest - t.at * high;
     if (t.weights) {
       t.o0 = tile * p.tile_w;
@@ -1138,6 +1144,17 @@ cudaError_t pair_gemm_kernels_init(int* most_ks) {
   return cudaSuccess;
 }
 
+namespace {
+
+// A dense product's tiles of rows, all of one size, to 32.
+void dense_rows(PairArgs& p) {
+  p.row_tiles = (p.M + p.tile - 1) / p.tile;
+  p.units = p.y != nullptr ? p.row_tiles * p.a_tiles : 0;
+  p.rows = p.M | ((p.M + p.row_tiles - 1) / p.row_tiles + 31) >> 5 << 26;
+}
+
+}  // namespace
+
 cudaError_t launch_pair_forward(const ProductArgs& a, bool int8, const PairDevice& dev, cudaStream_t st) {
   const bool gated = a.act != FFN_NONE;
   const uint64_t M = a.M, N = a.N, K = a.K, E = a.E;
@@ -1157,7 +1174,7 @@ cudaError_t launch_pair_forward(const ProductArgs& a, bool int8, const PairDevic
                                          : Plan{256, 256, 1, 0};
   p.tile = plan.tile;
   p.act = a.act;
-  p.row_tiles = (a.M + p.tile - 1) / p.tile;
+  dense_rows(p);
   p.per_band = reciprocal(BAND * p.a_tiles);
   Maps m;
   const int size = int8 ? 1 : 2;
@@ -1199,7 +1216,7 @@ cudaError_t launch_backward(const GradArgs& a, const Plan& plan, const PairDevic
   p.tile = plan.tile;
   p.tile_w = plan.tile_w;
   if (a.dw != nullptr) p.o_tiles = (a.N + p.tile_w - 1) / p.tile_w;
-  p.row_tiles = (a.M + p.tile - 1) / p.tile;
+  dense_rows(p);
   p.per_band = reciprocal(BAND * p.a_tiles);
   p.per_expert = reciprocal(a.dw != nullptr ? p.o_tiles * p.a_tiles : 1);
   Maps m;
@@ -1246,12 +1263,12 @@ cudaError_t launch_pair_backward(const GradArgs& a, const PairDevice& dev, cudaS
 }
 
 // Whether the few-row kernel takes a product.  By expert: up to 8 rows an expert on average (1,536 rows
-// of 256 experts 162 us, pairs 171; integers 108 and 130).  Dense: its passes of 8 rows over the weights,
+// of 256 experts 162 us, pairs 168; integers 107 and 131).  Dense: its passes of 8 rows over the weights,
 // from L2 at 10.5 TB/s (integers 6.8), against the pairs' plan:
 //   rows of N x K      few, pairs (us)
-//   32 of 2048 x 2048   6.3,  7.3    but 48:  8.3,  7.0    integers  64:  7.1,  8.5 but 128: 12.6, 10.3
-//   16 of 8192 x 2048   9.8, 10.1    but 24: 13.8, 10.1    integers  24:  9.7, 11.7 but  40: 14.7, 12.4
-//   16 of 4096 x 4096  10.4, 11.1    but 24: 14.2, 11.3    integers  32: 12.7, 13.4 but  40: 15.5, 13.5
+//   32 of 2048 x 2048   6.3,  6.8    but 48:  8.4,  6.4    integers  64:  7.0,  8.2 but 128: 12.7, 10.1
+//   16 of 8192 x 2048   9.9,  9.8    but 24: 13.8,  9.9    integers  24:  9.8, 11.7 but  40: 14.7, 12.3
+//   16 of 4096 x 4096  10.5, 10.9    but 24: 14.2, 11.0    integers  32: 12.8, 13.4 but  40: 15.5, 13.5
 bool few_rows_take(const ProductArgs& a, bool int8, const PairDevice& dev) {
   if (a.offsets != nullptr) return a.M <= 8LL * a.E;
   if (a.M <= 8) return true;
