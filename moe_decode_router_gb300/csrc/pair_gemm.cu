@@ -70,7 +70,7 @@ constexpr int SEG_F32 = 8, SEG_INT = 7;  // steps (of 64; integers: of 128) betw
 constexpr int OFF_GROUPS = OFF_BARS + 256;
 constexpr int pair_smem(int E) { return OFF_GROUPS + (3 * E + 1) * 4; }
 static_assert(pair_smem(ROUTE_MAX_E) <= 232448, "shared memory");
-static_assert((3 * RING + CODES + 5) * 8 + 8 <= 256, "barriers");
+static_assert((3 * RING + CODES + 5) * 8 + 12 <= 256, "barriers");
 
 // Warps and registers.  A kernel that adds up its accumulators has 8 output warps, which hold
 // 128 sums a thread and take registers that the others give up (a block is launched with LAUNCH
@@ -190,6 +190,7 @@ __global__ void __launch_bounds__(Shape<F32 || INT8, INT8>::THREADS, 1)
   uint64_t* taken_mem = tempty + 2;                             // tensor memory taken, by both CTAs
   uint32_t* tslot = reinterpret_cast<uint32_t*>(taken_mem + 1);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tslot + 1);
+  volatile uint32_t* copied = tslot + 2;  // gradients: steps that this CTA's producer has begun
   int* g_units = reinterpret_cast<int*>(sm + OFF_GROUPS);  // [E + 1] units before each group
   int* g_lo = g_units + p.E + 1;                           // [E] first row
   int* g_cnt = g_lo + p.E;                                 // [E] rows, and from bit 26 a tile's rows / 32
@@ -207,6 +208,7 @@ __global__ void __launch_bounds__(Shape<F32 || INT8, INT8>::THREADS, 1)
     }
     mbar_init(taken_mem, 2);
     *abort_flag = 0;
+    *copied = 0;
     fence_mbar_init();
   }
   if (tid == 32) {  // the copies' descriptors, on their way while the grid before this one ends
@@ -532,6 +534,7 @@ __global__ void __launch_bounds__(Shape<F32 || INT8, INT8>::THREADS, 1)
               for (int i = 0; i < boxes; ++i) tc05::tma_pair_2d(b + i * 8192, &maps.bw, oh + i * 64, c, bar);
           }
           ++issued;
+          if (MODE == BACKWARD) *copied = issued;
           if (++s == STAGES) {
             s = 0;
             ph ^= 1;
@@ -621,13 +624,25 @@ __global__ void __launch_bounds__(Shape<F32 || INT8, INT8>::THREADS, 1)
       if (MODE == BACKWARD) {
         uint32_t g = 0, parity = 0;  // steps so far; of `landed`, a bit a stage
         bool ok = true;
+        // The units before the one that is waited for (all of dx's among them) may take longer than a
+        // wait's limit: it begins anew while the producer, each of whose waits is for one step, gets on.
+        auto wait_behind = [&](uint64_t* bar, uint32_t phase) -> bool {
+          uint32_t seen = *copied;
+          while (!mbar_wait(bar, phase)) {
+            const uint32_t now = *copied;
+            if (*abort_flag) return false;
+            if (now == seen) return wait(bar, phase);
+            seen = now;
+          }
+          return true;
+        };
         for (int u = u0; u < n_units && ok; u += ustep) {
           const Unit t = unit_of(u);
           const Steps steps = steps_of(t);
           g += steps.to - steps.from;
           if (!(t.clen & 15) || steps.from == steps.to || steps.to < steps.all) continue;  // clen: 0 of what are not weights
           const uint32_t s = (g - 1) % STAGES;
-          ok = __all_sync(0xffffffffu, wait(&landed[s], (parity >> s) & 1));
+          ok = __all_sync(0xffffffffu, wait_behind(&landed[s], (parity >> s) & 1));
           if (!ok) break;
           parity ^= 1u << s;
           // a row of every piece of both operands: 8 lanes each
