@@ -10,7 +10,9 @@
 // 16 t .. 16 t + 15 of each 64 for either operand (8 bf16 or 16 integers: two mma).
 // DEEP pieces of 128 bytes a row (2 KB of weights a warp each) are under way at a time.
 // Every SPLIT-th piece of K is a warp's; SPLIT warps of a CTA share their rows and add
-// their sums in the warps' order, so that a small product has enough warps.  A dense
+// their sums in the warps' order, so that a small product has enough warps.  The tensor cores cut a
+// sum of bf16 products instead of rounding it (2^17 into one accumulator lost 7e-4 of it): where a
+// warp has more than ALONE, each pass's products begin from zero and are added in fp32.  A dense
 // product asks for its first weights before it waits for the kernel before it: into L2
 // alone, where a write of that kernel would still reach them.
 //
@@ -50,6 +52,7 @@ template <bool INT8, bool GATED, int SPLIT, int WARPS, int DEEP>
 __global__ void __launch_bounds__(WARPS * 32, (DEEP > 2 ? 16 : 24) / WARPS) few_rows_kernel(const ProductArgs p) {
   using S = typename Sum<INT8>::type;
   constexpr int SIZE = INT8 ? 1 : 2;
+  constexpr bool ROUND = !INT8 && DEEP > 2;
   __shared__ S red[SPLIT == 1 ? 1 : WARPS][128];
   __shared__ int range[3];
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -110,11 +113,15 @@ __global__ void __launch_bounds__(WARPS * 32, (DEEP > 2 ? 16 : 24) / WARPS) few_
         x[i][0] = in0 ? __ldg(reinterpret_cast<const uint4*>(a0 + k0)) : zero;
         x[i][1] = in1 ? __ldg(reinterpret_cast<const uint4*>(a0 + k1)) : zero;
       }
+      S part[4] = {0, 0, 0, 0};
 #pragma unroll
       for (int i = 0; i < U; ++i) {
-        mma_k64(acc, v[i][0], v[i][1], x[i][0]);
-        mma_k64(acc, v[i][2], v[i][3], x[i][1]);
+        mma_k64(ROUND ? part : acc, v[i][0], v[i][1], x[i][0]);
+        mma_k64(ROUND ? part : acc, v[i][2], v[i][3], x[i][1]);
       }
+      if (ROUND)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) acc[i] += part[i];
     }
   }
   auto put = [&](void* base, size_t at, float v) {
@@ -191,13 +198,21 @@ cudaError_t launch(const ProductArgs& p, cudaStream_t st) {
 //   dense, a warp's share of  8 of 8, 4    bf16 4 x 2048 x 8192 8.8 (2 pieces: 9.8), 1 x 2048 x 2048 3.3 (3.6)
 //     K is 4 pieces and more
 //   dense, less               8 of 8, 2    integers 8 x 8192 x 2048 5.5 (4 pieces: 7.5)
+// Shapes of 2 pieces have no registers for another set of sums (48 rows took 30.8 us with it, 28.8
+// without), so their warps have up to ALONE products; a longer contraction by expert takes 4.
+constexpr int ALONE = 1024;
 template <bool INT8, bool GATED>
 cudaError_t launch_shape(const ProductArgs& p, cudaStream_t st) {
   if (p.offsets == nullptr)
     return (long long)p.K * (INT8 ? 1 : 2) >= 8 * 4 * 128 ? launch<INT8, GATED, 8, 8, 4>(p, st)
                                                            : launch<INT8, GATED, 8, 8, 2>(p, st);
-  if (p.M <= 16) return launch<INT8, GATED, 8, 8, 2>(p, st);
-  if (p.M <= 128) return launch<INT8, GATED, 4, 4, 2>(p, st);
+  if (p.M <= 16)
+    return !INT8 && p.K > 8 * ALONE ? launch<INT8, GATED, 8, 8, 4>(p, st) : launch<INT8, GATED, 8, 8, 2>(p, st);
+  if (p.M <= 128) {
+    if constexpr (!INT8)
+      if (p.K > 4 * ALONE) return launch<INT8, GATED, 4, 4, 4>(p, st);
+    return launch<INT8, GATED, 4, 4, 2>(p, st);
+  }
   return launch<INT8, GATED, 1, 4, 4>(p, st);
 }
 
