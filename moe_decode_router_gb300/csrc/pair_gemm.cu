@@ -190,7 +190,7 @@ __global__ void __launch_bounds__(Shape<F32 || INT8, INT8>::THREADS, 1)
   uint64_t* taken_mem = tempty + 2;                             // tensor memory taken, by both CTAs
   uint32_t* tslot = reinterpret_cast<uint32_t*>(taken_mem + 1);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tslot + 1);
-  volatile uint32_t* copied = tslot + 2;  // gradients: steps that this CTA's producer has begun
+  volatile uint32_t* begun = tslot + 2;  // gradients: the unit that this CTA's producer has begun, + 1
   int* g_units = reinterpret_cast<int*>(sm + OFF_GROUPS);  // [E + 1] units before each group
   int* g_lo = g_units + p.E + 1;                           // [E] first row
   int* g_cnt = g_lo + p.E;                                 // [E] rows, and from bit 26 a tile's rows / 32
@@ -208,7 +208,7 @@ __global__ void __launch_bounds__(Shape<F32 || INT8, INT8>::THREADS, 1)
     }
     mbar_init(taken_mem, 2);
     *abort_flag = 0;
-    *copied = 0;
+    *begun = 0;
     fence_mbar_init();
   }
   if (tid == 32) {  // the copies' descriptors, on their way while the grid before this one ends
@@ -493,6 +493,7 @@ __global__ void __launch_bounds__(Shape<F32 || INT8, INT8>::THREADS, 1)
         const int sel = box_of(nh), boxes = (nh + 63) >> 6;
         const bool both = p.pieces_n && nh == 128, one = p.pieces_n && nh == 64;  // weights: pieces of 64 columns of B
         const uint32_t bytes = A_BYTES + (t.weights ? (uint32_t)boxes * 8192u : 2048u << sel);
+        if (MODE == BACKWARD && lane == 0) *begun = (uint32_t)u + 1;
         if (early && u == u0) follow();
         for (int k = steps.from; k < steps.to && lane == 0; ++k) {
           if (!wait(&empty[s], ph ^ 1)) {
@@ -534,7 +535,6 @@ __global__ void __launch_bounds__(Shape<F32 || INT8, INT8>::THREADS, 1)
               for (int i = 0; i < boxes; ++i) tc05::tma_pair_2d(b + i * 8192, &maps.bw, oh + i * 64, c, bar);
           }
           ++issued;
-          if (MODE == BACKWARD) *copied = issued;
           if (++s == STAGES) {
             s = 0;
             ph ^= 1;
@@ -625,11 +625,12 @@ __global__ void __launch_bounds__(Shape<F32 || INT8, INT8>::THREADS, 1)
         uint32_t g = 0, parity = 0;  // steps so far; of `landed`, a bit a stage
         bool ok = true;
         // The units before the one that is waited for (all of dx's among them) may take longer than a
-        // wait's limit: it begins anew while the producer, each of whose waits is for one step, gets on.
+        // wait's limit: it begins anew while the producer gets on to further units, one of which takes
+        // less (2^24 rows some 0.15e9 cycles of 2e9).
         auto wait_behind = [&](uint64_t* bar, uint32_t phase) -> bool {
-          uint32_t seen = *copied;
+          uint32_t seen = *begun;
           while (!mbar_wait(bar, phase)) {
-            const uint32_t now = *copied;
+            const uint32_t now = *begun;
             if (*abort_flag) return false;
             if (now == seen) return wait(bar, phase);
             seen = now;
