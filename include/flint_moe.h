@@ -415,7 +415,10 @@ int flint_moe_combine(const void *rows, int rows_type, int n_rows, const int32_t
  * and what the inputs hold there is not used.  NULL: dense, n_experts == 1.
  * No workspace is needed, every call is deterministic, and all may be captured
  * into a CUDA graph (the first call of a process on a device sets up the library
- * and must come before the capture).  Sums are fp32 (integer: exact).
+ * and must come before the capture).  Sums are fp32 (integer: exact).  The tensor
+ * cores cut them, by some n 2^-27 of the magnitudes of n terms; sums of more than
+ * 1024 terms (of bf16 outputs: of many more, up to 2^17, where that is a quarter of
+ * the output's rounding) are added up from parts with rounding.
  */
 
 /* Activation of a gated product: none (a plain product), x / (1 + exp(-x)), or

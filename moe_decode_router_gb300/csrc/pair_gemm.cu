@@ -36,7 +36,8 @@
 // 32-bit integers, whose conversions (16 lanes a cycle) are most of the time of the hand-over: 8191 x
 // 4096 x 4096 takes 173 us, 194 with integers from the start.  fp32 outputs of bf16 operands are
 // promoted the same way every 512 of the contracted dimension: the tensor cores cut a sum instead of
-// rounding it, which adds up.
+// rounding it, which adds up (n products of one sign lose some n 2^-27 of their sum: 2^17 a quarter of
+// bf16's rounding, 2^22 2.3 %).  A weights' gradient of more than 2^17 rows is, whatever its type.
 //
 // Where a dense product has units for few pairs alone, KS = 2 or 4 pairs of a cluster share a
 // unit's contraction.  Each leaves its sums in its stages, and after a cluster barrier adds its
@@ -56,6 +57,7 @@ namespace flint {
 namespace {
 
 enum { FORWARD, BACKWARD };
+enum { BF16, F32, BF16_ADDED };  // outputs (of gradients dw); the last two of bf16 operands are promoted
 
 constexpr int A_BYTES = 128 * 128, B_BYTES = 128 * 128, STAGE = A_BYTES + B_BYTES;
 constexpr int RING = 6;            // stages of operands
@@ -66,6 +68,7 @@ constexpr int OUT_BYTES = 8 * 32 * 80;  // output staging: rows of 64 bytes, 80 
 constexpr int OFF_OUT = RING * STAGE;
 constexpr int OFF_BARS = OFF_OUT + OUT_BYTES;
 constexpr int SEG_F32 = 8, SEG_INT = 7;  // steps (of 64; integers: of 128) between promotions
+constexpr int ALONE = 1 << 17;           // products that a bf16 output's accumulator takes without; N and K are no more
 
 constexpr int OFF_GROUPS = OFF_BARS + 256;
 constexpr int pair_smem(int E) { return OFF_GROUPS + (3 * E + 1) * 4; }
@@ -165,11 +168,11 @@ __device__ __forceinline__ void codes_to_f16(const uint4 c, uint4& lo, uint4& hi
   hi = make_uint4(o[4], o[5], o[6], o[7]);
 }
 
-template <int MODE, bool GATED, bool F32, bool INT8, int KS>
-__global__ void __launch_bounds__(Shape<F32 || INT8, INT8>::THREADS, 1)
+template <int MODE, bool GATED, int OUT, bool INT8, int KS>
+__global__ void __launch_bounds__(Shape<OUT != BF16 || INT8, INT8>::THREADS, 1)
     pair_gemm_kernel(const PairArgs p, const __grid_constant__ Maps maps) {
   constexpr int STAGES = INT8 ? TURNED : RING, BUFS = INT8 ? 1 : 2;
-  constexpr bool PROMOTE = F32 || INT8;
+  constexpr bool PROMOTE = OUT != BF16 || INT8;
   using W = Shape<PROMOTE, INT8>;
   constexpr int THREADS = W::THREADS, PRODUCER = W::OUT_WARPS, ISSUER = PRODUCER + 1, ZEROS = PRODUCER + 2,
                 KEEPER = PRODUCER + 3;
@@ -724,7 +727,7 @@ __global__ void __launch_bounds__(Shape<F32 || INT8, INT8>::THREADS, 1)
         for (int i = 0; i < CW; ++i) r[i] = x[i];
       }
       auto f = [&](int h, int k, int j) { return r[CW / 2 * h + 4 * k + j]; };
-      if (GATED && F32) {
+      if (GATED && OUT == F32) {
         float* y = static_cast<float*>(p.y);
 #pragma unroll
         for (int k = 0; k < GROUPS; ++k)
@@ -761,7 +764,7 @@ __global__ void __launch_bounds__(Shape<F32 || INT8, INT8>::THREADS, 1)
           return bf16x2_bits(activation(f(0, k, j), p.act) * f(1, k, j),
                              activation(f(0, k, j + 1), p.act) * f(1, k, j + 1));
         });
-      } else if (F32 && (MODE == FORWARD || t.weights)) {
+      } else if (OUT == F32 && (MODE == FORWARD || t.weights)) {
         float* y = static_cast<float*>(to);
 #pragma unroll
         for (int k = 0; k < GROUPS; ++k)
@@ -994,12 +997,12 @@ bool encode(CUtensorMap* m, int size, const void* base, std::initializer_list<ui
                   CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-template <int MODE, bool GATED, bool F32, bool INT8, int KS>
+template <int MODE, bool GATED, int OUT, bool INT8, int KS>
 cudaError_t launch_split(const PairArgs& p, const Maps& maps, long long most, int sm_count, cudaStream_t st) {
   const long long pairs = KS > 1 ? most : sm_count / 2;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(2u * KS * (unsigned)(most < pairs ? most : pairs));
-  cfg.blockDim = dim3(Shape<F32 || INT8, INT8>::THREADS);
+  cfg.blockDim = dim3(Shape<OUT != BF16 || INT8, INT8>::THREADS);
   cfg.dynamicSmemBytes = pair_smem(p.E);
   cfg.stream = st;
   cudaLaunchAttribute attr[2];
@@ -1011,13 +1014,13 @@ cudaError_t launch_split(const PairArgs& p, const Maps& maps, long long most, in
   attr[1].val.clusterDim.z = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 2;
-  return cudaLaunchKernelEx(&cfg, pair_gemm_kernel<MODE, GATED, F32, INT8, KS>, p, maps);
+  return cudaLaunchKernelEx(&cfg, pair_gemm_kernel<MODE, GATED, OUT, INT8, KS>, p, maps);
 }
-template <int MODE, bool GATED, bool F32, bool INT8 = false>
+template <int MODE, bool GATED, int OUT, bool INT8 = false>
 cudaError_t launch(const PairArgs& p, const Maps& maps, int ks, long long most, int sm_count, cudaStream_t st) {
-  if (ks == 4) return launch_split<MODE, GATED, F32, INT8, 4>(p, maps, most, sm_count, st);
-  if (ks == 2) return launch_split<MODE, GATED, F32, INT8, 2>(p, maps, most, sm_count, st);
-  return launch_split<MODE, GATED, F32, INT8, 1>(p, maps, most, sm_count, st);
+  if (ks == 4) return launch_split<MODE, GATED, OUT, INT8, 4>(p, maps, most, sm_count, st);
+  if (ks == 2) return launch_split<MODE, GATED, OUT, INT8, 2>(p, maps, most, sm_count, st);
+  return launch_split<MODE, GATED, OUT, INT8, 1>(p, maps, most, sm_count, st);
 }
 
 // Tiles of rows that a grouped (or dense) product may have, at most.
@@ -1114,15 +1117,16 @@ cudaError_t pair_gemm_kernels_init(int* most_ks) {
     g_encode = reinterpret_cast<EncodeTiled>(fn);
   }
 #define PAIR_KERNELS(ks)                                                                               \
-  {reinterpret_cast<const void*>(pair_gemm_kernel<FORWARD, true, false, false, ks>), 0},               \
-      {reinterpret_cast<const void*>(pair_gemm_kernel<FORWARD, false, false, false, ks>), 0},          \
-      {reinterpret_cast<const void*>(pair_gemm_kernel<BACKWARD, false, false, false, ks>), 0},         \
-      {reinterpret_cast<const void*>(pair_gemm_kernel<FORWARD, false, true, false, ks>), LAUNCH},      \
-      {reinterpret_cast<const void*>(pair_gemm_kernel<BACKWARD, false, true, false, ks>), LAUNCH},     \
-      {reinterpret_cast<const void*>(pair_gemm_kernel<FORWARD, false, false, true, ks>), LAUNCH_INT},  \
-      {reinterpret_cast<const void*>(pair_gemm_kernel<FORWARD, false, true, true, ks>), LAUNCH_INT},   \
-      {reinterpret_cast<const void*>(pair_gemm_kernel<FORWARD, true, false, true, ks>), LAUNCH_INT},   \
-      {reinterpret_cast<const void*>(pair_gemm_kernel<FORWARD, true, true, true, ks>), LAUNCH_INT}
+  {reinterpret_cast<const void*>(pair_gemm_kernel<FORWARD, true, BF16, false, ks>), 0},                \
+      {reinterpret_cast<const void*>(pair_gemm_kernel<FORWARD, false, BF16, false, ks>), 0},           \
+      {reinterpret_cast<const void*>(pair_gemm_kernel<BACKWARD, false, BF16, false, ks>), 0},          \
+      {reinterpret_cast<const void*>(pair_gemm_kernel<FORWARD, false, F32, false, ks>), LAUNCH},       \
+      {reinterpret_cast<const void*>(pair_gemm_kernel<BACKWARD, false, F32, false, ks>), LAUNCH},      \
+      {reinterpret_cast<const void*>(pair_gemm_kernel<BACKWARD, false, BF16_ADDED, false, ks>), LAUNCH}, \
+      {reinterpret_cast<const void*>(pair_gemm_kernel<FORWARD, false, BF16, true, ks>), LAUNCH_INT},   \
+      {reinterpret_cast<const void*>(pair_gemm_kernel<FORWARD, false, F32, true, ks>), LAUNCH_INT},    \
+      {reinterpret_cast<const void*>(pair_gemm_kernel<FORWARD, true, BF16, true, ks>), LAUNCH_INT},    \
+      {reinterpret_cast<const void*>(pair_gemm_kernel<FORWARD, true, F32, true, ks>), LAUNCH_INT}
   constexpr int LAUNCH = Shape<true, false>::LAUNCH, LAUNCH_INT = Shape<true, true>::LAUNCH;
   const struct {
     const void* f;
@@ -1151,8 +1155,8 @@ cudaError_t pair_gemm_kernels_init(int* most_ks) {
     cfg.attrs = &attr;
     cfg.numAttrs = 1;
     int fit = 0;
-    const cudaError_t e = ks == 2 ? cudaOccupancyMaxActiveClusters(&fit, pair_gemm_kernel<FORWARD, true, true, true, 2>, &cfg)
-                                  : cudaOccupancyMaxActiveClusters(&fit, pair_gemm_kernel<FORWARD, true, true, true, 4>, &cfg);
+    const cudaError_t e = ks == 2 ? cudaOccupancyMaxActiveClusters(&fit, pair_gemm_kernel<FORWARD, true, F32, true, 2>, &cfg)
+                                  : cudaOccupancyMaxActiveClusters(&fit, pair_gemm_kernel<FORWARD, true, F32, true, 4>, &cfg);
     if (e != cudaSuccess) (void)cudaGetLastError();
     if (e != cudaSuccess || fit < 1) break;
     *most_ks = ks;
@@ -1202,14 +1206,14 @@ cudaError_t launch_pair_forward(const ProductArgs& a, bool int8, const PairDevic
   m.aw = m.bw = m.bw1 = m.bw2 = m.a;
   const long long most = row_tiles(a.M, a.E, a.offsets != nullptr, p.tile) * p.a_tiles;
   if (int8) {
-    if (gated) return a.f32 ? launch<FORWARD, true, true, true>(p, m, plan.ks, most, dev.sms, st)
-                            : launch<FORWARD, true, false, true>(p, m, plan.ks, most, dev.sms, st);
-    return a.f32 ? launch<FORWARD, false, true, true>(p, m, plan.ks, most, dev.sms, st)
-                 : launch<FORWARD, false, false, true>(p, m, plan.ks, most, dev.sms, st);
+    if (gated) return a.f32 ? launch<FORWARD, true, F32, true>(p, m, plan.ks, most, dev.sms, st)
+                            : launch<FORWARD, true, BF16, true>(p, m, plan.ks, most, dev.sms, st);
+    return a.f32 ? launch<FORWARD, false, F32, true>(p, m, plan.ks, most, dev.sms, st)
+                 : launch<FORWARD, false, BF16, true>(p, m, plan.ks, most, dev.sms, st);
   }
-  if (gated) return launch<FORWARD, true, false>(p, m, plan.ks, most, dev.sms, st);
-  return a.f32 ? launch<FORWARD, false, true>(p, m, plan.ks, most, dev.sms, st)
-               : launch<FORWARD, false, false>(p, m, plan.ks, most, dev.sms, st);
+  if (gated) return launch<FORWARD, true, BF16>(p, m, plan.ks, most, dev.sms, st);
+  return a.f32 ? launch<FORWARD, false, F32>(p, m, plan.ks, most, dev.sms, st)
+               : launch<FORWARD, false, BF16>(p, m, plan.ks, most, dev.sms, st);
 }
 
 namespace {
@@ -1249,8 +1253,10 @@ cudaError_t launch_backward(const GradArgs& a, const Plan& plan, const PairDevic
   if (!ok) return cudaErrorInvalidValue;
   long long most = (long long)a.E * p.o_tiles * p.a_tiles;
   if (a.dx != nullptr) most += row_tiles(a.M, a.E, a.offsets != nullptr, p.tile) * p.a_tiles;
-  return a.f32 ? launch<BACKWARD, false, true>(p, m, plan.ks, most, dev.sms, st)
-               : launch<BACKWARD, false, false>(p, m, plan.ks, most, dev.sms, st);
+  // (an expert may have all of the rows)
+  if (a.f32) return launch<BACKWARD, false, F32>(p, m, plan.ks, most, dev.sms, st);
+  return a.dw != nullptr && a.M > ALONE ? launch<BACKWARD, false, BF16_ADDED>(p, m, plan.ks, most, dev.sms, st)
+                                        : launch<BACKWARD, false, BF16>(p, m, plan.ks, most, dev.sms, st);
 }
 
 }  // namespace

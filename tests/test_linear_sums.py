@@ -19,7 +19,7 @@ import torch
 
 import linear_reference as R
 from moe_decode_router_gb300 import flint_moe as F
-from test_linear_ops import dev, done, groups, rand
+from test_linear_ops import BF16, dev, done, groups, half_step, near, rand
 
 gpu = pytest.mark.gpu
 
@@ -74,3 +74,25 @@ def test_weight_gradient_in_fp32(counts):
     F.linear_backward(dy, x, w, dw=dw, offsets=offsets)
     done()
     assert off_by(dw[live], R.weight_gradient(dy, x, E, offsets)[0][live])[1] <= 2.0 ** -19
+
+
+@gpu
+@pytest.mark.parametrize("out", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("grouped", [False, True])
+@pytest.mark.parametrize("M", [(1 << 17) + 3, (1 << 22) + 5])
+def test_weight_gradient_of_many_rows(M, grouped, out):
+    """Terms of one sign: one accumulator over 2^22 of them would be off by 2 %, several times the
+    rounding to bf16."""
+    N, K, d = 64, 48, dev()
+    offsets = torch.tensor([0, 0, M], dtype=torch.int32, device=d) if grouped else None
+    dy, x, w = positive(2, M, N), positive(3, M, K), rand(1, 2 if grouped else 1, N, K)
+    dw, dx = torch.empty(w.shape, dtype=out, device=d), torch.empty_like(x)
+    F.linear_backward(dy, x, w, dx=dx, dw=dw, offsets=offsets)
+    done()
+    want = sum(a.double().T @ b.double() for a, b in zip(dy.split(1 << 18), x.split(1 << 18)))
+    # half a step of the type beside the sum's own error; the fp32 sum has M / 512 parts
+    tol = (BF16 if out == torch.bfloat16 else 0.0) + 1.01 * (32 * 2.0 ** -22 + (M / 512 + 8) * 2.0 ** -24)
+    assert off_by(dw[-1], want)[0] <= tol
+    assert not grouped or not bool(dw[0].any())
+    ref, mag = R.input_gradient(dy[-100:], w[-1:])
+    near(dx[-100:], ref, (N + 2) * 2.0 ** -23 * mag + half_step(dx, ref))
