@@ -65,8 +65,14 @@ static_assert((int)FFN_NONE == (int)FLINT_MOE_ACT_NONE && (int)FFN_SILU == (int)
                   (int)FFN_GELU == (int)FLINT_MOE_ACT_GELU,
               "activations");
 
-// The current device's set-up: the library's, and once that of the tensor-core kernels, whose
-// failure is the products' alone.
+// A failure of the tensor-core kernels' set-up that another try cannot change.
+bool lasting(cudaError_t e) {
+  return e == cudaErrorNotSupported || e == cudaErrorInvalidConfiguration || e == cudaErrorInvalidValue ||
+         e == cudaErrorNoKernelImageForDevice || e == cudaErrorInvalidDeviceFunction || e == cudaErrorSymbolNotFound;
+}
+
+// The current device's set-up: the library's, and that of the tensor-core kernels, once or, after a
+// failure that may pass, on the next call again.  Without those kernels most_ks is 0.
 int set_up(PairDevice* d) try {
   const int st = device_info(&d->sms, &d->err);
   if (st != FLINT_MOE_OK) return st;
@@ -75,17 +81,18 @@ int set_up(PairDevice* d) try {
   int dev = -1;
   if (cudaGetDevice(&dev) != cudaSuccess) return FLINT_MOE_ERR_CUDA;
   std::lock_guard<std::mutex> lk(mu);
-  auto it = most.find(dev);
-  if (it == most.end()) {
-    int ks = 0;
-    if (pair_gemm_kernels_init(&ks) != cudaSuccess) {
-      ks = 0;
-      (void)cudaGetLastError();
-    }
-    it = most.emplace(dev, ks).first;
+  const auto it = most.find(dev);
+  if (it != most.end()) {
+    d->most_ks = it->second;
+    return FLINT_MOE_OK;
   }
-  d->most_ks = it->second;
-  return d->most_ks > 0 ? FLINT_MOE_OK : FLINT_MOE_ERR_CUDA;
+  const cudaError_t e = pair_gemm_kernels_init(&d->most_ks);
+  if (e != cudaSuccess) {
+    d->most_ks = 0;
+    (void)cudaGetLastError();
+  }
+  if (e == cudaSuccess || lasting(e)) most.emplace(dev, d->most_ks);
+  return FLINT_MOE_OK;
 } catch (...) {  // no memory for the map, no mutex
   return FLINT_MOE_ERR_CUDA;
 }
@@ -96,6 +103,7 @@ int product(const ProductArgs& p, bool int8, flint_moe_stream_t stream) {
   if (rc != FLINT_MOE_OK) return rc;
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
   if (few_rows_take(p, int8, d)) return to_status(launch_few_rows(p, int8, st));
+  if (d.most_ks == 0) return FLINT_MOE_ERR_CUDA;
   return to_status(launch_pair_forward(p, int8, d, st));
 }
 
@@ -154,6 +162,7 @@ int flint_moe_linear_backward(const void* dy, const void* x, int M, const void* 
     return FLINT_MOE_ERR_INVALID_ARG;
   PairDevice d;
   if ((st = set_up(&d)) != FLINT_MOE_OK) return st;
+  if (d.most_ks == 0) return FLINT_MOE_ERR_CUDA;
   return gradients(dy, x, M, w, n_experts, offsets, N, K, dx, dw, dw_type, d,
                    reinterpret_cast<cudaStream_t>(stream));
 }
@@ -172,6 +181,7 @@ int flint_moe_gated_linear_backward(const void* dh, const void* gu, const void* 
     return FLINT_MOE_ERR_INVALID_ARG;
   PairDevice d;
   if ((st = set_up(&d)) != FLINT_MOE_OK) return st;
+  if (d.most_ks == 0) return FLINT_MOE_ERR_CUDA;
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   if (launch_gate_backward(dh, gu, offsets, M, I, n_experts, act, dgu, s) != cudaSuccess) return FLINT_MOE_ERR_CUDA;
   return gradients(dgu, x, M, w, n_experts, offsets, 2 * I, K, dx, dw, dw_type, d, s);

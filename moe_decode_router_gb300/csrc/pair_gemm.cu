@@ -1297,7 +1297,7 @@ bool few_rows_take(const ProductArgs& a, bool int8, const PairDevice& dev) {
   if (a.M > 256) return false;
   const long long bytes = (long long)a.N * a.K * (int8 ? 1 : 2), passes = (a.M + 7) / 8;
   return 3000 + passes * bytes / (int8 ? 6800 : 10500) <=
-         plan_forward(a.M, (a.N + 255) / 256, (a.K + 63) / 64, int8, dev.sms / 2, dev.most_ks).ns;
+         plan_forward(a.M, (a.N + 255) / 256, (a.K + 63) / 64, int8, dev.sms / 2, dev.most_ks > 0 ? dev.most_ks : 1).ns;
 }
 
 }  // namespace flint
