@@ -97,6 +97,15 @@ int set_up(PairDevice* d) try {
   return FLINT_MOE_ERR_CUDA;
 }
 
+// The library's set-up alone.
+int library_set_up() try {
+  int sms = 0;
+  unsigned* err = nullptr;
+  return device_info(&sms, &err);
+} catch (...) {
+  return FLINT_MOE_ERR_CUDA;
+}
+
 int product(const ProductArgs& p, bool int8, flint_moe_stream_t stream) {
   PairDevice d;
   const int rc = set_up(&d);
@@ -202,9 +211,7 @@ int flint_moe_integer_quantize_rows(const void* x, int x_type, long long row_str
                   {{x, ((size_t)(rows - 1) * (size_t)row_stride + K) * size}}, {},
                   {{pos, (size_t)rows * (pos ? top_k : 0) * 4}}))
     return FLINT_MOE_ERR_INVALID_ARG;
-  int sms = 0;
-  unsigned* err = nullptr;
-  const int st = device_info(&sms, &err);
+  const int st = library_set_up();
   if (st != FLINT_MOE_OK) return st;
   return to_status(launch_integer_rows(x, x_type == FLINT_MOE_T_BF16, row_stride, rows, K, pos, top_k, places, q,
                                        scales, reinterpret_cast<cudaStream_t>(stream)));

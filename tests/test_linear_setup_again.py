@@ -1,5 +1,6 @@
 """A set-up of the tensor-core kernels that fails: one that may pass is tried again by the next
-call, one that cannot is not, and the products of few rows need none of it.
+call, one that cannot is not, and the products of few rows need none of it.  What the library's
+set-up throws is a status of every call.
 
 csrc/linear_api.cu is linked against fakes of the library's set-up, of the kernels and of the
 runtime; nothing here reaches a GPU.
@@ -8,6 +9,7 @@ runtime; nothing here reaches a GPU.
 import ctypes
 import os
 import subprocess
+import sys
 
 import pytest
 
@@ -18,6 +20,7 @@ from test_linear_setup import RUNTIME, products, rows
 FAKES = r"""
 #include "flint_internal.h"
 using namespace flint;
+#include <new>
 static int error, failures, few, inits, launches;
 extern "C" {
 void fake_set(int e, int n, int f) { error = e; failures = n; few = f; }
@@ -27,6 +30,7 @@ int fake_launches() { return launches; }
 namespace flint {
 static cudaError_t launched(int n) { launches += n; return cudaSuccess; }
 int device_info(int* sms, unsigned** err) {
+  if (error < 0) throw std::bad_alloc();
   *sms = 152;
   *err = nullptr;
   return 0;
@@ -94,3 +98,27 @@ def test_few_rows_go_ahead(faked, error):
     assert products(L) == [0, 0, 0, BAD, BAD] and L.fake_launches() == 3
     L.fake_set(error, 1 << 20, 0)
     assert products(L) == [BAD] * 5 and L.fake_launches() == 3
+
+
+THROWS = """
+import sys
+sys.path[:0] = [%r, %r]
+import ctypes
+from moe_decode_router_gb300 import flint_moe as F
+from test_linear_setup import products, rows
+L = ctypes.CDLL(%r)
+for name, (res, args) in F._LINEAR_SIGS.items():
+    getattr(L, name).restype, getattr(L, name).argtypes = res, args
+L.fake_set(-1, 0, 0)
+assert products(L) == [F.FLINT_MOE_ERR_CUDA] * 5 and rows(L) == F.FLINT_MOE_ERR_CUDA
+L.fake_set(0, 0, 0)
+assert products(L) == [0] * 5 and rows(L) == 0
+"""
+
+
+def test_no_exception_leaves_a_call(faked):
+    """In a process of its own: an exception at a C entry would end it."""
+    here = os.path.dirname(os.path.abspath(__file__))
+    L = faked(0, 0)
+    r = subprocess.run([sys.executable, "-c", THROWS % (os.path.dirname(here), here, L._name)], capture_output=True, text=True, timeout=300)
+    assert r.returncode == 0, r.stderr
