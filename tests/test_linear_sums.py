@@ -96,3 +96,23 @@ def test_weight_gradient_of_many_rows(M, grouped, out):
     assert not grouped or not bool(dw[0].any())
     ref, mag = R.input_gradient(dy[-100:], w[-1:])
     near(dx[-100:], ref, (N + 2) * 2.0 ** -23 * mag + half_step(dx, ref))
+
+
+@gpu
+@pytest.mark.parametrize("K", [880, 896, 1040, 1792])
+@pytest.mark.parametrize("counts", [[3], [300], [150, 0, 151], [2] * 30])
+def test_integer_sums_keep_their_last_bit(counts, K):
+    """Sums of large odd products, up to 2^23.7 in 896 of K, which fp32 holds to the last bit."""
+    M, E, N, offsets, d = sum(counts), len(counts), 64, groups(counts), dev()
+    g = torch.Generator(device=d)
+    g.manual_seed(K)
+    a = torch.randint(100, 128, (M, K), dtype=torch.int8, generator=g, device=d)
+    b = torch.randint(100, 128, (E, N, K), dtype=torch.int8, generator=g, device=d)
+    a[1::3] *= -1
+    b[:, ::2, K // 2:] *= torch.randint(0, 2, (E, N // 2, K - K // 2), dtype=torch.int8, generator=g, device=d)
+    y, ones = torch.empty(M, N, device=d), torch.ones(max(M, E * N), device=d)
+    F.integer_gemm(a, ones[:M].contiguous(), b, ones[:E * N].reshape(E, N).contiguous(), y, offsets=offsets)
+    done()
+    want = R.integer_sums(a, b, offsets)
+    assert K > 896 or float(want.abs().max()) < 2 ** 24
+    assert torch.equal(y, want.float())
