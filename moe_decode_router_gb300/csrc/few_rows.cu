@@ -190,8 +190,9 @@ cudaError_t launch(const ProductArgs& p, cudaStream_t st) {
   return cudaLaunchKernelEx(&cfg, few_rows_kernel<INT8, GATED, SPLIT, WARPS, DEEP>, p);
 }
 
-// Warps that share K and pieces under way, measured (us; calls in a graph, weights from HBM; the
-// second digits are the next best).  256 experts of 1024 x 2048, and dense N x K:
+// Warps that share K and pieces under way, measured (us; calls in a graph; the second digits are the next
+// best).  By expert all figures are of 256 experts of 1024 x 2048 (floors: the weights of as many of them
+// as a uniform draw reaches; from call to call L2 keeps some), other widths follow them; dense N x K:
 //   up to 16 rows by expert   8 of 8, 2    bf16 6 rows 6.5 (4 of 4: 7.2)
 //   up to 128                 4 of 4, 2    integers 48 rows 19.2 (8 of 8: 21.9), bf16 96 rows 54.7 (55.7)
 //   more                      1 of 4, 4    integers 384 rows 67.0 (4 of 4: 70.1), bf16 123.0 (126.3), floors 60 and 125

@@ -34,7 +34,9 @@
 // Every 896 of K the accumulator (one alone, beside the weights: no MMA runs meanwhile) is added to
 // sums in registers: in fp32 while they are at most 2^21, and once one of a warp's has passed that in
 // 32-bit integers, whose conversions (16 lanes a cycle) are most of the time of the hand-over: 8191 x
-// 4096 x 4096 takes 173 us, 194 with integers from the start.  fp32 outputs of bf16 operands are
+// 4096 x 4096 takes 173 us, 194 with integers from the start (replays of a graph on a cool board; in a
+// row of calls 190).  Registers are short where sums are held (128 a thread): the integer kernels spill
+// 24 to 92 bytes a thread, the fp32 ones up to 24, outside the loops over steps of the contraction.  fp32 outputs of bf16 operands are
 // promoted the same way every 512 of the contracted dimension: the tensor cores cut a sum instead of
 // rounding it, which adds up (n products of one sign lose some n 2^-27 of their sum: 2^17 a quarter of
 // bf16's rounding, 2^22 2.3 %).  A weights' gradient of more than 2^17 rows is, whatever its type.
@@ -1292,7 +1294,9 @@ cudaError_t launch_pair_backward(const GradArgs& a, const PairDevice& dev, cudaS
 }
 
 // Whether the few-row kernel takes a product.  By expert: up to 8 rows an expert on average (1,536 rows
-// of 256 experts 162 us, pairs 168; integers 107 and 131).  Dense: its passes of 8 rows over the weights,
+// of 256 experts 162 us, pairs 168; integers 107 and 131).  The host knows no expert's rows: where many
+// fall to one, its weights are read again for every 8 of them, from L2, which takes longer than the
+// pairs would and less than the same rows spread over all experts.  Dense: its passes of 8 rows over the weights,
 // from L2 at 10.5 TB/s (integers 6.8), against the pairs' plan:
 //   rows of N x K      few, pairs (us)
 //   32 of 2048 x 2048   6.3,  6.8    but 48:  8.4,  6.4    integers  64:  7.0,  8.2 but 128: 12.7, 10.1
