@@ -11,8 +11,9 @@
 // DEEP pieces of 128 bytes a row (2 KB of weights a warp each) are under way at a time.
 // Every SPLIT-th piece of K is a warp's; SPLIT warps of a CTA share their rows and add
 // their sums in the warps' order, so that a small product has enough warps.  The tensor cores cut a
-// sum of bf16 products instead of rounding it (2^17 into one accumulator lost 7e-4 of it): where a
-// warp has more than ALONE, each pass's products begin from zero and are added in fp32.  A dense
+// sum of bf16 products instead of rounding it (2^17 into one accumulator lost 7e-4 of it), so in shapes
+// of 4 pieces each pass's products begin from zero and are added in fp32; a warp of a shape of 2 has no
+// more than ALONE.  A dense
 // product asks for its first weights before it waits for the kernel before it: into L2
 // alone, where a write of that kernel would still reach them.
 //

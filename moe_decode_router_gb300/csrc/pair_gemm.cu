@@ -35,11 +35,13 @@
 // sums in registers: in fp32 while they are at most 2^21, and once one of a warp's has passed that in
 // 32-bit integers, whose conversions (16 lanes a cycle) are most of the time of the hand-over: 8191 x
 // 4096 x 4096 takes 173 us, 194 with integers from the start (replays of a graph on a cool board; in a
-// row of calls 190).  Registers are short where sums are held (128 a thread): the integer kernels spill
-// 24 to 92 bytes a thread, the fp32 ones up to 24, outside the loops over steps of the contraction.  fp32 outputs of bf16 operands are
-// promoted the same way every 512 of the contracted dimension: the tensor cores cut a sum instead of
-// rounding it, which adds up (n products of one sign lose some n 2^-27 of their sum: 2^17 a quarter of
-// bf16's rounding, 2^22 2.3 %).  A weights' gradient of more than 2^17 rows is, whatever its type.
+// row of calls 190).  Registers are short where 128 sums a thread are held: the integer kernels spill 24
+// to 92 bytes a thread, the fp32 ones up to 24.
+//
+// fp32 outputs of bf16 operands are promoted the same way every 512 of the contracted dimension: the
+// tensor cores cut a sum instead of rounding it, which adds up (n products of one sign lose some n 2^-27
+// of their sum: 2^17 a quarter of bf16's rounding, 2^22 2.3 %).  A weights' gradient of more than 2^17
+// rows is promoted whatever its type.
 //
 // Where a dense product has units for few pairs alone, KS = 2 or 4 pairs of a cluster share a
 // unit's contraction.  Each leaves its sums in its stages, and after a cluster barrier adds its
